@@ -63,6 +63,7 @@ typedef enum dsa_dtype {
 #define DSA_DEVERR_WAIT_TIMEOUT 2 /* a bounded pipeline wait gave up */
 #define DSA_DEVERR_TOPK_COUNTS 3  /* a row-split Top-K slot fell outside [0, K): the row's
                                      histogram disagreed with its scores; the write was skipped */
+#define DSA_DEVERR_BLOCKS 4       /* a block plan could not place every token (see dsa_block_plan) */
 
 /* Human-readable name of a status code.  Never NULL. */
 const char* dsa_status_string(int status);
@@ -315,6 +316,88 @@ dsa_status dsa_quantize_fp8_rows(const void* x, int64_t x_row_stride, int rows, 
 dsa_status dsa_quantize_fp8_tiles(const void* x, int64_t x_row_stride, int rows, int width, int tile,
                                   uint8_t* codes, int64_t code_row_stride, float* scales,
                                   const int64_t* dst_rows, void* stream);
+
+/* --------------------------------------------------------------------------------------------
+ * dsa_block_plan -- the cache blocks of one serving step, planned on the device from the requests'
+ * lengths (the block-wise KV layout read through an index table, "Achieving Day-0 Readiness...",
+ * section 2.2): which free blocks each sequence takes, the block-table entries they fill, and the
+ * pool row of every token the step appends, ready for the cache writers (dst_rows of
+ * dsa_quantize_* and dsa_rope_append) and for the block_table of the attention entries.
+ *
+ * Sequence s holds c = max(n_ctx[s], 0) cached tokens and appends m = max(n_new[s], 0) (at most
+ * q_per_seq when that is positive).  It needs ceil((c + m) / block_size) - ceil(c / block_size) more
+ * blocks, and takes them from the front of the free list, sequences in order.  A sequence whose
+ * blocks exceed its block-table row, that reaches beyond the end of the free list, or whose packed
+ * rows end beyond `rows`, is not placed (after the second, later sequences that need a block are not
+ * either; those that need none still are).
+ *   n_ctx, n_new  device int32 [n_seq];  0 <= n_seq <= DSA_BLOCK_PLAN_MAX_SEQ
+ *   q_per_seq     0: rows are packed, sequence s at rows sum_{s' < s} m_s' ...; > 0: row
+ *                 s * q_per_seq + i is token i of sequence s (rows >= n_seq * q_per_seq)
+ *   free_blocks   device int32 [num_free] block ids; n_free device int32 [1] = how many of them are
+ *                 free now (clamped to [0, num_free]), or NULL for num_free
+ *   num_blocks    blocks in the pool: an id outside [0, num_blocks) met on the way records
+ *                 DSA_DEVERR_INDEX_RANGE and its tokens get no row
+ *   block_table   device int32 [n_seq][max_blocks]: entries below ceil(c / block_size) are read, the
+ *                 new blocks' entries are written, the others are left as they are
+ *   dst_rows      device int64 [rows]: pool row block * block_size + position % block_size of each
+ *                 token; -1 for a row without a token (a sequence that was not placed, padding, rows
+ *                 behind the last sequence)
+ *   pos, seq      device int32 [rows] or NULL: the token's position in its sequence, its sequence; -1
+ *   row_start     device int32 [n_seq + 1] or NULL: first row of each sequence, then the end
+ *   n_placed      device int32 [n_seq] or NULL: m, or 0 for a sequence that was not placed
+ *   taken         device int32 [1] or NULL: blocks taken from the front of the free list
+ * A token that was not placed records DSA_DEVERR_BLOCKS.  The free list itself is not changed: repeating a call repeats its results.
+ * Outputs may not overlap inputs (but block_table, in place) or one another.  max_blocks *
+ * block_size < 2^31.  One kernel, no workspace.
+ * ------------------------------------------------------------------------------------------ */
+#define DSA_BLOCK_PLAN_MAX_SEQ 16384
+dsa_status dsa_block_plan(const int32_t* n_ctx, const int32_t* n_new, int n_seq, int q_per_seq, int block_size,
+                          const int32_t* free_blocks, const int32_t* n_free, int num_free, int num_blocks,
+                          int32_t* block_table, int max_blocks, int rows, int64_t* dst_rows, int32_t* pos,
+                          int32_t* seq, int32_t* row_start, int32_t* n_placed, int32_t* taken, void* stream);
+
+/* --------------------------------------------------------------------------------------------
+ * dsa_rope / dsa_rope_append -- rotary positions with 1 to 4 axes (a text position; time, height
+ * and width of an image or video patch) on the rotary columns of queries, and of the rows that go
+ * into a cache (the latent row: 512 columns as they are, 64 rotary ones).
+ *
+ * Pair i (0 <= i < rot_dim / 2) of row r turns by theta = pos[r, pair_axis[i]] * inv_freq[i]:
+ *   y0 = x0 cos theta - x1 sin theta,   y1 = x1 cos theta + x0 sin theta
+ * where (x0, x1) are columns rot_off + (i, i + rot_dim / 2) for DSA_ROPE_HALF and rot_off +
+ * (2i, 2i + 1) for DSA_ROPE_PAIRS.  The angle is exact to fp32 at every 32-bit position.
+ *   pos        device int32 [rows][n_axes]
+ *   pair_axis  HOST bytes [rot_dim / 2], each below n_axes, read before the call returns; NULL when
+ *              n_axes = 1
+ *   inv_freq   device fp32 [rot_dim / 2], finite
+ * Supported: rot_dim even, at most 256; n_axes at most 4; finite inputs.
+ *
+ * dsa_rope: x [rows, heads, width] bf16 (element (r, h, c) at x + r*x_row_stride + h*x_head_stride + c,
+ * strides in ELEMENTS; heads must not overlap) -> out, the same shape with its own strides: the
+ * rotated columns turned (fp32 arithmetic, one rounding to bf16), the others copied.  out == x (with
+ * equal strides) turns in place; otherwise out must not overlap x.  inverse != 0 turns by -theta,
+ * which is also the gradient: dL/dx is dL/dy turned back.
+ *
+ * dsa_rope_append: rows x [rows, width] bf16 (pitch x_row_stride elements) are turned and written
+ * to row dst_rows[r] of a cache (dst_rows NULL: row r; a negative entry drops the row; an entry
+ * of dst_count or more records DSA_DEVERR_INDEX_RANGE and drops it).  The turned values are
+ * encoded from fp32, by dtype:
+ *   DSA_BF16           bf16, round to nearest even; scale unused
+ *   DSA_FP8_E4M3       codes and one fp32 scale per row, scale [dst_count]
+ *   DSA_FP8_E4M3_T128  codes and one fp32 scale per 128 columns, scale [dst_count][ceil(width/128)]
+ *   DSA_MXFP8_E4M3     codes and one E8M0 byte per 32 columns, scale [dst_count][width/32]
+ * with the scales and rounding of dsa_quantize_*.  dst row q at dst + q * dst_row_stride BYTES.
+ * Destination rows must be distinct.
+ * ------------------------------------------------------------------------------------------ */
+#define DSA_ROPE_HALF 0
+#define DSA_ROPE_PAIRS 1
+dsa_status dsa_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride, int rows, int heads, int width,
+                    int rot_off, int rot_dim, const int32_t* pos, int n_axes, const uint8_t* pair_axis,
+                    const float* inv_freq, int style, int inverse, void* out, int64_t out_row_stride,
+                    int64_t out_head_stride, void* stream);
+dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int width, int rot_off, int rot_dim,
+                           const int32_t* pos, int n_axes, const uint8_t* pair_axis, const float* inv_freq,
+                           int style, dsa_dtype dtype, void* dst, int64_t dst_row_stride, int64_t dst_count,
+                           void* scale, const int64_t* dst_rows, void* stream);
 
 /* --------------------------------------------------------------------------------------------
  * Fused chain: dsa_decode / dsa_prefill run steps 1-3 back to back on `stream` (the indexer's

@@ -1,0 +1,165 @@
+"""Host-side checks of the serving-step operators (no GPU): argument refusals before any launch, and
+the oracle's pins by hand-worked values and library routines."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+F = 16  # a fake, aligned device address: every call here is refused before it is used
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from top_sparse_attention_gb300 import build
+
+    build.build()
+    from top_sparse_attention_gb300 import _native
+
+    return _native.lib
+
+
+# (n_ctx, n_new, n_seq, q_per_seq, block_size, free, n_free, num_free, num_blocks, table, max_blocks, rows,
+#  dst_rows, pos, seq, row_start, n_placed, taken, stream)
+PLAN = [F, F, 4, 0, 64, F, None, 8, 64, F, 16, 100, F, F, F, F, F, F, None]
+
+
+@pytest.mark.parametrize("at,value,status", [
+    (0, None, 1), (1, None, 1), (9, None, 1), (12, None, 1), (5, None, 1),   # missing arrays
+    (2, -1, 1), (3, -1, 1), (4, 0, 1), (7, -1, 1), (8, -1, 1), (10, -1, 1), (11, -1, 1),  # sizes
+    (3, 26, 1),           # padded rows do not fit: 4 * 26 > 100
+    (2, 16385, 2),        # more sequences than supported
+    (10, 1 << 26, 2),     # max_blocks * block_size leaves 31 bits
+])
+def test_block_plan_refusals(lib, at, value, status):
+    args = list(PLAN)
+    args[at] = value
+    assert lib.dsa_block_plan(*args) == status
+
+
+def test_block_plan_with_nothing_to_do(lib):
+    assert lib.dsa_block_plan(None, None, 0, 0, 64, None, None, 0, 0, None, 0, 0, None, None, None, None, None, None, None) == 0
+
+
+# (x, row stride, head stride, rows, heads, width, rot_off, rot_dim, pos, n_axes, pair_axis, inv_freq, style,
+#  inverse, out, out row stride, out head stride, stream)
+ROPE = [F, 1024, 64, 8, 16, 64, 0, 64, F, 1, None, F, 0, 0, 4096, 1024, 64, None]
+# (x, row stride, rows, width, rot_off, rot_dim, pos, n_axes, pair_axis, inv_freq, style, dtype, dst, dst row
+#  bytes, dst_count, scale, dst_rows, stream)
+APPEND = [F, 576, 8, 576, 512, 64, F, 1, None, F, 0, 1, F, 576, 100, F, F, None]
+
+
+@pytest.mark.parametrize("at,value,status", [
+    (0, None, 1), (8, None, 1), (11, None, 1), (14, None, 1), (0, 17, 1), (14, 17, 1),
+    (3, -1, 1), (4, 0, 1), (5, 0, 1), (6, -1, 1), (6, 8, 1), (7, 0, 1), (7, 63, 1), (9, 0, 1),
+    (9, 2, 1),            # two axes without a table
+    (9, 5, 2), (12, 2, 1),
+    (1, 32, 1), (2, 32, 1), (15, 32, 1), (16, 0, 1),     # rows or heads that overlap
+])
+def test_rope_refusals(lib, at, value, status):
+    args = list(ROPE)
+    args[at] = value
+    assert lib.dsa_rope(*args) == status
+
+
+def test_rope_refuses_other_combinations(lib):
+    args = list(ROPE)
+    args[5], args[2], args[16], args[7] = 512, 512, 512, 258   # more than 128 pairs
+    args[1] = args[15] = 16 * 512
+    assert lib.dsa_rope(*args) == 2
+    args = list(ROPE)
+    args[9], args[10] = 2, bytes([0] * 31 + [2])               # an axis that does not exist
+    assert lib.dsa_rope(*args) == 1
+    args = list(ROPE)
+    args[14], args[15] = args[0], 2048                         # in place under another layout
+    assert lib.dsa_rope(*args) == 1
+    args = list(ROPE)
+    args[3], args[0], args[8] = 0, None, None                  # no rows
+    assert lib.dsa_rope(*args) == 0
+
+
+@pytest.mark.parametrize("at,value,status", [
+    (0, None, 1), (6, None, 1), (9, None, 1), (12, None, 1), (15, None, 1), (0, 17, 1), (15, 18, 1),
+    (2, -1, 1), (3, 0, 1), (4, 520, 1), (5, 62 + 3, 1), (11, 9, 2), (13, 575, 1), (14, -1, 1), (1, 500, 1),
+    (14, 4, None),
+])
+def test_rope_append_refusals(lib, at, value, status):
+    args = list(APPEND)
+    args[at] = value
+    if status is None:  # fewer destination rows than rows, without a list of them
+        args[16], status = None, 1
+    assert lib.dsa_rope_append(*args) == status
+
+
+def test_rope_append_mxfp8_needs_whole_groups(lib):
+    args = list(APPEND)
+    args[11], args[3], args[4], args[5] = 2, 120, 56, 64
+    assert lib.dsa_rope_append(*args) == 1
+
+
+def test_python_refuses_host_tensors_and_wrong_types():
+    import top_sparse_attention_gb300 as dsa
+
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        dsa.dsa_block_plan(i, i, i, i.view(2, 1), block_size=64, num_blocks=2, rows=2)
+    with pytest.raises(ValueError, match="CUDA"):
+        dsa.dsa_rope(torch.zeros(2, 64, dtype=torch.bfloat16), i, torch.zeros(32))
+    with pytest.raises(ValueError, match="CUDA"):
+        dsa.dsa_rope_append(torch.zeros(2, 64, dtype=torch.bfloat16), i, torch.zeros(32),
+                            torch.zeros(2, 64, dtype=torch.bfloat16), rot_off=0)
+
+
+# ---------------------------------------------------------------------------------------------
+# pins of the oracle
+
+def test_oracle_block_plan_by_hand():
+    # blocks of 4; sequence 0 has 3 of 4 positions used and adds 3 (one new block), sequence 1 is full
+    # at 4 and adds 1 (one), sequence 2 adds none, sequence 3 is new and adds 5 (two: one block too many)
+    table = np.array([[7, -1], [5, -1], [6, -1], [-1, -1]])
+    got = oracle.block_plan([3, 4, 2, 0], [3, 1, 0, 5], [9, 8, 3], table, block_size=4, num_blocks=10, rows=10)
+    assert got["dst_rows"].tolist() == [7 * 4 + 3, 36, 37, 32, -1, -1, -1, -1, -1, -1]
+    assert got["pos"].tolist() == [3, 4, 5, 4] + [-1] * 6
+    assert got["row_start"].tolist() == [0, 3, 4, 4, 9] and got["n_placed"].tolist() == [3, 1, 0, 0]
+    assert got["taken"].tolist() == [2] and not got["ok"]
+    assert got["table"].tolist() == [[7, 9], [5, 8], [6, -1], [-1, -1]]
+
+
+def test_oracle_rotation_by_hand_and_as_complex_numbers():
+    y = oracle.rotate([[3.0, 4.0]], [1], [np.pi / 2], rot_off=0, rot_dim=2)
+    np.testing.assert_allclose(y, [[-4.0, 3.0]], atol=1e-15)
+    rng = np.random.default_rng(0)
+    x, pos, f = rng.standard_normal((5, 3, 12)), rng.integers(0, 100, (5, 2)), rng.random(4)
+    axis = [0, 1, 1, 0]
+    for style in ("half", "pairs"):
+        y = oracle.rotate(x, pos, f, rot_off=2, rot_dim=8, pair_axis=axis, style=style)
+        theta = pos[:, axis] * f
+        r = x[..., 2:10]
+        z = r[..., :4] + 1j * r[..., 4:] if style == "half" else r[..., 0::2] + 1j * r[..., 1::2]
+        z = z * np.exp(1j * theta)[:, None]
+        want = np.concatenate([z.real, z.imag], -1) if style == "half" else np.stack([z.real, z.imag], -1).reshape(r.shape)
+        np.testing.assert_allclose(y[..., 2:10], want, atol=1e-12)
+        np.testing.assert_array_equal(y[..., :2], x[..., :2])
+        np.testing.assert_array_equal(y[..., 10:], x[..., 10:])
+        back = oracle.rotate(y, pos, f, rot_off=2, rot_dim=8, pair_axis=axis, style=style, inverse=True)
+        np.testing.assert_allclose(back, x, atol=1e-12)
+
+
+def test_oracle_tree_attention_is_masked_attention():
+    rng = np.random.default_rng(1)
+    N, H, D, DV, c, m = 5, 3, 24, 16, 11, 4
+    q, rows = rng.standard_normal((N, H, D)), rng.standard_normal((c + N, D))
+    sees = np.tril(rng.random((N, N)) < 0.5) | np.eye(N, dtype=bool)
+    out, lse = oracle.tree_attention(q, rows, c, m, sees, 0.2, DV)
+    mask = np.zeros((N, c + m), bool)
+    mask[:, :c] = True
+    mask[:, c:] = sees[:, :m]
+    t = torch.from_numpy
+    want = torch.nn.functional.scaled_dot_product_attention(
+        t(q).transpose(0, 1), t(rows[: c + m]).expand(H, -1, -1), t(rows[: c + m, :DV]).expand(H, -1, -1),
+        attn_mask=t(mask)[None], scale=0.2).transpose(0, 1)
+    np.testing.assert_allclose(out[:m], want.numpy()[:m], atol=1e-12)
+    assert np.all(out[m:] == 0) and np.all(lse[m:] == -np.inf)
+    # no context and an empty mask row: nothing is seen
+    out, lse = oracle.tree_attention(q, rows, 0, N, np.zeros((N, N), bool), 0.2, DV)
+    assert np.all(out == 0) and np.all(lse == -np.inf)

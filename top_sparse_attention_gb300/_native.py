@@ -15,7 +15,10 @@ LIB_PATH = os.path.join(PKG, "libdsa.so")
 DSA_OK = 0
 DSA_BF16, DSA_FP8_E4M3, DSA_MXFP8_E4M3, DSA_FP8_E4M3_T128 = 0, 1, 2, 3
 DSA_ATTN_AUTO, DSA_ATTN_TCGEN05 = 0, 1
-DEVERR = {0: "none", 1: "index out of range", 2: "wait timeout", 3: "row-split Top-K counts disagree"}
+DEVERR = {0: "none", 1: "index out of range", 2: "wait timeout", 3: "row-split Top-K counts disagree",
+          4: "block plan could not place every token"}
+DSA_BLOCK_PLAN_MAX_SEQ = 16384
+DSA_ROPE_HALF, DSA_ROPE_PAIRS = 0, 1
 
 EXPORTS = (
     "dsa_status_string", "dsa_abi_version", "dsa_get_device_error", "dsa_index_score",
@@ -23,7 +26,7 @@ EXPORTS = (
     "dsa_quantize_mxfp8", "dsa_quantize_fp8_rows", "dsa_quantize_fp8_tiles",
     "dsa_workspace_size", "dsa_launch_count", "dsa_decode", "dsa_prefill", "dsa_topk_noalloc",
     "dsa_selftest_wait_timeout", "dsa_topk_pairs", "dsa_topk_merge", "dsa_sparse_attn_partial",
-    "dsa_attn_combine", "dsa_set_attn_kernel",
+    "dsa_attn_combine", "dsa_set_attn_kernel", "dsa_block_plan", "dsa_rope", "dsa_rope_append",
 )
 
 
@@ -83,6 +86,9 @@ def _load():
         "dsa_quantize_mxfp8": (I, [P, I64, I, I, P, P, P, P]),
         "dsa_quantize_fp8_rows": (I, [P, I64, I, I, P, I64, P, P, P]),
         "dsa_quantize_fp8_tiles": (I, [P, I64, I, I, I, P, I64, P, P, P]),
+        "dsa_block_plan": (I, [P, P, I, I, I, P, P, I, I, P, I, I, P, P, P, P, P, P, P]),
+        "dsa_rope": (I, [P, I64, I64, I, I, I, I, I, P, I, ctypes.c_char_p, P, I, I, P, I64, I64, P]),
+        "dsa_rope_append": (I, [P, I64, I, I, I, I, P, I, ctypes.c_char_p, P, I, I, P, I64, I64, P, P, P]),
         "dsa_workspace_size": (I, [ctypes.POINTER(DsaArgs), I, ctypes.POINTER(SZ)]),
         "dsa_launch_count": (I, [ctypes.POINTER(DsaArgs), I, ctypes.POINTER(ctypes.c_int)]),
         "dsa_decode": (I, [ctypes.POINTER(DsaArgs), P, SZ, P]),

@@ -6,7 +6,7 @@ workspaces that the caller does not pass are allocated with torch on the inputs'
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -15,7 +15,8 @@ from . import _native as N
 __all__ = ["dsa_index_score", "dsa_topk", "dsa_topk_noalloc", "dsa_topk_pairs", "dsa_topk_merge",
            "dsa_sparse_attn_partial", "dsa_attn_combine", "dsa_sparse_attn", "DsaCall", "dsa_decode", "dsa_prefill",
            "dsa_workspace_size", "dsa_launch_count", "dsa_get_device_error", "ld_scores_for",
-           "dsa_quantize_mxfp8", "dsa_quantize_fp8_rows", "dsa_quantize_fp8_tiles"]
+           "dsa_quantize_mxfp8", "dsa_quantize_fp8_rows", "dsa_quantize_fp8_tiles",
+           "dsa_block_plan", "BlockPlan", "dsa_rope", "dsa_rope_append"]
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -314,6 +315,194 @@ def dsa_quantize_fp8_tiles(x, *, tile=128, codes=None, scales=None, dst_rows=Non
     N.check(N.lib.dsa_quantize_fp8_tiles(_p(x), x.stride(0), rows, width, tile, _p(codes), codes.stride(0),
                                          _p(scales), _p(dst_rows), _stream(stream)), "dsa_quantize_fp8_tiles")
     return codes, scales
+
+
+# The serving-step operators below check their tensors (device, dtype, layout) and run on the
+# tensors' own device and its current stream, whichever device is current.
+
+def _check(what, device, name, t, dtype, dims=None, dense=True):
+    if t is None:
+        return
+    if t.device != device:
+        raise ValueError(f"{what}: {name} is on {t.device}, the call on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {name} must be {dtype}, got {t.dtype}")
+    if dims is not None and t.dim() != dims:
+        raise ValueError(f"{what}: {name} must have {dims} axes, got shape {tuple(t.shape)}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be contiguous")
+
+
+def _cuda_device(what, t) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{what}: tensors must be on a CUDA device, got {t.device}")
+    return t.device
+
+
+def _run(what, fn, device, stream, *args):
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream.cuda_stream)
+    if st != N.DSA_OK:
+        N.check(st, what)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+class BlockPlan(NamedTuple):
+    """What dsa_block_plan gives (see dsa.h): per row `dst_rows` int64, `pos` and `seq` int32 (-1: no
+    token); `row_start` int32 [n_seq + 1]; `n_placed` int32 [n_seq]; `taken` int32 [1]."""
+    dst_rows: torch.Tensor
+    pos: torch.Tensor
+    seq: torch.Tensor
+    row_start: torch.Tensor
+    n_placed: torch.Tensor
+    taken: torch.Tensor
+
+
+def dsa_block_plan(n_ctx, n_new, free_blocks, block_table, *, block_size, num_blocks, rows=None, q_per_seq=0,
+                   n_free=None, out: Optional[BlockPlan] = None, stream=None) -> BlockPlan:
+    """Blocks, block-table entries and destination rows of a step that appends n_new[s] tokens to
+    sequences of n_ctx[s] (int32 [n_seq]).  New blocks come from the front of `free_blocks` (int32; the
+    first n_free[0] of them when given); `block_table` int32 [n_seq, max_blocks] is updated in place.
+    Rows are packed (`rows` given, at least the tokens of the step), or padded to q_per_seq per
+    sequence (`rows` defaults to n_seq * q_per_seq)."""
+    what = "dsa_block_plan"
+    dev = _cuda_device(what, n_ctx)
+    i32 = torch.int32
+    _check(what, dev, "n_ctx", n_ctx, i32, 1)
+    _check(what, dev, "n_new", n_new, i32, 1)
+    _check(what, dev, "free_blocks", free_blocks, i32, 1)
+    _check(what, dev, "n_free", n_free, i32)
+    _check(what, dev, "block_table", block_table, i32, 2)
+    n_seq = n_ctx.shape[0]
+    if n_new.shape[0] != n_seq or block_table.shape[0] != n_seq or (n_free is not None and n_free.numel() < 1):
+        raise ValueError(f"{what}: n_ctx, n_new and block_table must agree on the number of sequences")
+    if rows is None:
+        if q_per_seq <= 0:
+            raise ValueError(f"{what}: packed rows need their number (rows)")
+        rows = n_seq * q_per_seq
+    if out is None:
+        new = lambda n, t=i32: torch.empty(n, dtype=t, device=dev)  # noqa: E731
+        out = BlockPlan(new(rows, torch.int64), new(rows), new(rows), new(n_seq + 1), new(n_seq), new(1))
+    else:
+        for name, t, n, kind in (("dst_rows", out.dst_rows, rows, torch.int64), ("pos", out.pos, rows, i32),
+                                 ("seq", out.seq, rows, i32), ("row_start", out.row_start, n_seq + 1, i32),
+                                 ("n_placed", out.n_placed, n_seq, i32), ("taken", out.taken, 1, i32)):
+            _check(what, dev, name, t, kind, 1)
+            if t.shape[0] < n:
+                raise ValueError(f"{what}: {name} has {t.shape[0]} entries, needs {n}")
+    _run(what, N.lib.dsa_block_plan, dev, stream, n_ctx.data_ptr(), n_new.data_ptr(), n_seq, int(q_per_seq),
+         int(block_size), free_blocks.data_ptr(), _ptr(n_free), free_blocks.shape[0], int(num_blocks),
+         block_table.data_ptr(), block_table.shape[1], int(rows), out.dst_rows.data_ptr(), out.pos.data_ptr(),
+         out.seq.data_ptr(), out.row_start.data_ptr(), out.n_placed.data_ptr(), out.taken.data_ptr())
+    return out
+
+
+_ROPE_STYLE = {"half": N.DSA_ROPE_HALF, "pairs": N.DSA_ROPE_PAIRS}
+
+
+def _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style):
+    rows = x.shape[0]
+    if pos.dim() == 1:
+        pos = pos[:, None]
+    _check(what, dev, "pos", pos, torch.int32, 2)
+    _check(what, dev, "inv_freq", inv_freq, torch.float32, 1)
+    if rot_dim is None:
+        rot_dim = x.shape[-1] - rot_off
+    n_axes = pos.shape[1]
+    if pos.shape[0] != rows or 2 * inv_freq.shape[0] != rot_dim:
+        raise ValueError(f"{what}: pos must have one row per row of x, inv_freq rot_dim / 2 entries")
+    if pair_axis is None and sections is not None:
+        if len(sections) != n_axes:
+            raise ValueError(f"{what}: {len(sections)} sections for {n_axes} axes")
+        pair_axis = b"".join(bytes([a]) * int(n) for a, n in enumerate(sections))
+    elif pair_axis is not None:
+        pair_axis = bytes(pair_axis)
+    if pair_axis is not None and 2 * len(pair_axis) != rot_dim:
+        raise ValueError(f"{what}: {len(pair_axis)} pairs have an axis, rot_dim / 2 = {rot_dim // 2} need one")
+    if style not in _ROPE_STYLE:
+        raise ValueError(f"{what}: style must be one of {tuple(_ROPE_STYLE)}, got {style!r}")
+    return pos, rot_dim, n_axes, pair_axis, _ROPE_STYLE[style]
+
+
+def dsa_rope(x, pos, inv_freq, *, rot_off=0, rot_dim=None, sections=None, pair_axis=None, style="half",
+             inverse=False, out=None, stream=None) -> torch.Tensor:
+    """Rotary positions on columns [rot_off, rot_off + rot_dim) (default: to the last one) of bf16 x
+    [rows, heads, width] or [rows, width].  pos int32 [rows] or [rows, n_axes]; inv_freq fp32
+    [rot_dim / 2]; with several axes `sections` (pairs per axis, in order) or `pair_axis` (the axis
+    of each pair) says which axis turns a pair.  `out` may be x itself (in place) or any strided
+    tensor of x's shape that does not overlap it; `inverse` turns back (the gradient)."""
+    what = "dsa_rope"
+    dev = _cuda_device(what, x)
+    _check(what, dev, "x", x, torch.bfloat16, None, dense=False)
+    if x.dim() not in (2, 3) or (x.shape[-1] > 1 and x.stride(-1) != 1):
+        raise ValueError(f"{what}: x must be [rows, heads, width] or [rows, width] with dense columns")
+    pos, rot_dim, n_axes, pair_axis, code = _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _check(what, dev, "out", out, torch.bfloat16, x.dim(), dense=False)
+        if out.shape != x.shape or (out.shape[-1] > 1 and out.stride(-1) != 1):
+            raise ValueError(f"{what}: out must have x's shape and dense columns")
+    three = x.dim() == 3
+    heads = x.shape[1] if three else 1
+    if x.shape[0] == 0 or heads == 0:
+        return out
+    xh, oh = (x.stride(1), out.stride(1)) if three and heads > 1 else (x.shape[-1], x.shape[-1])
+    _run(what, N.lib.dsa_rope, dev, stream, x.data_ptr(), x.stride(0), xh, x.shape[0], heads, x.shape[-1], int(rot_off),
+         int(rot_dim), pos.data_ptr(), n_axes, pair_axis, inv_freq.data_ptr(), code, int(bool(inverse)), out.data_ptr(),
+         out.stride(0), oh)
+    return out
+
+
+def dsa_rope_append(x, pos, inv_freq, dst, *, scale=None, dst_rows=None, rot_off, rot_dim=None, sections=None,
+                    pair_axis=None, style="half", stream=None) -> None:
+    """bf16 rows x [rows, width], turned as in dsa_rope, encoded and written to rows dst_rows (int64
+    [rows]; negative: dropped; None: row r) of the cache rows dst [*, >= width]: bf16, or uint8 E4M3
+    codes with `scale` fp32 [*] (per row), fp32 [*, ceil(width / 128)] (per 128 columns) or uint8
+    [*, width / 32] (MXFP8 exponents)."""
+    what = "dsa_rope_append"
+    dev = _cuda_device(what, x)
+    _check(what, dev, "x", x, torch.bfloat16, 2, dense=False)
+    if x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError(f"{what}: x must have dense columns")
+    width = x.shape[1]
+    pos, rot_dim, n_axes, pair_axis, code = _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style)
+    if dst.dtype == torch.bfloat16:
+        kind, want = N.DSA_BF16, None
+    elif scale is None:
+        raise ValueError(f"{what}: E4M3 rows need their scales")
+    elif scale.dtype == torch.uint8:
+        kind, want = N.DSA_MXFP8_E4M3, (width // 32,)
+    elif scale.dim() == 1:
+        kind, want = N.DSA_FP8_E4M3, ()
+    else:
+        kind, want = N.DSA_FP8_E4M3_T128, (-(-width // 128),)
+    _check(what, dev, "dst", dst, torch.bfloat16 if kind == N.DSA_BF16 else torch.uint8, 2, dense=False)
+    if dst.shape[1] < width or dst.stride(1) != 1 or (dst.shape[0] > 1 and dst.stride(0) < width):
+        raise ValueError(f"{what}: dst rows must hold {width} dense columns")
+    if want is not None:
+        _check(what, dev, "scale", scale, torch.uint8 if kind == N.DSA_MXFP8_E4M3 else torch.float32)
+        if scale.shape[1:] != want or scale.shape[0] < dst.shape[0]:
+            raise ValueError(f"{what}: scale must be [{dst.shape[0]}{''.join(f', {n}' for n in want)}], got {tuple(scale.shape)}")
+    _check(what, dev, "dst_rows", dst_rows, torch.int64, 1)
+    if dst_rows is not None and dst_rows.shape[0] != x.shape[0]:
+        raise ValueError(f"{what}: dst_rows must have one entry per row of x")
+    if x.shape[0] == 0:
+        return
+    _run(what, N.lib.dsa_rope_append, dev, stream, x.data_ptr(), x.stride(0), x.shape[0], width, int(rot_off),
+         int(rot_dim), pos.data_ptr(), n_axes, pair_axis, inv_freq.data_ptr(), code, kind, dst.data_ptr(),
+         (dst.stride(0) if dst.shape[0] > 1 else width) * dst.element_size(), dst.shape[0], None if kind == N.DSA_BF16 else scale.data_ptr(),
+         _ptr(dst_rows))
 
 
 def dsa_launch_count(args: N.DsaArgs, prefill: bool) -> int:

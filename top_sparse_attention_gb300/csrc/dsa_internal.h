@@ -191,6 +191,49 @@ size_t sparse_attn_ws_bytes(int T, int H, int K, int D_v);
 cudaError_t launch_sparse_attn(SparseAttnParams p, int D_qk, int D_v, bool fp8, bool sepv,
                                void* ws, cudaStream_t stream, bool pdl, bool tiled);
 
+// ---------------------------------------------------------------------------------------------
+// the serving step around the chain: block plan, rotary positions
+
+struct BlockPlanParams {
+  const int32_t* n_ctx;    // [n_seq]
+  const int32_t* n_new;    // [n_seq]
+  int n_seq, q_per_seq, block_size;
+  const int32_t* free_blocks;  // [num_free]
+  const int32_t* n_free;   // device count, or null (num_free)
+  int num_free, num_blocks;
+  int32_t* block_table;    // [n_seq][max_blocks]
+  int max_blocks, rows;
+  int64_t* dst_rows;       // [rows]
+  int32_t* pos;            // [rows] or null
+  int32_t* seq;            // [rows] or null
+  int32_t* row_start;      // [n_seq + 1] or null
+  int32_t* n_placed;       // [n_seq] or null
+  int32_t* taken;          // [1] or null
+  int* err;                // device error word
+};
+
+constexpr int kRopeMaxPairs = 128;
+
+struct RopeParams {
+  const __nv_bfloat16* x;
+  int64_t x_row_stride, x_head_stride;  // in elements
+  int rows, heads, width, rot_off;
+  int pairs;               // rotated pairs (rot_dim / 2)
+  const int32_t* pos;      // [rows][pos_stride]
+  int pos_stride;          // number of axes
+  const float* inv_freq;   // [pairs]
+  uint8_t axis[kRopeMaxPairs];  // axis of each pair
+  bool half;               // pairs (i, i + pairs) instead of (2i, 2i + 1)
+  bool inverse, copy;      // turn back; also copy the columns that are not turned
+  __nv_bfloat16* out;      // dsa_rope
+  int64_t out_row_stride, out_head_stride;
+  uint8_t* dst;            // dsa_rope_append: cache rows, pitch dst_row_stride bytes
+  int64_t dst_row_stride, dst_count;
+  uint8_t* scale;          // fp32 or E8M0 scales of the destination rows
+  const int64_t* dst_rows; // [rows] or null
+  int* err;                // device error word
+};
+
 // Argument checks and device facts shared with entry points defined outside dsa_api.cu.
 dsa_status check_topk_args(const float* scores, int64_t ld_scores, int T, int q_per_seq, int q_pos0,
                            const int32_t* n_valid, int L, int K, const int32_t* idx);

@@ -1,0 +1,447 @@
+// Rotary positions with one or several axes, on queries (dsa_rope) and on the rows that the cache
+// writer stores (dsa_rope_append).
+//
+// Pair i of a row turns by theta = pos[row, axis(i)] * inv_freq[i]:
+//   y0 = x0 cos(theta) - x1 sin(theta),   y1 = x1 cos(theta) + x0 sin(theta),
+// the pair being elements (i, i + rot_dim / 2) of the rotated columns or (2i, 2i + 1).
+//
+// The angle.  A position of a million times a frequency of one loses the angle in fp32 (an ulp of
+// 10^6 is 0.06 rad).  Here inv_freq / 2 pi, in turns, becomes a 64-bit fixed-point fraction (from an
+// fp64 product, once per pair and row block); position times fraction modulo 2^64 is then exact
+// integer arithmetic that drops the whole turns by itself, and its top 32 bits over 2^31 are theta
+// in half turns, in [-1, 1), for sincospif.  The fp64 product is off by 2^-53 of the angle at most:
+// under 2^-30 turns up to position 2^24 (inv_freq <= 1), 2^-24 turns (fp32's own rounding) at 2^31.
+//
+// Bound: HBM bandwidth.  One warp per row (append) or per row and 16 heads (rope): the lanes take the
+// sines of the row's pairs once and share them through shared memory; 16-byte loads and stores.
+// Rotated values enter the cache format's rounding in fp32 (one rounding, not two).
+#include <math.h>
+
+#include "quant_common.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kHeadsPerWarp = 16;
+
+// The row's (cos, sin) for every pair, into this warp's shared table.
+__device__ __forceinline__ void fill_turns(const RopeParams& p, int64_t row, float2* cs) {
+  const int lane = threadIdx.x & 31;
+  const int32_t* pos = p.pos + row * p.pos_stride;
+  for (int i = lane; i < p.pairs; i += 32) {
+    const double turns = (double)p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+    const double frac = turns - rint(turns);                              // [-1/2, 1/2]
+    const uint64_t f = (uint64_t)__double2ll_rn(frac * 0x1p63) << 1;      // frac * 2^64 modulo 2^64
+    const uint64_t phase = (uint64_t)(int64_t)pos[p.axis[i]] * f;
+    float s, c;
+    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
+    cs[i] = make_float2(c, p.inverse ? -s : s);
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
+  const float y0 = a * cs.x - b * cs.y, y1 = b * cs.x + a * cs.y;
+  a = y0;
+  b = y1;
+}
+
+__device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    v[2 * i] = f.x, v[2 * i + 1] = f.y;
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ---------------------------------------------------------------------------------------------
+// dsa_rope: x [rows, heads, width] -> out, columns [rot_off, rot_off + 2 pairs) turned, the others
+// copied when out is another buffer.
+
+template <bool VEC>
+__global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeParams p) {
+  __shared__ float2 turns[kWarps][kRopeMaxPairs];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int hblocks = (p.heads + kHeadsPerWarp - 1) / kHeadsPerWarp;
+  const int64_t item = (int64_t)blockIdx.x * kWarps + warp;
+  if (item >= (int64_t)p.rows * hblocks) return;
+  const int64_t row = item / hblocks;
+  const int h0 = (int)(item - row * hblocks) * kHeadsPerWarp;
+  const int nh = min(kHeadsPerWarp, p.heads - h0);
+  const __nv_bfloat16* x = p.x + row * p.x_row_stride + h0 * p.x_head_stride;
+  __nv_bfloat16* out = p.out + row * p.out_row_stride + h0 * p.out_head_stride;
+  float2* cs = turns[warp];
+  fill_turns(p, row, cs);
+  if constexpr (VEC) {
+    const int per = p.half ? p.pairs / 8 : p.pairs / 4;  // items of one head
+    const int n = nh * per;
+    constexpr int U = 4;  // items in flight per lane
+    for (int i0 = lane; i0 < n; i0 += 32 * U) {
+      uint4 a[U], b[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + 32 * u;
+        if (i < n) {
+          const int h = i / per, c = i - h * per;
+          const __nv_bfloat16* src = x + h * p.x_head_stride + p.rot_off + 8 * c;
+          a[u] = *reinterpret_cast<const uint4*>(src);
+          if (p.half) b[u] = *reinterpret_cast<const uint4*>(src + p.pairs);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + 32 * u;
+        if (i < n) {
+          const int h = i / per, c = i - h * per;
+          __nv_bfloat16* dst = out + h * p.out_head_stride + p.rot_off + 8 * c;
+          float va[8], vb[8];
+          unpack8(a[u], va);
+          if (p.half) {
+            unpack8(b[u], vb);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) turn(va[k], vb[k], cs[8 * c + k]);
+            *reinterpret_cast<uint4*>(dst + p.pairs) = pack8(vb);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) turn(va[2 * k], va[2 * k + 1], cs[4 * c + k]);
+          }
+          *reinterpret_cast<uint4*>(dst) = pack8(va);
+        }
+      }
+    }
+    if (p.copy) {
+      const int rest = (p.width - 2 * p.pairs) / 8;
+      for (int i = lane; i < nh * rest; i += 32) {
+        const int h = i / rest;
+        int c = 8 * (i - h * rest);
+        if (c >= p.rot_off) c += 2 * p.pairs;
+        *reinterpret_cast<uint4*>(out + h * p.out_head_stride + c) =
+            *reinterpret_cast<const uint4*>(x + h * p.x_head_stride + c);
+      }
+    }
+  } else {
+    for (int i = lane; i < nh * p.pairs; i += 32) {
+      const int h = i / p.pairs, k = i - h * p.pairs;
+      const int c0 = p.rot_off + (p.half ? k : 2 * k), c1 = p.half ? c0 + p.pairs : c0 + 1;
+      float a = __bfloat162float(x[h * p.x_head_stride + c0]), b = __bfloat162float(x[h * p.x_head_stride + c1]);
+      turn(a, b, cs[k]);
+      out[h * p.out_head_stride + c0] = __float2bfloat16_rn(a);
+      out[h * p.out_head_stride + c1] = __float2bfloat16_rn(b);
+    }
+    if (p.copy) {
+      const int rest = p.width - 2 * p.pairs;
+      for (int i = lane; i < nh * rest; i += 32) {
+        const int h = i / rest;
+        int c = i - h * rest;
+        if (c >= p.rot_off) c += 2 * p.pairs;
+        out[h * p.out_head_stride + c] = x[h * p.x_head_stride + c];
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// dsa_rope_append: x [rows, width], turned, encoded as FMT and written to destination rows.
+
+enum { kFmtBf16 = 0, kFmtRow = 1, kFmtTile = 2, kFmtMx = 3 };
+
+__device__ __forceinline__ int mx_exponent(float amax) {
+  return amax > 0.f ? min(max(ilogbf(amax) - 8, -127), 127) : 0;
+}
+
+__device__ __forceinline__ uint2 encode8(const float (&v)[8], const Quotient& div) {
+  return make_uint2(pack4(to_e4m3(div(v[0])), to_e4m3(div(v[1])), to_e4m3(div(v[2])), to_e4m3(div(v[3]))),
+                    pack4(to_e4m3(div(v[4])), to_e4m3(div(v[5])), to_e4m3(div(v[6])), to_e4m3(div(v[7]))));
+}
+
+__device__ __forceinline__ float amax8(const float (&v)[8]) {
+  float a = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) a = fmaxf(a, fabsf(v[k]));
+  return a;
+}
+
+constexpr int kMaxChunks = 4;  // 8-element chunks per lane: rows up to 1024 elements
+
+// Vector form: lane j holds the 8-element chunks j, j + 32, ... of the row, so 4 consecutive lanes hold
+// a group of 32 and 16 lanes a tile of 128.
+template <int FMT>
+__global__ void __launch_bounds__(32 * kWarps) rope_append_vec_kernel(const RopeParams p) {
+  __shared__ float2 turns[kWarps][kRopeMaxPairs];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = (int64_t)blockIdx.x * kWarps + warp;
+  if (row >= p.rows) return;
+  const int64_t dst = p.dst_rows ? p.dst_rows[row] : row;
+  if (dst < 0) return;
+  if (dst >= p.dst_count) {
+    if (lane == 0) record_error(p.err, DSA_DEVERR_INDEX_RANGE);
+    return;
+  }
+  const __nv_bfloat16* x = p.x + row * p.x_row_stride;
+  const int nch = p.width / 8;
+  uint4 raw[kMaxChunks], other[kMaxChunks];
+#pragma unroll
+  for (int j = 0; j < kMaxChunks; ++j) {
+    const int c = lane + 32 * j;
+    raw[j] = other[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (c < nch) {
+      raw[j] = *reinterpret_cast<const uint4*>(x + 8 * c);
+      const int at = 8 * c - p.rot_off;
+      if (p.half && at >= 0 && at < 2 * p.pairs)
+        other[j] = *reinterpret_cast<const uint4*>(x + 8 * c + (at < p.pairs ? p.pairs : -p.pairs));
+    }
+  }
+  float2* cs = turns[warp];
+  fill_turns(p, row, cs);
+  float v[kMaxChunks][8];
+#pragma unroll
+  for (int j = 0; j < kMaxChunks; ++j) {
+    unpack8(raw[j], v[j]);
+    const int at = 8 * (lane + 32 * j) - p.rot_off;
+    if (at >= 0 && at < 2 * p.pairs) {
+      if (p.half) {
+        float w[8];
+        unpack8(other[j], w);
+        const bool low = at < p.pairs;
+        const float2* t = cs + (low ? at : at - p.pairs);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[j][k] = v[j][k] * t[k].x + w[k] * (low ? -t[k].y : t[k].y);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) turn(v[j][2 * k], v[j][2 * k + 1], cs[at / 2 + k]);
+      }
+    }
+  }
+  uint8_t* out = p.dst + dst * p.dst_row_stride;
+  if constexpr (FMT == kFmtBf16) {
+#pragma unroll
+    for (int j = 0; j < kMaxChunks; ++j) {
+      const int c = lane + 32 * j;
+      if (c < nch) *reinterpret_cast<uint4*>(out + 16 * c) = pack8(v[j]);
+    }
+  } else if constexpr (FMT == kFmtRow) {
+    float a = 0.f;
+#pragma unroll
+    for (int j = 0; j < kMaxChunks; ++j) a = fmaxf(a, amax8(v[j]));
+    const float amax = warp_amax(a);
+    const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+    const Quotient div(s);
+#pragma unroll
+    for (int j = 0; j < kMaxChunks; ++j) {
+      const int c = lane + 32 * j;
+      if (c < nch) *reinterpret_cast<uint2*>(out + 8 * c) = encode8(v[j], div);
+    }
+    if (lane == 0) reinterpret_cast<float*>(p.scale)[dst] = s;
+  } else if constexpr (FMT == kFmtTile) {
+    const int tiles = (p.width + 127) / 128;
+#pragma unroll
+    for (int j = 0; j < kMaxChunks; ++j) {
+      const int c = lane + 32 * j;
+      float a = amax8(v[j]);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+      const float s = a > 0.f ? __fdiv_rn(a, 448.f) : 1.f;
+      if (c < nch) {
+        *reinterpret_cast<uint2*>(out + 8 * c) = encode8(v[j], Quotient(s));
+        if ((lane & 15) == 0) reinterpret_cast<float*>(p.scale)[dst * tiles + c / 16] = s;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kMaxChunks; ++j) {
+      const int c = lane + 32 * j;
+      float a = amax8(v[j]);
+      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+      if (c < nch) {
+        const int e = mx_exponent(a);
+        const float inv = ldexpf(1.f, -e);  // a power of two: exact
+        uint8_t q[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k] = to_e4m3(v[j][k] * inv);
+        *reinterpret_cast<uint2*>(out + 8 * c) =
+            make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+        if ((lane & 3) == 0) p.scale[dst * (p.width / 32) + c / 4] = (uint8_t)(e + 127);
+      }
+    }
+  }
+}
+
+// Any width, pitch and alignment: the same arithmetic, one element per lane and step; each scale
+// group (the row, 128 or 32 elements) is taken in two passes, its maximum and its codes.
+template <int FMT>
+__global__ void __launch_bounds__(32 * kWarps) rope_append_kernel(const RopeParams p) {
+  __shared__ float2 turns[kWarps][kRopeMaxPairs];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = (int64_t)blockIdx.x * kWarps + warp;
+  if (row >= p.rows) return;
+  const int64_t dst = p.dst_rows ? p.dst_rows[row] : row;
+  if (dst < 0) return;
+  if (dst >= p.dst_count) {
+    if (lane == 0) record_error(p.err, DSA_DEVERR_INDEX_RANGE);
+    return;
+  }
+  const __nv_bfloat16* x = p.x + row * p.x_row_stride;
+  float2* cs = turns[warp];
+  fill_turns(p, row, cs);
+  auto value = [&](int c) {
+    const float v = __bfloat162float(x[c]);
+    const int at = c - p.rot_off;
+    if (at < 0 || at >= 2 * p.pairs) return v;
+    const bool low = p.half ? at < p.pairs : (at & 1) == 0;
+    const int k = p.half ? (low ? at : at - p.pairs) : at >> 1;
+    const float w = __bfloat162float(x[c + (p.half ? (low ? p.pairs : -p.pairs) : (low ? 1 : -1))]);
+    return v * cs[k].x + w * (low ? -cs[k].y : cs[k].y);
+  };
+  uint8_t* out = p.dst + dst * p.dst_row_stride;
+  if constexpr (FMT == kFmtBf16) {
+    for (int c = lane; c < p.width; c += 32)
+      *reinterpret_cast<__nv_bfloat16*>(out + 2 * c) = __float2bfloat16_rn(value(c));
+  } else {
+    const int group = FMT == kFmtRow ? p.width : FMT == kFmtTile ? 128 : 32;
+    const int groups = (p.width + group - 1) / group;
+    for (int g = 0; g < groups; ++g) {
+      const int lo = g * group, hi = min(lo + group, p.width);
+      float a = 0.f;
+      for (int c = lo + lane; c < hi; c += 32) a = fmaxf(a, fabsf(value(c)));
+      const float amax = warp_amax(a);
+      if constexpr (FMT == kFmtMx) {
+        const int e = mx_exponent(amax);
+        const float inv = ldexpf(1.f, -e);
+        for (int c = lo + lane; c < hi; c += 32) out[c] = to_e4m3(value(c) * inv);
+        if (lane == 0) p.scale[dst * groups + g] = (uint8_t)(e + 127);
+      } else {
+        const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+        const Quotient div(s);
+        for (int c = lo + lane; c < hi; c += 32) out[c] = to_e4m3(div(value(c)));
+        if (lane == 0) reinterpret_cast<float*>(p.scale)[dst * groups + g] = s;
+      }
+    }
+  }
+}
+
+// What both entries check of the rotation itself; fills the pair -> axis table.
+dsa_status rope_args(RopeParams* p, int width, int rot_off, int rot_dim, const int32_t* pos, int n_axes,
+                     const uint8_t* pair_axis, const float* inv_freq, int style, bool any_rows) {
+  if (width < 1 || rot_off < 0 || rot_dim < 2 || rot_dim % 2 != 0 || (int64_t)rot_off + rot_dim > width || n_axes < 1)
+    return DSA_ERR_INVALID_ARG;
+  if (style != DSA_ROPE_HALF && style != DSA_ROPE_PAIRS) return DSA_ERR_INVALID_ARG;
+  if (rot_dim > 2 * kRopeMaxPairs || n_axes > 4) return DSA_ERR_UNSUPPORTED;
+  if (n_axes > 1 && !pair_axis) return DSA_ERR_INVALID_ARG;
+  if (any_rows && (!pos || !inv_freq)) return DSA_ERR_INVALID_ARG;
+  p->pairs = rot_dim / 2;
+  for (int i = 0; i < p->pairs; ++i) {
+    const int a = pair_axis ? pair_axis[i] : 0;
+    if (a >= n_axes) return DSA_ERR_INVALID_ARG;
+    p->axis[i] = (uint8_t)a;
+  }
+  p->width = width;
+  p->rot_off = rot_off;
+  p->pos = pos;
+  p->pos_stride = n_axes;
+  p->inv_freq = inv_freq;
+  p->half = style == DSA_ROPE_HALF;
+  return DSA_OK;
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" {
+
+dsa_status dsa_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride, int rows, int heads, int width,
+                    int rot_off, int rot_dim, const int32_t* pos, int n_axes, const uint8_t* pair_axis,
+                    const float* inv_freq, int style, int inverse, void* out, int64_t out_row_stride,
+                    int64_t out_head_stride, void* stream) {
+  RopeParams p = {};
+  if (rows < 0 || heads < 1) return DSA_ERR_INVALID_ARG;
+  dsa_status s = rope_args(&p, width, rot_off, rot_dim, pos, n_axes, pair_axis, inv_freq, style, rows > 0);
+  if (s != DSA_OK) return s;
+  if (heads > 1 && (x_head_stride < width || out_head_stride < width)) return DSA_ERR_INVALID_ARG;
+  if (rows > 1 && (x_row_stride < width || out_row_stride < width)) return DSA_ERR_INVALID_ARG;
+  if (rows == 0) return DSA_OK;
+  if (!x || !out || !aligned2(x) || !aligned2(out)) return DSA_ERR_INVALID_ARG;
+  // in place means the same elements: another layout over the same memory would race
+  if (x == out && ((rows > 1 && x_row_stride != out_row_stride) || (heads > 1 && x_head_stride != out_head_stride)))
+    return DSA_ERR_INVALID_ARG;
+  if ((s = check_device_arch()) != DSA_OK) return s;
+  p.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.x_row_stride = x_row_stride;
+  p.x_head_stride = heads > 1 ? x_head_stride : 0;
+  p.out_row_stride = out_row_stride;
+  p.out_head_stride = heads > 1 ? out_head_stride : 0;
+  p.rows = rows;
+  p.heads = heads;
+  p.inverse = inverse != 0;
+  p.copy = x != out && width > rot_dim;
+  const bool vec = rot_off % 8 == 0 && p.pairs % 8 == 0 && (!p.copy || width % 8 == 0) && aligned(x, 16) &&
+                   aligned(out, 16) && (rows == 1 || (x_row_stride % 8 == 0 && out_row_stride % 8 == 0)) &&
+                   p.x_head_stride % 8 == 0 && p.out_head_stride % 8 == 0;
+  const int64_t items = (int64_t)rows * ((heads + kHeadsPerWarp - 1) / kHeadsPerWarp);
+  const int64_t grid = (items + kWarps - 1) / kWarps;
+  if (grid >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+  auto kern = vec ? rope_kernel<true> : rope_kernel<false>;
+  kern<<<(unsigned)grid, 32 * kWarps, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int width, int rot_off, int rot_dim,
+                           const int32_t* pos, int n_axes, const uint8_t* pair_axis, const float* inv_freq, int style,
+                           dsa_dtype dtype, void* dst, int64_t dst_row_stride, int64_t dst_count, void* scale,
+                           const int64_t* dst_rows, void* stream) {
+  RopeParams p = {};
+  if (rows < 0 || dst_count < 0) return DSA_ERR_INVALID_ARG;
+  dsa_status s = rope_args(&p, width, rot_off, rot_dim, pos, n_axes, pair_axis, inv_freq, style, rows > 0);
+  if (s != DSA_OK) return s;
+  if (dtype != DSA_BF16 && dtype != DSA_FP8_E4M3 && dtype != DSA_FP8_E4M3_T128 && dtype != DSA_MXFP8_E4M3)
+    return DSA_ERR_UNSUPPORTED;
+  const int64_t elem = dtype == DSA_BF16 ? 2 : 1;
+  if (dst_row_stride < width * elem || dst_row_stride % elem != 0 || (rows > 1 && x_row_stride < width))
+    return DSA_ERR_INVALID_ARG;
+  if (dtype == DSA_MXFP8_E4M3 && width % 32 != 0) return DSA_ERR_INVALID_ARG;
+  if (!dst_rows && rows > dst_count) return DSA_ERR_INVALID_ARG;
+  if (rows == 0) return DSA_OK;
+  if (!x || !dst || !aligned2(x) || (elem == 2 && !aligned2(dst))) return DSA_ERR_INVALID_ARG;
+  if (dtype != DSA_BF16 && !scale) return DSA_ERR_INVALID_ARG;
+  if ((dtype == DSA_FP8_E4M3 || dtype == DSA_FP8_E4M3_T128) && !aligned(scale, 4)) return DSA_ERR_INVALID_ARG;
+  if ((s = check_device_arch()) != DSA_OK) return s;
+  p.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  p.x_row_stride = x_row_stride;
+  p.rows = rows;
+  p.dst = reinterpret_cast<uint8_t*>(dst);
+  p.dst_row_stride = dst_row_stride;
+  p.dst_count = dst_count;
+  p.scale = reinterpret_cast<uint8_t*>(scale);
+  p.dst_rows = dst_rows;
+  p.err = device_error_word();
+  const uintptr_t out_align = elem == 2 ? 16 : 8;
+  const bool vec = width % 8 == 0 && width <= 256 * kMaxChunks && rot_off % 8 == 0 &&
+                   p.pairs % (p.half ? 8 : 4) == 0 && aligned(x, 16) && (rows == 1 || x_row_stride % 8 == 0) &&
+                   aligned(dst, out_align) && dst_row_stride % (int64_t)out_align == 0;
+  void (*kern)(const RopeParams) = nullptr;
+  switch (dtype) {
+    case DSA_BF16: kern = vec ? rope_append_vec_kernel<kFmtBf16> : rope_append_kernel<kFmtBf16>; break;
+    case DSA_FP8_E4M3: kern = vec ? rope_append_vec_kernel<kFmtRow> : rope_append_kernel<kFmtRow>; break;
+    case DSA_FP8_E4M3_T128: kern = vec ? rope_append_vec_kernel<kFmtTile> : rope_append_kernel<kFmtTile>; break;
+    default: kern = vec ? rope_append_vec_kernel<kFmtMx> : rope_append_kernel<kFmtMx>; break;
+  }
+  kern<<<(rows + kWarps - 1) / kWarps, 32 * kWarps, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+}  // extern "C"
