@@ -400,6 +400,57 @@ dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int wi
                            void* scale, const int64_t* dst_rows, void* stream);
 
 /* --------------------------------------------------------------------------------------------
+ * dsa_tree_attn -- exact softmax attention of drafted tokens over the whole visible latent cache:
+ * a step that verifies drafts (a chain of tokens, or a tree of them), a decode step of a dense layer,
+ * or one whose contexts are no longer than K, where a selection would keep every row.  The
+ * layouts are those of dsa_sparse_attn (576 / 512 latent row, V = its first 512 columns) and of
+ * the paged caches of dsa_args.
+ *
+ * Sequence s has c = n_ctx[s] cached positions (clamped to [0, L]) and m = n_new[s] drafted tokens
+ * (clamped to [0, q_per_seq]; NULL: q_per_seq), whose rows are already in the cache at positions c ...
+ * c + m - 1 (those at L or beyond do not exist).  Query t = s * q_per_seq + i is node i.  It sees
+ * the positions below c, and position c + j for every j < m whose bit is set in its mask row:
+ *   tree_mask  device uint32 [n_seq * q_per_seq][ceil(q_per_seq / 32)], bit j % 32 of word j / 32;
+ *              any set of nodes (usually its ancestors and itself); NULL: the nodes j <= i (a chain)
+ *   logit[p] = sm_scale * q[t,h] . Kv[p];  out[t,h,:] = sum_p softmax(logit)[p] * Kv[p, :512]  (bf16)
+ *   lse[t,h] = ln sum_p exp(logit[p])                                                        (fp32)
+ * over the positions it sees.  A node that sees nothing, and a node i >= m (padding), gets out = 0
+ * and lse = -inf.  The contents of a cache row do not matter to a node that does not see it (a
+ * position past the end, another branch of the tree: infinities and NaN included); a NaN in a row
+ * that a node sees makes that node's output NaN.
+ *   q          device bf16 [n_seq * q_per_seq, H, 576]
+ *   kv         row r of sequence s at kv + s*kv_seq_stride + r*kv_row_stride bytes; with block_table
+ *              a pool of num_blocks * block_size rows (see dsa_args: block_size a multiple of 64)
+ *   kv_scale   device fp32 of the rows as in dsa_sparse_attn (pool rows when paged); NULL for bf16
+ *   out        device bf16 [n_seq * q_per_seq, H, 512];  lse  device fp32 [..., H] or NULL
+ * A block id outside [0, num_blocks) on the way records DSA_DEVERR_INDEX_RANGE, and its positions are
+ * not seen.  ws: device memory of dsa_tree_attn_workspace_size bytes, 16-byte aligned, contents
+ * irrelevant; calls (and captured graphs) that share it must not run at the same time.
+ * Supported: D_qk = 576, D_v = 512; kv_dtype DSA_BF16, DSA_FP8_E4M3 or DSA_FP8_E4M3_T128 (finite
+ * codes); 1 <= H <= 128; 1 <= q_per_seq <= 1024; n_seq <= 4096; pointers 16-byte aligned, row
+ * strides multiples of 16 bytes.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct dsa_tree_args {
+  int n_seq, q_per_seq, L, H, D_qk, D_v;
+  float sm_scale;
+  dsa_dtype kv_dtype;
+  const int32_t* n_ctx;
+  const int32_t* n_new;
+  const uint32_t* tree_mask;
+  const void* q;
+  const void* kv;
+  const float* kv_scale;
+  int64_t kv_row_stride, kv_seq_stride;
+  void* out;
+  float* lse;
+  const int32_t* block_table; /* device int32 [n_seq][max_blocks] or NULL */
+  int block_size, max_blocks, num_blocks;
+} dsa_tree_args;
+
+dsa_status dsa_tree_attn_workspace_size(const dsa_tree_args* a, size_t* bytes);
+dsa_status dsa_tree_attn(const dsa_tree_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/* --------------------------------------------------------------------------------------------
  * Fused chain: dsa_decode / dsa_prefill run steps 1-3 back to back on `stream` (the indexer's
  * scoring, weighting and Top-K chain followed by the sparse gather kernel, Day 0 Support for New LLM
  * Architectures, Key Optimization 1), keeping the scores in the workspace.  dsa_decode expects

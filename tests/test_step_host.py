@@ -163,3 +163,64 @@ def test_oracle_tree_attention_is_masked_attention():
     # no context and an empty mask row: nothing is seen
     out, lse = oracle.tree_attention(q, rows, 0, N, np.zeros((N, N), bool), 0.2, DV)
     assert np.all(out == 0) and np.all(lse == -np.inf)
+
+
+# ---------------------------------------------------------------------------------------------
+# tree attention: refusals, and the argument struct
+
+def _tree_args(**kw):
+    from top_sparse_attention_gb300 import _native as N
+
+    a = N.DsaTreeArgs()
+    base = dict(n_seq=2, q_per_seq=4, L=128, H=16, D_qk=576, D_v=512, sm_scale=0.04, kv_dtype=0, n_ctx=F, q=F, kv=F, out=F,
+                kv_row_stride=1152, kv_seq_stride=1152 * 128)
+    base.update(kw)
+    for k, v in base.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n_seq=-1), 1), (dict(q_per_seq=0), 1), (dict(L=-1), 1), (dict(H=0), 1), (dict(n_ctx=None), 1), (dict(q=None), 1),
+    (dict(out=None), 1), (dict(kv=None), 1), (dict(q=24), 1), (dict(kv=24), 1), (dict(out=24), 1),
+    (dict(D_qk=512), 2), (dict(D_v=256), 2), (dict(H=129), 2), (dict(q_per_seq=1025), 2), (dict(n_seq=4097), 2), (dict(kv_dtype=2), 2),
+    (dict(kv_row_stride=1150), 1), (dict(kv_row_stride=1136), 1), (dict(kv_seq_stride=1000), 1),
+    (dict(kv_dtype=1, kv_row_stride=576, kv_seq_stride=576 * 128), 1),       # no scales
+    (dict(block_table=F, block_size=48, max_blocks=4, num_blocks=8), 1), (dict(block_table=F, block_size=64, max_blocks=1, num_blocks=8), 1),
+    (dict(block_table=F, block_size=64, max_blocks=2, num_blocks=0), 1), (dict(block_table=F, block_size=64, max_blocks=2, num_blocks=1 << 25), 2),
+])
+def test_tree_attn_refusals(lib, kw, status):
+    import ctypes
+
+    a, n = _tree_args(**kw), ctypes.c_size_t(0)
+    assert lib.dsa_tree_attn_workspace_size(ctypes.byref(a), ctypes.byref(n)) == status
+    assert lib.dsa_tree_attn(ctypes.byref(a), F, 1 << 40, None) == status
+
+
+def test_tree_attn_nothing_to_do_and_missing_arguments(lib):
+    import ctypes
+
+    a, n = _tree_args(n_seq=0, n_ctx=None, q=None, kv=None, out=None), ctypes.c_size_t(7)
+    assert lib.dsa_tree_attn_workspace_size(ctypes.byref(a), ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.dsa_tree_attn(ctypes.byref(a), None, 0, None) == 0
+    assert lib.dsa_tree_attn(None, None, 0, None) == 1
+    assert lib.dsa_tree_attn_workspace_size(ctypes.byref(a), None) == 1
+
+
+def test_tree_args_layout_matches_c(tmp_path, lib):
+    import ctypes
+    import os
+    import subprocess
+
+    from top_sparse_attention_gb300 import _native as N
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    fields = [f for f, _ in N.DsaTreeArgs._fields_]
+    body = "\n".join(f'  printf("%zu\\n", offsetof(dsa_tree_args, {f}));' for f in fields)
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "dsa.h"\nint main(void){\n'
+                   f'  printf("%zu\\n", sizeof(dsa_tree_args));\n{body}\n  return 0;\n}}\n')
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"), str(src), "-o",
+                    str(tmp_path / "layout")], check=True)
+    got = [int(v) for v in subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [ctypes.sizeof(N.DsaTreeArgs)] + [getattr(N.DsaTreeArgs, f).offset for f in fields]

@@ -27,6 +27,7 @@ EXPORTS = (
     "dsa_workspace_size", "dsa_launch_count", "dsa_decode", "dsa_prefill", "dsa_topk_noalloc",
     "dsa_selftest_wait_timeout", "dsa_topk_pairs", "dsa_topk_merge", "dsa_sparse_attn_partial",
     "dsa_attn_combine", "dsa_set_attn_kernel", "dsa_block_plan", "dsa_rope", "dsa_rope_append",
+    "dsa_tree_attn", "dsa_tree_attn_workspace_size",
 )
 
 
@@ -54,6 +55,21 @@ class DsaArgs(ctypes.Structure):
         ("kv_row_stride", ctypes.c_int64), ("kv_seq_stride", ctypes.c_int64),
         ("v_row_stride", ctypes.c_int64), ("v_seq_stride", ctypes.c_int64),
         ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("idx_out", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("block_size", ctypes.c_int), ("max_blocks", ctypes.c_int), ("num_blocks", ctypes.c_int),
+    ]
+
+
+class DsaTreeArgs(ctypes.Structure):
+    """Mirror of struct dsa_tree_args."""
+    _fields_ = [
+        ("n_seq", ctypes.c_int), ("q_per_seq", ctypes.c_int), ("L", ctypes.c_int),
+        ("H", ctypes.c_int), ("D_qk", ctypes.c_int), ("D_v", ctypes.c_int),
+        ("sm_scale", ctypes.c_float), ("kv_dtype", ctypes.c_int),
+        ("n_ctx", ctypes.c_void_p), ("n_new", ctypes.c_void_p), ("tree_mask", ctypes.c_void_p),
+        ("q", ctypes.c_void_p), ("kv", ctypes.c_void_p), ("kv_scale", ctypes.c_void_p),
+        ("kv_row_stride", ctypes.c_int64), ("kv_seq_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
         ("block_table", ctypes.c_void_p),
         ("block_size", ctypes.c_int), ("max_blocks", ctypes.c_int), ("num_blocks", ctypes.c_int),
     ]
@@ -89,6 +105,8 @@ def _load():
         "dsa_block_plan": (I, [P, P, I, I, I, P, P, I, I, P, I, I, P, P, P, P, P, P, P]),
         "dsa_rope": (I, [P, I64, I64, I, I, I, I, I, P, I, ctypes.c_char_p, P, I, I, P, I64, I64, P]),
         "dsa_rope_append": (I, [P, I64, I, I, I, I, P, I, ctypes.c_char_p, P, I, I, P, I64, I64, P, P, P]),
+        "dsa_tree_attn": (I, [ctypes.POINTER(DsaTreeArgs), P, SZ, P]),
+        "dsa_tree_attn_workspace_size": (I, [ctypes.POINTER(DsaTreeArgs), ctypes.POINTER(SZ)]),
         "dsa_workspace_size": (I, [ctypes.POINTER(DsaArgs), I, ctypes.POINTER(SZ)]),
         "dsa_launch_count": (I, [ctypes.POINTER(DsaArgs), I, ctypes.POINTER(ctypes.c_int)]),
         "dsa_decode": (I, [ctypes.POINTER(DsaArgs), P, SZ, P]),

@@ -16,7 +16,7 @@ __all__ = ["dsa_index_score", "dsa_topk", "dsa_topk_noalloc", "dsa_topk_pairs", 
            "dsa_sparse_attn_partial", "dsa_attn_combine", "dsa_sparse_attn", "DsaCall", "dsa_decode", "dsa_prefill",
            "dsa_workspace_size", "dsa_launch_count", "dsa_get_device_error", "ld_scores_for",
            "dsa_quantize_mxfp8", "dsa_quantize_fp8_rows", "dsa_quantize_fp8_tiles",
-           "dsa_block_plan", "BlockPlan", "dsa_rope", "dsa_rope_append"]
+           "dsa_block_plan", "BlockPlan", "dsa_rope", "dsa_rope_append", "dsa_tree_attn"]
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -503,6 +503,79 @@ def dsa_rope_append(x, pos, inv_freq, dst, *, scale=None, dst_rows=None, rot_off
          int(rot_dim), pos.data_ptr(), n_axes, pair_axis, inv_freq.data_ptr(), code, kind, dst.data_ptr(),
          (dst.stride(0) if dst.shape[0] > 1 else width) * dst.element_size(), dst.shape[0], None if kind == N.DSA_BF16 else scale.data_ptr(),
          _ptr(dst_rows))
+
+
+def dsa_tree_attn(q, kv, n_ctx, *, sm_scale, q_per_seq, n_new=None, tree_mask=None, kv_scale=None, block_table=None,
+                  block_size=0, L=None, out=None, lse=None, ws=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of drafted tokens over the visible latent cache (see dsa.h): (out [T, H, 512] bf16,
+    lse [T, H] fp32).  q bf16 [n_seq * q_per_seq, H, 576]; kv [n_seq, L, 576] bf16 or uint8 E4M3
+    codes (kv_scale [n_seq, L] or [n_seq, L, 5]), or with `block_table` (int32 [n_seq, max_blocks]) and
+    `block_size` a pool [rows, 576] (kv_scale [rows] or [rows, 5]) with `L` positions per sequence at
+    most.  n_ctx, n_new int32 [n_seq]; tree_mask int32 or uint32 [T, ceil(q_per_seq / 32)] bits, None
+    for a chain.  `ws` (uint8) is scratch that later calls on the same stream may reuse."""
+    what = "dsa_tree_attn"
+    dev = _cuda_device(what, q)
+    _check(what, dev, "q", q, torch.bfloat16, 3)
+    _check(what, dev, "n_ctx", n_ctx, torch.int32, 1)
+    _check(what, dev, "n_new", n_new, torch.int32, 1)
+    T, H, D = q.shape
+    n_seq = n_ctx.shape[0]
+    if q_per_seq < 1 or T != n_seq * q_per_seq or (n_new is not None and n_new.shape[0] != n_seq):
+        raise ValueError(f"{what}: {T} queries are not q_per_seq = {q_per_seq} nodes of {n_seq} sequences")
+    if tree_mask is not None:
+        _check(what, dev, "tree_mask", tree_mask, torch.uint32 if tree_mask.dtype == torch.uint32 else torch.int32, 2)
+        if tree_mask.shape[0] != T or tree_mask.shape[1] != (q_per_seq + 31) // 32:
+            raise ValueError(f"{what}: tree_mask must be [{T}, {(q_per_seq + 31) // 32}], got {tuple(tree_mask.shape)}")
+    paged = block_table is not None
+    axes = 2 if paged else 3
+    _check(what, dev, "kv", kv, torch.bfloat16 if kv.dtype == torch.bfloat16 else torch.uint8, axes, dense=False)
+    if kv.shape[-1] < D or kv.stride(-1) != 1:
+        raise ValueError(f"{what}: kv rows must hold {D} dense columns")
+    a = N.DsaTreeArgs()
+    a.kv_dtype = N.DSA_BF16
+    if kv.dtype == torch.uint8:
+        if kv_scale is None:
+            raise ValueError(f"{what}: E4M3 rows need their scales")
+        a.kv_dtype = N.DSA_FP8_E4M3_T128 if kv_scale.dim() == axes else N.DSA_FP8_E4M3
+        _check(what, dev, "kv_scale", kv_scale, torch.float32)
+        want = tuple(kv.shape[:-1]) + ((-(-D // 128),) if kv_scale.dim() == axes else ())
+        if tuple(kv_scale.shape) != want:
+            raise ValueError(f"{what}: kv_scale must be {list(want)}, got {tuple(kv_scale.shape)}")
+        a.kv_scale = kv_scale.data_ptr()
+    elem = kv.element_size()
+    if paged:
+        _check(what, dev, "block_table", block_table, torch.int32, 2)
+        if L is None or block_size <= 0 or block_table.shape[0] != n_seq:
+            raise ValueError(f"{what}: paged caches need L, block_size and one row of block_table per sequence")
+        a.block_table, a.block_size, a.max_blocks = block_table.data_ptr(), int(block_size), block_table.shape[1]
+        a.num_blocks = kv.shape[0] // int(block_size)
+        a.kv_row_stride = kv.stride(0) * elem
+    else:
+        if kv.shape[0] != n_seq or (L is not None and L != kv.shape[1]):
+            raise ValueError(f"{what}: kv must be [{n_seq}, L, {D}], got {tuple(kv.shape)}")
+        L = kv.shape[1]
+        a.kv_row_stride, a.kv_seq_stride = kv.stride(1) * elem, kv.stride(0) * elem
+    if out is None:
+        out = torch.empty(T, H, 512, dtype=torch.bfloat16, device=dev)
+    else:
+        _check(what, dev, "out", out, torch.bfloat16, 3)
+    if lse is None:
+        lse = torch.empty(T, H, dtype=torch.float32, device=dev)
+    else:
+        _check(what, dev, "lse", lse, torch.float32, 2)
+    if tuple(out.shape) != (T, H, 512) or tuple(lse.shape) != (T, H):
+        raise ValueError(f"{what}: out must be [{T}, {H}, 512], lse [{T}, {H}]")
+    a.n_seq, a.q_per_seq, a.L, a.H, a.D_qk, a.D_v, a.sm_scale = n_seq, int(q_per_seq), int(L), H, D, 512, float(sm_scale)
+    a.n_ctx, a.n_new, a.tree_mask = n_ctx.data_ptr(), _ptr(n_new), _ptr(tree_mask)
+    a.q, a.kv, a.out, a.lse = q.data_ptr(), kv.data_ptr(), out.data_ptr(), lse.data_ptr()
+    need = ctypes.c_size_t(0)
+    N.check(N.lib.dsa_tree_attn_workspace_size(ctypes.byref(a), ctypes.byref(need)), what)
+    if ws is None:
+        ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+    else:
+        _check(what, dev, "ws", ws, torch.uint8, 1)
+    _run(what, N.lib.dsa_tree_attn, dev, stream, ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel())
+    return out, lse
 
 
 def dsa_launch_count(args: N.DsaArgs, prefill: bool) -> int:

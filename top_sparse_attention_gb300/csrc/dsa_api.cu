@@ -313,6 +313,58 @@ dsa_status check_args(const dsa_args* a, int prefill) {
                            a->out);
 }
 
+dsa_status check_tree(const dsa_tree_args* a) {
+  if (!a || a->n_seq < 0 || a->q_per_seq < 1 || a->L < 0 || a->H < 1) return DSA_ERR_INVALID_ARG;
+  if (a->kv_dtype != DSA_BF16 && a->kv_dtype != DSA_FP8_E4M3 && a->kv_dtype != DSA_FP8_E4M3_T128)
+    return DSA_ERR_UNSUPPORTED;
+  if (a->D_qk != 576 || a->D_v != 512 || a->H > 128 || a->q_per_seq > 1024 || a->n_seq > 4096) return DSA_ERR_UNSUPPORTED;
+  const int64_t elem = a->kv_dtype == DSA_BF16 ? 2 : 1;
+  if (a->block_table) {
+    if (a->block_size <= 0 || a->block_size % 64 != 0 || a->num_blocks <= 0 || a->max_blocks < 0) return DSA_ERR_INVALID_ARG;
+    if ((int64_t)a->max_blocks * a->block_size < a->L) return DSA_ERR_INVALID_ARG;
+    if ((int64_t)a->num_blocks * a->block_size >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+  }
+  if (a->n_seq == 0) return DSA_OK;
+  if (!a->n_ctx || !a->q || !a->out || !aligned16(a->q) || !aligned16(a->out)) return DSA_ERR_INVALID_ARG;
+  if (a->L == 0) return DSA_OK;
+  if (!a->kv || !aligned16(a->kv)) return DSA_ERR_INVALID_ARG;
+  if (a->kv_row_stride % 16 != 0 || a->kv_row_stride < 576 * elem) return DSA_ERR_INVALID_ARG;
+  if (!a->block_table && a->n_seq > 1 &&
+      (a->kv_seq_stride % 16 != 0 || a->kv_seq_stride < (int64_t)a->L * a->kv_row_stride))
+    return DSA_ERR_INVALID_ARG;
+  if (a->kv_dtype != DSA_BF16 && !a->kv_scale) return DSA_ERR_INVALID_ARG;
+  return DSA_OK;
+}
+
+TreeAttnParams tree_params(const dsa_tree_args& a) {
+  TreeAttnParams p = {};
+  p.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
+  p.kv = reinterpret_cast<const uint8_t*>(a.kv);
+  p.kv_scale = a.kv_scale;
+  p.kv_row_stride = a.kv_row_stride;
+  p.kv_seq_stride = a.n_seq > 1 ? a.kv_seq_stride : 0;
+  p.n_ctx = a.n_ctx;
+  p.n_new = a.n_new;
+  p.mask = a.tree_mask;
+  p.n_seq = a.n_seq;
+  p.q_per_seq = a.q_per_seq;
+  p.mask_words = (a.q_per_seq + 31) / 32;
+  p.L = a.L;
+  p.H = a.H;
+  p.kv_fp8 = a.kv_dtype != DSA_BF16;
+  p.nsc = a.kv_dtype == DSA_BF16 ? 0 : a.kv_dtype == DSA_FP8_E4M3 ? 1 : 5;
+  p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  p.out = reinterpret_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  if (a.block_table) {
+    p.pages.table = a.block_table;
+    p.pages.block_size = a.block_size;
+    p.pages.max_blocks = a.max_blocks;
+    p.pages.num_blocks = a.num_blocks;
+  }
+  return p;
+}
+
 dsa_status run_chain(const dsa_args* a, void* ws, size_t ws_bytes, void* stream, int prefill) {
   dsa_status s = check_args(a, prefill);
   if (s != DSA_OK) return s;
@@ -657,6 +709,25 @@ dsa_status dsa_launch_count(const dsa_args* a, int prefill, int* launches) {
   }
   *launches = n;
   return DSA_OK;
+}
+
+dsa_status dsa_tree_attn_workspace_size(const dsa_tree_args* a, size_t* bytes) {
+  if (!bytes) return DSA_ERR_INVALID_ARG;
+  const dsa_status s = check_tree(a);
+  if (s != DSA_OK) return s;
+  *bytes = a->n_seq > 0 ? tree_attn_ws_bytes(tree_params(*a)) : 0;
+  return DSA_OK;
+}
+
+dsa_status dsa_tree_attn(const dsa_tree_args* a, void* ws, size_t ws_bytes, void* stream) {
+  dsa_status s = check_tree(a);
+  if (s != DSA_OK || a->n_seq == 0) return s;
+  TreeAttnParams p = tree_params(*a);
+  const size_t need = tree_attn_ws_bytes(p);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return DSA_ERR_WORKSPACE;
+  if ((s = check_device()) != DSA_OK) return s;
+  p.err = device_error_ptr();
+  return from_cuda(launch_tree_attn(p, ws, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 dsa_status dsa_decode(const dsa_args* a, void* ws, size_t ws_bytes, void* stream) {

@@ -234,6 +234,47 @@ struct RopeParams {
   int* err;                // device error word
 };
 
+// ---------------------------------------------------------------------------------------------
+// attention of drafted tokens over the latent cache
+
+struct TreeAttnParams {
+  const __nv_bfloat16* q;  // [n_seq * q_per_seq, H, 576]
+  const uint8_t* kv;
+  const float* kv_scale;   // nsc per row, or null
+  int64_t kv_row_stride, kv_seq_stride;
+  const int32_t* n_ctx;    // [n_seq]
+  const int32_t* n_new;    // [n_seq] or null (q_per_seq)
+  const uint32_t* mask;    // [n_seq * q_per_seq][mask_words] or null (chain)
+  int n_seq, q_per_seq, mask_words, L, H;
+  bool kv_fp8;
+  int nsc;                 // scales per row: 0 (bf16), 1, or 5 (128-element tiles)
+  float scale_log2;        // sm_scale * log2(e)
+  __nv_bfloat16* out;      // [n_seq * q_per_seq, H, 512]
+  float* lse;              // [n_seq * q_per_seq, H] or null
+  PagedCache pages;        // table null: contiguous per sequence
+  int* err;                // device error word
+};
+
+// Row of position `pos` within the sequence's cache (contiguous) or the pool (paged); -1 for a block id
+// outside the pool.
+__device__ __forceinline__ int64_t tree_row(const TreeAttnParams& p, int seq, int pos) {
+  if (!p.pages.table) return pos;
+  const int32_t b = __ldg(p.pages.table + (int64_t)seq * p.pages.max_blocks + pos / p.pages.block_size);
+  if ((unsigned)b >= (unsigned)p.pages.num_blocks) return -1;
+  return (int64_t)b * p.pages.block_size + pos % p.pages.block_size;
+}
+
+// Whether node `node` of sequence `seq` sees position `pos` (below the sequence's end).
+__device__ __forceinline__ bool tree_sees(const TreeAttnParams& p, int seq, int node, int pos, int ctx) {
+  const int j = pos - ctx;
+  if (j < 0) return true;
+  if (!p.mask) return j <= node;
+  return (p.mask[((int64_t)seq * p.q_per_seq + node) * p.mask_words + (j >> 5)] >> (j & 31)) & 1u;
+}
+
+size_t tree_attn_ws_bytes(const TreeAttnParams& p);
+cudaError_t launch_tree_attn(const TreeAttnParams& p, void* ws, cudaStream_t stream);
+
 // Argument checks and device facts shared with entry points defined outside dsa_api.cu.
 dsa_status check_topk_args(const float* scores, int64_t ld_scores, int T, int q_per_seq, int q_pos0,
                            const int32_t* n_valid, int L, int K, const int32_t* idx);
