@@ -427,7 +427,7 @@ dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int wi
  * not seen.  ws: device memory of dsa_tree_attn_workspace_size bytes, 16-byte aligned, contents
  * irrelevant; calls (and captured graphs) that share it must not run at the same time.
  * Supported: D_qk = 576, D_v = 512; kv_dtype DSA_BF16, DSA_FP8_E4M3 or DSA_FP8_E4M3_T128 (finite
- * codes); 1 <= H <= 128; 1 <= q_per_seq <= 1024; n_seq <= 4096; pointers 16-byte aligned, row
+ * codes); 1 <= H <= 128; 1 <= q_per_seq <= 1024; n_seq <= 4096; L <= 2^31 - 4097; pointers 16-byte aligned, row
  * strides multiples of 16 bytes.
  * ------------------------------------------------------------------------------------------ */
 typedef struct dsa_tree_args {

@@ -317,7 +317,9 @@ dsa_status check_tree(const dsa_tree_args* a) {
   if (!a || a->n_seq < 0 || a->q_per_seq < 1 || a->L < 0 || a->H < 1) return DSA_ERR_INVALID_ARG;
   if (a->kv_dtype != DSA_BF16 && a->kv_dtype != DSA_FP8_E4M3 && a->kv_dtype != DSA_FP8_E4M3_T128)
     return DSA_ERR_UNSUPPORTED;
-  if (a->D_qk != 576 || a->D_v != 512 || a->H > 128 || a->q_per_seq > 1024 || a->n_seq > 4096) return DSA_ERR_UNSUPPORTED;
+  if (a->D_qk != 576 || a->D_v != 512 || a->H > 128 || a->q_per_seq > 1024 || a->n_seq > 4096 ||
+      a->L > INT32_MAX - 4096)
+    return DSA_ERR_UNSUPPORTED;
   const int64_t elem = a->kv_dtype == DSA_BF16 ? 2 : 1;
   if (a->block_table) {
     if (a->block_size <= 0 || a->block_size % 64 != 0 || a->num_blocks <= 0 || a->max_blocks < 0) return DSA_ERR_INVALID_ARG;

@@ -133,18 +133,6 @@ __device__ __forceinline__ uint32_t bf16x2_of_e4m3_f32(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 
-// Two E4M3 codes (the bytes of x picked by `sel` into bits 8..15 and 24..31) as two bf16, exactly.
-// The code s.eeee.mmm placed as the bf16 pattern s.0000eeee.mmm0000 has 2^-120 times the code's
-// value: for e >= 1 both read 2^(e - bias) (1 + m/8), with biases 127 and 7; for e = 0 both are
-// subnormal, m/8 x 2^-126 and m/8 x 2^-6.  Scaling by 2^120 is exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t x, uint32_t sel) {
-  const uint32_t t = __byte_perm(x, 0u, sel);
-  const uint32_t pat = (t & 0x80008000u) | ((t & 0x7F007F00u) >> 4);
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(pat), "r"(0x7B807B80u));  // x 2^120
-  return r;
-}
-
 // Bulk copy of `bytes` (a multiple of 16) from global to shared memory on the TMA engine.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
