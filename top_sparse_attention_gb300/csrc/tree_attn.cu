@@ -142,6 +142,12 @@ __device__ __forceinline__ bool softmax_any(bool pred) {
   return r != 0;
 }
 
+// A value that is the same in all lanes, as one the compiler knows to be so (a warp-wide reduction writes
+// a uniform register): the MMA issuer's loop bounds and addresses go through it, because operands in
+// per-lane registers cost the issue of each instruction more than its execution (67 against 32 to 48
+// cycles).
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -151,6 +157,26 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Low words of shared-memory descriptors with 128-byte swizzle (the upper word, kDescHi, holds the 1024-byte
+// stride, the version and the swizzle): K-major operands, and MN-major ones whose 64-element atoms are one
+// box apart.  Adding bytes / 16 moves the start address.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t kmajor_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t mnmajor_lo(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((uint32_t)(kBox >> 4) << 16);
+}
+
+__device__ __forceinline__ void mma_f16_lo(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi)
+      : "memory");
 }
 
 // 16 rows (tensor-memory lanes) x 64 fp32 columns: v[4 j + {0, 1}] is row lane / 4, columns
@@ -350,7 +376,7 @@ __global__ void __launch_bounds__(Cfg<NR, FMT>::THREADS, 1)
   uint8_t* p_s = smem + C::OFF_P;
   float* sc_s = reinterpret_cast<float*>(smem + C::OFF_SC);
   Aux* a = reinterpret_cast<Aux*>(smem + C::OFF_AUX);
-  const int tid = threadIdx.x, lane = tid & 31, warp = warp_id();
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   int* err = p.err;
 
   if (warp == 0) {
@@ -425,101 +451,112 @@ __global__ void __launch_bounds__(Cfg<NR, FMT>::THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = make_idesc(1, 1, 64, kKeys);
-      constexpr uint32_t idesc_pv = make_idesc(1, 1, 128, NR) | (1u << 15);  // A (the tile) MN-major
-      const uint32_t qb = smem_u32(q_s), sb0 = smem_u32(slots), rb0 = smem_u32(rope_s), pb = smem_u32(p_s);
-      int qsl = 0, qph = 0, rs = 0, rph = 0;  // slots of the first product
-      int psl = 0;                            // slots of the second
-      uint32_t su = 0;                        // S buffers used
-      int tile = 0, items = 0;
-      bool ok = true;
-      // 64-column box j of the next tile's first product
-      auto qk_box = [&](uint32_t base, int j, uint32_t d, bool first) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_f16(d, smem_desc_sw128(qb + j * C::Q_BOX + 32 * k), smem_desc_sw128(base + 32 * k), idesc_qk,
-                  first && k == 0 ? 0u : 1u);
-      };
-      auto s_buf = [&]() { return tmem + C::S_COL + 64 * (su & (C::NSB - 1)); };
-      auto s_acquire = [&]() {
-        ok = ok && wait(a, &a->s_empty[su & (C::NSB - 1)], ((su / C::NSB) & 1) ^ 1, err);
+    // ---- MMA issuer.  The warp stays converged and one elected lane issues; descriptors are sums of
+    // 32-bit words (their upper words are one constant), so that issuing an instruction costs less than
+    // the tensor cores take for it
+    constexpr uint32_t idesc_qk = make_idesc(1, 1, 64, kKeys);
+    constexpr uint32_t idesc_pv = make_idesc(1, 1, 128, NR) | (1u << 15);  // A (the tile) MN-major
+    const uint32_t tm_base = (uint32_t)uniform((int)tmem);
+    const uint32_t q_lo = kmajor_lo(smem_u32(q_s)), k_lo = kmajor_lo(smem_u32(slots)), r_lo = kmajor_lo(smem_u32(rope_s));
+    const uint32_t v_lo = mnmajor_lo(smem_u32(slots)), p_lo = kmajor_lo(smem_u32(p_s));
+    int qsl = 0, qph = 0, rs = 0, rph = 0;  // slots of the first product
+    int psl = 0;                            // slots of the second
+    uint32_t su = 0;                        // S buffers used
+    int tile = 0, items = 0;
+    bool ok = true;
+    auto all = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, wait(a, bar, parity, err)); };
+    auto s_acquire = [&]() { all(&a->s_empty[su & (C::NSB - 1)], ((su / C::NSB) & 1) ^ 1); };
+    // part h of a tile's first product: blocks 2 h, 2 h + 1 (and the rotary columns with the second)
+    auto qk_part = [&](int h) {
+#pragma unroll 1
+      for (int b = 2 * h; b < 2 * h + 2; ++b) {
+        if (C::SACC > 1 || b == 0) s_acquire();
+        all(&a->full[qsl], qph);
+        if (!ok) return;
         tc_fence_after();
-      };
-      auto s_commit = [&]() {
-        tc_commit(&a->s_full[su & (C::NSB - 1)]);
-        ++su;
-      };
-      // part h of a tile's first product: blocks 2 h, 2 h + 1 (and the rotary columns with the second)
-      auto qk_part = [&](int h) {
-        for (int b = 2 * h; ok && b < 2 * h + 2; ++b) {
-          if (C::SACC > 1 || b == 0) s_acquire();
-          ok = ok && wait(a, &a->full[qsl], qph, err);
-          if (!ok) return;
-          tc_fence_after();
-          const uint32_t base = sb0 + qsl * kSlot;
-          qk_box(base, 2 * b, s_buf(), C::SACC > 1 || b == 0);
-          qk_box(base + kBox, 2 * b + 1, s_buf(), false);
-          if (C::SACC > 1) s_commit();
-          if (++qsl == C::SLOTS) qsl = 0, qph ^= 1;
+        const uint32_t d = tm_base + C::S_COL + 64 * (su & (C::NSB - 1));
+        const uint32_t A = q_lo + b * (2 * C::Q_BOX >> 4), B = k_lo + qsl * (kSlot >> 4);
+        const uint32_t acc0 = C::SACC == 1 && b > 0;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_f16_lo(d, A + ((k >> 2) * C::Q_BOX + 32 * (k & 3)) / 16, B + ((k >> 2) * kBox + 32 * (k & 3)) / 16, idesc_qk,
+                       k ? 1u : acc0);
+          if (C::SACC > 1) tc_commit(&a->s_full[su & (C::NSB - 1)]);
         }
-        if (h == 1) {
-          if (C::SACC > 1) s_acquire();
-          ok = ok && wait(a, &a->rfull[rs], rph, err);
-          if (!ok) return;
-          tc_fence_after();
-          qk_box(rb0 + rs * kBox, 8, s_buf(), C::SACC > 1);
-          s_commit();
+        __syncwarp();
+        if (C::SACC > 1) ++su;
+        if (++qsl == C::SLOTS) qsl = 0, qph ^= 1;
+      }
+      if (h == 1) {
+        if (C::SACC > 1) s_acquire();
+        all(&a->rfull[rs], rph);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t d = tm_base + C::S_COL + 64 * (su & (C::NSB - 1));
+        const uint32_t A = q_lo + (8 * C::Q_BOX >> 4), B = r_lo + rs * (kBox >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_f16_lo(d, A + 2 * k, B + 2 * k, idesc_qk, k || C::SACC == 1 ? 1u : 0u);
+          tc_commit(&a->s_full[su & (C::NSB - 1)]);
           tc_commit(&a->rempty[rs]);
-          if (++rs == C::ROPE_SLOTS) rs = 0, rph ^= 1;
         }
-      };
-      auto pv_part = [&](int h, bool first) {
-        for (int b = 2 * h; b < 2 * h + 2; ++b) {
-          const uint32_t base = sb0 + psl * kSlot;
-          const uint32_t pj = pb + (C::PC > 1 ? b : 0) * C::P_BYTES;
+        __syncwarp();
+        ++su;
+        if (++rs == C::ROPE_SLOTS) rs = 0, rph ^= 1;
+      }
+    };
+    auto pv_part = [&](int h, bool first) {
+      const uint32_t acc0 = first ? 0u : 1u;
+#pragma unroll 1
+      for (int b = 2 * h; b < 2 * h + 2; ++b) {
+        const uint32_t A = v_lo + psl * (kSlot >> 4), B = p_lo + (C::PC > 1 ? b : 0) * (C::P_BYTES >> 4);
+        const uint32_t d = tm_base + NR * b;
+        if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_f16(tmem + NR * b, smem_desc_sw128_mn(base + ks * 2048, kBox, 1024), smem_desc_sw128(pj + 32 * ks),
-                    idesc_pv, first && ks == 0 ? 0u : 1u);
+          for (int ks = 0; ks < 4; ++ks) mma_f16_lo(d, A + ks * (2048 >> 4), B + 2 * ks, idesc_pv, ks ? 1u : acc0);
           tc_commit(&a->empty[psl]);
-          if (++psl == C::SLOTS) psl = 0;
         }
-      };
-      for (int i = 0; ok && get_item<NR>(p, pl, a, i, it); ++i) {
-        if (it.t0 >= it.t1) continue;
-        ok = wait(a, &a->q_full, items & 1, err);
+        __syncwarp();
+        if (++psl == C::SLOTS) psl = 0;
+      }
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) tc_commit(bar);
+      __syncwarp();
+    };
+    for (int i = 0; ok && uniform(get_item<NR>(p, pl, a, i, it)); ++i) {
+      const int t0 = uniform(it.t0), t1 = uniform(it.t1);
+      if (t0 >= t1) continue;
+      all(&a->q_full, items & 1);
+      tc_fence_after();
+      if (ok) qk_part(0);
+      if (ok) qk_part(1);
+      for (int t = t0; ok && t < t1; ++t, ++tile) {
+        const bool next = t + 1 < t1, first = t == t0;
+        if (next) {
+          qk_part(0);
+          if (ok && !C::HALVES) qk_part(1);
+        } else {
+          commit(&a->q_empty);
+        }
+        all(&a->p_full, tile & 1);
+        if (first) all(&a->o_free, (items & 1) ^ 1);
+        if (!ok) break;
         tc_fence_after();
-        if (ok) qk_part(0);
-        if (ok) qk_part(1);
-        for (int t = it.t0; ok && t < it.t1; ++t, ++tile) {
-          const bool next = t + 1 < it.t1, first = t == it.t0;
-          if (next) {
-            qk_part(0);
-            if (ok && !C::HALVES) qk_part(1);
-          } else {
-            tc_commit(&a->q_empty);
-          }
-          ok = ok && wait(a, &a->p_full, tile & 1, err);
-          if (ok && first) ok = wait(a, &a->o_free, (items & 1) ^ 1, err);
-          if (!ok) break;
-          tc_fence_after();
-          pv_part(0, first);
-          if (next && C::HALVES) qk_part(1);
-          if (!ok) break;
-          pv_part(1, first);
-          tc_commit(&a->p_empty);
-          if (!next) tc_commit(&a->o_done);
-        }
-        ++items;
+        pv_part(0, first);
+        if (next && C::HALVES) qk_part(1);
+        if (!ok) break;
+        pv_part(1, first);
+        commit(&a->p_empty);
+        if (!next) commit(&a->o_done);
       }
-      if (*reinterpret_cast<volatile int*>(&a->abort)) {
-        tc_commit(&a->drain);  // wind down: what was issued ends before the tensor memory is freed
-        mbar_wait(&a->drain, 0, err);
-      }
+      ++items;
     }
-    __syncwarp();
+    if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&a->abort))) {
+      commit(&a->drain);  // wind down: what was issued ends before the tensor memory is freed
+      mbar_wait(&a->drain, 0, err);
+    }
   } else if (warp == 2 && C::FP8) {
     // ---- scales of the tile's positions (1 where there is none: the position is masked)
     int tiles = 0;
