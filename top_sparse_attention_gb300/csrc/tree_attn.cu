@@ -16,10 +16,10 @@
 //       l' = l 2^(m - m') + sum_p 2^(x_p - m'),   o' = o 2^(m - m') + sum_p 2^(x_p - m') v_p,
 //     where m is moved only when a tile's maximum exceeds it by more than 2^8 (weights stay below 2^8,
 //     fp32 sums and bf16 weights lose nothing by it), so o in tensor memory is rescaled rarely;
-//   * O_c[128 x 256] += P V_c: A = P (bf16) in tensor memory; B = the same tile read MN-major (values along
+//   * O_c[128 x 256] += P V_c: A = P (bf16) in shared memory; B = the same tile read MN-major (values along
 //     N), 4 steps of K = 16 with N = 256.
 // Why two CTAs: o for 128 rows x 512 values fills a tensor memory (512 columns), which leaves no room for S;
-// with half of the values it takes 256 columns, q 128, S 64, P 32 or 64.  One CTA with 64 rows, q in shared
+// with half of the values it takes 256 columns, q 128, two S buffers 128.  One CTA with 64 rows, q in shared
 // memory and o transposed read 245 KB of shared memory per tile for the MMAs (2000 cycles at 128 B per
 // cycle) and loaded each tile twice as often: 149 us instead of the time below for 8 x 8 nodes at 32K.
 //
@@ -27,8 +27,9 @@
 // outputs are fp32.  E4M3 rows are widened to bf16 exactly, and their scales are applied in fp32 to the
 // logit and to the weight (128-column scales: one S accumulator per scale tile, one P per value tile).
 //
-// Warp roles: producer (TMA), MMA issuer, scale loader, eight softmax warps (also the query load, the
-// rescale and the epilogue), for E4M3 four warps that widen the raw tile in shared memory.
+// Warp roles: producer (TMA), MMA issuer, scale loader, credits of the exchange, four senders, eight softmax
+// warps (also the query load, the rescale and the epilogue), for E4M3 four warps that widen the raw
+// tile in shared memory.
 //
 // Work split: items (sequence, chunk of its tiles, row tile), in this order, so that clusters that run
 // together read the same positions and the cache comes from HBM once.  The lengths are on the device:
@@ -51,8 +52,8 @@ constexpr int kRaw = kKeys * 288;         // the same columns as E4M3 codes: 64 
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLazy = 8.f;              // log2 growth of a row's maximum that is left unscaled
 constexpr int kItemsPerCta = 3;           // split launches are cut into at most this many items per cluster
-// tensor-memory columns: O, the value columns of q, S, P (one or two copies of 32 columns)
-constexpr int kColO = 0, kColQ = 256, kColS = 384, kColP = 448;
+// tensor-memory columns: O, the value columns of q, two S buffers
+constexpr int kColO = 0, kColQ = 256, kColS = 384;
 
 enum { kBf16 = 0, kFp8Row = 1, kFp8Tile = 2 };
 
@@ -61,17 +62,20 @@ struct Cfg {
   static constexpr bool FP8 = FMT != kBf16;
   static constexpr int NSC = FMT == kFp8Tile ? 5 : FMT == kFp8Row ? 1 : 0;
   static constexpr bool TILED = FMT == kFp8Tile;
-  static constexpr int THREADS = FP8 ? 512 : 384;
-  static constexpr int STAGES = FP8 ? 3 : 4;              // tiles in shared memory
-  static constexpr int RAWS = TILED ? 2 : FP8 ? 3 : 0;              // raw E4M3 tiles
+  static constexpr int THREADS = FP8 ? 640 : 512;
+  static constexpr int STAGES = FP8 ? 2 : 3;              // tiles in shared memory
+  static constexpr int RAWS = TILED ? 1 : FP8 ? 2 : 0;    // raw E4M3 tiles
+  static constexpr int PC = TILED ? 2 : 1;                // copies of P (one per 128 values)
   static constexpr int SC_DEPTH = 2;
   static constexpr int SC_BYTES = NSC * kKeys * 4;
-  static constexpr int X_BYTES = kRows * kKeys * 4;       // the peer's partial S
+  static constexpr int X_BYTES = kRows * kKeys * 4;       // the peer's partial S (two buffers)
   static constexpr int QR_BYTES = kRows * 128;            // q's rotary columns
+  static constexpr int P_BYTES = kRows * 128;             // P: 128 rows x 64 positions
   static constexpr int AUX = 2048;
   static constexpr int OFF_X = STAGES * kTile;
-  static constexpr int OFF_QR = OFF_X + X_BYTES;
-  static constexpr int OFF_RAW = OFF_QR + QR_BYTES;
+  static constexpr int OFF_QR = OFF_X + 2 * X_BYTES;
+  static constexpr int OFF_P = OFF_QR + QR_BYTES;
+  static constexpr int OFF_RAW = OFF_P + PC * P_BYTES;
   static constexpr int OFF_SC = OFF_RAW + RAWS * kRaw;
   static constexpr int OFF_AUX = OFF_SC + SC_DEPTH * SC_BYTES;
   static constexpr int SMEM = OFF_AUX + AUX + 1024;
@@ -107,7 +111,7 @@ __device__ __forceinline__ int live_row_tiles(const TreeAttnParams& p, int fresh
 
 struct Aux {
   uint64_t full[4], empty[4], raw_full[3], raw_empty[3];
-  uint64_t s_full, s_empty, x_full, x_free, p_full, pv_done, o_done, o_free, q_full, sc_full[2], sc_empty[2], drain;
+  uint64_t s_full[2], s_empty[2], x_full[2], x_read[2], x_free[2], p_full, pv_done, o_done, o_free, q_full, sc_full[2], sc_empty[2], drain;
   uint32_t tmem;
   int abort;
   int n_items;
@@ -398,6 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
   uint8_t* tiles_s = smem;
   uint8_t* x_s = smem + C::OFF_X;
   uint8_t* qr_s = smem + C::OFF_QR;
+  uint8_t* p_s = smem + C::OFF_P;
   uint8_t* raw_s = smem + C::OFF_RAW;
   float* sc_s = reinterpret_cast<float*>(smem + C::OFF_SC);
   Aux* a = reinterpret_cast<Aux*>(smem + C::OFF_AUX);
@@ -413,10 +418,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
     for (int i = 0; i < C::STAGES; ++i) mbar_init(&a->full[i], C::FP8 ? 4 : 1), mbar_init(&a->empty[i], 1);
     for (int i = 0; i < 3; ++i) mbar_init(&a->raw_full[i], 1), mbar_init(&a->raw_empty[i], 4);
     for (int i = 0; i < 2; ++i) mbar_init(&a->sc_full[i], 32), mbar_init(&a->sc_empty[i], 8);
-    mbar_init(&a->s_full, 1);
-    mbar_init(&a->s_empty, 8);
-    mbar_init(&a->x_full, 1);
-    mbar_init(&a->x_free, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&a->s_full[i], 1), mbar_init(&a->s_empty[i], C::TILED ? 8 : 12);
+      mbar_init(&a->x_full[i], 1), mbar_init(&a->x_read[i], 8), mbar_init(&a->x_free[i], 1);
+    }
     mbar_init(&a->p_full, 8);
     mbar_init(&a->pv_done, 1);
     mbar_init(&a->o_done, 1);
@@ -425,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
     mbar_init(&a->drain, 1);
     a->abort = 0;
     fence_mbar_init();
-    mbar_arrive_expect_tx(&a->x_full, C::X_BYTES);
+    for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&a->x_full[i], C::X_BYTES);
   }
   if (tid < kKeys) a->kbad[tid] = 0;
   if (pl.cap) plan_items(p, pl, a, reinterpret_cast<int*>(tiles_s));
@@ -489,9 +494,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
     const uint32_t tm_base = (uint32_t)uniform((int)tmem);
     const uint32_t k_lo = kmajor_lo(smem_u32(tiles_s)), v_lo = mnmajor_lo(smem_u32(tiles_s));
     const uint32_t qr_lo = kmajor_lo(smem_u32(qr_s)) + 4 * rank;  // this CTA's half: 64 bytes into the row
+    const uint32_t p_lo = kmajor_lo(smem_u32(p_s));
     int qs = 0, qph = 0, ps = 0;  // stages of the first and of the second product
     int tile = 0, items = 0;
-    uint32_t su = 0;              // uses of the S buffer
+    uint32_t su = 0;              // uses of the S buffers
     bool ok = true;
     auto all = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, wait(a, bar, parity, err)); };
     auto commit = [&](uint64_t* bar) {
@@ -503,10 +509,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
     // have read what S held.
     auto qk = [&](int g) {
       if (g <= 0) all(&a->full[qs], qph);
-      all(&a->s_empty, (su & 1) ^ 1);
+      all(&a->s_empty[su & 1], ((su >> 1) & 1) ^ 1);
       if (!ok) return;
       tc_fence_after();
-      const uint32_t d = tm_base + kColS, B = k_lo + qs * (kTile >> 4);
+      const uint32_t d = tm_base + kColS + 64 * (su & 1), B = k_lo + qs * (kTile >> 4);
       if (elect_one()) {
         if (g < 2) {
           const uint32_t q0 = tm_base + kColQ + (g > 0 ? 64 : 0), B0 = B + (g > 0 ? 2 * kBox >> 4 : 0);
@@ -519,7 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
           for (int k = 0; k < 2; ++k)
             mma_ss(d, qr_lo + 2 * k, B + (4 * kBox >> 4) + 4 * rank + 2 * k, idesc_qk, k || !C::TILED ? 1u : 0u);
         }
-        tc_commit(&a->s_full);
+        tc_commit(&a->s_full[su & 1]);
       }
       __syncwarp();
       ++su;
@@ -535,8 +541,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            mma_ts(tm_base + kColO + 128 * b, tm_base + kColP + 32 * b + 8 * ks, B + (2 * b * kBox + 2048 * ks) / 16, idesc_pv,
-                   ks ? 1u : acc0);
+            mma_ss(tm_base + kColO + 128 * b, p_lo + (b * C::P_BYTES + 32 * ks) / 16, B + (2 * b * kBox + 2048 * ks) / 16,
+                   idesc_pv, ks ? 1u : acc0);
         tc_commit(&a->empty[ps]);
         tc_commit(&a->pv_done);
       }
@@ -597,10 +603,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         mbar_arrive(&a->sc_full[d]);
       }
     }
-  } else if (warp >= 12) {
+  } else if (warp == 3) {
+    // ---- credits of the exchange: once the softmax warps have read the peer's part, its buffer is armed for
+    // the tile after next and the peer told so (here, because a release at cluster scope would hold up
+    // the softmax warps)
+    int tiles = 0;
+    bool ok = true;
+    const uint32_t peer_free = dsmem_addr(&a->x_free[0], rank ^ 1);
+    for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
+      for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
+        const int b = tiles & 1;
+        ok = __all_sync(0xffffffffu, wait(a, &a->x_read[b], (tiles >> 1) & 1, err));
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(&a->x_full[b], C::X_BYTES);
+          arrive_remote(peer_free + 8 * b);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp >= 16) {
     // ---- converters (E4M3): raw codes -> the swizzled bf16 boxes.  A half warp takes 128 codes of a position,
     // eight per lane (one 16-byte chunk of bf16), so that loads and stores touch every bank once.
-    const int cw = warp - 12, hw = lane >> 4, l16 = lane & 15;
+    const int cw = warp - 16, hw = lane >> 4, l16 = lane & 15;
     int rs = 0, rph = 0, st = 0, sph = 0;
     bool ok = true;
     auto widen = [&](uint2 v) {
@@ -614,18 +638,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         if (!ok) break;
         const uint8_t* raw = raw_s + rs * kRaw;
         uint8_t* dst = tiles_s + st * kTile;
-        // unit u of 128: position u / 2, codes 128 (u % 2) + 8 l16 ...
-#pragma unroll 4
-        for (int k = 0; k < 16; ++k) {
-          const int u = cw * 32 + 2 * k + hw, key = u >> 1, box = 2 * (u & 1) + (l16 >> 3), c = l16 & 7;
-          const uint2 v = *reinterpret_cast<const uint2*>(raw + key * 256 + 128 * (u & 1) + 8 * l16);
-          *reinterpret_cast<uint4*>(dst + box * kBox + key * 128 + ((c ^ (key & 7)) << 4)) = widen(v);
+        uint2 rot[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          rot[k] = *reinterpret_cast<const uint2*>(raw + kKeys * 256 + (cw * 16 + 8 * k + (lane >> 2)) * 32 + 8 * (lane & 3));
+        // unit u of 128: position u / 2, codes 128 (u % 2) + 8 l16 ...; eight loads in flight
+#pragma unroll 1
+        for (int k0 = 0; k0 < 16; k0 += 8) {
+          uint2 v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int u = cw * 32 + 2 * (k0 + k) + hw;
+            v[k] = *reinterpret_cast<const uint2*>(raw + (u >> 1) * 256 + 128 * (u & 1) + 8 * l16);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int u = cw * 32 + 2 * (k0 + k) + hw, key = u >> 1, box = 2 * (u & 1) + (l16 >> 3), c = l16 & 7;
+            *reinterpret_cast<uint4*>(dst + box * kBox + key * 128 + ((c ^ (key & 7)) << 4)) = widen(v[k]);
+          }
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {  // the rotary half: 32 codes of a position, four lanes
           const int key = cw * 16 + 8 * k + (lane >> 2), c = 4 * rank + (lane & 3);
-          const uint2 v = *reinterpret_cast<const uint2*>(raw + kKeys * 256 + key * 32 + 8 * (lane & 3));
-          *reinterpret_cast<uint4*>(dst + 4 * kBox + key * 128 + ((c ^ (key & 7)) << 4)) = widen(v);
+          *reinterpret_cast<uint4*>(dst + 4 * kBox + key * 128 + ((c ^ (key & 7)) << 4)) = widen(rot[k]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -637,13 +672,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         if (++st == C::STAGES) st = 0, sph ^= 1;
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 8) {
+    // ---- senders (but for tile scales, whose partial logits the softmax warps sum first): the partial S of
+    // this CTA's columns into the peer's buffer, a row per thread
+    const int w = warp - 4, row = 32 * w + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
+    const uint32_t peer_x = dsmem_addr(x_s, rank ^ 1) + row * 16, peer_full = dsmem_addr(&a->x_full[0], rank ^ 1);
+    int tiles = 0;
+    bool ok = !C::TILED;
+    for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
+      for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
+        const int b = tiles & 1;
+        ok = __all_sync(0xffffffffu, wait(a, &a->s_full[b], (tiles >> 1) & 1, err));
+        tc_fence_after();
+        float x[64];
+        tmem_ld_sync(lane_base + kColS + 64 * b, *reinterpret_cast<float (*)[32]>(x));
+        tmem_ld_sync(lane_base + kColS + 64 * b + 32, *reinterpret_cast<float (*)[32]>(x + 32));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&a->s_empty[b]);
+        ok = ok && __all_sync(0xffffffffu, wait_cluster(a, &a->x_free[b], ((tiles >> 1) & 1) ^ 1, err));
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) st_async16(peer_x + b * C::X_BYTES + j * kRows * 16, x + 4 * j, peer_full + 8 * b);
+      }
+    }
+  } else if (warp >= 8 && warp < 16) {
     // ---- softmax, query load, rescale, epilogue.  Thread = row (tensor-memory lane) and half h of the tile's
     // positions (32), of the query's columns and of the value columns
-    const int w = warp - 4, h = w >> 2, row = 32 * (w & 3) + lane, st = tid - 128;
+    const int w = warp - 8, h = w >> 2, row = 32 * (w & 3) + lane, st = tid - 256;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (w & 3)) << 16);
     const uint32_t peer_x = dsmem_addr(x_s, rank ^ 1) + (h * 8 * kRows + row) * 16;
-    const uint32_t peer_full = dsmem_addr(&a->x_full, rank ^ 1), peer_free = dsmem_addr(&a->x_free, rank ^ 1);
+    const uint32_t peer_full = dsmem_addr(&a->x_full[0], rank ^ 1);
     const float4* my_x = reinterpret_cast<const float4*>(x_s) + h * 8 * kRows + row;
     int tile = 0, items = 0;
     uint32_t su = 0;
@@ -693,6 +753,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
       for (int t = it.t0; t < it.t1; ++t, ++tile) {
         const bool tail = (t + 1) * kKeys > it.ctx;
         const float* sc = sc_s + (tile % C::SC_DEPTH) * kKeys * C::NSC + 32 * h * C::NSC;
+        const int xb = tile & 1;
         float x[32];
         // ---- this CTA's partial logits
         if constexpr (C::FP8) ok = ok && wait(a, &a->sc_full[tile % C::SC_DEPTH], (tile / C::SC_DEPTH) & 1, err);
@@ -701,42 +762,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
           for (int k = 0; k < 32; ++k) x[k] = 0.f;
 #pragma unroll 1
           for (int g = 0; g < 3; ++g, ++su) {
-            ok = ok && wait(a, &a->s_full, su & 1, err);
+            ok = ok && wait(a, &a->s_full[su & 1], (su >> 1) & 1, err);
             tc_fence_after();
             float s[32];
-            tmem_ld_sync(lane_base + kColS + 32 * h, s);
+            tmem_ld_sync(lane_base + kColS + 64 * (su & 1) + 32 * h, s);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&a->s_empty);
+            if (lane == 0) mbar_arrive(&a->s_empty[su & 1]);
             const float* f = sc + (g < 2 ? 2 * rank + g : 4);
 #pragma unroll
             for (int k = 0; k < 32; ++k) x[k] = fmaf(f[5 * k], s[k], x[k]);
           }
         } else {
-          ok = ok && wait(a, &a->s_full, tile & 1, err);
+          ok = ok && wait(a, &a->s_full[xb], (tile >> 1) & 1, err);
           tc_fence_after();
-          tmem_ld_sync(lane_base + kColS + 32 * h, x);
+          tmem_ld_sync(lane_base + kColS + 64 * xb + 32 * h, x);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&a->s_empty);
+          if (lane == 0) mbar_arrive(&a->s_empty[xb]);
         }
-        // ---- the peer's part: ours goes to its buffer once it has read the tile before
-        ok = ok && wait_cluster(a, &a->x_free, (tile & 1) ^ 1, err);
-        if (ok) {
+        // ---- the peer's part
+        if constexpr (C::TILED) {
+          ok = ok && wait_cluster(a, &a->x_free[xb], ((tile >> 1) & 1) ^ 1, err);
+          if (ok) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) st_async16(peer_x + j * kRows * 16, x + 4 * j, peer_full);
+            for (int j = 0; j < 8; ++j) st_async16(peer_x + xb * C::X_BYTES + j * kRows * 16, x + 4 * j, peer_full + 8 * xb);
+          }
         }
-        ok = ok && wait_cluster(a, &a->x_full, tile & 1, err);
+        ok = ok && wait_cluster(a, &a->x_full[xb], (tile >> 1) & 1, err);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float4 v = my_x[j * kRows];
+          const float4 v = my_x[xb * (C::X_BYTES / 16) + j * kRows];
           x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
         }
         __syncwarp();
-        if (lane == 0) {
-          if (w == 0) mbar_arrive_expect_tx(&a->x_full, C::X_BYTES);  // arm the next tile's count
-          arrive_remote(peer_free);
-        }
+        if (lane == 0) mbar_arrive(&a->x_read[xb]);
         // ---- scale, mask
         if constexpr (FMT == kFp8Row) {
 #pragma unroll
@@ -836,23 +896,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         ok = ok && wait(a, &a->pv_done, (tile & 1) ^ 1, err);  // the tile before has read its P
         tc_fence_after();
 #pragma unroll
-        for (int pc = 0; pc < (C::TILED ? 2 : 1); ++pc) {
-          uint32_t v[16];
+        for (int pc = 0; pc < C::PC; ++pc) {
+          uint8_t* d = p_s + pc * C::P_BYTES + row * 128;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float y0 = x[2 * k], y1 = x[2 * k + 1];
-            if constexpr (C::FP8) {
-              // a hidden position's weight is 0 whatever its scale holds
-              const float f0 = sc[2 * k * C::NSC + (C::TILED ? 2 * rank + pc : 0)];
-              const float f1 = sc[(2 * k + 1) * C::NSC + (C::TILED ? 2 * rank + pc : 0)];
-              y0 = y0 == 0.f ? 0.f : y0 * f0;
-              y1 = y1 == 0.f ? 0.f : y1 * f1;
+          for (int j = 0; j < 4; ++j) {  // 16-byte chunks of eight positions
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int e = 8 * j + 2 * k;
+              float y0 = x[e], y1 = x[e + 1];
+              if constexpr (C::FP8) {
+                // a hidden position's weight is 0 whatever its scale holds
+                const float f0 = sc[e * C::NSC + (C::TILED ? 2 * rank + pc : 0)];
+                const float f1 = sc[(e + 1) * C::NSC + (C::TILED ? 2 * rank + pc : 0)];
+                y0 = y0 == 0.f ? 0.f : y0 * f0;
+                y1 = y1 == 0.f ? 0.f : y1 * f1;
+              }
+              v[k] = pack_bf16(y0, y1);
             }
-            v[k] = pack_bf16(y0, y1);
+            *reinterpret_cast<uint4*>(d + (((4 * h + j) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
           }
-          tmem_st16(lane_base + kColP + 32 * pc + 16 * h, v);
         }
-        tmem_wait_st();
+        fence_proxy_async_smem();
+        tmem_wait_st();  // (a rescale's stores)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
