@@ -23,10 +23,13 @@ __all__ = list(_API + _NATIVE) + ["call_from_tensors", "INPUT_KEYS"]
 
 def __getattr__(name):
     if name in _API:
-        return getattr(importlib.import_module(".api", __name__), name)
-    if name in _NATIVE:
-        return getattr(importlib.import_module("._native", __name__), name)
-    raise AttributeError(name)
+        value = getattr(importlib.import_module(".api", __name__), name)
+    elif name in _NATIVE:
+        value = getattr(importlib.import_module("._native", __name__), name)
+    else:
+        raise AttributeError(name)
+    globals()[name] = value  # found directly from now on
+    return value
 
 
 def call_from_tensors(tensors: dict, **kw):

@@ -339,16 +339,25 @@ def _cuda_device(what, t) -> torch.device:
     return t.device
 
 
+# The current stream's handle and the current device without building torch objects (a serving step makes
+# several short calls, and the host's share of each is most of its time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _run(what, fn, device, stream, *args):
+    i = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        handle = _raw_stream(i)
     elif stream.device != device:
         raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, stream.cuda_stream)
+    else:
+        handle = stream.cuda_stream
+    if _current_device() == i:
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, handle)
     if st != N.DSA_OK:
         N.check(st, what)
 
@@ -391,8 +400,10 @@ def dsa_block_plan(n_ctx, n_new, free_blocks, block_table, *, block_size, num_bl
             raise ValueError(f"{what}: packed rows need their number (rows)")
         rows = n_seq * q_per_seq
     if out is None:
-        new = lambda n, t=i32: torch.empty(n, dtype=t, device=dev)  # noqa: E731
-        out = BlockPlan(new(rows, torch.int64), new(rows), new(rows), new(n_seq + 1), new(n_seq), new(1))
+        # one allocation for all outputs
+        dst, *parts = torch.empty(4 * rows + 2 * n_seq + 2, dtype=i32, device=dev).split_with_sizes(
+            (2 * rows, rows, rows, n_seq + 1, n_seq, 1))
+        out = BlockPlan(dst.view(torch.int64), *parts)
     else:
         for name, t, n, kind in (("dst_rows", out.dst_rows, rows, torch.int64), ("pos", out.pos, rows, i32),
                                  ("seq", out.seq, rows, i32), ("row_start", out.row_start, n_seq + 1, i32),

@@ -41,10 +41,11 @@ __device__ __forceinline__ SeqNeed need_of(const BlockPlanParams& p, int s) {
   n.c = max(p.n_ctx[s], 0);
   n.m = max(p.n_new[s], 0);
   if (p.q_per_seq > 0) n.m = min(n.m, p.q_per_seq);
-  const int64_t have = ((int64_t)n.c + p.block_size - 1) / p.block_size;
-  const int64_t total = ((int64_t)n.c + n.m + p.block_size - 1) / p.block_size;
-  n.fits = total <= p.max_blocks;
-  n.need = n.fits ? (int)(total - have) : 0;
+  // (both sums stay below 2^32: each term is at most 2^31 - 1)
+  const uint32_t b = (uint32_t)p.block_size, last = b - 1;
+  const uint32_t have = ((uint32_t)n.c + last) / b;
+  n.fits = (int64_t)n.c + n.m <= (int64_t)p.max_blocks * p.block_size;
+  n.need = n.fits ? (int)(((uint32_t)n.c + (uint32_t)n.m + last) / b - have) : 0;
   return n;
 }
 
@@ -123,8 +124,8 @@ __global__ void __launch_bounds__(kThreads) block_plan_kernel(const BlockPlanPar
   for (int64_t r = (int64_t)blockIdx.x * blockDim.x + tid; r < p.rows; r += stride) {
     int s, i;
     if (padded) {
-      s = (int)(r / p.q_per_seq);
-      i = (int)(r - (int64_t)s * p.q_per_seq);
+      s = (int)((uint32_t)r / (uint32_t)p.q_per_seq);
+      i = (int)r - s * p.q_per_seq;
     } else {
       int lo = 0, hi = p.n_seq;  // the last sequence (n_seq: none) whose rows start at or before r
       while (lo < hi) {
@@ -142,8 +143,8 @@ __global__ void __launch_bounds__(kThreads) block_plan_kernel(const BlockPlanPar
       const int m = padded ? min(max(p.n_new[s], 0), p.q_per_seq) : max(p.n_new[s], 0);
       if (i < m) {
         const int at = c + i;  // fits: below max_blocks * block_size
-        const int j = at / p.block_size, in = at - j * p.block_size;
-        const int have = (int)(((int64_t)c + p.block_size - 1) / p.block_size);
+        const int j = (int)((uint32_t)at / (uint32_t)p.block_size), in = at - j * p.block_size;
+        const int have = (int)(((uint32_t)c + (uint32_t)p.block_size - 1) / (uint32_t)p.block_size);
         int32_t* entry = p.block_table + (int64_t)s * p.max_blocks + j;
         const int id = j < have ? *entry : p.free_blocks[blk_off[s] + j - have];
         if ((unsigned)id < (unsigned)p.num_blocks) {
@@ -206,8 +207,9 @@ extern "C" dsa_status dsa_block_plan(const int32_t* n_ctx, const int32_t* n_new,
   const int64_t want = ((int64_t)rows + (int64_t)threads * kRowsPerThread - 1) / ((int64_t)threads * kRowsPerThread);
   const int grid = (int)(want < 1 ? 1 : want > 304 ? 304 : want);
   const size_t smem = ((size_t)2 * n_seq + 1) * sizeof(int32_t);
-  if (cudaFuncSetAttribute(block_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (2 * DSA_BLOCK_PLAN_MAX_SEQ + 1) * (int)sizeof(int32_t)) != cudaSuccess)
+  static std::atomic<uint64_t> allowed{0};
+  if (allow_smem_once(&allowed, reinterpret_cast<const void*>(block_plan_kernel),
+                      (2 * DSA_BLOCK_PLAN_MAX_SEQ + 1) * (int)sizeof(int32_t)) != cudaSuccess)
     return DSA_ERR_CUDA;
   block_plan_kernel<<<grid, threads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;

@@ -3,6 +3,7 @@
 // synchronises, except dsa_get_device_error, which reads the device error word.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "dsa_internal.h"
@@ -30,16 +31,23 @@ int* device_error_ptr() {
   return ptrs[dev];
 }
 
-// The kernels are built for sm_103a only; other devices are rejected before any launch.
+// The kernels are built for sm_103a only; other devices are rejected before any launch.  A device's
+// answer is kept: the two attribute queries are a noticeable part of a short call.
 dsa_status check_device() {
+  static std::atomic<int> known[64] = {};  // 0: not asked, 1 + status
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
+  if (dev >= 0 && dev < 64) {
+    const int k = known[dev].load(std::memory_order_relaxed);
+    if (k) return (dsa_status)(k - 1);
+  }
   int major = 0, minor = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
     return DSA_ERR_CUDA;
-  if (major != 10 || minor != 3) return DSA_ERR_UNSUPPORTED;
-  return DSA_OK;
+  const dsa_status s = major == 10 && minor == 3 ? DSA_OK : DSA_ERR_UNSUPPORTED;
+  if (dev >= 0 && dev < 64) known[dev].store(1 + s, std::memory_order_relaxed);
+  return s;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -417,6 +425,17 @@ dsa_status check_topk_args(const float* scores, int64_t ld_scores, int T, int q_
 }
 
 dsa_status check_device_arch() { return check_device(); }
+
+cudaError_t allow_smem_once(std::atomic<uint64_t>* done, const void* kern, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done->load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 int* device_error_word() { return device_error_ptr(); }
 

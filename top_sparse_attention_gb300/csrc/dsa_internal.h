@@ -7,6 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "dsa_common.cuh"
@@ -279,6 +280,9 @@ cudaError_t launch_tree_attn(const TreeAttnParams& p, void* ws, cudaStream_t str
 dsa_status check_topk_args(const float* scores, int64_t ld_scores, int T, int q_per_seq, int q_pos0,
                            const int32_t* n_valid, int L, int K, const int32_t* idx);
 dsa_status check_device_arch();
+// Raises a kernel's dynamic shared-memory limit, once per device (`done`: a static of the caller, one per
+// kernel).
+cudaError_t allow_smem_once(std::atomic<uint64_t>* done, const void* kern, int bytes);
 int* device_error_word();
 
 // Driver entry point for tensor-map encoding (resolved once through the runtime).

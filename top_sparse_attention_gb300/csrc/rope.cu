@@ -12,8 +12,8 @@
 // in half turns, in [-1, 1), for sincospif.  The fp64 product is off by 2^-53 of the angle at most:
 // under 2^-30 turns up to position 2^24 (inv_freq <= 1), 2^-24 turns (fp32's own rounding) at 2^31.
 //
-// Bound: HBM bandwidth.  One warp per row (append) or per row and 16 heads (rope): the lanes take the
-// sines of the row's pairs once and share them through shared memory; 16-byte loads and stores.
+// Bound: HBM bandwidth.  A warp takes one row (append) or 16 heads of a row (rope) after another: the lanes
+// take the sines of the row's pairs once and share them through shared memory; 16-byte loads and stores.
 // Rotated values enter the cache format's rounding in fp32 (one rounding, not two).
 #include <math.h>
 
@@ -24,20 +24,42 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kHeadsPerWarp = 16;
+constexpr int kSms = 152;
+constexpr int kCtasPerSm = 3;  // resident CTAs (registers); a large launch has this many per SM
 
-// The row's (cos, sin) for every pair, into this warp's shared table.
-__device__ __forceinline__ void fill_turns(const RopeParams& p, int64_t row, float2* cs) {
-  const int lane = threadIdx.x & 31;
-  const int32_t* pos = p.pos + row * p.pos_stride;
-  for (int i = lane; i < p.pairs; i += 32) {
+// What a CTA keeps in shared memory: the pairs' frequencies as fixed-point turns, and per warp the (cos,
+// sin) of the row in hand.
+struct RopeSmem {
+  uint64_t freq[kRopeMaxPairs];
+  float2 turns[kWarps][kRopeMaxPairs];
+  uint8_t axis[kRopeMaxPairs];  // (a copy: lanes read different entries, which parameters serve one by one)
+};
+
+// inv_freq / 2 pi modulo 1, times 2^64 (once per CTA: a row's fp64 products would cost more than its loads).
+__device__ __forceinline__ void fill_freq(const RopeParams& p, RopeSmem& s) {
+  for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) {
     const double turns = (double)p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
     const double frac = turns - rint(turns);                              // [-1/2, 1/2]
-    const uint64_t f = (uint64_t)__double2ll_rn(frac * 0x1p63) << 1;      // frac * 2^64 modulo 2^64
-    const uint64_t phase = (uint64_t)(int64_t)pos[p.axis[i]] * f;
-    float s, c;
-    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-    cs[i] = make_float2(c, p.inverse ? -s : s);
+    s.freq[i] = (uint64_t)__double2ll_rn(frac * 0x1p63) << 1;
+    s.axis[i] = p.axis[i];
   }
+  __syncthreads();
+}
+
+// (cos, sin) of a pair at a position.
+__device__ __forceinline__ float2 pair_turn(const RopeParams& p, uint64_t freq, int pos) {
+  const uint64_t phase = (uint64_t)(int64_t)pos * freq;
+  float s, c;
+  sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
+  return make_float2(c, p.inverse ? -s : s);
+}
+
+// The row's (cos, sin) for every pair, into this warp's shared table.
+__device__ __forceinline__ void fill_turns(const RopeParams& p, int64_t row, const RopeSmem& sm, float2* cs) {
+  const int lane = threadIdx.x & 31;
+  const int32_t* pos = p.pos + row * p.pos_stride;
+  __syncwarp();  // the table's last row has been used
+  for (int i = lane; i < p.pairs; i += 32) cs[i] = pair_turn(p, sm.freq[i], pos[sm.axis[i]]);
   __syncwarp();
 }
 
@@ -70,58 +92,101 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // dsa_rope: x [rows, heads, width] -> out, columns [rot_off, rot_off + 2 pairs) turned, the others
 // copied when out is another buffer.
 
-template <bool VEC>
-__global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeParams p) {
-  __shared__ float2 turns[kWarps][kRopeMaxPairs];
+// 16-byte chunks.  A warp's items (16 heads of a row) are software-pipelined: the next item's loads, and its
+// position, are in flight while one is turned and stored.
+__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) rope_vec_kernel(const RopeParams p) {
+  __shared__ RopeSmem sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hblocks = (p.heads + kHeadsPerWarp - 1) / kHeadsPerWarp;
-  const int64_t item = (int64_t)blockIdx.x * kWarps + warp;
-  if (item >= (int64_t)p.rows * hblocks) return;
-  const int64_t row = item / hblocks;
-  const int h0 = (int)(item - row * hblocks) * kHeadsPerWarp;
-  const int nh = min(kHeadsPerWarp, p.heads - h0);
-  const __nv_bfloat16* x = p.x + row * p.x_row_stride + h0 * p.x_head_stride;
-  __nv_bfloat16* out = p.out + row * p.out_row_stride + h0 * p.out_head_stride;
-  float2* cs = turns[warp];
-  fill_turns(p, row, cs);
-  if constexpr (VEC) {
-    const int per = p.half ? p.pairs / 8 : p.pairs / 4;  // items of one head
-    const int n = nh * per;
-    constexpr int U = 4;  // items in flight per lane
-    for (int i0 = lane; i0 < n; i0 += 32 * U) {
-      uint4 a[U], b[U];
+  const int64_t items = (int64_t)p.rows * hblocks, step = (int64_t)gridDim.x * kWarps;
+  fill_freq(p, sm);
+  float2* cs = sm.turns[warp];
+  const int per = p.half ? p.pairs / 8 : p.pairs / 4;  // loads of one head: a chunk and its other half, or a chunk
+  constexpr int U = 2;                                 // chunk pairs per lane and batch
+  const uint64_t f0 = lane < p.pairs ? sm.freq[lane] : 0;
+  const int ax0 = lane < p.pairs ? sm.axis[lane] : 0;
+  uint4 a[U], b[U];
+  int pos0 = 0;
+  // batch of chunks [base, base + 64) of an item: chunk i is head i / per, columns 8 (i % per) (and the same of
+  // the other half); neighbouring pairs take two chunks per step
+  auto chunk = [&](int i, int& h, int& c) {
+    h = i / per;
+    c = i - h * per;
+  };
+  auto fetch = [&](int64_t item, int base) {
+    const int64_t row = hblocks == 1 ? item : item / hblocks;
+    const int h0 = (int)(item - row * hblocks) * kHeadsPerWarp, n = min(kHeadsPerWarp, p.heads - h0) * per;
+    const __nv_bfloat16* x = p.x + row * p.x_row_stride + h0 * p.x_head_stride + p.rot_off;
+    if (base == 0) pos0 = p.pos[row * p.pos_stride + ax0];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + 32 * u;
-        if (i < n) {
-          const int h = i / per, c = i - h * per;
-          const __nv_bfloat16* src = x + h * p.x_head_stride + p.rot_off + 8 * c;
-          a[u] = *reinterpret_cast<const uint4*>(src);
-          if (p.half) b[u] = *reinterpret_cast<const uint4*>(src + p.pairs);
-        }
+    for (int u = 0; u < U; ++u) {
+      int h, c;
+      const int i = base + (p.half ? 32 * u : 64 * u) + lane;
+      if (i < n) {
+        chunk(i, h, c);
+        const __nv_bfloat16* src = x + h * p.x_head_stride + 8 * c;
+        a[u] = *reinterpret_cast<const uint4*>(src);
+        if (p.half) b[u] = *reinterpret_cast<const uint4*>(src + p.pairs);
       }
+      if (!p.half && i + 32 < n) {
+        chunk(i + 32, h, c);
+        b[u] = *reinterpret_cast<const uint4*>(x + h * p.x_head_stride + 8 * c);
+      }
+    }
+  };
+  const int width = p.half ? 32 * U : 64 * U;  // chunks per batch
+  int64_t item = (int64_t)blockIdx.x * kWarps + warp;
+  if (item < items) fetch(item, 0);
+#pragma unroll 1
+  for (; item < items; item += step) {
+    const int64_t row = hblocks == 1 ? item : item / hblocks;
+    const int h0 = (int)(item - row * hblocks) * kHeadsPerWarp, nh = min(kHeadsPerWarp, p.heads - h0), n = nh * per;
+    __nv_bfloat16* out = p.out + row * p.out_row_stride + h0 * p.out_head_stride;
+    __syncwarp();
+    if (lane < p.pairs) cs[lane] = pair_turn(p, f0, pos0);
+    for (int i = lane + 32; i < p.pairs; i += 32)
+      cs[i] = pair_turn(p, sm.freq[i], p.pos[row * p.pos_stride + sm.axis[i]]);
+    __syncwarp();
+    for (int base = 0; base < n; base += width) {
+      uint4 va[U], vb[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) va[u] = a[u], vb[u] = b[u];
+      if (base + width < n) fetch(item, base + width);
+      else if (item + step < items) fetch(item + step, 0);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + 32 * u;
-        if (i < n) {
-          const int h = i / per, c = i - h * per;
-          __nv_bfloat16* dst = out + h * p.out_head_stride + p.rot_off + 8 * c;
-          float va[8], vb[8];
-          unpack8(a[u], va);
-          if (p.half) {
-            unpack8(b[u], vb);
+        int h, c;
+        const int i = base + (p.half ? 32 * u : 64 * u) + lane;
+        float x0[8], x1[8];
+        unpack8(va[u], x0);
+        unpack8(vb[u], x1);
+        if (p.half) {
+          if (i < n) {
+            chunk(i, h, c);
+            __nv_bfloat16* dst = out + h * p.out_head_stride + p.rot_off + 8 * c;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) turn(va[k], vb[k], cs[8 * c + k]);
-            *reinterpret_cast<uint4*>(dst + p.pairs) = pack8(vb);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) turn(va[2 * k], va[2 * k + 1], cs[4 * c + k]);
+            for (int k = 0; k < 8; ++k) turn(x0[k], x1[k], cs[8 * c + k]);
+            *reinterpret_cast<uint4*>(dst) = pack8(x0);
+            *reinterpret_cast<uint4*>(dst + p.pairs) = pack8(x1);
           }
-          *reinterpret_cast<uint4*>(dst) = pack8(va);
+        } else {
+          if (i < n) {
+            chunk(i, h, c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) turn(x0[2 * k], x0[2 * k + 1], cs[4 * c + k]);
+            *reinterpret_cast<uint4*>(out + h * p.out_head_stride + p.rot_off + 8 * c) = pack8(x0);
+          }
+          if (i + 32 < n) {
+            chunk(i + 32, h, c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) turn(x1[2 * k], x1[2 * k + 1], cs[4 * c + k]);
+            *reinterpret_cast<uint4*>(out + h * p.out_head_stride + p.rot_off + 8 * c) = pack8(x1);
+          }
         }
       }
     }
     if (p.copy) {
+      const __nv_bfloat16* x = p.x + row * p.x_row_stride + h0 * p.x_head_stride;
       const int rest = (p.width - 2 * p.pairs) / 8;
       for (int i = lane; i < nh * rest; i += 32) {
         const int h = i / rest;
@@ -131,7 +196,24 @@ __global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeParams p) {
             *reinterpret_cast<const uint4*>(x + h * p.x_head_stride + c);
       }
     }
-  } else {
+  }
+}
+
+// Any offset, pitch and alignment: one pair per lane and step.
+__global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeParams p) {
+  __shared__ RopeSmem sm;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int hblocks = (p.heads + kHeadsPerWarp - 1) / kHeadsPerWarp;
+  const int64_t items = (int64_t)p.rows * hblocks;
+  fill_freq(p, sm);
+  float2* cs = sm.turns[warp];
+#pragma unroll 1
+  for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < items; item += (int64_t)gridDim.x * kWarps) {
+    const int64_t row = item / hblocks;
+    const int h0 = (int)(item - row * hblocks) * kHeadsPerWarp, nh = min(kHeadsPerWarp, p.heads - h0);
+    const __nv_bfloat16* x = p.x + row * p.x_row_stride + h0 * p.x_head_stride;
+    __nv_bfloat16* out = p.out + row * p.out_row_stride + h0 * p.out_head_stride;
+    fill_turns(p, row, sm, cs);
     for (int i = lane; i < nh * p.pairs; i += 32) {
       const int h = i / p.pairs, k = i - h * p.pairs;
       const int c0 = p.rot_off + (p.half ? k : 2 * k), c1 = p.half ? c0 + p.pairs : c0 + 1;
@@ -161,9 +243,28 @@ __device__ __forceinline__ int mx_exponent(float amax) {
   return amax > 0.f ? min(max(ilogbf(amax) - 8, -127), 127) : 0;
 }
 
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
+         (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
+}
+
+// Eight codes of v / s: by the reciprocal where that gives the quotient's codes (Quotient has the
+// argument), with one test for the eight: the smallest distance, in 2^-20 of a binade, of a product from
+// an E4M3 rounding midpoint (mantissa bits 0x80000 below bit 20, both sides 4), and the smallest product.
 __device__ __forceinline__ uint2 encode8(const float (&v)[8], const Quotient& div) {
-  return make_uint2(pack4(to_e4m3(div(v[0])), to_e4m3(div(v[1])), to_e4m3(div(v[2])), to_e4m3(div(v[3]))),
-                    pack4(to_e4m3(div(v[4])), to_e4m3(div(v[5])), to_e4m3(div(v[6])), to_e4m3(div(v[7]))));
+  float q[8], least = INFINITY;
+  uint32_t near = 0xFFFFFFFFu;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    q[k] = v[k] * div.r;
+    near = min(near, __float_as_uint(q[k]) * 4096u - (0x7FFFCu << 12));
+    least = fminf(least, fabsf(q[k]));
+  }
+  if (!(div.fast && near > (8u << 12) && least >= 0x1p-6f)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) q[k] = q[k] == 0.f && div.fast ? q[k] : div(v[k]);
+  }
+  return make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
 }
 
 __device__ __forceinline__ float amax8(const float (&v)[8]) {
@@ -176,104 +277,143 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
 constexpr int kMaxChunks = 4;  // 8-element chunks per lane: rows up to 1024 elements
 
 // Vector form: lane j holds the 8-element chunks j, j + 32, ... of the row, so 4 consecutive lanes hold
-// a group of 32 and 16 lanes a tile of 128.
-template <int FMT>
-__global__ void __launch_bounds__(32 * kWarps) rope_append_vec_kernel(const RopeParams p) {
-  __shared__ float2 turns[kWarps][kRopeMaxPairs];
+// a group of 32 and 16 lanes a tile of 128.  The rotary columns are turned pair by pair, a pair per lane (PP
+// per lane), into fp32 in shared memory, from where the lanes that hold their chunks take them.  The next
+// row's loads (its chunks, pairs, position and destination) are in flight while a row is encoded.
+template <int FMT, int NCH, int PP>
+__global__ void __launch_bounds__(32 * kWarps, NCH == 3 ? kCtasPerSm : 1) rope_append_vec_kernel(const RopeParams p) {
+  __shared__ RopeSmem sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = (int64_t)blockIdx.x * kWarps + warp;
-  if (row >= p.rows) return;
-  const int64_t dst = p.dst_rows ? p.dst_rows[row] : row;
-  if (dst < 0) return;
-  if (dst >= p.dst_count) {
-    if (lane == 0) record_error(p.err, DSA_DEVERR_INDEX_RANGE);
-    return;
-  }
-  const __nv_bfloat16* x = p.x + row * p.x_row_stride;
   const int nch = p.width / 8;
-  uint4 raw[kMaxChunks], other[kMaxChunks];
+  const int64_t step = (int64_t)gridDim.x * kWarps;
+  fill_freq(p, sm);
+  float* turned = reinterpret_cast<float*>(sm.turns[warp]);  // [2 pairs] the row's rotary columns
+  uint64_t freq[PP];
+  int axis[PP];
 #pragma unroll
-  for (int j = 0; j < kMaxChunks; ++j) {
-    const int c = lane + 32 * j;
-    raw[j] = other[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (c < nch) {
-      raw[j] = *reinterpret_cast<const uint4*>(x + 8 * c);
-      const int at = 8 * c - p.rot_off;
-      if (p.half && at >= 0 && at < 2 * p.pairs)
-        other[j] = *reinterpret_cast<const uint4*>(x + 8 * c + (at < p.pairs ? p.pairs : -p.pairs));
-    }
+  for (int i = 0; i < PP; ++i) {
+    const int k = lane + 32 * i;
+    freq[i] = k < p.pairs ? sm.freq[k] : 0;
+    axis[i] = k < p.pairs ? sm.axis[k] : 0;
   }
-  float2* cs = turns[warp];
-  fill_turns(p, row, cs);
-  float v[kMaxChunks][8];
+  uint4 raw[NCH];
+  __nv_bfloat16 x0[PP], x1[PP];
+  int pos[PP];
+  int64_t dst = -1;
+  auto fetch = [&](int64_t row) {
+    const __nv_bfloat16* x = p.x + row * p.x_row_stride;
+    dst = p.dst_rows ? p.dst_rows[row] : row;
 #pragma unroll
-  for (int j = 0; j < kMaxChunks; ++j) {
-    unpack8(raw[j], v[j]);
-    const int at = 8 * (lane + 32 * j) - p.rot_off;
-    if (at >= 0 && at < 2 * p.pairs) {
-      if (p.half) {
-        float w[8];
-        unpack8(other[j], w);
-        const bool low = at < p.pairs;
-        const float2* t = cs + (low ? at : at - p.pairs);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[j][k] = v[j][k] * t[k].x + w[k] * (low ? -t[k].y : t[k].y);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) turn(v[j][2 * k], v[j][2 * k + 1], cs[at / 2 + k]);
+    for (int i = 0; i < PP; ++i) {
+      const int k = lane + 32 * i;
+      if (k < p.pairs) {
+        pos[i] = p.pos[row * p.pos_stride + axis[i]];
+        const int c0 = p.rot_off + (p.half ? k : 2 * k);
+        x0[i] = x[c0];
+        x1[i] = x[p.half ? c0 + p.pairs : c0 + 1];
       }
     }
-  }
-  uint8_t* out = p.dst + dst * p.dst_row_stride;
-  if constexpr (FMT == kFmtBf16) {
 #pragma unroll
-    for (int j = 0; j < kMaxChunks; ++j) {
+    for (int j = 0; j < NCH; ++j) {
       const int c = lane + 32 * j;
-      if (c < nch) *reinterpret_cast<uint4*>(out + 16 * c) = pack8(v[j]);
+      raw[j] = c < nch ? *reinterpret_cast<const uint4*>(x + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
     }
-  } else if constexpr (FMT == kFmtRow) {
-    float a = 0.f;
+  };
+  int64_t row = (int64_t)blockIdx.x * kWarps + warp;
+  if (row < p.rows) fetch(row);
+#pragma unroll 1
+  for (; row < p.rows;) {
+    const int64_t at_row = dst;
+    const bool drop = at_row < 0 || at_row >= p.dst_count;  // the same for the whole warp
+    if (at_row >= p.dst_count && lane == 0) record_error(p.err, DSA_DEVERR_INDEX_RANGE);
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < kMaxChunks; ++j) a = fmaxf(a, amax8(v[j]));
-    const float amax = warp_amax(a);
-    const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-    const Quotient div(s);
-#pragma unroll
-    for (int j = 0; j < kMaxChunks; ++j) {
-      const int c = lane + 32 * j;
-      if (c < nch) *reinterpret_cast<uint2*>(out + 8 * c) = encode8(v[j], div);
-    }
-    if (lane == 0) reinterpret_cast<float*>(p.scale)[dst] = s;
-  } else if constexpr (FMT == kFmtTile) {
-    const int tiles = (p.width + 127) / 128;
-#pragma unroll
-    for (int j = 0; j < kMaxChunks; ++j) {
-      const int c = lane + 32 * j;
-      float a = amax8(v[j]);
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-      const float s = a > 0.f ? __fdiv_rn(a, 448.f) : 1.f;
-      if (c < nch) {
-        *reinterpret_cast<uint2*>(out + 8 * c) = encode8(v[j], Quotient(s));
-        if ((lane & 15) == 0) reinterpret_cast<float*>(p.scale)[dst * tiles + c / 16] = s;
+    for (int i = 0; i < PP; ++i) {
+      const int k = lane + 32 * i;
+      if (k < p.pairs) {
+        float a = __bfloat162float(x0[i]), b = __bfloat162float(x1[i]);
+        turn(a, b, pair_turn(p, freq[i], pos[i]));
+        turned[p.half ? k : 2 * k] = a;
+        turned[p.half ? k + p.pairs : 2 * k + 1] = b;
       }
     }
-  } else {
+    __syncwarp();
+    float v[NCH][8];
 #pragma unroll
-    for (int j = 0; j < kMaxChunks; ++j) {
-      const int c = lane + 32 * j;
-      float a = amax8(v[j]);
-      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-      if (c < nch) {
-        const int e = mx_exponent(a);
-        const float inv = ldexpf(1.f, -e);  // a power of two: exact
-        uint8_t q[8];
+    for (int j = 0; j < NCH; ++j) {
+      unpack8(raw[j], v[j]);
+      const int at = 8 * (lane + 32 * j) - p.rot_off;
+      if (at >= 0 && at < 2 * p.pairs) {
+        const float4 t0 = *reinterpret_cast<const float4*>(turned + at), t1 = *reinterpret_cast<const float4*>(turned + at + 4);
+        v[j][0] = t0.x, v[j][1] = t0.y, v[j][2] = t0.z, v[j][3] = t0.w;
+        v[j][4] = t1.x, v[j][5] = t1.y, v[j][6] = t1.z, v[j][7] = t1.w;
+      }
+    }
+    row += step;
+    if (row < p.rows) fetch(row);
+    if (drop) continue;
+    uint8_t* out = p.dst + at_row * p.dst_row_stride;
+    if constexpr (FMT == kFmtBf16) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q[k] = to_e4m3(v[j][k] * inv);
-        *reinterpret_cast<uint2*>(out + 8 * c) =
-            make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
-        if ((lane & 3) == 0) p.scale[dst * (p.width / 32) + c / 4] = (uint8_t)(e + 127);
+      for (int j = 0; j < NCH; ++j) {
+        const int c = lane + 32 * j;
+        if (c < nch) *reinterpret_cast<uint4*>(out + 16 * c) = pack8(v[j]);
+      }
+    } else if constexpr (FMT == kFmtRow) {
+      float a = 0.f;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) a = fmaxf(a, amax8(v[j]));
+      const float amax = warp_amax(a);
+      const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+      const Quotient div(s);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const int c = lane + 32 * j;
+        if (c < nch) *reinterpret_cast<uint2*>(out + 8 * c) = encode8(v[j], div);
+      }
+      if (lane == 0) reinterpret_cast<float*>(p.scale)[at_row] = s;
+    } else if constexpr (FMT == kFmtTile) {
+      const int tiles = (p.width + 127) / 128;
+      // the tiles' maxima, one per 16 lanes and j; then lane j of each 16 takes tile j's scale and reciprocal
+      // (a division each, once instead of NCH times)
+      float own = 0.f;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        float a = amax8(v[j]);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        if ((lane & 15) == j) own = a;
+      }
+      Quotient div(own > 0.f ? __fdiv_rn(own, 448.f) : 1.f);
+      const float s_own = div.s, r_own = div.r;
+      const uint32_t fast = __ballot_sync(0xffffffffu, div.fast);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const int c = lane + 32 * j, from = (lane & 16) + j;
+        div.s = __shfl_sync(0xffffffffu, s_own, from);
+        div.r = __shfl_sync(0xffffffffu, r_own, from);
+        div.fast = (fast >> from) & 1;
+        if (c < nch) {
+          *reinterpret_cast<uint2*>(out + 8 * c) = encode8(v[j], div);
+          if ((lane & 15) == 0) reinterpret_cast<float*>(p.scale)[at_row * tiles + c / 16] = div.s;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        if (32 * j >= nch) break;
+        const int c = lane + 32 * j;
+        float a = amax8(v[j]);
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        if (c < nch) {
+          const int e = mx_exponent(a);
+          const float inv = ldexpf(1.f, -e);  // a power of two: exact
+          *reinterpret_cast<uint2*>(out + 8 * c) =
+              make_uint2(e4m3x4(v[j][0] * inv, v[j][1] * inv, v[j][2] * inv, v[j][3] * inv),
+                         e4m3x4(v[j][4] * inv, v[j][5] * inv, v[j][6] * inv, v[j][7] * inv));
+          if ((lane & 3) == 0) p.scale[at_row * (p.width / 32) + c / 4] = (uint8_t)(e + 127);
+        }
       }
     }
   }
@@ -283,8 +423,9 @@ __global__ void __launch_bounds__(32 * kWarps) rope_append_vec_kernel(const Rope
 // group (the row, 128 or 32 elements) is taken in two passes, its maximum and its codes.
 template <int FMT>
 __global__ void __launch_bounds__(32 * kWarps) rope_append_kernel(const RopeParams p) {
-  __shared__ float2 turns[kWarps][kRopeMaxPairs];
+  __shared__ RopeSmem sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  fill_freq(p, sm);
   const int64_t row = (int64_t)blockIdx.x * kWarps + warp;
   if (row >= p.rows) return;
   const int64_t dst = p.dst_rows ? p.dst_rows[row] : row;
@@ -294,8 +435,8 @@ __global__ void __launch_bounds__(32 * kWarps) rope_append_kernel(const RopePara
     return;
   }
   const __nv_bfloat16* x = p.x + row * p.x_row_stride;
-  float2* cs = turns[warp];
-  fill_turns(p, row, cs);
+  float2* cs = sm.turns[warp];
+  fill_turns(p, row, sm, cs);
   auto value = [&](int c) {
     const float v = __bfloat162float(x[c]);
     const int at = c - p.rot_off;
@@ -330,6 +471,12 @@ __global__ void __launch_bounds__(32 * kWarps) rope_append_kernel(const RopePara
       }
     }
   }
+}
+
+using AppendKernel = void (*)(const RopeParams);
+template <int FMT>
+AppendKernel append_vec(bool small) {
+  return small ? rope_append_vec_kernel<FMT, 3, 1> : rope_append_vec_kernel<FMT, kMaxChunks, 4>;
 }
 
 // What both entries check of the rotation itself; fills the pair -> axis table.
@@ -393,9 +540,10 @@ dsa_status dsa_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride, 
                    aligned(out, 16) && (rows == 1 || (x_row_stride % 8 == 0 && out_row_stride % 8 == 0)) &&
                    p.x_head_stride % 8 == 0 && p.out_head_stride % 8 == 0;
   const int64_t items = (int64_t)rows * ((heads + kHeadsPerWarp - 1) / kHeadsPerWarp);
-  const int64_t grid = (items + kWarps - 1) / kWarps;
-  if (grid >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
-  auto kern = vec ? rope_kernel<true> : rope_kernel<false>;
+  const int64_t want = (items + kWarps - 1) / kWarps;
+  const int64_t most = vec ? kSms * kCtasPerSm : 8 * kSms;
+  const int64_t grid = want < most ? want : most;
+  auto kern = vec ? rope_vec_kernel : rope_kernel;
   kern<<<(unsigned)grid, 32 * kWarps, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
@@ -431,16 +579,21 @@ dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int wi
   p.err = device_error_word();
   const uintptr_t out_align = elem == 2 ? 16 : 8;
   const bool vec = width % 8 == 0 && width <= 256 * kMaxChunks && rot_off % 8 == 0 &&
-                   p.pairs % (p.half ? 8 : 4) == 0 && aligned(x, 16) && (rows == 1 || x_row_stride % 8 == 0) &&
+                   (2 * p.pairs) % 8 == 0 && aligned(x, 16) && (rows == 1 || x_row_stride % 8 == 0) &&
                    aligned(dst, out_align) && dst_row_stride % (int64_t)out_align == 0;
-  void (*kern)(const RopeParams) = nullptr;
+  // rows of up to 768 columns with up to 32 pairs (the latent row) take the form with fewer registers
+  const bool small = width <= 768 && p.pairs <= 32;
+  AppendKernel kern = nullptr;
   switch (dtype) {
-    case DSA_BF16: kern = vec ? rope_append_vec_kernel<kFmtBf16> : rope_append_kernel<kFmtBf16>; break;
-    case DSA_FP8_E4M3: kern = vec ? rope_append_vec_kernel<kFmtRow> : rope_append_kernel<kFmtRow>; break;
-    case DSA_FP8_E4M3_T128: kern = vec ? rope_append_vec_kernel<kFmtTile> : rope_append_kernel<kFmtTile>; break;
-    default: kern = vec ? rope_append_vec_kernel<kFmtMx> : rope_append_kernel<kFmtMx>; break;
+    case DSA_BF16: kern = vec ? append_vec<kFmtBf16>(small) : rope_append_kernel<kFmtBf16>; break;
+    case DSA_FP8_E4M3: kern = vec ? append_vec<kFmtRow>(small) : rope_append_kernel<kFmtRow>; break;
+    case DSA_FP8_E4M3_T128: kern = vec ? append_vec<kFmtTile>(small) : rope_append_kernel<kFmtTile>; break;
+    default: kern = vec ? append_vec<kFmtMx>(small) : rope_append_kernel<kFmtMx>; break;
   }
-  kern<<<(rows + kWarps - 1) / kWarps, 32 * kWarps, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  int grid = (rows + kWarps - 1) / kWarps;
+  const int most = kSms * (small ? kCtasPerSm : 1);
+  if (vec && grid > most) grid = most;
+  kern<<<grid, 32 * kWarps, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 

@@ -1076,7 +1076,8 @@ cudaError_t launch_fmt(const TreeAttnParams& p, TreePlan pl, void* ws, cudaStrea
     pl.part_o = reinterpret_cast<float4*>(w);
   }
   auto kern = tree_attn_kernel<FMT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem_once(&allowed, reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   e = launch_kernel(kern, dim3(2 * pl.grid), dim3(C::THREADS), C::SMEM, stream, false, tm, tm_rope, p, pl);
   if (e != cudaSuccess || !pl.cap) return e;
