@@ -9,9 +9,9 @@
 // columns, so every byte of the cache enters one SM's shared memory once and serves both products:
 //   * partial S[128 x 64] = Q_c K_c^T: A = the rows in tensor memory (M = 128, 256 columns of q; the rotary
 //     half from shared memory), B = the tile (K-major), 18 steps of K = 16;
-//   * the two CTAs send each other their partial S through distributed shared memory (st.async, counted on
-//     the receiver's mbarrier) and both add them: S0 + S1 is the same number on both sides, so both take
-//     the same softmax and no other exchange is needed;
+//   * each CTA takes the softmax of 64 of the rows: the other sends it its partial S of those rows through
+//     distributed shared memory (st.async, counted on the receiver's mbarrier), and gets their P (bf16)
+//     back, so both hold P for all rows: 24 KB per tile each way;
 //   * one pass over the positions keeps a reference maximum m and a sum l per row,
 //       l' = l 2^(m - m') + sum_p 2^(x_p - m'),   o' = o 2^(m - m') + sum_p 2^(x_p - m') v_p,
 //     where m is moved only when a tile's maximum exceeds it by more than 2^8 (weights stay below 2^8,
@@ -27,9 +27,9 @@
 // outputs are fp32.  E4M3 rows are widened to bf16 exactly, and their scales are applied in fp32 to the
 // logit and to the weight (128-column scales: one S accumulator per scale tile, one P per value tile).
 //
-// Warp roles: producer (TMA), MMA issuer, scale loader, credits of the exchange, four senders, eight softmax
-// warps (also the query load, the rescale and the epilogue), for E4M3 four warps that widen the raw
-// tile in shared memory.
+// Warp roles: producer (TMA), MMA issuer, scale loader, credits of the exchange, eight row warps (four take
+// the softmax of this CTA's rows, four send the other's partial logits and take in its P; all of them
+// the query load, the rescale and the epilogue), for E4M3 four warps that load, widen and store the tile.
 //
 // Work split: items (sequence, chunk of its tiles, row tile), in this order, so that clusters that run
 // together read the same positions and the cache comes from HBM once.  The lengths are on the device:
@@ -48,7 +48,6 @@ constexpr int kRows = 128;                // query rows per cluster
 constexpr int kKeys = 64;                 // positions per tile
 constexpr int kBox = kKeys * 128;         // one 64-column box of a tile: 64 rows x 128 bytes
 constexpr int kTile = 5 * kBox;           // four value boxes and the rotary one
-constexpr int kRaw = kKeys * 288;         // the same columns as E4M3 codes: 64 x 256 and 64 x 32
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLazy = 8.f;              // log2 growth of a row's maximum that is left unscaled
 constexpr int kItemsPerCta = 3;           // split launches are cut into at most this many items per cluster
@@ -62,21 +61,22 @@ struct Cfg {
   static constexpr bool FP8 = FMT != kBf16;
   static constexpr int NSC = FMT == kFp8Tile ? 5 : FMT == kFp8Row ? 1 : 0;
   static constexpr bool TILED = FMT == kFp8Tile;
-  static constexpr int THREADS = FP8 ? 640 : 512;
-  static constexpr int STAGES = FP8 ? 2 : 3;              // tiles in shared memory
-  static constexpr int RAWS = TILED ? 1 : FP8 ? 2 : 0;    // raw E4M3 tiles
+  static constexpr int THREADS = FP8 ? 512 : 384;
+  static constexpr int STAGES = 3;                        // tiles in shared memory
   static constexpr int PC = TILED ? 2 : 1;                // copies of P (one per 128 values)
+  static constexpr int PB = TILED ? 1 : 2;                // P buffers
   static constexpr int SC_DEPTH = 2;
   static constexpr int SC_BYTES = NSC * kKeys * 4;
-  static constexpr int X_BYTES = kRows * kKeys * 4;       // the peer's partial S (two buffers)
+  static constexpr int X_BYTES = kRows / 2 * kKeys * 4;   // the peer's partial S of our rows (two buffers)
   static constexpr int QR_BYTES = kRows * 128;            // q's rotary columns
   static constexpr int P_BYTES = kRows * 128;             // P: 128 rows x 64 positions
-  static constexpr int AUX = 2048;
+  // what a CTA sends of a tile: its rows of P, their rescale factors, the positions to clear
+  static constexpr int MSG_BYTES = PC * P_BYTES / 2 + 64 * 4 + 4 * 4;
+  static constexpr int AUX = 2560;
   static constexpr int OFF_X = STAGES * kTile;
   static constexpr int OFF_QR = OFF_X + 2 * X_BYTES;
   static constexpr int OFF_P = OFF_QR + QR_BYTES;
-  static constexpr int OFF_RAW = OFF_P + PC * P_BYTES;
-  static constexpr int OFF_SC = OFF_RAW + RAWS * kRaw;
+  static constexpr int OFF_SC = OFF_P + PB * PC * P_BYTES;
   static constexpr int OFF_AUX = OFF_SC + SC_DEPTH * SC_BYTES;
   static constexpr int SMEM = OFF_AUX + AUX + 1024;
   static_assert(SMEM <= kSmemMax, "shared memory");
@@ -110,27 +110,41 @@ __device__ __forceinline__ int live_row_tiles(const TreeAttnParams& p, int fresh
 }
 
 struct Aux {
-  uint64_t full[4], empty[4], raw_full[3], raw_empty[3];
-  uint64_t s_full[2], s_empty[2], x_full[2], x_read[2], x_free[2], p_full, pv_done, o_done, o_free, q_full, sc_full[2], sc_empty[2], drain;
+  uint64_t full[3], empty[3];
+  uint64_t s_full[2], s_empty[2], x_full[2], x_read[2], x_free[2];
+  uint64_t p_full[2], p_msg[2], p_free[2], pv_done[2], stat_full, o_done, o_free, q_full, sc_full[2], sc_empty[2], drain;
   uint32_t tmem;
   int abort;
   int n_items;
   int tile_bad[4];
   int items[kItemsPerCta][8];
-  int kbad[kKeys];
-  float red[2][kRows];     // per half row: maxima, then sums
+  float fac[2][64];        // the peer's rescale factors of its rows
+  uint32_t clear[2][4];    // positions to clear, from the peer (quarter, half)
+  uint32_t clear_own[2][4];
+  float red[2][64];        // per half of our rows: maxima, then sums
+  float stat[64];          // the peer's sums
 };
-static_assert(sizeof(Aux) <= 2048, "Aux");
+static_assert(sizeof(Aux) <= 2560, "Aux");
 
-// A bounded wait that gives up at once when another wait of this CTA already has.
-__device__ __forceinline__ bool wait(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
-  if (mbar_try_wait(bar, parity)) return true;
-  if (*reinterpret_cast<volatile int*>(&a->abort)) return false;
-  if (mbar_wait(bar, parity, err)) return true;
-  *reinterpret_cast<volatile int*>(&a->abort) = 1;
-  return false;
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, P;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
+// A bounded wait.  Once one wait of the CTA has run out, the others return at once: the warps then walk
+// through the rest of their work without waiting (every address stays in range), so that their common
+// barriers still match, and the kernel ends.
+__device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err, bool cluster);
+__device__ __forceinline__ bool wait(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
+  return mbar_test(bar, parity) || wait_slow(a, bar, parity, err, false);
+}
 // The same for a barrier that the other CTA of the cluster arrives on: what it did before is visible after.
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -144,12 +158,22 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
   return ok != 0;
 }
 __device__ __forceinline__ bool wait_cluster(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
-  if (try_wait_cluster(bar, parity)) return true;
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, P;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok || wait_slow(a, bar, parity, err, true);
+}
+__device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err, bool cluster) {
   const unsigned long long t0 = globaltimer_ns();
   for (uint32_t i = 0;; ++i) {
-    if (try_wait_cluster(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&a->abort)) return false;
-    if ((i & 255u) == 255u && globaltimer_ns() - t0 > kWaitLimitNs) {
+    if (cluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 63u && globaltimer_ns() - t0 > kWaitLimitNs) {
       record_error(err, DSA_DEVERR_WAIT_TIMEOUT);
       *reinterpret_cast<volatile int*>(&a->abort) = 1;
       return false;
@@ -169,19 +193,26 @@ __device__ __forceinline__ void st_async16(uint32_t addr, const float* v, uint32
                : "memory");
 }
 
-__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ bool softmax_any(bool pred) {
+__device__ __forceinline__ void st_async4(uint32_t addr, uint32_t v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
+               : "memory");
+}
+
+// Barriers: of the two warps that share 32 rows (id 1 or 2), of all eight row warps (id 3).
+__device__ __forceinline__ void pair_bar(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_any(int id, bool pred) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 2, 256, p;\n\t"
+      "bar.red.or.pred q, %2, 64, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)pred)
+      : "r"((uint32_t)pred), "r"(id)
       : "memory");
   return r != 0;
 }
+__device__ __forceinline__ void row_bar() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
 // A value that is the same in all lanes, as one the compiler knows to be so (a warp-wide reduction writes
 // a uniform register): the MMA issuer's loop bounds and addresses go through it, because operands in
@@ -394,8 +425,7 @@ __device__ __forceinline__ bool get_item(const TreeAttnParams& p, const TreePlan
 
 template <int FMT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1)
-    tree_attn_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_rope,
-                     const TreeAttnParams p, const TreePlan pl) {
+    tree_attn_kernel(const __grid_constant__ CUtensorMap tm, const TreeAttnParams p, const TreePlan pl) {
   using C = Cfg<FMT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -403,11 +433,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
   uint8_t* x_s = smem + C::OFF_X;
   uint8_t* qr_s = smem + C::OFF_QR;
   uint8_t* p_s = smem + C::OFF_P;
-  uint8_t* raw_s = smem + C::OFF_RAW;
   float* sc_s = reinterpret_cast<float*>(smem + C::OFF_SC);
   Aux* a = reinterpret_cast<Aux*>(smem + C::OFF_AUX);
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
-  const int rank = uniform((int)cluster_rank());  // which half of the columns
+  const int rank = uniform((int)cluster_rank());  // which half of the columns, and which 64 of the rows
   int* err = p.err;
 
   if (warp == 0) {
@@ -415,24 +444,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
     tmem_relinquish();
   }
   if (tid == 32) {
-    for (int i = 0; i < C::STAGES; ++i) mbar_init(&a->full[i], C::FP8 ? 4 : 1), mbar_init(&a->empty[i], 1);
-    for (int i = 0; i < 3; ++i) mbar_init(&a->raw_full[i], 1), mbar_init(&a->raw_empty[i], 4);
-    for (int i = 0; i < 2; ++i) mbar_init(&a->sc_full[i], 32), mbar_init(&a->sc_empty[i], 8);
+    for (int i = 0; i < 3; ++i) mbar_init(&a->full[i], C::FP8 ? 4 : 1), mbar_init(&a->empty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&a->s_full[i], 1), mbar_init(&a->s_empty[i], C::TILED ? 8 : 12);
-      mbar_init(&a->x_full[i], 1), mbar_init(&a->x_read[i], 8), mbar_init(&a->x_free[i], 1);
+      mbar_init(&a->s_full[i], 1), mbar_init(&a->s_empty[i], 8);
+      mbar_init(&a->x_full[i], 1), mbar_init(&a->x_read[i], 4), mbar_init(&a->x_free[i], 1);
+      mbar_init(&a->p_full[i], 8), mbar_init(&a->p_msg[i], 1), mbar_init(&a->p_free[i], 1), mbar_init(&a->pv_done[i], 1);
+      mbar_init(&a->sc_full[i], 32), mbar_init(&a->sc_empty[i], C::TILED ? 8 : 4);
     }
-    mbar_init(&a->p_full, 8);
-    mbar_init(&a->pv_done, 1);
+    mbar_init(&a->stat_full, 1);
     mbar_init(&a->o_done, 1);
     mbar_init(&a->o_free, 8);
     mbar_init(&a->q_full, 256);
     mbar_init(&a->drain, 1);
     a->abort = 0;
     fence_mbar_init();
-    for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&a->x_full[i], C::X_BYTES);
+    for (int i = 0; i < 2; ++i) {
+      mbar_arrive_expect_tx(&a->x_full[i], C::X_BYTES);
+      mbar_arrive_expect_tx(&a->p_msg[i], C::MSG_BYTES);
+    }
+    mbar_arrive_expect_tx(&a->stat_full, 64 * 4);
   }
-  if (tid < kKeys) a->kbad[tid] = 0;
   if (pl.cap) plan_items(p, pl, a, reinterpret_cast<int*>(tiles_s));
   fence_proxy_async_smem();  // the plan's scratch is a tile that the copies write
   tc_fence_before();
@@ -444,12 +475,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
 
   Item it;
   if (warp == 0) {
-    // ---- producer: this CTA's columns of each tile by TMA (bf16: into the tile; E4M3: the raw codes)
-    if (lane == 0) {
+    // ---- producer (bf16): this CTA's columns of each tile by TMA
+    if (lane == 0 && !C::FP8) {
       prefetch_tmap(&tm);
-      constexpr int N = C::FP8 ? C::RAWS : C::STAGES;
-      uint64_t* full = C::FP8 ? a->raw_full : a->full;
-      uint64_t* empty = C::FP8 ? a->raw_empty : a->empty;
       int sl = 0, ph = 0, tiles = 0;
       bool ok = true;
       for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
@@ -463,26 +491,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
             row = bad ? p.pages.num_blocks * p.pages.block_size : (int)r;
             if (bad) record_error(err, DSA_DEVERR_INDEX_RANGE);
           }
-          ok = wait(a, &empty[sl], ph ^ 1, err);
+          ok = wait(a, &a->empty[sl], ph ^ 1, err);
           if (!ok) break;
-          if (!C::FP8) a->tile_bad[tiles & 3] = bad;
-          if (C::FP8) {
-            uint8_t* dst = raw_s + sl * kRaw;
-            mbar_arrive_expect_tx(&full[sl], kRaw);
-            tma_load_3d(dst, &tm, &full[sl], 256 * rank, row, z);
-            tma_load_3d(dst + kKeys * 256, &tm_rope, &full[sl], 512 + 32 * rank, row, z);
-          } else {
-            uint8_t* dst = tiles_s + sl * kTile;
-            mbar_arrive_expect_tx(&full[sl], kTile);
+          a->tile_bad[tiles & 3] = bad;
+          uint8_t* dst = tiles_s + sl * kTile;
+          mbar_arrive_expect_tx(&a->full[sl], kTile);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) tma_load_3d(dst + b * kBox, &tm, &full[sl], 256 * rank + 64 * b, row, z);
-            tma_load_3d(dst + 4 * kBox, &tm, &full[sl], 512, row, z);
-          }
-          if (++sl == N) sl = 0, ph ^= 1;
+          for (int b = 0; b < 4; ++b) tma_load_3d(dst + b * kBox, &tm, &a->full[sl], 256 * rank + 64 * b, row, z);
+          tma_load_3d(dst + 4 * kBox, &tm, &a->full[sl], 512, row, z);
+          if (++sl == C::STAGES) sl = 0, ph ^= 1;
         }
       }
       if (*reinterpret_cast<volatile int*>(&a->abort))  // wind down: the copies in flight land first
-        for (int s = 0; s < N; ++s) mbar_wait(&full[s], s < sl ? ph : ph ^ 1, err);
+        for (int s = 0; s < C::STAGES; ++s) mbar_wait(&a->full[s], s < sl ? ph : ph ^ 1, err);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -499,18 +520,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
     int tile = 0, items = 0;
     uint32_t su = 0;              // uses of the S buffers
     bool ok = true;
-    auto all = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, wait(a, bar, parity, err)); };
+    auto all = [&](uint64_t* bar, uint32_t parity) { ok = __all_sync(0xffffffffu, wait(a, bar, parity, err)) && ok; };
     auto commit = [&](uint64_t* bar) {
       if (elect_one()) tc_commit(bar);
       __syncwarp();
     };
     // First product of the next tile, group g of its columns: all of them (-1), or for 128-column scales
-    // one accumulation per scale tile (0, 1: 128 value columns; 2: the rotary ones).  The softmax warps
-    // have read what S held.
+    // one accumulation per scale tile (0, 1: 128 value columns; 2: the rotary ones).  The row warps have
+    // read what the S buffer held.
     auto qk = [&](int g) {
       if (g <= 0) all(&a->full[qs], qph);
       all(&a->s_empty[su & 1], ((su >> 1) & 1) ^ 1);
-      if (!ok) return;
       tc_fence_after();
       const uint32_t d = tm_base + kColS + 64 * (su & 1), B = k_lo + qs * (kTile >> 4);
       if (elect_one()) {
@@ -533,46 +553,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         if (++qs == C::STAGES) qs = 0, qph ^= 1;
       }
     };
+    auto qk_tile = [&]() {
+      if (C::TILED) qk(0), qk(1), qk(2);
+      else qk(-1);
+    };
     auto pv = [&](bool first) {
       const uint32_t acc0 = first ? 0u : 1u, B = v_lo + ps * (kTile >> 4);
+      const uint32_t P = p_lo + (tile % C::PB) * (C::PC * C::P_BYTES >> 4);
       if (elect_one()) {
         constexpr int NB = C::TILED ? 2 : 1;  // value tiles of N = 128 with a P each, or all 256 at once
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            mma_ss(tm_base + kColO + 128 * b, p_lo + (b * C::P_BYTES + 32 * ks) / 16, B + (2 * b * kBox + 2048 * ks) / 16,
+            mma_ss(tm_base + kColO + 128 * b, P + (b * C::P_BYTES + 32 * ks) / 16, B + (2 * b * kBox + 2048 * ks) / 16,
                    idesc_pv, ks ? 1u : acc0);
         tc_commit(&a->empty[ps]);
-        tc_commit(&a->pv_done);
+        tc_commit(&a->pv_done[tile & 1]);
       }
       __syncwarp();
       if (++ps == C::STAGES) ps = 0;
     };
-    for (int i = 0; ok && uniform(get_item(p, pl, a, i, it)); ++i) {
+    constexpr int AHEAD = C::TILED ? 1 : 2;  // tiles whose first product is issued before P of this one is there
+    for (int i = 0; uniform(get_item(p, pl, a, i, it)); ++i) {
       const int t0 = uniform(it.t0), t1 = uniform(it.t1);
       if (t0 >= t1) continue;
       all(&a->q_full, items & 1);
       tc_fence_after();
-      if (C::TILED) {
-        for (int g = 0; ok && g < 3; ++g) qk(g);
-      } else if (ok) {
-        qk(-1);
-      }
-      for (int t = t0; ok && t < t1; ++t, ++tile) {
-        const bool next = t + 1 < t1;
-        if (next && ok) qk(C::TILED ? 0 : -1);
-        all(&a->p_full, tile & 1);
+      int tq = t0;  // the next tile to start
+      for (; tq < t1 && tq < t0 + AHEAD; ++tq) qk_tile();
+      for (int t = t0; t < t1; ++t, ++tile) {
+        // the tile after next early, if it and its S buffer are ready; P of this one first otherwise
+        bool started = tq >= t1;
+        if (!started && (C::TILED || __all_sync(0xffffffffu, mbar_test(&a->full[qs], qph) &&
+                                                                 mbar_test(&a->s_empty[su & 1], ((su >> 1) & 1) ^ 1)))) {
+          qk_tile();
+          ++tq;
+          started = true;
+        }
+        all(&a->p_full[tile & 1], (tile >> 1) & 1);
         if (t == t0) all(&a->o_free, (items & 1) ^ 1);
-        if (!ok) break;
         tc_fence_after();
         pv(t == t0);
-        if (!next) commit(&a->o_done);
-        if (next && C::TILED) {
-          qk(1);
-          if (ok) qk(2);
+        if (!started) {
+          qk_tile();
+          ++tq;
         }
       }
+      commit(&a->o_done);
       ++items;
     }
     if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&a->abort))) {
@@ -598,123 +626,163 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < C::NSC * 2; ++k) sc_s[d * kKeys * C::NSC + lane + 32 * k] = v[k];
-        if (lane == 0) a->tile_bad[tiles & 3] = bad;
+        if (lane == 0) {
+          a->tile_bad[tiles & 3] = bad;
+          if (bad) record_error(err, DSA_DEVERR_INDEX_RANGE);
+        }
         __syncwarp();
         mbar_arrive(&a->sc_full[d]);
       }
     }
   } else if (warp == 3) {
-    // ---- credits of the exchange: once the softmax warps have read the peer's part, its buffer is armed for
-    // the tile after next and the peer told so (here, because a release at cluster scope would hold up
-    // the softmax warps)
+    // ---- credits of the exchange (here, because a release at cluster scope would hold up the row warps): once
+    // our softmax warps have read the peer's part of S, its buffer is armed for the tile after next and
+    // the peer told so; once a second product has read P, the peer may send into that buffer again
     int tiles = 0;
     bool ok = true;
-    const uint32_t peer_free = dsmem_addr(&a->x_free[0], rank ^ 1);
+    const uint32_t peer_x = dsmem_addr(&a->x_free[0], rank ^ 1), peer_p = dsmem_addr(&a->p_free[0], rank ^ 1);
     for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
       for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
         const int b = tiles & 1;
         ok = __all_sync(0xffffffffu, wait(a, &a->x_read[b], (tiles >> 1) & 1, err));
         if (ok && lane == 0) {
           mbar_arrive_expect_tx(&a->x_full[b], C::X_BYTES);
-          arrive_remote(peer_free + 8 * b);
+          arrive_remote(peer_x + 8 * b);
         }
+        __syncwarp();
+        ok = ok && __all_sync(0xffffffffu, wait(a, &a->pv_done[b], (tiles >> 1) & 1, err));
+        if (ok && lane == 0) arrive_remote(peer_p + 8 * (tiles % C::PB));
         __syncwarp();
       }
     }
-  } else if (warp >= 16) {
-    // ---- converters (E4M3): raw codes -> the swizzled bf16 boxes.  A half warp takes 128 codes of a position,
-    // eight per lane (one 16-byte chunk of bf16), so that loads and stores touch every bank once.
-    const int cw = warp - 16, hw = lane >> 4, l16 = lane & 15;
-    int rs = 0, rph = 0, st = 0, sph = 0;
+  } else if (warp >= 12) {
+    // ---- converters (E4M3): 16 codes per lane and step, loaded a tile ahead, widened into the swizzled bf16
+    // boxes.  Eight lanes take four 16-code chunks of one box from two neighbouring positions: their eight
+    // 16-byte stores fall into different banks.
+    const int ct = tid - 384, cw = warp - 12;
+    int st = 0, sph = 0;
     bool ok = true;
-    auto widen = [&](uint2 v) {
-      return make_uint4(e4m3x2_to_bf16x2(v.x, 0x1404), e4m3x2_to_bf16x2(v.x, 0x3424), e4m3x2_to_bf16x2(v.y, 0x1404),
-                        e4m3x2_to_bf16x2(v.y, 0x3424));
+    uint4 raw[9];
+    auto place = [&](int k, int& key, int& box, int& c) {  // chunk c of 16 codes of a box of 64 columns
+      if (k < 8) {
+        const int unit = 16 * k + 4 * cw + (lane >> 3);
+        box = unit & 3, key = 2 * (unit >> 2) + ((lane >> 2) & 1), c = lane & 3;
+      } else {  // the rotary half: 32 codes of a position
+        box = 4, key = ct >> 1, c = 2 * rank + (ct & 1);
+      }
+    };
+    auto tile_rows = [&](const Item& x, int t) -> const uint8_t* {
+      if (t >= x.t1) return nullptr;
+      const int64_t row = tree_row(p, x.seq, t * kKeys);
+      if (row < 0) return nullptr;
+      return p.kv + (p.pages.table ? 0 : (int64_t)x.seq * p.kv_seq_stride) + row * p.kv_row_stride;
+    };
+    auto fetch = [&](const uint8_t* r, int n, int k) {
+      int key, box, c;
+      place(k, key, box, c);
+      const int col = (box < 4 ? 256 * rank + 64 * box : 512) + 16 * c;
+      raw[k] = r && key < n ? __ldg(reinterpret_cast<const uint4*>(r + (int64_t)key * p.kv_row_stride + col))
+                            : make_uint4(0u, 0u, 0u, 0u);
     };
     for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
+      const uint8_t* r = tile_rows(it, it.t0);
+#pragma unroll
+      for (int k = 0; k < 9; ++k) fetch(r, it.len - it.t0 * kKeys, k);
       for (int t = it.t0; ok && t < it.t1; ++t) {
-        ok = __all_sync(0xffffffffu, wait(a, &a->raw_full[rs], rph, err));
-        ok = ok && __all_sync(0xffffffffu, wait(a, &a->empty[st], sph ^ 1, err));
+        r = tile_rows(it, t + 1);
+        const int n = it.len - (t + 1) * kKeys;
+        ok = __all_sync(0xffffffffu, wait(a, &a->empty[st], sph ^ 1, err));
         if (!ok) break;
-        const uint8_t* raw = raw_s + rs * kRaw;
         uint8_t* dst = tiles_s + st * kTile;
-        uint2 rot[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          rot[k] = *reinterpret_cast<const uint2*>(raw + kKeys * 256 + (cw * 16 + 8 * k + (lane >> 2)) * 32 + 8 * (lane & 3));
-        // unit u of 128: position u / 2, codes 128 (u % 2) + 8 l16 ...; eight loads in flight
-#pragma unroll 1
-        for (int k0 = 0; k0 < 16; k0 += 8) {
-          uint2 v[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int u = cw * 32 + 2 * (k0 + k) + hw;
-            v[k] = *reinterpret_cast<const uint2*>(raw + (u >> 1) * 256 + 128 * (u & 1) + 8 * l16);
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int u = cw * 32 + 2 * (k0 + k) + hw, key = u >> 1, box = 2 * (u & 1) + (l16 >> 3), c = l16 & 7;
-            *reinterpret_cast<uint4*>(dst + box * kBox + key * 128 + ((c ^ (key & 7)) << 4)) = widen(v[k]);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {  // the rotary half: 32 codes of a position, four lanes
-          const int key = cw * 16 + 8 * k + (lane >> 2), c = 4 * rank + (lane & 3);
-          *reinterpret_cast<uint4*>(dst + 4 * kBox + key * 128 + ((c ^ (key & 7)) << 4)) = widen(rot[k]);
+        for (int k = 0; k < 9; ++k) {
+          int key, box, c;
+          place(k, key, box, c);
+          uint8_t* d = dst + box * kBox + key * 128;
+          const uint4 v = raw[k];
+          *reinterpret_cast<uint4*>(d + (((2 * c) ^ (key & 7)) << 4)) =
+              make_uint4(e4m3x2_to_bf16x2(v.x, 0x1404), e4m3x2_to_bf16x2(v.x, 0x3424), e4m3x2_to_bf16x2(v.y, 0x1404),
+                         e4m3x2_to_bf16x2(v.y, 0x3424));
+          *reinterpret_cast<uint4*>(d + (((2 * c + 1) ^ (key & 7)) << 4)) =
+              make_uint4(e4m3x2_to_bf16x2(v.z, 0x1404), e4m3x2_to_bf16x2(v.z, 0x3424), e4m3x2_to_bf16x2(v.w, 0x1404),
+                         e4m3x2_to_bf16x2(v.w, 0x3424));
+          fetch(r, n, k);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&a->full[st]);
-          mbar_arrive(&a->raw_empty[rs]);
-        }
-        if (++rs == C::RAWS) rs = 0, rph ^= 1;
+        if (lane == 0) mbar_arrive(&a->full[st]);
         if (++st == C::STAGES) st = 0, sph ^= 1;
       }
     }
-  } else if (warp >= 4 && warp < 8) {
-    // ---- senders (but for tile scales, whose partial logits the softmax warps sum first): the partial S of
-    // this CTA's columns into the peer's buffer, a row per thread
-    const int w = warp - 4, row = 32 * w + lane;
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
-    const uint32_t peer_x = dsmem_addr(x_s, rank ^ 1) + row * 16, peer_full = dsmem_addr(&a->x_full[0], rank ^ 1);
-    int tiles = 0;
-    bool ok = !C::TILED;
-    for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
-      for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
-        const int b = tiles & 1;
-        ok = __all_sync(0xffffffffu, wait(a, &a->s_full[b], (tiles >> 1) & 1, err));
-        tc_fence_after();
-        float x[64];
-        tmem_ld_sync(lane_base + kColS + 64 * b, *reinterpret_cast<float (*)[32]>(x));
-        tmem_ld_sync(lane_base + kColS + 64 * b + 32, *reinterpret_cast<float (*)[32]>(x + 32));
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&a->s_empty[b]);
-        ok = ok && __all_sync(0xffffffffu, wait_cluster(a, &a->x_free[b], ((tiles >> 1) & 1) ^ 1, err));
-        if (!ok) break;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) st_async16(peer_x + b * C::X_BYTES + j * kRows * 16, x + 4 * j, peer_full + 8 * b);
-      }
-    }
-  } else if (warp >= 8 && warp < 16) {
-    // ---- softmax, query load, rescale, epilogue.  Thread = row (tensor-memory lane) and half h of the tile's
-    // positions (32), of the query's columns and of the value columns
-    const int w = warp - 8, h = w >> 2, row = 32 * (w & 3) + lane, st = tid - 256;
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * (w & 3)) << 16);
-    const uint32_t peer_x = dsmem_addr(x_s, rank ^ 1) + (h * 8 * kRows + row) * 16;
-    const uint32_t peer_full = dsmem_addr(&a->x_full[0], rank ^ 1);
-    const float4* my_x = reinterpret_cast<const float4*>(x_s) + h * 8 * kRows + row;
+  } else if (warp >= 4) {
+    // ---- row warps.  Thread = row (tensor-memory lane) and half h of the tile's positions (32), of the query's
+    // columns and of the value columns.  Rows 64 rank ... are ours (softmax), the others the peer's.
+    const int w = warp - 4, h = w >> 2, quarter = w & 3, row = 32 * quarter + lane, r64 = row & 63;
+    const bool own = (quarter >> 1) == rank;
+    const int bar_id = 1 + (quarter & 1);
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
+    const uint32_t peer_x = dsmem_addr(x_s, rank ^ 1) + (h * 8 * 64 + r64) * 16;
+    const uint32_t peer_xf = dsmem_addr(&a->x_full[0], rank ^ 1), peer_msg = dsmem_addr(&a->p_msg[0], rank ^ 1);
+    const uint32_t peer_p = dsmem_addr(p_s, rank ^ 1) + row * 128, peer_fac = dsmem_addr(&a->fac[0][r64], rank ^ 1);
+    const uint32_t peer_clear = dsmem_addr(&a->clear[0][2 * (quarter & 1) + h], rank ^ 1);
+    const float4* my_x = reinterpret_cast<const float4*>(x_s) + h * 8 * 64 + r64;
     int tile = 0, items = 0;
     uint32_t su = 0;
     bool ok = true;
     const int rows = p.q_per_seq * p.H;
+
+    // This CTA's partial logits of tile n (its columns; with tile scales, scaled), 32 positions of this row.
+    auto partial = [&](int n, float (&x)[32]) {
+      if constexpr (C::TILED) {
+        const float* sc = sc_s + (n % C::SC_DEPTH) * kKeys * 5 + 32 * h * 5;
+        ok = wait(a, &a->sc_full[n % C::SC_DEPTH], (n / C::SC_DEPTH) & 1, err) && ok;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = 0.f;
+#pragma unroll 1
+        for (int g = 0; g < 3; ++g, ++su) {
+          ok = wait(a, &a->s_full[su & 1], (su >> 1) & 1, err) && ok;
+          tc_fence_after();
+          float s[32];
+          tmem_ld_sync(lane_base + kColS + 64 * (su & 1) + 32 * h, s);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&a->s_empty[su & 1]);
+          const float* f = sc + (g < 2 ? 2 * rank + g : 4);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = fmaf(f[5 * k], s[k], x[k]);
+        }
+      } else {
+        ok = wait(a, &a->s_full[n & 1], (n >> 1) & 1, err) && ok;
+        tc_fence_after();
+        tmem_ld_sync(lane_base + kColS + 64 * (n & 1) + 32 * h, x);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&a->s_empty[n & 1]);
+      }
+    };
+    // O of this row (128 of the columns) times f, once the tile before has been added.
+    auto rescale = [&](int n, float f) {
+      ok = wait(a, &a->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err) && ok;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 16) {
+        float o[16];
+        tmem_ld_sync(lane_base + kColO + 128 * h + c, o);
+        uint32_t v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(o[k] * f);
+        tmem_st16(lane_base + kColO + 128 * h + c, v);
+      }
+      tmem_wait_st();
+    };
+
     for (int i = 0; get_item(p, pl, a, i, it); ++i) {
       const int row_lo = it.rt * kRows;
       const int64_t at = (int64_t)it.seq * rows + row_lo;  // the item's first row in out and lse
       const int nrows = min(kRows, rows - row_lo);
       if (it.t0 >= it.t1) {  // nothing to see: padding nodes, or an empty sequence
         if (rank == 0) {
+          const int st = tid - 128;
           for (int k = st; k < nrows * (kDv / 8); k += 256)
             reinterpret_cast<uint4*>(p.out + at * kDv)[k] = make_uint4(0u, 0u, 0u, 0u);
           if (p.lse && st < nrows) p.lse[at + st] = -INFINITY;
@@ -747,199 +815,212 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         fence_proxy_async_smem();
         mbar_arrive(&a->q_full);
       }
-      const int node = min((row_lo + row) / p.H, p.q_per_seq - 1);
-      float m = -INFINITY, l = 0.f;
-      bool dead = false;  // (the same for all eight warps, unlike ok)
-      for (int t = it.t0; t < it.t1; ++t, ++tile) {
-        const bool tail = (t + 1) * kKeys > it.ctx;
-        const float* sc = sc_s + (tile % C::SC_DEPTH) * kKeys * C::NSC + 32 * h * C::NSC;
-        const int xb = tile & 1;
-        float x[32];
-        // ---- this CTA's partial logits
-        if constexpr (C::FP8) ok = ok && wait(a, &a->sc_full[tile % C::SC_DEPTH], (tile / C::SC_DEPTH) & 1, err);
-        if constexpr (C::TILED) {
+      float l = 0.f;
+      if (own) {
+        // ======== softmax of our rows
+        const int node = min((row_lo + row) / p.H, p.q_per_seq - 1);
+        float m = -INFINITY;
+        for (int t = it.t0; t < it.t1; ++t, ++tile) {
+          const int xb = tile & 1, pb = tile % C::PB;
+          const bool tail = (t + 1) * kKeys > it.ctx;
+          const float* sc = sc_s + (tile % C::SC_DEPTH) * kKeys * C::NSC + 32 * h * C::NSC;
+          float x[32];
+          partial(tile, x);
+          ok = wait_cluster(a, &a->x_full[xb], (tile >> 1) & 1, err) && ok;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = 0.f;
-#pragma unroll 1
-          for (int g = 0; g < 3; ++g, ++su) {
-            ok = ok && wait(a, &a->s_full[su & 1], (su >> 1) & 1, err);
-            tc_fence_after();
-            float s[32];
-            tmem_ld_sync(lane_base + kColS + 64 * (su & 1) + 32 * h, s);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&a->s_empty[su & 1]);
-            const float* f = sc + (g < 2 ? 2 * rank + g : 4);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = fmaf(f[5 * k], s[k], x[k]);
+          for (int j = 0; j < 8; ++j) {
+            const float4 v = my_x[xb * (C::X_BYTES / 16) + j * 64];
+            x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
           }
-        } else {
-          ok = ok && wait(a, &a->s_full[xb], (tile >> 1) & 1, err);
-          tc_fence_after();
-          tmem_ld_sync(lane_base + kColS + 64 * xb + 32 * h, x);
-          tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&a->s_empty[xb]);
-        }
-        // ---- the peer's part
-        if constexpr (C::TILED) {
-          ok = ok && wait_cluster(a, &a->x_free[xb], ((tile >> 1) & 1) ^ 1, err);
-          if (ok) {
+          if (lane == 0) mbar_arrive(&a->x_read[xb]);
+          // ---- scale, mask
+          if constexpr (FMT == kFp8Row) {
+            ok = wait(a, &a->sc_full[tile % C::SC_DEPTH], (tile / C::SC_DEPTH) & 1, err) && ok;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) st_async16(peer_x + xb * C::X_BYTES + j * kRows * 16, x + 4 * j, peer_full + 8 * xb);
+            for (int k = 0; k < 32; k += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(sc + k);
+              x[k] *= f.x * p.scale_log2, x[k + 1] *= f.y * p.scale_log2;
+              x[k + 2] *= f.z * p.scale_log2, x[k + 3] *= f.w * p.scale_log2;
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] *= p.scale_log2;
           }
-        }
-        ok = ok && wait_cluster(a, &a->x_full[xb], (tile >> 1) & 1, err);
+          const bool bad = p.pages.table && a->tile_bad[tile & 3];
+          uint32_t clear = 0;
+          if (tail || bad) {
+            const uint32_t see = bad ? 0u : (uint32_t)(seen_bits(p, it, node, t) >> (32 * h));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float4 v = my_x[xb * (C::X_BYTES / 16) + j * kRows];
-          x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&a->x_read[xb]);
-        // ---- scale, mask
-        if constexpr (FMT == kFp8Row) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(sc + k);
-            x[k] *= f.x * p.scale_log2, x[k + 1] *= f.y * p.scale_log2;
-            x[k + 2] *= f.z * p.scale_log2, x[k + 3] *= f.w * p.scale_log2;
+            for (int k = 0; k < 32; ++k) {
+              if (!((see >> k) & 1)) {
+                // a hidden position that may hold infinities or NaN (its logit is not finite, or it lies past
+                // the end): its values are cleared in the tile, so that 0 * value is 0
+                if (!C::FP8 && (!(fabsf(x[k]) < INFINITY) || t * kKeys + 32 * h + k >= it.len)) clear |= 1u << k;
+                x[k] = -INFINITY;
+              }
+            }
+            clear = __reduce_or_sync(0xffffffffu, clear);
           }
-        } else {
+          // ---- the reference maximum moves when a position exceeds it by more than kLazy
+          float mx = x[0];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] *= p.scale_log2;
-        }
-        const bool bad = p.pages.table && a->tile_bad[tile & 3];
-        if (tail || bad) {
-          bool hidden_bad = false;
-          const uint32_t see = bad ? 0u : (uint32_t)(seen_bits(p, it, node, t) >> (32 * h));
+          for (int k = 1; k < 32; ++k) mx = fmaxf(mx, x[k]);
+          a->red[h][r64] = mx;
+          float f = 1.f;
+          if (pair_any(bar_id, mx > m + kLazy)) {
+            mx = fmaxf(a->red[0][r64], a->red[1][r64]);
+            if (mx > m + kLazy) {  // (m = -inf: nothing summed yet, the factor is 0)
+              f = ex2(m - mx);
+              m = mx;
+              l *= f;
+            }
+            if (t > it.t0) rescale(tile, f);
+            pair_bar(bar_id);  // red is read before the next tile's maxima are written
+          }
+          // ---- weights
+          const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            if (!((see >> k) & 1)) {
-              // a hidden position that may hold infinities or NaN (its logit is not finite, or it lies past
-              // the end): its values are cleared below, so that 0 * value is 0
-              if (!C::FP8 && (!(fabsf(x[k]) < INFINITY) || t * kKeys + 32 * h + k >= it.len)) {
-                a->kbad[32 * h + k] = 1;
-                hidden_bad = true;
-              }
-              x[k] = -INFINITY;
-            }
+            x[k] = ex2(x[k] - mu);
+            l += x[k];
           }
-          if (!C::FP8 && softmax_any(hidden_bad)) {
-            // zero the cleared positions' value columns in the tile (its first product is done): a position
-            // past the end always, another one only if it holds something that is not finite
-            const int key = st >> 2;
-            if (a->kbad[key]) {
-              uint8_t* line = tiles_s + (tile % C::STAGES) * kTile + (st & 3) * kBox + key * 128;
-              bool clear = t * kKeys + key >= it.len;
-              if (!clear) {
+          // the tile that used this P buffer has been added, here and at the peer
+          if (tile >= C::PB) ok = wait(a, &a->pv_done[(tile - C::PB) & 1], ((tile - C::PB) >> 1) & 1, err) && ok;
+          ok = wait_cluster(a, &a->p_free[pb], ((tile / C::PB) & 1) ^ 1, err) && ok;
+          const uint32_t msg = peer_msg + 8 * pb;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                  const uint4 u = *reinterpret_cast<const uint4*>(line + 16 * c);
-                  const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
+          for (int pc = 0; pc < C::PC; ++pc) {
+            const int off = (pb * C::PC + pc) * C::P_BYTES;
 #pragma unroll
-                  for (int q = 0; q < 4; ++q)
-                    clear |= (ws[q] & 0x7F80u) == 0x7F80u || (ws[q] & 0x7F800000u) == 0x7F800000u;
+            for (int j = 0; j < 4; ++j) {  // 16-byte chunks of eight positions
+              uint32_t v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int e = 8 * j + 2 * k;
+                float y0 = x[e], y1 = x[e + 1];
+                if constexpr (C::FP8) {
+                  // the weight carries the position's scale (of the values' tile, here of this CTA's columns: the
+                  // peer's copy is made below); a hidden position's weight is 0 whatever its scale holds
+                  const float f0 = sc[e * C::NSC + (C::TILED ? 2 * rank + pc : 0)];
+                  const float f1 = sc[(e + 1) * C::NSC + (C::TILED ? 2 * rank + pc : 0)];
+                  y0 = y0 == 0.f ? 0.f : y0 * f0;
+                  y1 = y1 == 0.f ? 0.f : y1 * f1;
+                }
+                v[k] = pack_bf16(y0, y1);
+              }
+              const int sw = ((4 * h + j) ^ (row & 7)) << 4;
+              *reinterpret_cast<uint4*>(p_s + off + row * 128 + sw) = make_uint4(v[0], v[1], v[2], v[3]);
+              if constexpr (C::TILED) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int e = 8 * j + 2 * k;
+                  const float f0 = sc[e * 5 + 2 * (rank ^ 1) + pc], f1 = sc[(e + 1) * 5 + 2 * (rank ^ 1) + pc];
+                  v[k] = pack_bf16(x[e] == 0.f ? 0.f : x[e] * f0, x[e + 1] == 0.f ? 0.f : x[e + 1] * f1);
                 }
               }
-              if (clear) {
+              if (ok) st_async16(peer_p + off + sw, reinterpret_cast<const float*>(v), msg);
+            }
+          }
+          if (ok) {
+            if (h == 0) st_async4(peer_fac + 256 * pb, __float_as_uint(f), msg);
+            if (lane == 0) st_async4(peer_clear + 16 * pb, clear, msg);
+          }
+          if (!C::FP8 && tail) {
+            if (lane == 0) a->clear_own[tile & 1][2 * (quarter & 1) + h] = clear;
+            row_bar();  // the other four warps clear the tile
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (C::FP8) mbar_arrive(&a->sc_empty[tile % C::SC_DEPTH]);
+            mbar_arrive(&a->p_full[tile & 1]);
+          }
+        }
+        // ---- the item's sums, to the peer as well
+        pair_bar(bar_id);
+        a->red[h][r64] = l;
+        pair_bar(bar_id);
+        l = a->red[0][r64] + a->red[1][r64];
+        pair_bar(bar_id);
+        if (h == 0) {
+          if (ok) st_async4(dsmem_addr(&a->stat[r64], rank ^ 1), __float_as_uint(l), dsmem_addr(&a->stat_full, rank ^ 1));
+          const bool live = row < nrows && (row_lo + row) / p.H < it.fresh;
+          if (it.slot >= 0) pl.part_ml[(int64_t)it.slot * kRows + row] = make_float2(m, l);
+          else if (p.lse && row < nrows) p.lse[at + row] = !live || l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+      } else {
+        // ======== the peer's rows: send it our partial logits a tile ahead, take in its P
+        auto send = [&](int n) {
+          float x[32];
+          partial(n, x);
+          if constexpr (C::TILED) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&a->sc_empty[n % C::SC_DEPTH]);
+          }
+          ok = wait_cluster(a, &a->x_free[n & 1], ((n >> 1) & 1) ^ 1, err) && ok;
+          if (ok) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(line + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+            for (int j = 0; j < 8; ++j)
+              st_async16(peer_x + (n & 1) * C::X_BYTES + j * 64 * 16, x + 4 * j, peer_xf + 8 * (n & 1));
+          }
+        };
+        send(tile);
+        for (int t = it.t0; t < it.t1; ++t, ++tile) {
+          const int pb = tile % C::PB;
+          if (t + 1 < it.t1) send(tile + 1);
+          ok = wait_cluster(a, &a->p_msg[pb], (tile / C::PB) & 1, err) && ok;
+          const float f = a->fac[pb][r64];
+          uint32_t clear[2] = {a->clear[pb][0] | a->clear[pb][2], a->clear[pb][1] | a->clear[pb][3]};
+          if (t > it.t0 && __any_sync(0xffffffffu, f != 1.f)) rescale(tile, f);
+          if (!C::FP8 && (t + 1) * kKeys > it.ctx) {
+            row_bar();
+            // zero the value columns of the positions to clear (the tile's first product is done): a position
+            // past the end always, another one only if it holds something that is not finite
+            const uint32_t* mine = a->clear_own[tile & 1];
+            clear[0] |= mine[0] | mine[2];
+            clear[1] |= mine[1] | mine[3];
+            const int st = (h * 2 + (quarter & 1)) * 32 + lane, key = st >> 1;  // a position, two of its four boxes
+            if ((clear[key >> 5] >> (key & 31)) & 1) {
+              for (int b = 2 * (st & 1); b < 2 * (st & 1) + 2; ++b) {
+                uint8_t* line = tiles_s + (tile % C::STAGES) * kTile + b * kBox + key * 128;
+                bool zero = t * kKeys + key >= it.len;
+                if (!zero) {
+#pragma unroll
+                  for (int c = 0; c < 8; ++c) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(line + 16 * c);
+                    const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                      zero |= (ws[q] & 0x7F80u) == 0x7F80u || (ws[q] & 0x7F800000u) == 0x7F800000u;
+                  }
+                }
+                if (zero) {
+#pragma unroll
+                  for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(line + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+                }
               }
             }
-            fence_proxy_async_smem();
-            softmax_bar();
-            if (st < kKeys) a->kbad[st] = 0;
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (warp == (rank ? 4 : 6)) mbar_arrive_expect_tx(&a->p_msg[pb], C::MSG_BYTES);  // for this buffer's next use
+            mbar_arrive(&a->p_full[tile & 1]);
           }
         }
-        // ---- the reference maximum moves when a position exceeds it by more than kLazy
-        float mx = x[0];
-#pragma unroll
-        for (int k = 1; k < 32; ++k) mx = fmaxf(mx, x[k]);
-        a->red[h][row] = mx;
-        const bool any = softmax_any(mx > m + kLazy || !ok);
-        if (any) {
-          if (softmax_any(!ok)) {
-            dead = true;
-            break;
-          }
-          mx = fmaxf(a->red[0][row], a->red[1][row]);
-          float f = 1.f;
-          if (mx > m + kLazy) {  // (m = -inf: nothing summed yet, the factor is 0)
-            f = ex2(m - mx);
-            m = mx;
-            l *= f;
-          }
-          if (t > it.t0) {
-            // the second product of the tile before is done: O may be rescaled
-            ok = ok && wait(a, &a->pv_done, (tile & 1) ^ 1, err);
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 16) {
-              float o[16];
-              tmem_ld_sync(lane_base + kColO + 128 * h + c, o);
-              uint32_t v[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(o[k] * f);
-              tmem_st16(lane_base + kColO + 128 * h + c, v);
-            }
-          }
-          softmax_bar();  // red is read before the next tile's maxima are written
-        }
-        // ---- weights
-        const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          x[k] = ex2(x[k] - mu);
-          l += x[k];
-        }
-        ok = ok && wait(a, &a->pv_done, (tile & 1) ^ 1, err);  // the tile before has read its P
-        tc_fence_after();
-#pragma unroll
-        for (int pc = 0; pc < C::PC; ++pc) {
-          uint8_t* d = p_s + pc * C::P_BYTES + row * 128;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {  // 16-byte chunks of eight positions
-            uint32_t v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int e = 8 * j + 2 * k;
-              float y0 = x[e], y1 = x[e + 1];
-              if constexpr (C::FP8) {
-                // a hidden position's weight is 0 whatever its scale holds
-                const float f0 = sc[e * C::NSC + (C::TILED ? 2 * rank + pc : 0)];
-                const float f1 = sc[(e + 1) * C::NSC + (C::TILED ? 2 * rank + pc : 0)];
-                y0 = y0 == 0.f ? 0.f : y0 * f0;
-                y1 = y1 == 0.f ? 0.f : y1 * f1;
-              }
-              v[k] = pack_bf16(y0, y1);
-            }
-            *reinterpret_cast<uint4*>(d + (((4 * h + j) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-          }
-        }
-        fence_proxy_async_smem();
-        tmem_wait_st();  // (a rescale's stores)
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (C::FP8) mbar_arrive(&a->sc_empty[tile % C::SC_DEPTH]);
-          mbar_arrive(&a->p_full);
-        }
+        ok = wait_cluster(a, &a->stat_full, items & 1, err) && ok;
+        l = a->stat[r64];
+        row_bar();
       }
-      if (dead) break;
-      // ---- the item's sums, then its outputs
-      softmax_bar();
-      a->red[h][row] = l;
-      softmax_bar();
-      l = a->red[0][row] + a->red[1][row];
+      // ---- the item's outputs
+      if (own) row_bar();
+      if (!own && lane == 0 && warp == (rank ? 4 : 6)) mbar_arrive_expect_tx(&a->stat_full, 64 * 4);
       const bool live = row < nrows && (row_lo + row) / p.H < it.fresh;
       const float inv = live && l != 0.f ? 1.f / l : 0.f;
-      if (rank == 0 && h == 0) {
-        if (it.slot >= 0) pl.part_ml[(int64_t)it.slot * kRows + row] = make_float2(m, l);
-        else if (p.lse && row < nrows) p.lse[at + row] = !live || l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-      }
-      ok = ok && wait(a, &a->o_done, items & 1, err);
-      if (softmax_any(!ok)) break;
+      ok = wait(a, &a->o_done, items & 1, err) && ok;
       tc_fence_after();
       const int v0 = 256 * rank + 128 * h;
 #pragma unroll 1
@@ -1058,14 +1139,11 @@ cudaError_t launch_fmt(const TreeAttnParams& p, TreePlan pl, void* ws, cudaStrea
   const cuuint64_t dims[3] = {(cuuint64_t)kDqk, n, paged ? 1 : (cuuint64_t)p.n_seq};
   const cuuint64_t strides[2] = {(cuuint64_t)p.kv_row_stride,
                                  paged || p.n_seq == 1 ? n * (cuuint64_t)p.kv_row_stride : (cuuint64_t)p.kv_seq_stride};
-  CUtensorMap tm, tm_rope;
-  const cuuint32_t box[3] = {C::FP8 ? 256u : 64u, (cuuint32_t)kKeys, 1}, rope_box[3] = {32, (cuuint32_t)kKeys, 1};
-  const auto type = C::FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const auto swizzle = C::FP8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
-  void* kv = const_cast<uint8_t*>(p.kv);
-  if (encode_tensor_map(&tm, type, 3, kv, dims, strides, box, swizzle) != CUDA_SUCCESS) return cudaErrorInvalidValue;
-  tm_rope = tm;
-  if (C::FP8 && encode_tensor_map(&tm_rope, type, 3, kv, dims, strides, rope_box, swizzle) != CUDA_SUCCESS)
+  CUtensorMap tm;
+  memset(&tm, 0, sizeof(tm));
+  const cuuint32_t box[3] = {64, (cuuint32_t)kKeys, 1};
+  if (!C::FP8 && encode_tensor_map(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint8_t*>(p.kv), dims, strides, box,
+                                   CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   if (pl.cap) {
     uint8_t* w = reinterpret_cast<uint8_t*>(ws);
@@ -1079,7 +1157,7 @@ cudaError_t launch_fmt(const TreeAttnParams& p, TreePlan pl, void* ws, cudaStrea
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem_once(&allowed, reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(kern, dim3(2 * pl.grid), dim3(C::THREADS), C::SMEM, stream, false, tm, tm_rope, p, pl);
+  e = launch_kernel(kern, dim3(2 * pl.grid), dim3(C::THREADS), C::SMEM, stream, false, tm, p, pl);
   if (e != cudaSuccess || !pl.cap) return e;
   return launch_kernel(tree_combine_kernel, dim3((p.q_per_seq * p.H + 7) / 8, p.n_seq, 4), dim3(256), 0, stream, true, p, pl);
 }
