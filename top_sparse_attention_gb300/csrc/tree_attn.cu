@@ -10,7 +10,7 @@
 //   * partial S[128 x 64] = Q_c K_c^T: A = the rows in tensor memory (M = 128, 256 columns of q; the rotary
 //     half from shared memory), B = the tile (K-major), 18 steps of K = 16;
 //   * each CTA takes the softmax of 64 of the rows: the other sends it its partial S of those rows through
-//     distributed shared memory (st.async, counted on the receiver's mbarrier), and gets their P (bf16)
+//     distributed shared memory (bulk copies, counted on the receiver's mbarrier), and gets their P (bf16)
 //     back, so both hold P for all rows: 24 KB per tile each way;
 //   * one pass over the positions keeps a reference maximum m and a sum l per row,
 //       l' = l 2^(m - m') + sum_p 2^(x_p - m'),   o' = o 2^(m - m') + sum_p 2^(x_p - m') v_p,
@@ -62,7 +62,7 @@ struct Cfg {
   static constexpr int NSC = FMT == kFp8Tile ? 5 : FMT == kFp8Row ? 1 : 0;
   static constexpr bool TILED = FMT == kFp8Tile;
   static constexpr int THREADS = FP8 ? 512 : 384;
-  static constexpr int STAGES = 3;                        // tiles in shared memory
+  static constexpr int STAGES = TILED ? 2 : 3;            // tiles in shared memory
   static constexpr int PC = TILED ? 2 : 1;                // copies of P (one per 128 values)
   static constexpr int PB = TILED ? 1 : 2;                // P buffers
   static constexpr int SC_DEPTH = 2;
@@ -72,11 +72,15 @@ struct Cfg {
   static constexpr int P_BYTES = kRows * 128;             // P: 128 rows x 64 positions
   // what a CTA sends of a tile: its rows of P, their rescale factors, the positions to clear
   static constexpr int MSG_BYTES = PC * P_BYTES / 2 + 64 * 4 + 4 * 4;
+  static constexpr int OUT_BYTES = X_BYTES;               // our partial S of the peer's rows, on its way there
+  static constexpr int PP_BYTES = TILED ? PC * P_BYTES / 2 : 0;  // with tile scales: the peer's copies of our P
   static constexpr int AUX = 2560;
   static constexpr int OFF_X = STAGES * kTile;
   static constexpr int OFF_QR = OFF_X + 2 * X_BYTES;
   static constexpr int OFF_P = OFF_QR + QR_BYTES;
-  static constexpr int OFF_SC = OFF_P + PB * PC * P_BYTES;
+  static constexpr int OFF_OUT = OFF_P + PB * PC * P_BYTES;
+  static constexpr int OFF_PP = OFF_OUT + OUT_BYTES;
+  static constexpr int OFF_SC = OFF_PP + PP_BYTES;
   static constexpr int OFF_AUX = OFF_SC + SC_DEPTH * SC_BYTES;
   static constexpr int SMEM = OFF_AUX + AUX + 1024;
   static_assert(SMEM <= kSmemMax, "shared memory");
@@ -118,7 +122,8 @@ struct Aux {
   int n_items;
   int tile_bad[4];
   int items[kItemsPerCta][8];
-  float fac[2][64];        // the peer's rescale factors of its rows
+  alignas(16) float fac[2][64];  // the peer's rescale factors of its rows
+  alignas(16) float fac_own[2][64];  // ours, on their way there
   uint32_t clear[2][4];    // positions to clear, from the peer (quarter, half)
   uint32_t clear_own[2][4];
   float red[2][64];        // per half of our rows: maxima, then sums
@@ -185,13 +190,16 @@ __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// 16 bytes into the other CTA's shared memory, counted on its mbarrier.
-__device__ __forceinline__ void st_async16(uint32_t addr, const float* v, uint32_t bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
-               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
-               "r"(bar)
+// `bytes` of this CTA's shared memory into the other CTA's, counted on its mbarrier.  (Stores of 16 bytes per
+// lane, each counted by itself, took 1300 to 1900 cycles for a tile's 16 KB to arrive.)
+__device__ __forceinline__ void copy_remote(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(smem_u32(src)), "r"(bytes), "r"(bar)
                : "memory");
 }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All of this thread's copies have read their source.
+__device__ __forceinline__ void copy_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 __device__ __forceinline__ void st_async4(uint32_t addr, uint32_t v, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
@@ -433,6 +441,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
   uint8_t* x_s = smem + C::OFF_X;
   uint8_t* qr_s = smem + C::OFF_QR;
   uint8_t* p_s = smem + C::OFF_P;
+  uint8_t* out_s = smem + C::OFF_OUT;
+  uint8_t* pp_s = smem + C::OFF_PP;
   float* sc_s = reinterpret_cast<float*>(smem + C::OFF_SC);
   Aux* a = reinterpret_cast<Aux*>(smem + C::OFF_AUX);
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
@@ -686,10 +696,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
     };
     for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
       const uint8_t* r = tile_rows(it, it.t0);
+      const uint8_t* r1 = tile_rows(it, it.t0 + 1);  // the block table is read two tiles ahead, the codes one
 #pragma unroll
       for (int k = 0; k < 9; ++k) fetch(r, it.len - it.t0 * kKeys, k);
       for (int t = it.t0; ok && t < it.t1; ++t) {
-        r = tile_rows(it, t + 1);
+        r = r1;
+        r1 = tile_rows(it, t + 2);
         const int n = it.len - (t + 1) * kKeys;
         ok = __all_sync(0xffffffffu, wait(a, &a->empty[st], sph ^ 1, err));
         if (!ok) break;
@@ -721,11 +733,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
     const bool own = (quarter >> 1) == rank;
     const int bar_id = 1 + (quarter & 1);
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
-    const uint32_t peer_x = dsmem_addr(x_s, rank ^ 1) + (h * 8 * 64 + r64) * 16;
+    const int unit = 2 * (quarter & 1) + h;  // of the exchanged logits: 32 rows x 32 positions, [8 chunks][32 rows] x 16 B
+    const uint32_t peer_x = dsmem_addr(x_s, rank ^ 1) + unit * 4096;
     const uint32_t peer_xf = dsmem_addr(&a->x_full[0], rank ^ 1), peer_msg = dsmem_addr(&a->p_msg[0], rank ^ 1);
-    const uint32_t peer_p = dsmem_addr(p_s, rank ^ 1) + row * 128, peer_fac = dsmem_addr(&a->fac[0][r64], rank ^ 1);
-    const uint32_t peer_clear = dsmem_addr(&a->clear[0][2 * (quarter & 1) + h], rank ^ 1);
-    const float4* my_x = reinterpret_cast<const float4*>(x_s) + h * 8 * 64 + r64;
+    const uint32_t peer_p = dsmem_addr(p_s, rank ^ 1) + 32 * quarter * 128;
+    const uint32_t peer_fac = dsmem_addr(&a->fac[0][32 * (quarter & 1)], rank ^ 1);
+    const uint32_t peer_clear = dsmem_addr(&a->clear[0][unit], rank ^ 1);
+    const float4* my_x = reinterpret_cast<const float4*>(x_s) + unit * 256 + lane;
     int tile = 0, items = 0;
     uint32_t su = 0;
     bool ok = true;
@@ -829,7 +843,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
           ok = wait_cluster(a, &a->x_full[xb], (tile >> 1) & 1, err) && ok;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float4 v = my_x[xb * (C::X_BYTES / 16) + j * 64];
+            const float4 v = my_x[xb * (C::X_BYTES / 16) + j * 32];
             x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
           }
           __syncwarp();
@@ -888,6 +902,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
           // the tile that used this P buffer has been added, here and at the peer
           if (tile >= C::PB) ok = wait(a, &a->pv_done[(tile - C::PB) & 1], ((tile - C::PB) >> 1) & 1, err) && ok;
           ok = wait_cluster(a, &a->p_free[pb], ((tile / C::PB) & 1) ^ 1, err) && ok;
+          if (C::TILED) {
+            if (h == 0 && lane == 0) copy_wait_read();  // the staged copies of the tile before have left
+            pair_bar(bar_id);
+          }
           const uint32_t msg = peer_msg + 8 * pb;
 #pragma unroll
           for (int pc = 0; pc < C::PC; ++pc) {
@@ -911,26 +929,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
               }
               const int sw = ((4 * h + j) ^ (row & 7)) << 4;
               *reinterpret_cast<uint4*>(p_s + off + row * 128 + sw) = make_uint4(v[0], v[1], v[2], v[3]);
-              if constexpr (C::TILED) {
+              if constexpr (C::TILED) {  // the peer's copy carries the scales of its value tiles
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   const int e = 8 * j + 2 * k;
                   const float f0 = sc[e * 5 + 2 * (rank ^ 1) + pc], f1 = sc[(e + 1) * 5 + 2 * (rank ^ 1) + pc];
                   v[k] = pack_bf16(x[e] == 0.f ? 0.f : x[e] * f0, x[e + 1] == 0.f ? 0.f : x[e + 1] * f1);
                 }
+                *reinterpret_cast<uint4*>(pp_s + pc * (C::P_BYTES / 2) + r64 * 128 + sw) = make_uint4(v[0], v[1], v[2], v[3]);
               }
-              if (ok) st_async16(peer_p + off + sw, reinterpret_cast<const float*>(v), msg);
             }
           }
-          if (ok) {
-            if (h == 0) st_async4(peer_fac + 256 * pb, __float_as_uint(f), msg);
-            if (lane == 0) st_async4(peer_clear + 16 * pb, clear, msg);
+          if (h == 0) a->fac_own[pb][r64] = f;
+          fence_proxy_async_smem();
+          pair_bar(bar_id);  // both halves of the 32 rows are written
+          if (ok && lane == 0) {
+            if (h == 0) {
+#pragma unroll
+              for (int pc = 0; pc < C::PC; ++pc)
+                copy_remote(peer_p + (pb * C::PC + pc) * C::P_BYTES,
+                            C::TILED ? pp_s + pc * (C::P_BYTES / 2) + 32 * (quarter & 1) * 128
+                                     : p_s + (pb * C::PC + pc) * C::P_BYTES + 32 * quarter * 128,
+                            4096, msg);
+              copy_remote(peer_fac + 256 * pb, &a->fac_own[pb][32 * (quarter & 1)], 128, msg);
+              copy_commit();
+            }
+            st_async4(peer_clear + 16 * pb, clear, msg);
           }
           if (!C::FP8 && tail) {
             if (lane == 0) a->clear_own[tile & 1][2 * (quarter & 1) + h] = clear;
             row_bar();  // the other four warps clear the tile
           }
-          fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -960,10 +989,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
             if (lane == 0) mbar_arrive(&a->sc_empty[n % C::SC_DEPTH]);
           }
           ok = wait_cluster(a, &a->x_free[n & 1], ((n >> 1) & 1) ^ 1, err) && ok;
-          if (ok) {
+          if (lane == 0) copy_wait_read();  // the tile before has left
+          __syncwarp();
+          float4* o = reinterpret_cast<float4*>(out_s + unit * 4096) + lane;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              st_async16(peer_x + (n & 1) * C::X_BYTES + j * 64 * 16, x + 4 * j, peer_xf + 8 * (n & 1));
+          for (int j = 0; j < 8; ++j) o[32 * j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (ok && lane == 0) {
+            copy_remote(peer_x + (n & 1) * C::X_BYTES, out_s + unit * 4096, 4096, peer_xf + 8 * (n & 1));
+            copy_commit();
           }
         };
         send(tile);
@@ -1050,6 +1085,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
       ++items;
     }
   }
+  copy_wait_read();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no CTA leaves while the other may still write into its shared memory
