@@ -4,32 +4,33 @@
 //   logit[p] = sm_scale * q[i, h] . Kv[p],  out[i, h] = sum_p softmax(logit)[p] * Kv[p, :512].
 //
 // A "row" is one head of one node; the rows of a sequence are consecutive in q and share its cache.
-// A cluster of two CTAs takes 128 rows and walks tiles of 64 positions.  The cache row's columns are
-// split between the two: CTA c holds value columns 256 c ... 256 c + 255 and half of the 64 rotary
-// columns, so every byte of the cache enters one SM's shared memory once and serves both products:
-//   * partial S[128 x 64] = Q_c K_c^T: A = the rows in tensor memory (M = 128, 256 columns of q; the rotary
-//     half from shared memory), B = the tile (K-major), 18 steps of K = 16;
-//   * each CTA takes the softmax of 64 of the rows: the other sends it its partial S of those rows through
-//     distributed shared memory (bulk copies, counted on the receiver's mbarrier), and gets their P (bf16)
-//     back, so both hold P for all rows: 24 KB per tile each way;
+// A cluster of two CTAs takes 128 rows and walks tiles of 64 positions.  CTA c takes the first product
+// and the softmax of 32 of the positions, and the second product of half of the value columns:
+//   * S[128 x 32] = Q K_c^T: A = the rows (M = 128; 384 of their columns in tensor memory, 192 in shared
+//     memory), B = its 32 positions (K-major), 36 steps of K = 16;
 //   * one pass over the positions keeps a reference maximum m and a sum l per row,
 //       l' = l 2^(m - m') + sum_p 2^(x_p - m'),   o' = o 2^(m - m') + sum_p 2^(x_p - m') v_p,
 //     where m is moved only when a tile's maximum exceeds it by more than 2^8 (weights stay below 2^8,
-//     fp32 sums and bf16 weights lose nothing by it), so o in tensor memory is rescaled rarely;
-//   * O_c[128 x 256] += P V_c: A = P (bf16) in shared memory; B = the same tile read MN-major (values along
-//     N), 4 steps of K = 16 with N = 256.
+//     fp32 sums and bf16 weights lose nothing by it), so o in tensor memory is rescaled rarely.  The CTAs send
+//     each other their rows' maxima over their positions a tile ahead, so both move m alike;
+//   * each sends the other its P[128 x 32] (bf16): 8 KB per tile through distributed shared memory;
+//   * O_c[128 x 256] += P V_c: A = P in shared memory, B = 256 value columns of all 64 positions, read MN-major
+//     (values along N), 4 steps of K = 16 with N = 256.  A CTA's own positions are in shared memory whole, of
+//     the other's only these 256 columns are loaded besides: 832 of 1152 bytes per position and CTA.
 // Why two CTAs: o for 128 rows x 512 values fills a tensor memory (512 columns), which leaves no room for S;
-// with half of the values it takes 256 columns, q 128, two S buffers 128.  One CTA with 64 rows, q in shared
-// memory and o transposed read 245 KB of shared memory per tile for the MMAs (2000 cycles at 128 B per
-// cycle) and loaded each tile twice as often: 149 us instead of the time below for 8 x 8 nodes at 32K.
+// with half of the values it takes 256 columns, q 192, two S buffers 64.  Measured against it (8 x 64 nodes
+// at 32K, E4M3 rows; 8 x 8 nodes at 32K, bf16): one CTA with 64 rows, q in shared memory and o
+// transposed, 1805 and 149 us (245 KB of shared memory read per tile by the MMAs, room for two tiles);
+// columns of the rows split between the CTAs, whose partial S then travel, 1090 and 120 us (16 to 32 KB
+// per tile at about 20 bytes per cycle between two SMs).
 //
 // Weights are rounded to bf16 for the second product (as the bf16 cache is); sums, maxima, logits and
 // outputs are fp32.  E4M3 rows are widened to bf16 exactly, and their scales are applied in fp32 to the
-// logit and to the weight (128-column scales: one S accumulator per scale tile, one P per value tile).
+// logit and to the weight (128-column scales: one S accumulation per scale tile, one P per value tile).
 //
-// Warp roles: producer (TMA), MMA issuer, scale loader, credits of the exchange, eight row warps (four take
-// the softmax of this CTA's rows, four send the other's partial logits and take in its P; all of them
-// the query load, the rescale and the epilogue), for E4M3 four warps that load, widen and store the tile.
+// Warp roles: producer (TMA), MMA issuer, scale loader, credits of the exchange, four softmax warps (a row per
+// thread; also the query load, the rescale and the epilogue), for E4M3 eight warps that load, widen and
+// store the tile.
 //
 // Work split: items (sequence, chunk of its tiles, row tile), in this order, so that clusters that run
 // together read the same positions and the cache comes from HBM once.  The lengths are on the device:
@@ -45,14 +46,16 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kDqk = 576, kDv = 512;
 constexpr int kRows = 128;                // query rows per cluster
-constexpr int kKeys = 64;                 // positions per tile
-constexpr int kBox = kKeys * 128;         // one 64-column box of a tile: 64 rows x 128 bytes
-constexpr int kTile = 5 * kBox;           // four value boxes and the rotary one
+constexpr int kKeys = 64;                 // positions per tile, half of them per CTA
+constexpr int kBox = 32 * 128;            // 64 columns of 32 positions: 32 rows x 128 bytes
+constexpr int kSlotV = 8 * kBox;          // this CTA's value columns: its positions (4 boxes), the other's (4)
+constexpr int kSlotK = 5 * kBox;          // the other columns of its positions: 4 boxes of values, the rotary one
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLazy = 8.f;              // log2 growth of a row's maximum that is left unscaled
 constexpr int kItemsPerCta = 3;           // split launches are cut into at most this many items per cluster
-// tensor-memory columns: O, the value columns of q, two S buffers
-constexpr int kColO = 0, kColQ = 256, kColS = 384;
+// tensor-memory columns: O, six of the nine 64-column boxes of q, two S buffers
+constexpr int kColO = 0, kColQ = 256, kColS = 448;
+constexpr int kBoxesT = 6;                // q's boxes in tensor memory (the others are in shared memory)
 
 enum { kBf16 = 0, kFp8Row = 1, kFp8Tile = 2 };
 
@@ -61,25 +64,22 @@ struct Cfg {
   static constexpr bool FP8 = FMT != kBf16;
   static constexpr int NSC = FMT == kFp8Tile ? 5 : FMT == kFp8Row ? 1 : 0;
   static constexpr bool TILED = FMT == kFp8Tile;
-  static constexpr int THREADS = FP8 ? 512 : 384;
-  static constexpr int STAGES = TILED ? 2 : 3;            // tiles in shared memory
+  static constexpr int THREADS = FP8 ? 512 : 256;
+  static constexpr int VS = TILED ? 2 : 3, KS = 2;        // slots of both kinds
+  static constexpr int GROUPS = TILED ? 5 : 1;            // S accumulations per tile
   static constexpr int PC = TILED ? 2 : 1;                // copies of P (one per 128 values)
   static constexpr int PB = TILED ? 1 : 2;                // P buffers
   static constexpr int SC_DEPTH = 2;
-  static constexpr int SC_BYTES = NSC * kKeys * 4;
-  static constexpr int X_BYTES = kRows / 2 * kKeys * 4;   // the peer's partial S of our rows (two buffers)
-  static constexpr int QR_BYTES = kRows * 128;            // q's rotary columns
-  static constexpr int P_BYTES = kRows * 128;             // P: 128 rows x 64 positions
-  // what a CTA sends of a tile: its rows of P, their rescale factors, the positions to clear
-  static constexpr int MSG_BYTES = PC * P_BYTES / 2 + 64 * 4 + 4 * 4;
-  static constexpr int OUT_BYTES = X_BYTES;               // our partial S of the peer's rows, on its way there
-  static constexpr int PP_BYTES = TILED ? PC * P_BYTES / 2 : 0;  // with tile scales: the peer's copies of our P
-  static constexpr int AUX = 2560;
-  static constexpr int OFF_X = STAGES * kTile;
-  static constexpr int OFF_QR = OFF_X + 2 * X_BYTES;
-  static constexpr int OFF_P = OFF_QR + QR_BYTES;
-  static constexpr int OFF_OUT = OFF_P + PB * PC * P_BYTES;
-  static constexpr int OFF_PP = OFF_OUT + OUT_BYTES;
+  static constexpr int SC_BYTES = NSC * 32 * 4;           // scales of this CTA's positions
+  static constexpr int Q_BOX = kRows * 128, Q_BYTES = (9 - kBoxesT) * Q_BOX;
+  static constexpr int P_HALF = kRows * 64;               // 128 rows x 32 positions
+  static constexpr int P_BYTES = 2 * P_HALF;
+  static constexpr int PP_BYTES = TILED ? PC * P_HALF : 0;  // with tile scales: the other's copies of our P, on their way
+  static constexpr int AUX = 4096;
+  static constexpr int OFF_K = VS * kSlotV;
+  static constexpr int OFF_Q = OFF_K + KS * kSlotK;
+  static constexpr int OFF_P = OFF_Q + Q_BYTES;
+  static constexpr int OFF_PP = OFF_P + PB * PC * P_BYTES;
   static constexpr int OFF_SC = OFF_PP + PP_BYTES;
   static constexpr int OFF_AUX = OFF_SC + SC_DEPTH * SC_BYTES;
   static constexpr int SMEM = OFF_AUX + AUX + 1024;
@@ -114,22 +114,20 @@ __device__ __forceinline__ int live_row_tiles(const TreeAttnParams& p, int fresh
 }
 
 struct Aux {
-  uint64_t full[3], empty[3];
-  uint64_t s_full[2], s_empty[2], x_full[2], x_read[2], x_free[2];
-  uint64_t p_full[2], p_msg[2], p_free[2], pv_done[2], stat_full, o_done, o_free, q_full, sc_full[2], sc_empty[2], drain;
+  uint64_t v_full[3], v_empty[3], k_full[2], k_empty[2];
+  uint64_t s_full[2], s_empty[2], m_msg[4], p_full[2], p_msg[2], p_free[2], pv_done[2];
+  uint64_t stat_full, o_done, o_free, q_full, sc_full[2], sc_empty[2], drain;
   uint32_t tmem;
   int abort;
   int n_items;
   int tile_bad[4];
   int items[kItemsPerCta][8];
-  alignas(16) float fac[2][64];  // the peer's rescale factors of its rows
-  alignas(16) float fac_own[2][64];  // ours, on their way there
-  uint32_t clear[2][4];    // positions to clear, from the peer (quarter, half)
-  uint32_t clear_own[2][4];
-  float red[2][64];        // per half of our rows: maxima, then sums
-  float stat[64];          // the peer's sums
+  alignas(16) float mx[4][kRows];  // the other's maxima over its positions, by tile % 4
+  uint32_t clear[4][4];            // positions of the other's to clear (per warp of rows)
+  uint32_t clear_own[4][4];        // and of ours
+  float stat[kRows];               // the other's sums
 };
-static_assert(sizeof(Aux) <= 2560, "Aux");
+static_assert(sizeof(Aux) <= 4096, "Aux");
 
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -190,8 +188,8 @@ __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// `bytes` of this CTA's shared memory into the other CTA's, counted on its mbarrier.  (Stores of 16 bytes per
-// lane, each counted by itself, took 1300 to 1900 cycles for a tile's 16 KB to arrive.)
+// `bytes` of this CTA's shared memory into the other CTA's, counted on its mbarrier (measured one way: 320
+// cycles for 64 bytes, 520 for 4 KB, 1100 for 16 KB).
 __device__ __forceinline__ void copy_remote(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "r"(smem_u32(src)), "r"(bytes), "r"(bar)
@@ -206,21 +204,7 @@ __device__ __forceinline__ void st_async4(uint32_t addr, uint32_t v, uint32_t ba
                : "memory");
 }
 
-// Barriers: of the two warps that share 32 rows (id 1 or 2), of all eight row warps (id 3).
-__device__ __forceinline__ void pair_bar(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool pair_any(int id, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, %2, 64, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)pred), "r"(id)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void row_bar() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // A value that is the same in all lanes, as one the compiler knows to be so (a warp-wide reduction writes
 // a uniform register): the MMA issuer's loop bounds and addresses go through it, because operands in
@@ -241,22 +225,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // Low words of shared-memory descriptors with 128-byte swizzle (the upper word, kDescHi, holds the 1024-byte
 // stride, the version and the swizzle): K-major operands, and MN-major ones whose 64-element atoms are one
-// box apart.  Adding bytes / 16 moves the start address.
+// box apart.  Adding bytes / 16 moves the start address.  P's rows are 64 bytes, with 64-byte swizzle
+// (kDescHi64: 8 rows are 512 bytes; 16-byte chunk c of row r lies at chunk c ^ (r / 2 % 4)).
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescHi64 = (512u >> 4) | (1u << 14) | (4u << 29);
 __device__ __forceinline__ uint32_t kmajor_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
 __device__ __forceinline__ uint32_t mnmajor_lo(uint32_t saddr) {
   return ((saddr & 0x3FFFFu) >> 4) | ((uint32_t)(kBox >> 4) << 16);
 }
 
 // D += A B^T with A in shared memory, or in tensor memory (lane = row, two bf16 per column).
+template <uint32_t A_HI = kDescHi>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-      "mov.b64 da, {%1, %5};\n\t"
+      "mov.b64 da, {%1, %6};\n\t"
       "mov.b64 db, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi)
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi), "r"(A_HI)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
@@ -437,58 +424,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
   using C = Cfg<FMT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* tiles_s = smem;
-  uint8_t* x_s = smem + C::OFF_X;
-  uint8_t* qr_s = smem + C::OFF_QR;
+  uint8_t* v_s = smem;
+  uint8_t* k_s = smem + C::OFF_K;
+  uint8_t* q_s = smem + C::OFF_Q;
   uint8_t* p_s = smem + C::OFF_P;
-  uint8_t* out_s = smem + C::OFF_OUT;
   uint8_t* pp_s = smem + C::OFF_PP;
   float* sc_s = reinterpret_cast<float*>(smem + C::OFF_SC);
   Aux* a = reinterpret_cast<Aux*>(smem + C::OFF_AUX);
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
-  const int rank = uniform((int)cluster_rank());  // which half of the columns, and which 64 of the rows
+  const int rank = uniform((int)cluster_rank());  // which 32 positions of a tile, which half of the value columns
   int* err = p.err;
 
   if (warp == 0) {
     tmem_alloc(&a->tmem, 512);
     tmem_relinquish();
   }
+  constexpr uint32_t kMaxBytes = kRows * 4 + 4 * 4;  // a tile's maxima and clear words
+  constexpr uint32_t kPBytes = C::PC * C::P_HALF;    // a tile's P from the other CTA
   if (tid == 32) {
-    for (int i = 0; i < 3; ++i) mbar_init(&a->full[i], C::FP8 ? 4 : 1), mbar_init(&a->empty[i], 1);
+    const int fillers = C::FP8 ? 8 : 1;  // arrivals that fill a slot: converter warps, or the TMA's thread
+    for (int i = 0; i < 3; ++i) mbar_init(&a->v_full[i], fillers), mbar_init(&a->v_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&a->s_full[i], 1), mbar_init(&a->s_empty[i], 8);
-      mbar_init(&a->x_full[i], 1), mbar_init(&a->x_read[i], 4), mbar_init(&a->x_free[i], 1);
-      mbar_init(&a->p_full[i], 8), mbar_init(&a->p_msg[i], 1), mbar_init(&a->p_free[i], 1), mbar_init(&a->pv_done[i], 1);
-      mbar_init(&a->sc_full[i], 32), mbar_init(&a->sc_empty[i], C::TILED ? 8 : 4);
+      mbar_init(&a->k_full[i], fillers), mbar_init(&a->k_empty[i], 1);
+      mbar_init(&a->s_full[i], 1), mbar_init(&a->s_empty[i], 4);
+      mbar_init(&a->p_full[i], 4), mbar_init(&a->p_msg[i], 1), mbar_init(&a->p_free[i], 1), mbar_init(&a->pv_done[i], 1);
+      mbar_init(&a->sc_full[i], 32), mbar_init(&a->sc_empty[i], 4);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&a->m_msg[i], 1);
     mbar_init(&a->stat_full, 1);
     mbar_init(&a->o_done, 1);
-    mbar_init(&a->o_free, 8);
-    mbar_init(&a->q_full, 256);
+    mbar_init(&a->o_free, 4);
+    mbar_init(&a->q_full, 128);
     mbar_init(&a->drain, 1);
     a->abort = 0;
     fence_mbar_init();
-    for (int i = 0; i < 2; ++i) {
-      mbar_arrive_expect_tx(&a->x_full[i], C::X_BYTES);
-      mbar_arrive_expect_tx(&a->p_msg[i], C::MSG_BYTES);
-    }
-    mbar_arrive_expect_tx(&a->stat_full, 64 * 4);
+    for (int i = 0; i < 4; ++i) mbar_arrive_expect_tx(&a->m_msg[i], kMaxBytes);
+    for (int i = 0; i < C::PB; ++i) mbar_arrive_expect_tx(&a->p_msg[i], kPBytes);
+    mbar_arrive_expect_tx(&a->stat_full, kRows * 4);
   }
-  if (pl.cap) plan_items(p, pl, a, reinterpret_cast<int*>(tiles_s));
-  fence_proxy_async_smem();  // the plan's scratch is a tile that the copies write
+  if (pl.cap) plan_items(p, pl, a, reinterpret_cast<int*>(v_s));
+  fence_proxy_async_smem();  // the plan's scratch is a slot that the copies write
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // the peer's barriers are ready too
+  cluster_sync();  // the other CTA's barriers are ready too
   tc_fence_after();
   const uint32_t tmem = a->tmem;
   pdl_launch_dependents();
 
   Item it;
   if (warp == 0) {
-    // ---- producer (bf16): this CTA's columns of each tile by TMA
+    // ---- producer (bf16): boxes of 64 columns x 32 positions by TMA
     if (lane == 0 && !C::FP8) {
       prefetch_tmap(&tm);
-      int sl = 0, ph = 0, tiles = 0;
+      int vs = 0, vph = 0, ks = 0, kph = 0, tiles = 0;
       bool ok = true;
       for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
         for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
@@ -501,88 +489,120 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
             row = bad ? p.pages.num_blocks * p.pages.block_size : (int)r;
             if (bad) record_error(err, DSA_DEVERR_INDEX_RANGE);
           }
-          ok = wait(a, &a->empty[sl], ph ^ 1, err);
+          const int mine = row + 32 * rank, other = row + 32 * (rank ^ 1);
+          ok = wait(a, &a->v_empty[vs], vph ^ 1, err);
           if (!ok) break;
           a->tile_bad[tiles & 3] = bad;
-          uint8_t* dst = tiles_s + sl * kTile;
-          mbar_arrive_expect_tx(&a->full[sl], kTile);
+          uint8_t* dst = v_s + vs * kSlotV;
+          mbar_arrive_expect_tx(&a->v_full[vs], kSlotV);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) tma_load_3d(dst + b * kBox, &tm, &a->full[sl], 256 * rank + 64 * b, row, z);
-          tma_load_3d(dst + 4 * kBox, &tm, &a->full[sl], 512, row, z);
-          if (++sl == C::STAGES) sl = 0, ph ^= 1;
+          for (int b = 0; b < 4; ++b) tma_load_3d(dst + b * kBox, &tm, &a->v_full[vs], 256 * rank + 64 * b, mine, z);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) tma_load_3d(dst + (4 + b) * kBox, &tm, &a->v_full[vs], 256 * rank + 64 * b, other, z);
+          if (++vs == C::VS) vs = 0, vph ^= 1;
+          ok = wait(a, &a->k_empty[ks], kph ^ 1, err);
+          if (!ok) break;
+          dst = k_s + ks * kSlotK;
+          mbar_arrive_expect_tx(&a->k_full[ks], kSlotK);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) tma_load_3d(dst + b * kBox, &tm, &a->k_full[ks], 256 * (rank ^ 1) + 64 * b, mine, z);
+          tma_load_3d(dst + 4 * kBox, &tm, &a->k_full[ks], 512, mine, z);
+          if (++ks == C::KS) ks = 0, kph ^= 1;
         }
       }
-      if (*reinterpret_cast<volatile int*>(&a->abort))  // wind down: the copies in flight land first
-        for (int s = 0; s < C::STAGES; ++s) mbar_wait(&a->full[s], s < sl ? ph : ph ^ 1, err);
+      if (*reinterpret_cast<volatile int*>(&a->abort)) {  // wind down: the copies in flight land first
+        for (int s = 0; s < C::VS; ++s) mbar_wait(&a->v_full[s], s < vs ? vph : vph ^ 1, err);
+        for (int s = 0; s < C::KS; ++s) mbar_wait(&a->k_full[s], s < ks ? kph : kph ^ 1, err);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---- MMA issuer.  The warp stays converged and one elected lane issues; descriptors are sums of
-    // 32-bit words (their upper words are one constant), so that issuing an instruction costs less than
+    // 32-bit words (their upper words are constants), so that issuing an instruction costs less than
     // the tensor cores take for it
-    constexpr uint32_t idesc_qk = make_idesc(1, 1, kRows, kKeys);
+    constexpr uint32_t idesc_qk = make_idesc(1, 1, kRows, 32);
     constexpr uint32_t idesc_pv = make_idesc(1, 1, kRows, C::TILED ? 128 : 256) | (1u << 16);  // B (values) MN-major
     const uint32_t tm_base = (uint32_t)uniform((int)tmem);
-    const uint32_t k_lo = kmajor_lo(smem_u32(tiles_s)), v_lo = mnmajor_lo(smem_u32(tiles_s));
-    const uint32_t qr_lo = kmajor_lo(smem_u32(qr_s)) + 4 * rank;  // this CTA's half: 64 bytes into the row
-    const uint32_t p_lo = kmajor_lo(smem_u32(p_s));
-    int qs = 0, qph = 0, ps = 0;  // stages of the first and of the second product
+    const uint32_t kv_lo = kmajor_lo(smem_u32(v_s)), kk_lo = kmajor_lo(smem_u32(k_s)), v_lo = mnmajor_lo(smem_u32(v_s));
+    const uint32_t q_lo = kmajor_lo(smem_u32(q_s)), p_lo = kmajor_lo(smem_u32(p_s));
+    int vs = 0, vph = 0, ks = 0, kph = 0;  // slots of the first product
+    int ps = 0;                            // value slot of the second
     int tile = 0, items = 0;
-    uint32_t su = 0;              // uses of the S buffers
+    uint32_t su = 0;                       // uses of the S buffers
     bool ok = true;
     auto all = [&](uint64_t* bar, uint32_t parity) { ok = __all_sync(0xffffffffu, wait(a, bar, parity, err)) && ok; };
     auto commit = [&](uint64_t* bar) {
       if (elect_one()) tc_commit(bar);
       __syncwarp();
     };
-    // First product of the next tile, group g of its columns: all of them (-1), or for 128-column scales
-    // one accumulation per scale tile (0, 1: 128 value columns; 2: the rotary ones).  The row warps have
-    // read what the S buffer held.
-    auto qk = [&](int g) {
-      if (g <= 0) all(&a->full[qs], qph);
-      all(&a->s_empty[su & 1], ((su >> 1) & 1) ^ 1);
-      tc_fence_after();
-      const uint32_t d = tm_base + kColS + 64 * (su & 1), B = k_lo + qs * (kTile >> 4);
-      if (elect_one()) {
-        if (g < 2) {
-          const uint32_t q0 = tm_base + kColQ + (g > 0 ? 64 : 0), B0 = B + (g > 0 ? 2 * kBox >> 4 : 0);
+    // Box j of q against this CTA's positions: 4 steps of K = 16.
+    auto qk_box = [&](uint32_t d, int j, uint32_t B, bool first) {
 #pragma unroll
-          for (int k = 0; k < (C::TILED ? 8 : 16); ++k)
-            mma_ts(d, q0 + 8 * k, B0 + ((k >> 2) * kBox + 32 * (k & 3)) / 16, idesc_qk, k ? 1u : 0u);
-        }
-        if (g < 0 || g == 2) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            mma_ss(d, qr_lo + 2 * k, B + (4 * kBox >> 4) + 4 * rank + 2 * k, idesc_qk, k || !C::TILED ? 1u : 0u);
-        }
-        tc_commit(&a->s_full[su & 1]);
-      }
-      __syncwarp();
-      ++su;
-      if (g < 0 || g == 2) {
-        if (++qs == C::STAGES) qs = 0, qph ^= 1;
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t acc = first && k == 0 ? 0u : 1u;
+        if (j < kBoxesT) mma_ts(d, tm_base + kColQ + 32 * j + 8 * k, B + 2 * k, idesc_qk, acc);
+        else mma_ss(d, q_lo + (j - kBoxesT) * (C::Q_BOX >> 4) + 2 * k, B + 2 * k, idesc_qk, acc);
       }
     };
+    // First product of the next tile; with tile scales one accumulation (pair of boxes) after another through
+    // the S buffers.  The softmax warps have read what a buffer held.
     auto qk_tile = [&]() {
-      if (C::TILED) qk(0), qk(1), qk(2);
-      else qk(-1);
+      all(&a->v_full[vs], vph);
+      all(&a->k_full[ks], kph);
+      const uint32_t V = kv_lo + vs * (kSlotV >> 4), K = kk_lo + ks * (kSlotK >> 4);
+#pragma unroll 1
+      for (int g = 0; g < C::GROUPS; ++g, ++su) {
+        all(&a->s_empty[su & 1], ((su >> 1) & 1) ^ 1);
+        tc_fence_after();
+        const uint32_t d = tm_base + kColS + 32 * (su & 1);
+        if (elect_one()) {
+          if (C::TILED) {
+            if (g < 4) {
+              const uint32_t B = ((g >> 1) == rank ? V : K) + (2 * (g & 1) * kBox >> 4);
+              if (g < 3) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  mma_ts(d, tm_base + kColQ + 64 * g + 8 * k, B + ((k >> 2) * kBox + 32 * (k & 3)) / 16, idesc_qk, k ? 1u : 0u);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  mma_ss(d, q_lo + ((k >> 2) * C::Q_BOX + 32 * (k & 3)) / 16, B + ((k >> 2) * kBox + 32 * (k & 3)) / 16, idesc_qk,
+                         k ? 1u : 0u);
+              }
+            } else {
+              qk_box(d, 8, K + (4 * kBox >> 4), true);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) qk_box(d, j, ((j >> 2) == rank ? V : K) + ((j & 3) * kBox >> 4), j == 0);
+            qk_box(d, 8, K + (4 * kBox >> 4), false);
+          }
+          tc_commit(&a->s_full[su & 1]);
+          if (g == C::GROUPS - 1) tc_commit(&a->k_empty[ks]);
+        }
+        __syncwarp();
+      }
+      if (++vs == C::VS) vs = 0, vph ^= 1;
+      if (++ks == C::KS) ks = 0, kph ^= 1;
     };
     auto pv = [&](bool first) {
-      const uint32_t acc0 = first ? 0u : 1u, B = v_lo + ps * (kTile >> 4);
+      const uint32_t acc0 = first ? 0u : 1u, V = v_lo + ps * (kSlotV >> 4);
       const uint32_t P = p_lo + (tile % C::PB) * (C::PC * C::P_BYTES >> 4);
       if (elect_one()) {
         constexpr int NB = C::TILED ? 2 : 1;  // value tiles of N = 128 with a P each, or all 256 at once
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_ss(tm_base + kColO + 128 * b, P + (b * C::P_BYTES + 32 * ks) / 16, B + (2 * b * kBox + 2048 * ks) / 16,
-                   idesc_pv, ks ? 1u : acc0);
-        tc_commit(&a->empty[ps]);
+          for (int s = 0; s < 4; ++s) {  // two steps over this CTA's positions, two over the other's
+            const uint32_t half = (uint32_t)((s >> 1) ^ rank);  // whose P: the halves of the buffer are by CTA
+            mma_ss<kDescHi64>(tm_base + kColO + 128 * b, P + (b * C::P_BYTES >> 4) + half * (C::P_HALF >> 4) + 2 * (s & 1),
+                              V + ((4 * (s >> 1) + 2 * b) * kBox + 2048 * (s & 1)) / 16, idesc_pv, s ? 1u : acc0);
+          }
+        tc_commit(&a->v_empty[ps]);
         tc_commit(&a->pv_done[tile & 1]);
       }
       __syncwarp();
-      if (++ps == C::STAGES) ps = 0;
+      if (++ps == C::VS) ps = 0;
     };
     constexpr int AHEAD = C::TILED ? 1 : 2;  // tiles whose first product is issued before P of this one is there
     for (int i = 0; uniform(get_item(p, pl, a, i, it)); ++i) {
@@ -595,14 +615,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
       for (int t = t0; t < t1; ++t, ++tile) {
         // the tile after next early, if it and its S buffer are ready; P of this one first otherwise
         bool started = tq >= t1;
-        if (!started && (C::TILED || __all_sync(0xffffffffu, mbar_test(&a->full[qs], qph) &&
+        if (!started && (C::TILED || __all_sync(0xffffffffu, mbar_test(&a->v_full[vs], vph) && mbar_test(&a->k_full[ks], kph) &&
                                                                  mbar_test(&a->s_empty[su & 1], ((su >> 1) & 1) ^ 1)))) {
           qk_tile();
           ++tq;
           started = true;
         }
+        const int pb = tile % C::PB;
         all(&a->p_full[tile & 1], (tile >> 1) & 1);
+        ok = __all_sync(0xffffffffu, wait_cluster(a, &a->p_msg[pb], (tile / C::PB) & 1, err)) && ok;
+        if (lane == 0) mbar_arrive_expect_tx(&a->p_msg[pb], kPBytes);  // for this buffer's next use
         if (t == t0) all(&a->o_free, (items & 1) ^ 1);
+        __syncwarp();
         tc_fence_after();
         pv(t == t0);
         if (!started) {
@@ -618,24 +642,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
       mbar_wait(&a->drain, 0, err);
     }
   } else if (warp == 2 && C::FP8) {
-    // ---- scales of the tile's positions (1 where there is none: the position is masked)
+    // ---- scales of this CTA's positions (1 where there is none: the position is masked)
     int tiles = 0;
     bool ok = true;
     for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
       for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
-        const int d = tiles % C::SC_DEPTH;
+        const int d = tiles % C::SC_DEPTH, pos = t * kKeys + 32 * rank;
         int64_t row = tree_row(p, it.seq, t * kKeys);
         const bool bad = row < 0;
-        if (!p.pages.table) row += (int64_t)it.seq * p.L;
-        const int n = min(kKeys, it.len - t * kKeys) * C::NSC;
+        row += 32 * rank + (p.pages.table ? 0 : (int64_t)it.seq * p.L);
+        const int n = (it.len - pos) * C::NSC;
         const float* src = p.kv_scale + row * C::NSC;
-        float v[C::NSC * 2 + 1];
+        float v[C::NSC + 1];
 #pragma unroll
-        for (int k = 0; k < C::NSC * 2; ++k) v[k] = !bad && lane + 32 * k < n ? __ldg(src + lane + 32 * k) : 1.f;
+        for (int k = 0; k < C::NSC; ++k) v[k] = !bad && lane + 32 * k < n ? __ldg(src + lane + 32 * k) : 1.f;
         ok = __all_sync(0xffffffffu, wait(a, &a->sc_empty[d], ((tiles / C::SC_DEPTH) & 1) ^ 1, err));
         if (!ok) break;
 #pragma unroll
-        for (int k = 0; k < C::NSC * 2; ++k) sc_s[d * kKeys * C::NSC + lane + 32 * k] = v[k];
+        for (int k = 0; k < C::NSC; ++k) sc_s[d * 32 * C::NSC + lane + 32 * k] = v[k];
         if (lane == 0) {
           a->tile_bad[tiles & 3] = bad;
           if (bad) record_error(err, DSA_DEVERR_INDEX_RANGE);
@@ -645,41 +669,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
       }
     }
   } else if (warp == 3) {
-    // ---- credits of the exchange (here, because a release at cluster scope would hold up the row warps): once
-    // our softmax warps have read the peer's part of S, its buffer is armed for the tile after next and
-    // the peer told so; once a second product has read P, the peer may send into that buffer again
+    // ---- credits of the exchange (here, because a release at cluster scope would hold up the softmax warps):
+    // once a second product has read P, the other CTA may send into that buffer again
     int tiles = 0;
     bool ok = true;
-    const uint32_t peer_x = dsmem_addr(&a->x_free[0], rank ^ 1), peer_p = dsmem_addr(&a->p_free[0], rank ^ 1);
+    const uint32_t peer_p = dsmem_addr(&a->p_free[0], rank ^ 1);
     for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
       for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
-        const int b = tiles & 1;
-        ok = __all_sync(0xffffffffu, wait(a, &a->x_read[b], (tiles >> 1) & 1, err));
-        if (ok && lane == 0) {
-          mbar_arrive_expect_tx(&a->x_full[b], C::X_BYTES);
-          arrive_remote(peer_x + 8 * b);
-        }
-        __syncwarp();
-        ok = ok && __all_sync(0xffffffffu, wait(a, &a->pv_done[b], (tiles >> 1) & 1, err));
+        ok = __all_sync(0xffffffffu, wait(a, &a->pv_done[tiles & 1], (tiles >> 1) & 1, err));
         if (ok && lane == 0) arrive_remote(peer_p + 8 * (tiles % C::PB));
         __syncwarp();
       }
     }
-  } else if (warp >= 12) {
+  } else if (warp >= 8) {
     // ---- converters (E4M3): 16 codes per lane and step, loaded a tile ahead, widened into the swizzled bf16
     // boxes.  Eight lanes take four 16-code chunks of one box from two neighbouring positions: their eight
-    // 16-byte stores fall into different banks.
-    const int ct = tid - 384, cw = warp - 12;
-    int st = 0, sph = 0;
+    // 16-byte stores fall into different banks.  A warp takes one pair of positions of each group of 8 pairs:
+    // step k < 4: box k of our value columns, ours; < 8: the other's positions; < 12: our other columns; 12: rotary.
+    const int cw = warp - 8;
+    int vs = 0, vph = 0, ks = 0, kph = 0;
     bool ok = true;
-    uint4 raw[9];
-    auto place = [&](int k, int& key, int& box, int& c) {  // chunk c of 16 codes of a box of 64 columns
-      if (k < 8) {
-        const int unit = 16 * k + 4 * cw + (lane >> 3);
-        box = unit & 3, key = 2 * (unit >> 2) + ((lane >> 2) & 1), c = lane & 3;
-      } else {  // the rotary half: 32 codes of a position
-        box = 4, key = ct >> 1, c = 2 * rank + (ct & 1);
-      }
+    constexpr int STEPS = 7;  // two boxes per step (lanes 0-15, 16-31), the rotary one alone
+    uint4 raw[STEPS];
+    // step k: box 2 k + lane / 16; the warp's pair of positions: 2 cw + 16 (lane / 8 % 2) ... (of 32)
+    auto place = [&](int k, int& box, int& key, int& c) {
+      box = 2 * k + (lane >> 4);
+      c = lane & 3;
+      key = 2 * cw + ((lane >> 2) & 1) + 16 * ((lane >> 3) & 1);
     };
     auto tile_rows = [&](const Item& x, int t) -> const uint8_t* {
       if (t >= x.t1) return nullptr;
@@ -688,107 +704,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
       return p.kv + (p.pages.table ? 0 : (int64_t)x.seq * p.kv_seq_stride) + row * p.kv_row_stride;
     };
     auto fetch = [&](const uint8_t* r, int n, int k) {
-      int key, box, c;
-      place(k, key, box, c);
-      const int col = (box < 4 ? 256 * rank + 64 * box : 512) + 16 * c;
-      raw[k] = r && key < n ? __ldg(reinterpret_cast<const uint4*>(r + (int64_t)key * p.kv_row_stride + col))
-                            : make_uint4(0u, 0u, 0u, 0u);
+      int box, key, c;
+      place(k, box, key, c);
+      // boxes 0-3: our value columns of our positions, 4-7: of the other's, 8-11: our positions' other columns, 12
+      const int at = key + 32 * (box >= 4 && box < 8 ? rank ^ 1 : rank);
+      const int col = (box < 8 ? 256 * rank + 64 * (box & 3) : box < 12 ? 256 * (rank ^ 1) + 64 * (box & 3) : 512) + 16 * c;
+      raw[k] = r && at < n && box < 13 ? __ldg(reinterpret_cast<const uint4*>(r + (int64_t)at * p.kv_row_stride + col))
+                                       : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto store = [&](int k) {
+      int box, key, c;
+      place(k, box, key, c);
+      if (box >= 13) return;
+      uint8_t* d = (box < 8 ? v_s + vs * kSlotV + box * kBox : k_s + ks * kSlotK + (box - 8) * kBox) + key * 128;
+      const uint4 v = raw[k];
+      *reinterpret_cast<uint4*>(d + (((2 * c) ^ (key & 7)) << 4)) =
+          make_uint4(e4m3x2_to_bf16x2(v.x, 0x1404), e4m3x2_to_bf16x2(v.x, 0x3424), e4m3x2_to_bf16x2(v.y, 0x1404),
+                     e4m3x2_to_bf16x2(v.y, 0x3424));
+      *reinterpret_cast<uint4*>(d + (((2 * c + 1) ^ (key & 7)) << 4)) =
+          make_uint4(e4m3x2_to_bf16x2(v.z, 0x1404), e4m3x2_to_bf16x2(v.z, 0x3424), e4m3x2_to_bf16x2(v.w, 0x1404),
+                     e4m3x2_to_bf16x2(v.w, 0x3424));
     };
     for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
       const uint8_t* r = tile_rows(it, it.t0);
       const uint8_t* r1 = tile_rows(it, it.t0 + 1);  // the block table is read two tiles ahead, the codes one
 #pragma unroll
-      for (int k = 0; k < 9; ++k) fetch(r, it.len - it.t0 * kKeys, k);
+      for (int k = 0; k < STEPS; ++k) fetch(r, it.len - it.t0 * kKeys, k);
       for (int t = it.t0; ok && t < it.t1; ++t) {
         r = r1;
         r1 = tile_rows(it, t + 2);
         const int n = it.len - (t + 1) * kKeys;
-        ok = __all_sync(0xffffffffu, wait(a, &a->empty[st], sph ^ 1, err));
+        ok = __all_sync(0xffffffffu, wait(a, &a->v_empty[vs], vph ^ 1, err));
         if (!ok) break;
-        uint8_t* dst = tiles_s + st * kTile;
 #pragma unroll
-        for (int k = 0; k < 9; ++k) {
-          int key, box, c;
-          place(k, key, box, c);
-          uint8_t* d = dst + box * kBox + key * 128;
-          const uint4 v = raw[k];
-          *reinterpret_cast<uint4*>(d + (((2 * c) ^ (key & 7)) << 4)) =
-              make_uint4(e4m3x2_to_bf16x2(v.x, 0x1404), e4m3x2_to_bf16x2(v.x, 0x3424), e4m3x2_to_bf16x2(v.y, 0x1404),
-                         e4m3x2_to_bf16x2(v.y, 0x3424));
-          *reinterpret_cast<uint4*>(d + (((2 * c + 1) ^ (key & 7)) << 4)) =
-              make_uint4(e4m3x2_to_bf16x2(v.z, 0x1404), e4m3x2_to_bf16x2(v.z, 0x3424), e4m3x2_to_bf16x2(v.w, 0x1404),
-                         e4m3x2_to_bf16x2(v.w, 0x3424));
+        for (int k = 0; k < 4; ++k) {
+          store(k);
           fetch(r, n, k);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&a->full[st]);
-        if (++st == C::STAGES) st = 0, sph ^= 1;
+        if (lane == 0) mbar_arrive(&a->v_full[vs]);
+        if (++vs == C::VS) vs = 0, vph ^= 1;
+        ok = __all_sync(0xffffffffu, wait(a, &a->k_empty[ks], kph ^ 1, err));
+        if (!ok) break;
+#pragma unroll
+        for (int k = 4; k < STEPS; ++k) {
+          store(k);
+          fetch(r, n, k);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&a->k_full[ks]);
+        if (++ks == C::KS) ks = 0, kph ^= 1;
       }
     }
   } else if (warp >= 4) {
-    // ---- row warps.  Thread = row (tensor-memory lane) and half h of the tile's positions (32), of the query's
-    // columns and of the value columns.  Rows 64 rank ... are ours (softmax), the others the peer's.
-    const int w = warp - 4, h = w >> 2, quarter = w & 3, row = 32 * quarter + lane, r64 = row & 63;
-    const bool own = (quarter >> 1) == rank;
-    const int bar_id = 1 + (quarter & 1);
+    // ---- softmax warps: thread = row = tensor-memory lane, this CTA's 32 positions
+    const int quarter = warp - 4, row = 32 * quarter + lane, st = tid - 128;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
-    const int unit = 2 * (quarter & 1) + h;  // of the exchanged logits: 32 rows x 32 positions, [8 chunks][32 rows] x 16 B
-    const uint32_t peer_x = dsmem_addr(x_s, rank ^ 1) + unit * 4096;
-    const uint32_t peer_xf = dsmem_addr(&a->x_full[0], rank ^ 1), peer_msg = dsmem_addr(&a->p_msg[0], rank ^ 1);
-    const uint32_t peer_p = dsmem_addr(p_s, rank ^ 1) + 32 * quarter * 128;
-    const uint32_t peer_fac = dsmem_addr(&a->fac[0][32 * (quarter & 1)], rank ^ 1);
-    const uint32_t peer_clear = dsmem_addr(&a->clear[0][unit], rank ^ 1);
-    const float4* my_x = reinterpret_cast<const float4*>(x_s) + unit * 256 + lane;
+    const uint32_t peer_mx = dsmem_addr(&a->mx[0][row], rank ^ 1), peer_mm = dsmem_addr(&a->m_msg[0], rank ^ 1);
+    const uint32_t peer_clear = dsmem_addr(&a->clear[0][quarter], rank ^ 1);
+    const uint32_t peer_p = dsmem_addr(p_s, rank ^ 1) + rank * C::P_HALF + 32 * quarter * 64;
+    const uint32_t peer_pm = dsmem_addr(&a->p_msg[0], rank ^ 1);
+    const uint32_t peer_stat = dsmem_addr(&a->stat[row], rank ^ 1), peer_sf = dsmem_addr(&a->stat_full, rank ^ 1);
     int tile = 0, items = 0;
     uint32_t su = 0;
     bool ok = true;
     const int rows = p.q_per_seq * p.H;
-
-    // This CTA's partial logits of tile n (its columns; with tile scales, scaled), 32 positions of this row.
-    auto partial = [&](int n, float (&x)[32]) {
-      if constexpr (C::TILED) {
-        const float* sc = sc_s + (n % C::SC_DEPTH) * kKeys * 5 + 32 * h * 5;
-        ok = wait(a, &a->sc_full[n % C::SC_DEPTH], (n / C::SC_DEPTH) & 1, err) && ok;
-#pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = 0.f;
-#pragma unroll 1
-        for (int g = 0; g < 3; ++g, ++su) {
-          ok = wait(a, &a->s_full[su & 1], (su >> 1) & 1, err) && ok;
-          tc_fence_after();
-          float s[32];
-          tmem_ld_sync(lane_base + kColS + 64 * (su & 1) + 32 * h, s);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&a->s_empty[su & 1]);
-          const float* f = sc + (g < 2 ? 2 * rank + g : 4);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = fmaf(f[5 * k], s[k], x[k]);
-        }
-      } else {
-        ok = wait(a, &a->s_full[n & 1], (n >> 1) & 1, err) && ok;
-        tc_fence_after();
-        tmem_ld_sync(lane_base + kColS + 64 * (n & 1) + 32 * h, x);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&a->s_empty[n & 1]);
-      }
-    };
-    // O of this row (128 of the columns) times f, once the tile before has been added.
-    auto rescale = [&](int n, float f) {
-      ok = wait(a, &a->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err) && ok;
-      tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < 128; c += 16) {
-        float o[16];
-        tmem_ld_sync(lane_base + kColO + 128 * h + c, o);
-        uint32_t v[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(o[k] * f);
-        tmem_st16(lane_base + kColO + 128 * h + c, v);
-      }
-      tmem_wait_st();
-    };
 
     for (int i = 0; get_item(p, pl, a, i, it); ++i) {
       const int row_lo = it.rt * kRows;
@@ -796,285 +778,254 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
       const int nrows = min(kRows, rows - row_lo);
       if (it.t0 >= it.t1) {  // nothing to see: padding nodes, or an empty sequence
         if (rank == 0) {
-          const int st = tid - 128;
-          for (int k = st; k < nrows * (kDv / 8); k += 256)
+          for (int k = st; k < nrows * (kDv / 8); k += 128)
             reinterpret_cast<uint4*>(p.out + at * kDv)[k] = make_uint4(0u, 0u, 0u, 0u);
           if (p.lse && st < nrows) p.lse[at + st] = -INFINITY;
         }
         continue;
       }
-      // the query's rows: 128 of this CTA's 256 value columns into tensor memory, half of its 32 rotary
-      // columns into shared memory (the previous item's products are done: its epilogue waited for them)
+      // the query's row: 384 columns into tensor memory, 192 into shared memory (the previous item's products
+      // are done: its epilogue waited for them)
       {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (at + (row < nrows ? row : 0)) * kDqk);
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        uint4 r[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) r[k] = row < nrows ? __ldg(src + 64 + 4 * rank + 2 * h + k) : zero;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
+#pragma unroll 4
+        for (int c = 0; c < 8 * (9 - kBoxesT); ++c)
+          cp_async16(q_s + (c >> 3) * C::Q_BOX + row * 128 + (((c & 7) ^ (row & 7)) << 4), src + 8 * kBoxesT + c, row < nrows);
+        cp_async_commit();
+#pragma unroll 3
+        for (int g = 0; g < 2 * kBoxesT; ++g) {
           uint32_t v[16];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 u = row < nrows ? __ldg(src + 32 * rank + 16 * h + 4 * g + k) : zero;
+            const uint4 u = row < nrows ? __ldg(src + 4 * g + k) : zero;
             v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
           }
-          tmem_st16(lane_base + kColQ + 64 * h + 16 * g, v);
+          tmem_st16(lane_base + kColQ + 16 * g, v);
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          *reinterpret_cast<uint4*>(qr_s + row * 128 + (((4 * rank + 2 * h + k) ^ (row & 7)) << 4)) = r[k];
+        cp_async_wait<0>();
         tmem_wait_st();
         tc_fence_before();
         fence_proxy_async_smem();
         mbar_arrive(&a->q_full);
       }
-      float l = 0.f;
-      if (own) {
-        // ======== softmax of our rows
-        const int node = min((row_lo + row) / p.H, p.q_per_seq - 1);
-        float m = -INFINITY;
-        for (int t = it.t0; t < it.t1; ++t, ++tile) {
-          const int xb = tile & 1, pb = tile % C::PB;
-          const bool tail = (t + 1) * kKeys > it.ctx;
-          const float* sc = sc_s + (tile % C::SC_DEPTH) * kKeys * C::NSC + 32 * h * C::NSC;
-          float x[32];
-          partial(tile, x);
-          ok = wait_cluster(a, &a->x_full[xb], (tile >> 1) & 1, err) && ok;
+      const int node = min((row_lo + row) / p.H, p.q_per_seq - 1);
+      float m = -INFINITY, l = 0.f;
+
+      // Logits of tile n (position tile t) for this row, scaled and masked; their maximum goes to the other CTA.
+      auto stage = [&](int n, int t, float (&x)[32], float& mx) {
+        const float* sc = sc_s + (n % C::SC_DEPTH) * 32 * C::NSC;
+        if constexpr (C::FP8) ok = wait(a, &a->sc_full[n % C::SC_DEPTH], (n / C::SC_DEPTH) & 1, err) && ok;
+        if constexpr (C::TILED) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 v = my_x[xb * (C::X_BYTES / 16) + j * 32];
-            x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
-          }
+          for (int k = 0; k < 32; ++k) x[k] = 0.f;
+        }
+#pragma unroll 1
+        for (int g = 0; g < C::GROUPS; ++g, ++su) {
+          ok = wait(a, &a->s_full[su & 1], (su >> 1) & 1, err) && ok;
+          tc_fence_after();
+          float s[32];
+          tmem_ld_sync(lane_base + kColS + 32 * (su & 1), s);
+          tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&a->x_read[xb]);
-          // ---- scale, mask
-          if constexpr (FMT == kFp8Row) {
-            ok = wait(a, &a->sc_full[tile % C::SC_DEPTH], (tile / C::SC_DEPTH) & 1, err) && ok;
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(sc + k);
-              x[k] *= f.x * p.scale_log2, x[k + 1] *= f.y * p.scale_log2;
-              x[k + 2] *= f.z * p.scale_log2, x[k + 3] *= f.w * p.scale_log2;
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] *= p.scale_log2;
-          }
-          const bool bad = p.pages.table && a->tile_bad[tile & 3];
-          uint32_t clear = 0;
-          if (tail || bad) {
-            const uint32_t see = bad ? 0u : (uint32_t)(seen_bits(p, it, node, t) >> (32 * h));
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              if (!((see >> k) & 1)) {
-                // a hidden position that may hold infinities or NaN (its logit is not finite, or it lies past
-                // the end): its values are cleared in the tile, so that 0 * value is 0
-                if (!C::FP8 && (!(fabsf(x[k]) < INFINITY) || t * kKeys + 32 * h + k >= it.len)) clear |= 1u << k;
-                x[k] = -INFINITY;
-              }
-            }
-            clear = __reduce_or_sync(0xffffffffu, clear);
-          }
-          // ---- the reference maximum moves when a position exceeds it by more than kLazy
-          float mx = x[0];
-#pragma unroll
-          for (int k = 1; k < 32; ++k) mx = fmaxf(mx, x[k]);
-          a->red[h][r64] = mx;
-          float f = 1.f;
-          if (pair_any(bar_id, mx > m + kLazy)) {
-            mx = fmaxf(a->red[0][r64], a->red[1][r64]);
-            if (mx > m + kLazy) {  // (m = -inf: nothing summed yet, the factor is 0)
-              f = ex2(m - mx);
-              m = mx;
-              l *= f;
-            }
-            if (t > it.t0) rescale(tile, f);
-            pair_bar(bar_id);  // red is read before the next tile's maxima are written
-          }
-          // ---- weights
-          const float mu = m == -INFINITY ? 0.f : m;
+          if (lane == 0) mbar_arrive(&a->s_empty[su & 1]);
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            x[k] = ex2(x[k] - mu);
-            l += x[k];
+            if constexpr (C::TILED) x[k] = fmaf(sc[5 * k + g], s[k], x[k]);
+            else if constexpr (C::FP8) x[k] = s[k] * sc[k] * p.scale_log2;
+            else x[k] = s[k] * p.scale_log2;
           }
-          // the tile that used this P buffer has been added, here and at the peer
-          if (tile >= C::PB) ok = wait(a, &a->pv_done[(tile - C::PB) & 1], ((tile - C::PB) >> 1) & 1, err) && ok;
-          ok = wait_cluster(a, &a->p_free[pb], ((tile / C::PB) & 1) ^ 1, err) && ok;
-          if (C::TILED) {
-            if (h == 0 && lane == 0) copy_wait_read();  // the staged copies of the tile before have left
-            pair_bar(bar_id);
+        }
+        if constexpr (C::TILED) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] *= p.scale_log2;
+        }
+        const bool bad = p.pages.table && a->tile_bad[n & 3];
+        uint32_t clear = 0;
+        if ((t + 1) * kKeys > it.ctx || bad) {
+          const uint32_t see = bad ? 0u : (uint32_t)(seen_bits(p, it, node, t) >> (32 * rank));
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (!((see >> k) & 1)) {
+              // a hidden position that may hold infinities or NaN (its logit is not finite, or it lies past
+              // the end): its values are cleared in the tile, so that 0 * value is 0
+              if (!C::FP8 && (!(fabsf(x[k]) < INFINITY) || t * kKeys + 32 * rank + k >= it.len)) clear |= 1u << k;
+              x[k] = -INFINITY;
+            }
           }
-          const uint32_t msg = peer_msg + 8 * pb;
+          clear = __reduce_or_sync(0xffffffffu, clear);
+        }
+        mx = x[0];
 #pragma unroll
-          for (int pc = 0; pc < C::PC; ++pc) {
-            const int off = (pb * C::PC + pc) * C::P_BYTES;
+        for (int k = 1; k < 32; ++k) mx = fmaxf(mx, x[k]);
+        if (lane == 0) a->clear_own[n & 3][quarter] = clear;
+        if (ok) {
+          st_async4(peer_mx + (n & 3) * (kRows * 4), __float_as_uint(mx), peer_mm + 8 * (n & 3));
+          if (lane == 0) st_async4(peer_clear + (n & 3) * 16, clear, peer_mm + 8 * (n & 3));
+        }
+      };
+
+      float x[32], y[32], mx, my = -INFINITY;
+      stage(tile, it.t0, x, mx);
+      for (int t = it.t0; t < it.t1; ++t, ++tile) {
+        // the next tile's logits first, if they are there: their maxima travel while this tile is finished
+        const bool more = t + 1 < it.t1;
+        bool staged = false;
+        if (more && __all_sync(0xffffffffu, mbar_test(&a->s_full[su & 1], (su >> 1) & 1))) {
+          stage(tile + 1, t + 1, y, my);
+          staged = true;
+        }
+        ok = wait_cluster(a, &a->m_msg[tile & 3], (tile >> 2) & 1, err) && ok;
+        const float other = a->mx[tile & 3][row];
+        if (!C::FP8 && (t + 1) * kKeys > it.ctx) {
+          // zero the value columns of the positions to clear (their logits have been taken): a position past the
+          // end always, another one only if it holds something that is not finite
+          softmax_bar();
+          uint32_t clear[2] = {0u, 0u};  // ours, the other's
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {  // 16-byte chunks of eight positions
-              uint32_t v[4];
+          for (int k = 0; k < 4; ++k) clear[0] |= a->clear_own[tile & 3][k], clear[1] |= a->clear[tile & 3][k];
+          const int who = st >> 6, key = (st >> 1) & 31;  // two threads per position, two of its four boxes each
+          if ((clear[who] >> key) & 1) {
+            for (int b = 2 * (st & 1); b < 2 * (st & 1) + 2; ++b) {
+              uint8_t* line = v_s + (tile % C::VS) * kSlotV + (4 * who + b) * kBox + key * 128;
+              bool zero = t * kKeys + 32 * (who ? rank ^ 1 : rank) + key >= it.len;
+              if (!zero) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int e = 8 * j + 2 * k;
-                float y0 = x[e], y1 = x[e + 1];
-                if constexpr (C::FP8) {
-                  // the weight carries the position's scale (of the values' tile, here of this CTA's columns: the
-                  // peer's copy is made below); a hidden position's weight is 0 whatever its scale holds
-                  const float f0 = sc[e * C::NSC + (C::TILED ? 2 * rank + pc : 0)];
-                  const float f1 = sc[(e + 1) * C::NSC + (C::TILED ? 2 * rank + pc : 0)];
-                  y0 = y0 == 0.f ? 0.f : y0 * f0;
-                  y1 = y1 == 0.f ? 0.f : y1 * f1;
+                for (int c = 0; c < 8; ++c) {
+                  const uint4 u = *reinterpret_cast<const uint4*>(line + 16 * c);
+                  const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    zero |= (ws[q] & 0x7F80u) == 0x7F80u || (ws[q] & 0x7F800000u) == 0x7F800000u;
                 }
-                v[k] = pack_bf16(y0, y1);
               }
-              const int sw = ((4 * h + j) ^ (row & 7)) << 4;
-              *reinterpret_cast<uint4*>(p_s + off + row * 128 + sw) = make_uint4(v[0], v[1], v[2], v[3]);
-              if constexpr (C::TILED) {  // the peer's copy carries the scales of its value tiles
+              if (zero) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const int e = 8 * j + 2 * k;
-                  const float f0 = sc[e * 5 + 2 * (rank ^ 1) + pc], f1 = sc[(e + 1) * 5 + 2 * (rank ^ 1) + pc];
-                  v[k] = pack_bf16(x[e] == 0.f ? 0.f : x[e] * f0, x[e + 1] == 0.f ? 0.f : x[e + 1] * f1);
-                }
-                *reinterpret_cast<uint4*>(pp_s + pc * (C::P_BYTES / 2) + r64 * 128 + sw) = make_uint4(v[0], v[1], v[2], v[3]);
+                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(line + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
               }
             }
           }
-          if (h == 0) a->fac_own[pb][r64] = f;
-          fence_proxy_async_smem();
-          pair_bar(bar_id);  // both halves of the 32 rows are written
-          if (ok && lane == 0) {
-            if (h == 0) {
+        }
+        __syncwarp();
+        // the reference maximum moves, here and in the other CTA alike
+        const float top = fmaxf(mx, other);
+        if (__any_sync(0xffffffffu, top > m + kLazy)) {
+          float f = 1.f;
+          if (top > m + kLazy) {  // (m = -inf: nothing summed yet, the factor is 0)
+            f = ex2(m - top);
+            m = top;
+            l *= f;
+          }
+          if (t > it.t0) {
+            // the second product of the tile before is done: O may be rescaled
+            ok = wait(a, &a->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, err) && ok;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 16) {
+              float o[16];
+              tmem_ld_sync(lane_base + kColO + c, o);
+              uint32_t v[16];
 #pragma unroll
-              for (int pc = 0; pc < C::PC; ++pc)
-                copy_remote(peer_p + (pb * C::PC + pc) * C::P_BYTES,
-                            C::TILED ? pp_s + pc * (C::P_BYTES / 2) + 32 * (quarter & 1) * 128
-                                     : p_s + (pb * C::PC + pc) * C::P_BYTES + 32 * quarter * 128,
-                            4096, msg);
-              copy_remote(peer_fac + 256 * pb, &a->fac_own[pb][32 * (quarter & 1)], 128, msg);
-              copy_commit();
+              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(o[k] * f);
+              tmem_st16(lane_base + kColO + c, v);
             }
-            st_async4(peer_clear + 16 * pb, clear, msg);
-          }
-          if (!C::FP8 && tail) {
-            if (lane == 0) a->clear_own[tile & 1][2 * (quarter & 1) + h] = clear;
-            row_bar();  // the other four warps clear the tile
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (C::FP8) mbar_arrive(&a->sc_empty[tile % C::SC_DEPTH]);
-            mbar_arrive(&a->p_full[tile & 1]);
+            tmem_wait_st();
           }
         }
-        // ---- the item's sums, to the peer as well
-        pair_bar(bar_id);
-        a->red[h][r64] = l;
-        pair_bar(bar_id);
-        l = a->red[0][r64] + a->red[1][r64];
-        pair_bar(bar_id);
-        if (h == 0) {
-          if (ok) st_async4(dsmem_addr(&a->stat[r64], rank ^ 1), __float_as_uint(l), dsmem_addr(&a->stat_full, rank ^ 1));
-          const bool live = row < nrows && (row_lo + row) / p.H < it.fresh;
-          if (it.slot >= 0) pl.part_ml[(int64_t)it.slot * kRows + row] = make_float2(m, l);
-          else if (p.lse && row < nrows) p.lse[at + row] = !live || l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        }
-      } else {
-        // ======== the peer's rows: send it our partial logits a tile ahead, take in its P
-        auto send = [&](int n) {
-          float x[32];
-          partial(n, x);
-          if constexpr (C::TILED) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&a->sc_empty[n % C::SC_DEPTH]);
-          }
-          ok = wait_cluster(a, &a->x_free[n & 1], ((n >> 1) & 1) ^ 1, err) && ok;
-          if (lane == 0) copy_wait_read();  // the tile before has left
-          __syncwarp();
-          float4* o = reinterpret_cast<float4*>(out_s + unit * 4096) + lane;
+        // ---- weights
+        const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[32 * j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-          fence_proxy_async_smem();
+        for (int k = 0; k < 32; ++k) {
+          x[k] = ex2(x[k] - mu);
+          l += x[k];
+        }
+        // the tile that used this P buffer has been added, here and in the other CTA
+        const int pb = tile % C::PB;
+        if (tile >= C::PB) ok = wait(a, &a->pv_done[(tile - C::PB) & 1], ((tile - C::PB) >> 1) & 1, err) && ok;
+        ok = wait_cluster(a, &a->p_free[pb], ((tile / C::PB) & 1) ^ 1, err) && ok;
+        if (C::TILED) {
+          if (lane == 0) copy_wait_read();  // the staged copies of the tile before have left
           __syncwarp();
-          if (ok && lane == 0) {
-            copy_remote(peer_x + (n & 1) * C::X_BYTES, out_s + unit * 4096, 4096, peer_xf + 8 * (n & 1));
-            copy_commit();
+        }
+        const float* sc = sc_s + (tile % C::SC_DEPTH) * 32 * C::NSC;
+        // P (times the positions' scales; a hidden position's weight is 0 whatever its scale holds)
+        auto put = [&](uint8_t* dst, int g) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // 16-byte chunks of eight positions
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int e = 8 * j + 2 * k;
+              float y0 = x[e], y1 = x[e + 1];
+              if constexpr (C::FP8) {
+                y0 = y0 == 0.f ? 0.f : y0 * sc[e * C::NSC + g];
+                y1 = y1 == 0.f ? 0.f : y1 * sc[(e + 1) * C::NSC + g];
+              }
+              v[k] = pack_bf16(y0, y1);
+            }
+            *reinterpret_cast<uint4*>(dst + row * 64 + ((j ^ ((row >> 1) & 3)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
           }
         };
-        send(tile);
-        for (int t = it.t0; t < it.t1; ++t, ++tile) {
-          const int pb = tile % C::PB;
-          if (t + 1 < it.t1) send(tile + 1);
-          ok = wait_cluster(a, &a->p_msg[pb], (tile / C::PB) & 1, err) && ok;
-          const float f = a->fac[pb][r64];
-          uint32_t clear[2] = {a->clear[pb][0] | a->clear[pb][2], a->clear[pb][1] | a->clear[pb][3]};
-          if (t > it.t0 && __any_sync(0xffffffffu, f != 1.f)) rescale(tile, f);
-          if (!C::FP8 && (t + 1) * kKeys > it.ctx) {
-            row_bar();
-            // zero the value columns of the positions to clear (the tile's first product is done): a position
-            // past the end always, another one only if it holds something that is not finite
-            const uint32_t* mine = a->clear_own[tile & 1];
-            clear[0] |= mine[0] | mine[2];
-            clear[1] |= mine[1] | mine[3];
-            const int st = (h * 2 + (quarter & 1)) * 32 + lane, key = st >> 1;  // a position, two of its four boxes
-            if ((clear[key >> 5] >> (key & 31)) & 1) {
-              for (int b = 2 * (st & 1); b < 2 * (st & 1) + 2; ++b) {
-                uint8_t* line = tiles_s + (tile % C::STAGES) * kTile + b * kBox + key * 128;
-                bool zero = t * kKeys + key >= it.len;
-                if (!zero) {
 #pragma unroll
-                  for (int c = 0; c < 8; ++c) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(line + 16 * c);
-                    const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                      zero |= (ws[q] & 0x7F80u) == 0x7F80u || (ws[q] & 0x7F800000u) == 0x7F800000u;
-                  }
-                }
-                if (zero) {
-#pragma unroll
-                  for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(line + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
-                }
-              }
-            }
-          }
-          fence_proxy_async_smem();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (warp == (rank ? 4 : 6)) mbar_arrive_expect_tx(&a->p_msg[pb], C::MSG_BYTES);  // for this buffer's next use
-            mbar_arrive(&a->p_full[tile & 1]);
-          }
+        for (int pc = 0; pc < C::PC; ++pc) {
+          put(p_s + (pb * C::PC + pc) * C::P_BYTES + rank * C::P_HALF, C::TILED ? 2 * rank + pc : 0);
+          if (C::TILED) put(pp_s + pc * C::P_HALF, 2 * (rank ^ 1) + pc);  // the scales of the other's value tiles
         }
-        ok = wait_cluster(a, &a->stat_full, items & 1, err) && ok;
-        l = a->stat[r64];
-        row_bar();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (ok) {
+#pragma unroll
+            for (int pc = 0; pc < C::PC; ++pc)
+              copy_remote(peer_p + (pb * C::PC + pc) * C::P_BYTES,
+                          (C::TILED ? pp_s + pc * C::P_HALF : p_s + pb * C::P_BYTES + rank * C::P_HALF) + 32 * quarter * 64,
+                          32 * 64, peer_pm + 8 * pb);
+            copy_commit();
+          }
+          if (quarter == 0) mbar_arrive_expect_tx(&a->m_msg[tile & 3], kMaxBytes);  // for the tile four on
+          if constexpr (C::FP8) mbar_arrive(&a->sc_empty[tile % C::SC_DEPTH]);
+          mbar_arrive(&a->p_full[tile & 1]);
+        }
+        if (more) {
+          if (!staged) stage(tile + 1, t + 1, y, my);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = y[k];
+          mx = my;
+        }
       }
-      // ---- the item's outputs
-      if (own) row_bar();
-      if (!own && lane == 0 && warp == (rank ? 4 : 6)) mbar_arrive_expect_tx(&a->stat_full, 64 * 4);
+      // ---- the item's sums, to the other CTA as well
+      if (ok) st_async4(peer_stat, __float_as_uint(l), peer_sf);
+      ok = wait_cluster(a, &a->stat_full, items & 1, err) && ok;
+      // (added in the same order on both sides)
+      l = rank ? a->stat[row] + l : l + a->stat[row];
+      softmax_bar();
+      if (st == 0) mbar_arrive_expect_tx(&a->stat_full, kRows * 4);
       const bool live = row < nrows && (row_lo + row) / p.H < it.fresh;
       const float inv = live && l != 0.f ? 1.f / l : 0.f;
+      if (rank == 0) {
+        if (it.slot >= 0) pl.part_ml[(int64_t)it.slot * kRows + row] = make_float2(m, l);
+        else if (p.lse && row < nrows) p.lse[at + row] = !live || l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
       ok = wait(a, &a->o_done, items & 1, err) && ok;
       tc_fence_after();
-      const int v0 = 256 * rank + 128 * h;
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
+      for (int c = 0; c < 256; c += 32) {
         float o[32];
-        tmem_ld_sync(lane_base + kColO + 128 * h + c, o);
+        tmem_ld_sync(lane_base + kColO + c, o);
         if (row < nrows && it.slot >= 0) {
-          float4* dst = pl.part_o + ((int64_t)it.slot * (kDv / 4) + (v0 + c) / 4) * kRows + row;
+          float4* dst = pl.part_o + ((int64_t)it.slot * (kDv / 4) + (256 * rank + c) / 4) * kRows + row;
 #pragma unroll
           for (int k = 0; k < 8; ++k) dst[k * kRows] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         } else if (row < nrows) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + (at + row) * kDv + v0 + c);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + (at + row) * kDv + 256 * rank + c);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t y[4];
+            uint32_t w[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              y[q] = live ? pack_bf16(o[8 * k + 2 * q] * inv, o[8 * k + 2 * q + 1] * inv) : 0u;
-            dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
+              w[q] = live ? pack_bf16(o[8 * k + 2 * q] * inv, o[8 * k + 2 * q + 1] * inv) : 0u;
+            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
         __syncwarp();
@@ -1177,7 +1128,7 @@ cudaError_t launch_fmt(const TreeAttnParams& p, TreePlan pl, void* ws, cudaStrea
                                  paged || p.n_seq == 1 ? n * (cuuint64_t)p.kv_row_stride : (cuuint64_t)p.kv_seq_stride};
   CUtensorMap tm;
   memset(&tm, 0, sizeof(tm));
-  const cuuint32_t box[3] = {64, (cuuint32_t)kKeys, 1};
+  const cuuint32_t box[3] = {64, 32, 1};
   if (!C::FP8 && encode_tensor_map(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint8_t*>(p.kv), dims, strides, box,
                                    CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
