@@ -428,7 +428,7 @@ dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int wi
  * irrelevant; calls (and captured graphs) that share it must not run at the same time.
  * Supported: D_qk = 576, D_v = 512; kv_dtype DSA_BF16, DSA_FP8_E4M3 or DSA_FP8_E4M3_T128 (finite
  * codes); 1 <= H <= 128; 1 <= q_per_seq <= 1024; n_seq <= 4096; L <= 2^31 - 4097; pointers 16-byte aligned, row
- * strides multiples of 16 bytes.
+ * strides multiples of 16 bytes, rows at most 2^24 bytes apart.
  * ------------------------------------------------------------------------------------------ */
 typedef struct dsa_tree_args {
   int n_seq, q_per_seq, L, H, D_qk, D_v;

@@ -6,7 +6,7 @@
 // A "row" is one head of one node; the rows of a sequence are consecutive in q and share its cache.
 // A cluster of two CTAs takes 128 rows and walks tiles of 64 positions.  CTA c takes the first product
 // and the softmax of 32 of the positions, and the second product of half of the value columns:
-//   * S[128 x 32] = Q K_c^T: A = the rows (M = 128; 384 of their columns in tensor memory, 192 in shared
+//   * S[128 x 32] = Q K_c^T: A = the rows (M = 128; 448 of their columns in tensor memory, 128 in shared
 //     memory), B = its 32 positions (K-major), 36 steps of K = 16;
 //   * one pass over the positions keeps a reference maximum m and a sum l per row,
 //       l' = l 2^(m - m') + sum_p 2^(x_p - m'),   o' = o 2^(m - m') + sum_p 2^(x_p - m') v_p,
@@ -18,7 +18,7 @@
 //     (values along N), 4 steps of K = 16 with N = 256.  A CTA's own positions are in shared memory whole, of
 //     the other's only these 256 columns are loaded besides: 832 of 1152 bytes per position and CTA.
 // Why two CTAs: o for 128 rows x 512 values fills a tensor memory (512 columns), which leaves no room for S;
-// with half of the values it takes 256 columns, q 192, two S buffers 64.  Measured against it (8 x 64 nodes
+// with half of the values it takes 256 columns, q 224, S 32.  Measured against it (8 x 64 nodes
 // at 32K, E4M3 rows; 8 x 8 nodes at 32K, bf16): one CTA with 64 rows, q in shared memory and o
 // transposed, 1805 and 149 us (245 KB of shared memory read per tile by the MMAs, room for two tiles);
 // columns of the rows split between the CTAs, whose partial S then travel, 1090 and 120 us (16 to 32 KB
@@ -28,9 +28,9 @@
 // outputs are fp32.  E4M3 rows are widened to bf16 exactly, and their scales are applied in fp32 to the
 // logit and to the weight (128-column scales: one S accumulation per scale tile, one P per value tile).
 //
-// Warp roles: producer (TMA), MMA issuer, scale loader, credits of the exchange, four softmax warps (a row per
-// thread; also the query load, the rescale and the epilogue), for E4M3 eight warps that load, widen and
-// store the tile.
+// Warp roles: producer (TMA), MMA issuer, scale loader, credits of the exchange, eight softmax warps (a row and
+// 16 positions per thread; also the query load, the rescale and the epilogue), for E4M3 eight warps that
+// load, widen and store the tile.
 //
 // Work split: items (sequence, chunk of its tiles, row tile), in this order, so that clusters that run
 // together read the same positions and the cache comes from HBM once.  The lengths are on the device:
@@ -48,14 +48,13 @@ constexpr int kDqk = 576, kDv = 512;
 constexpr int kRows = 128;                // query rows per cluster
 constexpr int kKeys = 64;                 // positions per tile, half of them per CTA
 constexpr int kBox = 32 * 128;            // 64 columns of 32 positions: 32 rows x 128 bytes
-constexpr int kSlotV = 8 * kBox;          // this CTA's value columns: its positions (4 boxes), the other's (4)
+constexpr int kSlotV = 4 * kBox;          // a CTA's value columns of 32 positions (its own, or the other's)
 constexpr int kSlotK = 5 * kBox;          // the other columns of its positions: 4 boxes of values, the rotary one
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLazy = 8.f;              // log2 growth of a row's maximum that is left unscaled
 constexpr int kItemsPerCta = 3;           // split launches are cut into at most this many items per cluster
-// tensor-memory columns: O, six of the nine 64-column boxes of q, two S buffers
-constexpr int kColO = 0, kColQ = 256, kColS = 448;
-constexpr int kBoxesT = 6;                // q's boxes in tensor memory (the others are in shared memory)
+// tensor-memory columns: O, seven (six) of the nine 64-column boxes of q, one S buffer (two)
+constexpr int kColO = 0, kColQ = 256;
 
 enum { kBf16 = 0, kFp8Row = 1, kFp8Tile = 2 };
 
@@ -64,19 +63,25 @@ struct Cfg {
   static constexpr bool FP8 = FMT != kBf16;
   static constexpr int NSC = FMT == kFp8Tile ? 5 : FMT == kFp8Row ? 1 : 0;
   static constexpr bool TILED = FMT == kFp8Tile;
-  static constexpr int THREADS = FP8 ? 512 : 256;
-  static constexpr int VS = TILED ? 2 : 3, KS = 2;        // slots of both kinds
+  static constexpr int THREADS = FP8 ? 640 : 384;
+  // slots: our positions' value columns (held from the first product to the second), their other columns (first
+  // product only), the other's positions (second product only)
+  static constexpr int AS = TILED ? 3 : 4, KS = 2, BS = TILED ? 2 : 3;
+  static constexpr int BT = TILED ? 6 : 7;                // q's boxes in tensor memory (the others are in shared memory)
+  static constexpr int SB = TILED ? 2 : 1;                // S buffers
+  static constexpr int PB = TILED ? 1 : 2;                // P buffers
+  static constexpr int COL_S = kColQ + 32 * BT;
   static constexpr int GROUPS = TILED ? 5 : 1;            // S accumulations per tile
   static constexpr int PC = TILED ? 2 : 1;                // copies of P (one per 128 values)
-  static constexpr int PB = TILED ? 1 : 2;                // P buffers
   static constexpr int SC_DEPTH = 2;
   static constexpr int SC_BYTES = NSC * 32 * 4;           // scales of this CTA's positions
-  static constexpr int Q_BOX = kRows * 128, Q_BYTES = (9 - kBoxesT) * Q_BOX;
+  static constexpr int Q_BOX = kRows * 128, Q_BYTES = (9 - BT) * Q_BOX;
   static constexpr int P_HALF = kRows * 64;               // 128 rows x 32 positions
   static constexpr int P_BYTES = 2 * P_HALF;
   static constexpr int PP_BYTES = TILED ? PC * P_HALF : 0;  // with tile scales: the other's copies of our P, on their way
-  static constexpr int AUX = 4096;
-  static constexpr int OFF_K = VS * kSlotV;
+  static constexpr int AUX = 8192;
+  static constexpr int OFF_B = AS * kSlotV;
+  static constexpr int OFF_K = OFF_B + BS * kSlotV;
   static constexpr int OFF_Q = OFF_K + KS * kSlotK;
   static constexpr int OFF_P = OFF_Q + Q_BYTES;
   static constexpr int OFF_PP = OFF_P + PB * PC * P_BYTES;
@@ -114,20 +119,22 @@ __device__ __forceinline__ int live_row_tiles(const TreeAttnParams& p, int fresh
 }
 
 struct Aux {
-  uint64_t v_full[3], v_empty[3], k_full[2], k_empty[2];
+  uint64_t a_full[4], a_empty[4], b_full[3], b_empty[3], k_full[2], k_empty[2];
   uint64_t s_full[2], s_empty[2], m_msg[4], p_full[2], p_msg[2], p_free[2], pv_done[2];
   uint64_t stat_full, o_done, o_free, q_full, sc_full[2], sc_empty[2], drain;
   uint32_t tmem;
   int abort;
   int n_items;
-  int tile_bad[4];
+  int tile_bad[8];
   int items[kItemsPerCta][8];
-  alignas(16) float mx[4][kRows];  // the other's maxima over its positions, by tile % 4
-  uint32_t clear[4][4];            // positions of the other's to clear (per warp of rows)
-  uint32_t clear_own[4][4];        // and of ours
-  float stat[kRows];               // the other's sums
+  // each half's maxima over its 16 positions, ours (by tile % 2; at an item's end its sums) and the other CTA's (by
+  // tile % 4), and the positions to clear
+  alignas(16) float mx_own[2][2][kRows];
+  alignas(16) float mx[4][2][kRows];
+  uint32_t clear_own[4][8], clear[4][8];
+  float stat[2][kRows];  // the other's sums, by half
 };
-static_assert(sizeof(Aux) <= 4096, "Aux");
+static_assert(sizeof(Aux) <= 8192, "Aux");
 
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -141,9 +148,10 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// A bounded wait.  Once one wait of the CTA has run out, the others return at once: the warps then walk
-// through the rest of their work without waiting (every address stays in range), so that their common
-// barriers still match, and the kernel ends.
+// A bounded wait.  Once one wait of the CTA has run out, the others return at once: the softmax warps then walk
+// through the rest of their work (every address stays in range), so that their common barriers still match; the
+// other roles leave.  A thread whose wait failed arrives on no mbarrier, arms none and sends nothing any more: an
+// arrival is only legal in a phase that the arriving thread has seen begin.
 __device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err, bool cluster);
 __device__ __forceinline__ bool wait(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
   return mbar_test(bar, parity) || wait_slow(a, bar, parity, err, false);
@@ -160,7 +168,7 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_cluster(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
+__device__ __forceinline__ bool test_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred P;\n\t"
@@ -169,7 +177,10 @@ __device__ __forceinline__ bool wait_cluster(Aux* a, uint64_t* bar, uint32_t par
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
-  return ok || wait_slow(a, bar, parity, err, true);
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
+  return test_cluster(bar, parity) || wait_slow(a, bar, parity, err, true);
 }
 __device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err, bool cluster) {
   const unsigned long long t0 = globaltimer_ns();
@@ -204,7 +215,15 @@ __device__ __forceinline__ void st_async4(uint32_t addr, uint32_t v, uint32_t ba
                : "memory");
 }
 
-__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Barriers of the eight softmax warps, and of the two that share 32 rows (ids 2 to 5).
+__device__ __forceinline__ void softmax_bar() {
+  __syncwarp();
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+__device__ __forceinline__ void pair_bar(int quarter) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory");
+}
 
 // A value that is the same in all lanes, as one the compiler knows to be so (a warp-wide reduction writes
 // a uniform register): the MMA issuer's loop bounds and addresses go through it, because operands in
@@ -424,7 +443,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
   using C = Cfg<FMT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* v_s = smem;
+  uint8_t* a_s = smem;
+  uint8_t* b_s = smem + C::OFF_B;
   uint8_t* k_s = smem + C::OFF_K;
   uint8_t* q_s = smem + C::OFF_Q;
   uint8_t* p_s = smem + C::OFF_P;
@@ -439,30 +459,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
     tmem_alloc(&a->tmem, 512);
     tmem_relinquish();
   }
-  constexpr uint32_t kMaxBytes = kRows * 4 + 4 * 4;  // a tile's maxima and clear words
+  constexpr uint32_t kMaxBytes = 2 * kRows * 4 + 8 * 4;  // a tile's maxima and clear words
   constexpr uint32_t kPBytes = C::PC * C::P_HALF;    // a tile's P from the other CTA
   if (tid == 32) {
     const int fillers = C::FP8 ? 8 : 1;  // arrivals that fill a slot: converter warps, or the TMA's thread
-    for (int i = 0; i < 3; ++i) mbar_init(&a->v_full[i], fillers), mbar_init(&a->v_empty[i], 1);
+    for (int i = 0; i < C::AS; ++i) mbar_init(&a->a_full[i], fillers), mbar_init(&a->a_empty[i], 1);
+    for (int i = 0; i < C::BS; ++i) mbar_init(&a->b_full[i], fillers), mbar_init(&a->b_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&a->k_full[i], fillers), mbar_init(&a->k_empty[i], 1);
-      mbar_init(&a->s_full[i], 1), mbar_init(&a->s_empty[i], 4);
-      mbar_init(&a->p_full[i], 4), mbar_init(&a->p_msg[i], 1), mbar_init(&a->p_free[i], 1), mbar_init(&a->pv_done[i], 1);
-      mbar_init(&a->sc_full[i], 32), mbar_init(&a->sc_empty[i], 4);
+      mbar_init(&a->s_full[i], 1), mbar_init(&a->s_empty[i], 8);
+      mbar_init(&a->p_full[i], 8), mbar_init(&a->p_msg[i], 1), mbar_init(&a->p_free[i], 1), mbar_init(&a->pv_done[i], 1);
+      mbar_init(&a->sc_full[i], 32), mbar_init(&a->sc_empty[i], 8);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&a->m_msg[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&a->m_msg[i], 9);
     mbar_init(&a->stat_full, 1);
     mbar_init(&a->o_done, 1);
-    mbar_init(&a->o_free, 4);
-    mbar_init(&a->q_full, 128);
+    mbar_init(&a->o_free, 8);
+    mbar_init(&a->q_full, 256);
     mbar_init(&a->drain, 1);
     a->abort = 0;
     fence_mbar_init();
     for (int i = 0; i < 4; ++i) mbar_arrive_expect_tx(&a->m_msg[i], kMaxBytes);
     for (int i = 0; i < C::PB; ++i) mbar_arrive_expect_tx(&a->p_msg[i], kPBytes);
-    mbar_arrive_expect_tx(&a->stat_full, kRows * 4);
+    mbar_arrive_expect_tx(&a->stat_full, 2 * kRows * 4);
   }
-  if (pl.cap) plan_items(p, pl, a, reinterpret_cast<int*>(v_s));
+  if (pl.cap) plan_items(p, pl, a, reinterpret_cast<int*>(a_s));
   fence_proxy_async_smem();  // the plan's scratch is a slot that the copies write
   tc_fence_before();
   __syncthreads();
@@ -476,7 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
     // ---- producer (bf16): boxes of 64 columns x 32 positions by TMA
     if (lane == 0 && !C::FP8) {
       prefetch_tmap(&tm);
-      int vs = 0, vph = 0, ks = 0, kph = 0, tiles = 0;
+      int as = 0, aph = 0, bs = 0, bph = 0, ks = 0, kph = 0, tiles = 0;
       bool ok = true;
       for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
         for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
@@ -490,16 +511,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
             if (bad) record_error(err, DSA_DEVERR_INDEX_RANGE);
           }
           const int mine = row + 32 * rank, other = row + 32 * (rank ^ 1);
-          ok = wait(a, &a->v_empty[vs], vph ^ 1, err);
+          ok = wait(a, &a->a_empty[as], aph ^ 1, err);
           if (!ok) break;
-          a->tile_bad[tiles & 3] = bad;
-          uint8_t* dst = v_s + vs * kSlotV;
-          mbar_arrive_expect_tx(&a->v_full[vs], kSlotV);
+          a->tile_bad[tiles & 7] = bad;
+          uint8_t* dst = a_s + as * kSlotV;
+          mbar_arrive_expect_tx(&a->a_full[as], kSlotV);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) tma_load_3d(dst + b * kBox, &tm, &a->v_full[vs], 256 * rank + 64 * b, mine, z);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) tma_load_3d(dst + (4 + b) * kBox, &tm, &a->v_full[vs], 256 * rank + 64 * b, other, z);
-          if (++vs == C::VS) vs = 0, vph ^= 1;
+          for (int b = 0; b < 4; ++b) tma_load_3d(dst + b * kBox, &tm, &a->a_full[as], 256 * rank + 64 * b, mine, z);
+          if (++as == C::AS) as = 0, aph ^= 1;
           ok = wait(a, &a->k_empty[ks], kph ^ 1, err);
           if (!ok) break;
           dst = k_s + ks * kSlotK;
@@ -508,10 +527,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
           for (int b = 0; b < 4; ++b) tma_load_3d(dst + b * kBox, &tm, &a->k_full[ks], 256 * (rank ^ 1) + 64 * b, mine, z);
           tma_load_3d(dst + 4 * kBox, &tm, &a->k_full[ks], 512, mine, z);
           if (++ks == C::KS) ks = 0, kph ^= 1;
+          ok = wait(a, &a->b_empty[bs], bph ^ 1, err);
+          if (!ok) break;
+          dst = b_s + bs * kSlotV;
+          mbar_arrive_expect_tx(&a->b_full[bs], kSlotV);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) tma_load_3d(dst + b * kBox, &tm, &a->b_full[bs], 256 * rank + 64 * b, other, z);
+          if (++bs == C::BS) bs = 0, bph ^= 1;
         }
       }
       if (*reinterpret_cast<volatile int*>(&a->abort)) {  // wind down: the copies in flight land first
-        for (int s = 0; s < C::VS; ++s) mbar_wait(&a->v_full[s], s < vs ? vph : vph ^ 1, err);
+        for (int s = 0; s < C::AS; ++s) mbar_wait(&a->a_full[s], s < as ? aph : aph ^ 1, err);
+        for (int s = 0; s < C::BS; ++s) mbar_wait(&a->b_full[s], s < bs ? bph : bph ^ 1, err);
         for (int s = 0; s < C::KS; ++s) mbar_wait(&a->k_full[s], s < ks ? kph : kph ^ 1, err);
       }
     }
@@ -523,14 +550,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
     constexpr uint32_t idesc_qk = make_idesc(1, 1, kRows, 32);
     constexpr uint32_t idesc_pv = make_idesc(1, 1, kRows, C::TILED ? 128 : 256) | (1u << 16);  // B (values) MN-major
     const uint32_t tm_base = (uint32_t)uniform((int)tmem);
-    const uint32_t kv_lo = kmajor_lo(smem_u32(v_s)), kk_lo = kmajor_lo(smem_u32(k_s)), v_lo = mnmajor_lo(smem_u32(v_s));
+    const uint32_t ka_lo = kmajor_lo(smem_u32(a_s)), kk_lo = kmajor_lo(smem_u32(k_s));
+    const uint32_t va_lo = mnmajor_lo(smem_u32(a_s)), vb_lo = mnmajor_lo(smem_u32(b_s));
     const uint32_t q_lo = kmajor_lo(smem_u32(q_s)), p_lo = kmajor_lo(smem_u32(p_s));
-    int vs = 0, vph = 0, ks = 0, kph = 0;  // slots of the first product
-    int ps = 0;                            // value slot of the second
+    int as = 0, aph = 0, ks = 0, kph = 0;  // slots of the first product
+    int ps = 0, bs = 0, bph = 0;           // of the second
     int tile = 0, items = 0;
     uint32_t su = 0;                       // uses of the S buffers
     bool ok = true;
-    auto all = [&](uint64_t* bar, uint32_t parity) { ok = __all_sync(0xffffffffu, wait(a, bar, parity, err)) && ok; };
     auto commit = [&](uint64_t* bar) {
       if (elect_one()) tc_commit(bar);
       __syncwarp();
@@ -540,53 +567,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t acc = first && k == 0 ? 0u : 1u;
-        if (j < kBoxesT) mma_ts(d, tm_base + kColQ + 32 * j + 8 * k, B + 2 * k, idesc_qk, acc);
-        else mma_ss(d, q_lo + (j - kBoxesT) * (C::Q_BOX >> 4) + 2 * k, B + 2 * k, idesc_qk, acc);
+        if (j < C::BT) mma_ts(d, tm_base + kColQ + 32 * j + 8 * k, B + 2 * k, idesc_qk, acc);
+        else mma_ss(d, q_lo + (j - C::BT) * (C::Q_BOX >> 4) + 2 * k, B + 2 * k, idesc_qk, acc);
       }
     };
-    // First product of the next tile; with tile scales one accumulation (pair of boxes) after another through
-    // the S buffers.  The softmax warps have read what a buffer held.
-    auto qk_tile = [&]() {
-      all(&a->v_full[vs], vph);
-      all(&a->k_full[ks], kph);
-      const uint32_t V = kv_lo + vs * (kSlotV >> 4), K = kk_lo + ks * (kSlotK >> 4);
-#pragma unroll 1
-      for (int g = 0; g < C::GROUPS; ++g, ++su) {
-        all(&a->s_empty[su & 1], ((su >> 1) & 1) ^ 1);
-        tc_fence_after();
-        const uint32_t d = tm_base + kColS + 32 * (su & 1);
-        if (elect_one()) {
-          if (C::TILED) {
-            if (g < 4) {
-              const uint32_t B = ((g >> 1) == rank ? V : K) + (2 * (g & 1) * kBox >> 4);
-              if (g < 3) {
+    auto test = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)); };
+    // First product, one accumulation: the whole tile, or with tile scales a pair of boxes (g) after another
+    // through the S buffers.  The softmax warps have read what the buffer held.
+    auto qk_ready = [&](int g) {
+      return test(&a->s_empty[su % C::SB], ((su / C::SB) & 1) ^ 1) &&
+             (g > 0 || (test(&a->a_full[as], aph) && test(&a->k_full[ks], kph)));
+    };
+    auto qk = [&](int g) {
+      const uint32_t V = ka_lo + as * (kSlotV >> 4), K = kk_lo + ks * (kSlotK >> 4);
+      const uint32_t d = tm_base + C::COL_S + 32 * (su % C::SB);
+      const bool last = g == C::GROUPS - 1;
+      tc_fence_after();
+      if (elect_one()) {
+        if (C::TILED) {
+          if (g < 4) {
+            const uint32_t B = ((g >> 1) == rank ? V : K) + (2 * (g & 1) * kBox >> 4);
+            if (g < 3) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  mma_ts(d, tm_base + kColQ + 64 * g + 8 * k, B + ((k >> 2) * kBox + 32 * (k & 3)) / 16, idesc_qk, k ? 1u : 0u);
-              } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  mma_ss(d, q_lo + ((k >> 2) * C::Q_BOX + 32 * (k & 3)) / 16, B + ((k >> 2) * kBox + 32 * (k & 3)) / 16, idesc_qk,
-                         k ? 1u : 0u);
-              }
+              for (int k = 0; k < 8; ++k)
+                mma_ts(d, tm_base + kColQ + 64 * g + 8 * k, B + ((k >> 2) * kBox + 32 * (k & 3)) / 16, idesc_qk, k ? 1u : 0u);
             } else {
-              qk_box(d, 8, K + (4 * kBox >> 4), true);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mma_ss(d, q_lo + ((k >> 2) * C::Q_BOX + 32 * (k & 3)) / 16, B + ((k >> 2) * kBox + 32 * (k & 3)) / 16, idesc_qk,
+                       k ? 1u : 0u);
             }
           } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) qk_box(d, j, ((j >> 2) == rank ? V : K) + ((j & 3) * kBox >> 4), j == 0);
-            qk_box(d, 8, K + (4 * kBox >> 4), false);
+            qk_box(d, 8, K + (4 * kBox >> 4), true);
           }
-          tc_commit(&a->s_full[su & 1]);
-          if (g == C::GROUPS - 1) tc_commit(&a->k_empty[ks]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) qk_box(d, j, ((j >> 2) == rank ? V : K) + ((j & 3) * kBox >> 4), j == 0);
+          qk_box(d, 8, K + (4 * kBox >> 4), false);
         }
-        __syncwarp();
+        tc_commit(&a->s_full[su % C::SB]);
+        if (last) tc_commit(&a->k_empty[ks]);
       }
-      if (++vs == C::VS) vs = 0, vph ^= 1;
-      if (++ks == C::KS) ks = 0, kph ^= 1;
+      __syncwarp();
+      ++su;
+      if (last) {
+        if (++as == C::AS) as = 0, aph ^= 1;
+        if (++ks == C::KS) ks = 0, kph ^= 1;
+      }
+    };
+    // Second product of a tile: its weights from both CTAs, and the other's positions, are there.
+    auto pv_ready = [&](bool first) {
+      const int pb = tile % C::PB;
+      return test(&a->p_full[tile & 1], (tile >> 1) & 1) &&
+             __all_sync(0xffffffffu, test_cluster(&a->p_msg[pb], (tile / C::PB) & 1)) && test(&a->b_full[bs], bph) &&
+             (!first || test(&a->o_free, (items & 1) ^ 1));
     };
     auto pv = [&](bool first) {
-      const uint32_t acc0 = first ? 0u : 1u, V = v_lo + ps * (kSlotV >> 4);
+      if (lane == 0) mbar_arrive_expect_tx(&a->p_msg[tile % C::PB], kPBytes);  // for this buffer's next use
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t acc0 = first ? 0u : 1u, A = va_lo + ps * (kSlotV >> 4), B = vb_lo + bs * (kSlotV >> 4);
       const uint32_t P = p_lo + (tile % C::PB) * (C::PC * C::P_BYTES >> 4);
       if (elect_one()) {
         constexpr int NB = C::TILED ? 2 : 1;  // value tiles of N = 128 with a P each, or all 256 at once
@@ -596,45 +636,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
           for (int s = 0; s < 4; ++s) {  // two steps over this CTA's positions, two over the other's
             const uint32_t half = (uint32_t)((s >> 1) ^ rank);  // whose P: the halves of the buffer are by CTA
             mma_ss<kDescHi64>(tm_base + kColO + 128 * b, P + (b * C::P_BYTES >> 4) + half * (C::P_HALF >> 4) + 2 * (s & 1),
-                              V + ((4 * (s >> 1) + 2 * b) * kBox + 2048 * (s & 1)) / 16, idesc_pv, s ? 1u : acc0);
+                              (s < 2 ? A : B) + (2 * b * kBox + 2048 * (s & 1)) / 16, idesc_pv, s ? 1u : acc0);
           }
-        tc_commit(&a->v_empty[ps]);
+        tc_commit(&a->a_empty[ps]);
+        tc_commit(&a->b_empty[bs]);
         tc_commit(&a->pv_done[tile & 1]);
       }
       __syncwarp();
-      if (++ps == C::VS) ps = 0;
+      if (++ps == C::AS) ps = 0;
+      if (++bs == C::BS) bs = 0, bph ^= 1;
     };
-    constexpr int AHEAD = C::TILED ? 1 : 2;  // tiles whose first product is issued before P of this one is there
-    for (int i = 0; uniform(get_item(p, pl, a, i, it)); ++i) {
+    for (int i = 0; ok && uniform(get_item(p, pl, a, i, it)); ++i) {
       const int t0 = uniform(it.t0), t1 = uniform(it.t1);
       if (t0 >= t1) continue;
-      all(&a->q_full, items & 1);
-      tc_fence_after();
-      int tq = t0;  // the next tile to start
-      for (; tq < t1 && tq < t0 + AHEAD; ++tq) qk_tile();
-      for (int t = t0; t < t1; ++t, ++tile) {
-        // the tile after next early, if it and its S buffer are ready; P of this one first otherwise
-        bool started = tq >= t1;
-        if (!started && (C::TILED || __all_sync(0xffffffffu, mbar_test(&a->v_full[vs], vph) && mbar_test(&a->k_full[ks], kph) &&
-                                                                 mbar_test(&a->s_empty[su & 1], ((su >> 1) & 1) ^ 1)))) {
-          qk_tile();
-          ++tq;
-          started = true;
+      ok = __all_sync(0xffffffffu, wait(a, &a->q_full, items & 1, err));
+      // whichever product can go: the first one runs ahead as far as S buffers and slots allow
+      int t = t0, n = t0, g = 0;  // next tile of the second product; of the first, and its accumulation
+      unsigned long long since = 0;
+      for (uint32_t idle = 0; ok && t < t1;) {
+        if (idle++ == 0) since = 0;
+        if (n < t1 && qk_ready(g)) {
+          qk(g);
+          if (++g == C::GROUPS) g = 0, ++n;
+          idle = 0;
         }
-        const int pb = tile % C::PB;
-        all(&a->p_full[tile & 1], (tile >> 1) & 1);
-        ok = __all_sync(0xffffffffu, wait_cluster(a, &a->p_msg[pb], (tile / C::PB) & 1, err)) && ok;
-        if (lane == 0) mbar_arrive_expect_tx(&a->p_msg[pb], kPBytes);  // for this buffer's next use
-        if (t == t0) all(&a->o_free, (items & 1) ^ 1);
-        __syncwarp();
-        tc_fence_after();
-        pv(t == t0);
-        if (!started) {
-          qk_tile();
-          ++tq;
+        if (t < n && pv_ready(t == t0)) {
+          pv(t == t0);
+          ++t, ++tile;
+          idle = 0;
+        }
+        if ((idle & 255u) == 255u) {  // a bounded wait, as the others
+          const unsigned long long now = globaltimer_ns();
+          if (since == 0) since = now;
+          const bool late = now - since > kWaitLimitNs;
+          if (__any_sync(0xffffffffu, late) && !*reinterpret_cast<volatile int*>(&a->abort)) {
+            record_error(err, DSA_DEVERR_WAIT_TIMEOUT);
+            *reinterpret_cast<volatile int*>(&a->abort) = 1;
+          }
+          ok = !__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&a->abort));
         }
       }
-      commit(&a->o_done);
+      if (ok) commit(&a->o_done);
       ++items;
     }
     if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&a->abort))) {
@@ -659,9 +701,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         ok = __all_sync(0xffffffffu, wait(a, &a->sc_empty[d], ((tiles / C::SC_DEPTH) & 1) ^ 1, err));
         if (!ok) break;
 #pragma unroll
-        for (int k = 0; k < C::NSC; ++k) sc_s[d * 32 * C::NSC + lane + 32 * k] = v[k];
+        for (int k = 0; k < C::NSC; ++k) {
+          const int e = lane + 32 * k, key = e / (C::NSC + !C::NSC);
+          sc_s[(d * C::NSC + e - key * C::NSC) * 32 + key] = v[k];  // [scale of the row][position]
+        }
         if (lane == 0) {
-          a->tile_bad[tiles & 3] = bad;
+          a->tile_bad[tiles & 7] = bad;
           if (bad) record_error(err, DSA_DEVERR_INDEX_RANGE);
         }
         __syncwarp();
@@ -681,13 +726,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         __syncwarp();
       }
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 12) {
     // ---- converters (E4M3): 16 codes per lane and step, loaded a tile ahead, widened into the swizzled bf16
     // boxes.  Eight lanes take four 16-code chunks of one box from two neighbouring positions: their eight
     // 16-byte stores fall into different banks.  A warp takes one pair of positions of each group of 8 pairs:
     // step k < 4: box k of our value columns, ours; < 8: the other's positions; < 12: our other columns; 12: rotary.
-    const int cw = warp - 8;
-    int vs = 0, vph = 0, ks = 0, kph = 0;
+    const int cw = warp - 12;
+    int as = 0, aph = 0, bs = 0, bph = 0, ks = 0, kph = 0;
     bool ok = true;
     constexpr int STEPS = 7;  // two boxes per step (lanes 0-15, 16-31), the rotary one alone
     uint4 raw[STEPS];
@@ -703,20 +748,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
       if (row < 0) return nullptr;
       return p.kv + (p.pages.table ? 0 : (int64_t)x.seq * p.kv_seq_stride) + row * p.kv_row_stride;
     };
-    auto fetch = [&](const uint8_t* r, int n, int k) {
+    // of this lane's chunk of step k: its position in the tile and its offset from the tile's first row (boxes 0-3:
+    // our value columns of our positions, 4-7: of the other's, 8-11: our positions' other columns, 12: rotary)
+    int off[STEPS];
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
       int box, key, c;
       place(k, box, key, c);
-      // boxes 0-3: our value columns of our positions, 4-7: of the other's, 8-11: our positions' other columns, 12
-      const int at = key + 32 * (box >= 4 && box < 8 ? rank ^ 1 : rank);
-      const int col = (box < 8 ? 256 * rank + 64 * (box & 3) : box < 12 ? 256 * (rank ^ 1) + 64 * (box & 3) : 512) + 16 * c;
-      raw[k] = r && at < n && box < 13 ? __ldg(reinterpret_cast<const uint4*>(r + (int64_t)at * p.kv_row_stride + col))
-                                       : make_uint4(0u, 0u, 0u, 0u);
+      const int pos = key + 32 * (box >= 4 && box < 8 ? rank ^ 1 : rank);
+      const int col = box < 8 ? 256 * rank + 64 * (box & 3) : box < 12 ? 256 * (rank ^ 1) + 64 * (box & 3) : 512;
+      off[k] = pos * (int)p.kv_row_stride + col + 16 * c;
+    }
+    const int at0 = 2 * cw + ((lane >> 2) & 1) + 16 * ((lane >> 3) & 1);
+    auto fetch = [&](const uint8_t* r, int n, int k) {
+      const bool other = k >= 2 && k < 4;
+      bool in = r != nullptr && (k < 6 || lane < 16);
+      if (n < kKeys) in = in && at0 + 32 * (other ? rank ^ 1 : rank) < n;
+      raw[k] = in ? __ldg(reinterpret_cast<const uint4*>(r + off[k])) : make_uint4(0u, 0u, 0u, 0u);
     };
-    auto store = [&](int k) {
+    auto store = [&](uint8_t* slot, int k) {
       int box, key, c;
       place(k, box, key, c);
       if (box >= 13) return;
-      uint8_t* d = (box < 8 ? v_s + vs * kSlotV + box * kBox : k_s + ks * kSlotK + (box - 8) * kBox) + key * 128;
+      uint8_t* d = slot + (k < 4 ? box & 3 : box - 8) * kBox + key * 128;
       const uint4 v = raw[k];
       *reinterpret_cast<uint4*>(d + (((2 * c) ^ (key & 7)) << 4)) =
           make_uint4(e4m3x2_to_bf16x2(v.x, 0x1404), e4m3x2_to_bf16x2(v.x, 0x3424), e4m3x2_to_bf16x2(v.y, 0x1404),
@@ -734,39 +788,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         r = r1;
         r1 = tile_rows(it, t + 2);
         const int n = it.len - (t + 1) * kKeys;
-        ok = __all_sync(0xffffffffu, wait(a, &a->v_empty[vs], vph ^ 1, err));
-        if (!ok) break;
+        // steps [k0, k1) into a slot
+        auto fill = [&](uint8_t* slot, int k0, int k1, uint64_t* full) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          store(k);
-          fetch(r, n, k);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&a->v_full[vs]);
-        if (++vs == C::VS) vs = 0, vph ^= 1;
+          for (int k = 0; k < STEPS; ++k) {
+            if (k >= k0 && k < k1) {
+              store(slot, k);
+              fetch(r, n, k);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+        };
+        ok = __all_sync(0xffffffffu, wait(a, &a->a_empty[as], aph ^ 1, err));
+        if (!ok) break;
+        fill(a_s + as * kSlotV, 0, 2, &a->a_full[as]);
+        if (++as == C::AS) as = 0, aph ^= 1;
         ok = __all_sync(0xffffffffu, wait(a, &a->k_empty[ks], kph ^ 1, err));
         if (!ok) break;
-#pragma unroll
-        for (int k = 4; k < STEPS; ++k) {
-          store(k);
-          fetch(r, n, k);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&a->k_full[ks]);
+        fill(k_s + ks * kSlotK, 4, STEPS, &a->k_full[ks]);
         if (++ks == C::KS) ks = 0, kph ^= 1;
+        ok = __all_sync(0xffffffffu, wait(a, &a->b_empty[bs], bph ^ 1, err));
+        if (!ok) break;
+        fill(b_s + bs * kSlotV, 2, 4, &a->b_full[bs]);
+        if (++bs == C::BS) bs = 0, bph ^= 1;
       }
     }
   } else if (warp >= 4) {
-    // ---- softmax warps: thread = row = tensor-memory lane, this CTA's 32 positions
-    const int quarter = warp - 4, row = 32 * quarter + lane, st = tid - 128;
+    // ---- softmax warps: thread = row = tensor-memory lane, half h of this CTA's 32 positions
+    const int w = warp - 4, h = w >> 2, quarter = w & 3, row = 32 * quarter + lane, st = tid - 128;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
-    const uint32_t peer_mx = dsmem_addr(&a->mx[0][row], rank ^ 1), peer_mm = dsmem_addr(&a->m_msg[0], rank ^ 1);
-    const uint32_t peer_clear = dsmem_addr(&a->clear[0][quarter], rank ^ 1);
+    const uint32_t peer_mx = dsmem_addr(&a->mx[0][h][row], rank ^ 1), peer_mm = dsmem_addr(&a->m_msg[0], rank ^ 1);
+    const uint32_t peer_clear = dsmem_addr(&a->clear[0][w], rank ^ 1);
     const uint32_t peer_p = dsmem_addr(p_s, rank ^ 1) + rank * C::P_HALF + 32 * quarter * 64;
     const uint32_t peer_pm = dsmem_addr(&a->p_msg[0], rank ^ 1);
-    const uint32_t peer_stat = dsmem_addr(&a->stat[row], rank ^ 1), peer_sf = dsmem_addr(&a->stat_full, rank ^ 1);
+    const uint32_t peer_stat = dsmem_addr(&a->stat[h][row], rank ^ 1), peer_sf = dsmem_addr(&a->stat_full, rank ^ 1);
+    const int p_at = row * 64, p_sw = (row >> 1) & 3;  // this row in a half of P, and its swizzle
     int tile = 0, items = 0;
     uint32_t su = 0;
     bool ok = true;
@@ -778,137 +836,151 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
       const int nrows = min(kRows, rows - row_lo);
       if (it.t0 >= it.t1) {  // nothing to see: padding nodes, or an empty sequence
         if (rank == 0) {
-          for (int k = st; k < nrows * (kDv / 8); k += 128)
+          for (int k = st; k < nrows * (kDv / 8); k += 256)
             reinterpret_cast<uint4*>(p.out + at * kDv)[k] = make_uint4(0u, 0u, 0u, 0u);
           if (p.lse && st < nrows) p.lse[at + st] = -INFINITY;
         }
         continue;
       }
-      // the query's row: 384 columns into tensor memory, 192 into shared memory (the previous item's products
-      // are done: its epilogue waited for them)
+      // the query's row: most boxes into tensor memory, the others into shared memory, half of them per half h
+      // (the previous item's products are done: its epilogue waited for them)
       {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (at + (row < nrows ? row : 0)) * kDqk);
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 4
-        for (int c = 0; c < 8 * (9 - kBoxesT); ++c)
-          cp_async16(q_s + (c >> 3) * C::Q_BOX + row * 128 + (((c & 7) ^ (row & 7)) << 4), src + 8 * kBoxesT + c, row < nrows);
+        for (int k = 0; k < 4 * (9 - C::BT); ++k) {
+          const int c = 2 * k + h;
+          cp_async16(q_s + (c >> 3) * C::Q_BOX + row * 128 + (((c & 7) ^ (row & 7)) << 4), src + 8 * C::BT + c, row < nrows);
+        }
         cp_async_commit();
-#pragma unroll 3
-        for (int g = 0; g < 2 * kBoxesT; ++g) {
+#pragma unroll 4
+        for (int g = 0; g < C::BT; ++g) {
           uint32_t v[16];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 u = row < nrows ? __ldg(src + 4 * g + k) : zero;
+            const uint4 u = row < nrows ? __ldg(src + 8 * g + 4 * h + k) : zero;
             v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
           }
-          tmem_st16(lane_base + kColQ + 16 * g, v);
+          tmem_st16(lane_base + kColQ + 32 * g + 16 * h, v);
         }
         cp_async_wait<0>();
         tmem_wait_st();
         tc_fence_before();
         fence_proxy_async_smem();
-        mbar_arrive(&a->q_full);
+        if (ok) mbar_arrive(&a->q_full);
       }
       const int node = min((row_lo + row) / p.H, p.q_per_seq - 1);
       float m = -INFINITY, l = 0.f;
 
-      // Logits of tile n (position tile t) for this row, scaled and masked; their maximum goes to the other CTA.
-      auto stage = [&](int n, int t, float (&x)[32], float& mx) {
-        const float* sc = sc_s + (n % C::SC_DEPTH) * 32 * C::NSC;
+      // Logits of tile n (position tile t) for this row, scaled and masked; their maximum goes to the other
+      // half's warp and to the other CTA.
+      auto stage = [&](int n, int t, float (&x)[16]) {
+        const float* sc = sc_s + (n % C::SC_DEPTH) * 32 * C::NSC + 16 * h;
         if constexpr (C::FP8) ok = wait(a, &a->sc_full[n % C::SC_DEPTH], (n / C::SC_DEPTH) & 1, err) && ok;
         if constexpr (C::TILED) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = 0.f;
+          for (int k = 0; k < 16; ++k) x[k] = 0.f;
         }
 #pragma unroll 1
         for (int g = 0; g < C::GROUPS; ++g, ++su) {
-          ok = wait(a, &a->s_full[su & 1], (su >> 1) & 1, err) && ok;
+          ok = wait(a, &a->s_full[su % C::SB], (su / C::SB) & 1, err) && ok;
           tc_fence_after();
-          float s[32];
-          tmem_ld_sync(lane_base + kColS + 32 * (su & 1), s);
+          float s[16];
+          tmem_ld_sync(lane_base + C::COL_S + 32 * (su % C::SB) + 16 * h, s);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&a->s_empty[su & 1]);
+          if (lane == 0 && ok) mbar_arrive(&a->s_empty[su % C::SB]);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            if constexpr (C::TILED) x[k] = fmaf(sc[5 * k + g], s[k], x[k]);
-            else if constexpr (C::FP8) x[k] = s[k] * sc[k] * p.scale_log2;
-            else x[k] = s[k] * p.scale_log2;
+          for (int k = 0; k < 16; k += 4) {
+            float4 f = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+            if constexpr (C::FP8) f = *reinterpret_cast<const float4*>(sc + 32 * g + k);
+            if constexpr (C::TILED) {
+              x[k] = fmaf(f.x, s[k], x[k]), x[k + 1] = fmaf(f.y, s[k + 1], x[k + 1]);
+              x[k + 2] = fmaf(f.z, s[k + 2], x[k + 2]), x[k + 3] = fmaf(f.w, s[k + 3], x[k + 3]);
+            } else {
+              if constexpr (C::FP8) f.x *= p.scale_log2, f.y *= p.scale_log2, f.z *= p.scale_log2, f.w *= p.scale_log2;
+              x[k] = s[k] * f.x, x[k + 1] = s[k + 1] * f.y, x[k + 2] = s[k + 2] * f.z, x[k + 3] = s[k + 3] * f.w;
+            }
           }
         }
         if constexpr (C::TILED) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] *= p.scale_log2;
+          for (int k = 0; k < 16; ++k) x[k] *= p.scale_log2;
         }
-        const bool bad = p.pages.table && a->tile_bad[n & 3];
+        const bool bad = p.pages.table && a->tile_bad[n & 7];
         uint32_t clear = 0;
         if ((t + 1) * kKeys > it.ctx || bad) {
-          const uint32_t see = bad ? 0u : (uint32_t)(seen_bits(p, it, node, t) >> (32 * rank));
+          const uint32_t see = bad ? 0u : (uint32_t)(seen_bits(p, it, node, t) >> (32 * rank + 16 * h));
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
+          for (int k = 0; k < 16; ++k) {
             if (!((see >> k) & 1)) {
               // a hidden position that may hold infinities or NaN (its logit is not finite, or it lies past
               // the end): its values are cleared in the tile, so that 0 * value is 0
-              if (!C::FP8 && (!(fabsf(x[k]) < INFINITY) || t * kKeys + 32 * rank + k >= it.len)) clear |= 1u << k;
+              if (!C::FP8 && (!(fabsf(x[k]) < INFINITY) || t * kKeys + 32 * rank + 16 * h + k >= it.len)) clear |= 1u << (16 * h + k);
               x[k] = -INFINITY;
             }
           }
           clear = __reduce_or_sync(0xffffffffu, clear);
         }
-        mx = x[0];
+        float mx = x[0];
 #pragma unroll
-        for (int k = 1; k < 32; ++k) mx = fmaxf(mx, x[k]);
-        if (lane == 0) a->clear_own[n & 3][quarter] = clear;
+        for (int k = 1; k < 16; ++k) mx = fmaxf(mx, x[k]);
+        const int slot = n & 3;
+        a->mx_own[n & 1][h][row] = mx;
+        if (lane == 0) a->clear_own[slot][w] = clear;
         if (ok) {
-          st_async4(peer_mx + (n & 3) * (kRows * 4), __float_as_uint(mx), peer_mm + 8 * (n & 3));
-          if (lane == 0) st_async4(peer_clear + (n & 3) * 16, clear, peer_mm + 8 * (n & 3));
+          st_async4(peer_mx + slot * (2 * kRows * 4), __float_as_uint(mx), peer_mm + 8 * slot);
+          if (lane == 0) st_async4(peer_clear + slot * 32, clear, peer_mm + 8 * slot);
         }
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(&a->m_msg[slot]);
       };
 
-      float x[32], y[32], mx, my = -INFINITY;
-      stage(tile, it.t0, x, mx);
+      float x[16], y[16];
+      stage(tile, it.t0, x);
       for (int t = it.t0; t < it.t1; ++t, ++tile) {
-        // the next tile's logits first, if they are there: their maxima travel while this tile is finished
+        // the next tile's logits first, if they are there: their maxima travel while this tile is finished.  (With
+        // tile scales always: there an S buffer is refilled only when all eight warps have read it, so they have
+        // to take the tiles' steps in one order.)
         const bool more = t + 1 < it.t1;
         bool staged = false;
-        if (more && __all_sync(0xffffffffu, mbar_test(&a->s_full[su & 1], (su >> 1) & 1))) {
-          stage(tile + 1, t + 1, y, my);
+        if (more && (C::TILED || __all_sync(0xffffffffu, mbar_test(&a->s_full[su % C::SB], (su / C::SB) & 1)))) {
+          stage(tile + 1, t + 1, y);
           staged = true;
         }
-        ok = wait_cluster(a, &a->m_msg[tile & 3], (tile >> 2) & 1, err) && ok;
-        const float other = a->mx[tile & 3][row];
+        const int slot = tile & 3, pb = tile % C::PB;
+        ok = wait_cluster(a, &a->m_msg[slot], (tile >> 2) & 1, err) && ok;
+        const float top = fmaxf(fmaxf(a->mx_own[tile & 1][0][row], a->mx_own[tile & 1][1][row]),
+                                fmaxf(a->mx[slot][0][row], a->mx[slot][1][row]));
         if (!C::FP8 && (t + 1) * kKeys > it.ctx) {
           // zero the value columns of the positions to clear (their logits have been taken): a position past the
           // end always, another one only if it holds something that is not finite
-          softmax_bar();
           uint32_t clear[2] = {0u, 0u};  // ours, the other's
 #pragma unroll
-          for (int k = 0; k < 4; ++k) clear[0] |= a->clear_own[tile & 3][k], clear[1] |= a->clear[tile & 3][k];
-          const int who = st >> 6, key = (st >> 1) & 31;  // two threads per position, two of its four boxes each
+          for (int k = 0; k < 8; ++k) clear[0] |= a->clear_own[slot][k], clear[1] |= a->clear[slot][k];
+          const int who = st >> 7, key = (st >> 2) & 31;  // a position, one of its four boxes
           if ((clear[who] >> key) & 1) {
-            for (int b = 2 * (st & 1); b < 2 * (st & 1) + 2; ++b) {
-              uint8_t* line = v_s + (tile % C::VS) * kSlotV + (4 * who + b) * kBox + key * 128;
-              bool zero = t * kKeys + 32 * (who ? rank ^ 1 : rank) + key >= it.len;
-              if (!zero) {
+            uint8_t* line = (who ? b_s + (tile % C::BS) * kSlotV : a_s + (tile % C::AS) * kSlotV) + (st & 3) * kBox + key * 128;
+            bool zero = t * kKeys + 32 * (who ? rank ^ 1 : rank) + key >= it.len;
+            if (who) ok = wait(a, &a->b_full[tile % C::BS], (tile / C::BS) & 1, err) && ok;  // (loaded for the second product only)
+            if (!zero) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                  const uint4 u = *reinterpret_cast<const uint4*>(line + 16 * c);
-                  const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
+              for (int c = 0; c < 8; ++c) {
+                const uint4 u = *reinterpret_cast<const uint4*>(line + 16 * c);
+                const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                  for (int q = 0; q < 4; ++q)
-                    zero |= (ws[q] & 0x7F80u) == 0x7F80u || (ws[q] & 0x7F800000u) == 0x7F800000u;
-                }
-              }
-              if (zero) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(line + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+                for (int q = 0; q < 4; ++q)
+                  zero |= (ws[q] & 0x7F80u) == 0x7F80u || (ws[q] & 0x7F800000u) == 0x7F800000u;
               }
             }
+            if (zero) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(line + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
+          __syncwarp();
         }
-        __syncwarp();
-        // the reference maximum moves, here and in the other CTA alike
-        const float top = fmaxf(mx, other);
+        // the reference maximum moves, in both halves' warps and in the other CTA alike
         if (__any_sync(0xffffffffu, top > m + kLazy)) {
           float f = 1.f;
           if (top > m + kLazy) {  // (m = -inf: nothing summed yet, the factor is 0)
@@ -917,11 +989,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
             l *= f;
           }
           if (t > it.t0) {
-            // the second product of the tile before is done: O may be rescaled
+            // the second product of the tile before is done: O may be rescaled (half of its columns per warp)
             ok = wait(a, &a->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, err) && ok;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 16) {
+            for (int c = 128 * h; c < 128 * h + 128; c += 16) {
               float o[16];
               tmem_ld_sync(lane_base + kColO + c, o);
               uint32_t v[16];
@@ -935,35 +1007,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         // ---- weights
         const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
+        for (int k = 0; k < 16; ++k) {
           x[k] = ex2(x[k] - mu);
           l += x[k];
         }
-        // the tile that used this P buffer has been added, here and in the other CTA
-        const int pb = tile % C::PB;
+        // the tile that used this P buffer has been added, here and in the other CTA (so the copies of it have left)
         if (tile >= C::PB) ok = wait(a, &a->pv_done[(tile - C::PB) & 1], ((tile - C::PB) >> 1) & 1, err) && ok;
         ok = wait_cluster(a, &a->p_free[pb], ((tile / C::PB) & 1) ^ 1, err) && ok;
-        if (C::TILED) {
-          if (lane == 0) copy_wait_read();  // the staged copies of the tile before have left
-          __syncwarp();
-        }
-        const float* sc = sc_s + (tile % C::SC_DEPTH) * 32 * C::NSC;
-        // P (times the positions' scales; a hidden position's weight is 0 whatever its scale holds)
+        const float* sc = sc_s + (tile % C::SC_DEPTH) * 32 * C::NSC + 16 * h;
+        // P, times the positions' scales (a hidden position's weight is 0 whatever its scale holds)
+        const bool hides = C::FP8 && ((t + 1) * kKeys > it.ctx || (p.pages.table && a->tile_bad[tile & 7]));
         auto put = [&](uint8_t* dst, int g) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // 16-byte chunks of eight positions
-            uint32_t v[4];
+          for (int j = 0; j < 2; ++j) {  // 16-byte chunks of eight positions
+            float z[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int e = 8 * j + 2 * k;
-              float y0 = x[e], y1 = x[e + 1];
-              if constexpr (C::FP8) {
-                y0 = y0 == 0.f ? 0.f : y0 * sc[e * C::NSC + g];
-                y1 = y1 == 0.f ? 0.f : y1 * sc[(e + 1) * C::NSC + g];
+            for (int k = 0; k < 8; ++k) z[k] = x[8 * j + k];
+            if constexpr (C::FP8) {
+              const float4 f0 = *reinterpret_cast<const float4*>(sc + 32 * g + 8 * j);
+              const float4 f1 = *reinterpret_cast<const float4*>(sc + 32 * g + 8 * j + 4);
+              z[0] *= f0.x, z[1] *= f0.y, z[2] *= f0.z, z[3] *= f0.w;
+              z[4] *= f1.x, z[5] *= f1.y, z[6] *= f1.z, z[7] *= f1.w;
+              if (hides) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) z[k] = x[8 * j + k] == 0.f ? 0.f : z[k];
               }
-              v[k] = pack_bf16(y0, y1);
             }
-            *reinterpret_cast<uint4*>(dst + row * 64 + ((j ^ ((row >> 1) & 3)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(dst + p_at + (((2 * h + j) ^ p_sw) << 4)) =
+                make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
           }
         };
 #pragma unroll
@@ -973,44 +1044,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (ok) {
+        pair_bar(quarter);  // both halves of the 32 rows are there
+        if (lane == 0 && ok) {
+          if (h == 0) {
 #pragma unroll
             for (int pc = 0; pc < C::PC; ++pc)
               copy_remote(peer_p + (pb * C::PC + pc) * C::P_BYTES,
                           (C::TILED ? pp_s + pc * C::P_HALF : p_s + pb * C::P_BYTES + rank * C::P_HALF) + 32 * quarter * 64,
                           32 * 64, peer_pm + 8 * pb);
             copy_commit();
+          } else if (quarter == 0) {
+            mbar_arrive_expect_tx(&a->m_msg[slot], kMaxBytes);  // for the tile four on
           }
-          if (quarter == 0) mbar_arrive_expect_tx(&a->m_msg[tile & 3], kMaxBytes);  // for the tile four on
           if constexpr (C::FP8) mbar_arrive(&a->sc_empty[tile % C::SC_DEPTH]);
           mbar_arrive(&a->p_full[tile & 1]);
         }
         if (more) {
-          if (!staged) stage(tile + 1, t + 1, y, my);
+          if (!staged) stage(tile + 1, t + 1, y);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = y[k];
-          mx = my;
+          for (int k = 0; k < 16; ++k) x[k] = y[k];
         }
       }
       // ---- the item's sums, to the other CTA as well
+      a->mx_own[0][h][row] = l;
       if (ok) st_async4(peer_stat, __float_as_uint(l), peer_sf);
       ok = wait_cluster(a, &a->stat_full, items & 1, err) && ok;
-      // (added in the same order on both sides)
-      l = rank ? a->stat[row] + l : l + a->stat[row];
       softmax_bar();
-      if (st == 0) mbar_arrive_expect_tx(&a->stat_full, kRows * 4);
+      {
+        // (added in the same order on both sides)
+        const float mine = a->mx_own[0][0][row] + a->mx_own[0][1][row], theirs = a->stat[0][row] + a->stat[1][row];
+        l = rank ? theirs + mine : mine + theirs;
+      }
+      if (st == 0 && ok) mbar_arrive_expect_tx(&a->stat_full, 2 * kRows * 4);
       const bool live = row < nrows && (row_lo + row) / p.H < it.fresh;
       const float inv = live && l != 0.f ? 1.f / l : 0.f;
-      if (rank == 0) {
+      if (rank == 0 && h == 0) {
         if (it.slot >= 0) pl.part_ml[(int64_t)it.slot * kRows + row] = make_float2(m, l);
         else if (p.lse && row < nrows) p.lse[at + row] = !live || l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
       ok = wait(a, &a->o_done, items & 1, err) && ok;
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
+      for (int c = 128 * h; c < 128 * h + 128; c += 32) {
         float o[32];
         tmem_ld_sync(lane_base + kColO + c, o);
         if (row < nrows && it.slot >= 0) {
@@ -1021,18 +1096,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
           uint4* dst = reinterpret_cast<uint4*>(p.out + (at + row) * kDv + 256 * rank + c);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
+            uint32_t v[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              w[q] = live ? pack_bf16(o[8 * k + 2 * q] * inv, o[8 * k + 2 * q + 1] * inv) : 0u;
-            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+              v[q] = live ? pack_bf16(o[8 * k + 2 * q] * inv, o[8 * k + 2 * q + 1] * inv) : 0u;
+            dst[k] = make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
         __syncwarp();
       }
+      softmax_bar();  // the sums have been read
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&a->o_free);
+      if (lane == 0 && ok) mbar_arrive(&a->o_free);
       ++items;
     }
   }
