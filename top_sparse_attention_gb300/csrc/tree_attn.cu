@@ -36,6 +36,8 @@
 // together read the same positions and the cache comes from HBM once.  The lengths are on the device:
 // every CTA evaluates the same cost model over them and picks the chunk length (plan_items); partial
 // results are merged by tree_combine_kernel.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <string.h>
 
 #include "dsa_internal.h"
@@ -45,50 +47,58 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kDqk = 576, kDv = 512;
-constexpr int kRows = 128;                // query rows per cluster
-constexpr int kKeys = 64;                 // positions per tile, half of them per CTA
-constexpr int kBox = 32 * 128;            // 64 columns of 32 positions: 32 rows x 128 bytes
-constexpr int kSlotV = 4 * kBox;          // a CTA's value columns of 32 positions (its own, or the other's)
-constexpr int kSlotK = 5 * kBox;          // the other columns of its positions: 4 boxes of values, the rotary one
+constexpr int kRows = 128;                // query rows per pair of CTAs
+constexpr int kKeys = 64;                 // positions per tile
+constexpr int kBox = kKeys * 128;         // 64 columns of a tile: 64 rows x 128 bytes
+constexpr int kSlotV = 4 * kBox;          // a CTA's value columns
+constexpr int kBoxC = kKeys * 64;         // 64 columns of a tile's E4M3 codes
+constexpr int kSlotC = 9 * kBoxC;
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLazy = 8.f;              // log2 growth of a row's maximum that is left unscaled
 constexpr int kItemsPerCta = 3;           // split launches are cut into at most this many items per cluster
-// tensor-memory columns: O, seven (six) of the nine 64-column boxes of q, one S buffer (two)
-constexpr int kColO = 0, kColQ = 256;
+constexpr int kColO = 0;                  // tensor-memory columns: O, then boxes of q, then S
 
 enum { kBf16 = 0, kFp8Row = 1, kFp8Tile = 2 };
+
+struct Aux {
+  uint64_t v_full[3], v_empty[3], k_full[7], k_empty[7], c_full[3], c_empty[3], s_full[2], s_empty[2], p_full, pv_done;
+  uint64_t o_done, o_free, q_full, sc_full[2], sc_empty[2], drain;
+  uint32_t tmem;
+  int abort;
+  int n_items;
+  int tile_bad[8];
+  int items[kItemsPerCta][8];
+  alignas(16) float mx[2][2][kRows];  // the rows' maxima over half of a tile
+  float sum[2][kRows];                // and, at an item's end, their sums
+  uint32_t clear[2][8];               // positions to clear
+};
 
 template <int FMT>
 struct Cfg {
   static constexpr bool FP8 = FMT != kBf16;
   static constexpr int NSC = FMT == kFp8Tile ? 5 : FMT == kFp8Row ? 1 : 0;
   static constexpr bool TILED = FMT == kFp8Tile;
-  static constexpr int THREADS = FP8 ? 640 : 384;
-  // slots: our positions' value columns (held from the first product to the second), their other columns (first
-  // product only), the other's positions (second product only)
-  static constexpr int AS = TILED ? 3 : 4, KS = 2, BS = TILED ? 2 : 3;
-  static constexpr int BT = TILED ? 6 : 7;                // q's boxes in tensor memory (the others are in shared memory)
+  static constexpr int THREADS = FP8 ? 512 : 384;
+  // bf16: slots of this CTA's value columns (held from the first product to the second) and boxes of the others
+  // (first product only).  E4M3: slots of a tile's codes, and of the value columns widened to bf16.
+  static constexpr int VS = FP8 ? 1 : 3, KS = FP8 ? 0 : 7, CS = TILED ? 2 : FP8 ? 3 : 0;
   static constexpr int SB = TILED ? 2 : 1;                // S buffers
-  static constexpr int PB = TILED ? 1 : 2;                // P buffers
-  static constexpr int COL_S = kColQ + 32 * BT;
+  static constexpr int BT = TILED ? 4 : 6;                // q's boxes in tensor memory (the others are in shared memory)
+  static constexpr int COL_Q = 256, COL_S = COL_Q + 32 * BT;
   static constexpr int GROUPS = TILED ? 5 : 1;            // S accumulations per tile
   static constexpr int PC = TILED ? 2 : 1;                // copies of P (one per 128 values)
-  static constexpr int SC_DEPTH = 2;
-  static constexpr int SC_BYTES = NSC * 32 * 4;           // scales of this CTA's positions
+  static constexpr int SC_BYTES = NSC * kKeys * 4;
   static constexpr int Q_BOX = kRows * 128, Q_BYTES = (9 - BT) * Q_BOX;
-  static constexpr int P_HALF = kRows * 64;               // 128 rows x 32 positions
-  static constexpr int P_BYTES = 2 * P_HALF;
-  static constexpr int PP_BYTES = TILED ? PC * P_HALF : 0;  // with tile scales: the other's copies of our P, on their way
-  static constexpr int AUX = 8192;
-  static constexpr int OFF_B = AS * kSlotV;
-  static constexpr int OFF_K = OFF_B + BS * kSlotV;
-  static constexpr int OFF_Q = OFF_K + KS * kSlotK;
+  static constexpr int P_BYTES = kRows * 128;             // 128 rows x 64 positions
+  static constexpr int OFF_K = VS * kSlotV;
+  static constexpr int OFF_C = OFF_K + KS * kBox;
+  static constexpr int OFF_Q = OFF_C + CS * kSlotC;
   static constexpr int OFF_P = OFF_Q + Q_BYTES;
-  static constexpr int OFF_PP = OFF_P + PB * PC * P_BYTES;
-  static constexpr int OFF_SC = OFF_PP + PP_BYTES;
-  static constexpr int OFF_AUX = OFF_SC + SC_DEPTH * SC_BYTES;
-  static constexpr int SMEM = OFF_AUX + AUX + 1024;
+  static constexpr int OFF_SC = OFF_P + PC * P_BYTES;
+  static constexpr int OFF_AUX = OFF_SC + 2 * SC_BYTES;
+  static constexpr int SMEM = OFF_AUX + (int)sizeof(Aux) + 1024;
   static_assert(SMEM <= kSmemMax, "shared memory");
+  static_assert(COL_S + kKeys * SB <= 512, "tensor memory");
 };
 
 struct Item {
@@ -118,24 +128,6 @@ __device__ __forceinline__ int live_row_tiles(const TreeAttnParams& p, int fresh
   return (fresh * p.H + kRows - 1) / kRows;  // row tiles that hold a node below `fresh`
 }
 
-struct Aux {
-  uint64_t a_full[4], a_empty[4], b_full[3], b_empty[3], k_full[2], k_empty[2];
-  uint64_t s_full[2], s_empty[2], m_msg[4], p_full[2], p_msg[2], p_free[2], pv_done[2];
-  uint64_t stat_full, o_done, o_free, q_full, sc_full[2], sc_empty[2], drain;
-  uint32_t tmem;
-  int abort;
-  int n_items;
-  int tile_bad[8];
-  int items[kItemsPerCta][8];
-  // each half's maxima over its 16 positions, ours (by tile % 2; at an item's end its sums) and the other CTA's (by
-  // tile % 4), and the positions to clear
-  alignas(16) float mx_own[2][2][kRows];
-  alignas(16) float mx[4][2][kRows];
-  uint32_t clear_own[4][8], clear[4][8];
-  float stat[2][kRows];  // the other's sums, by half
-};
-static_assert(sizeof(Aux) <= 8192, "Aux");
-
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -152,67 +144,21 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 // through the rest of their work (every address stays in range), so that their common barriers still match; the
 // other roles leave.  A thread whose wait failed arrives on no mbarrier, arms none and sends nothing any more: an
 // arrival is only legal in a phase that the arriving thread has seen begin.
-__device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err, bool cluster);
+__device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err);
 __device__ __forceinline__ bool wait(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
-  return mbar_test(bar, parity) || wait_slow(a, bar, parity, err, false);
+  return mbar_test(bar, parity) || wait_slow(a, bar, parity, err);
 }
-// The same for a barrier that the other CTA of the cluster arrives on: what it did before is visible after.
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, P;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool test_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\t"
-      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, P;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_cluster(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
-  return test_cluster(bar, parity) || wait_slow(a, bar, parity, err, true);
-}
-__device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err, bool cluster) {
+__device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
   const unsigned long long t0 = globaltimer_ns();
   for (uint32_t i = 0;; ++i) {
     if (*reinterpret_cast<volatile int*>(&a->abort)) return false;
-    if (cluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if ((i & 63u) == 63u && globaltimer_ns() - t0 > kWaitLimitNs) {
       record_error(err, DSA_DEVERR_WAIT_TIMEOUT);
       *reinterpret_cast<volatile int*>(&a->abort) = 1;
       return false;
     }
   }
-}
-
-__device__ __forceinline__ void arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// `bytes` of this CTA's shared memory into the other CTA's, counted on its mbarrier (measured one way: 320
-// cycles for 64 bytes, 520 for 4 KB, 1100 for 16 KB).
-__device__ __forceinline__ void copy_remote(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "r"(smem_u32(src)), "r"(bytes), "r"(bar)
-               : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// All of this thread's copies have read their source.
-__device__ __forceinline__ void copy_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-
-__device__ __forceinline__ void st_async4(uint32_t addr, uint32_t v, uint32_t bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
-               : "memory");
 }
 
 // Barriers of the eight softmax warps, and of the two that share 32 rows (ids 2 to 5).
@@ -244,8 +190,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // Low words of shared-memory descriptors with 128-byte swizzle (the upper word, kDescHi, holds the 1024-byte
 // stride, the version and the swizzle): K-major operands, and MN-major ones whose 64-element atoms are one
-// box apart.  Adding bytes / 16 moves the start address.  P's rows are 64 bytes, with 64-byte swizzle
-// (kDescHi64: 8 rows are 512 bytes; 16-byte chunk c of row r lies at chunk c ^ (r / 2 % 4)).
+// box apart.  Adding bytes / 16 moves the start address.  Boxes of codes have rows of 64 bytes, with 64-byte
+// swizzle (kDescHi64: 8 rows are 512 bytes; 16-byte chunk c of row r lies at chunk c ^ (r / 2 % 4)).
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t kDescHi64 = (512u >> 4) | (1u << 14) | (4u << 29);
 __device__ __forceinline__ uint32_t kmajor_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
@@ -253,26 +199,58 @@ __device__ __forceinline__ uint32_t mnmajor_lo(uint32_t saddr) {
   return ((saddr & 0x3FFFFu) >> 4) | ((uint32_t)(kBox >> 4) << 16);
 }
 
-// D += A B^T with A in shared memory, or in tensor memory (lane = row, two bf16 per column).
-template <uint32_t A_HI = kDescHi>
+// D += A B^T with A in shared memory, or in tensor memory (lane = row, two bf16 or four 8-bit elements per
+// column); F8: 8-bit operands, B's rows 64 bytes.
+template <bool F8 = false>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-      "mov.b64 da, {%1, %6};\n\t"
-      "mov.b64 db, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi), "r"(A_HI)
-      : "memory");
+  if constexpr (F8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\t"
+        "mov.b64 db, {%2, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi), "r"(kDescHi64)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi)
+        : "memory");
 }
+template <bool F8 = false>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
-      "mov.b64 db, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi)
-      : "memory");
+  if constexpr (F8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi64)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi)
+        : "memory");
+}
+
+// Two values v (|v| < 2^8, of bf16) as E4M3 plus E5M2: the first takes four of the eight significant bits, what is
+// left is a multiple of the last bit of at most eight of them, which three bits hold.  So v = e4 + e5 exactly for
+// |v| >= 2^-6, and to 2^-13 below.
+__device__ __forceinline__ void split_fp8(float lo, float hi, uint32_t& e4, uint32_t& e5) {
+  const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+  const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3);
+  const float2 f = __half22float2(__half2(back));
+  e4 = a;
+  e5 = __nv_cvt_float2_to_fp8x2(make_float2(lo - f.x, hi - f.y), __NV_SATFINITE, __NV_E5M2);
 }
 
 // Registers -> tensor memory: this thread's lane, 16 columns.
@@ -437,67 +415,64 @@ __device__ __forceinline__ bool get_item(const TreeAttnParams& p, const TreePlan
   return true;
 }
 
+template <int N>
+struct Int {
+  static constexpr int v = N;
+};
+
 template <int FMT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tm, const TreeAttnParams p, const TreePlan pl) {
   using C = Cfg<FMT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* a_s = smem;
-  uint8_t* b_s = smem + C::OFF_B;
+  uint8_t* v_s = smem;
   uint8_t* k_s = smem + C::OFF_K;
+  uint8_t* c_s = smem + C::OFF_C;
   uint8_t* q_s = smem + C::OFF_Q;
   uint8_t* p_s = smem + C::OFF_P;
-  uint8_t* pp_s = smem + C::OFF_PP;
   float* sc_s = reinterpret_cast<float*>(smem + C::OFF_SC);
   Aux* a = reinterpret_cast<Aux*>(smem + C::OFF_AUX);
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
-  const int rank = uniform((int)cluster_rank());  // which 32 positions of a tile, which half of the value columns
+  const int rank = (int)(blockIdx.x & 1);  // which half of the value columns
   int* err = p.err;
 
   if (warp == 0) {
     tmem_alloc(&a->tmem, 512);
     tmem_relinquish();
   }
-  constexpr uint32_t kMaxBytes = 2 * kRows * 4 + 8 * 4;  // a tile's maxima and clear words
-  constexpr uint32_t kPBytes = C::PC * C::P_HALF;    // a tile's P from the other CTA
   if (tid == 32) {
-    const int fillers = C::FP8 ? 8 : 1;  // arrivals that fill a slot: converter warps, or the TMA's thread
-    for (int i = 0; i < C::AS; ++i) mbar_init(&a->a_full[i], fillers), mbar_init(&a->a_empty[i], 1);
-    for (int i = 0; i < C::BS; ++i) mbar_init(&a->b_full[i], fillers), mbar_init(&a->b_empty[i], 1);
+    // (the converters' four warps fill the value columns, and read a slot of codes beside the first product)
+    for (int i = 0; i < C::VS; ++i) mbar_init(&a->v_full[i], C::FP8 ? 4 : 1), mbar_init(&a->v_empty[i], 1);
+    for (int i = 0; i < C::KS; ++i) mbar_init(&a->k_full[i], 1), mbar_init(&a->k_empty[i], 1);
+    for (int i = 0; i < C::CS; ++i) mbar_init(&a->c_full[i], 1), mbar_init(&a->c_empty[i], 1 + 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&a->k_full[i], fillers), mbar_init(&a->k_empty[i], 1);
       mbar_init(&a->s_full[i], 1), mbar_init(&a->s_empty[i], 8);
-      mbar_init(&a->p_full[i], 8), mbar_init(&a->p_msg[i], 1), mbar_init(&a->p_free[i], 1), mbar_init(&a->pv_done[i], 1);
       mbar_init(&a->sc_full[i], 32), mbar_init(&a->sc_empty[i], 8);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&a->m_msg[i], 9);
-    mbar_init(&a->stat_full, 1);
+    mbar_init(&a->p_full, 8);
+    mbar_init(&a->pv_done, 1);
     mbar_init(&a->o_done, 1);
     mbar_init(&a->o_free, 8);
     mbar_init(&a->q_full, 256);
     mbar_init(&a->drain, 1);
     a->abort = 0;
     fence_mbar_init();
-    for (int i = 0; i < 4; ++i) mbar_arrive_expect_tx(&a->m_msg[i], kMaxBytes);
-    for (int i = 0; i < C::PB; ++i) mbar_arrive_expect_tx(&a->p_msg[i], kPBytes);
-    mbar_arrive_expect_tx(&a->stat_full, 2 * kRows * 4);
   }
-  if (pl.cap) plan_items(p, pl, a, reinterpret_cast<int*>(a_s));
+  if (pl.cap) plan_items(p, pl, a, reinterpret_cast<int*>(v_s));
   fence_proxy_async_smem();  // the plan's scratch is a slot that the copies write
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // the other CTA's barriers are ready too
   tc_fence_after();
   const uint32_t tmem = a->tmem;
   pdl_launch_dependents();
 
   Item it;
   if (warp == 0) {
-    // ---- producer (bf16): boxes of 64 columns x 32 positions by TMA
-    if (lane == 0 && !C::FP8) {
+    // ---- producer: boxes of 64 columns x 64 positions by TMA
+    if (lane == 0) {
       prefetch_tmap(&tm);
-      int as = 0, aph = 0, bs = 0, bph = 0, ks = 0, kph = 0, tiles = 0;
+      int vs = 0, vph = 0, ks = 0, kph = 0, cs = 0, cph = 0, tiles = 0;
       bool ok = true;
       for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
         for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
@@ -510,36 +485,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
             row = bad ? p.pages.num_blocks * p.pages.block_size : (int)r;
             if (bad) record_error(err, DSA_DEVERR_INDEX_RANGE);
           }
-          const int mine = row + 32 * rank, other = row + 32 * (rank ^ 1);
-          ok = wait(a, &a->a_empty[as], aph ^ 1, err);
-          if (!ok) break;
-          a->tile_bad[tiles & 7] = bad;
-          uint8_t* dst = a_s + as * kSlotV;
-          mbar_arrive_expect_tx(&a->a_full[as], kSlotV);
+          if constexpr (C::FP8) {
+            ok = wait(a, &a->c_empty[cs], cph ^ 1, err);
+            if (!ok) break;
+            a->tile_bad[tiles & 7] = bad;
+            mbar_arrive_expect_tx(&a->c_full[cs], kSlotC);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) tma_load_3d(dst + b * kBox, &tm, &a->a_full[as], 256 * rank + 64 * b, mine, z);
-          if (++as == C::AS) as = 0, aph ^= 1;
-          ok = wait(a, &a->k_empty[ks], kph ^ 1, err);
-          if (!ok) break;
-          dst = k_s + ks * kSlotK;
-          mbar_arrive_expect_tx(&a->k_full[ks], kSlotK);
+            for (int b = 0; b < 9; ++b)
+              tma_load_3d(c_s + cs * kSlotC + b * kBoxC, &tm, &a->c_full[cs], b < 8 ? 64 * (b ^ (rank << 2)) : 512, row, z);
+            if (++cs == C::CS) cs = 0, cph ^= 1;
+          } else {
+            for (int b = 0; b < 5; ++b) {
+              ok = wait(a, &a->k_empty[ks], kph ^ 1, err);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&a->k_full[ks], kBox);
+              tma_load_3d(k_s + ks * kBox, &tm, &a->k_full[ks], b < 4 ? 256 * (rank ^ 1) + 64 * b : 512, row, z);
+              if (++ks == C::KS) ks = 0, kph ^= 1;
+            }
+            ok = ok && wait(a, &a->v_empty[vs], vph ^ 1, err);
+            if (!ok) break;
+            a->tile_bad[tiles & 7] = bad;
+            mbar_arrive_expect_tx(&a->v_full[vs], kSlotV);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) tma_load_3d(dst + b * kBox, &tm, &a->k_full[ks], 256 * (rank ^ 1) + 64 * b, mine, z);
-          tma_load_3d(dst + 4 * kBox, &tm, &a->k_full[ks], 512, mine, z);
-          if (++ks == C::KS) ks = 0, kph ^= 1;
-          ok = wait(a, &a->b_empty[bs], bph ^ 1, err);
-          if (!ok) break;
-          dst = b_s + bs * kSlotV;
-          mbar_arrive_expect_tx(&a->b_full[bs], kSlotV);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) tma_load_3d(dst + b * kBox, &tm, &a->b_full[bs], 256 * rank + 64 * b, other, z);
-          if (++bs == C::BS) bs = 0, bph ^= 1;
+            for (int b = 0; b < 4; ++b)
+              tma_load_3d(v_s + vs * kSlotV + b * kBox, &tm, &a->v_full[vs], 256 * rank + 64 * b, row, z);
+            if (++vs == C::VS) vs = 0, vph ^= 1;
+          }
         }
       }
       if (*reinterpret_cast<volatile int*>(&a->abort)) {  // wind down: the copies in flight land first
-        for (int s = 0; s < C::AS; ++s) mbar_wait(&a->a_full[s], s < as ? aph : aph ^ 1, err);
-        for (int s = 0; s < C::BS; ++s) mbar_wait(&a->b_full[s], s < bs ? bph : bph ^ 1, err);
+        for (int s = 0; !C::FP8 && s < C::VS; ++s) mbar_wait(&a->v_full[s], s < vs ? vph : vph ^ 1, err);
         for (int s = 0; s < C::KS; ++s) mbar_wait(&a->k_full[s], s < ks ? kph : kph ^ 1, err);
+        for (int s = 0; s < C::CS; ++s) mbar_wait(&a->c_full[s], s < cs ? cph : cph ^ 1, err);
       }
     }
     __syncwarp();
@@ -547,14 +524,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
     // ---- MMA issuer.  The warp stays converged and one elected lane issues; descriptors are sums of
     // 32-bit words (their upper words are constants), so that issuing an instruction costs less than
     // the tensor cores take for it
-    constexpr uint32_t idesc_qk = make_idesc(1, 1, kRows, 32);
+    constexpr uint32_t idesc_qk = make_idesc(1, 1, kRows, kKeys);  // bf16
+    constexpr uint32_t idesc_e4 = make_idesc(0, 0, kRows, kKeys), idesc_e5 = make_idesc(1, 0, kRows, kKeys);
     constexpr uint32_t idesc_pv = make_idesc(1, 1, kRows, C::TILED ? 128 : 256) | (1u << 16);  // B (values) MN-major
     const uint32_t tm_base = (uint32_t)uniform((int)tmem);
-    const uint32_t ka_lo = kmajor_lo(smem_u32(a_s)), kk_lo = kmajor_lo(smem_u32(k_s));
-    const uint32_t va_lo = mnmajor_lo(smem_u32(a_s)), vb_lo = mnmajor_lo(smem_u32(b_s));
+    const uint32_t kv_lo = kmajor_lo(smem_u32(v_s)), kk_lo = kmajor_lo(smem_u32(k_s));
+    const uint32_t vv_lo = mnmajor_lo(smem_u32(v_s)), c_lo = kmajor_lo(smem_u32(c_s));
     const uint32_t q_lo = kmajor_lo(smem_u32(q_s)), p_lo = kmajor_lo(smem_u32(p_s));
-    int as = 0, aph = 0, ks = 0, kph = 0;  // slots of the first product
-    int ps = 0, bs = 0, bph = 0;           // of the second
+    int vs = 0, vph = 0, ks = 0, kph = 0, cs = 0, cph = 0;  // slots of the first product
+    int ps = 0;                                             // of the second
     int tile = 0, items = 0;
     uint32_t su = 0;                       // uses of the S buffers
     bool ok = true;
@@ -562,118 +540,119 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
       if (elect_one()) tc_commit(bar);
       __syncwarp();
     };
-    // Box j of q against this CTA's positions: 4 steps of K = 16.
+    auto all = [&](uint64_t* bar, uint32_t parity) { ok = __all_sync(0xffffffffu, wait(a, bar, parity, err)) && ok; };
+    // Box j of q (in the order of the slots: our value columns, the other columns, the rotary ones) against the
+    // tile's positions: 4 steps of K = 16.  With E4M3 rows q's bf16 values are E4M3 plus E5M2: two steps of
+    // K = 32, each for both parts, at the same cost, and the codes need no widening.
     auto qk_box = [&](uint32_t d, int j, uint32_t B, bool first) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t acc = first && k == 0 ? 0u : 1u;
-        if (j < C::BT) mma_ts(d, tm_base + kColQ + 32 * j + 8 * k, B + 2 * k, idesc_qk, acc);
-        else mma_ss(d, q_lo + (j - C::BT) * (C::Q_BOX >> 4) + 2 * k, B + 2 * k, idesc_qk, acc);
+        const uint32_t id = !C::FP8 ? idesc_qk : k & 1 ? idesc_e5 : idesc_e4;
+        const uint32_t b = B + 2 * (C::FP8 ? k >> 1 : k);
+        if (j < C::BT) mma_ts<C::FP8>(d, tm_base + C::COL_Q + 32 * j + 8 * k, b, id, acc);
+        else mma_ss<C::FP8>(d, q_lo + (j - C::BT) * (C::Q_BOX >> 4) + 2 * k, b, id, acc);
       }
     };
-    auto test = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)); };
-    // First product, one accumulation: the whole tile, or with tile scales a pair of boxes (g) after another
-    // through the S buffers.  The softmax warps have read what the buffer held.
-    auto qk_ready = [&](int g) {
-      return test(&a->s_empty[su % C::SB], ((su / C::SB) & 1) ^ 1) &&
-             (g > 0 || (test(&a->a_full[as], aph) && test(&a->k_full[ks], kph)));
-    };
-    auto qk = [&](int g) {
-      const uint32_t V = ka_lo + as * (kSlotV >> 4), K = kk_lo + ks * (kSlotK >> 4);
-      const uint32_t d = tm_base + C::COL_S + 32 * (su % C::SB);
-      const bool last = g == C::GROUPS - 1;
+    // Slot of box j of the K ring, from the next one on, and its phase.
+    auto k_slot = [&](int j) { return ks + j >= C::KS ? ks + j - C::KS : ks + j; };
+    auto k_phase = [&](int j) { return ks + j >= C::KS ? kph ^ 1 : kph; };
+    // Boxes [J0, J1) of the first product into the S buffer of use `su`.  One lane per barrier: a wait costs about
+    // 120 cycles even when there is nothing to wait for, and the tensor cores run dry.
+    auto qk = [&](auto J0, auto J1) {
+      constexpr int j0 = decltype(J0)::v, j1 = decltype(J1)::v;
+      const uint32_t d = tm_base + C::COL_S + kKeys * (su % C::SB);
+      uint64_t* bar = &a->s_empty[su % C::SB];
+      uint32_t parity = ((su / C::SB) & 1) ^ 1;
+      if (C::FP8) {
+        if (lane == 1) bar = &a->c_full[cs], parity = cph;
+      } else {
+        if (lane == 1) bar = &a->v_full[vs], parity = vph;
+        if (lane >= 2 && lane < 7) bar = &a->k_full[k_slot(lane - 2)], parity = k_phase(lane - 2);
+      }
+      all(bar, parity);
+      if (!ok) return;
       tc_fence_after();
       if (elect_one()) {
-        if (C::TILED) {
-          if (g < 4) {
-            const uint32_t B = ((g >> 1) == rank ? V : K) + (2 * (g & 1) * kBox >> 4);
-            if (g < 3) {
+        if (C::FP8) {
+          const uint32_t B = c_lo + cs * (kSlotC >> 4);
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mma_ts(d, tm_base + kColQ + 64 * g + 8 * k, B + ((k >> 2) * kBox + 32 * (k & 3)) / 16, idesc_qk, k ? 1u : 0u);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mma_ss(d, q_lo + ((k >> 2) * C::Q_BOX + 32 * (k & 3)) / 16, B + ((k >> 2) * kBox + 32 * (k & 3)) / 16, idesc_qk,
-                       k ? 1u : 0u);
-            }
-          } else {
-            qk_box(d, 8, K + (4 * kBox >> 4), true);
-          }
+          for (int j = j0; j < j1; ++j) qk_box(d, j, B + (j * kBoxC >> 4), j == j0);
+          if (j1 == 9) tc_commit(&a->c_empty[cs]);
         } else {
+          // those of the K ring first: their slots are the scarcer ones, and loading them again takes longer than
+          // the rest of this product
+          const uint32_t V = kv_lo + vs * (kSlotV >> 4);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) qk_box(d, j, ((j >> 2) == rank ? V : K) + ((j & 3) * kBox >> 4), j == 0);
-          qk_box(d, 8, K + (4 * kBox >> 4), false);
+          for (int j = 4; j < 9; ++j) {
+            qk_box(d, j, kk_lo + k_slot(j - 4) * (kBox >> 4), j == 4);
+            tc_commit(&a->k_empty[k_slot(j - 4)]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) qk_box(d, j, V + (j * kBox >> 4), false);
         }
         tc_commit(&a->s_full[su % C::SB]);
-        if (last) tc_commit(&a->k_empty[ks]);
       }
       __syncwarp();
       ++su;
-      if (last) {
-        if (++as == C::AS) as = 0, aph ^= 1;
-        if (++ks == C::KS) ks = 0, kph ^= 1;
+      if (j1 == 9) {
+        if (C::FP8) {
+          if (++cs == C::CS) cs = 0, cph ^= 1;
+        } else {
+          if (++vs == C::VS) vs = 0, vph ^= 1;
+          ks += 5;
+          if (ks >= C::KS) ks -= C::KS, kph ^= 1;
+        }
       }
     };
-    // Second product of a tile: its weights from both CTAs, and the other's positions, are there.
-    auto pv_ready = [&](bool first) {
-      const int pb = tile % C::PB;
-      return test(&a->p_full[tile & 1], (tile >> 1) & 1) &&
-             __all_sync(0xffffffffu, test_cluster(&a->p_msg[pb], (tile / C::PB) & 1)) && test(&a->b_full[bs], bph) &&
-             (!first || test(&a->o_free, (items & 1) ^ 1));
-    };
     auto pv = [&](bool first) {
-      if (lane == 0) mbar_arrive_expect_tx(&a->p_msg[tile % C::PB], kPBytes);  // for this buffer's next use
-      __syncwarp();
+      uint64_t* bar = &a->p_full;
+      uint32_t parity = tile & 1;
+      if (first && lane == 1) bar = &a->o_free, parity = (items & 1) ^ 1;
+      if (C::FP8 && lane == 2) bar = &a->v_full[0];
+      all(bar, parity);
+      if (!ok) return;
       tc_fence_after();
-      const uint32_t acc0 = first ? 0u : 1u, A = va_lo + ps * (kSlotV >> 4), B = vb_lo + bs * (kSlotV >> 4);
-      const uint32_t P = p_lo + (tile % C::PB) * (C::PC * C::P_BYTES >> 4);
+      const uint32_t acc0 = first ? 0u : 1u, V = vv_lo + ps * (kSlotV >> 4);
       if (elect_one()) {
         constexpr int NB = C::TILED ? 2 : 1;  // value tiles of N = 128 with a P each, or all 256 at once
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {  // two steps over this CTA's positions, two over the other's
-            const uint32_t half = (uint32_t)((s >> 1) ^ rank);  // whose P: the halves of the buffer are by CTA
-            mma_ss<kDescHi64>(tm_base + kColO + 128 * b, P + (b * C::P_BYTES >> 4) + half * (C::P_HALF >> 4) + 2 * (s & 1),
-                              (s < 2 ? A : B) + (2 * b * kBox + 2048 * (s & 1)) / 16, idesc_pv, s ? 1u : acc0);
-          }
-        tc_commit(&a->a_empty[ps]);
-        tc_commit(&a->b_empty[bs]);
-        tc_commit(&a->pv_done[tile & 1]);
+          for (int s = 0; s < 4; ++s)
+            mma_ss(tm_base + kColO + 128 * b, p_lo + (b * C::P_BYTES >> 4) + 2 * s, V + (2 * b * kBox + 2048 * s) / 16, idesc_pv,
+                   s ? 1u : acc0);
+        tc_commit(&a->v_empty[ps]);
+        tc_commit(&a->pv_done);
       }
       __syncwarp();
-      if (++ps == C::AS) ps = 0;
-      if (++bs == C::BS) bs = 0, bph ^= 1;
+      if (++ps == C::VS) ps = 0;
+      ++tile;
     };
     for (int i = 0; ok && uniform(get_item(p, pl, a, i, it)); ++i) {
       const int t0 = uniform(it.t0), t1 = uniform(it.t1);
       if (t0 >= t1) continue;
-      ok = __all_sync(0xffffffffu, wait(a, &a->q_full, items & 1, err));
-      // whichever product can go: the first one runs ahead as far as S buffers and slots allow
-      int t = t0, n = t0, g = 0;  // next tile of the second product; of the first, and its accumulation
-      unsigned long long since = 0;
-      for (uint32_t idle = 0; ok && t < t1;) {
-        if (idle++ == 0) since = 0;
-        if (n < t1 && qk_ready(g)) {
-          qk(g);
-          if (++g == C::GROUPS) g = 0, ++n;
-          idle = 0;
-        }
-        if (t < n && pv_ready(t == t0)) {
-          pv(t == t0);
-          ++t, ++tile;
-          idle = 0;
-        }
-        if ((idle & 255u) == 255u) {  // a bounded wait, as the others
-          const unsigned long long now = globaltimer_ns();
-          if (since == 0) since = now;
-          const bool late = now - since > kWaitLimitNs;
-          if (__any_sync(0xffffffffu, late) && !*reinterpret_cast<volatile int*>(&a->abort)) {
-            record_error(err, DSA_DEVERR_WAIT_TIMEOUT);
-            *reinterpret_cast<volatile int*>(&a->abort) = 1;
+      all(&a->q_full, items & 1);
+      if constexpr (C::TILED) {
+        // an accumulation per scale tile: two run ahead of the softmax warps
+        qk(Int<0>{}, Int<2>{});
+        qk(Int<2>{}, Int<4>{});
+        for (int t = t0; ok && t < t1; ++t) {
+          qk(Int<4>{}, Int<6>{});
+          qk(Int<6>{}, Int<8>{});
+          qk(Int<8>{}, Int<9>{});
+          if (t + 1 < t1) {
+            qk(Int<0>{}, Int<2>{});
+            qk(Int<2>{}, Int<4>{});
           }
-          ok = !__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&a->abort));
+          pv(t == t0);
+        }
+      } else {
+        // the next tile's first product, then this one's second
+        qk(Int<0>{}, Int<9>{});
+        for (int t = t0; ok && t < t1; ++t) {
+          if (t + 1 < t1) qk(Int<0>{}, Int<9>{});
+          pv(t == t0);
         }
       }
       if (ok) commit(&a->o_done);
@@ -684,151 +663,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
       mbar_wait(&a->drain, 0, err);
     }
   } else if (warp == 2 && C::FP8) {
-    // ---- scales of this CTA's positions (1 where there is none: the position is masked)
+    // ---- scales of the tile's positions (1 where there is none: the position is masked)
     int tiles = 0;
     bool ok = true;
     for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
       for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
-        const int d = tiles % C::SC_DEPTH, pos = t * kKeys + 32 * rank;
+        const int d = tiles & 1;
         int64_t row = tree_row(p, it.seq, t * kKeys);
         const bool bad = row < 0;
-        row += 32 * rank + (p.pages.table ? 0 : (int64_t)it.seq * p.L);
-        const int n = (it.len - pos) * C::NSC;
+        row += p.pages.table ? 0 : (int64_t)it.seq * p.L;
+        const int n = (it.len - t * kKeys) * C::NSC;
         const float* src = p.kv_scale + row * C::NSC;
-        float v[C::NSC + 1];
+        float v[2 * C::NSC + 1];
 #pragma unroll
-        for (int k = 0; k < C::NSC; ++k) v[k] = !bad && lane + 32 * k < n ? __ldg(src + lane + 32 * k) : 1.f;
-        ok = __all_sync(0xffffffffu, wait(a, &a->sc_empty[d], ((tiles / C::SC_DEPTH) & 1) ^ 1, err));
+        for (int k = 0; k < 2 * C::NSC; ++k) v[k] = !bad && lane + 32 * k < n ? __ldg(src + lane + 32 * k) : 1.f;
+        ok = __all_sync(0xffffffffu, wait(a, &a->sc_empty[d], ((tiles >> 1) & 1) ^ 1, err));
         if (!ok) break;
 #pragma unroll
-        for (int k = 0; k < C::NSC; ++k) {
+        for (int k = 0; k < 2 * C::NSC; ++k) {
           const int e = lane + 32 * k, key = e / (C::NSC + !C::NSC);
-          sc_s[(d * C::NSC + e - key * C::NSC) * 32 + key] = v[k];  // [scale of the row][position]
+          sc_s[(d * C::NSC + e - key * C::NSC) * kKeys + key] = v[k];  // [scale of the row][position]
         }
-        if (lane == 0) {
-          a->tile_bad[tiles & 7] = bad;
-          if (bad) record_error(err, DSA_DEVERR_INDEX_RANGE);
-        }
-        __syncwarp();
         mbar_arrive(&a->sc_full[d]);
       }
     }
-  } else if (warp == 3) {
-    // ---- credits of the exchange (here, because a release at cluster scope would hold up the softmax warps):
-    // once a second product has read P, the other CTA may send into that buffer again
-    int tiles = 0;
+  } else if (warp >= 12) {
+    // ---- converters (E4M3): this CTA's value columns, widened into swizzled bf16 boxes for the second product.
+    // 16 codes per lane and step: eight positions of a box, four lanes each, so that eight lanes' 16-byte loads
+    // and stores fall into different banks.
+    const int w = warp - 12, c = lane & 3;
+    int cs = 0, cph = 0, tiles = 0;
     bool ok = true;
-    const uint32_t peer_p = dsmem_addr(&a->p_free[0], rank ^ 1);
     for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
       for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
-        ok = __all_sync(0xffffffffu, wait(a, &a->pv_done[tiles & 1], (tiles >> 1) & 1, err));
-        if (ok && lane == 0) arrive_remote(peer_p + 8 * (tiles % C::PB));
+        ok = __all_sync(0xffffffffu, wait(a, &a->c_full[cs], cph, err));
+        if (!ok) break;
+        const uint8_t* src = c_s + cs * kSlotC;
+        uint4 raw[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int key = 8 * (w + 4 * (k >> 2)) + (lane >> 2);
+          raw[k] = *reinterpret_cast<const uint4*>(src + (k & 3) * kBoxC + key * 64 + ((c ^ ((key >> 1) & 3)) << 4));
+        }
         __syncwarp();
-      }
-    }
-  } else if (warp >= 12) {
-    // ---- converters (E4M3): 16 codes per lane and step, loaded a tile ahead, widened into the swizzled bf16
-    // boxes.  Eight lanes take four 16-code chunks of one box from two neighbouring positions: their eight
-    // 16-byte stores fall into different banks.  A warp takes one pair of positions of each group of 8 pairs:
-    // step k < 4: box k of our value columns, ours; < 8: the other's positions; < 12: our other columns; 12: rotary.
-    const int cw = warp - 12;
-    int as = 0, aph = 0, bs = 0, bph = 0, ks = 0, kph = 0;
-    bool ok = true;
-    constexpr int STEPS = 7;  // two boxes per step (lanes 0-15, 16-31), the rotary one alone
-    uint4 raw[STEPS];
-    // step k: box 2 k + lane / 16; the warp's pair of positions: 2 cw + 16 (lane / 8 % 2) ... (of 32)
-    auto place = [&](int k, int& box, int& key, int& c) {
-      box = 2 * k + (lane >> 4);
-      c = lane & 3;
-      key = 2 * cw + ((lane >> 2) & 1) + 16 * ((lane >> 3) & 1);
-    };
-    auto tile_rows = [&](const Item& x, int t) -> const uint8_t* {
-      if (t >= x.t1) return nullptr;
-      const int64_t row = tree_row(p, x.seq, t * kKeys);
-      if (row < 0) return nullptr;
-      return p.kv + (p.pages.table ? 0 : (int64_t)x.seq * p.kv_seq_stride) + row * p.kv_row_stride;
-    };
-    // of this lane's chunk of step k: its position in the tile and its offset from the tile's first row (boxes 0-3:
-    // our value columns of our positions, 4-7: of the other's, 8-11: our positions' other columns, 12: rotary)
-    int off[STEPS];
-#pragma unroll
-    for (int k = 0; k < STEPS; ++k) {
-      int box, key, c;
-      place(k, box, key, c);
-      const int pos = key + 32 * (box >= 4 && box < 8 ? rank ^ 1 : rank);
-      const int col = box < 8 ? 256 * rank + 64 * (box & 3) : box < 12 ? 256 * (rank ^ 1) + 64 * (box & 3) : 512;
-      off[k] = pos * (int)p.kv_row_stride + col + 16 * c;
-    }
-    const int at0 = 2 * cw + ((lane >> 2) & 1) + 16 * ((lane >> 3) & 1);
-    auto fetch = [&](const uint8_t* r, int n, int k) {
-      const bool other = k >= 2 && k < 4;
-      bool in = r != nullptr && (k < 6 || lane < 16);
-      if (n < kKeys) in = in && at0 + 32 * (other ? rank ^ 1 : rank) < n;
-      raw[k] = in ? __ldg(reinterpret_cast<const uint4*>(r + off[k])) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    auto store = [&](uint8_t* slot, int k) {
-      int box, key, c;
-      place(k, box, key, c);
-      if (box >= 13) return;
-      uint8_t* d = slot + (k < 4 ? box & 3 : box - 8) * kBox + key * 128;
-      const uint4 v = raw[k];
-      *reinterpret_cast<uint4*>(d + (((2 * c) ^ (key & 7)) << 4)) =
-          make_uint4(e4m3x2_to_bf16x2(v.x, 0x1404), e4m3x2_to_bf16x2(v.x, 0x3424), e4m3x2_to_bf16x2(v.y, 0x1404),
-                     e4m3x2_to_bf16x2(v.y, 0x3424));
-      *reinterpret_cast<uint4*>(d + (((2 * c + 1) ^ (key & 7)) << 4)) =
-          make_uint4(e4m3x2_to_bf16x2(v.z, 0x1404), e4m3x2_to_bf16x2(v.z, 0x3424), e4m3x2_to_bf16x2(v.w, 0x1404),
-                     e4m3x2_to_bf16x2(v.w, 0x3424));
-    };
-    for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
-      const uint8_t* r = tile_rows(it, it.t0);
-      const uint8_t* r1 = tile_rows(it, it.t0 + 1);  // the block table is read two tiles ahead, the codes one
-#pragma unroll
-      for (int k = 0; k < STEPS; ++k) fetch(r, it.len - it.t0 * kKeys, k);
-      for (int t = it.t0; ok && t < it.t1; ++t) {
-        r = r1;
-        r1 = tile_rows(it, t + 2);
-        const int n = it.len - (t + 1) * kKeys;
-        // steps [k0, k1) into a slot
-        auto fill = [&](uint8_t* slot, int k0, int k1, uint64_t* full) {
-#pragma unroll
-          for (int k = 0; k < STEPS; ++k) {
-            if (k >= k0 && k < k1) {
-              store(slot, k);
-              fetch(r, n, k);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full);
-        };
-        ok = __all_sync(0xffffffffu, wait(a, &a->a_empty[as], aph ^ 1, err));
+        if (lane == 0) mbar_arrive(&a->c_empty[cs]);
+        if (++cs == C::CS) cs = 0, cph ^= 1;
+        ok = __all_sync(0xffffffffu, wait(a, &a->v_empty[0], (tiles & 1) ^ 1, err));
         if (!ok) break;
-        fill(a_s + as * kSlotV, 0, 2, &a->a_full[as]);
-        if (++as == C::AS) as = 0, aph ^= 1;
-        ok = __all_sync(0xffffffffu, wait(a, &a->k_empty[ks], kph ^ 1, err));
-        if (!ok) break;
-        fill(k_s + ks * kSlotK, 4, STEPS, &a->k_full[ks]);
-        if (++ks == C::KS) ks = 0, kph ^= 1;
-        ok = __all_sync(0xffffffffu, wait(a, &a->b_empty[bs], bph ^ 1, err));
-        if (!ok) break;
-        fill(b_s + bs * kSlotV, 2, 4, &a->b_full[bs]);
-        if (++bs == C::BS) bs = 0, bph ^= 1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int key = 8 * (w + 4 * (k >> 2)) + (lane >> 2);
+          uint8_t* d = v_s + (k & 3) * kBox + key * 128;
+          const uint4 v = raw[k];
+          *reinterpret_cast<uint4*>(d + (((2 * c) ^ (key & 7)) << 4)) =
+              make_uint4(e4m3x2_to_bf16x2(v.x, 0x1404), e4m3x2_to_bf16x2(v.x, 0x3424), e4m3x2_to_bf16x2(v.y, 0x1404),
+                         e4m3x2_to_bf16x2(v.y, 0x3424));
+          *reinterpret_cast<uint4*>(d + (((2 * c + 1) ^ (key & 7)) << 4)) =
+              make_uint4(e4m3x2_to_bf16x2(v.z, 0x1404), e4m3x2_to_bf16x2(v.z, 0x3424), e4m3x2_to_bf16x2(v.w, 0x1404),
+                         e4m3x2_to_bf16x2(v.w, 0x3424));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&a->v_full[0]);
       }
     }
   } else if (warp >= 4) {
-    // ---- softmax warps: thread = row = tensor-memory lane, half h of this CTA's 32 positions
+    // ---- softmax warps: thread = row = tensor-memory lane, half h of the tile's positions
     const int w = warp - 4, h = w >> 2, quarter = w & 3, row = 32 * quarter + lane, st = tid - 128;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
-    const uint32_t peer_mx = dsmem_addr(&a->mx[0][h][row], rank ^ 1), peer_mm = dsmem_addr(&a->m_msg[0], rank ^ 1);
-    const uint32_t peer_clear = dsmem_addr(&a->clear[0][w], rank ^ 1);
-    const uint32_t peer_p = dsmem_addr(p_s, rank ^ 1) + rank * C::P_HALF + 32 * quarter * 64;
-    const uint32_t peer_pm = dsmem_addr(&a->p_msg[0], rank ^ 1);
-    const uint32_t peer_stat = dsmem_addr(&a->stat[h][row], rank ^ 1), peer_sf = dsmem_addr(&a->stat_full, rank ^ 1);
-    const int p_at = row * 64, p_sw = (row >> 1) & 3;  // this row in a half of P, and its swizzle
+    uint8_t* p_row = p_s + row * 128;
+    const int rows = p.q_per_seq * p.H;
     int tile = 0, items = 0;
     uint32_t su = 0;
     bool ok = true;
-    const int rows = p.q_per_seq * p.H;
 
     for (int i = 0; get_item(p, pl, a, i, it); ++i) {
       const int row_lo = it.rt * kRows;
@@ -842,28 +749,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         }
         continue;
       }
-      // the query's row: most boxes into tensor memory, the others into shared memory, half of them per half h
-      // (the previous item's products are done: its epilogue waited for them)
+      float row_scale = p.scale_log2;
+      // the query's row, its boxes in the order of the slots: the first ones into tensor memory, the others into
+      // shared memory, half of each per half h (the previous item's products are done: its epilogue waited for them)
       {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (at + (row < nrows ? row : 0)) * kDqk);
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        auto box = [&](int j) { return src + 8 * (j < 8 ? j ^ (rank << 2) : 8); };
+        if constexpr (C::FP8) {
+          // scaled by a power of two, the row's largest value to [2^7, 2^8), and split into two 8-bit parts: per box
+          // and half of its columns 32 bytes of the one, then of the other
+          uint32_t top = 0;
 #pragma unroll 4
-        for (int k = 0; k < 4 * (9 - C::BT); ++k) {
-          const int c = 2 * k + h;
-          cp_async16(q_s + (c >> 3) * C::Q_BOX + row * 128 + (((c & 7) ^ (row & 7)) << 4), src + 8 * C::BT + c, row < nrows);
-        }
-        cp_async_commit();
-#pragma unroll 4
-        for (int g = 0; g < C::BT; ++g) {
-          uint32_t v[16];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 u = row < nrows ? __ldg(src + 8 * g + 4 * h + k) : zero;
-            v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
+          for (int g = 0; g < 36; ++g) {
+            const uint4 u = row < nrows ? __ldg(src + 36 * h + g) : zero;
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu)));
           }
-          tmem_st16(lane_base + kColQ + 32 * g + 16 * h, v);
+          a->mx[0][h][row] = __uint_as_float(max(top & 0xFFFFu, top >> 16) << 16);
+          pair_bar(quarter);
+          const int e = (__float_as_int(fmaxf(a->mx[0][0][row], a->mx[0][1][row])) >> 23) - 127;
+          const int up = min(7 - e, 126);
+          const float mul = __int_as_float((up + 127) << 23);
+          // (an infinity or NaN in the row: every logit is NaN)
+          row_scale = e == 128 ? __int_as_float(0x7FC00000) : p.scale_log2 * __int_as_float((127 - up) << 23);
+#pragma unroll 1
+          for (int g = 0; g < 9; ++g) {
+            uint32_t v[16];  // 32 values as E4M3, the same as E5M2
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 u = row < nrows ? __ldg(box(g) + 4 * h + k) : zero;
+              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int n = 0; n < 2; ++n) {
+                uint32_t a0, a1, b0, b1;
+                split_fp8(__uint_as_float(w[2 * n] << 16) * mul, __uint_as_float(w[2 * n] & 0xFFFF0000u) * mul, a0, b0);
+                split_fp8(__uint_as_float(w[2 * n + 1] << 16) * mul, __uint_as_float(w[2 * n + 1] & 0xFFFF0000u) * mul, a1, b1);
+                v[2 * k + n] = a0 | a1 << 16;
+                v[8 + 2 * k + n] = b0 | b1 << 16;
+              }
+            }
+            if (g < C::BT) {
+              tmem_st16(lane_base + C::COL_Q + 32 * g + 16 * h, v);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4*>(q_s + (g - C::BT) * C::Q_BOX + row * 128 + (((4 * h + k) ^ (row & 7)) << 4)) =
+                    make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+          }
+          pair_bar(quarter);  // (the maxima have been read)
+        } else {
+#pragma unroll 4
+          for (int k = 0; k < 4 * (9 - C::BT); ++k) {
+            const int b = k >> 2, c = 2 * (k & 3) + h;
+            cp_async16(q_s + b * C::Q_BOX + row * 128 + ((c ^ (row & 7)) << 4), box(C::BT + b) + c, row < nrows);
+          }
+          cp_async_commit();
+#pragma unroll 3
+          for (int g = 0; g < C::BT; ++g) {
+            uint32_t v[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 u = row < nrows ? __ldg(box(g) + 4 * h + k) : zero;
+              v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
+            }
+            tmem_st16(lane_base + C::COL_Q + 32 * g + 16 * h, v);
+          }
+          cp_async_wait<0>();
         }
-        cp_async_wait<0>();
         tmem_wait_st();
         tc_fence_before();
         fence_proxy_async_smem();
@@ -872,97 +825,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
       const int node = min((row_lo + row) / p.H, p.q_per_seq - 1);
       float m = -INFINITY, l = 0.f;
 
-      // Logits of tile n (position tile t) for this row, scaled and masked; their maximum goes to the other
-      // half's warp and to the other CTA.
-      auto stage = [&](int n, int t, float (&x)[16]) {
-        const float* sc = sc_s + (n % C::SC_DEPTH) * 32 * C::NSC + 16 * h;
-        if constexpr (C::FP8) ok = wait(a, &a->sc_full[n % C::SC_DEPTH], (n / C::SC_DEPTH) & 1, err) && ok;
+      for (int t = it.t0; t < it.t1; ++t, ++tile) {
+        // ---- logits, scaled and masked
+        float x[32];
+        const float* sc = sc_s + (tile & 1) * kKeys * C::NSC + 32 * h;
+        if constexpr (C::FP8) ok = wait(a, &a->sc_full[tile & 1], (tile >> 1) & 1, err) && ok;
         if constexpr (C::TILED) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = 0.f;
+          for (int k = 0; k < 32; ++k) x[k] = 0.f;
         }
 #pragma unroll 1
         for (int g = 0; g < C::GROUPS; ++g, ++su) {
           ok = wait(a, &a->s_full[su % C::SB], (su / C::SB) & 1, err) && ok;
           tc_fence_after();
-          float s[16];
-          tmem_ld_sync(lane_base + C::COL_S + 32 * (su % C::SB) + 16 * h, s);
+          float s[32];
+          tmem_ld_sync(lane_base + C::COL_S + kKeys * (su % C::SB) + 32 * h, s);
           tc_fence_before();
           __syncwarp();
           if (lane == 0 && ok) mbar_arrive(&a->s_empty[su % C::SB]);
+          // (the groups are in the order of the slots, the scales in that of the columns)
+          const float* scg = sc + kKeys * (g < 4 ? g ^ (rank << 1) : 4) * C::TILED;
 #pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            float4 f = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
-            if constexpr (C::FP8) f = *reinterpret_cast<const float4*>(sc + 32 * g + k);
+          for (int k = 0; k < 32; k += 4) {
+            float4 f = make_float4(row_scale, row_scale, row_scale, row_scale);
+            if constexpr (C::FP8) f = *reinterpret_cast<const float4*>(scg + k);
             if constexpr (C::TILED) {
               x[k] = fmaf(f.x, s[k], x[k]), x[k + 1] = fmaf(f.y, s[k + 1], x[k + 1]);
               x[k + 2] = fmaf(f.z, s[k + 2], x[k + 2]), x[k + 3] = fmaf(f.w, s[k + 3], x[k + 3]);
             } else {
-              if constexpr (C::FP8) f.x *= p.scale_log2, f.y *= p.scale_log2, f.z *= p.scale_log2, f.w *= p.scale_log2;
+              if constexpr (C::FP8) f.x *= row_scale, f.y *= row_scale, f.z *= row_scale, f.w *= row_scale;
               x[k] = s[k] * f.x, x[k + 1] = s[k + 1] * f.y, x[k + 2] = s[k + 2] * f.z, x[k + 3] = s[k + 3] * f.w;
             }
           }
         }
         if constexpr (C::TILED) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] *= p.scale_log2;
+          for (int k = 0; k < 32; ++k) x[k] *= row_scale;
         }
-        const bool bad = p.pages.table && a->tile_bad[n & 7];
+        const bool bad = p.pages.table && a->tile_bad[tile & 7];
+        const bool edge = (t + 1) * kKeys > it.ctx;  // drafted positions, or the sequence's end
         uint32_t clear = 0;
-        if ((t + 1) * kKeys > it.ctx || bad) {
-          const uint32_t see = bad ? 0u : (uint32_t)(seen_bits(p, it, node, t) >> (32 * rank + 16 * h));
+        if (edge || bad) {
+          const uint32_t see = bad ? 0u : (uint32_t)(seen_bits(p, it, node, t) >> (32 * h));
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
+          for (int k = 0; k < 32; ++k) {
             if (!((see >> k) & 1)) {
               // a hidden position that may hold infinities or NaN (its logit is not finite, or it lies past
               // the end): its values are cleared in the tile, so that 0 * value is 0
-              if (!C::FP8 && (!(fabsf(x[k]) < INFINITY) || t * kKeys + 32 * rank + 16 * h + k >= it.len)) clear |= 1u << (16 * h + k);
+              if (!C::FP8 && (!(fabsf(x[k]) < INFINITY) || t * kKeys + 32 * h + k >= it.len)) clear |= 1u << k;
               x[k] = -INFINITY;
             }
           }
-          clear = __reduce_or_sync(0xffffffffu, clear);
         }
-        float mx = x[0];
+        // ---- the rows' maxima over the tile
+        float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int k = 1; k < 16; ++k) mx = fmaxf(mx, x[k]);
-        const int slot = n & 3;
-        a->mx_own[n & 1][h][row] = mx;
-        if (lane == 0) a->clear_own[slot][w] = clear;
-        if (ok) {
-          st_async4(peer_mx + slot * (2 * kRows * 4), __float_as_uint(mx), peer_mm + 8 * slot);
-          if (lane == 0) st_async4(peer_clear + slot * 32, clear, peer_mm + 8 * slot);
-        }
-        __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(&a->m_msg[slot]);
-      };
-
-      float x[16], y[16];
-      stage(tile, it.t0, x);
-      for (int t = it.t0; t < it.t1; ++t, ++tile) {
-        // the next tile's logits first, if they are there: their maxima travel while this tile is finished.  (With
-        // tile scales always: there an S buffer is refilled only when all eight warps have read it, so they have
-        // to take the tiles' steps in one order.)
-        const bool more = t + 1 < it.t1;
-        bool staged = false;
-        if (more && (C::TILED || __all_sync(0xffffffffu, mbar_test(&a->s_full[su % C::SB], (su / C::SB) & 1)))) {
-          stage(tile + 1, t + 1, y);
-          staged = true;
-        }
-        const int slot = tile & 3, pb = tile % C::PB;
-        ok = wait_cluster(a, &a->m_msg[slot], (tile >> 2) & 1, err) && ok;
-        const float top = fmaxf(fmaxf(a->mx_own[tile & 1][0][row], a->mx_own[tile & 1][1][row]),
-                                fmaxf(a->mx[slot][0][row], a->mx[slot][1][row]));
-        if (!C::FP8 && (t + 1) * kKeys > it.ctx) {
+        for (int k = 4; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], x[k]);
+        const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        a->mx[tile & 1][h][row] = mine;
+        if (!C::FP8 && edge) {
           // zero the value columns of the positions to clear (their logits have been taken): a position past the
           // end always, another one only if it holds something that is not finite
-          uint32_t clear[2] = {0u, 0u};  // ours, the other's
+          clear = __reduce_or_sync(0xffffffffu, clear);
+          if (lane == 0) a->clear[tile & 1][w] = clear;
+          softmax_bar();
+          const int key = st >> 2;  // a position, one of its four boxes
+          uint32_t word = 0u;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) clear[0] |= a->clear_own[slot][k], clear[1] |= a->clear[slot][k];
-          const int who = st >> 7, key = (st >> 2) & 31;  // a position, one of its four boxes
-          if ((clear[who] >> key) & 1) {
-            uint8_t* line = (who ? b_s + (tile % C::BS) * kSlotV : a_s + (tile % C::AS) * kSlotV) + (st & 3) * kBox + key * 128;
-            bool zero = t * kKeys + 32 * (who ? rank ^ 1 : rank) + key >= it.len;
-            if (who) ok = wait(a, &a->b_full[tile % C::BS], (tile / C::BS) & 1, err) && ok;  // (loaded for the second product only)
+          for (int k = 0; k < 4; ++k) word |= a->clear[tile & 1][(key >> 5) * 4 + k];
+          if ((word >> (key & 31)) & 1) {
+            uint8_t* line = v_s + (tile % C::VS) * kSlotV + (st & 3) * kBox + key * 128;
+            bool zero = t * kKeys + key >= it.len;
             if (!zero) {
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
@@ -979,8 +912,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
             }
           }
           __syncwarp();
+        } else {
+          pair_bar(quarter);
         }
-        // the reference maximum moves, in both halves' warps and in the other CTA alike
+        const float top = fmaxf(mine, a->mx[tile & 1][h ^ 1][row]);
+        // the second product of the tile before is done: O may be rescaled, P written
+        if (tile > 0) ok = wait(a, &a->pv_done, (tile - 1) & 1, err) && ok;
+        // the reference maximum moves, in both halves' warps alike
         if (__any_sync(0xffffffffu, top > m + kLazy)) {
           float f = 1.f;
           if (top > m + kLazy) {  // (m = -inf: nothing summed yet, the factor is 0)
@@ -989,8 +927,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
             l *= f;
           }
           if (t > it.t0) {
-            // the second product of the tile before is done: O may be rescaled (half of its columns per warp)
-            ok = wait(a, &a->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, err) && ok;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 128 * h; c < 128 * h + 128; c += 16) {
@@ -1004,28 +940,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
             tmem_wait_st();
           }
         }
-        // ---- weights
+        // ---- weights, times the positions' scales (a hidden position's weight is 0 whatever its scale holds)
         const float mu = m == -INFINITY ? 0.f : m;
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < 32; ++k) {
           x[k] = ex2(x[k] - mu);
-          l += x[k];
+          sum[k & 1] += x[k];
         }
-        // the tile that used this P buffer has been added, here and in the other CTA (so the copies of it have left)
-        if (tile >= C::PB) ok = wait(a, &a->pv_done[(tile - C::PB) & 1], ((tile - C::PB) >> 1) & 1, err) && ok;
-        ok = wait_cluster(a, &a->p_free[pb], ((tile / C::PB) & 1) ^ 1, err) && ok;
-        const float* sc = sc_s + (tile % C::SC_DEPTH) * 32 * C::NSC + 16 * h;
-        // P, times the positions' scales (a hidden position's weight is 0 whatever its scale holds)
-        const bool hides = C::FP8 && ((t + 1) * kKeys > it.ctx || (p.pages.table && a->tile_bad[tile & 7]));
-        auto put = [&](uint8_t* dst, int g) {
+        l += sum[0] + sum[1];
+        const bool hides = C::FP8 && (edge || bad);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {  // 16-byte chunks of eight positions
+        for (int b = 0; b < C::PC; ++b) {
+          const float* scb = sc + kKeys * (2 * rank + b) * C::TILED;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // 16-byte chunks of eight positions
             float z[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) z[k] = x[8 * j + k];
             if constexpr (C::FP8) {
-              const float4 f0 = *reinterpret_cast<const float4*>(sc + 32 * g + 8 * j);
-              const float4 f1 = *reinterpret_cast<const float4*>(sc + 32 * g + 8 * j + 4);
+              const float4 f0 = *reinterpret_cast<const float4*>(scb + 8 * j);
+              const float4 f1 = *reinterpret_cast<const float4*>(scb + 8 * j + 4);
               z[0] *= f0.x, z[1] *= f0.y, z[2] *= f0.z, z[3] *= f0.w;
               z[4] *= f1.x, z[5] *= f1.y, z[6] *= f1.z, z[7] *= f1.w;
               if (hides) {
@@ -1033,49 +968,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
                 for (int k = 0; k < 8; ++k) z[k] = x[8 * j + k] == 0.f ? 0.f : z[k];
               }
             }
-            *reinterpret_cast<uint4*>(dst + p_at + (((2 * h + j) ^ p_sw) << 4)) =
+            *reinterpret_cast<uint4*>(p_row + b * C::P_BYTES + (((4 * h + j) ^ (row & 7)) << 4)) =
                 make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
           }
-        };
-#pragma unroll
-        for (int pc = 0; pc < C::PC; ++pc) {
-          put(p_s + (pb * C::PC + pc) * C::P_BYTES + rank * C::P_HALF, C::TILED ? 2 * rank + pc : 0);
-          if (C::TILED) put(pp_s + pc * C::P_HALF, 2 * (rank ^ 1) + pc);  // the scales of the other's value tiles
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        pair_bar(quarter);  // both halves of the 32 rows are there
+        __syncwarp();
         if (lane == 0 && ok) {
-          if (h == 0) {
-#pragma unroll
-            for (int pc = 0; pc < C::PC; ++pc)
-              copy_remote(peer_p + (pb * C::PC + pc) * C::P_BYTES,
-                          (C::TILED ? pp_s + pc * C::P_HALF : p_s + pb * C::P_BYTES + rank * C::P_HALF) + 32 * quarter * 64,
-                          32 * 64, peer_pm + 8 * pb);
-            copy_commit();
-          } else if (quarter == 0) {
-            mbar_arrive_expect_tx(&a->m_msg[slot], kMaxBytes);  // for the tile four on
-          }
-          if constexpr (C::FP8) mbar_arrive(&a->sc_empty[tile % C::SC_DEPTH]);
-          mbar_arrive(&a->p_full[tile & 1]);
-        }
-        if (more) {
-          if (!staged) stage(tile + 1, t + 1, y);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = y[k];
+          mbar_arrive(&a->p_full);
+          if constexpr (C::FP8) mbar_arrive(&a->sc_empty[tile & 1]);
         }
       }
-      // ---- the item's sums, to the other CTA as well
-      a->mx_own[0][h][row] = l;
-      if (ok) st_async4(peer_stat, __float_as_uint(l), peer_sf);
-      ok = wait_cluster(a, &a->stat_full, items & 1, err) && ok;
-      softmax_bar();
-      {
-        // (added in the same order on both sides)
-        const float mine = a->mx_own[0][0][row] + a->mx_own[0][1][row], theirs = a->stat[0][row] + a->stat[1][row];
-        l = rank ? theirs + mine : mine + theirs;
-      }
-      if (st == 0 && ok) mbar_arrive_expect_tx(&a->stat_full, 2 * kRows * 4);
+      // ---- the rows' sums (their halves added in the same order everywhere)
+      a->sum[h][row] = l;
+      pair_bar(quarter);
+      l = a->sum[0][row] + a->sum[1][row];
       const bool live = row < nrows && (row_lo + row) / p.H < it.fresh;
       const float inv = live && l != 0.f ? 1.f / l : 0.f;
       if (rank == 0 && h == 0) {
@@ -1105,16 +1013,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FMT>::THREADS, 1
         }
         __syncwarp();
       }
-      softmax_bar();  // the sums have been read
+      pair_bar(quarter);  // the sums have been read
       tc_fence_before();
       if (lane == 0 && ok) mbar_arrive(&a->o_free);
       ++items;
     }
   }
-  copy_wait_read();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // no CTA leaves while the other may still write into its shared memory
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -1179,15 +1085,15 @@ __global__ void tree_nothing_kernel(const TreeAttnParams p, int64_t rows) {
   if (p.lse && i < rows) p.lse[i] = -INFINITY;
 }
 
-constexpr int kClusters = 76;  // two of the 152 SMs each
+constexpr int kPairs = 76;  // of CTAs: two of the 152 SMs each
 
 // A launch with many units needs no split: its rounds of the grid are full enough.
 TreePlan plan_of(const TreeAttnParams& p) {
   TreePlan pl = {};
   pl.row_tiles = (p.q_per_seq * p.H + kRows - 1) / kRows;
   pl.units = p.n_seq * pl.row_tiles;
-  pl.cap = pl.units <= kItemsPerCta * kClusters ? kItemsPerCta * kClusters : 0;
-  pl.grid = pl.cap ? kClusters : (pl.units < kClusters ? pl.units : kClusters);
+  pl.cap = pl.units <= kItemsPerCta * kPairs ? kItemsPerCta * kPairs : 0;
+  pl.grid = pl.cap ? kPairs : (pl.units < kPairs ? pl.units : kPairs);
   return pl;
 }
 
@@ -1203,9 +1109,10 @@ cudaError_t launch_fmt(const TreeAttnParams& p, TreePlan pl, void* ws, cudaStrea
                                  paged || p.n_seq == 1 ? n * (cuuint64_t)p.kv_row_stride : (cuuint64_t)p.kv_seq_stride};
   CUtensorMap tm;
   memset(&tm, 0, sizeof(tm));
-  const cuuint32_t box[3] = {64, 32, 1};
-  if (!C::FP8 && encode_tensor_map(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint8_t*>(p.kv), dims, strides, box,
-                                   CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+  const cuuint32_t box[3] = {64, kKeys, 1};
+  if (encode_tensor_map(&tm, C::FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                        const_cast<uint8_t*>(p.kv), dims, strides, box,
+                        C::FP8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   if (pl.cap) {
     uint8_t* w = reinterpret_cast<uint8_t*>(ws);
