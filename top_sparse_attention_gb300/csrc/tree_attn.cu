@@ -56,12 +56,13 @@ constexpr int kSlotC = 9 * kBoxC;
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLazy = 8.f;              // log2 growth of a row's maximum that is left unscaled
 constexpr int kItemsPerCta = 3;           // split launches are cut into at most this many items per cluster
+constexpr int kAhead = 3;                 // tiles between the request to L2 and the load into shared memory
 constexpr int kColO = 0;                  // tensor-memory columns: O, then boxes of q, then S
 
 enum { kBf16 = 0, kFp8Row = 1, kFp8Tile = 2 };
 
 struct Aux {
-  uint64_t v_full[3], v_empty[3], k_full[7], k_empty[7], c_full[3], c_empty[3], s_full[2], s_empty[2], p_full, pv_done;
+  uint64_t v_full[3], v_empty[3], k_full[7], k_empty[7], c_full[2], c_empty[2], s_full[2], s_empty[2], p_full, pv_done;
   uint64_t o_done, o_free, q_full, sc_full[2], sc_empty[2], drain;
   uint32_t tmem;
   int abort;
@@ -81,24 +82,22 @@ struct Cfg {
   static constexpr int THREADS = FP8 ? 512 : 384;
   // bf16: slots of this CTA's value columns (held from the first product to the second) and boxes of the others
   // (first product only).  E4M3: slots of a tile's codes, and of the value columns widened to bf16.
-  static constexpr int VS = FP8 ? 1 : 3, KS = FP8 ? 0 : 7, CS = TILED ? 2 : FP8 ? 3 : 0;
+  static constexpr int VS = TILED ? 1 : FP8 ? 2 : 3, KS = FP8 ? 0 : 7, CS = FP8 ? 2 : 0;
   static constexpr int SB = TILED ? 2 : 1;                // S buffers
-  static constexpr int BT = TILED ? 4 : 6;                // q's boxes in tensor memory (the others are in shared memory)
-  static constexpr int COL_Q = 256, COL_S = COL_Q + 32 * BT;
+  static constexpr int BT = TILED ? 2 : 5;                // q's boxes in tensor memory (the others are in shared memory)
+  static constexpr int COL_Q = 256, COL_S = COL_Q + 32 * BT, COL_P = COL_S + kKeys * SB;
   static constexpr int GROUPS = TILED ? 5 : 1;            // S accumulations per tile
   static constexpr int PC = TILED ? 2 : 1;                // copies of P (one per 128 values)
   static constexpr int SC_BYTES = NSC * kKeys * 4;
   static constexpr int Q_BOX = kRows * 128, Q_BYTES = (9 - BT) * Q_BOX;
-  static constexpr int P_BYTES = kRows * 128;             // 128 rows x 64 positions
   static constexpr int OFF_K = VS * kSlotV;
   static constexpr int OFF_C = OFF_K + KS * kBox;
   static constexpr int OFF_Q = OFF_C + CS * kSlotC;
-  static constexpr int OFF_P = OFF_Q + Q_BYTES;
-  static constexpr int OFF_SC = OFF_P + PC * P_BYTES;
+  static constexpr int OFF_SC = OFF_Q + Q_BYTES;
   static constexpr int OFF_AUX = OFF_SC + 2 * SC_BYTES;
   static constexpr int SMEM = OFF_AUX + (int)sizeof(Aux) + 1024;
   static_assert(SMEM <= kSmemMax, "shared memory");
-  static_assert(COL_S + kKeys * SB <= 512, "tensor memory");
+  static_assert(COL_P + 32 * PC <= 512, "tensor memory");
 };
 
 struct Item {
@@ -151,9 +150,10 @@ __device__ __forceinline__ bool wait(Aux* a, uint64_t* bar, uint32_t parity, int
 __device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
   const unsigned long long t0 = globaltimer_ns();
   for (uint32_t i = 0;; ++i) {
-    if (*reinterpret_cast<volatile int*>(&a->abort)) return false;
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 63u && globaltimer_ns() - t0 > kWaitLimitNs) {
+    if ((i & 15u) != 15u) continue;
+    if (*reinterpret_cast<volatile int*>(&a->abort)) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
       record_error(err, DSA_DEVERR_WAIT_TIMEOUT);
       *reinterpret_cast<volatile int*>(&a->abort) = 1;
       return false;
@@ -242,15 +242,19 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
         : "memory");
 }
 
-// Two values v (|v| < 2^8, of bf16) as E4M3 plus E5M2: the first takes four of the eight significant bits, what is
-// left is a multiple of the last bit of at most eight of them, which three bits hold.  So v = e4 + e5 exactly for
-// |v| >= 2^-6, and to 2^-13 below.
-__device__ __forceinline__ void split_fp8(float lo, float hi, uint32_t& e4, uint32_t& e5) {
-  const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-  const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3);
-  const float2 f = __half22float2(__half2(back));
+// Two bf16 values, times mul (a power of two that brings them below 2^8), as E4M3 plus E5M2: the first takes four of
+// the eight significant bits, what is left is a multiple of the last bit of at most eight of them, which three bits
+// hold.  So v = e4 + e5 exactly for |v| >= 2^-6, and to 2^-13 below (fp16 holds the values between, to 2^-25).
+__device__ __forceinline__ void split_fp8(uint32_t x, float mul, uint32_t& e4, uint32_t& e5) {
+  const __half2 v = __floats2half2_rn(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xFFFF0000u) * mul);
+  const __nv_fp8x2_storage_t a = __nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
   e4 = a;
-  e5 = __nv_cvt_float2_to_fp8x2(make_float2(lo - f.x, hi - f.y), __NV_SATFINITE, __NV_E5M2);
+  e5 = __nv_cvt_halfraw2_to_fp8x2(__hsub2(v, __half2(__nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3))), __NV_SATFINITE, __NV_E5M2);
+}
+
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* tm, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(tm), "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 
 // Registers -> tensor memory: this thread's lane, 16 columns.
@@ -430,7 +434,6 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
   uint8_t* k_s = smem + C::OFF_K;
   uint8_t* c_s = smem + C::OFF_C;
   uint8_t* q_s = smem + C::OFF_Q;
-  uint8_t* p_s = smem + C::OFF_P;
   float* sc_s = reinterpret_cast<float*>(smem + C::OFF_SC);
   Aux* a = reinterpret_cast<Aux*>(smem + C::OFF_AUX);
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
@@ -467,15 +470,27 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
   const uint32_t tmem = a->tmem;
   pdl_launch_dependents();
 
-  Item it;
+  Item it = {};
   if (warp == 0) {
     // ---- producer: boxes of 64 columns x 64 positions by TMA
     if (lane == 0) {
       prefetch_tmap(&tm);
       int vs = 0, vph = 0, ks = 0, kph = 0, cs = 0, cph = 0, tiles = 0;
       bool ok = true;
+      // Tiles on their way to L2, this CTA's value columns of them (the other one of the pair asks for the others):
+      // the slots alone do not cover the latency of the memory.
+      auto ahead = [&](int t) {
+        if (t >= it.t1) return;
+        int64_t row = t * kKeys;
+        if (p.pages.table && (row = tree_row(p, it.seq, (int)row)) < 0) return;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) tma_prefetch_3d(&tm, 256 * rank + 64 * b, (int)row, p.pages.table ? 0 : it.seq);
+        if (rank) tma_prefetch_3d(&tm, 512, (int)row, p.pages.table ? 0 : it.seq);
+      };
       for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
+        for (int t = it.t0; !C::FP8 && t < it.t0 + kAhead; ++t) ahead(t);
         for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
+          if (!C::FP8) ahead(t + kAhead);
           int row = t * kKeys, z = it.seq, bad = 0;
           if (p.pages.table) {
             const int64_t r = tree_row(p, it.seq, row);
@@ -530,9 +545,9 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
     const uint32_t tm_base = (uint32_t)uniform((int)tmem);
     const uint32_t kv_lo = kmajor_lo(smem_u32(v_s)), kk_lo = kmajor_lo(smem_u32(k_s));
     const uint32_t vv_lo = mnmajor_lo(smem_u32(v_s)), c_lo = kmajor_lo(smem_u32(c_s));
-    const uint32_t q_lo = kmajor_lo(smem_u32(q_s)), p_lo = kmajor_lo(smem_u32(p_s));
+    const uint32_t q_lo = kmajor_lo(smem_u32(q_s));
     int vs = 0, vph = 0, ks = 0, kph = 0, cs = 0, cph = 0;  // slots of the first product
-    int ps = 0;                                             // of the second
+    int ps = 0, pph = 0;                                    // of the second
     int tile = 0, items = 0;
     uint32_t su = 0;                       // uses of the S buffers
     bool ok = true;
@@ -609,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
       uint64_t* bar = &a->p_full;
       uint32_t parity = tile & 1;
       if (first && lane == 1) bar = &a->o_free, parity = (items & 1) ^ 1;
-      if (C::FP8 && lane == 2) bar = &a->v_full[0];
+      if (C::FP8 && lane == 2) bar = &a->v_full[ps], parity = pph;
       all(bar, parity);
       if (!ok) return;
       tc_fence_after();
@@ -620,13 +635,13 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            mma_ss(tm_base + kColO + 128 * b, p_lo + (b * C::P_BYTES >> 4) + 2 * s, V + (2 * b * kBox + 2048 * s) / 16, idesc_pv,
+            mma_ts(tm_base + kColO + 128 * b, tm_base + C::COL_P + 32 * b + 8 * s, V + (2 * b * kBox + 2048 * s) / 16, idesc_pv,
                    s ? 1u : acc0);
         tc_commit(&a->v_empty[ps]);
         tc_commit(&a->pv_done);
       }
       __syncwarp();
-      if (++ps == C::VS) ps = 0;
+      if (++ps == C::VS) ps = 0, pph ^= 1;
       ++tile;
     };
     for (int i = 0; ok && uniform(get_item(p, pl, a, i, it)); ++i) {
@@ -692,10 +707,10 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
     // 16 codes per lane and step: eight positions of a box, four lanes each, so that eight lanes' 16-byte loads
     // and stores fall into different banks.
     const int w = warp - 12, c = lane & 3;
-    int cs = 0, cph = 0, tiles = 0;
+    int cs = 0, cph = 0, vs = 0, vph = 0;
     bool ok = true;
     for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
-      for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
+      for (int t = it.t0; ok && t < it.t1; ++t) {
         ok = __all_sync(0xffffffffu, wait(a, &a->c_full[cs], cph, err));
         if (!ok) break;
         const uint8_t* src = c_s + cs * kSlotC;
@@ -708,12 +723,12 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&a->c_empty[cs]);
         if (++cs == C::CS) cs = 0, cph ^= 1;
-        ok = __all_sync(0xffffffffu, wait(a, &a->v_empty[0], (tiles & 1) ^ 1, err));
+        ok = __all_sync(0xffffffffu, wait(a, &a->v_empty[vs], vph ^ 1, err));
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int key = 8 * (w + 4 * (k >> 2)) + (lane >> 2);
-          uint8_t* d = v_s + (k & 3) * kBox + key * 128;
+          uint8_t* d = v_s + vs * kSlotV + (k & 3) * kBox + key * 128;
           const uint4 v = raw[k];
           *reinterpret_cast<uint4*>(d + (((2 * c) ^ (key & 7)) << 4)) =
               make_uint4(e4m3x2_to_bf16x2(v.x, 0x1404), e4m3x2_to_bf16x2(v.x, 0x3424), e4m3x2_to_bf16x2(v.y, 0x1404),
@@ -724,14 +739,14 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&a->v_full[0]);
+        if (lane == 0) mbar_arrive(&a->v_full[vs]);
+        if (++vs == C::VS) vs = 0, vph ^= 1;
       }
     }
   } else if (warp >= 4) {
     // ---- softmax warps: thread = row = tensor-memory lane, half h of the tile's positions
     const int w = warp - 4, h = w >> 2, quarter = w & 3, row = 32 * quarter + lane, st = tid - 128;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
-    uint8_t* p_row = p_s + row * 128;
     const int rows = p.q_per_seq * p.H;
     int tile = 0, items = 0;
     uint32_t su = 0;
@@ -750,22 +765,73 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         continue;
       }
       float row_scale = p.scale_log2;
-      // the query's row, its boxes in the order of the slots: the first ones into tensor memory, the others into
-      // shared memory, half of each per half h (the previous item's products are done: its epilogue waited for them)
+      // The query's rows, their boxes in the order of the slots: the first ones into tensor memory, the others into
+      // shared memory (the previous item's products are done: its epilogue waited for them).  A warp takes half h of
+      // each box of its 32 rows; four lanes read 64 bytes of a row (a lane per row would touch 32 lines per load:
+      // 6.7 us for the whole), and 2 KB per warp of the other boxes' memory turn them into rows per lane.
       {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (at + (row < nrows ? row : 0)) * kDqk);
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        auto box = [&](int j) { return src + 8 * (j < 8 ? j ^ (rank << 2) : 8); };
-        if constexpr (C::FP8) {
-          // scaled by a power of two, the row's largest value to [2^7, 2^8), and split into two 8-bit parts: per box
-          // and half of its columns 32 bytes of the one, then of the other
-          uint32_t top = 0;
-#pragma unroll 4
-          for (int g = 0; g < 36; ++g) {
-            const uint4 u = row < nrows ? __ldg(src + 36 * h + g) : zero;
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu)));
+        const int r4 = lane >> 2, c4 = lane & 3;
+        const __nv_bfloat16* src = p.q + (at + 32 * quarter) * kDqk + 32 * h + 8 * c4;
+        uint8_t* turn = q_s + w * 2048;
+        uint32_t top = 0;
+        auto load = [&](int j, int i) -> uint4 {  // this lane's chunk of box j, row 8 i + r4 of the warp's
+          const int r = 8 * i + r4;
+          if (32 * quarter + r >= nrows) return make_uint4(0u, 0u, 0u, 0u);
+          return __ldg(reinterpret_cast<const uint4*>(src + r * kDqk + 64 * (j < 8 ? j ^ (rank << 2) : 8)));
+        };
+        auto greatest = [&](const uint4& u) {
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu)));
+        };
+        constexpr int kBatch = 3;
+#pragma unroll
+        for (int j0 = 0; j0 < 9; j0 += kBatch) {
+          uint4 u[kBatch][4];
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[b][i] = load(j0 + b, i);
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int j = j0 + b;
+            if (j < C::BT) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + r4;
+                *reinterpret_cast<uint4*>(turn + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4)) = u[b][i];
+              }
+              __syncwarp();
+              uint32_t v[16];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint4 x = *reinterpret_cast<const uint4*>(turn + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4));
+                if (C::FP8) greatest(x);
+                v[4 * k] = x.x, v[4 * k + 1] = x.y, v[4 * k + 2] = x.z, v[4 * k + 3] = x.w;
+              }
+              tmem_st16(lane_base + C::COL_Q + 32 * j + 16 * h, v);
+              __syncwarp();
+            } else {
+              if (j == C::BT) softmax_bar();  // no warp turns rows any more
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = 32 * quarter + 8 * i + r4;
+                *reinterpret_cast<uint4*>(q_s + (j - C::BT) * C::Q_BOX + r * 128 + (((4 * h + c4) ^ (r & 7)) << 4)) = u[b][i];
+              }
+            }
           }
+        }
+        if constexpr (C::FP8) {
+          // In place: scaled by a power of two, the row's largest value to [2^7, 2^8), and split into two 8-bit parts,
+          // per box and half of its columns 32 bytes of the one, then of the other.
+          auto mine = [&](int j, int k) {
+            return reinterpret_cast<uint4*>(q_s + (j - C::BT) * C::Q_BOX + row * 128 + (((4 * h + k) ^ (row & 7)) << 4));
+          };
+          __syncwarp();
+#pragma unroll
+          for (int j = C::BT; j < 9; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) greatest(*mine(j, k));
           a->mx[0][h][row] = __uint_as_float(max(top & 0xFFFFu, top >> 16) << 16);
+          tmem_wait_st();
           pair_bar(quarter);
           const int e = (__float_as_int(fmaxf(a->mx[0][0][row], a->mx[0][1][row])) >> 23) - 127;
           const int up = min(7 - e, 126);
@@ -773,49 +839,35 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
           // (an infinity or NaN in the row: every logit is NaN)
           row_scale = e == 128 ? __int_as_float(0x7FC00000) : p.scale_log2 * __int_as_float((127 - up) << 23);
 #pragma unroll 1
-          for (int g = 0; g < 9; ++g) {
-            uint32_t v[16];  // 32 values as E4M3, the same as E5M2
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 u = row < nrows ? __ldg(box(g) + 4 * h + k) : zero;
-              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-              for (int n = 0; n < 2; ++n) {
-                uint32_t a0, a1, b0, b1;
-                split_fp8(__uint_as_float(w[2 * n] << 16) * mul, __uint_as_float(w[2 * n] & 0xFFFF0000u) * mul, a0, b0);
-                split_fp8(__uint_as_float(w[2 * n + 1] << 16) * mul, __uint_as_float(w[2 * n + 1] & 0xFFFF0000u) * mul, a1, b1);
-                v[2 * k + n] = a0 | a1 << 16;
-                v[8 + 2 * k + n] = b0 | b1 << 16;
-              }
-            }
-            if (g < C::BT) {
-              tmem_st16(lane_base + C::COL_Q + 32 * g + 16 * h, v);
+          for (int j = 0; j < 9; ++j) {
+            float raw[16];
+            if (j < C::BT) {
+              tmem_ld_sync(lane_base + C::COL_Q + 32 * j + 16 * h, raw);
             } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                *reinterpret_cast<uint4*>(q_s + (g - C::BT) * C::Q_BOX + row * 128 + (((4 * h + k) ^ (row & 7)) << 4)) =
-                    make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+              for (int k = 0; k < 4; ++k) {
+                const uint4 x = *mine(j, k);
+                raw[4 * k] = __uint_as_float(x.x), raw[4 * k + 1] = __uint_as_float(x.y);
+                raw[4 * k + 2] = __uint_as_float(x.z), raw[4 * k + 3] = __uint_as_float(x.w);
+              }
+            }
+            uint32_t v[16];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              uint32_t a0, a1, b0, b1;
+              split_fp8(__float_as_uint(raw[2 * k]), mul, a0, b0);
+              split_fp8(__float_as_uint(raw[2 * k + 1]), mul, a1, b1);
+              v[k] = a0 | a1 << 16;
+              v[8 + k] = b0 | b1 << 16;
+            }
+            if (j < C::BT) {
+              tmem_st16(lane_base + C::COL_Q + 32 * j + 16 * h, v);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) *mine(j, k) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             }
           }
           pair_bar(quarter);  // (the maxima have been read)
-        } else {
-#pragma unroll 4
-          for (int k = 0; k < 4 * (9 - C::BT); ++k) {
-            const int b = k >> 2, c = 2 * (k & 3) + h;
-            cp_async16(q_s + b * C::Q_BOX + row * 128 + ((c ^ (row & 7)) << 4), box(C::BT + b) + c, row < nrows);
-          }
-          cp_async_commit();
-#pragma unroll 3
-          for (int g = 0; g < C::BT; ++g) {
-            uint32_t v[16];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 u = row < nrows ? __ldg(box(g) + 4 * h + k) : zero;
-              v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
-            }
-            tmem_st16(lane_base + C::COL_Q + 32 * g + 16 * h, v);
-          }
-          cp_async_wait<0>();
         }
         tmem_wait_st();
         tc_fence_before();
@@ -829,13 +881,23 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         // ---- logits, scaled and masked
         float x[32];
         const float* sc = sc_s + (tile & 1) * kKeys * C::NSC + 32 * h;
+        float4 scale[C::FP8 ? 8 : 1];  // of the positions (tile scales: of one column tile after another)
+        auto scales = [&](const float* from) {
+          if constexpr (C::FP8) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) scale[k] = *reinterpret_cast<const float4*>(from + 4 * k);
+          }
+        };
         if constexpr (C::FP8) ok = wait(a, &a->sc_full[tile & 1], (tile >> 1) & 1, err) && ok;
+        if constexpr (!C::TILED) scales(sc);
         if constexpr (C::TILED) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = 0.f;
         }
 #pragma unroll 1
         for (int g = 0; g < C::GROUPS; ++g, ++su) {
+          // (the groups are in the order of the slots, the scales in that of the columns)
+          if constexpr (C::TILED) scales(sc + kKeys * (g < 4 ? g ^ (rank << 1) : 4));
           ok = wait(a, &a->s_full[su % C::SB], (su / C::SB) & 1, err) && ok;
           tc_fence_after();
           float s[32];
@@ -843,12 +905,10 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0 && ok) mbar_arrive(&a->s_empty[su % C::SB]);
-          // (the groups are in the order of the slots, the scales in that of the columns)
-          const float* scg = sc + kKeys * (g < 4 ? g ^ (rank << 1) : 4) * C::TILED;
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
             float4 f = make_float4(row_scale, row_scale, row_scale, row_scale);
-            if constexpr (C::FP8) f = *reinterpret_cast<const float4*>(scg + k);
+            if constexpr (C::FP8) f = scale[k >> 2];
             if constexpr (C::TILED) {
               x[k] = fmaf(f.x, s[k], x[k]), x[k + 1] = fmaf(f.y, s[k + 1], x[k + 1]);
               x[k + 2] = fmaf(f.z, s[k + 2], x[k + 2]), x[k + 3] = fmaf(f.w, s[k + 3], x[k + 3]);
@@ -909,6 +969,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
             if (zero) {
 #pragma unroll
               for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(line + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
             }
           }
           __syncwarp();
@@ -952,27 +1013,21 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         const bool hides = C::FP8 && (edge || bad);
 #pragma unroll
         for (int b = 0; b < C::PC; ++b) {
-          const float* scb = sc + kKeys * (2 * rank + b) * C::TILED;
+          if constexpr (C::TILED) scales(sc + kKeys * (2 * rank + b));
+          uint32_t v[16];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // 16-byte chunks of eight positions
-            float z[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) z[k] = x[8 * j + k];
+          for (int k = 0; k < 32; k += 2) {
+            float z0 = x[k], z1 = x[k + 1];
             if constexpr (C::FP8) {
-              const float4 f0 = *reinterpret_cast<const float4*>(scb + 8 * j);
-              const float4 f1 = *reinterpret_cast<const float4*>(scb + 8 * j + 4);
-              z[0] *= f0.x, z[1] *= f0.y, z[2] *= f0.z, z[3] *= f0.w;
-              z[4] *= f1.x, z[5] *= f1.y, z[6] *= f1.z, z[7] *= f1.w;
-              if (hides) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) z[k] = x[8 * j + k] == 0.f ? 0.f : z[k];
-              }
+              const float4 f = scale[k >> 2];
+              z0 *= k & 2 ? f.z : f.x, z1 *= k & 2 ? f.w : f.y;
+              if (hides) z0 = x[k] == 0.f ? 0.f : z0, z1 = x[k + 1] == 0.f ? 0.f : z1;
             }
-            *reinterpret_cast<uint4*>(p_row + b * C::P_BYTES + (((4 * h + j) ^ (row & 7)) << 4)) =
-                make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
+            v[k >> 1] = pack_bf16(z0, z1);
           }
+          tmem_st16(lane_base + C::COL_P + 32 * b + 16 * h, v);
         }
-        fence_proxy_async_smem();
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && ok) {
