@@ -248,24 +248,19 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
          (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
 }
 
-// Eight codes of v / s: by the reciprocal where that gives the quotient's codes (Quotient has the
-// argument), with one test for the eight: the smallest distance, in 2^-20 of a binade, of a product from
-// an E4M3 rounding midpoint (mantissa bits 0x80000 below bit 20, both sides 4), and the smallest product.
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], const Quotient& div) {
-  float q[8], least = INFINITY;
-  uint32_t near = 0xFFFFFFFFu;
+// Eight codes of the IEEE quotients v / s.  The products with r (1 + 2^-21) and r (1 - 2^-21), r = 1 / s to half an
+// ulp, have the quotient between them, and E4M3's rounding is monotone: where both give the same codes, those are
+// the quotient's.  Otherwise (a rounding midpoint within 2^-21; r or s not normal) the divisions are made.
+__device__ __forceinline__ uint2 encode8(const float (&v)[8], float s, float lo, float hi, bool fast) {
+  const uint2 a = make_uint2(e4m3x4(v[0] * lo, v[1] * lo, v[2] * lo, v[3] * lo), e4m3x4(v[4] * lo, v[5] * lo, v[6] * lo, v[7] * lo));
+  const uint2 b = make_uint2(e4m3x4(v[0] * hi, v[1] * hi, v[2] * hi, v[3] * hi), e4m3x4(v[4] * hi, v[5] * hi, v[6] * hi, v[7] * hi));
+  if (fast && a.x == b.x && a.y == b.y) return a;
+  float q[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    q[k] = v[k] * div.r;
-    near = min(near, __float_as_uint(q[k]) * 4096u - (0x7FFFCu << 12));
-    least = fminf(least, fabsf(q[k]));
-  }
-  if (!(div.fast && near > (8u << 12) && least >= 0x1p-6f)) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) q[k] = q[k] == 0.f && div.fast ? q[k] : div(v[k]);
-  }
+  for (int k = 0; k < 8; ++k) q[k] = v[k] == 0.f ? v[k] : __fdiv_rn(v[k], s);
   return make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
 }
+constexpr float kAbove = 1.f + 0x1p-21f, kBelow = 1.f - 0x1p-21f;
 
 __device__ __forceinline__ float amax8(const float (&v)[8]) {
   float a = 0.f;
@@ -275,8 +270,159 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
 }
 
 constexpr int kMaxChunks = 4;  // 8-element chunks per lane: rows up to 1024 elements
+// The form with half a warp per row: tiles per row, resident CTAs (registers), and the rows from which it pays (tile
+// scales, us: 8192 rows 9.0 against 7.8 of a warp per row, 65536 41.1 against 43.3, 131072 76.5 against 84.8; MX 6.0
+// against 6.2, 27.4 against 32.3, 49.7 against 61.2; row scales and bf16 gain nothing or lose).
+constexpr int kHalfTiles = 5, kHalfCtasPerSm = 2, kHalfRows = 32768;
 
-// Vector form: lane j holds the 8-element chunks j, j + 32, ... of the row, so 4 consecutive lanes hold
+// Rows of up to 128 NT columns with up to 32 pairs (the latent row): half a warp takes a row, lane j of it the
+// 8-element chunks j, j + 16, ..., so that a slot of the 16 lanes is a tile of 128.  (A warp per row leaves a
+// quarter of the lanes idle at 576 columns and spends the row's other instructions on one row: 562 per row instead
+// of 427.)  The rotary columns are turned pair by pair, two pairs per
+// lane, into fp32 in shared memory, from where the lanes that hold their chunks take them.  The next row's loads (its
+// chunks, pairs, position and destination) are in flight while a row is encoded.
+template <int FMT, int NT>
+__global__ void __launch_bounds__(32 * kWarps, kHalfCtasPerSm) rope_append_half_kernel(const RopeParams p) {
+  __shared__ RopeSmem sm;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = lane >> 4, hl = lane & 15;
+  const int nch = p.width / 8;
+  const int64_t step = (int64_t)gridDim.x * kWarps * 2;
+  fill_freq(p, sm);
+  float* turned = reinterpret_cast<float*>(sm.turns[warp]) + 64 * half;  // the row's rotary columns
+  uint64_t freq[2];
+  int axis[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = hl + 16 * i;
+    freq[i] = k < p.pairs ? sm.freq[k] : 0;
+    axis[i] = k < p.pairs ? sm.axis[k] : 0;
+  }
+  // the rotary columns' first chunk from this lane's chunk 0 on (at most one of its chunks is among them)
+  const int rot0 = hl - p.rot_off / 8, rots = p.pairs / 4;
+  uint4 raw[NT];
+  __nv_bfloat16 x0[2], x1[2];
+  int pos[2] = {0, 0};
+  int64_t dst = -1;
+  auto fetch = [&](int64_t row) {
+    dst = -1;
+    if (row >= p.rows) return;
+    const __nv_bfloat16* x = p.x + row * p.x_row_stride;
+    dst = p.dst_rows ? p.dst_rows[row] : row;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int k = hl + 16 * i;
+      if (k < p.pairs) {
+        pos[i] = p.pos[row * p.pos_stride + axis[i]];
+        const int c0 = p.rot_off + (p.half ? k : 2 * k);
+        x0[i] = x[c0];
+        x1[i] = x[p.half ? c0 + p.pairs : c0 + 1];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int c = hl + 16 * j;
+      raw[j] = c < nch ? *reinterpret_cast<const uint4*>(x + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  int64_t row0 = ((int64_t)blockIdx.x * kWarps + warp) * 2;  // the warp's pair of rows
+#pragma unroll
+  for (int j = 0; j < NT; ++j) raw[j] = make_uint4(0u, 0u, 0u, 0u);
+  x0[0] = x0[1] = x1[0] = x1[1] = __float2bfloat16_rn(0.f);
+  if (row0 < p.rows) fetch(row0 + half);
+#pragma unroll 1
+  for (; row0 < p.rows; row0 += step) {
+    const int64_t at_row = dst;
+    const bool keep = at_row >= 0 && at_row < p.dst_count;
+    if (at_row >= p.dst_count && hl == 0) record_error(p.err, DSA_DEVERR_INDEX_RANGE);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int k = hl + 16 * i;
+      float a = __bfloat162float(x0[i]), b = __bfloat162float(x1[i]);
+      turn(a, b, pair_turn(p, freq[i], pos[i]));
+      if (k < p.pairs) {
+        turned[p.half ? k : 2 * k] = a;
+        turned[p.half ? k + p.pairs : 2 * k + 1] = b;
+      }
+    }
+    __syncwarp();
+    float v[NT][8];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      unpack8(raw[j], v[j]);
+      const int at = rot0 + 16 * j;
+      if (at >= 0 && at < rots) {
+        const float4 t0 = *reinterpret_cast<const float4*>(turned + 8 * at), t1 = *reinterpret_cast<const float4*>(turned + 8 * at + 4);
+        v[j][0] = t0.x, v[j][1] = t0.y, v[j][2] = t0.z, v[j][3] = t0.w;
+        v[j][4] = t1.x, v[j][5] = t1.y, v[j][6] = t1.z, v[j][7] = t1.w;
+      }
+    }
+    if (row0 + step < p.rows) fetch(row0 + step + half);
+    uint8_t* out = p.dst + at_row * p.dst_row_stride;
+    auto across = [](float a, int lanes) {
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1)
+        if (o < lanes) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+      return a;
+    };
+    if constexpr (FMT == kFmtBf16) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int c = hl + 16 * j;
+        if (keep && c < nch) *reinterpret_cast<uint4*>(out + 16 * c) = pack8(v[j]);
+      }
+    } else if constexpr (FMT == kFmtRow) {
+      float a = 0.f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) a = fmaxf(a, amax8(v[j]));
+      const float amax = across(a, 16);
+      const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+      const Quotient div(s);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int c = hl + 16 * j;
+        if (keep && c < nch)
+          *reinterpret_cast<uint2*>(out + 8 * c) = encode8(v[j], s, div.r * kBelow, div.r * kAbove, div.fast);
+      }
+      if (keep && hl == 0) reinterpret_cast<float*>(p.scale)[at_row] = s;
+    } else if constexpr (FMT == kFmtTile) {
+      // lane j of each half takes tile j's scale and reciprocal (a division each, once instead of NT times)
+      float own = 0.f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const float a = across(amax8(v[j]), 16);
+        if (hl == j) own = a;
+      }
+      const Quotient div(own > 0.f ? __fdiv_rn(own, 448.f) : 1.f);
+      const int tiles = (nch + 15) / 16;
+      if (keep && hl < tiles) reinterpret_cast<float*>(p.scale)[at_row * tiles + hl] = div.s;
+      const uint32_t fast = __ballot_sync(0xffffffffu, div.fast);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int c = hl + 16 * j, from = (lane & 16) + j;
+        const float s = __shfl_sync(0xffffffffu, div.s, from), r = __shfl_sync(0xffffffffu, div.r, from);
+        if (keep && c < nch)
+          *reinterpret_cast<uint2*>(out + 8 * c) = encode8(v[j], s, r * kBelow, r * kAbove, (fast >> from) & 1);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int c = hl + 16 * j;
+        const float a = across(amax8(v[j]), 4);
+        if (keep && c < nch) {
+          const int e = mx_exponent(a);
+          const float inv = ldexpf(1.f, -e);  // a power of two: exact
+          *reinterpret_cast<uint2*>(out + 8 * c) =
+              make_uint2(e4m3x4(v[j][0] * inv, v[j][1] * inv, v[j][2] * inv, v[j][3] * inv),
+                         e4m3x4(v[j][4] * inv, v[j][5] * inv, v[j][6] * inv, v[j][7] * inv));
+          if ((lane & 3) == 0) p.scale[at_row * (p.width / 32) + c / 4] = (uint8_t)(e + 127);
+        }
+      }
+    }
+  }
+}
+
+// Vector form: a warp takes a row, lane j the 8-element chunks j, j + 32, ... of the row, so 4 consecutive lanes hold
 // a group of 32 and 16 lanes a tile of 128.  The rotary columns are turned pair by pair, a pair per lane (PP
 // per lane), into fp32 in shared memory, from where the lanes that hold their chunks take them.  The next
 // row's loads (its chunks, pairs, position and destination) are in flight while a row is encoded.
@@ -369,7 +515,7 @@ __global__ void __launch_bounds__(32 * kWarps, NCH == 3 ? kCtasPerSm : 1) rope_a
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
         const int c = lane + 32 * j;
-        if (c < nch) *reinterpret_cast<uint2*>(out + 8 * c) = encode8(v[j], div);
+        if (c < nch) *reinterpret_cast<uint2*>(out + 8 * c) = encode8(v[j], s, div.r * kBelow, div.r * kAbove, div.fast);
       }
       if (lane == 0) reinterpret_cast<float*>(p.scale)[at_row] = s;
     } else if constexpr (FMT == kFmtTile) {
@@ -394,7 +540,7 @@ __global__ void __launch_bounds__(32 * kWarps, NCH == 3 ? kCtasPerSm : 1) rope_a
         div.r = __shfl_sync(0xffffffffu, r_own, from);
         div.fast = (fast >> from) & 1;
         if (c < nch) {
-          *reinterpret_cast<uint2*>(out + 8 * c) = encode8(v[j], div);
+          *reinterpret_cast<uint2*>(out + 8 * c) = encode8(v[j], div.s, div.r * kBelow, div.r * kAbove, div.fast);
           if ((lane & 15) == 0) reinterpret_cast<float*>(p.scale)[at_row * tiles + c / 16] = div.s;
         }
       }
@@ -475,7 +621,9 @@ __global__ void __launch_bounds__(32 * kWarps) rope_append_kernel(const RopePara
 
 using AppendKernel = void (*)(const RopeParams);
 template <int FMT>
-AppendKernel append_vec(bool small) {
+AppendKernel append_vec(bool small, bool half) {
+  if constexpr (FMT == kFmtTile || FMT == kFmtMx)
+    if (half) return rope_append_half_kernel<FMT, kHalfTiles>;
   return small ? rope_append_vec_kernel<FMT, 3, 1> : rope_append_vec_kernel<FMT, kMaxChunks, 4>;
 }
 
@@ -581,17 +729,20 @@ dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int wi
   const bool vec = width % 8 == 0 && width <= 256 * kMaxChunks && rot_off % 8 == 0 &&
                    (2 * p.pairs) % 8 == 0 && aligned(x, 16) && (rows == 1 || x_row_stride % 8 == 0) &&
                    aligned(dst, out_align) && dst_row_stride % (int64_t)out_align == 0;
-  // rows of up to 768 columns with up to 32 pairs (the latent row) take the form with fewer registers
+  // rows of up to 768 columns with up to 32 pairs (the latent row) take the form with fewer registers; many of up to
+  // 640 with scales per 128 or 32 columns half a warp each
   const bool small = width <= 768 && p.pairs <= 32;
+  const bool half = vec && p.pairs <= 32 && width <= 128 * kHalfTiles && rows >= kHalfRows &&
+                    (dtype == DSA_FP8_E4M3_T128 || dtype == DSA_MXFP8_E4M3);
   AppendKernel kern = nullptr;
   switch (dtype) {
-    case DSA_BF16: kern = vec ? append_vec<kFmtBf16>(small) : rope_append_kernel<kFmtBf16>; break;
-    case DSA_FP8_E4M3: kern = vec ? append_vec<kFmtRow>(small) : rope_append_kernel<kFmtRow>; break;
-    case DSA_FP8_E4M3_T128: kern = vec ? append_vec<kFmtTile>(small) : rope_append_kernel<kFmtTile>; break;
-    default: kern = vec ? append_vec<kFmtMx>(small) : rope_append_kernel<kFmtMx>; break;
+    case DSA_BF16: kern = vec ? append_vec<kFmtBf16>(small, half) : rope_append_kernel<kFmtBf16>; break;
+    case DSA_FP8_E4M3: kern = vec ? append_vec<kFmtRow>(small, half) : rope_append_kernel<kFmtRow>; break;
+    case DSA_FP8_E4M3_T128: kern = vec ? append_vec<kFmtTile>(small, half) : rope_append_kernel<kFmtTile>; break;
+    default: kern = vec ? append_vec<kFmtMx>(small, half) : rope_append_kernel<kFmtMx>; break;
   }
-  int grid = (rows + kWarps - 1) / kWarps;
-  const int most = kSms * (small ? kCtasPerSm : 1);
+  int grid = half ? (rows + 2 * kWarps - 1) / (2 * kWarps) : (rows + kWarps - 1) / kWarps;
+  const int most = kSms * (half ? kHalfCtasPerSm : small ? kCtasPerSm : 1);
   if (vec && grid > most) grid = most;
   kern<<<grid, 32 * kWarps, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
