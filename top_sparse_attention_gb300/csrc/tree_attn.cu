@@ -252,6 +252,10 @@ __device__ __forceinline__ void split_fp8(uint32_t x, float mul, uint32_t& e4, u
   e5 = __nv_cvt_halfraw2_to_fp8x2(__hsub2(v, __half2(__nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3))), __NV_SATFINITE, __NV_E5M2);
 }
 
+// `bytes` (a multiple of 16) on their way to L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* tm, int x, int y, int z) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(tm), "r"(x), "r"(y), "r"(z)
                : "memory");
@@ -487,7 +491,15 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         for (int b = 0; b < 4; ++b) tma_prefetch_3d(&tm, 256 * rank + 64 * b, (int)row, p.pages.table ? 0 : it.seq);
         if (rank) tma_prefetch_3d(&tm, 512, (int)row, p.pages.table ? 0 : it.seq);
       };
+      // an item's query rows too: the first one's before its tiles queue up at the memory, the others' an item ahead
+      auto query = [&](const Item& x) {
+        const int lo = x.rt * kRows, n = min(kRows, p.q_per_seq * p.H - lo);
+        if (rank == 0 && x.t0 < x.t1) prefetch_l2(p.q + ((int64_t)x.seq * p.q_per_seq * p.H + lo) * kDqk, n * kDqk * 2);
+      };
+      Item next;
+      if (get_item(p, pl, a, 0, next)) query(next);
       for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
+        if (get_item(p, pl, a, i + 1, next)) query(next);
         for (int t = it.t0; !C::FP8 && t < it.t0 + kAhead; ++t) ahead(t);
         for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
           if (!C::FP8) ahead(t + kAhead);
