@@ -195,6 +195,65 @@ def test_row_pitch(dsa, kv, pitch):
 
 
 @pytest.mark.parametrize("kv", FORMATS)
+def test_more_row_tiles_than_fill_the_device_evenly(dsa, kv):
+    # 26 row tiles of each of three sequences: their tiles are shared out end to end, and a row tile's parts merged
+    c = Case(20, [1200, 1310, 1150], 104, 32, kv)
+    out, lse = c.call(dsa, 1 / 24)
+    c.check(out, lse, 1 / 24, nodes=[4 * k + k % 4 for k in range(26)])
+
+
+@pytest.mark.parametrize("kv", ["fp8", "t128"])
+def test_queries_of_a_wide_range(dsa, kv):
+    # E4M3 rows: a query row enters as E4M3 plus E5M2, exact from 2^-13 of its largest value on, to 2^-20 of it below
+    c = Case(21, [150, 20], 4, 16, kv, 64)
+    rng = np.random.default_rng(21)
+    f = np.ldexp(1.0, -rng.integers(0, 30, tuple(c.q.shape)))
+    f *= np.ldexp(1.0, rng.integers(-60, 40, (c.q.shape[0], c.q.shape[1], 1)))  # rows of any size
+    f[1, 3] = 0.0
+    c.q = (c.q.double() * torch.from_numpy(f).cuda()).bfloat16()
+    q = c.q.double().cpu().numpy().reshape(2, 4, 16, D)
+    big = np.abs(q).max(-1, keepdims=True)
+    sm = 1 / 24
+    out, lse = c.call(dsa, sm)
+    out, lse = out.double().cpu().numpy().reshape(2, 4, 16, DV), lse.double().cpu().numpy().reshape(2, 4, 16)
+    for s in range(2):
+        ctx = int(c.ctx[s])
+        for i in range(4):
+            at = list(range(ctx)) + [ctx + j for j in range(4) if c.bits[s, i, j]]
+            kv64 = c.val[[c.row_of(s, p) for p in at]]
+            want, want_lse = oracle.tree_attention(q[s, i:i + 1], kv64, len(at), 1, np.zeros((1, 1), bool), sm, DV)
+            x = sm * q[s, i] @ kv64.T
+            A = np.exp(x - want_lse[0][:, None]) @ np.abs(kv64[:, :DV])
+            # the fp32 sums' part as in `check`, and 2^-20 of the row's largest value per product
+            ds = sm * (2.0**-22 * (D + 2) * (np.abs(q[s, i]) @ np.abs(kv64).T) + 2.0**-20 * big[s, i] * np.abs(kv64).sum(1)).max(1)
+            ok = ds < 0.25  # (rows whose logits are far beyond that have a single winner)
+            tol = 2.0**-8 * np.abs(want[0]) + (2.0**-8 + 2.0**-14 + 2 * np.expm1(np.minimum(ds, 1.0))[:, None]) * A
+            assert np.all((np.abs(out[s, i] - want[0]) <= tol)[ok]), (s, i)
+            assert np.all((np.abs(lse[s, i] - want_lse[0]) <= ds + 2.0**-20 * (np.abs(want_lse[0]) + 1))[ok]), (s, i)
+            assert ok.sum() >= 8  # (exponents below 12 or so of the 100 drawn)
+
+
+@pytest.mark.parametrize("kv", ["fp8", "t128"])
+def test_a_query_row_that_is_not_finite(dsa, kv):
+    c = Case(22, [100, 40], 2, 16, kv)
+    c.q[1, 5, 77] = float("inf")
+    c.q[2, 0, 3] = float("nan")
+    out, _ = c.call(dsa, 1 / 24)
+    bad = torch.zeros(4, 16, dtype=torch.bool, device="cuda")
+    bad[1, 5] = bad[2, 0] = True
+    assert bool(torch.isnan(out.view(4, 16, DV)[bad]).all()) and bool(torch.isfinite(out.view(4, 16, DV)[~bad]).all())
+
+
+@pytest.mark.parametrize("kv", ["fp8", "t128"])
+@pytest.mark.parametrize("block", [0, 64])
+def test_hidden_codes_do_not_matter(dsa, kv, block):
+    c = Case(23, [70, 128, 5], 6, 16, kv, block, new=[6, 3, 2], L=200)
+    used = [c.row_of(s, p) for s in range(3) for p in range(int(c.ctx[s] + c.new[s]))]
+    c.cache[torch.from_numpy(np.setdiff1d(np.arange(c.rows), used)).cuda()] = 0x7F  # E4M3's NaN
+    c.run(dsa)
+
+
+@pytest.mark.parametrize("kv", FORMATS)
 def test_sharp_softmax_and_a_maximum_that_keeps_rising(dsa, kv):
     c = Case(10, [700, 300], 4, 16, kv)
     c.run(dsa, sm_scale=0.7)

@@ -56,13 +56,13 @@ constexpr int kSlotC = 9 * kBoxC;
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLazy = 8.f;              // log2 growth of a row's maximum that is left unscaled
 constexpr int kItemsPerCta = 3;           // split launches are cut into at most this many items per cluster
-constexpr int kAhead = 3;                 // tiles between the request to L2 and the load into shared memory
+constexpr int kAhead = 2;                 // tiles between the request to L2 and the load into shared memory
 constexpr int kColO = 0;                  // tensor-memory columns: O, then boxes of q, then S
 
 enum { kBf16 = 0, kFp8Row = 1, kFp8Tile = 2 };
 
 struct Aux {
-  uint64_t v_full[3], v_empty[3], k_full[7], k_empty[7], c_full[2], c_empty[2], s_full[2], s_empty[2], p_full, pv_done;
+  uint64_t v_full[3], v_empty[3], k_full[10], k_empty[10], c_full[2], c_empty[2], s_full[2], s_empty[2], p_full, pv_done;
   uint64_t o_done, o_free, q_full, sc_full[2], sc_empty[2], drain;
   uint32_t tmem;
   int abort;
@@ -112,7 +112,7 @@ struct TreePlan {
   int units;               // n_seq * row_tiles
   int cap;                 // partial slots; 0: no unit is split
   int grid;                // clusters
-  int* head;               // [0]: chunk length in tiles (0: not split), [1 + s]: first item of sequence s
+  int* head;               // [0]: tiles of a chunk, or minus those of a span; [1 + s]: first item or tile of sequence s
   float4* part_o;          // [cap][128 groups of four values][128 rows]
   float2* part_ml;         // [cap][128 rows]
 };
@@ -298,8 +298,13 @@ __device__ __forceinline__ uint64_t seen_bits(const TreeAttnParams& p, const Ite
   return v;
 }
 
-// Splits the sequences' tiles into items.  Cost of chunks of CH tiles: the fullest CTA's items, each CH
-// tiles plus the fill and drain of its pipeline, and for a split the merge.  Fills this cluster's list;
+// Splits the sequences' tiles into items, for each pair of CTAs a list.  Two kinds of plan:
+//   * chunks of CH tiles of every unit (a row tile of a sequence), dealt out in turn: pairs that run together read
+//     the same positions;
+//   * where no unit is much shorter than a pair's share W of all tiles, spans of W of the units' tiles laid end to end:
+//     no pair waits for another, and none has more than three items (a full unit between two parts).
+// The cost of each in tiles: the fullest pair's items and the fill and drain of its pipeline for each, and for a split
+// the merge.  (8 x 64 nodes at 32K, E4M3: 64 units of 512 tiles on 76 pairs, 710 us whole, 630 us as spans.)
 // CTA 0 leaves the plan for the merge.  Scratch: 3 n_seq + 160 ints of shared memory.
 __device__ void plan_items(const TreeAttnParams& p, const TreePlan& pl, Aux* a, int* scratch) {
   constexpr float kItemCost = 4.f, kMergeCost = 4.f, kMergePerItem = 0.02f;  // in tiles
@@ -316,10 +321,19 @@ __device__ void plan_items(const TreeAttnParams& p, const TreePlan& pl, Aux* a, 
     nt[s] = live[s] ? (len + kKeys - 1) / kKeys : 0;
   }
   __syncthreads();
+  long long total = 0;  // (in the first warp) all units' tiles
+  int least = INT_MAX;  // of a unit; 0: there are row tiles of padding nodes, or empty sequences
   if (tid < 32) {
     int m = 1;
-    for (int s = tid; s < n; s += 32) m = max(m, nt[s]);
+    for (int s = tid; s < n; s += 32) {
+      m = max(m, nt[s]);
+      least = min(least, live[s] == pl.row_tiles ? nt[s] : 0);
+      total += (long long)nt[s] * pl.row_tiles;
+    }
     m = __reduce_max_sync(0xffffffffu, m);
+    least = __reduce_min_sync(0xffffffffu, least);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (tid == 0) chunk[65] = m;
   }
   __syncthreads();
@@ -355,10 +369,16 @@ __device__ void plan_items(const TreeAttnParams& p, const TreePlan& pl, Aux* a, 
     for (int o = 16; o; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
     const uint32_t m0 = __ballot_sync(0xffffffffu, c0 == best), m1 = __ballot_sync(0xffffffffu, c1 == best);
     const int ch = chunk[m0 ? __ffs(m0) - 1 : 31 + __ffs(m1)];
-    int run = 0;
+    const long long share = (total + pl.grid - 1) / pl.grid;
+    const bool spans = total <= INT_MAX - 4096 && least > 0 && 2ll * least >= share &&
+                       share + 2 * kItemCost + kMergeCost + kMergePerItem * (pl.units + pl.grid) < best;
+    const int W = (int)share;
+    int run = 0;  // items, or tiles
     for (int s0 = 0; s0 < n; s0 += 32) {
       const int s = s0 + tid;
-      const int c = s < n ? live[s] * (nt[s] ? (nt[s] + ch - 1) / ch : 1) + (pl.row_tiles - live[s]) : 0;
+      const int c = s >= n ? 0
+                    : spans ? nt[s] * pl.row_tiles
+                            : live[s] * (nt[s] ? (nt[s] + ch - 1) / ch : 1) + (pl.row_tiles - live[s]);
       int incl = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -369,43 +389,67 @@ __device__ void plan_items(const TreeAttnParams& p, const TreePlan& pl, Aux* a, 
       run += __shfl_sync(0xffffffffu, incl, 31);
     }
     __syncwarp();
-    // this cluster's items: its number, + grid, ...
-    const int first = (int)(blockIdx.x >> 1), mine = first + tid * pl.grid;
-    if (tid < kItemsPerCta && mine < run) {
+    // this pair's items: tiles [pair W, (pair + 1) W), or the items of its number, + grid, ...
+    const int pair = (int)(blockIdx.x >> 1), mine = spans ? pair * W : pair + tid * pl.grid;
+    auto sequence = [&](int at) {  // whose tiles or items hold number `at`
       int lo = 0, hi = n - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (base[mid] <= mine) lo = mid;
+        if (base[mid] <= at) lo = mid;
         else hi = mid - 1;
       }
-      const int s = lo, at = mine - base[s];
-      const int chunks = nt[s] ? (nt[s] + ch - 1) / ch : 1;
-      Item it;
-      seq_facts(p, s, it.ctx, it.fresh, it.len);
-      it.seq = s;
-      it.slot = -1;
-      it.t0 = it.t1 = 0;
-      if (at < live[s] * chunks) {
-        const int j = at / live[s];
-        it.rt = at - j * live[s];
-        it.t0 = min(j * ch, nt[s]);
-        it.t1 = min(it.t0 + ch, nt[s]);
-        if (chunks > 1) it.slot = mine;
-      } else {
-        it.rt = live[s] + at - live[s] * chunks;
+      return lo;
+    };
+    if (spans) {
+      if (tid == 0) {
+        const int end = min(run - mine, W) + mine;
+        int count = 0;
+        for (int at = mine; at < end; ++count) {
+          Item it;
+          it.seq = sequence(at);
+          seq_facts(p, it.seq, it.ctx, it.fresh, it.len);
+          const int tiles = nt[it.seq];
+          it.rt = (at - base[it.seq]) / tiles;
+          const int unit = base[it.seq] + it.rt * tiles;
+          it.t0 = at - unit;
+          it.t1 = min(tiles, end - unit);
+          it.slot = it.t1 - it.t0 < tiles ? pair * kItemsPerCta + count : -1;
+          memcpy(a->items[count], &it, sizeof(it));
+          at = unit + it.t1;
+        }
+        a->n_items = count;
       }
-      memcpy(a->items[tid], &it, sizeof(it));
+    } else {
+      if (tid < kItemsPerCta && mine < run) {
+        const int s = sequence(mine), at = mine - base[s];
+        const int chunks = nt[s] ? (nt[s] + ch - 1) / ch : 1;
+        Item it;
+        seq_facts(p, s, it.ctx, it.fresh, it.len);
+        it.seq = s;
+        it.slot = -1;
+        it.t0 = it.t1 = 0;
+        if (at < live[s] * chunks) {
+          const int j = at / live[s];
+          it.rt = at - j * live[s];
+          it.t0 = min(j * ch, nt[s]);
+          it.t1 = min(it.t0 + ch, nt[s]);
+          if (chunks > 1) it.slot = mine;
+        } else {
+          it.rt = live[s] + at - live[s] * chunks;
+        }
+        memcpy(a->items[tid], &it, sizeof(it));
+      }
+      if (tid == 0) a->n_items = pair < run ? (run - pair + pl.grid - 1) / pl.grid : 0;
     }
-    if (tid == 0) a->n_items = first < run ? (run - first + pl.grid - 1) / pl.grid : 0;
     if (blockIdx.x == 0) {
-      if (tid == 0) pl.head[0] = ch;
+      if (tid == 0) pl.head[0] = spans ? -W : ch;
       for (int s = tid; s < n; s += 32) pl.head[1 + s] = base[s];
     }
   }
   __syncthreads();
 }
 
-// Item i of this cluster: from the list of a split launch, or the unit of number cluster + i * grid whole.
+// Item i of this pair: from the list of a split launch, or the unit of number pair + i * grid whole.
 __device__ __forceinline__ bool get_item(const TreeAttnParams& p, const TreePlan& pl, const Aux* a, int i, Item& it) {
   if (pl.cap) {
     if (i >= a->n_items) return false;
@@ -594,7 +638,6 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
       if (C::FP8) {
         if (lane == 1) bar = &a->c_full[cs], parity = cph;
       } else {
-        if (lane == 1) bar = &a->v_full[vs], parity = vph;
         if (lane >= 2 && lane < 7) bar = &a->k_full[k_slot(lane - 2)], parity = k_phase(lane - 2);
       }
       all(bar, parity);
@@ -606,19 +649,28 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
 #pragma unroll
           for (int j = j0; j < j1; ++j) qk_box(d, j, B + (j * kBoxC >> 4), j == j0);
           if (j1 == 9) tc_commit(&a->c_empty[cs]);
+          tc_commit(&a->s_full[su % C::SB]);
         } else {
           // those of the K ring first: their slots are the scarcer ones, and loading them again takes longer than
           // the rest of this product
-          const uint32_t V = kv_lo + vs * (kSlotV >> 4);
 #pragma unroll
           for (int j = 4; j < 9; ++j) {
             qk_box(d, j, kk_lo + k_slot(j - 4) * (kBox >> 4), j == 4);
             tc_commit(&a->k_empty[k_slot(j - 4)]);
           }
+        }
+      }
+      if (!C::FP8) {  // the value columns, waited for while the others are multiplied
+        __syncwarp();
+        all(&a->v_full[vs], vph);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t V = kv_lo + vs * (kSlotV >> 4);
 #pragma unroll
           for (int j = 0; j < 4; ++j) qk_box(d, j, V + (j * kBox >> 4), false);
+          tc_commit(&a->s_full[su % C::SB]);
         }
-        tc_commit(&a->s_full[su % C::SB]);
       }
       __syncwarp();
       ++su;
@@ -1105,11 +1157,35 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeAttnParams 
   seq_facts(p, seq, ctx, fresh, len);
   const int live = live_row_tiles(p, fresh);
   const int rt = row / kRows, r = row - rt * kRows;
-  const int ch = pl.head[0], nt = (len + kKeys - 1) / kKeys;
-  int chunks = nt ? (nt + ch - 1) / ch : 1;
+  const int plan = pl.head[0], nt = (len + kKeys - 1) / kKeys, base = pl.head[1 + seq];
+  int chunks, slot0, stride;  // the unit's partials: slots slot0 (the first), then from slot1 on, `stride` apart
+  int slot1;
+  if (plan > 0) {
+    chunks = nt ? (nt + plan - 1) / plan : 1;
+    slot0 = base + rt, slot1 = slot0 + live, stride = live;
+  } else {
+    // tiles [begin, begin + nt) over spans of W: those after the first begin within this unit (their item 0); in
+    // the first one it comes after the units that end there (of one length in a sequence)
+    const int W = -plan, begin = base + rt * nt, first = begin / W;
+    chunks = nt ? (begin + nt - 1) / W - first + 1 : 1;
+    int before = 0;
+    for (int s = seq, at = begin, r = rt; at > first * W; ++before) {
+      if (r == 0) {
+        int c, f, e;
+        seq_facts(p, --s, c, f, e);
+        at -= (e + kKeys - 1) / kKeys;
+        r = pl.row_tiles - 1;
+      } else {
+        int c, f, e;
+        seq_facts(p, s, c, f, e);
+        at -= (e + kKeys - 1) / kKeys;
+        --r;
+      }
+    }
+    slot0 = first * kItemsPerCta + before, slot1 = (first + 1) * kItemsPerCta, stride = kItemsPerCta;
+  }
   if (rt >= live || chunks == 1) return;  // written by the attention kernel
   if (row / p.H >= fresh) chunks = 0;     // a padding node beside live ones: zeros
-  const int item0 = pl.head[1 + seq] + rt;
   float M = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int B = 8;
@@ -1118,7 +1194,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeAttnParams 
     float4 v[B];
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-      const int64_t s = item0 + (j0 + k) * live;
+      const int64_t s = j0 + k == 0 ? slot0 : slot1 + (j0 + k - 1) * stride;
       const bool in = j0 + k < chunks;
       ml[k] = in ? pl.part_ml[s * kRows + r] : make_float2(-INFINITY, 0.f);
       v[k] = in ? pl.part_o[(s * (kDv / 4) + c4) * kRows + r] : make_float4(0.f, 0.f, 0.f, 0.f);
