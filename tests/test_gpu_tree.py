@@ -202,6 +202,24 @@ def test_more_row_tiles_than_fill_the_device_evenly(dsa, kv):
     c.check(out, lse, 1 / 24, nodes=[4 * k + k % 4 for k in range(26)])
 
 
+@pytest.mark.parametrize("kv", FORMATS)
+def test_row_tiles_of_padding_nodes_beside_shared_out_ones(dsa, kv):
+    # 3 row tiles per sequence, of which two to none hold nodes, over contexts of 20 to 60 tiles
+    rng = np.random.default_rng(24)
+    ctx = rng.integers(1280, 3800, 24)
+    new = rng.choice([12, 11, 8, 5, 4, 1, 0], 24)
+    ctx[3], new[3] = 0, 0
+    c = Case(24, ctx, 12, 32, kv, 64, new=new)
+    out, lse = c.call(dsa, 1 / 24)
+    c.check(out, lse, 1 / 24, nodes=[0, 3, 7, 10, 11])
+
+
+@pytest.mark.parametrize("n", [300, 700])
+def test_many_short_sequences(dsa, n):
+    rng = np.random.default_rng(n)
+    Case(n, rng.integers(0, 150, n), 2, 16, "bf16", new=rng.integers(0, 3, n)).run(dsa)
+
+
 @pytest.mark.parametrize("kv", ["fp8", "t128"])
 def test_queries_of_a_wide_range(dsa, kv):
     # E4M3 rows: a query row enters as E4M3 plus E5M2, exact from 2^-13 of its largest value on, to 2^-20 of it below

@@ -55,7 +55,8 @@ constexpr int kBoxC = kKeys * 64;         // 64 columns of a tile's E4M3 codes
 constexpr int kSlotC = 9 * kBoxC;
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLazy = 8.f;              // log2 growth of a row's maximum that is left unscaled
-constexpr int kItemsPerCta = 3;           // split launches are cut into at most this many items per cluster
+constexpr int kMaxItems = 8;              // of a pair of CTAs, in a planned launch
+constexpr int kSlotsPerPair = 3;          // partial results
 constexpr int kAhead = 2;                 // tiles between the request to L2 and the load into shared memory
 constexpr int kColO = 0;                  // tensor-memory columns: O, then boxes of q, then S
 
@@ -68,7 +69,7 @@ struct Aux {
   int abort;
   int n_items;
   int tile_bad[8];
-  int items[kItemsPerCta][8];
+  int items[kMaxItems][8];
   alignas(16) float mx[2][2][kRows];  // the rows' maxima over half of a tile
   float sum[2][kRows];                // and, at an item's end, their sums
   uint32_t clear[2][8];               // positions to clear
@@ -110,7 +111,7 @@ struct Item {
 struct TreePlan {
   int row_tiles;           // per sequence
   int units;               // n_seq * row_tiles
-  int cap;                 // partial slots; 0: no unit is split
+  int cap;                 // partial slots; 0: a launch of many units, without a plan
   int grid;                // clusters
   int* head;               // [0]: tiles of a chunk, or minus those of a span; [1 + s]: first item or tile of sequence s
   float4* part_o;          // [cap][128 groups of four values][128 rows]
@@ -301,8 +302,8 @@ __device__ __forceinline__ uint64_t seen_bits(const TreeAttnParams& p, const Ite
 // Splits the sequences' tiles into items, for each pair of CTAs a list.  Two kinds of plan:
 //   * chunks of CH tiles of every unit (a row tile of a sequence), dealt out in turn: pairs that run together read
 //     the same positions;
-//   * where no unit is much shorter than a pair's share W of all tiles, spans of W of the units' tiles laid end to end:
-//     no pair waits for another, and none has more than three items (a full unit between two parts).
+//   * spans of W tiles, a pair's share, of the units' tiles laid end to end: no pair waits for another.  Only the
+//     first and the last item of a span are parts of a unit.  (Units of W / 6 at least: kMaxItems.)
 // The cost of each in tiles: the fullest pair's items and the fill and drain of its pipeline for each, and for a split
 // the merge.  (8 x 64 nodes at 32K, E4M3: 64 units of 512 tiles on 76 pairs, 710 us whole, 630 us as spans.)
 // CTA 0 leaves the plan for the merge.  Scratch: 3 n_seq + 160 ints of shared memory.
@@ -322,13 +323,13 @@ __device__ void plan_items(const TreeAttnParams& p, const TreePlan& pl, Aux* a, 
   }
   __syncthreads();
   long long total = 0;  // (in the first warp) all units' tiles
-  int least = INT_MAX;  // of a unit; 0: there are row tiles of padding nodes, or empty sequences
+  int least = INT_MAX;  // of a unit that has any
   if (tid < 32) {
     int m = 1;
     for (int s = tid; s < n; s += 32) {
       m = max(m, nt[s]);
-      least = min(least, live[s] == pl.row_tiles ? nt[s] : 0);
-      total += (long long)nt[s] * pl.row_tiles;
+      if (nt[s]) least = min(least, nt[s]);
+      total += (long long)nt[s] * live[s];
     }
     m = __reduce_max_sync(0xffffffffu, m);
     least = __reduce_min_sync(0xffffffffu, least);
@@ -358,7 +359,7 @@ __device__ void plan_items(const TreeAttnParams& p, const TreePlan& pl, Aux* a, 
     sp |= __shfl_xor_sync(0xffffffffu, sp, 2);
     const int rounds = (items + pl.grid - 1) / pl.grid;
     float v = rounds * (ch + kItemCost) + (sp ? kMergeCost + kMergePerItem * items : 0.f);
-    if (sp && items > pl.cap) v = INFINITY;
+    if ((sp && items > pl.cap) || rounds > kMaxItems) v = INFINITY;
     if ((tid & 3) == 0) cost[c] = v, chunk[c] = ch;
   }
   __syncthreads();
@@ -370,14 +371,14 @@ __device__ void plan_items(const TreeAttnParams& p, const TreePlan& pl, Aux* a, 
     const uint32_t m0 = __ballot_sync(0xffffffffu, c0 == best), m1 = __ballot_sync(0xffffffffu, c1 == best);
     const int ch = chunk[m0 ? __ffs(m0) - 1 : 31 + __ffs(m1)];
     const long long share = (total + pl.grid - 1) / pl.grid;
-    const bool spans = total <= INT_MAX - 4096 && least > 0 && 2ll * least >= share &&
-                       share + 2 * kItemCost + kMergeCost + kMergePerItem * (pl.units + pl.grid) < best;
+    const bool spans = total > 0 && total <= INT_MAX - 4096 && (kMaxItems - 2ll) * least >= share &&
+                       share + kItemCost * (2 + pl.units / pl.grid) + kMergeCost + 2 * kMergePerItem * pl.grid < best;
     const int W = (int)share;
     int run = 0;  // items, or tiles
     for (int s0 = 0; s0 < n; s0 += 32) {
       const int s = s0 + tid;
       const int c = s >= n ? 0
-                    : spans ? nt[s] * pl.row_tiles
+                    : spans ? nt[s] * live[s]
                             : live[s] * (nt[s] ? (nt[s] + ch - 1) / ch : 1) + (pl.row_tiles - live[s]);
       int incl = c;
 #pragma unroll
@@ -413,14 +414,14 @@ __device__ void plan_items(const TreeAttnParams& p, const TreePlan& pl, Aux* a, 
           const int unit = base[it.seq] + it.rt * tiles;
           it.t0 = at - unit;
           it.t1 = min(tiles, end - unit);
-          it.slot = it.t1 - it.t0 < tiles ? pair * kItemsPerCta + count : -1;
+          it.slot = it.t0 > 0 ? 2 * pair : it.t1 < tiles ? 2 * pair + 1 : -1;
           memcpy(a->items[count], &it, sizeof(it));
           at = unit + it.t1;
         }
         a->n_items = count;
       }
     } else {
-      if (tid < kItemsPerCta && mine < run) {
+      if (tid < kMaxItems && mine < run) {
         const int s = sequence(mine), at = mine - base[s];
         const int chunks = nt[s] ? (nt[s] + ch - 1) / ch : 1;
         Item it;
@@ -1158,34 +1159,19 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeAttnParams 
   const int live = live_row_tiles(p, fresh);
   const int rt = row / kRows, r = row - rt * kRows;
   const int plan = pl.head[0], nt = (len + kKeys - 1) / kKeys, base = pl.head[1 + seq];
-  int chunks, slot0, stride;  // the unit's partials: slots slot0 (the first), then from slot1 on, `stride` apart
-  int slot1;
+  int chunks, slot0, slot1, stride;  // the unit's partials: slot0 holds the first, slot1, slot1 + stride, ... the others
   if (plan > 0) {
     chunks = nt ? (nt + plan - 1) / plan : 1;
     slot0 = base + rt, slot1 = slot0 + live, stride = live;
+    if (rt >= live || chunks == 1) return;  // written by the attention kernel
   } else {
-    // tiles [begin, begin + nt) over spans of W: those after the first begin within this unit (their item 0); in
-    // the first one it comes after the units that end there (of one length in a sequence)
+    // tiles [begin, begin + nt) over spans of W: the last item of the first span, the first ones of the others
     const int W = -plan, begin = base + rt * nt, first = begin / W;
-    chunks = nt ? (begin + nt - 1) / W - first + 1 : 1;
-    int before = 0;
-    for (int s = seq, at = begin, r = rt; at > first * W; ++before) {
-      if (r == 0) {
-        int c, f, e;
-        seq_facts(p, --s, c, f, e);
-        at -= (e + kKeys - 1) / kKeys;
-        r = pl.row_tiles - 1;
-      } else {
-        int c, f, e;
-        seq_facts(p, s, c, f, e);
-        at -= (e + kKeys - 1) / kKeys;
-        --r;
-      }
-    }
-    slot0 = first * kItemsPerCta + before, slot1 = (first + 1) * kItemsPerCta, stride = kItemsPerCta;
+    chunks = rt < live && nt ? (begin + nt - 1) / W - first + 1 : 0;
+    slot0 = 2 * first + 1, slot1 = 2 * (first + 1), stride = 2;
+    if (chunks == 1) return;
   }
-  if (rt >= live || chunks == 1) return;  // written by the attention kernel
-  if (row / p.H >= fresh) chunks = 0;     // a padding node beside live ones: zeros
+  if (row / p.H >= fresh) chunks = 0;  // a padding node: zeros
   float M = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int B = 8;
@@ -1230,12 +1216,12 @@ __global__ void tree_nothing_kernel(const TreeAttnParams p, int64_t rows) {
 
 constexpr int kPairs = 76;  // of CTAs: two of the 152 SMs each
 
-// A launch with many units needs no split: its rounds of the grid are full enough.
+// A launch with many units needs no plan: its rounds of the grid are full enough.
 TreePlan plan_of(const TreeAttnParams& p) {
   TreePlan pl = {};
   pl.row_tiles = (p.q_per_seq * p.H + kRows - 1) / kRows;
   pl.units = p.n_seq * pl.row_tiles;
-  pl.cap = pl.units <= kItemsPerCta * kPairs ? kItemsPerCta * kPairs : 0;
+  pl.cap = pl.units <= kMaxItems * kPairs ? kSlotsPerPair * kPairs : 0;
   pl.grid = pl.cap ? kPairs : (pl.units < kPairs ? pl.units : kPairs);
   return pl;
 }
