@@ -265,14 +265,6 @@ __device__ __forceinline__ int64_t tree_row(const TreeAttnParams& p, int seq, in
   return (int64_t)b * p.pages.block_size + pos % p.pages.block_size;
 }
 
-// Whether node `node` of sequence `seq` sees position `pos` (below the sequence's end).
-__device__ __forceinline__ bool tree_sees(const TreeAttnParams& p, int seq, int node, int pos, int ctx) {
-  const int j = pos - ctx;
-  if (j < 0) return true;
-  if (!p.mask) return j <= node;
-  return (p.mask[((int64_t)seq * p.q_per_seq + node) * p.mask_words + (j >> 5)] >> (j & 31)) & 1u;
-}
-
 size_t tree_attn_ws_bytes(const TreeAttnParams& p);
 cudaError_t launch_tree_attn(const TreeAttnParams& p, void* ws, cudaStream_t stream);
 

@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
     const uint32_t q_lo = kmajor_lo(smem_u32(q_s));
     int vs = 0, vph = 0, ks = 0, kph = 0, cs = 0, cph = 0;  // slots of the first product
     int ps = 0, pph = 0;                                    // of the second
-    int tile = 0, items = 0;
+    int tile = 0, qt = 0, items = 0;       // tiles of the second product, of the first
     uint32_t su = 0;                       // uses of the S buffers
     bool ok = true;
     auto commit = [&](uint64_t* bar) {
@@ -638,6 +638,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
       uint32_t parity = ((su / C::SB) & 1) ^ 1;
       if (C::FP8) {
         if (lane == 1) bar = &a->c_full[cs], parity = cph;
+        if (!C::TILED && lane == 2) bar = &a->sc_full[qt & 1], parity = (qt >> 1) & 1;  // (the softmax warps rely on it)
       } else {
         if (lane >= 2 && lane < 7) bar = &a->k_full[k_slot(lane - 2)], parity = k_phase(lane - 2);
       }
@@ -676,6 +677,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
       __syncwarp();
       ++su;
       if (j1 == 9) {
+        ++qt;
         if (C::FP8) {
           if (++cs == C::CS) cs = 0, cph ^= 1;
         } else {
@@ -953,17 +955,20 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
             for (int k = 0; k < 8; ++k) scale[k] = *reinterpret_cast<const float4*>(from + 4 * k);
           }
         };
-        if constexpr (C::FP8) ok = wait(a, &a->sc_full[tile & 1], (tile >> 1) & 1, err) && ok;
-        if constexpr (!C::TILED) scales(sc);
         if constexpr (C::TILED) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = 0.f;
         }
 #pragma unroll 1
         for (int g = 0; g < C::GROUPS; ++g, ++su) {
-          // (the groups are in the order of the slots, the scales in that of the columns)
-          if constexpr (C::TILED) scales(sc + kKeys * (g < 4 ? g ^ (rank << 1) : 4));
+          // (the groups are in the order of the slots, the scales in that of the columns; those are loaded before the
+          // wait where the wait for the first accumulation has not shown that they are there)
+          if (C::TILED) {
+            if (g == 0) ok = wait(a, &a->sc_full[tile & 1], (tile >> 1) & 1, err) && ok;
+            scales(sc + kKeys * (g < 4 ? g ^ (rank << 1) : 4));
+          }
           ok = wait(a, &a->s_full[su % C::SB], (su / C::SB) & 1, err) && ok;
+          if (!C::TILED) scales(sc);
           tc_fence_after();
           float s[32];
           tmem_ld_sync(lane_base + C::COL_S + kKeys * (su % C::SB) + 32 * h, s);
