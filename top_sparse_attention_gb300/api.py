@@ -400,10 +400,11 @@ def dsa_block_plan(n_ctx, n_new, free_blocks, block_table, *, block_size, num_bl
             raise ValueError(f"{what}: packed rows need their number (rows)")
         rows = n_seq * q_per_seq
     if out is None:
-        # one allocation for all outputs
-        dst, *parts = torch.empty(4 * rows + 2 * n_seq + 2, dtype=i32, device=dev).split_with_sizes(
-            (2 * rows, rows, rows, n_seq + 1, n_seq, 1))
-        out = BlockPlan(dst.view(torch.int64), *parts)
+        # (six allocations take 9 us of the host, six views of one 12.5: most of it when they are freed)
+        new = torch.empty
+        out = BlockPlan(new(rows, dtype=torch.int64, device=dev), new(rows, dtype=i32, device=dev),
+                        new(rows, dtype=i32, device=dev), new(n_seq + 1, dtype=i32, device=dev),
+                        new(n_seq, dtype=i32, device=dev), new(1, dtype=i32, device=dev))
     else:
         for name, t, n, kind in (("dst_rows", out.dst_rows, rows, torch.int64), ("pos", out.pos, rows, i32),
                                  ("seq", out.seq, rows, i32), ("row_start", out.row_start, n_seq + 1, i32),
@@ -422,15 +423,14 @@ _ROPE_STYLE = {"half": N.DSA_ROPE_HALF, "pairs": N.DSA_ROPE_PAIRS}
 
 
 def _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style):
-    rows = x.shape[0]
-    if pos.dim() == 1:
-        pos = pos[:, None]
-    _check(what, dev, "pos", pos, torch.int32, 2)
+    shape = x.shape
+    one = pos.dim() == 1
+    _check(what, dev, "pos", pos, torch.int32, 1 if one else 2)
     _check(what, dev, "inv_freq", inv_freq, torch.float32, 1)
     if rot_dim is None:
-        rot_dim = x.shape[-1] - rot_off
-    n_axes = pos.shape[1]
-    if pos.shape[0] != rows or 2 * inv_freq.shape[0] != rot_dim:
+        rot_dim = shape[-1] - rot_off
+    n_axes = 1 if one else pos.shape[1]
+    if pos.shape[0] != shape[0] or 2 * inv_freq.shape[0] != rot_dim:
         raise ValueError(f"{what}: pos must have one row per row of x, inv_freq rot_dim / 2 entries")
     if pair_axis is None and sections is not None:
         if len(sections) != n_axes:
@@ -442,7 +442,7 @@ def _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axi
         raise ValueError(f"{what}: {len(pair_axis)} pairs have an axis, rot_dim / 2 = {rot_dim // 2} need one")
     if style not in _ROPE_STYLE:
         raise ValueError(f"{what}: style must be one of {tuple(_ROPE_STYLE)}, got {style!r}")
-    return pos, rot_dim, n_axes, pair_axis, _ROPE_STYLE[style]
+    return rot_dim, n_axes, pair_axis, _ROPE_STYLE[style]
 
 
 def dsa_rope(x, pos, inv_freq, *, rot_off=0, rot_dim=None, sections=None, pair_axis=None, style="half",
@@ -455,23 +455,25 @@ def dsa_rope(x, pos, inv_freq, *, rot_off=0, rot_dim=None, sections=None, pair_a
     what = "dsa_rope"
     dev = _cuda_device(what, x)
     _check(what, dev, "x", x, torch.bfloat16, None, dense=False)
-    if x.dim() not in (2, 3) or (x.shape[-1] > 1 and x.stride(-1) != 1):
+    shape, xs = x.shape, x.stride()
+    if len(shape) not in (2, 3) or (shape[-1] > 1 and xs[-1] != 1):
         raise ValueError(f"{what}: x must be [rows, heads, width] or [rows, width] with dense columns")
-    pos, rot_dim, n_axes, pair_axis, code = _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style)
+    rot_dim, n_axes, pair_axis, code = _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        os = out.stride()
     else:
-        _check(what, dev, "out", out, torch.bfloat16, x.dim(), dense=False)
-        if out.shape != x.shape or (out.shape[-1] > 1 and out.stride(-1) != 1):
+        _check(what, dev, "out", out, torch.bfloat16, len(shape), dense=False)
+        os = out.stride()
+        if out.shape != shape or (shape[-1] > 1 and os[-1] != 1):
             raise ValueError(f"{what}: out must have x's shape and dense columns")
-    three = x.dim() == 3
-    heads = x.shape[1] if three else 1
-    if x.shape[0] == 0 or heads == 0:
+    rows, width = shape[0], shape[-1]
+    heads = shape[1] if len(shape) == 3 else 1
+    if rows == 0 or heads == 0:
         return out
-    xh, oh = (x.stride(1), out.stride(1)) if three and heads > 1 else (x.shape[-1], x.shape[-1])
-    _run(what, N.lib.dsa_rope, dev, stream, x.data_ptr(), x.stride(0), xh, x.shape[0], heads, x.shape[-1], int(rot_off),
-         int(rot_dim), pos.data_ptr(), n_axes, pair_axis, inv_freq.data_ptr(), code, int(bool(inverse)), out.data_ptr(),
-         out.stride(0), oh)
+    xh, oh = (xs[1], os[1]) if heads > 1 else (width, width)
+    _run(what, N.lib.dsa_rope, dev, stream, x.data_ptr(), xs[0], xh, rows, heads, width, int(rot_off), int(rot_dim),
+         pos.data_ptr(), n_axes, pair_axis, inv_freq.data_ptr(), code, int(bool(inverse)), out.data_ptr(), os[0], oh)
     return out
 
 
@@ -484,10 +486,10 @@ def dsa_rope_append(x, pos, inv_freq, dst, *, scale=None, dst_rows=None, rot_off
     what = "dsa_rope_append"
     dev = _cuda_device(what, x)
     _check(what, dev, "x", x, torch.bfloat16, 2, dense=False)
-    if x.shape[1] > 1 and x.stride(1) != 1:
+    (rows, width), (x_row, x_col) = x.shape, x.stride()
+    if width > 1 and x_col != 1:
         raise ValueError(f"{what}: x must have dense columns")
-    width = x.shape[1]
-    pos, rot_dim, n_axes, pair_axis, code = _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style)
+    rot_dim, n_axes, pair_axis, code = _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style)
     if dst.dtype == torch.bfloat16:
         kind, want = N.DSA_BF16, None
     elif scale is None:
@@ -499,21 +501,22 @@ def dsa_rope_append(x, pos, inv_freq, dst, *, scale=None, dst_rows=None, rot_off
     else:
         kind, want = N.DSA_FP8_E4M3_T128, (-(-width // 128),)
     _check(what, dev, "dst", dst, torch.bfloat16 if kind == N.DSA_BF16 else torch.uint8, 2, dense=False)
-    if dst.shape[1] < width or dst.stride(1) != 1 or (dst.shape[0] > 1 and dst.stride(0) < width):
+    (n_dst, dst_width), (dst_row, dst_col) = dst.shape, dst.stride()
+    if dst_width < width or dst_col != 1 or (n_dst > 1 and dst_row < width):
         raise ValueError(f"{what}: dst rows must hold {width} dense columns")
     if want is not None:
         _check(what, dev, "scale", scale, torch.uint8 if kind == N.DSA_MXFP8_E4M3 else torch.float32)
-        if scale.shape[1:] != want or scale.shape[0] < dst.shape[0]:
-            raise ValueError(f"{what}: scale must be [{dst.shape[0]}{''.join(f', {n}' for n in want)}], got {tuple(scale.shape)}")
+        if scale.shape[1:] != want or scale.shape[0] < n_dst:
+            raise ValueError(f"{what}: scale must be [{n_dst}{''.join(f', {n}' for n in want)}], got {tuple(scale.shape)}")
     _check(what, dev, "dst_rows", dst_rows, torch.int64, 1)
-    if dst_rows is not None and dst_rows.shape[0] != x.shape[0]:
+    if dst_rows is not None and dst_rows.shape[0] != rows:
         raise ValueError(f"{what}: dst_rows must have one entry per row of x")
-    if x.shape[0] == 0:
+    if rows == 0:
         return
-    _run(what, N.lib.dsa_rope_append, dev, stream, x.data_ptr(), x.stride(0), x.shape[0], width, int(rot_off),
-         int(rot_dim), pos.data_ptr(), n_axes, pair_axis, inv_freq.data_ptr(), code, kind, dst.data_ptr(),
-         (dst.stride(0) if dst.shape[0] > 1 else width) * dst.element_size(), dst.shape[0], None if kind == N.DSA_BF16 else scale.data_ptr(),
-         _ptr(dst_rows))
+    _run(what, N.lib.dsa_rope_append, dev, stream, x.data_ptr(), x_row, rows, width, int(rot_off), int(rot_dim),
+         pos.data_ptr(), n_axes, pair_axis, inv_freq.data_ptr(), code, kind, dst.data_ptr(),
+         (dst_row if n_dst > 1 else width) * (2 if kind == N.DSA_BF16 else 1), n_dst,
+         None if kind == N.DSA_BF16 else scale.data_ptr(), _ptr(dst_rows))
 
 
 def dsa_tree_attn(q, kv, n_ctx, *, sm_scale, q_per_seq, n_new=None, tree_mask=None, kv_scale=None, block_table=None,
@@ -539,43 +542,47 @@ def dsa_tree_attn(q, kv, n_ctx, *, sm_scale, q_per_seq, n_new=None, tree_mask=No
             raise ValueError(f"{what}: tree_mask must be [{T}, {(q_per_seq + 31) // 32}], got {tuple(tree_mask.shape)}")
     paged = block_table is not None
     axes = 2 if paged else 3
-    _check(what, dev, "kv", kv, torch.bfloat16 if kv.dtype == torch.bfloat16 else torch.uint8, axes, dense=False)
-    if kv.shape[-1] < D or kv.stride(-1) != 1:
+    bf16 = kv.dtype == torch.bfloat16
+    _check(what, dev, "kv", kv, torch.bfloat16 if bf16 else torch.uint8, axes, dense=False)
+    shape, strides = kv.shape, kv.stride()
+    if shape[-1] < D or strides[-1] != 1:
         raise ValueError(f"{what}: kv rows must hold {D} dense columns")
     a = N.DsaTreeArgs()
     a.kv_dtype = N.DSA_BF16
-    if kv.dtype == torch.uint8:
+    if not bf16:
         if kv_scale is None:
             raise ValueError(f"{what}: E4M3 rows need their scales")
         a.kv_dtype = N.DSA_FP8_E4M3_T128 if kv_scale.dim() == axes else N.DSA_FP8_E4M3
         _check(what, dev, "kv_scale", kv_scale, torch.float32)
-        want = tuple(kv.shape[:-1]) + ((-(-D // 128),) if kv_scale.dim() == axes else ())
+        want = tuple(shape[:-1]) + ((-(-D // 128),) if kv_scale.dim() == axes else ())
         if tuple(kv_scale.shape) != want:
             raise ValueError(f"{what}: kv_scale must be {list(want)}, got {tuple(kv_scale.shape)}")
         a.kv_scale = kv_scale.data_ptr()
-    elem = kv.element_size()
+    elem = 2 if bf16 else 1
     if paged:
         _check(what, dev, "block_table", block_table, torch.int32, 2)
         if L is None or block_size <= 0 or block_table.shape[0] != n_seq:
             raise ValueError(f"{what}: paged caches need L, block_size and one row of block_table per sequence")
         a.block_table, a.block_size, a.max_blocks = block_table.data_ptr(), int(block_size), block_table.shape[1]
-        a.num_blocks = kv.shape[0] // int(block_size)
-        a.kv_row_stride = kv.stride(0) * elem
+        a.num_blocks = shape[0] // int(block_size)
+        a.kv_row_stride = strides[0] * elem
     else:
-        if kv.shape[0] != n_seq or (L is not None and L != kv.shape[1]):
-            raise ValueError(f"{what}: kv must be [{n_seq}, L, {D}], got {tuple(kv.shape)}")
-        L = kv.shape[1]
-        a.kv_row_stride, a.kv_seq_stride = kv.stride(1) * elem, kv.stride(0) * elem
+        if shape[0] != n_seq or (L is not None and L != shape[1]):
+            raise ValueError(f"{what}: kv must be [{n_seq}, L, {D}], got {tuple(shape)}")
+        L = shape[1]
+        a.kv_row_stride, a.kv_seq_stride = strides[1] * elem, strides[0] * elem
     if out is None:
-        out = torch.empty(T, H, 512, dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=dev)
     else:
         _check(what, dev, "out", out, torch.bfloat16, 3)
+        if tuple(out.shape) != (T, H, 512):
+            raise ValueError(f"{what}: out must be [{T}, {H}, 512]")
     if lse is None:
-        lse = torch.empty(T, H, dtype=torch.float32, device=dev)
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
     else:
         _check(what, dev, "lse", lse, torch.float32, 2)
-    if tuple(out.shape) != (T, H, 512) or tuple(lse.shape) != (T, H):
-        raise ValueError(f"{what}: out must be [{T}, {H}, 512], lse [{T}, {H}]")
+        if tuple(lse.shape) != (T, H):
+            raise ValueError(f"{what}: lse must be [{T}, {H}]")
     a.n_seq, a.q_per_seq, a.L, a.H, a.D_qk, a.D_v, a.sm_scale = n_seq, int(q_per_seq), int(L), H, D, 512, float(sm_scale)
     a.n_ctx, a.n_new, a.tree_mask = n_ctx.data_ptr(), _ptr(n_new), _ptr(tree_mask)
     a.q, a.kv, a.out, a.lse = q.data_ptr(), kv.data_ptr(), out.data_ptr(), lse.data_ptr()
