@@ -417,7 +417,9 @@ dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int wi
  * over the positions it sees.  A node that sees nothing, and a node i >= m (padding), gets out = 0
  * and lse = -inf.  The contents of a cache row do not matter to a node that does not see it (a
  * position past the end, another branch of the tree: infinities and NaN included); a NaN in a row
- * that a node sees makes that node's output NaN.
+ * that a node sees makes that node's output NaN.  With E4M3 rows the elements of a query row below
+ * 2^-13 of its largest one are taken to 2^-20 of that one (the others exactly, as with bf16 rows), and an
+ * infinity or NaN in it makes that row's output NaN.
  *   q          device bf16 [n_seq * q_per_seq, H, 576]
  *   kv         row r of sequence s at kv + s*kv_seq_stride + r*kv_row_stride bytes; with block_table
  *              a pool of num_blocks * block_size rows (see dsa_args: block_size a multiple of 64)
@@ -428,7 +430,7 @@ dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int wi
  * irrelevant; calls (and captured graphs) that share it must not run at the same time.
  * Supported: D_qk = 576, D_v = 512; kv_dtype DSA_BF16, DSA_FP8_E4M3 or DSA_FP8_E4M3_T128 (finite
  * codes); 1 <= H <= 128; 1 <= q_per_seq <= 1024; n_seq <= 4096; L <= 2^31 - 4097; pointers 16-byte aligned, row
- * strides multiples of 16 bytes, rows at most 2^24 bytes apart.
+ * strides multiples of 16 bytes, below 2^40.
  * ------------------------------------------------------------------------------------------ */
 typedef struct dsa_tree_args {
   int n_seq, q_per_seq, L, H, D_qk, D_v;

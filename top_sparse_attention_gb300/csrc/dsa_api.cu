@@ -339,7 +339,9 @@ dsa_status check_tree(const dsa_tree_args* a) {
   if (a->L == 0) return DSA_OK;
   if (!a->kv || !aligned16(a->kv)) return DSA_ERR_INVALID_ARG;
   if (a->kv_row_stride % 16 != 0 || a->kv_row_stride < 576 * elem) return DSA_ERR_INVALID_ARG;
-  if (a->kv_row_stride > (1 << 24)) return DSA_ERR_UNSUPPORTED;
+  // (the strides of a tensor map)
+  if (a->kv_row_stride >= (1ll << 40) || (!a->block_table && a->n_seq > 1 && a->kv_seq_stride >= (1ll << 40)))
+    return DSA_ERR_UNSUPPORTED;
   if (!a->block_table && a->n_seq > 1 &&
       (a->kv_seq_stride % 16 != 0 || a->kv_seq_stride < (int64_t)a->L * a->kv_row_stride))
     return DSA_ERR_INVALID_ARG;

@@ -4,38 +4,40 @@
 //   logit[p] = sm_scale * q[i, h] . Kv[p],  out[i, h] = sum_p softmax(logit)[p] * Kv[p, :512].
 //
 // A "row" is one head of one node; the rows of a sequence are consecutive in q and share its cache.
-// A cluster of two CTAs takes 128 rows and walks tiles of 64 positions.  CTA c takes the first product
-// and the softmax of 32 of the positions, and the second product of half of the value columns:
-//   * S[128 x 32] = Q K_c^T: A = the rows (M = 128; 448 of their columns in tensor memory, 128 in shared
-//     memory), B = its 32 positions (K-major), 36 steps of K = 16;
+// Two CTAs take 128 rows and walk tiles of 64 positions; each takes the first product of all of them and the second
+// one for half of the value columns, on its own (no cluster: nothing is exchanged):
+//   * S[128 x 64] = Q K^T, 36 steps: A = the rows (M = 128; 320 of their columns in tensor memory, 128 with tile
+//     scales, the others in shared memory), B = the positions (K-major);
 //   * one pass over the positions keeps a reference maximum m and a sum l per row,
 //       l' = l 2^(m - m') + sum_p 2^(x_p - m'),   o' = o 2^(m - m') + sum_p 2^(x_p - m') v_p,
 //     where m is moved only when a tile's maximum exceeds it by more than 2^8 (weights stay below 2^8,
-//     fp32 sums and bf16 weights lose nothing by it), so o in tensor memory is rescaled rarely.  The CTAs send
-//     each other their rows' maxima over their positions a tile ahead, so both move m alike;
-//   * each sends the other its P[128 x 32] (bf16): 8 KB per tile through distributed shared memory;
-//   * O_c[128 x 256] += P V_c: A = P in shared memory, B = 256 value columns of all 64 positions, read MN-major
-//     (values along N), 4 steps of K = 16 with N = 256.  A CTA's own positions are in shared memory whole, of
-//     the other's only these 256 columns are loaded besides: 832 of 1152 bytes per position and CTA.
-// Why two CTAs: o for 128 rows x 512 values fills a tensor memory (512 columns), which leaves no room for S;
-// with half of the values it takes 256 columns, q 224, S 32.  Measured against it (8 x 64 nodes
-// at 32K, E4M3 rows; 8 x 8 nodes at 32K, bf16): one CTA with 64 rows, q in shared memory and o
-// transposed, 1805 and 149 us (245 KB of shared memory read per tile by the MMAs, room for two tiles);
-// columns of the rows split between the CTAs, whose partial S then travel, 1090 and 120 us (16 to 32 KB
-// per tile at about 20 bytes per cycle between two SMs).
+//     fp32 sums and bf16 weights lose nothing by it), so o in tensor memory is rescaled rarely;
+//   * O_c[128 x 256] += P V_c: A = the weights, bf16, in tensor memory, B = 256 value columns of the positions, read
+//     MN-major (values along N), 4 steps of K = 16 with N = 256.
+// Why two CTAs: o for 128 rows x 512 values fills a tensor memory (512 columns), which leaves no room for S; with half
+// of the values it takes 256 columns, q 160, S 64, the weights 32.  Why both take the whole first product: an MMA of
+// N = 64 with A in tensor memory takes 32 cycles, one of N = 32 33, so that sharing the positions out saves nothing.
+// Measured (8 x 64 nodes at 32K, E4M3 rows; 8 x 8 nodes at 32K, bf16; us): this form 622 and 94; the positions of the
+// first product shared out and weights exchanged through distributed shared memory 1002 and 105; columns shared out
+// and partial S exchanged 1090 and 120; one CTA with 64 rows and q in shared memory 1805 and 149.
 //
-// Weights are rounded to bf16 for the second product (as the bf16 cache is); sums, maxima, logits and
-// outputs are fp32.  E4M3 rows are widened to bf16 exactly, and their scales are applied in fp32 to the
-// logit and to the weight (128-column scales: one S accumulation per scale tile, one P per value tile).
+// Weights are rounded to bf16 for the second product (as the bf16 cache is); sums, maxima, logits and outputs are
+// fp32.  E4M3 codes enter the first product as they are: q's bf16 values, scaled by a power of two per row, are the sum
+// of an E4M3 and an E5M2 value, exactly down to 2^-13 of the row's largest value and to 2^-20 of it below, and the
+// 8-bit MMAs (K = 32, both parts) cost what bf16 ones would, at half of the shared memory.  For the second product the
+// codes of a CTA's own value columns are widened to bf16 exactly.  (Widening all of them: 1002 us instead of 803 at the
+// time, 8 x 64 nodes.)  The positions' scales are applied in fp32 to the logit and to the weight (128-column scales:
+// one S accumulation per scale tile, one P per value tile).
 //
-// Warp roles: producer (TMA), MMA issuer, scale loader, credits of the exchange, eight softmax warps (a row and
-// 16 positions per thread; also the query load, the rescale and the epilogue), for E4M3 eight warps that
-// load, widen and store the tile.
+// Bound: with few rows the memory, with many the tensor cores: 36 x 32 to 48 + 512 cycles per tile are 1920 of the
+// measured 2400 (bf16) to 2600; with tile scales the softmax warps' turn from one accumulation to the next (6200).
 //
-// Work split: items (sequence, chunk of its tiles, row tile), in this order, so that clusters that run
-// together read the same positions and the cache comes from HBM once.  The lengths are on the device:
-// every CTA evaluates the same cost model over them and picks the chunk length (plan_items); partial
-// results are merged by tree_combine_kernel.
+// Warp roles: producer (TMA), MMA issuer, scale loader, eight softmax warps (a row and 32 positions per thread; also
+// the query load, the rescale and the epilogue), for E4M3 four warps that widen the value columns.
+//
+// Work split: items (sequence, chunk of its tiles, row tile) for pairs of CTAs.  The lengths are on the device:
+// every CTA evaluates the same cost model over them (plan_items); partial results are merged by
+// tree_combine_kernel.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <string.h>
@@ -58,12 +60,12 @@ constexpr float kLazy = 8.f;              // log2 growth of a row's maximum that
 constexpr int kMaxItems = 8;              // of a pair of CTAs, in a planned launch
 constexpr int kSlotsPerPair = 3;          // partial results
 constexpr int kAhead = 2;                 // tiles between the request to L2 and the load into shared memory
-constexpr int kColO = 0;                  // tensor-memory columns: O, then boxes of q, then S
+constexpr int kColO = 0;                  // tensor-memory columns: O, then boxes of q, S and the weights
 
 enum { kBf16 = 0, kFp8Row = 1, kFp8Tile = 2 };
 
 struct Aux {
-  uint64_t v_full[3], v_empty[3], k_full[10], k_empty[10], c_full[2], c_empty[2], s_full[2], s_empty[2], p_full, pv_done;
+  uint64_t v_full[3], v_empty[3], k_full[7], k_empty[7], c_full[2], c_empty[2], s_full[2], s_empty[2], p_full, pv_done;
   uint64_t o_done, o_free, q_full, sc_full[2], sc_empty[2], drain;
   uint32_t tmem;
   int abort;
@@ -112,7 +114,7 @@ struct TreePlan {
   int row_tiles;           // per sequence
   int units;               // n_seq * row_tiles
   int cap;                 // partial slots; 0: a launch of many units, without a plan
-  int grid;                // clusters
+  int grid;                // pairs of CTAs
   int* head;               // [0]: tiles of a chunk, or minus those of a span; [1 + s]: first item or tile of sequence s
   float4* part_o;          // [cap][128 groups of four values][128 rows]
   float2* part_ml;         // [cap][128 rows]
