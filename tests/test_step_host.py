@@ -184,6 +184,7 @@ def _tree_args(**kw):
     (dict(n_seq=-1), 1), (dict(q_per_seq=0), 1), (dict(L=-1), 1), (dict(H=0), 1), (dict(n_ctx=None), 1), (dict(q=None), 1),
     (dict(out=None), 1), (dict(kv=None), 1), (dict(q=24), 1), (dict(kv=24), 1), (dict(out=24), 1),
     (dict(D_qk=512), 2), (dict(D_v=256), 2), (dict(H=129), 2), (dict(q_per_seq=1025), 2), (dict(n_seq=4097), 2), (dict(kv_dtype=2), 2),
+    (dict(kv_row_stride=1 << 40, kv_seq_stride=1 << 48), 2), (dict(n_seq=2, kv_seq_stride=1 << 40), 2),
     (dict(kv_row_stride=1150), 1), (dict(kv_row_stride=1136), 1), (dict(kv_seq_stride=1000), 1),
     (dict(kv_dtype=1, kv_row_stride=576, kv_seq_stride=576 * 128), 1),       # no scales
     (dict(block_table=F, block_size=48, max_blocks=4, num_blocks=8), 1), (dict(block_table=F, block_size=64, max_blocks=1, num_blocks=8), 1),

@@ -186,6 +186,26 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 operations per instruction.  (8 x 64 nodes at 32K, E4M3 rows with row scales: 625 -> 597 us; with tile
+// scales, where the waits between the accumulations bind, they measured slower, 196 against 185 us, and are not used.)
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t&>(r)) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t&>(r)) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -977,17 +997,16 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0 && ok) mbar_arrive(&a->s_empty[su % C::SB]);
+          const float2 rs = make_float2(row_scale, row_scale);
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            float4 f = make_float4(row_scale, row_scale, row_scale, row_scale);
-            if constexpr (C::FP8) f = scale[k >> 2];
-            if constexpr (C::TILED) {
-              x[k] = fmaf(f.x, s[k], x[k]), x[k + 1] = fmaf(f.y, s[k + 1], x[k + 1]);
-              x[k + 2] = fmaf(f.z, s[k + 2], x[k + 2]), x[k + 3] = fmaf(f.w, s[k + 3], x[k + 3]);
-            } else {
-              if constexpr (C::FP8) f.x *= row_scale, f.y *= row_scale, f.z *= row_scale, f.w *= row_scale;
-              x[k] = s[k] * f.x, x[k + 1] = s[k + 1] * f.y, x[k + 2] = s[k + 2] * f.z, x[k + 3] = s[k + 3] * f.w;
-            }
+          for (int k = 0; k < 32; k += 2) {
+            const float2 z = make_float2(s[k], s[k + 1]);
+            float2 f = rs, y;
+            if constexpr (C::FP8) f = k & 2 ? make_float2(scale[k >> 2].z, scale[k >> 2].w) : make_float2(scale[k >> 2].x, scale[k >> 2].y);
+            if constexpr (C::TILED) y = make_float2(fmaf(f.x, z.x, x[k]), fmaf(f.y, z.y, x[k + 1]));
+            else if constexpr (C::FP8) y = mul2(z, mul2(f, rs));
+            else y = mul2(z, rs);
+            x[k] = y.x, x[k + 1] = y.y;
           }
         }
         if constexpr (C::TILED) {
@@ -1075,13 +1094,19 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         }
         // ---- weights, times the positions' scales (a hidden position's weight is 0 whatever its scale holds)
         const float mu = m == -INFINITY ? 0.f : m;
-        float sum[2] = {0.f, 0.f};
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          x[k] = ex2(x[k] - mu);
-          sum[k & 1] += x[k];
+        for (int k = 0; k < 32; k += 2) {
+          if constexpr (C::TILED) {
+            x[k] = ex2(x[k] - mu), x[k + 1] = ex2(x[k + 1] - mu);
+            sum.x += x[k], sum.y += x[k + 1];
+          } else {
+            const float2 y = add2(make_float2(x[k], x[k + 1]), make_float2(-mu, -mu));
+            x[k] = ex2(y.x), x[k + 1] = ex2(y.y);
+            sum = add2(sum, make_float2(x[k], x[k + 1]));
+          }
         }
-        l += sum[0] + sum[1];
+        l += sum.x + sum.y;
         const bool hides = C::FP8 && (edge || bad);
 #pragma unroll
         for (int b = 0; b < C::PC; ++b) {
@@ -1092,7 +1117,13 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
             float z0 = x[k], z1 = x[k + 1];
             if constexpr (C::FP8) {
               const float4 f = scale[k >> 2];
-              z0 *= k & 2 ? f.z : f.x, z1 *= k & 2 ? f.w : f.y;
+              const float2 f2 = k & 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y);
+              if constexpr (C::TILED) {
+                z0 *= f2.x, z1 *= f2.y;
+              } else {
+                const float2 z = mul2(make_float2(z0, z1), f2);
+                z0 = z.x, z1 = z.y;
+              }
               if (hides) z0 = x[k] == 0.f ? 0.f : z0, z1 = x[k + 1] == 0.f ? 0.f : z1;
             }
             v[k >> 1] = pack_bf16(z0, z1);
