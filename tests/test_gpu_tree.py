@@ -220,6 +220,27 @@ def test_many_short_sequences(dsa, n):
     Case(n, rng.integers(0, 150, n), 2, 16, "bf16", new=rng.integers(0, 3, n)).run(dsa)
 
 
+@pytest.mark.parametrize("kv", FORMATS)
+def test_a_context_of_hundreds_of_millions_of_positions(dsa, kv):
+    # a table that names the same two blocks again and again: the softmax is theirs, lse that of `times` copies; the
+    # scales' number (five per position) passes 2^31.  Sums: 7.0e6 tiles over 76 pairs of CTAs (92500 each), an fp32
+    # rounding of the sum per tile and of the output per 16 positions (truncated: an ulp), so 92500 * 2^-24 = 0.6 % and
+    # 4 * 92500 * 2^-23 = 4.4 % at the very worst
+    times = 3_515_625  # 450 million positions
+    c = Case(25, [128 * times], 1, 3, kv, 64, mask="chain", new=[0], L=128)
+    table = torch.from_numpy(c.table[0, :2].copy()).cuda().repeat(times)[None].contiguous()
+    out, lse = dsa.dsa_tree_attn(
+        c.q, c.cache, torch.tensor([128 * times - 1], dtype=torch.int32, device="cuda"), sm_scale=1 / 24, q_per_seq=1,
+        kv_scale=c.scale, block_table=table, block_size=64, L=128 * times)
+    kv64 = c.val[[c.row_of(0, p) for p in range(128)]]
+    q = c.q.double().cpu().numpy().reshape(1, 3, D)
+    want, want_lse = oracle.tree_attention(q, kv64, 128, 1, np.zeros((1, 1), bool), 1 / 24, DV)
+    x = q[0] @ kv64.T / 24
+    A = np.exp(x - want_lse[0][:, None]) @ np.abs(kv64[:, :DV])
+    assert np.all(np.abs(lse.double().cpu().numpy()[0] - want_lse[0] - np.log(times)) <= 0.006 + 2.0**-10)
+    assert np.all(np.abs(out.double().cpu().numpy()[0] - want[0]) <= (0.05 + 2.0**-7) * A)
+
+
 @pytest.mark.parametrize("kv", ["fp8", "t128"])
 def test_queries_of_a_wide_range(dsa, kv):
     # E4M3 rows: a query row enters as E4M3 plus E5M2, exact from 2^-13 of its largest value on, to 2^-20 of it below

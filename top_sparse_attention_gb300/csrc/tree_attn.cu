@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         int64_t row = tree_row(p, it.seq, t * kKeys);
         const bool bad = row < 0;
         row += p.pages.table ? 0 : (int64_t)it.seq * p.L;
-        const int n = (it.len - t * kKeys) * C::NSC;
+        const int n = min(it.len - t * kKeys, kKeys) * C::NSC;
         const float* src = p.kv_scale + row * C::NSC;
         float v[2 * C::NSC + 1];
 #pragma unroll
