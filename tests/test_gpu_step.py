@@ -322,6 +322,41 @@ def test_rope_append_at_position_zero_is_the_quantiser(dsa, fmt):
     assert torch.equal(cache, want[0]) and torch.equal(scale, want[1])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "t128", "mx"])
+@pytest.mark.parametrize("width,rot_off,rot_dim,kind,style,pitch", [
+    (576, 512, 64, "three", "half", 576), (576, 512, 64, None, "pairs", 592), (640, 0, 32, "two", "pairs", 640),
+    (160, 96, 64, "two", "half", 168), (704, 64, 64, None, "half", 704),
+])
+def test_rope_append_of_many_rows_is_that_of_few(dsa, fmt, width, rot_off, rot_dim, kind, style, pitch):
+    # one call of so many rows that a warp may take two at a time, against calls of few: bit for bit, also at quotients
+    # that are rounding midpoints (small integers, scales that are 7 times a power of two over 448)
+    rows = 32768 + 777
+    rng = np.random.default_rng(width + rot_dim)
+    n_axes, axis = _axes(kind, rot_dim // 2)
+    x = torch.from_numpy(rng.standard_normal((rows, width)) * np.ldexp(1.0, rng.integers(-12, 12, (rows, 1)))).bfloat16()
+    x[1000:3000] = torch.from_numpy(rng.integers(-28, 29, (2000, width)).astype(np.float32)).bfloat16()
+    x[4000:4010] = 0
+    pos = rng.integers(0, 1 << 18, (rows, n_axes))
+    pos[1000:3000] = 0
+    pool = rows + 20
+    dst = rng.permutation(pool)[:rows].astype(np.int64)
+    dst[[3, 4000, rows - 1]] = -1
+    x, pos, dst, f = x.cuda(), _i32(pos), torch.from_numpy(dst).cuda(), torch.from_numpy(_inv_freq(rot_dim // 2)).cuda()
+    kw = dict(rot_off=rot_off, rot_dim=rot_dim, pair_axis=axis, style=style)
+    cache, scale = _append(dsa, fmt, x, pos, f, dst, pool, pitch, **kw)
+    few = torch.full_like(cache, 3.0 if fmt == "bf16" else 0xEF)
+    few_scale = None if scale is None else torch.full_like(scale, 0xCD if fmt == "mx" else -7.0)
+    for i in range(0, rows, 3001):
+        dsa.dsa_rope_append(x[i:i + 3001], pos[i:i + 3001], f, few[:, :width], scale=few_scale, dst_rows=dst[i:i + 3001], **kw)
+    assert torch.equal(cache, few) and (scale is None or torch.equal(scale, few_scale))
+    big = dst.clone()
+    big[77] = pool  # past the cache: dropped and reported
+    if fmt == "t128" and width == 576:
+        dsa.dsa_rope_append(x, pos, f, cache[:, :width], scale=scale, dst_rows=big, **kw)
+        assert dsa.dsa_get_device_error() == 1
+        assert torch.equal(cache, few) and torch.equal(scale, few_scale)
+
+
 def test_rope_append_row_past_the_cache_is_dropped(dsa):
     x = torch.ones(3, 64, dtype=torch.bfloat16, device="cuda")
     cache = torch.zeros(6, 64, dtype=torch.bfloat16, device="cuda")

@@ -63,8 +63,9 @@ __device__ __forceinline__ void fill_turns(const RopeParams& p, int64_t row, con
   __syncwarp();
 }
 
+// (The roundings are spelled out, so that every kernel of this file turns a pair to the same bits.)
 __device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
-  const float y0 = a * cs.x - b * cs.y, y1 = b * cs.x + a * cs.y;
+  const float y0 = fmaf(a, cs.x, -__fmul_rn(b, cs.y)), y1 = fmaf(b, cs.x, __fmul_rn(a, cs.y));
   a = y0;
   b = y1;
 }
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(32 * kWarps) rope_append_kernel(const RopePara
     const bool low = p.half ? at < p.pairs : (at & 1) == 0;
     const int k = p.half ? (low ? at : at - p.pairs) : at >> 1;
     const float w = __bfloat162float(x[c + (p.half ? (low ? p.pairs : -p.pairs) : (low ? 1 : -1))]);
-    return v * cs[k].x + w * (low ? -cs[k].y : cs[k].y);
+    return fmaf(v, cs[k].x, __fmul_rn(w, low ? -cs[k].y : cs[k].y));
   };
   uint8_t* out = p.dst + dst * p.dst_row_stride;
   if constexpr (FMT == kFmtBf16) {
