@@ -241,6 +241,36 @@ def test_a_context_of_hundreds_of_millions_of_positions(dsa, kv):
     assert np.all(np.abs(out.double().cpu().numpy()[0] - want[0]) <= (0.05 + 2.0**-7) * A)
 
 
+@pytest.mark.parametrize("kv", FORMATS)
+def test_halves_of_the_values_whose_logits_round_apart(dsa, kv):
+    # 2^25 + 1.5 - 2^25 + 8 is 8 or 9.5 in fp32, by the order of the columns, and a row's reference maximum moves at
+    # more than 8: the CTAs that take the two halves of the values may go either way.  All rows hold the same values in
+    # the columns looked at, so those are the output whatever the weights, also where the parts of a context are merged
+    n_tiles = 400
+    c = Case(26, [64 * n_tiles], 1, 2, kv, mask="chain", new=[0], L=64 * n_tiles)
+    const = torch.from_numpy(np.random.default_rng(26).choice([1.0, -0.5, 2.0, 3.5, -1.25], D)).float()
+    odd = (torch.arange(c.rows) // 64) % 2 == 1
+    rows = const.repeat(c.rows, 1)
+    used = [5, 130, 300, 301]
+    rows[:, used] = 0.0
+    rows[odd, 5], rows[odd, 130], rows[odd, 300], rows[odd, 301] = 256.0, 1.0, -256.0, 8.0
+    q = torch.zeros(D)
+    q[5], q[130], q[300], q[301] = 2.0**17, 1.5, 2.0**17, 1.0
+    c.q = q.repeat(1, 2, 1).bfloat16().cuda()
+    if kv == "bf16":
+        c.cache.copy_(rows.bfloat16())
+    else:
+        c.cache.copy_(rows.to(torch.float8_e4m3fn).view(torch.uint8))
+        c.scale.fill_(1.0)
+    out, _ = dsa.dsa_tree_attn(c.q, c.cache.unflatten(0, (1, c.L)), torch.tensor([c.L], dtype=torch.int32, device="cuda"),
+                               sm_scale=float(np.log(2.0)), q_per_seq=1, n_new=torch.zeros(1, dtype=torch.int32, device="cuda") + 1,
+                               kv_scale=None if kv == "bf16" else c.scale.unflatten(0, (1, c.L)))
+    keep = np.setdiff1d(np.arange(DV), used)
+    want = const[keep].double().numpy()
+    # each weight is rounded to bf16 for the product and not in the sum (2^-8), the output once more (2^-8)
+    assert np.all(np.abs(out.double().cpu().numpy()[0][:, keep] - want) <= np.abs(want) * 2.0**-6.9)
+
+
 @pytest.mark.parametrize("kv", ["fp8", "t128"])
 def test_queries_of_a_wide_range(dsa, kv):
     # E4M3 rows: a query row enters as E4M3 plus E5M2, exact from 2^-13 of its largest value on, to 2^-20 of it below

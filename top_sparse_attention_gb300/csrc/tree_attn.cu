@@ -117,7 +117,7 @@ struct TreePlan {
   int grid;                // pairs of CTAs
   int* head;               // [0]: tiles of a chunk, or minus those of a span; [1 + s]: first item or tile of sequence s
   float4* part_o;          // [cap][128 groups of four values][128 rows]
-  float2* part_ml;         // [cap][128 rows]
+  float2* part_ml;         // [cap][half of the values][128 rows]
 };
 
 __device__ __forceinline__ void seq_facts(const TreeAttnParams& p, int seq, int& ctx, int& fresh, int& len) {
@@ -1144,9 +1144,10 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
       l = a->sum[0][row] + a->sum[1][row];
       const bool live = row < nrows && (row_lo + row) / p.H < it.fresh;
       const float inv = live && l != 0.f ? 1.f / l : 0.f;
-      if (rank == 0 && h == 0) {
-        if (it.slot >= 0) pl.part_ml[(int64_t)it.slot * kRows + row] = make_float2(m, l);
-        else if (p.lse && row < nrows) p.lse[at + row] = !live || l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      if (h == 0) {
+        // (each CTA's own: the two sum the logits' columns in different orders, so that their maxima may differ)
+        if (it.slot >= 0) pl.part_ml[((int64_t)it.slot * 2 + rank) * kRows + row] = make_float2(m, l);
+        else if (rank == 0 && p.lse && row < nrows) p.lse[at + row] = !live || l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
       ok = wait(a, &a->o_done, items & 1, err) && ok;
       tc_fence_after();
@@ -1220,7 +1221,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeAttnParams 
     for (int k = 0; k < B; ++k) {
       const int64_t s = j0 + k == 0 ? slot0 : slot1 + (j0 + k - 1) * stride;
       const bool in = j0 + k < chunks;
-      ml[k] = in ? pl.part_ml[s * kRows + r] : make_float2(-INFINITY, 0.f);
+      ml[k] = in ? pl.part_ml[(s * 2 + (c4 >> 6)) * kRows + r] : make_float2(-INFINITY, 0.f);
       v[k] = in ? pl.part_o[(s * (kDv / 4) + c4) * kRows + r] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float Mb = M;
@@ -1286,7 +1287,7 @@ cudaError_t launch_fmt(const TreeAttnParams& p, TreePlan pl, void* ws, cudaStrea
     pl.head = reinterpret_cast<int*>(w);
     w += head_bytes(p);
     pl.part_ml = reinterpret_cast<float2*>(w);
-    w += (size_t)pl.cap * kRows * sizeof(float2);
+    w += (size_t)pl.cap * 2 * kRows * sizeof(float2);
     pl.part_o = reinterpret_cast<float4*>(w);
   }
   auto kern = tree_attn_kernel<FMT>;
@@ -1303,7 +1304,7 @@ cudaError_t launch_fmt(const TreeAttnParams& p, TreePlan pl, void* ws, cudaStrea
 size_t tree_attn_ws_bytes(const TreeAttnParams& p) {
   const TreePlan pl = plan_of(p);
   if (!pl.cap || p.L == 0) return 0;
-  return head_bytes(p) + (size_t)pl.cap * kRows * (sizeof(float2) + kDv * sizeof(float));
+  return head_bytes(p) + (size_t)pl.cap * kRows * (2 * sizeof(float2) + kDv * sizeof(float));
 }
 
 cudaError_t launch_tree_attn(const TreeAttnParams& p, void* ws, cudaStream_t stream) {
