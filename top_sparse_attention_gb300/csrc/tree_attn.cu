@@ -17,7 +17,7 @@
 // Why two CTAs: o for 128 rows x 512 values fills a tensor memory (512 columns), which leaves no room for S; with half
 // of the values it takes 256 columns, q 160, S 64, the weights 32.  Why both take the whole first product: an MMA of
 // N = 64 with A in tensor memory takes 32 cycles, one of N = 32 33, so that sharing the positions out saves nothing.
-// Measured (8 x 64 nodes at 32K, E4M3 rows; 8 x 8 nodes at 32K, bf16; us): this form 595 and 92; the positions of the
+// Measured (8 x 64 nodes at 32K, E4M3 rows; 8 x 8 nodes at 32K, bf16; us): this form 590 and 93; the positions of the
 // first product shared out and weights exchanged through distributed shared memory 1002 and 105; columns shared out
 // and partial S exchanged 1090 and 120; one CTA with 64 rows and q in shared memory 1805 and 149.
 //
@@ -146,14 +146,22 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 // through the rest of their work (every address stays in range), so that their common barriers still match; the
 // other roles leave.  A thread whose wait failed arrives on no mbarrier, arms none and sends nothing any more: an
 // arrival is only legal in a phase that the arriving thread has seen begin.
+template <int SLEEP>
 __device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err);
 __device__ __forceinline__ bool wait(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
-  return mbar_test(bar, parity) || wait_slow(a, bar, parity, err);
+  return mbar_test(bar, parity) || wait_slow<0>(a, bar, parity, err);
 }
+// The same for the roles that run ahead of the others (producer, scale loader, converters): they look again after 50
+// ns, since warps that poll take issue slots from the others (8 x 64 nodes at 32K, E4M3 rows: 603 -> 590 us).
+__device__ __forceinline__ bool wait_ahead(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
+  return mbar_test(bar, parity) || wait_slow<50>(a, bar, parity, err);
+}
+template <int SLEEP>
 __device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
   const unsigned long long t0 = globaltimer_ns();
   for (uint32_t i = 0;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
+    if (SLEEP) __nanosleep(SLEEP);
     if ((i & 15u) != 15u) continue;
     if (*reinterpret_cast<volatile int*>(&a->abort)) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
@@ -580,7 +588,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
             if (bad) record_error(err, DSA_DEVERR_INDEX_RANGE);
           }
           if constexpr (C::FP8) {
-            ok = wait(a, &a->c_empty[cs], cph ^ 1, err);
+            ok = wait_ahead(a, &a->c_empty[cs], cph ^ 1, err);
             if (!ok) break;
             a->tile_bad[tiles & 7] = bad;
             mbar_arrive_expect_tx(&a->c_full[cs], kSlotC);
@@ -590,13 +598,13 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
             if (++cs == C::CS) cs = 0, cph ^= 1;
           } else {
             for (int b = 0; b < 5; ++b) {
-              ok = wait(a, &a->k_empty[ks], kph ^ 1, err);
+              ok = wait_ahead(a, &a->k_empty[ks], kph ^ 1, err);
               if (!ok) break;
               mbar_arrive_expect_tx(&a->k_full[ks], kBox);
               tma_load_3d(k_s + ks * kBox, &tm, &a->k_full[ks], b < 4 ? 256 * (rank ^ 1) + 64 * b : 512, row, z);
               if (++ks == C::KS) ks = 0, kph ^= 1;
             }
-            ok = ok && wait(a, &a->v_empty[vs], vph ^ 1, err);
+            ok = ok && wait_ahead(a, &a->v_empty[vs], vph ^ 1, err);
             if (!ok) break;
             a->tile_bad[tiles & 7] = bad;
             mbar_arrive_expect_tx(&a->v_full[vs], kSlotV);
@@ -781,7 +789,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         float v[2 * C::NSC + 1];
 #pragma unroll
         for (int k = 0; k < 2 * C::NSC; ++k) v[k] = !bad && lane + 32 * k < n ? __ldg(src + lane + 32 * k) : 1.f;
-        ok = __all_sync(0xffffffffu, wait(a, &a->sc_empty[d], ((tiles >> 1) & 1) ^ 1, err));
+        ok = __all_sync(0xffffffffu, wait_ahead(a, &a->sc_empty[d], ((tiles >> 1) & 1) ^ 1, err));
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < 2 * C::NSC; ++k) {
@@ -800,7 +808,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
     bool ok = true;
     for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
       for (int t = it.t0; ok && t < it.t1; ++t) {
-        ok = __all_sync(0xffffffffu, wait(a, &a->c_full[cs], cph, err));
+        ok = __all_sync(0xffffffffu, wait_ahead(a, &a->c_full[cs], cph, err));
         if (!ok) break;
         const uint8_t* src = c_s + cs * kSlotC;
         uint4 raw[8];
@@ -812,7 +820,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&a->c_empty[cs]);
         if (++cs == C::CS) cs = 0, cph ^= 1;
-        ok = __all_sync(0xffffffffu, wait(a, &a->v_empty[vs], vph ^ 1, err));
+        ok = __all_sync(0xffffffffu, wait_ahead(a, &a->v_empty[vs], vph ^ 1, err));
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
