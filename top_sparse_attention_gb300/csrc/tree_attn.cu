@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
           top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu)));
         };
         constexpr int kBatch = 3;
-#pragma unroll
+#pragma unroll(C::FP8 ? 3 : 1)  // (rolled, bf16: 0.5 us less for the first item, whose code is not in the caches)
         for (int j0 = 0; j0 < 9; j0 += kBatch) {
           uint4 u[kBatch][4];
 #pragma unroll
@@ -1027,14 +1027,9 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         if (edge || bad) {
           const uint32_t see = bad ? 0u : (uint32_t)(seen_bits(p, it, node, t) >> (32 * h));
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            if (!((see >> k) & 1)) {
-              // a hidden position that may hold infinities or NaN (its logit is not finite, or it lies past
-              // the end): its values are cleared in the tile, so that 0 * value is 0
-              if (!C::FP8 && (!(fabsf(x[k]) < INFINITY) || t * kKeys + 32 * h + k >= it.len)) clear |= 1u << k;
-              x[k] = -INFINITY;
-            }
-          }
+          for (int k = 0; k < 32; ++k)
+            if (!((see >> k) & 1)) x[k] = -INFINITY;
+          clear = ~see;
         }
         // ---- the rows' maxima over the tile
         float mx[4] = {x[0], x[1], x[2], x[3]};
@@ -1043,8 +1038,9 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         a->mx[tile & 1][h][row] = mine;
         if (!C::FP8 && edge) {
-          // zero the value columns of the positions to clear (their logits have been taken): a position past the
-          // end always, another one only if it holds something that is not finite
+          // zero the value columns of positions that some row does not see (the logits have been taken), so that 0 * value
+          // is 0: a position past the end always, another one only if it holds something that is not finite (and who
+          // sees that has no finite logit)
           clear = __reduce_or_sync(0xffffffffu, clear);
           if (lane == 0) a->clear[tile & 1][w] = clear;
           softmax_bar();
@@ -1195,14 +1191,19 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
 }
 
 // Merges the chunks of each split row: out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j.  A CTA takes eight
-// rows and 128 value columns, a thread one row and four values, eight chunks' loads in flight.
-__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeAttnParams p, const TreePlan pl) {
-  pdl_wait();
-  const int rows = p.q_per_seq * p.H;
-  const int seq = blockIdx.y, row = blockIdx.x * 8 + (threadIdx.x & 7), c4 = blockIdx.z * 32 + (threadIdx.x >> 3);
-  if (row >= rows) return;
+// rows and 128 value columns, a thread one row, four values and every G-th chunk, B chunks' loads in flight.  G = 4
+// for launches of few row tiles, which have many chunks each (one token over 2K, 33 chunks: 17.3 us the call with G = 1,
+// 16.1 with 4; 8 row tiles of 9 chunks: 93 with 1, 97 with 4; 64 of two: 590, 631).
+template <int G>
+__global__ void __launch_bounds__(256 * G) tree_combine_kernel(const TreeAttnParams p, const TreePlan pl) {
+  constexpr int B = G > 1 ? 4 : 8;
+  __shared__ float2 part_ml[G][256];
+  __shared__ float4 part_o[G][256];
+  const int rows = p.q_per_seq * p.H, at = threadIdx.x & 255, g = threadIdx.x >> 8;
+  const int seq = blockIdx.y, row = blockIdx.x * 8 + (at & 7), c4 = blockIdx.z * 32 + (at >> 3);
   int ctx, fresh, len;
-  seq_facts(p, seq, ctx, fresh, len);
+  seq_facts(p, seq, ctx, fresh, len);  // (the lengths were there before the attention kernel began)
+  pdl_wait();
   const int live = live_row_tiles(p, fresh);
   const int rt = row / kRows, r = row - rt * kRows;
   const int plan = pl.head[0], nt = (len + kKeys - 1) / kKeys, base = pl.head[1 + seq];
@@ -1219,40 +1220,48 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeAttnParams 
     if (chunks == 1) return;
   }
   if (row / p.H >= fresh) chunks = 0;  // a padding node: zeros
+  if (row >= rows) chunks = 0;
   float M = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int B = 8;
-  for (int j0 = 0; j0 < chunks; j0 += B) {
-    float2 ml[B];
-    float4 v[B];
-#pragma unroll
-    for (int k = 0; k < B; ++k) {
-      const int64_t s = j0 + k == 0 ? slot0 : slot1 + (j0 + k - 1) * stride;
-      const bool in = j0 + k < chunks;
-      ml[k] = in ? pl.part_ml[(s * 2 + (c4 >> 6)) * kRows + r] : make_float2(-INFINITY, 0.f);
-      v[k] = in ? pl.part_o[(s * (kDv / 4) + c4) * kRows + r] : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+  auto add = [&](const float2* ml, const float4* v, int n) {  // n partial results to (M, l, o)
     float Mb = M;
-#pragma unroll
-    for (int k = 0; k < B; ++k) Mb = fmaxf(Mb, ml[k].x);
+    for (int k = 0; k < n; ++k) Mb = fmaxf(Mb, ml[k].x);
     const float mu = Mb == -INFINITY ? 0.f : Mb;
     const float f = exp2f(M - mu);
     l *= f;
     o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-#pragma unroll
-    for (int k = 0; k < B; ++k) {
-      if (j0 + k >= chunks) continue;
-      const float g = exp2f(ml[k].x - mu);
-      l += g * ml[k].y;
-      o.x += g * v[k].x, o.y += g * v[k].y, o.z += g * v[k].z, o.w += g * v[k].w;
+    for (int k = 0; k < n; ++k) {
+      const float w = exp2f(ml[k].x - mu);
+      l += w * ml[k].y;
+      o.x += w * v[k].x, o.y += w * v[k].y, o.z += w * v[k].z, o.w += w * v[k].w;
     }
     M = Mb;
+  };
+  for (int j0 = g; j0 < chunks; j0 += G * B) {
+    float2 ml[B];
+    float4 v[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const int j = j0 + k * G;
+      const int64_t s = j == 0 ? slot0 : slot1 + (j - 1) * stride;
+      const bool in = j < chunks;
+      ml[k] = in ? pl.part_ml[(s * 2 + (c4 >> 6)) * kRows + r] : make_float2(-INFINITY, 0.f);
+      v[k] = in ? pl.part_o[(s * (kDv / 4) + c4) * kRows + r] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    add(ml, v, B);
   }
-  const int64_t at = (int64_t)seq * rows + row;
+  if (G > 1) {
+    if (g > 0) part_ml[g][at] = make_float2(M, l), part_o[g][at] = o;
+    __syncthreads();
+  }
+  if (g > 0 || row >= rows) return;
+#pragma unroll
+  for (int k = 1; k < G; ++k) add(&part_ml[k][at], &part_o[k][at], 1);
+  const int64_t to = (int64_t)seq * rows + row;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2*>(p.out + at * kDv + 4 * c4) =
+  *reinterpret_cast<uint2*>(p.out + to * kDv + 4 * c4) =
       make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  if (p.lse && c4 == 0) p.lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+  if (p.lse && c4 == 0) p.lse[to] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
 }
 
 __global__ void tree_nothing_kernel(const TreeAttnParams p, int64_t rows) {
@@ -1304,7 +1313,9 @@ cudaError_t launch_fmt(const TreeAttnParams& p, TreePlan pl, void* ws, cudaStrea
   if (e != cudaSuccess) return e;
   e = launch_kernel(kern, dim3(2 * pl.grid), dim3(C::THREADS), C::SMEM, stream, false, tm, p, pl);
   if (e != cudaSuccess || !pl.cap) return e;
-  return launch_kernel(tree_combine_kernel, dim3((p.q_per_seq * p.H + 7) / 8, p.n_seq, 4), dim3(256), 0, stream, true, p, pl);
+  const bool few = 16 * pl.units <= kPairs;
+  return launch_kernel(few ? tree_combine_kernel<4> : tree_combine_kernel<1>, dim3((p.q_per_seq * p.H + 7) / 8, p.n_seq, 4),
+                       dim3(few ? 1024 : 256), 0, stream, true, p, pl);
 }
 
 }  // namespace
