@@ -1191,16 +1191,16 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
 }
 
 // Merges the chunks of each split row: out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j.  A CTA takes eight
-// rows and 128 value columns, a thread one row, four values and every G-th chunk, B chunks' loads in flight.  G = 4
-// for launches of few row tiles, which have many chunks each (one token over 2K, 33 chunks: 17.3 us the call with G = 1,
-// 16.1 with 4; 8 row tiles of 9 chunks: 93 with 1, 97 with 4; 64 of two: 590, 631).
+// rows, a thread one row, four values and every G-th chunk, B chunks' loads in flight.  G = 16 (and 32 value columns
+// per CTA) for launches of few row tiles, which have many chunks each, G = 1 (and 128) for others: one token over 2K, 33
+// chunks: 17.3 us the call with G = 1, 14.7 with 16; 8 row tiles of 9 chunks: 91 with 1, 95 to 97 with 2 and 4.
 template <int G>
-__global__ void __launch_bounds__(256 * G) tree_combine_kernel(const TreeAttnParams p, const TreePlan pl) {
-  constexpr int B = G > 1 ? 4 : 8;
-  __shared__ float2 part_ml[G][256];
-  __shared__ float4 part_o[G][256];
-  const int rows = p.q_per_seq * p.H, at = threadIdx.x & 255, g = threadIdx.x >> 8;
-  const int seq = blockIdx.y, row = blockIdx.x * 8 + (at & 7), c4 = blockIdx.z * 32 + (at >> 3);
+__global__ void __launch_bounds__(G > 1 ? 64 * G : 256) tree_combine_kernel(const TreeAttnParams p, const TreePlan pl) {
+  constexpr int B = G > 1 ? 4 : 8, T = G > 1 ? 64 : 256;  // threads that share out rows and columns
+  __shared__ float2 part_ml[G][T];
+  __shared__ float4 part_o[G][T];
+  const int rows = p.q_per_seq * p.H, at = threadIdx.x % T, g = threadIdx.x / T;
+  const int seq = blockIdx.y, row = blockIdx.x * 8 + (at & 7), c4 = blockIdx.z * (T / 8) + (at >> 3);
   int ctx, fresh, len;
   seq_facts(p, seq, ctx, fresh, len);  // (the lengths were there before the attention kernel began)
   pdl_wait();
@@ -1313,9 +1313,10 @@ cudaError_t launch_fmt(const TreeAttnParams& p, TreePlan pl, void* ws, cudaStrea
   if (e != cudaSuccess) return e;
   e = launch_kernel(kern, dim3(2 * pl.grid), dim3(C::THREADS), C::SMEM, stream, false, tm, p, pl);
   if (e != cudaSuccess || !pl.cap) return e;
-  const bool few = 16 * pl.units <= kPairs;
-  return launch_kernel(few ? tree_combine_kernel<4> : tree_combine_kernel<1>, dim3((p.q_per_seq * p.H + 7) / 8, p.n_seq, 4),
-                       dim3(few ? 1024 : 256), 0, stream, true, p, pl);
+  const unsigned rows8 = (p.q_per_seq * p.H + 7) / 8;
+  if (16 * pl.units <= kPairs)
+    return launch_kernel(tree_combine_kernel<16>, dim3(rows8, p.n_seq, 16), dim3(1024), 0, stream, true, p, pl);
+  return launch_kernel(tree_combine_kernel<1>, dim3(rows8, p.n_seq, 4), dim3(256), 0, stream, true, p, pl);
 }
 
 }  // namespace
