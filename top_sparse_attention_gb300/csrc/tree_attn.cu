@@ -17,7 +17,7 @@
 // Why two CTAs: o for 128 rows x 512 values fills a tensor memory (512 columns), which leaves no room for S; with half
 // of the values it takes 256 columns, q 160, S 64, the weights 32.  Why both take the whole first product: an MMA of
 // N = 64 with A in tensor memory takes 32 cycles, one of N = 32 33, so that sharing the positions out saves nothing.
-// Measured (8 x 64 nodes at 32K, E4M3 rows; 8 x 8 nodes at 32K, bf16; us): this form 590 and 93; the positions of the
+// Measured (8 x 64 nodes at 32K, E4M3 rows; 8 x 8 nodes at 32K, bf16; us): this form 580 and 92; the positions of the
 // first product shared out and weights exchanged through distributed shared memory 1002 and 105; columns shared out
 // and partial S exchanged 1090 and 120; one CTA with 64 rows and q in shared memory 1805 and 149.
 //
