@@ -369,27 +369,7 @@ __global__ void __launch_bounds__(32 * kWarps, kHalfCtasPerSm) rope_append_half_
         if (o < lanes) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
       return a;
     };
-    if constexpr (FMT == kFmtBf16) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int c = hl + 16 * j;
-        if (keep && c < nch) *reinterpret_cast<uint4*>(out + 16 * c) = pack8(v[j]);
-      }
-    } else if constexpr (FMT == kFmtRow) {
-      float a = 0.f;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) a = fmaxf(a, amax8(v[j]));
-      const float amax = across(a, 16);
-      const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-      const Quotient div(s);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int c = hl + 16 * j;
-        if (keep && c < nch)
-          *reinterpret_cast<uint2*>(out + 8 * c) = encode8(v[j], s, div.r * kBelow, div.r * kAbove, div.fast);
-      }
-      if (keep && hl == 0) reinterpret_cast<float*>(p.scale)[at_row] = s;
-    } else if constexpr (FMT == kFmtTile) {
+    if constexpr (FMT == kFmtTile) {
       // lane j of each half takes tile j's scale and reciprocal (a division each, once instead of NT times)
       float own = 0.f;
 #pragma unroll
