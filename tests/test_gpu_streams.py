@@ -1,0 +1,92 @@
+"""Calls on a stream other than the current one: their scratch and outputs belong to that stream's pool, and calls on
+two streams at once, with work of the current stream beside them, give what the same calls give one after another."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dsa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from top_sparse_attention_gb300 import build
+
+    build.build()
+    import top_sparse_attention_gb300 as m
+
+    torch.cuda.set_device(0)
+    yield m
+    torch.cuda.synchronize()
+    assert m.dsa_get_device_error() == 0
+
+
+def _i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+
+
+def _pool_of(t):
+    """The stream whose pool holds t's block."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not in any pool")
+
+
+def _tree_inputs(seed, n_seq=2, ctx=9000, N=3, H=16):
+    g = torch.Generator().manual_seed(seed)
+    kv = torch.randn(n_seq, ctx + N, 576, generator=g).bfloat16().cuda()
+    q = torch.randn(n_seq * N, H, 576, generator=g).bfloat16().cuda()
+    return q, kv, _i32([ctx, ctx - 100 * seed])
+
+
+def test_outputs_belong_to_the_stream_of_the_call(dsa):
+    s = torch.cuda.Stream()
+    q, kv, ctx = _tree_inputs(1)
+    f = torch.ones(32, device="cuda")
+    x = torch.ones(5, 64, dtype=torch.bfloat16, device="cuda")
+    one = _i32([1, 1])
+    torch.cuda.synchronize()
+    outs = list(dsa.dsa_tree_attn(q, kv, ctx, sm_scale=1 / 24, q_per_seq=3, stream=s))
+    outs.append(dsa.dsa_rope(x, _i32(np.arange(5)), f, stream=s))
+    outs += dsa.dsa_block_plan(one, one, _i32(np.arange(8)), _i32(np.zeros((2, 4))), block_size=64, num_blocks=8, rows=2, stream=s)
+    s.synchronize()
+    assert {_pool_of(t) for t in outs} == {s.cuda_stream}
+    assert _pool_of(dsa.dsa_rope(x, _i32(np.arange(5)), f)) == torch.cuda.current_stream().cuda_stream
+
+
+def test_tree_attention_on_two_side_streams_without_a_workspace(dsa):
+    cases = [_tree_inputs(k) for k in (1, 2)]
+    kw = dict(sm_scale=1 / 24, q_per_seq=3)
+    want = [dsa.dsa_tree_attn(q, kv, ctx, **kw) for q, kv, ctx in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for (q, kv, ctx), s in zip(cases, streams):
+            got.append(dsa.dsa_tree_attn(q, kv, ctx, stream=s, **kw))
+            # the current stream's next allocation of the workspace's size, written at once
+            torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for k, (out, lse) in enumerate(got):
+        assert torch.equal(out, want[k % 2][0]) and torch.equal(lse, want[k % 2][1])
+
+
+def test_outputs_of_a_side_stream_outlive_their_last_reader(dsa):
+    # `got` is dropped while the current stream still reads it; the side stream's next output may not take its block
+    s = torch.cuda.Stream()
+    f, pos = torch.ones(32, device="cuda"), _i32(np.arange(1 << 14))
+    x = torch.randn(1 << 14, 16, 64, device="cuda").bfloat16()
+    want = dsa.dsa_rope(x, pos, f)
+    torch.cuda.synchronize()
+    sums = []
+    for _ in range(10):
+        got = dsa.dsa_rope(x, pos, f, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda._sleep(2_000_000)  # (about a millisecond of waiting in front of the read)
+        sums.append(got.clone())
+        del got
+        dsa.dsa_rope(x, pos, f, inverse=True, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want) for t in sums)

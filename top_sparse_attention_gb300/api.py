@@ -318,7 +318,9 @@ def dsa_quantize_fp8_tiles(x, *, tile=128, codes=None, scales=None, dst_rows=Non
 
 
 # The serving-step operators below check their tensors (device, dtype, layout) and run on the
-# tensors' own device and its current stream, whichever device is current.
+# tensors' own device and its current stream, whichever device is current, or on the `stream` given: then
+# the inputs have to be ready on that stream and to live until its work is done, and the outputs are ready
+# when it is.
 
 def _check(what, device, name, t, dtype, dims=None, dense=True):
     if t is None:
@@ -366,6 +368,33 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+# What a call allocates belongs to the stream that it runs on.  torch's allocator hands a freed block to later work of
+# the stream that it was allocated on, without waiting for any other stream: scratch from the current stream's pool
+# would be given away while the kernels on the caller's `stream` still use it, and an output's block may still be read
+# by pending work of the current stream.
+
+def _side(stream, device):
+    """`stream`, where it is given and is not the device's current one; None otherwise."""
+    return None if stream is None or stream.cuda_stream == _raw_stream(device.index) else stream
+
+
+def _scratch(side, shape, dtype, device):
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(side):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _hand_back(t, device):
+    """The caller's current stream reads `t` too: its block waits for that stream before it is used again."""
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _output(side, shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device) if side is None else _hand_back(_scratch(side, shape, dtype, device), device)
+
+
 class BlockPlan(NamedTuple):
     """What dsa_block_plan gives (see dsa.h): per row `dst_rows` int64, `pos` and `seq` int32 (-1: no
     token); `row_start` int32 [n_seq + 1]; `n_placed` int32 [n_seq]; `taken` int32 [1]."""
@@ -401,10 +430,9 @@ def dsa_block_plan(n_ctx, n_new, free_blocks, block_table, *, block_size, num_bl
         rows = n_seq * q_per_seq
     if out is None:
         # (six allocations take 9 us of the host, six views of one 12.5: most of it when they are freed)
-        new = torch.empty
-        out = BlockPlan(new(rows, dtype=torch.int64, device=dev), new(rows, dtype=i32, device=dev),
-                        new(rows, dtype=i32, device=dev), new(n_seq + 1, dtype=i32, device=dev),
-                        new(n_seq, dtype=i32, device=dev), new(1, dtype=i32, device=dev))
+        side = _side(stream, dev)
+        out = BlockPlan(_output(side, rows, torch.int64, dev), _output(side, rows, i32, dev), _output(side, rows, i32, dev),
+                        _output(side, n_seq + 1, i32, dev), _output(side, n_seq, i32, dev), _output(side, 1, i32, dev))
     else:
         for name, t, n, kind in (("dst_rows", out.dst_rows, rows, torch.int64), ("pos", out.pos, rows, i32),
                                  ("seq", out.seq, rows, i32), ("row_start", out.row_start, n_seq + 1, i32),
@@ -460,7 +488,7 @@ def dsa_rope(x, pos, inv_freq, *, rot_off=0, rot_dim=None, sections=None, pair_a
         raise ValueError(f"{what}: x must be [rows, heads, width] or [rows, width] with dense columns")
     rot_dim, n_axes, pair_axis, code = _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out = _output(_side(stream, dev), shape, torch.bfloat16, dev)
         os = out.stride()
     else:
         _check(what, dev, "out", out, torch.bfloat16, len(shape), dense=False)
@@ -571,14 +599,15 @@ def dsa_tree_attn(q, kv, n_ctx, *, sm_scale, q_per_seq, n_new=None, tree_mask=No
             raise ValueError(f"{what}: kv must be [{n_seq}, L, {D}], got {tuple(shape)}")
         L = shape[1]
         a.kv_row_stride, a.kv_seq_stride = strides[1] * elem, strides[0] * elem
+    side = _side(stream, dev)
     if out is None:
-        out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=dev)
+        out = _output(side, (T, H, 512), torch.bfloat16, dev)
     else:
         _check(what, dev, "out", out, torch.bfloat16, 3)
         if tuple(out.shape) != (T, H, 512):
             raise ValueError(f"{what}: out must be [{T}, {H}, 512]")
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        lse = _output(side, (T, H), torch.float32, dev)
     else:
         _check(what, dev, "lse", lse, torch.float32, 2)
         if tuple(lse.shape) != (T, H):
@@ -589,7 +618,7 @@ def dsa_tree_attn(q, kv, n_ctx, *, sm_scale, q_per_seq, n_new=None, tree_mask=No
     need = ctypes.c_size_t(0)
     N.check(N.lib.dsa_tree_attn_workspace_size(ctypes.byref(a), ctypes.byref(need)), what)
     if ws is None:
-        ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+        ws = _scratch(side, need.value, torch.uint8, dev) if need.value else None
     else:
         _check(what, dev, "ws", ws, torch.uint8, 1)
     _run(what, N.lib.dsa_tree_attn, dev, stream, ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel())
