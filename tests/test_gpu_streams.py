@@ -90,3 +90,31 @@ def test_outputs_of_a_side_stream_outlive_their_last_reader(dsa):
         dsa.dsa_rope(x, pos, f, inverse=True, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(t, want) for t in sums)
+
+
+def test_chain_entries_on_side_streams_without_workspaces(dsa):
+    # the separate entries and the fused call, each with what it allocates itself, two streams in turn, the current
+    # stream writing blocks of the same sizes beside them
+    import synth
+
+    wl = synth.small_workload("decode_b8_l32k_bf16", T=4, L=9000, K=512, name="streams")
+    dev = {k: (v.cuda() if v is not None else None) for k, v in synth.make_inputs(wl).items()}
+    kw = dict(K=wl.K, sm_scale=wl.sm_scale, q_per_seq=wl.q_per_seq, q_pos0=wl.q_pos0)
+    want, want_lse, want_idx = (t.clone() for t in dsa.call_from_tensors(dev, **kw)())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for k in range(12):
+        s = streams[k % 2]
+        scores = dsa.dsa_index_score(dev["q_idx"], dev["w"], dev["k_idx"], n_valid=dev["n_valid"], stream=s)
+        idx = dsa.dsa_topk(scores, wl.K, L=wl.L, n_valid=dev["n_valid"], stream=s)
+        got.append(dsa.dsa_sparse_attn(dev["q"], dev["kv"], idx, sm_scale=wl.sm_scale, stream=s) + (idx,))
+        got.append(dsa.call_from_tensors(dev, **kw)(s))  # the call object is dropped at once
+        torch.full((1 << 22,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    fused = got[1::2]
+    for out, lse, idx in fused:
+        assert torch.equal(out, want) and torch.equal(lse, want_lse) and torch.equal(idx, want_idx)
+    for out, lse, idx in got[0::2]:
+        assert torch.equal(idx.sort(1).values, want_idx.sort(1).values)
+        assert torch.equal(out, got[0][0]) and (out.float() - want.float()).abs().max() <= 2e-2

@@ -5,6 +5,7 @@ workspaces that the caller does not pass are allocated with torch on the inputs'
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import NamedTuple, Optional, Tuple
 
@@ -17,6 +18,71 @@ __all__ = ["dsa_index_score", "dsa_topk", "dsa_topk_noalloc", "dsa_topk_pairs", 
            "dsa_workspace_size", "dsa_launch_count", "dsa_get_device_error", "ld_scores_for",
            "dsa_quantize_mxfp8", "dsa_quantize_fp8_rows", "dsa_quantize_fp8_tiles",
            "dsa_block_plan", "BlockPlan", "dsa_rope", "dsa_rope_append", "dsa_tree_attn"]
+
+
+# The current stream's handle and the current device without building torch objects (a serving step makes
+# several short calls, and the host's share of each is most of its time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+# What a call allocates belongs to the stream that it runs on.  torch's allocator hands a freed block to later work of
+# the stream that it was allocated on, without waiting for any other stream: scratch from the current stream's pool
+# would be given away while the kernels on the caller's `stream` still use it, and an output's block may still be read
+# by pending work of the current stream.
+
+def _side(stream, device):
+    """`stream`, where it is given and is not the device's current one; None otherwise."""
+    return None if stream is None or stream.cuda_stream == _raw_stream(device.index) else stream
+
+
+def _scratch(side, shape, dtype, device, zero=False):
+    with contextlib.nullcontext() if side is None else torch.cuda.stream(side):
+        return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
+
+
+def _hand_back(t, device):
+    """The caller's current stream reads `t` too: its block waits for that stream before it is used again."""
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _output(side, shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device) if side is None else _hand_back(_scratch(side, shape, dtype, device), device)
+
+
+def _zeros(stream, n, device):
+    """A zero-filled workspace of n bytes: filled on the stream that the call runs on."""
+    return _scratch(_side(stream, device), n, torch.uint8, device, zero=True)
+
+
+class Owned:
+    """Buffers that an object keeps for its calls (outputs, a workspace that was zero-filled), made on the current
+    stream.  `follow` puts the first call on any other stream behind them, and holds their blocks back until that
+    stream's work is done, should the object be dropped before it."""
+
+    def __init__(self, *tensors):
+        self._tensors = [t for t in tensors if t is not None]
+        self._device = self._tensors[0].device
+        current = torch.cuda.current_stream(self._device)
+        self._known = {current.cuda_stream}
+        self._captured = torch.cuda.is_current_stream_capturing()
+        self._made = torch.cuda.Event()
+        self._made.record(current)
+
+    def follow(self, stream):
+        if (_raw_stream(self._device.index) if stream is None else stream.cuda_stream) in self._known:
+            return
+        if stream is None:
+            stream = torch.cuda.current_stream(self._device)
+        with torch.cuda.stream(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+        if capturing or self._captured:
+            return  # a graph cannot wait for what is outside of it: the capture's own forks and joins order it
+        stream.wait_event(self._made)
+        for t in self._tensors:
+            t.record_stream(stream)
+        self._known.add(stream.cuda_stream)
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -63,7 +129,7 @@ def dsa_index_score(q_idx, w, k_idx, *, q_idx_sf=None, k_idx_sf=None, q_per_seq=
     T, H_idx, d = q_idx.shape
     L = k_idx.shape[1]
     if scores is None:
-        scores = torch.empty(T, ld_scores_for(L), dtype=torch.float32, device=q_idx.device)
+        scores = _output(_side(stream, q_idx.device), (T, ld_scores_for(L)), torch.float32, q_idx.device)
     st = N.lib.dsa_index_score(_p(q_idx), _p(q_idx_sf), _p(w), _p(k_idx), _p(k_idx_sf),
                                _seq_stride(k_idx), _seq_stride(k_idx_sf), T, q_per_seq, q_pos0,
                                _p(n_valid), L, H_idx, d, _idx_dtype(q_idx), _p(scores),
@@ -77,10 +143,10 @@ def dsa_topk(scores, K, *, L, q_per_seq=1, q_pos0=-1, n_valid=None, idx=None, ws
     uint8 tensor of at least dsa_topk_workspace_size bytes that later calls may reuse."""
     T = scores.shape[0]
     if idx is None:
-        idx = torch.empty(T, K, dtype=torch.int32, device=scores.device)
+        idx = _output(_side(stream, scores.device), (T, K), torch.int32, scores.device)
     ws_bytes = N.lib.dsa_topk_workspace_size(T, L, K)
     if ws is None:
-        ws = torch.zeros(max(ws_bytes, 16), dtype=torch.uint8, device=scores.device) if ws_bytes else None
+        ws = _zeros(stream, max(ws_bytes, 16), scores.device) if ws_bytes else None
     else:
         ws_bytes = ws.numel()
     st = N.lib.dsa_topk(_p(scores), scores.stride(0), T, q_per_seq, q_pos0, _p(n_valid), L, K, _p(idx),
@@ -94,7 +160,7 @@ def dsa_topk_noalloc(scores, K, *, L, q_per_seq=1, q_pos0=-1, n_valid=None, idx=
     (at most 16 queries per call; calls that overlap on the GPU race, see dsa.h)."""
     T = scores.shape[0]
     if idx is None:
-        idx = torch.empty(T, K, dtype=torch.int32, device=scores.device)
+        idx = _output(_side(stream, scores.device), (T, K), torch.int32, scores.device)
     st = N.lib.dsa_topk_noalloc(_p(scores), scores.stride(0), T, q_per_seq, q_pos0, _p(n_valid), L, K,
                                 _p(idx), _stream(stream))
     N.check(st, "dsa_topk_noalloc")
@@ -111,12 +177,12 @@ def dsa_sparse_attn(q, kv, idx, *, sm_scale, kv_v=None, kv_scale=None, D_v=None,
     if D_v is None:
         D_v = kv_v.shape[-1] if kv_v is not None else (512 if D_qk == 576 else D_qk)
     if out is None:
-        out = torch.empty(T, H, D_v, dtype=torch.bfloat16, device=q.device)
+        out = _output(_side(stream, q.device), (T, H, D_v), torch.bfloat16, q.device)
     if lse is None:
-        lse = torch.empty(T, H, dtype=torch.float32, device=q.device)
+        lse = _output(_side(stream, q.device), (T, H), torch.float32, q.device)
     need = N.lib.dsa_sparse_attn_workspace_size(T, H, K, D_v)
     if ws is None and need:
-        ws = torch.zeros(need, dtype=torch.uint8, device=q.device)
+        ws = _zeros(stream, need, q.device)
     st = N.lib.dsa_sparse_attn(_p(q), _p(kv), _p(kv_v), _p(kv_scale), kv.stride(1) * kv.element_size(),
                                _seq_stride(kv), 0 if kv_v is None else kv_v.stride(1) * 2, _seq_stride(kv_v),
                                _p(idx), T, q_per_seq, L, K, H, D_qk, D_v, float(sm_scale), _kv_dtype(kv, kv_scale),
@@ -132,7 +198,7 @@ def dsa_topk_pairs(scores, K, *, L, pos_offset, cand_pos, cand_scores, q_per_seq
     T = scores.shape[0]
     ws_bytes = N.lib.dsa_topk_workspace_size(T, L, K)
     if ws is None:
-        ws = torch.zeros(max(ws_bytes, 16), dtype=torch.uint8, device=scores.device)
+        ws = _zeros(stream, max(ws_bytes, 16), scores.device)
     st = N.lib.dsa_topk_pairs(_p(scores), scores.stride(0), T, q_per_seq, q_pos0, _p(n_valid), L, K,
                               int(pos_offset), _p(cand_pos), _p(cand_scores), cand_pos.stride(0), _p(ws),
                               ws.numel(), _stream(stream))
@@ -151,7 +217,7 @@ def dsa_topk_merge(cand_scores, cand_pos, K, *, idx=None, stream=None) -> torch.
         parts, T, n = cand_pos.shape
         ld, pst = cand_pos.stride(1), cand_pos.stride(0)
     if idx is None:
-        idx = torch.empty(T, K, dtype=torch.int32, device=cand_pos.device)
+        idx = _output(_side(stream, cand_pos.device), (T, K), torch.int32, cand_pos.device)
     st = N.lib.dsa_topk_merge(_p(cand_scores), _p(cand_pos), T, parts, n, ld, pst, K, _p(idx), _stream(stream))
     N.check(st, "dsa_topk_merge")
     return idx
@@ -167,12 +233,12 @@ def dsa_sparse_attn_partial(q, kv, idx, *, sm_scale, pos_lo, kv_v=None, kv_scale
     if D_v is None:
         D_v = kv_v.shape[-1] if kv_v is not None else (512 if D_qk == 576 else D_qk)
     if o_part is None:
-        o_part = torch.empty(T, H, D_v, dtype=torch.float32, device=q.device)
+        o_part = _output(_side(stream, q.device), (T, H, D_v), torch.float32, q.device)
     if lse_part is None:
-        lse_part = torch.empty(T, H, dtype=torch.float32, device=q.device)
+        lse_part = _output(_side(stream, q.device), (T, H), torch.float32, q.device)
     need = N.lib.dsa_sparse_attn_workspace_size(T, H, K, D_v)
     if ws is None and need:
-        ws = torch.zeros(need, dtype=torch.uint8, device=q.device)
+        ws = _zeros(stream, need, q.device)
     st = N.lib.dsa_sparse_attn_partial(
         _p(q), _p(kv), _p(kv_v), _p(kv_scale), kv.stride(1) * kv.element_size(), _seq_stride(kv),
         0 if kv_v is None else kv_v.stride(1) * 2, _seq_stride(kv_v), _p(idx), T, q_per_seq, L, K, H, D_qk, D_v,
@@ -187,9 +253,9 @@ def dsa_attn_combine(o_parts, lse_parts, *, out=None, lse=None, stream=None):
     output [T, H, D_v] and its log-sum-exp [T, H]."""
     G, T, H, D_v = o_parts.shape
     if out is None:
-        out = torch.empty(T, H, D_v, dtype=torch.bfloat16, device=o_parts.device)
+        out = _output(_side(stream, o_parts.device), (T, H, D_v), torch.bfloat16, o_parts.device)
     if lse is None:
-        lse = torch.empty(T, H, dtype=torch.float32, device=o_parts.device)
+        lse = _output(_side(stream, o_parts.device), (T, H), torch.float32, o_parts.device)
     st = N.lib.dsa_attn_combine(_p(o_parts), _p(lse_parts), G, o_parts.stride(0), lse_parts.stride(0), T, H, D_v,
                                 _p(out), _p(lse), _stream(stream))
     N.check(st, "dsa_attn_combine")
@@ -261,8 +327,10 @@ class DsaCall:
         self.ws = ws
         self._fn = N.lib.dsa_prefill if self.prefill else N.lib.dsa_decode
         self.launches = dsa_launch_count(a, self.prefill)  # kernels per call
+        self._owned = Owned(self.out, self.lse, self.idx, self.ws)
 
     def __call__(self, stream=None):
+        self._owned.follow(stream)
         st = self._fn(ctypes.byref(self.args), _p(self.ws), self.ws.numel(), _stream(stream))
         N.check(st, "dsa_prefill" if self.prefill else "dsa_decode")
         return self.out, self.lse, self.idx
@@ -281,9 +349,9 @@ def dsa_quantize_mxfp8(x, *, codes=None, sf=None, dst_rows=None, stream=None):
     [*, d/32] (a cache append); without it new [rows, d] / [rows, d/32] tensors are returned."""
     rows, d = x.shape
     if codes is None:
-        codes = torch.empty(rows, d, dtype=torch.uint8, device=x.device)
+        codes = _output(_side(stream, x.device), (rows, d), torch.uint8, x.device)
     if sf is None:
-        sf = torch.empty(rows, d // 32, dtype=torch.uint8, device=x.device)
+        sf = _output(_side(stream, x.device), (rows, d // 32), torch.uint8, x.device)
     N.check(N.lib.dsa_quantize_mxfp8(_p(x), x.stride(0), rows, d, _p(codes), _p(sf), _p(dst_rows),
                                      _stream(stream)), "dsa_quantize_mxfp8")
     return codes, sf
@@ -294,9 +362,9 @@ def dsa_quantize_fp8_rows(x, *, codes=None, scales=None, dst_rows=None, stream=N
     dsa_quantize_mxfp8 (codes [*, >= width] with any row pitch, scales [*])."""
     rows, width = x.shape
     if codes is None:
-        codes = torch.empty(rows, width, dtype=torch.uint8, device=x.device)
+        codes = _output(_side(stream, x.device), (rows, width), torch.uint8, x.device)
     if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+        scales = _output(_side(stream, x.device), rows, torch.float32, x.device)
     N.check(N.lib.dsa_quantize_fp8_rows(_p(x), x.stride(0), rows, width, _p(codes), codes.stride(0),
                                         _p(scales), _p(dst_rows), _stream(stream)),
             "dsa_quantize_fp8_rows")
@@ -309,9 +377,9 @@ def dsa_quantize_fp8_tiles(x, *, tile=128, codes=None, scales=None, dst_rows=Non
     rows, width = x.shape
     nt = -(-width // tile)
     if codes is None:
-        codes = torch.empty(rows, width, dtype=torch.uint8, device=x.device)
+        codes = _output(_side(stream, x.device), (rows, width), torch.uint8, x.device)
     if scales is None:
-        scales = torch.empty(rows, nt, dtype=torch.float32, device=x.device)
+        scales = _output(_side(stream, x.device), (rows, nt), torch.float32, x.device)
     N.check(N.lib.dsa_quantize_fp8_tiles(_p(x), x.stride(0), rows, width, tile, _p(codes), codes.stride(0),
                                          _p(scales), _p(dst_rows), _stream(stream)), "dsa_quantize_fp8_tiles")
     return codes, scales
@@ -341,12 +409,6 @@ def _cuda_device(what, t) -> torch.device:
     return t.device
 
 
-# The current stream's handle and the current device without building torch objects (a serving step makes
-# several short calls, and the host's share of each is most of its time).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-
-
 def _run(what, fn, device, stream, *args):
     i = device.index
     if stream is None:
@@ -366,33 +428,6 @@ def _run(what, fn, device, stream, *args):
 
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
-
-
-# What a call allocates belongs to the stream that it runs on.  torch's allocator hands a freed block to later work of
-# the stream that it was allocated on, without waiting for any other stream: scratch from the current stream's pool
-# would be given away while the kernels on the caller's `stream` still use it, and an output's block may still be read
-# by pending work of the current stream.
-
-def _side(stream, device):
-    """`stream`, where it is given and is not the device's current one; None otherwise."""
-    return None if stream is None or stream.cuda_stream == _raw_stream(device.index) else stream
-
-
-def _scratch(side, shape, dtype, device):
-    if side is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(side):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _hand_back(t, device):
-    """The caller's current stream reads `t` too: its block waits for that stream before it is used again."""
-    t.record_stream(torch.cuda.current_stream(device))
-    return t
-
-
-def _output(side, shape, dtype, device):
-    return torch.empty(shape, dtype=dtype, device=device) if side is None else _hand_back(_scratch(side, shape, dtype, device), device)
 
 
 class BlockPlan(NamedTuple):

@@ -102,11 +102,13 @@ class SliceSteps:
         self.topk_ws = torch.zeros(max(16, N.lib.dsa_topk_workspace_size(T, self.L_g, K)), dtype=torch.uint8,
                                    device=dev)
         self.attn_ws = None
+        self._owned = api.Owned(self.scores, self.topk_ws, self.n_valid)
 
     def pairs(self, q_idx, q_idx_sf, w, cand_pos, cand_scores, stream=None):
         """Steps 1-2: this slice's Top-K as (score, global position) pairs into cand_pos /
         cand_scores ([T, K] views, int32 / fp32)."""
         c = self.caches
+        self._owned.follow(stream)
         api.dsa_index_score(q_idx, w, c["k_idx"], q_idx_sf=q_idx_sf, k_idx_sf=c["k_idx_sf"], n_valid=self.n_valid,
                             scores=self.scores, stream=stream)
         api.dsa_topk_pairs(self.scores, self.K, L=self.L_g, pos_offset=self.plan.lo(self.g), cand_pos=cand_pos,
@@ -122,6 +124,8 @@ class SliceSteps:
             D_v = o_part.shape[-1]
             need = N.lib.dsa_sparse_attn_workspace_size(T, H, idx.shape[1], D_v)
             self.attn_ws = torch.zeros(max(16, need), dtype=torch.uint8, device=q.device)
+            self._owned_attn = api.Owned(self.attn_ws)
+        self._owned_attn.follow(stream)
         api.dsa_sparse_attn_partial(q, c["kv"], idx, sm_scale=self.sm_scale, pos_lo=self.plan.lo(self.g),
                                     kv_v=c["kv_v"], kv_scale=c["kv_scale"], D_v=o_part.shape[-1], o_part=o_part,
                                     lse_part=lse_part, ws=self.attn_ws, stream=stream)
@@ -145,8 +149,10 @@ class SplitDecode:
         self.lse_parts = torch.empty(G, T, H, dtype=torch.float32, device=dev)
         self.out = torch.empty(T, H, D_v, dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty(T, H, dtype=torch.float32, device=dev)
+        self._owned = api.Owned(self.cand_pos, self.cand_scores, self.idx, self.o_parts, self.lse_parts, self.out, self.lse)
 
     def __call__(self, q_idx, q_idx_sf, w, q, stream=None):
+        self._owned.follow(stream)
         for g, st in enumerate(self.steps):
             st.pairs(q_idx, q_idx_sf, w, self.cand_pos[g], self.cand_scores[g], stream=stream)
         api.dsa_topk_merge(self.cand_scores, self.cand_pos, self.K, idx=self.idx, stream=stream)
