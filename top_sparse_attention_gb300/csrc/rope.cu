@@ -34,9 +34,10 @@ constexpr int kCtasPerSm = 3;  // resident CTAs (registers); a large launch has 
 // sin) of the row in hand.
 struct RopeSmem {
   uint64_t freq[kRopeMaxPairs];
-  float2 turns[kWarps][kRopeMaxPairs];
+  alignas(16) float2 turns[kWarps][kRopeMaxPairs];  // (the append kernels read turned columns from here as float4)
   uint8_t axis[kRopeMaxPairs];  // (a copy: lanes read different entries, which parameters serve one by one)
 };
+static_assert(alignof(RopeSmem) >= 16 && offsetof(RopeSmem, turns) % 16 == 0, "float4 reads");
 
 // inv_freq / 2 pi modulo 1, times 2^64 (once per CTA: a row's fp64 products would cost more than its loads).
 __device__ __forceinline__ void fill_freq(const RopeParams& p, RopeSmem& s) {
