@@ -414,7 +414,8 @@ dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int wi
  *              any set of nodes (usually its ancestors and itself); NULL: the nodes j <= i (a chain)
  *   logit[p] = sm_scale * q[t,h] . Kv[p];  out[t,h,:] = sum_p softmax(logit)[p] * Kv[p, :512]  (bf16)
  *   lse[t,h] = ln sum_p exp(logit[p])                                                        (fp32)
- * over the positions it sees.  A node that sees nothing, and a node i >= m (padding), gets out = 0
+ * over the positions it sees; the weights are rounded to bf16 and summed in fp32, which is off by at most
+ * 2^-11 + L 2^-39 of sum_p softmax_p |Kv[p]|.  A node that sees nothing, and a node i >= m (padding), gets out = 0
  * and lse = -inf.  The contents of a cache row do not matter to a node that does not see it (a
  * position past the end, another branch of the tree: infinities and NaN included); a NaN in a row
  * that a node sees makes that node's output NaN.  With E4M3 rows the elements of a query row below

@@ -225,3 +225,27 @@ def test_tree_args_layout_matches_c(tmp_path, lib):
                     str(tmp_path / "layout")], check=True)
     got = [int(v) for v in subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True, check=True).stdout.split()]
     assert got == [ctypes.sizeof(N.DsaTreeArgs)] + [getattr(N.DsaTreeArgs, f).offset for f in fields]
+
+
+def test_tree_attn_workspace_holds_accumulators_of_long_contexts(lib):
+    import ctypes
+
+    def size(**kw):
+        a, n = _tree_args(**kw), ctypes.c_size_t(0)
+        assert lib.dsa_tree_attn_workspace_size(ctypes.byref(a), ctypes.byref(n)) == 0
+        return n.value
+
+    def contiguous(L, n_seq, **kw):
+        return size(L=L, n_seq=n_seq, kv_seq_stride=1152 * L, **kw)
+
+    # up to 1024 tiles of 64 positions: partial results only, and those only where row tiles are split
+    row = 128 * (2 * 8 + 512 * 4)
+    parts = contiguous(65536, 2)
+    assert parts >= 228 * row and contiguous(64, 2) == parts and contiguous(65536, 609) == 0
+    # beyond: 128 rows of sums, half of the values, for each of 152 CTAs
+    sums = 152 * 128 * (2 * 8 + 256 * 4)
+    assert contiguous(65537, 2) == parts + sums
+    assert contiguous(65537, 609) == sums
+    a = _tree_args(L=65537, n_seq=609, kv_seq_stride=1152 * 65537)
+    assert lib.dsa_tree_attn(ctypes.byref(a), None, 0, None) == 3  # workspace
+    assert lib.dsa_tree_attn(ctypes.byref(a), F, sums - 1, None) == 3

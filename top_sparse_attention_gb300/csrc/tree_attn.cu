@@ -59,6 +59,14 @@ constexpr int kSmemMax = 227 * 1024;
 constexpr float kLazy = 8.f;              // log2 growth of a row's maximum that is left unscaled
 constexpr int kMaxItems = 8;              // of a pair of CTAs, in a planned launch
 constexpr int kSlotsPerPair = 3;          // partial results
+// The tensor cores truncate their sums, four to a tile, so o loses up to 2^-23 of itself each time, always in the same
+// direction: 0.037 % over 1024 tiles, 0.34 % over 8192, 2.7 % over 65536 (measured).  Launches whose contexts may be longer
+// than kLong tiles walk an item in stretches of kStretch tiles, whose o and l are added up in fp32, in memory: 0.02 % at
+// any length.  They are a form of the kernel of their own, because it costs something where nothing is long too (device us
+// without and with it, contexts of 32K: 8 x 8 nodes bf16 98.5 and 99.5, 8 x 64 E4M3 rows 606 and 624, 8 x 64 tile scales
+// 1280 and 1309; contexts of 60K, two stretches: 8 x 64 bf16 1300 and 1312, E4M3 1161 and 1170, tile scales 2301 and 2372).
+// (A break inside the tile loop cost up to 9 %, stretches as an outer loop around it 11 %: the loop's registers.)
+constexpr int kLong = 1024, kStretch = 512;
 constexpr int kAhead = 2;                 // tiles between the request to L2 and the load into shared memory
 constexpr int kColO = 0;                  // tensor-memory columns: O, then boxes of q, S and the weights
 
@@ -118,6 +126,9 @@ struct TreePlan {
   int* head;               // [0]: tiles of a chunk, or minus those of a span; [1 + s]: first item or tile of sequence s
   float4* part_o;          // [cap][128 groups of four values][128 rows]
   float2* part_ml;         // [cap][half of the values][128 rows]
+  // per CTA of a launch with long contexts: the sums of an item's stretches so far
+  float4* sum_o;           // [2 grid][64 groups of four values][128 rows]
+  float2* sum_ml;          // [2 grid][half of a tile's positions][128 rows]: the reference maximum, the sum of weights
 };
 
 __device__ __forceinline__ void seq_facts(const TreeAttnParams& p, int seq, int& ctx, int& fresh, int& len) {
@@ -491,12 +502,32 @@ __device__ __forceinline__ bool get_item(const TreeAttnParams& p, const TreePlan
   return true;
 }
 
+// The next item, or with LONG the next stretch of one: tiles [t0, t1) of those that end at `st.stop`.
+struct Stretch {
+  int stop = 0;
+  bool first = true;
+};
+template <bool LONG>
+__device__ __forceinline__ bool next_item(const TreeAttnParams& p, const TreePlan& pl, const Aux* a, int& i, Item& it, Stretch& st) {
+  if (!LONG) return get_item(p, pl, a, i, it);
+  st.first = it.t1 >= st.stop;
+  if (st.first) {
+    if (!get_item(p, pl, a, i, it)) return false;
+    st.stop = it.t1;
+  } else {
+    it.t0 = it.t1;
+    --i;
+  }
+  it.t1 = min(st.stop, it.t0 + kStretch);
+  return true;
+}
+
 template <int N>
 struct Int {
   static constexpr int v = N;
 };
 
-template <int FMT>
+template <int FMT, bool LONG>
 __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tm, const TreeAttnParams p, const TreePlan pl) {
   using C = Cfg<FMT>;
@@ -543,6 +574,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
   pdl_launch_dependents();
 
   Item it = {};
+  Stretch st;
   if (warp == 0) {
     // ---- producer: boxes of 64 columns x 64 positions by TMA
     if (lane == 0) {
@@ -566,7 +598,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
       };
       Item next;
       if (get_item(p, pl, a, 0, next)) query(next);
-      for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
+      for (int i = 0; ok && next_item<LONG>(p, pl, a, i, it, st); ++i) {
         if (get_item(p, pl, a, i + 1, next)) query(next);
         for (int t = it.t0; !C::FP8 && t < it.t0 + kAhead; ++t) ahead(t);
         for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
@@ -734,7 +766,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
       if (++ps == C::VS) ps = 0, pph ^= 1;
       ++tile;
     };
-    for (int i = 0; ok && uniform(get_item(p, pl, a, i, it)); ++i) {
+    for (int i = 0; ok && uniform(next_item<LONG>(p, pl, a, i, it, st)); ++i) {
       const int t0 = uniform(it.t0), t1 = uniform(it.t1);
       if (t0 >= t1) continue;
       all(&a->q_full, items & 1);
@@ -771,7 +803,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
     // ---- scales of the tile's positions (1 where there is none: the position is masked)
     int tiles = 0;
     bool ok = true;
-    for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
+    for (int i = 0; ok && next_item<LONG>(p, pl, a, i, it, st); ++i) {
       for (int t = it.t0; ok && t < it.t1; ++t, ++tiles) {
         const int d = tiles & 1;
         int64_t row = tree_row(p, it.seq, t * kKeys);
@@ -799,7 +831,7 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
     const int w = warp - 12, c = lane & 3;
     int cs = 0, cph = 0, vs = 0, vph = 0;
     bool ok = true;
-    for (int i = 0; ok && get_item(p, pl, a, i, it); ++i) {
+    for (int i = 0; ok && next_item<LONG>(p, pl, a, i, it, st); ++i) {
       for (int t = it.t0; ok && t < it.t1; ++t) {
         ok = __all_sync(0xffffffffu, wait_ahead(a, &a->c_full[cs], cph, err));
         if (!ok) break;
@@ -835,22 +867,22 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
     }
   } else if (warp >= 4) {
     // ---- softmax warps: thread = row = tensor-memory lane, half h of the tile's positions
-    const int w = warp - 4, h = w >> 2, quarter = w & 3, row = 32 * quarter + lane, st = tid - 128;
+    const int w = warp - 4, h = w >> 2, quarter = w & 3, row = 32 * quarter + lane, tw = tid - 128;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
     const int rows = p.q_per_seq * p.H;
     int tile = 0, items = 0;
     uint32_t su = 0;
     bool ok = true;
 
-    for (int i = 0; get_item(p, pl, a, i, it); ++i) {
+    for (int i = 0; next_item<LONG>(p, pl, a, i, it, st); ++i) {
       const int row_lo = it.rt * kRows;
       const int64_t at = (int64_t)it.seq * rows + row_lo;  // the item's first row in out and lse
       const int nrows = min(kRows, rows - row_lo);
       if (it.t0 >= it.t1) {  // nothing to see: padding nodes, or an empty sequence
         if (rank == 0) {
-          for (int k = st; k < nrows * (kDv / 8); k += 256)
+          for (int k = tw; k < nrows * (kDv / 8); k += 256)
             reinterpret_cast<uint4*>(p.out + at * kDv)[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (p.lse && st < nrows) p.lse[at + st] = -INFINITY;
+          if (p.lse && tw < nrows) p.lse[at + tw] = -INFINITY;
         }
         continue;
       }
@@ -1037,12 +1069,12 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
           clear = __reduce_or_sync(0xffffffffu, clear);
           if (lane == 0) a->clear[tile & 1][w] = clear;
           softmax_bar();
-          const int key = st >> 2;  // a position, one of its four boxes
+          const int key = tw >> 2;  // a position, one of its four boxes
           uint32_t word = 0u;
 #pragma unroll
           for (int k = 0; k < 4; ++k) word |= a->clear[tile & 1][(key >> 5) * 4 + k];
           if ((word >> (key & 31)) & 1) {
-            uint8_t* line = v_s + (tile % C::VS) * kSlotV + (st & 3) * kBox + key * 128;
+            uint8_t* line = v_s + (tile % C::VS) * kSlotV + (tw & 3) * kBox + key * 128;
             bool zero = t * kKeys + key >= it.len;
             if (!zero) {
 #pragma unroll
@@ -1136,12 +1168,26 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         }
       }
       // ---- the rows' sums (their halves added in the same order everywhere)
+      float now = 1.f, before = 0.f;  // what brings this stretch's sums, and those of the ones before, to their maximum
+      float4* sum_o = nullptr;        // this thread's: no other one touches them
+      const bool last = !LONG || it.t1 == st.stop;
+      if (LONG && !(st.first && last)) {
+        sum_o = pl.sum_o + ((int64_t)blockIdx.x * 64 + 32 * h) * kRows + row;
+        float2* ml = pl.sum_ml + ((int64_t)blockIdx.x * 2 + h) * kRows + row;
+        const float2 old = st.first ? make_float2(-INFINITY, 0.f) : *ml;
+        const float M = fmaxf(m, old.x);
+        now = m == -INFINITY ? 0.f : ex2(m - M);
+        before = old.x == -INFINITY ? 0.f : ex2(old.x - M);
+        m = M;
+        l = fmaf(old.y, before, l * now);
+        if (!last) *ml = make_float2(m, l);
+      }
       a->sum[h][row] = l;
       pair_bar(quarter);
       l = a->sum[0][row] + a->sum[1][row];
       const bool live = row < nrows && (row_lo + row) / p.H < it.fresh;
       const float inv = live && l != 0.f ? 1.f / l : 0.f;
-      if (h == 0) {
+      if (h == 0 && last) {
         // (each CTA's own: the two sum the logits' columns in different orders, so that their maxima may differ)
         if (it.slot >= 0) pl.part_ml[((int64_t)it.slot * 2 + rank) * kRows + row] = make_float2(m, l);
         else if (rank == 0 && p.lse && row < nrows) p.lse[at + row] = !live || l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -1152,7 +1198,18 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
       for (int c = 128 * h; c < 128 * h + 128; c += 32) {
         float o[32];
         tmem_ld_sync(lane_base + kColO + c, o);
-        if (row < nrows && it.slot >= 0) {
+        if (LONG && sum_o) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k, sum_o += kRows) {
+            float4 v = st.first ? make_float4(0.f, 0.f, 0.f, 0.f) : *sum_o;
+            v.x = fmaf(v.x, before, o[4 * k] * now), v.y = fmaf(v.y, before, o[4 * k + 1] * now);
+            v.z = fmaf(v.z, before, o[4 * k + 2] * now), v.w = fmaf(v.w, before, o[4 * k + 3] * now);
+            if (!last) *sum_o = v;
+            o[4 * k] = v.x, o[4 * k + 1] = v.y, o[4 * k + 2] = v.z, o[4 * k + 3] = v.w;
+          }
+        }
+        if (!last) {
+        } else if (row < nrows && it.slot >= 0) {
           float4* dst = pl.part_o + ((int64_t)it.slot * (kDv / 4) + (256 * rank + c) / 4) * kRows + row;
 #pragma unroll
           for (int k = 0; k < 8; ++k) dst[k * kRows] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
@@ -1275,10 +1332,14 @@ TreePlan plan_of(const TreeAttnParams& p) {
   return pl;
 }
 
+bool long_contexts(const TreeAttnParams& p) { return p.L > kLong * kKeys; }
+constexpr size_t kPartBytes = (size_t)kRows * (2 * sizeof(float2) + kDv * sizeof(float));     // of a partial result
+constexpr size_t kSumBytes = (size_t)kRows * (2 * sizeof(float2) + kDv / 2 * sizeof(float));  // a CTA's sums
+
 size_t head_bytes(const TreeAttnParams& p) { return align_up((size_t)(1 + p.n_seq) * sizeof(int), 256); }
 
-template <int FMT>
-cudaError_t launch_fmt(const TreeAttnParams& p, TreePlan pl, void* ws, cudaStream_t stream) {
+template <int FMT, bool LONG>
+cudaError_t launch_form(const TreeAttnParams& p, TreePlan pl, void* ws, cudaStream_t stream) {
   using C = Cfg<FMT>;
   const bool paged = p.pages.table != nullptr;
   const cuuint64_t n = paged ? (cuuint64_t)p.pages.num_blocks * p.pages.block_size : (cuuint64_t)p.L;
@@ -1292,15 +1353,19 @@ cudaError_t launch_fmt(const TreeAttnParams& p, TreePlan pl, void* ws, cudaStrea
                         const_cast<uint8_t*>(p.kv), dims, strides, box,
                         C::FP8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
+  uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   if (pl.cap) {
-    uint8_t* w = reinterpret_cast<uint8_t*>(ws);
     pl.head = reinterpret_cast<int*>(w);
     w += head_bytes(p);
     pl.part_ml = reinterpret_cast<float2*>(w);
-    w += (size_t)pl.cap * 2 * kRows * sizeof(float2);
-    pl.part_o = reinterpret_cast<float4*>(w);
+    pl.part_o = reinterpret_cast<float4*>(w + (size_t)pl.cap * 2 * kRows * sizeof(float2));
+    w += pl.cap * kPartBytes;
   }
-  auto kern = tree_attn_kernel<FMT>;
+  if (LONG) {
+    pl.sum_ml = reinterpret_cast<float2*>(w);
+    pl.sum_o = reinterpret_cast<float4*>(w + (size_t)2 * pl.grid * 2 * kRows * sizeof(float2));
+  }
+  auto kern = tree_attn_kernel<FMT, LONG>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem_once(&allowed, reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
@@ -1312,12 +1377,17 @@ cudaError_t launch_fmt(const TreeAttnParams& p, TreePlan pl, void* ws, cudaStrea
   return launch_kernel(tree_combine_kernel<1>, dim3(rows8, p.n_seq, 4), dim3(256), 0, stream, true, p, pl);
 }
 
+template <int FMT>
+cudaError_t launch_fmt(const TreeAttnParams& p, const TreePlan& pl, void* ws, cudaStream_t stream) {
+  return long_contexts(p) ? launch_form<FMT, true>(p, pl, ws, stream) : launch_form<FMT, false>(p, pl, ws, stream);
+}
+
 }  // namespace
 
 size_t tree_attn_ws_bytes(const TreeAttnParams& p) {
   const TreePlan pl = plan_of(p);
-  if (!pl.cap || p.L == 0) return 0;
-  return head_bytes(p) + (size_t)pl.cap * kRows * (2 * sizeof(float2) + kDv * sizeof(float));
+  if (p.L == 0) return 0;
+  return (pl.cap ? head_bytes(p) + pl.cap * kPartBytes : 0) + (long_contexts(p) ? 2 * pl.grid * kSumBytes : 0);
 }
 
 cudaError_t launch_tree_attn(const TreeAttnParams& p, void* ws, cudaStream_t stream) {
