@@ -364,11 +364,12 @@ dsa_status dsa_block_plan(const int32_t* n_ctx, const int32_t* n_new, int n_seq,
  * Pair i (0 <= i < rot_dim / 2) of row r turns by theta = pos[r, pair_axis[i]] * inv_freq[i]:
  *   y0 = x0 cos theta - x1 sin theta,   y1 = x1 cos theta + x0 sin theta
  * where (x0, x1) are columns rot_off + (i, i + rot_dim / 2) for DSA_ROPE_HALF and rot_off +
- * (2i, 2i + 1) for DSA_ROPE_PAIRS.  The angle is exact to fp32 at every 32-bit position.
+ * (2i, 2i + 1) for DSA_ROPE_PAIRS.  The angle, modulo whole turns, is right to fp32 at every 32-bit position
+ * (to 2^-33 turns, or 2^-24 of itself where that is more).
  *   pos        device int32 [rows][n_axes]
  *   pair_axis  HOST bytes [rot_dim / 2], each below n_axes, read before the call returns; NULL when
  *              n_axes = 1
- *   inv_freq   device fp32 [rot_dim / 2], finite
+ *   inv_freq   device fp32 [rot_dim / 2], at most 2^40 in size
  * Supported: rot_dim even, at most 256; n_axes at most 4; finite inputs.
  *
  * dsa_rope: x [rows, heads, width] bf16 (element (r, h, c) at x + r*x_row_stride + h*x_head_stride + c,

@@ -6,11 +6,13 @@
 // the pair being elements (i, i + rot_dim / 2) of the rotated columns or (2i, 2i + 1).
 //
 // The angle.  A position of a million times a frequency of one loses the angle in fp32 (an ulp of
-// 10^6 is 0.06 rad).  Here inv_freq / 2 pi, in turns, becomes a 64-bit fixed-point fraction (from an
-// fp64 product, once per pair and row block); position times fraction modulo 2^64 is then exact
-// integer arithmetic that drops the whole turns by itself, and its top 32 bits over 2^31 are theta
-// in half turns, in [-1, 1), for sincospif.  The fp64 product is off by 2^-53 of the angle at most:
-// under 2^-30 turns up to position 2^24 (inv_freq <= 1), 2^-24 turns (fp32's own rounding) at 2^31.
+// 10^6 is 0.06 rad).  Here inv_freq / 2 pi, in turns, becomes a 64-bit fixed-point fraction (its
+// significand times 128 bits of 1 / 2 pi, in integers, once per pair and CTA; fp64 took 0.2 us longer);
+// position times fraction modulo 2^64 is then exact integer arithmetic that drops the whole turns by
+// itself, and it is theta in half turns, in [-1, 1), for sincospif: rounded to fp32 from all 64 bits, so
+// that small angles keep their digits.  The fraction is cut off, by less than 2^-64 (for |inv_freq| <=
+// 2^40, where 1 / 2 pi has bits enough), so the angle is off by at most 2^-33 turns at the farthest
+// position.
 //
 // A warp takes one row (append; half a warp for many rows with tile or MXFP8 scales) or 16 heads of a row (rope) after
 // another: the lanes take the sines of the row's pairs once and share them through shared memory; 16-byte loads and
@@ -39,12 +41,23 @@ struct RopeSmem {
 };
 static_assert(alignof(RopeSmem) >= 16 && offsetof(RopeSmem, turns) % 16 == 0, "float4 reads");
 
-// inv_freq / 2 pi modulo 1, times 2^64 (once per CTA: a row's fp64 products would cost more than its loads).
+// f / 2 pi modulo 1, times 2^64.  With f = m 2^e and C = 2^130 / 2 pi it is m C 2^(e - 66), of which the low 64 bits of
+// the whole part are kept.
+__device__ __forceinline__ uint64_t turn_fraction(float f) {
+  constexpr uint64_t kHi = 0xa2f9836e4e441529ull, kLo = 0xfc2757d1f534ddc0ull;  // C
+  const uint32_t bits = __float_as_uint(f), ex = bits >> 23 & 255;
+  const uint32_t m = (bits & 0x7FFFFFu) | (ex ? 0x800000u : 0u);
+  const int down = min(max(66 + 150 - (int)max(ex, 1u), 1), 64 + 127);
+  const uint64_t low = kLo * m;
+  const unsigned __int128 high = (unsigned __int128)kHi * m + __umul64hi(kLo, m);  // m C = high 2^64 + low
+  const uint64_t r = down < 64 ? (uint64_t)(high << (64 - down)) | low >> down : (uint64_t)(high >> (down - 64));
+  return (int32_t)bits < 0 ? 0 - r : r;
+}
+
+// The pairs' fractions (once per CTA).
 __device__ __forceinline__ void fill_freq(const RopeParams& p, RopeSmem& s) {
   for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) {
-    const double turns = (double)p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-    const double frac = turns - rint(turns);                              // [-1/2, 1/2]
-    s.freq[i] = (uint64_t)__double2ll_rn(frac * 0x1p63) << 1;
+    s.freq[i] = turn_fraction(p.inv_freq[i]);
     s.axis[i] = p.axis[i];
   }
   __syncthreads();
@@ -54,7 +67,7 @@ __device__ __forceinline__ void fill_freq(const RopeParams& p, RopeSmem& s) {
 __device__ __forceinline__ float2 pair_turn(const RopeParams& p, uint64_t freq, int pos) {
   const uint64_t phase = (uint64_t)(int64_t)pos * freq;
   float s, c;
-  sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
+  sincospif(__ll2float_rn((int64_t)phase) * 0x1p-63f, &s, &c);
   return make_float2(c, p.inverse ? -s : s);
 }
 
