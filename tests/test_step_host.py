@@ -249,3 +249,18 @@ def test_tree_attn_workspace_holds_accumulators_of_long_contexts(lib):
     a = _tree_args(L=65537, n_seq=609, kv_seq_stride=1152 * 65537)
     assert lib.dsa_tree_attn(ctypes.byref(a), None, 0, None) == 3  # workspace
     assert lib.dsa_tree_attn(ctypes.byref(a), F, sums - 1, None) == 3
+
+
+@pytest.mark.parametrize("sections,ok", [((16, 16), True), ((0, 32), True), ((32, 0), True), ((-8, 32), False), ((32, -1), False),
+                                         ((40, -8), False), ((16, 15), False), ((32,), False)])
+def test_sections_are_numbers_of_pairs(sections, ok):
+    # a negative count used to be taken for none: (-8, 32) turned all 32 pairs by the second axis
+    from top_sparse_attention_gb300 import api
+
+    x, pos, f = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(2, 2, dtype=torch.int32), torch.zeros(32)
+    args = ("dsa_rope", x.device, x, pos, f, 0, None, sections, None, "half")
+    if ok:
+        assert api._rope_args(*args)[2] == b"\0" * sections[0] + b"\1" * sections[1]
+    else:
+        with pytest.raises(ValueError):
+            api._rope_args(*args)

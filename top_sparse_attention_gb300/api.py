@@ -498,6 +498,8 @@ def _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axi
     if pair_axis is None and sections is not None:
         if len(sections) != n_axes:
             raise ValueError(f"{what}: {len(sections)} sections for {n_axes} axes")
+        if min(sections) < 0:
+            raise ValueError(f"{what}: sections are numbers of pairs, got {tuple(sections)}")
         pair_axis = b"".join(bytes([a]) * int(n) for a, n in enumerate(sections))
     elif pair_axis is not None:
         pair_axis = bytes(pair_axis)
