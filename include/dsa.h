@@ -387,7 +387,7 @@ dsa_status dsa_block_plan(const int32_t* n_ctx, const int32_t* n_new, int n_seq,
  *   DSA_FP8_E4M3_T128  codes and one fp32 scale per 128 columns, scale [dst_count][ceil(width/128)]
  *   DSA_MXFP8_E4M3     codes and one E8M0 byte per 32 columns, scale [dst_count][width/32]
  * with the scales and rounding of dsa_quantize_*.  dst row q at dst + q * dst_row_stride BYTES.
- * Destination rows must be distinct.
+ * Destination rows must be distinct, and dst must not overlap x.
  * ------------------------------------------------------------------------------------------ */
 #define DSA_ROPE_HALF 0
 #define DSA_ROPE_PAIRS 1
@@ -428,8 +428,8 @@ dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int wi
  *   kv_scale   device fp32 of the rows as in dsa_sparse_attn (pool rows when paged); NULL for bf16
  *   out        device bf16 [n_seq * q_per_seq, H, 512];  lse  device fp32 [..., H] or NULL
  * A block id outside [0, num_blocks) on the way records DSA_DEVERR_INDEX_RANGE, and its positions are
- * not seen.  ws: device memory of dsa_tree_attn_workspace_size bytes, 16-byte aligned, contents
- * irrelevant; calls (and captured graphs) that share it must not run at the same time.
+ * not seen.  ws: device memory of dsa_tree_attn_workspace_size bytes (partial results, and with L above 65536
+ * the sums of long walks), 16-byte aligned, contents irrelevant; calls (and captured graphs) that share it must not run at the same time.
  * Supported: D_qk = 576, D_v = 512; kv_dtype DSA_BF16, DSA_FP8_E4M3 or DSA_FP8_E4M3_T128 (finite
  * codes); 1 <= H <= 128; 1 <= q_per_seq <= 1024; n_seq <= 4096; L <= 2^31 - 4097; pointers 16-byte aligned, row
  * strides multiples of 16 bytes, below 2^40.

@@ -17,9 +17,10 @@
 // A warp takes one row (append; half a warp for many rows with tile or MXFP8 scales) or 16 heads of a row (rope) after
 // another: the lanes take the sines of the row's pairs once and share them through shared memory; 16-byte loads and
 // stores.  Rotated values enter the cache format's rounding in fp32 (one rounding, not two).
-// Bound, and measured: bf16 rows by HBM (131072 rows of 576, 302 MB: 51 us, 5.9 TB/s); E4M3 rows by instructions (tile
-// scales 77 us, row scales 62, MXFP8 50); rope into 128-byte pieces of wider rows by the pattern of its writes (32768 x
-// 16 heads, 134 MB: 34 us; copying the pieces alone takes 68 to 75); small calls by the launch (3 us).
+// Bound, and measured: bf16 rows by HBM (131072 rows of 576, 302 MB: 54 us, 5.6 TB/s); E4M3 rows by instructions (tile
+// scales 77 us, row scales 65, MXFP8 50); rope into 128-byte pieces of wider rows by no single unit (32768 x 16 heads,
+// 134 MB: 34 us, with issue slots 53 % busy, DRAM 33 %, and a third of the waits for loads); small calls by the launch (3
+// us).
 #include <math.h>
 
 #include "quant_common.cuh"

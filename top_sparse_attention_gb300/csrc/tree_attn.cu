@@ -16,10 +16,12 @@
 //     MN-major (values along N), 4 steps of K = 16 with N = 256.
 // Why two CTAs: o for 128 rows x 512 values fills a tensor memory (512 columns), which leaves no room for S; with half
 // of the values it takes 256 columns, q 160, S 64, the weights 32.  Why both take the whole first product: an MMA of
-// N = 64 with A in tensor memory takes 32 cycles, one of N = 32 33, so that sharing the positions out saves nothing.
-// Measured (8 x 64 nodes at 32K, E4M3 rows; 8 x 8 nodes at 32K, bf16; us): this form 580 and 92; the positions of the
-// first product shared out and weights exchanged through distributed shared memory 1002 and 105; columns shared out
-// and partial S exchanged 1090 and 120; one CTA with 64 rows and q in shared memory 1805 and 149.
+// N = 64 with A in tensor memory takes 32 cycles, one of N = 32 33, so that sharing the 64 positions of a tile out
+// saves nothing (a tile of 128 shared out would take N = 64 each; that was not built).
+// Measured (8 x 64 nodes at 32K, E4M3 rows; 8 x 8 nodes at 32K, bf16; device us): this form 611 and 91.  The forms before
+// it, as they were when they gave way: the positions of the first product shared out and weights exchanged through
+// distributed shared memory 1002 and 105; columns shared out and partial S exchanged 1090 and 120; one CTA with 64 rows
+// and q in shared memory 1805 and 149.
 //
 // Weights are rounded to bf16 for the second product (as the bf16 cache is); sums, maxima, logits and outputs are
 // fp32.  E4M3 codes enter the first product as they are: q's bf16 values, scaled by a power of two per row, are the sum
@@ -337,7 +339,8 @@ __device__ __forceinline__ uint64_t seen_bits(const TreeAttnParams& p, const Ite
 //   * chunks of CH tiles of every unit (a row tile of a sequence), dealt out in turn: pairs that run together read
 //     the same positions;
 //   * spans of W tiles, a pair's share, of the units' tiles laid end to end: no pair waits for another.  Only the
-//     first and the last item of a span are parts of a unit.  (Units of W / 6 at least: kMaxItems.)
+//     first and the last item of a span are parts of a unit.  (Units of W / 6 at least: kMaxItems.  One that is shorter
+//     leaves the launch to chunks.)
 // The cost of each in tiles: the fullest pair's items and the fill and drain of its pipeline for each, and for a split
 // the merge.  (8 x 64 nodes at 32K, E4M3: 64 units of 512 tiles on 76 pairs, 710 us whole, 630 us as spans.)
 // CTA 0 leaves the plan for the merge.  Scratch: 3 n_seq + 160 ints of shared memory.
@@ -1322,7 +1325,8 @@ __global__ void tree_nothing_kernel(const TreeAttnParams p, int64_t rows) {
 
 constexpr int kPairs = 76;  // of CTAs: two of the 152 SMs each
 
-// A launch with many units needs no plan: its rounds of the grid are full enough.
+// A launch of more units than the lists of items hold has no plan: pairs take whole units in turn.  Its many rounds of the
+// grid are full enough where the contexts are alike; a single long one among short ones is walked by one pair.
 TreePlan plan_of(const TreeAttnParams& p) {
   TreePlan pl = {};
   pl.row_tiles = (p.q_per_seq * p.H + kRows - 1) / kRows;
