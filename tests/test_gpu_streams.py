@@ -118,3 +118,32 @@ def test_chain_entries_on_side_streams_without_workspaces(dsa):
     for out, lse, idx in got[0::2]:
         assert torch.equal(idx.sort(1).values, want_idx.sort(1).values)
         assert torch.equal(out, got[0][0]) and (out.float() - want.float()).abs().max() <= 2e-2
+
+
+def test_calls_on_a_forked_stream_of_a_capture(dsa):
+    # scratch and outputs of calls on a side stream inside a capture come from the graph's pool; replays repeat them
+    q, kv, ctx = _tree_inputs(3)
+    f, pos = torch.ones(32, device="cuda"), _i32(np.arange(6))
+    kw = dict(sm_scale=1 / 24, q_per_seq=3)
+
+    def step(stream):
+        turned = dsa.dsa_rope(q, pos, f, rot_off=512, stream=stream)
+        return (turned,) + dsa.dsa_tree_attn(turned, kv, ctx, stream=stream, **kw)
+
+    want = step(None)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        side.wait_stream(main)
+        a = step(side)
+        b = step(None)
+        main.wait_stream(side)
+        c = [t.clone() for t in a]
+    for _ in range(3):
+        for t in (*a, *b, *c):
+            t.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        for got in (a, b, c):
+            assert all(torch.equal(x, y) for x, y in zip(got, want))
