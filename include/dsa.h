@@ -401,6 +401,116 @@ dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int wi
                            void* scale, const int64_t* dst_rows, void* stream);
 
 /* --------------------------------------------------------------------------------------------
+ * dsa_norm_rope / dsa_norm_rope_append -- dsa_rope and dsa_rope_append with a norm before the rotation, in
+ * the same pass: the norm of each head's query or key, of the latent's 512 columns, or of an indexer key.
+ *
+ * Over columns [off, off + dim) of each vector (head h of row r; with the append, row r):
+ *   y_c = (x_c - mu) w_c / sqrt(var + eps) + b_c
+ * with mu = 0 and var = mean x^2 (DSA_NORM_RMS), or mu the mean and var the mean squared distance from it
+ * (DSA_NORM_LAYER); then the rotary columns turn as in dsa_rope (they may be normed columns, others, or
+ * some of each) and the result is rounded once.  fp32 in between.  The other columns are copied.
+ *   weight, bias  device fp32 [dim] or NULL (ones, zeros)
+ *   eps           finite, at least 0 (with 0 a vector of zeros has no norm and gives NaN)
+ * All other arguments are those of dsa_rope (without inverse) and dsa_rope_append.  out == x (with equal strides)
+ * works in place.
+ * Supported: width at most 1024; finite inputs.
+ * ------------------------------------------------------------------------------------------ */
+#define DSA_NORM_RMS 0
+#define DSA_NORM_LAYER 1
+typedef struct dsa_norm {
+  int kind, off, dim;
+  float eps;
+  const float* weight;
+  const float* bias;
+} dsa_norm;
+
+dsa_status dsa_norm_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride, int rows, int heads, int width,
+                         const dsa_norm* norm, int rot_off, int rot_dim, const int32_t* pos, int n_axes,
+                         const uint8_t* pair_axis, const float* inv_freq, int style, void* out, int64_t out_row_stride,
+                         int64_t out_head_stride, void* stream);
+dsa_status dsa_norm_rope_append(const void* x, int64_t x_row_stride, int rows, int width, const dsa_norm* norm,
+                                int rot_off, int rot_dim, const int32_t* pos, int n_axes, const uint8_t* pair_axis,
+                                const float* inv_freq, int style, dsa_dtype dtype, void* dst, int64_t dst_row_stride,
+                                int64_t dst_count, void* scale, const int64_t* dst_rows, void* stream);
+
+/* --------------------------------------------------------------------------------------------
+ * dsa_latent_expand -- the expanded form of the latent cache, step 1: cached rows expanded to the key and value
+ * of every head, for attention of many queries over them (a prompt, or a chunk of one over its cached context),
+ * where products over 192 + 128 columns a head cost less than ones over 576 + 512.
+ *
+ * Position j of sequence s (0 <= j < kv_start[s+1] - kv_start[s]) becomes row r = kv_start[s] + j of the outputs:
+ *   out[r, h, i] = sum_{c < 512} row[c] * w[h, i, c]  (bf16, i < 256: 128 key columns, then 128 value columns)
+ *   rope_out[r, :] = row[512 .. 575]                  (bf16, the rotary columns that all heads share)
+ * with row[] the cache row's values (codes times scale), sums in fp32.  With one scale per row the scale multiplies
+ * the sum; with one per 128 columns each code times its scale is rounded to bf16 before the product.
+ *   kv_start   device int32 [n_seq + 1], not decreasing; output rows outside [kv_start[0], min(rows, kv_start[n_seq]))
+ *              are left as they were
+ *   kv, kv_scale, kv_row_stride, kv_seq_stride, block_table ...  the latent cache as in dsa_tree_attn
+ *   L          positions per sequence of the cache; a position at L or beyond, or in a block outside [0, num_blocks),
+ *              records DSA_DEVERR_INDEX_RANGE and gives zeros
+ *   w          device bf16 [H, 256, 512]
+ *   out        device bf16 [rows, H, 256];  rope_out  device bf16 [rows, 64] or NULL
+ * Supported: kv_dtype DSA_BF16, DSA_FP8_E4M3 or DSA_FP8_E4M3_T128 (finite codes); H <= 128; n_seq <= 4096; pointers
+ * (but kv_start and block_table) 16-byte aligned, kv_scale 4-byte, row strides multiples of 16 bytes.  No workspace.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct dsa_expand_args {
+  int n_seq, rows, L, H;
+  dsa_dtype kv_dtype;
+  const int32_t* kv_start;
+  const void* kv;
+  const float* kv_scale;
+  int64_t kv_row_stride, kv_seq_stride;
+  const void* w;
+  void* out;
+  void* rope_out;
+  const int32_t* block_table; /* device int32 [n_seq][max_blocks] or NULL */
+  int block_size, max_blocks, num_blocks;
+} dsa_expand_args;
+
+dsa_status dsa_latent_expand(const dsa_expand_args* a, void* stream);
+
+/* --------------------------------------------------------------------------------------------
+ * dsa_expanded_attn -- the expanded form, step 2: exact softmax attention of packed, ragged prompts (or chunks of them)
+ * over expanded keys and values.  Sequence s has the m = q_start[s+1] - q_start[s] queries q_start[s] ... and the
+ * n = kv_start[s+1] - kv_start[s] positions kv_start[s] ... of k, k_rope and v.  Query i of it sees the positions p <=
+ * n - m + i (causal != 0: the queries are the sequence's last positions), or all n:
+ *   logit[p] = sm_scale * (q[i, h, :128] . k[p, h, :] + q[i, h, 128:] . k_rope[p, :])
+ *   out[i, h, :] = sum_p softmax(logit)[p] * v[p, h, :]  (bf16);   lse[i, h] = ln sum_p exp(logit[p])  (fp32)
+ * The weights are rounded to bf16 and summed in fp32.  A query that sees nothing gets out = 0 and lse = -inf.  What
+ * the rows of a position hold does not matter to a query that does not see it (infinities and NaN included); an infinity
+ * or NaN in a value that a query sees appears in its output.
+ *   q          device bf16 [T, H, 192]
+ *   k, v       device bf16: head h of row r at r * row_stride + h * head_stride ELEMENTS, 128 columns (with
+ *              dsa_latent_expand's output, k = out and v = out + 128, strides 256 H and 256)
+ *   k_rope     device bf16 [N, 64]
+ *   q_start, kv_start  device int32 [n_seq + 1], not decreasing, at most T and N; rows of q behind the last sequence
+ *              are not read, their out and lse left as they were
+ *   max_len    positions of the longest sequence at most (0: N): sizes the workspace.  A longer sequence records
+ *              DSA_DEVERR_INDEX_RANGE and its queries' results are not defined
+ *   out        device bf16 [T, H, 128];  lse  device fp32 [T, H] or NULL
+ * ws: device memory of dsa_expanded_attn_workspace_size bytes, 256-byte aligned, contents irrelevant; calls (and
+ * captured graphs) that share it must not run at the same time.
+ * Supported: sm_scale > 0; 1 <= H <= 128; n_seq <= 4096; T, N below 2^24 rows; pointers 16-byte aligned, strides
+ * multiples of 8 elements, below 2^39.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct dsa_expanded_attn_args {
+  int n_seq, T, N, H, max_len, causal;
+  float sm_scale;
+  const int32_t* q_start;
+  const int32_t* kv_start;
+  const void* q;
+  const void* k;
+  const void* k_rope;
+  const void* v;
+  int64_t k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+  void* out;
+  float* lse;
+} dsa_expanded_attn_args;
+
+dsa_status dsa_expanded_attn_workspace_size(const dsa_expanded_attn_args* a, size_t* bytes);
+dsa_status dsa_expanded_attn(const dsa_expanded_attn_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/* --------------------------------------------------------------------------------------------
  * dsa_tree_attn -- exact softmax attention of drafted tokens over the whole visible latent cache:
  * a step that verifies drafts (a chain of tokens, or a tree of them), a decode step of a dense layer,
  * or one whose contexts are no longer than K, where a selection would keep every row.  The

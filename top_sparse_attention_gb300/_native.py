@@ -19,6 +19,7 @@ DEVERR = {0: "none", 1: "index out of range", 2: "wait timeout", 3: "row-split T
           4: "block plan could not place every token"}
 DSA_BLOCK_PLAN_MAX_SEQ = 16384
 DSA_ROPE_HALF, DSA_ROPE_PAIRS = 0, 1
+DSA_NORM_RMS, DSA_NORM_LAYER = 0, 1
 
 EXPORTS = (
     "dsa_status_string", "dsa_abi_version", "dsa_get_device_error", "dsa_index_score",
@@ -27,7 +28,8 @@ EXPORTS = (
     "dsa_workspace_size", "dsa_launch_count", "dsa_decode", "dsa_prefill", "dsa_topk_noalloc",
     "dsa_selftest_wait_timeout", "dsa_topk_pairs", "dsa_topk_merge", "dsa_sparse_attn_partial",
     "dsa_attn_combine", "dsa_set_attn_kernel", "dsa_block_plan", "dsa_rope", "dsa_rope_append",
-    "dsa_tree_attn", "dsa_tree_attn_workspace_size",
+    "dsa_tree_attn", "dsa_tree_attn_workspace_size", "dsa_norm_rope", "dsa_norm_rope_append",
+    "dsa_latent_expand", "dsa_expanded_attn", "dsa_expanded_attn_workspace_size",
 )
 
 
@@ -75,6 +77,40 @@ class DsaTreeArgs(ctypes.Structure):
     ]
 
 
+class DsaNorm(ctypes.Structure):
+    """Mirror of struct dsa_norm."""
+    _fields_ = [
+        ("kind", ctypes.c_int), ("off", ctypes.c_int), ("dim", ctypes.c_int), ("eps", ctypes.c_float),
+        ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+    ]
+
+
+class DsaExpandArgs(ctypes.Structure):
+    """Mirror of struct dsa_expand_args."""
+    _fields_ = [
+        ("n_seq", ctypes.c_int), ("rows", ctypes.c_int), ("L", ctypes.c_int), ("H", ctypes.c_int),
+        ("kv_dtype", ctypes.c_int), ("kv_start", ctypes.c_void_p),
+        ("kv", ctypes.c_void_p), ("kv_scale", ctypes.c_void_p),
+        ("kv_row_stride", ctypes.c_int64), ("kv_seq_stride", ctypes.c_int64),
+        ("w", ctypes.c_void_p), ("out", ctypes.c_void_p), ("rope_out", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("block_size", ctypes.c_int), ("max_blocks", ctypes.c_int), ("num_blocks", ctypes.c_int),
+    ]
+
+
+class DsaExpandedAttnArgs(ctypes.Structure):
+    """Mirror of struct dsa_expanded_attn_args."""
+    _fields_ = [
+        ("n_seq", ctypes.c_int), ("T", ctypes.c_int), ("N", ctypes.c_int), ("H", ctypes.c_int),
+        ("max_len", ctypes.c_int), ("causal", ctypes.c_int), ("sm_scale", ctypes.c_float),
+        ("q_start", ctypes.c_void_p), ("kv_start", ctypes.c_void_p),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("k_rope", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_row_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("v_row_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python -m top_sparse_attention_gb300.build` "
@@ -105,6 +141,12 @@ def _load():
         "dsa_block_plan": (I, [P, P, I, I, I, P, P, I, I, P, I, I, P, P, P, P, P, P, P]),
         "dsa_rope": (I, [P, I64, I64, I, I, I, I, I, P, I, ctypes.c_char_p, P, I, I, P, I64, I64, P]),
         "dsa_rope_append": (I, [P, I64, I, I, I, I, P, I, ctypes.c_char_p, P, I, I, P, I64, I64, P, P, P]),
+        "dsa_norm_rope": (I, [P, I64, I64, I, I, I, ctypes.POINTER(DsaNorm), I, I, P, I, ctypes.c_char_p, P, I, P, I64, I64, P]),
+        "dsa_norm_rope_append": (I, [P, I64, I, I, ctypes.POINTER(DsaNorm), I, I, P, I, ctypes.c_char_p, P, I, I, P, I64, I64, P,
+                                     P, P]),
+        "dsa_latent_expand": (I, [ctypes.POINTER(DsaExpandArgs), P]),
+        "dsa_expanded_attn": (I, [ctypes.POINTER(DsaExpandedAttnArgs), P, SZ, P]),
+        "dsa_expanded_attn_workspace_size": (I, [ctypes.POINTER(DsaExpandedAttnArgs), ctypes.POINTER(SZ)]),
         "dsa_tree_attn": (I, [ctypes.POINTER(DsaTreeArgs), P, SZ, P]),
         "dsa_tree_attn_workspace_size": (I, [ctypes.POINTER(DsaTreeArgs), ctypes.POINTER(SZ)]),
         "dsa_workspace_size": (I, [ctypes.POINTER(DsaArgs), I, ctypes.POINTER(SZ)]),

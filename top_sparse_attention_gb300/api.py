@@ -17,7 +17,8 @@ __all__ = ["dsa_index_score", "dsa_topk", "dsa_topk_noalloc", "dsa_topk_pairs", 
            "dsa_sparse_attn_partial", "dsa_attn_combine", "dsa_sparse_attn", "DsaCall", "dsa_decode", "dsa_prefill",
            "dsa_workspace_size", "dsa_launch_count", "dsa_get_device_error", "ld_scores_for",
            "dsa_quantize_mxfp8", "dsa_quantize_fp8_rows", "dsa_quantize_fp8_tiles",
-           "dsa_block_plan", "BlockPlan", "dsa_rope", "dsa_rope_append", "dsa_tree_attn"]
+           "dsa_block_plan", "BlockPlan", "dsa_rope", "dsa_rope_append", "dsa_tree_attn",
+           "dsa_norm_rope", "dsa_norm_rope_append", "dsa_latent_expand", "dsa_expanded_attn"]
 
 
 # The current stream's handle and the current device without building torch objects (a serving step makes
@@ -510,20 +511,15 @@ def _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axi
     return rot_dim, n_axes, pair_axis, _ROPE_STYLE[style]
 
 
-def dsa_rope(x, pos, inv_freq, *, rot_off=0, rot_dim=None, sections=None, pair_axis=None, style="half",
-             inverse=False, out=None, stream=None) -> torch.Tensor:
-    """Rotary positions on columns [rot_off, rot_off + rot_dim) (default: to the last one) of bf16 x
-    [rows, heads, width] or [rows, width].  pos int32 [rows] or [rows, n_axes]; inv_freq fp32
-    [rot_dim / 2]; with several axes `sections` (pairs per axis, in order) or `pair_axis` (the axis
-    of each pair) says which axis turns a pair.  `out` may be x itself (in place) or any strided
-    tensor of x's shape that does not overlap it; `inverse` turns back (the gradient)."""
-    what = "dsa_rope"
+def _turned(what, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style, out, stream, between, fn, after):
+    """dsa_rope and dsa_norm_rope: `between` makes the arguments in front of the rotation's, `after` those behind its style."""
     dev = _cuda_device(what, x)
     _check(what, dev, "x", x, torch.bfloat16, None, dense=False)
     shape, xs = x.shape, x.stride()
     if len(shape) not in (2, 3) or (shape[-1] > 1 and xs[-1] != 1):
         raise ValueError(f"{what}: x must be [rows, heads, width] or [rows, width] with dense columns")
     rot_dim, n_axes, pair_axis, code = _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style)
+    extra = between(dev, shape[-1])
     if out is None:
         out = _output(_side(stream, dev), shape, torch.bfloat16, dev)
         os = out.stride()
@@ -537,24 +533,19 @@ def dsa_rope(x, pos, inv_freq, *, rot_off=0, rot_dim=None, sections=None, pair_a
     if rows == 0 or heads == 0:
         return out
     xh, oh = (xs[1], os[1]) if heads > 1 else (width, width)
-    _run(what, N.lib.dsa_rope, dev, stream, x.data_ptr(), xs[0], xh, rows, heads, width, int(rot_off), int(rot_dim),
-         pos.data_ptr(), n_axes, pair_axis, inv_freq.data_ptr(), code, int(bool(inverse)), out.data_ptr(), os[0], oh)
+    _run(what, fn, dev, stream, x.data_ptr(), xs[0], xh, rows, heads, width, *extra, int(rot_off), int(rot_dim),
+         pos.data_ptr(), n_axes, pair_axis, inv_freq.data_ptr(), code, *after, out.data_ptr(), os[0], oh)
     return out
 
 
-def dsa_rope_append(x, pos, inv_freq, dst, *, scale=None, dst_rows=None, rot_off, rot_dim=None, sections=None,
-                    pair_axis=None, style="half", stream=None) -> None:
-    """bf16 rows x [rows, width], turned as in dsa_rope, encoded and written to rows dst_rows (int64
-    [rows]; negative: dropped; None: row r) of the cache rows dst [*, >= width]: bf16, or uint8 E4M3
-    codes with `scale` fp32 [*] (per row), fp32 [*, ceil(width / 128)] (per 128 columns) or uint8
-    [*, width / 32] (MXFP8 exponents)."""
-    what = "dsa_rope_append"
+def _appended(what, x, pos, inv_freq, dst, scale, dst_rows, rot_off, rot_dim, sections, pair_axis, style, stream, between, fn):
     dev = _cuda_device(what, x)
     _check(what, dev, "x", x, torch.bfloat16, 2, dense=False)
     (rows, width), (x_row, x_col) = x.shape, x.stride()
     if width > 1 and x_col != 1:
         raise ValueError(f"{what}: x must have dense columns")
     rot_dim, n_axes, pair_axis, code = _rope_args(what, dev, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style)
+    extra = between(dev, width)
     if dst.dtype == torch.bfloat16:
         kind, want = N.DSA_BF16, None
     elif scale is None:
@@ -578,10 +569,109 @@ def dsa_rope_append(x, pos, inv_freq, dst, *, scale=None, dst_rows=None, rot_off
         raise ValueError(f"{what}: dst_rows must have one entry per row of x")
     if rows == 0:
         return
-    _run(what, N.lib.dsa_rope_append, dev, stream, x.data_ptr(), x_row, rows, width, int(rot_off), int(rot_dim),
+    _run(what, fn, dev, stream, x.data_ptr(), x_row, rows, width, *extra, int(rot_off), int(rot_dim),
          pos.data_ptr(), n_axes, pair_axis, inv_freq.data_ptr(), code, kind, dst.data_ptr(),
          (dst_row if n_dst > 1 else width) * (2 if kind == N.DSA_BF16 else 1), n_dst,
          None if kind == N.DSA_BF16 else scale.data_ptr(), _ptr(dst_rows))
+
+
+def _nothing(dev, width):
+    return ()
+
+
+def dsa_rope(x, pos, inv_freq, *, rot_off=0, rot_dim=None, sections=None, pair_axis=None, style="half",
+             inverse=False, out=None, stream=None) -> torch.Tensor:
+    """Rotary positions on columns [rot_off, rot_off + rot_dim) (default: to the last one) of bf16 x
+    [rows, heads, width] or [rows, width].  pos int32 [rows] or [rows, n_axes]; inv_freq fp32
+    [rot_dim / 2]; with several axes `sections` (pairs per axis, in order) or `pair_axis` (the axis
+    of each pair) says which axis turns a pair.  `out` may be x itself (in place) or any strided
+    tensor of x's shape that does not overlap it; `inverse` turns back (the gradient)."""
+    return _turned("dsa_rope", x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style, out, stream, _nothing,
+                   N.lib.dsa_rope, (int(bool(inverse)),))
+
+
+def dsa_rope_append(x, pos, inv_freq, dst, *, scale=None, dst_rows=None, rot_off, rot_dim=None, sections=None,
+                    pair_axis=None, style="half", stream=None) -> None:
+    """bf16 rows x [rows, width], turned as in dsa_rope, encoded and written to rows dst_rows (int64
+    [rows]; negative: dropped; None: row r) of the cache rows dst [*, >= width]: bf16, or uint8 E4M3
+    codes with `scale` fp32 [*] (per row), fp32 [*, ceil(width / 128)] (per 128 columns) or uint8
+    [*, width / 32] (MXFP8 exponents)."""
+    _appended("dsa_rope_append", x, pos, inv_freq, dst, scale, dst_rows, rot_off, rot_dim, sections, pair_axis, style, stream,
+              _nothing, N.lib.dsa_rope_append)
+
+
+_NORM_KIND = {"rms": N.DSA_NORM_RMS, "layer": N.DSA_NORM_LAYER}
+
+
+def _norm(what, norm, weight, bias, eps, norm_off, norm_dim):
+    """Checks the norm and gives the C struct of it as the argument behind the width."""
+    if norm not in _NORM_KIND:
+        raise ValueError(f"{what}: norm must be one of {tuple(_NORM_KIND)}, got {norm!r}")
+
+    def make(dev, width):
+        dim = width - norm_off if norm_dim is None else norm_dim
+        for name, t in (("weight", weight), ("bias", bias)):
+            _check(what, dev, name, t, torch.float32, 1)
+            if t is not None and t.shape[0] != dim:
+                raise ValueError(f"{what}: {name} must have {dim} entries, got {t.shape[0]}")
+        return (ctypes.byref(N.DsaNorm(_NORM_KIND[norm], int(norm_off), int(dim), float(eps), _ptr(weight), _ptr(bias))),)
+
+    return make
+
+
+def dsa_norm_rope(x, pos, inv_freq, *, norm="rms", weight=None, bias=None, eps=1e-6, norm_off=0, norm_dim=None, rot_off=0,
+                  rot_dim=None, sections=None, pair_axis=None, style="half", out=None, stream=None) -> torch.Tensor:
+    """dsa_rope with a norm before it, in one pass and rounded once: columns [norm_off, norm_off + norm_dim) (default:
+    to the last one) of each head become (x - mean) / sqrt(var + eps) * weight + bias (`norm` "layer"), or x / sqrt(mean
+    x^2 + eps) * weight + bias ("rms"); weight and bias fp32 [norm_dim] or None.  Widths up to 1024."""
+    what = "dsa_norm_rope"
+    return _turned(what, x, pos, inv_freq, rot_off, rot_dim, sections, pair_axis, style, out, stream,
+                   _norm(what, norm, weight, bias, eps, norm_off, norm_dim), N.lib.dsa_norm_rope, ())
+
+
+def dsa_norm_rope_append(x, pos, inv_freq, dst, *, norm="rms", weight=None, bias=None, eps=1e-6, norm_off=0, norm_dim=None,
+                         scale=None, dst_rows=None, rot_off, rot_dim=None, sections=None, pair_axis=None, style="half",
+                         stream=None) -> None:
+    """dsa_rope_append with the norm of dsa_norm_rope before it: latent rows (norm_dim=512, rot_off=512) or indexer keys
+    into a cache."""
+    what = "dsa_norm_rope_append"
+    _appended(what, x, pos, inv_freq, dst, scale, dst_rows, rot_off, rot_dim, sections, pair_axis, style, stream,
+              _norm(what, norm, weight, bias, eps, norm_off, norm_dim), N.lib.dsa_norm_rope_append)
+
+
+def _latent_cache(what, dev, a, kv, kv_scale, n_seq, block_table, block_size, L, width=576):
+    """Checks a latent cache (contiguous or paged, any format) and fills its fields of the C struct."""
+    paged = block_table is not None
+    axes = 2 if paged else 3
+    bf16 = kv.dtype == torch.bfloat16
+    _check(what, dev, "kv", kv, torch.bfloat16 if bf16 else torch.uint8, axes, dense=False)
+    shape, strides = kv.shape, kv.stride()
+    if shape[-1] < width or strides[-1] != 1:
+        raise ValueError(f"{what}: kv rows must hold {width} dense columns")
+    a.kv_dtype = N.DSA_BF16
+    if not bf16:
+        if kv_scale is None:
+            raise ValueError(f"{what}: E4M3 rows need their scales")
+        a.kv_dtype = N.DSA_FP8_E4M3_T128 if kv_scale.dim() == axes else N.DSA_FP8_E4M3
+        _check(what, dev, "kv_scale", kv_scale, torch.float32)
+        want = tuple(shape[:-1]) + ((-(-width // 128),) if kv_scale.dim() == axes else ())
+        if tuple(kv_scale.shape) != want:
+            raise ValueError(f"{what}: kv_scale must be {list(want)}, got {tuple(kv_scale.shape)}")
+        a.kv_scale = kv_scale.data_ptr()
+    elem = 2 if bf16 else 1
+    if paged:
+        _check(what, dev, "block_table", block_table, torch.int32, 2)
+        if L is None or block_size <= 0 or block_table.shape[0] != n_seq:
+            raise ValueError(f"{what}: paged caches need L, block_size and one row of block_table per sequence")
+        a.block_table, a.block_size, a.max_blocks = block_table.data_ptr(), int(block_size), block_table.shape[1]
+        a.num_blocks = shape[0] // int(block_size)
+        a.kv_row_stride = strides[0] * elem
+    else:
+        if shape[0] != n_seq or (L is not None and L != shape[1]):
+            raise ValueError(f"{what}: kv must be [{n_seq}, L, {width}], got {tuple(shape)}")
+        L = shape[1]
+        a.kv_row_stride, a.kv_seq_stride = strides[1] * elem, strides[0] * elem
+    a.kv, a.n_seq, a.L = kv.data_ptr(), n_seq, int(L)
 
 
 def dsa_tree_attn(q, kv, n_ctx, *, sm_scale, q_per_seq, n_new=None, tree_mask=None, kv_scale=None, block_table=None,
@@ -605,37 +695,8 @@ def dsa_tree_attn(q, kv, n_ctx, *, sm_scale, q_per_seq, n_new=None, tree_mask=No
         _check(what, dev, "tree_mask", tree_mask, torch.uint32 if tree_mask.dtype == torch.uint32 else torch.int32, 2)
         if tree_mask.shape[0] != T or tree_mask.shape[1] != (q_per_seq + 31) // 32:
             raise ValueError(f"{what}: tree_mask must be [{T}, {(q_per_seq + 31) // 32}], got {tuple(tree_mask.shape)}")
-    paged = block_table is not None
-    axes = 2 if paged else 3
-    bf16 = kv.dtype == torch.bfloat16
-    _check(what, dev, "kv", kv, torch.bfloat16 if bf16 else torch.uint8, axes, dense=False)
-    shape, strides = kv.shape, kv.stride()
-    if shape[-1] < D or strides[-1] != 1:
-        raise ValueError(f"{what}: kv rows must hold {D} dense columns")
     a = N.DsaTreeArgs()
-    a.kv_dtype = N.DSA_BF16
-    if not bf16:
-        if kv_scale is None:
-            raise ValueError(f"{what}: E4M3 rows need their scales")
-        a.kv_dtype = N.DSA_FP8_E4M3_T128 if kv_scale.dim() == axes else N.DSA_FP8_E4M3
-        _check(what, dev, "kv_scale", kv_scale, torch.float32)
-        want = tuple(shape[:-1]) + ((-(-D // 128),) if kv_scale.dim() == axes else ())
-        if tuple(kv_scale.shape) != want:
-            raise ValueError(f"{what}: kv_scale must be {list(want)}, got {tuple(kv_scale.shape)}")
-        a.kv_scale = kv_scale.data_ptr()
-    elem = 2 if bf16 else 1
-    if paged:
-        _check(what, dev, "block_table", block_table, torch.int32, 2)
-        if L is None or block_size <= 0 or block_table.shape[0] != n_seq:
-            raise ValueError(f"{what}: paged caches need L, block_size and one row of block_table per sequence")
-        a.block_table, a.block_size, a.max_blocks = block_table.data_ptr(), int(block_size), block_table.shape[1]
-        a.num_blocks = shape[0] // int(block_size)
-        a.kv_row_stride = strides[0] * elem
-    else:
-        if shape[0] != n_seq or (L is not None and L != shape[1]):
-            raise ValueError(f"{what}: kv must be [{n_seq}, L, {D}], got {tuple(shape)}")
-        L = shape[1]
-        a.kv_row_stride, a.kv_seq_stride = strides[1] * elem, strides[0] * elem
+    _latent_cache(what, dev, a, kv, kv_scale, n_seq, block_table, block_size, L, D)
     side = _side(stream, dev)
     if out is None:
         out = _output(side, (T, H, 512), torch.bfloat16, dev)
@@ -649,9 +710,9 @@ def dsa_tree_attn(q, kv, n_ctx, *, sm_scale, q_per_seq, n_new=None, tree_mask=No
         _check(what, dev, "lse", lse, torch.float32, 2)
         if tuple(lse.shape) != (T, H):
             raise ValueError(f"{what}: lse must be [{T}, {H}]")
-    a.n_seq, a.q_per_seq, a.L, a.H, a.D_qk, a.D_v, a.sm_scale = n_seq, int(q_per_seq), int(L), H, D, 512, float(sm_scale)
+    a.q_per_seq, a.H, a.D_qk, a.D_v, a.sm_scale = int(q_per_seq), H, D, 512, float(sm_scale)
     a.n_ctx, a.n_new, a.tree_mask = n_ctx.data_ptr(), _ptr(n_new), _ptr(tree_mask)
-    a.q, a.kv, a.out, a.lse = q.data_ptr(), kv.data_ptr(), out.data_ptr(), lse.data_ptr()
+    a.q, a.out, a.lse = q.data_ptr(), out.data_ptr(), lse.data_ptr()
     need = ctypes.c_size_t(0)
     N.check(N.lib.dsa_tree_attn_workspace_size(ctypes.byref(a), ctypes.byref(need)), what)
     if ws is None:
@@ -659,6 +720,108 @@ def dsa_tree_attn(q, kv, n_ctx, *, sm_scale, q_per_seq, n_new=None, tree_mask=No
     else:
         _check(what, dev, "ws", ws, torch.uint8, 1)
     _run(what, N.lib.dsa_tree_attn, dev, stream, ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel())
+    return out, lse
+
+
+def dsa_latent_expand(kv, w, kv_start, *, rows=None, kv_scale=None, block_table=None, block_size=0, L=None, out=None, rope_out=None,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Cached latent rows expanded to every head's key and value (see dsa.h): (out bf16 [rows, H, 256], 128 key columns
+    then 128 value columns, and rope_out bf16 [rows, 64]).  kv and kv_scale as in dsa_tree_attn; w bf16 [H, 256, 512];
+    kv_start int32 [n_seq + 1]: position j of sequence s becomes row kv_start[s] + j.  `rows` is the outputs' number of
+    rows (needed where neither is given); with `block_table` L defaults to all that a row of it holds."""
+    what = "dsa_latent_expand"
+    dev = _cuda_device(what, w)
+    _check(what, dev, "w", w, torch.bfloat16, 3)
+    _check(what, dev, "kv_start", kv_start, torch.int32, 1)
+    H = w.shape[0]
+    if tuple(w.shape[1:]) != (256, 512):
+        raise ValueError(f"{what}: w must be [H, 256, 512], got {tuple(w.shape)}")
+    if kv_start.shape[0] < 1:
+        raise ValueError(f"{what}: kv_start must have one entry more than there are sequences")
+    n_seq = kv_start.shape[0] - 1
+    if rows is None:
+        rows = out.shape[0] if out is not None else rope_out.shape[0] if rope_out is not None else None
+        if rows is None:
+            raise ValueError(f"{what}: the outputs' number of rows is needed (rows)")
+    if block_table is not None and L is None:
+        L = block_table.shape[-1] * block_size
+    a = N.DsaExpandArgs()
+    _latent_cache(what, dev, a, kv, kv_scale, n_seq, block_table, block_size, L)
+    side = _side(stream, dev)
+    given = []
+    for name, t, shape in (("out", out, (rows, H, 256)), ("rope_out", rope_out, (rows, 64))):
+        if t is None:
+            t = _output(side, shape, torch.bfloat16, dev)
+        else:
+            _check(what, dev, name, t, torch.bfloat16, len(shape))
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{what}: {name} must be {list(shape)}, got {tuple(t.shape)}")
+        given.append(t)
+    out, rope_out = given
+    a.rows, a.H, a.kv_start, a.w = int(rows), H, kv_start.data_ptr(), w.data_ptr()
+    a.out, a.rope_out = out.data_ptr(), rope_out.data_ptr()
+    if rows > 0 and H > 0:
+        _run(what, N.lib.dsa_latent_expand, dev, stream, ctypes.byref(a))
+    return out, rope_out
+
+
+def dsa_expanded_attn(q, k, k_rope, v, q_start, kv_start, *, sm_scale, causal=True, max_len=None, out=None, lse=None, ws=None,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of packed ragged prompts, or chunks of them, over expanded keys and values (see dsa.h): (out [T, H, 128]
+    bf16, lse [T, H] fp32).  q bf16 [T, H, 192]; k, v bf16 [N, H, 128] with dense columns (views of dsa_latent_expand's
+    output); k_rope bf16 [N, 64]; q_start, kv_start int32 [n_seq + 1].  Causal: a sequence's queries are its last
+    positions.  `max_len` (positions of the longest sequence at most; None: N) sizes the workspace; `ws` (uint8) is scratch
+    that later calls on the same stream may reuse."""
+    what = "dsa_expanded_attn"
+    dev = _cuda_device(what, q)
+    _check(what, dev, "q", q, torch.bfloat16, 3)
+    T, H, D = q.shape
+    if D != 192:
+        raise ValueError(f"{what}: q must be [T, H, 192], got {tuple(q.shape)}")
+    rows = k.shape[0]
+    _check(what, dev, "k_rope", k_rope, torch.bfloat16, 2)
+    for name, t in (("k", k), ("v", v)):
+        _check(what, dev, name, t, torch.bfloat16, 3, dense=False)
+        if tuple(t.shape) != (rows, H, 128) or t.stride(2) != 1:
+            raise ValueError(f"{what}: {name} must be [N, {H}, 128] with dense columns, got {tuple(t.shape)}")
+    if tuple(k_rope.shape) != (rows, 64):
+        raise ValueError(f"{what}: k_rope must be [{rows}, 64], got {tuple(k_rope.shape)}")
+    _check(what, dev, "q_start", q_start, torch.int32, 1)
+    _check(what, dev, "kv_start", kv_start, torch.int32, 1)
+    if q_start.shape[0] < 1 or q_start.shape != kv_start.shape:
+        raise ValueError(f"{what}: q_start and kv_start must have one entry more than there are sequences")
+    side = _side(stream, dev)
+    if out is None:
+        out = _output(side, (T, H, 128), torch.bfloat16, dev)
+    else:
+        _check(what, dev, "out", out, torch.bfloat16, 3)
+        if tuple(out.shape) != (T, H, 128):
+            raise ValueError(f"{what}: out must be [{T}, {H}, 128]")
+    if lse is None:
+        lse = _output(side, (T, H), torch.float32, dev)
+    else:
+        _check(what, dev, "lse", lse, torch.float32, 2)
+        if tuple(lse.shape) != (T, H):
+            raise ValueError(f"{what}: lse must be [{T}, {H}]")
+    if T == 0 or H == 0:
+        return out, lse
+    a = N.DsaExpandedAttnArgs()
+    a.n_seq, a.T, a.N, a.H = q_start.shape[0] - 1, T, rows, H
+    a.max_len, a.causal, a.sm_scale = 0 if max_len is None else int(max_len), int(bool(causal)), float(sm_scale)
+    a.q_start, a.kv_start = q_start.data_ptr(), kv_start.data_ptr()
+    a.q, a.k, a.k_rope, a.v = q.data_ptr(), k.data_ptr(), k_rope.data_ptr(), v.data_ptr()
+    for name, t in (("k", k), ("v", v)):  # (an axis of one has any stride)
+        head = t.stride(1) if H > 1 else 128
+        setattr(a, name + "_head_stride", head)
+        setattr(a, name + "_row_stride", t.stride(0) if rows > 1 else max(128, head * H))
+    a.out, a.lse = out.data_ptr(), lse.data_ptr()
+    need = ctypes.c_size_t(0)
+    N.check(N.lib.dsa_expanded_attn_workspace_size(ctypes.byref(a), ctypes.byref(need)), what)
+    if ws is None:
+        ws = _scratch(side, need.value, torch.uint8, dev) if need.value else None
+    else:
+        _check(what, dev, "ws", ws, torch.uint8, 1)
+    _run(what, N.lib.dsa_expanded_attn, dev, stream, ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel())
     return out, lse
 
 

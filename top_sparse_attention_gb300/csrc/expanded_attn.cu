@@ -1,0 +1,737 @@
+// Attention of prompts, or chunks of them, over expanded keys and values (dsa_expanded_attn): head h of query i of sequence s,
+// with m queries over n positions,
+//   logit[p] = sm_scale (q[:128] . k[p, h] + q[128:] . k_rope[p]),  out = sum_p softmax(logit)[p] v[p, h]
+// over the positions p <= n - m + i (causal) or all n.  Sequences are packed, one behind another.
+//
+// A CTA takes 256 queries of a head, two tiles of 128, and walks tiles of 128 positions, each loaded once for both.  Per tile
+// of queries and positions:
+//   * S[128 x 128] = Q K^T: 12 steps of K = 16, both operands in shared memory (the rotary columns are a box of K of their
+//     own, that all heads read);
+//   * one pass over the positions keeps a reference maximum m and a sum l per row as in tree_attn.cu: m moves only where
+//     a tile's maximum exceeds it by more than 2^8, so that O is rescaled rarely;
+//   * P, bf16, takes the place of S in tensor memory, and O[128 x 128] += P V: 8 steps, A in tensor memory, V MN-major.
+// Tensor memory: S and O of both tiles, 4 x 128 columns.  The two tiles take turns: while four warps take the softmax of one
+// (a thread a row), the tensor cores multiply for the other: O += P V of the last positions, then S of the next ones.
+// The instructions of one thread execute in order, so that S may follow the P V that reads P in the same columns, and a
+// finished S means that the P V before it has finished.
+//
+// Shared memory: both tiles of Q (96 KB) and a ring of eight boxes of 64 columns x 128 positions (three of K, two of V per
+// tile), whose boxes are refilled as soon as their product is done.
+//
+// Positions that some row of a tile of positions does not see: their logits become -inf; what lies behind the sequence's
+// end is cleared from V, and infinities and NaN at positions that only some rows see too (0 * inf is NaN), which are
+// added afterwards for the rows that see them.
+//
+// Work: blocks of 256 queries x chunks of `chunk` tiles of positions, longest first (plan_kernel: the lengths are on the
+// device), each for every head, dealt to the CTAs back and forth.  Blocks of more than one chunk leave fp32 partial
+// results, merged by merge_kernel.  Chunks of 512 tiles at most: the tensor cores truncate their sums, and O would lose
+// 2^-24 of itself per step (0.04 % over 65536 positions).
+//
+// Bound: tensor cores, 12 x 64 + 8 x 64 cycles per tile of 128 x 128.
+#include <limits.h>
+#include <string.h>
+
+#include <initializer_list>
+
+#include "tc_common.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kNope = 128, kRope = 64, kDv = 128;
+constexpr int kTile = 128;                  // rows of a tile of queries, positions of a tile of them
+constexpr int kBlock = 2 * kTile;
+constexpr int kBox = kTile * 128;           // 64 columns of 128 rows
+constexpr int kRing = 8;
+constexpr int kOffRing = 6 * kBox;          // two tiles of Q first
+constexpr int kThreads = 384;
+constexpr float kLazy = 8.f;                // log2 growth of a row's maximum that is left unscaled
+constexpr int kSms = 152;
+constexpr int kMaxChunk = 512, kMinChunk = 4;  // tiles
+constexpr int kMaxSeq = 4096;
+constexpr uint32_t kColS = 0, kColO = 256;
+
+struct ExpandedAttnParams {
+  const int32_t* q_start;  // [n_seq + 1]
+  const int32_t* kv_start; // [n_seq + 1]
+  int n_seq, T, N, H;      // rows of q, rows of k and v
+  int max_len;             // positions of the longest sequence, at most
+  bool causal;
+  float scale_log2;        // sm_scale * log2(e)
+  const __nv_bfloat16* v;  // (element strides)
+  int64_t v_row_stride, v_head_stride;
+  __nv_bfloat16* out;      // [T, H, 128]
+  float* lse;              // [T, H] or null
+  int chunk;               // tiles of 128 positions
+  int max_work;
+  int* n_work;             // workspace: the list of work, partial results [chunks][T][H]
+  int4* work;
+  float2* part_ml;
+  float* part_o;
+  int* err;                // device error word
+};
+
+struct Aux {
+  uint64_t q_full[2], q_empty[2], full[kRing], empty[kRing], s_full[2], p_full[2], o_done[2], o_free[2], drain;
+  uint32_t tmem;
+  int abort;
+  int not_finite;  // an infinity or NaN was cleared from V
+};
+constexpr int kOffAux = kOffRing + kRing * kBox;
+constexpr int kSmem = kOffAux + (int)sizeof(Aux) + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+struct Work {
+  int seq, q0, t0, t1;  // queries q0 ... of the sequence, tiles [t0, t1) of positions
+};
+
+struct Facts {
+  int q_row, m;   // the sequence's first row of q, its queries
+  int k_row, n;   // its first row of k and v, its positions
+  int nrows;      // queries of the block
+  int first, step;  // row i of the block sees first + i * step positions (clamped to [0, n])
+};
+
+__device__ __forceinline__ void seq_facts(const ExpandedAttnParams& p, int seq, Facts& f) {
+  f.q_row = min(max(p.q_start[seq], 0), p.T);
+  f.m = min(max(p.q_start[seq + 1], f.q_row), p.T) - f.q_row;
+  f.k_row = min(max(p.kv_start[seq], 0), p.N);
+  f.n = min(min(max(p.kv_start[seq + 1], f.k_row), p.N) - f.k_row, p.max_len);
+}
+__device__ __forceinline__ Facts block_facts(const ExpandedAttnParams& p, int seq, int q0) {
+  Facts f;
+  seq_facts(p, seq, f);
+  f.nrows = min(kBlock, f.m - q0);
+  f.step = p.causal ? 1 : 0;
+  f.first = p.causal ? f.n - f.m + q0 + 1 : f.n;
+  return f;
+}
+__device__ __forceinline__ int sees(const Facts& f, int i) { return min(max(f.first + i * f.step, 0), f.n); }
+__device__ __forceinline__ int tiles_of(int positions) { return (positions + kTile - 1) / kTile; }
+// Tiles of positions of a block: those that its last query sees.
+__device__ __forceinline__ int block_tiles(const Facts& f) { return tiles_of(sees(f, f.nrows - 1)); }
+// Tiles of [w.t0, w.t1) that tile t of the queries takes.
+__device__ __forceinline__ int tiles_for(const Facts& f, const Work& w, int t) {
+  if (f.nrows <= t * kTile) return 0;
+  return max(min(w.t1, tiles_of(sees(f, min(f.nrows, (t + 1) * kTile) - 1))) - w.t0, 0);
+}
+
+// ---------------------------------------------------------------------------------------------
+// the list of work: blocks and their chunks, the longest first (a counting sort by tiles; which of two of equal length
+// comes first does not matter to the results)
+
+__global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) {
+  __shared__ int base[kMaxSeq + 1];          // blocks before each sequence
+  __shared__ int place[kMaxChunk + 1];       // by tiles: how many, then where the next goes
+  __shared__ int warp_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int run = 0;
+  for (int s0 = 0; s0 < p.n_seq; s0 += 1024) {  // running sums of the sequences' blocks
+    const int s = s0 + tid;
+    Facts f;
+    int c = 0;
+    if (s < p.n_seq) {
+      seq_facts(p, s, f);
+      c = (f.m + kBlock - 1) / kBlock;
+      if (p.kv_start[s + 1] - p.kv_start[s] > f.n) record_error(p.err, DSA_DEVERR_INDEX_RANGE);
+    }
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+      int v = warp_sum[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      warp_sum[lane] = v;
+    }
+    __syncthreads();
+    if (s < p.n_seq) base[s] = run + incl - c + (warp ? warp_sum[warp - 1] : 0);
+    run += warp_sum[31];
+    __syncthreads();
+  }
+  if (tid == 0) base[p.n_seq] = run;
+  for (int i = tid; i <= kMaxChunk; i += 1024) place[i] = 0;
+  __syncthreads();
+  // pass 0 counts, pass 1 places
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int b = tid; b < run; b += 1024) {
+      int lo = 0, hi = p.n_seq - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (base[mid] <= b) lo = mid;
+        else hi = mid - 1;
+      }
+      const int q0 = (b - base[lo]) * kBlock;
+      const int n = block_tiles(block_facts(p, lo, q0));
+      int t0 = 0;
+      do {
+        const int t1 = min(t0 + p.chunk, n);
+        const int at = atomicAdd(&place[t1 - t0], 1);
+        if (pass && at < p.max_work) p.work[at] = make_int4(lo, q0, t0, t1);
+        t0 = t1;
+      } while (t0 < n);
+    }
+    __syncthreads();
+    if (pass == 0) {
+      if (tid == 0) {
+        int sum = 0;
+        for (int i = kMaxChunk; i >= 0; --i) {
+          const int c = place[i];
+          place[i] = sum;
+          sum += c;
+        }
+        *p.n_work = min(sum, p.max_work);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ bool get_work(const ExpandedAttnParams& p, int64_t n_items, int r, Work& w, int& head, Facts& f) {
+  const int g = (int)gridDim.x, c = (int)blockIdx.x;
+  const int64_t i = (int64_t)r * g + (r & 1 ? g - 1 - c : c);
+  if (i >= n_items) return false;
+  const int4 v = p.work[i / p.H];
+  head = (int)(i % p.H);
+  w.seq = v.x, w.q0 = v.y, w.t0 = v.z, w.t1 = v.w;
+  f = block_facts(p, w.seq, w.q0);
+  return true;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    expanded_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v,
+                         const ExpandedAttnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = smem + kOffRing;
+  Aux* a = reinterpret_cast<Aux*>(smem + kOffAux);
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
+  int* err = p.err;
+
+  if (warp == 0) {
+    tmem_alloc(&a->tmem, 512);
+    tmem_relinquish();
+  }
+  if (tid == 32) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&a->q_full[i], 1), mbar_init(&a->q_empty[i], 1);
+      mbar_init(&a->s_full[i], 1), mbar_init(&a->p_full[i], 4);
+      mbar_init(&a->o_done[i], 1), mbar_init(&a->o_free[i], 4);
+    }
+    for (int i = 0; i < kRing; ++i) mbar_init(&a->full[i], 1), mbar_init(&a->empty[i], 1);
+    mbar_init(&a->drain, 1);
+    a->abort = 0;
+    a->not_finite = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = a->tmem;
+  pdl_wait();  // the plan
+  const int64_t n_items = (int64_t)*p.n_work * p.H;
+
+  Work w;
+  Facts f;
+  int head;
+  if (warp < 4) {
+    if (warp == 0) {
+      // ---- producer
+      if (lane == 0) {
+        prefetch_tmap(&tm_q), prefetch_tmap(&tm_k), prefetch_tmap(&tm_r), prefetch_tmap(&tm_v);
+        int s = 0, ph = 0, uses[2] = {0, 0};
+        bool ok = true;
+        auto box = [&](const CUtensorMap* tm, int x, int y, int z, bool flat) {
+          ok = ok && wait_ahead(a, &a->empty[s], ph ^ 1, err);
+          if (!ok) return;
+          mbar_arrive_expect_tx(&a->full[s], kBox);
+          if (flat) tma_load_2d(ring + s * kBox, tm, &a->full[s], x, z);
+          else tma_load_3d(ring + s * kBox, tm, &a->full[s], x, y, z);
+          if (++s == kRing) s = 0, ph ^= 1;
+        };
+        auto query = [&](int t) {
+          ok = ok && wait_ahead(a, &a->q_empty[t], (uses[t] & 1) ^ 1, err);
+          if (!ok) return;
+          ++uses[t];
+          mbar_arrive_expect_tx(&a->q_full[t], 3 * kBox);
+          for (int b = 0; b < 3; ++b) tma_load_3d(smem + (3 * t + b) * kBox, &tm_q, &a->q_full[t], 64 * b, head, f.q_row + w.q0 + kTile * t);
+        };
+        for (int r = 0; ok && get_work(p, n_items, r, w, head, f); ++r) {
+          const int n0 = tiles_for(f, w, 0), n1 = tiles_for(f, w, 1), n = max(n0, n1);
+          if (n0) query(0);
+          for (int j = 0; ok && j < n; ++j) {
+            const int row = f.k_row + (w.t0 + j) * kTile;
+            box(&tm_k, 0, head, row, false);
+            box(&tm_k, 64, head, row, false);
+            box(&tm_r, 0, 0, row, true);
+            if (j == 0 && n1) query(1);
+            box(&tm_v, 0, head, row, false);
+            box(&tm_v, 64, head, row, false);
+          }
+        }
+        if (*reinterpret_cast<volatile int*>(&a->abort)) {  // wind down: the copies in flight land first
+          for (int i = 0; i < kRing; ++i) mbar_wait(&a->full[i], i < s ? ph : ph ^ 1, err);
+          for (int t = 0; t < 2; ++t) mbar_wait(&a->q_full[t], (uses[t] & 1) ^ 1, err);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---- MMA issuer
+      constexpr uint32_t idesc_qk = make_idesc(1, 1, kTile, kTile);
+      constexpr uint32_t idesc_pv = make_idesc(1, 1, kTile, 64) | (1u << 16);  // B (values) MN-major
+      const uint32_t base = (uint32_t)uniform((int)tmem);
+      const uint32_t q_lo = kmajor_lo(smem_u32(smem)), k_lo = kmajor_lo(smem_u32(ring)), v_lo = mnmajor_lo(smem_u32(ring), kBox);
+      uint32_t at = 0;  // boxes before the tile of positions in hand
+      int used[2] = {0, 0}, soft[2] = {0, 0};  // items and softmax tiles of each tile of queries
+      bool ok = true;
+      auto all = [&](uint64_t* bar, uint32_t parity) { ok = __all_sync(0xffffffffu, wait(a, bar, parity, err)) && ok; };
+      auto boxes_full = [&](uint32_t first, int n) {  // one lane per barrier
+        const uint32_t b = first + (lane < n ? lane : 0);
+        all(&a->full[b % kRing], (b / kRing) & 1);
+      };
+      auto release = [&](uint32_t first, int n) {
+        if (elect_one())
+          for (int i = 0; i < n; ++i) tc_commit(&a->empty[(first + i) % kRing]);
+        __syncwarp();
+      };
+      for (int r = 0; ok && uniform(get_work(p, n_items, r, w, head, f)); ++r) {
+        const int n0 = uniform(tiles_for(f, w, 0)), n1 = uniform(tiles_for(f, w, 1)), n = max(n0, n1);
+        auto qk = [&](int t, int j) {  // S of tile t and positions j
+          const int nt = t ? n1 : n0;
+          const uint32_t kb = at + 5 * j;
+          boxes_full(kb, 3);
+          if (j == 0) all(&a->q_full[t], used[t] & 1);
+          if (!ok) return;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int b = 0; b < 3; ++b) {
+              const uint32_t B = k_lo + ((kb + b) % kRing) * (kBox >> 4), A = q_lo + (3 * t + b) * (kBox >> 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mma_ss(base + kColS + kTile * t, A + 2 * i, B + 2 * i, idesc_qk, b || i ? 1u : 0u);
+            }
+            tc_commit(&a->s_full[t]);
+            if (j == nt - 1) tc_commit(&a->q_empty[t]);
+          }
+          __syncwarp();
+        };
+        auto pv = [&](int t, int j) {
+          const int nt = t ? n1 : n0;
+          const uint32_t vb = at + 5 * j + 3;
+          boxes_full(vb, 2);
+          all(&a->p_full[t], soft[t] & 1);
+          if (j == 0) all(&a->o_free[t], (used[t] & 1) ^ 1);
+          if (!ok) return;
+          ++soft[t];
+          tc_fence_after();
+          if (elect_one()) {
+            // value columns 0 .. 63 and 64 .. 127 are two boxes, which need not follow each other in the ring
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const uint32_t B = v_lo + ((vb + b) % kRing) * (kBox >> 4);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                mma_ts(base + kColO + kTile * t + 64 * b, base + kColS + kTile * t + 8 * i, B + i * (2048 >> 4), idesc_pv, j || i ? 1u : 0u);
+            }
+            if (j == nt - 1) tc_commit(&a->o_done[t]);
+          }
+          __syncwarp();
+        };
+        if (n0) qk(0, 0);
+        if (ok && n1) qk(1, 0);
+        if (ok && n) release(at, 3);
+        for (int j = 0; ok && j < n; ++j) {
+          if (j < n0) pv(0, j);
+          if (ok && j + 1 < n0) qk(0, j + 1);
+          if (ok && j < n1) pv(1, j);
+          if (ok) release(at + 5 * j + 3, 2);
+          if (ok && j + 1 < n1) qk(1, j + 1);
+          if (ok && j + 1 < n) release(at + 5 * (j + 1), 3);
+        }
+        at += 5 * n;
+        used[0] += n0 > 0, used[1] += n1 > 0;
+      }
+      if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&a->abort))) {  // wind down: what was issued ends first
+        if (elect_one()) tc_commit(&a->drain);
+        __syncwarp();
+        mbar_wait(&a->drain, 0, err);
+      }
+    }
+  } else {
+    // ---- softmax: four warps for each tile of queries, a thread a row
+    const int t = (warp >> 2) - 1, quarter = warp & 3, row = 32 * quarter + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
+    const uint32_t col_s = lane_base + kColS + kTile * t, col_o = lane_base + kColO + kTile * t;
+    uint32_t at = 0;
+    int soft = 0, used = 0;
+    bool ok = true;
+    for (int r = 0; get_work(p, n_items, r, w, head, f); ++r) {
+      const int n0 = tiles_for(f, w, 0), n1 = tiles_for(f, w, 1), n = t ? n1 : n0;
+      const int i = kTile * t + row;                             // row of the block
+      const int see = i < f.nrows ? sees(f, i) : 0;              // positions that it sees
+      const int least = sees(f, kTile * t);                      // positions that every row of this tile sees
+      const int64_t out_row = (int64_t)(f.q_row + w.q0 + i) * p.H + head;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++soft) {
+        const int pos = (w.t0 + j) * kTile;
+        const bool edge = pos + kTile > least;
+        if (edge && (t == 0 || j >= n0)) {
+          // a thread a position: its values, where some row does not see it (the tile of later queries finds them so)
+          const uint32_t vb = at + 5 * j + 3;
+          ok = wait(a, &a->full[vb % kRing], (vb / kRing) & 1, err) && ok;
+          ok = wait(a, &a->full[(vb + 1) % kRing], ((vb + 1) / kRing) & 1, err) && ok;
+          const bool behind = pos + row >= f.n;
+          if (ok && pos + row >= least) {
+            bool found = false;
+#pragma unroll 1
+            for (int c = 0; c < 16; ++c) {
+              uint4* chunk = reinterpret_cast<uint4*>(ring + ((vb + (c >> 3)) % kRing) * kBox + row * 128 + (((c ^ row) & 7) << 4));
+              uint4 v = make_uint4(0u, 0u, 0u, 0u);
+              bool bad = behind;
+              if (!behind) {
+                v = *chunk;
+                uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  if ((u[q] & 0x7F80u) == 0x7F80u) u[q] &= 0xFFFF0000u, bad = true;
+                  if ((u[q] & 0x7F800000u) == 0x7F800000u) u[q] &= 0xFFFFu, bad = true;
+                }
+                v = make_uint4(u[0], u[1], u[2], u[3]);
+                found |= bad;
+              }
+              if (bad) *chunk = v;
+            }
+            if (found) *reinterpret_cast<volatile int*>(&a->not_finite) = 1;
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+        }
+        ok = wait(a, &a->s_full[t], soft & 1, err) && ok;
+        tc_fence_after();
+        const int mine = see - pos;  // positions of the tile that this row sees
+        // S is read twice, for the maximum and for the weights: 128 values at once do not fit the registers
+        auto logits = [&](int c, float (&x)[32]) {
+          tmem_ld_sync(col_s + c, x);
+          if (edge) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = c + k < mine ? x[k] : -INFINITY;
+          }
+        };
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) {
+          float x[32];
+          logits(c, x);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], x[k]);
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        if (__any_sync(0xffffffffu, top > m + kLazy)) {
+          float g = 1.f;
+          if (top > m + kLazy) {  // (m = -inf: nothing summed yet, the factor is 0)
+            g = ex2(m - top);
+            m = top;
+            l *= g;
+          }
+          if (j > 0) {
+#pragma unroll 1
+            for (int c = 0; c < kDv; c += 16) {
+              float o[16];
+              tmem_ld_sync(col_o + c, o);
+              uint32_t v[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(o[k] * g);
+              tmem_st16(col_o + c, v);
+            }
+          }
+        }
+        const float mu = m == -INFINITY ? 0.f : -m;
+        const float2 scale = make_float2(p.scale_log2, p.scale_log2), minus = make_float2(mu, mu);
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) {
+          float x[32];
+          logits(c, x);
+          uint32_t v[16];
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float2 y = ffma2(make_float2(x[k], x[k + 1]), scale, minus);
+            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+            sum = add2(sum, e);
+            v[k >> 1] = pack_bf16(e.x, e.y);
+          }
+          tmem_st16(col_s + c / 2, v);
+        }
+        l += sum.x + sum.y;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(&a->p_full[t]);
+      }
+      at += 5 * max(n0, n1);
+      // ---- the rows' results
+      const int chunks = tiles_of(sees(f, f.nrows - 1)) > p.chunk ? 2 : 1;  // (more than one)
+      const bool live = i < f.nrows;
+      if (n > 0) {
+        ok = wait(a, &a->o_done[t], used & 1, err) && ok;
+        tc_fence_after();
+        ++used;
+      }
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      const int part = w.t0 / p.chunk;
+      if (live) {
+        if (chunks > 1) p.part_ml[(int64_t)part * p.T * p.H + out_row] = make_float2(m, l);
+        else if (p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
+      // (from the first tile of positions that was looked through: of the first queries' where they are multiplied with it)
+      const int cleared = sees(f, 0) / kTile * kTile;
+      const bool odd = n > 0 && *reinterpret_cast<volatile int*>(&a->not_finite);
+#pragma unroll 1
+      for (int c = 0; c < kDv; c += 32) {
+        float o[32];
+        if (n > 0) {
+          tmem_ld_sync(col_o + c, o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+        }
+        if (odd && live) {  // what was cleared from V, for the rows that see it (rows before it never read it)
+          const int upto = min(see, (w.t0 + n) * kTile);
+          for (int q = max(cleared, w.t0 * kTile); q < upto; ++q) {
+            const __nv_bfloat16* v = p.v + (int64_t)(f.k_row + q) * p.v_row_stride + head * p.v_head_stride + c;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float y = __bfloat162float(v[k]);
+              if (!(fabsf(y) < INFINITY)) o[k] += y;
+            }
+          }
+        }
+        if (!live) {
+        } else if (chunks > 1) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + ((int64_t)part * p.T * p.H + out_row) * kDv + c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * kDv + c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = pack_bf16(o[8 * k + 2 * q] * inv, o[8 * k + 2 * q + 1] * inv);
+            dst[k] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (n > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(&a->o_free[t]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merges the chunks of the rows that have more than one: out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.  32
+// threads a row and head, four columns each.
+__global__ void __launch_bounds__(256) merge_kernel(const ExpandedAttnParams p) {
+  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), rows = (int64_t)p.T * p.H;
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  if (at >= rows) return;
+  const int t = (int)(at / p.H);
+  if (t < p.q_start[0] || t >= p.q_start[p.n_seq]) return;
+  int lo = 0, hi = p.n_seq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.q_start[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  Facts f;
+  seq_facts(p, lo, f);
+  const int i = t - f.q_row;
+  if (i < 0 || i >= f.m) return;
+  f = block_facts(p, lo, i / kBlock * kBlock);
+  const int chunks = (block_tiles(f) + p.chunk - 1) / p.chunk;
+  if (chunks <= 1) return;  // written by the attention kernel
+  float M = -INFINITY;
+  for (int c = 0; c < chunks; ++c) M = fmaxf(M, p.part_ml[c * rows + at].x);
+  const float mu = M == -INFINITY ? 0.f : M;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < chunks; ++c) {
+    const float2 ml = p.part_ml[c * rows + at];
+    if (ml.y == 0.f) continue;  // the row saw nothing there
+    const float g = exp2f(ml.x - mu);
+    const float4 v = reinterpret_cast<const float4*>(p.part_o + (c * rows + at) * kDv)[lane];
+    l = fmaf(g, ml.y, l);
+    o.x = fmaf(g, v.x, o.x), o.y = fmaf(g, v.y, o.y), o.z = fmaf(g, v.z, o.z), o.w = fmaf(g, v.w, o.w);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  reinterpret_cast<uint2*>(p.out + at * kDv)[lane] = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+}
+
+int blocks_of(const ExpandedAttnParams& p) {  // at most
+  const int64_t b = p.n_seq == 1 ? (p.T + kBlock - 1) / kBlock : (int64_t)p.T / kBlock + p.n_seq;
+  return (int)(b < p.T ? b : p.T);
+}
+int longest(const ExpandedAttnParams& p) { return (int)(((int64_t)(p.max_len < p.N ? p.max_len : p.N) + kTile - 1) / kTile); }
+int parts_of(const ExpandedAttnParams& p) { return longest(p) > p.chunk ? (longest(p) + p.chunk - 1) / p.chunk : 1; }
+
+// Tiles of positions of a chunk: one chunk per block where the blocks of all heads fill the SMs, else as many as
+// make two rounds of them, by the sequences' mean length.
+constexpr int64_t kMostPartial = 512ll << 20;
+int chunk_of(ExpandedAttnParams p) {
+  const int64_t items = (int64_t)blocks_of(p) * p.H;
+  const int mean = (int)(((int64_t)p.N + (int64_t)p.n_seq * kTile - 1) / ((int64_t)p.n_seq * kTile));
+  const int64_t splits = (2 * kSms) / (items > 0 ? items : 1);
+  p.chunk = kMaxChunk;
+  if (splits > 1) {
+    const int64_t c = ((int64_t)mean + splits - 1) / splits;
+    p.chunk = (int)(c < kMinChunk ? kMinChunk : c > kMaxChunk ? kMaxChunk : c);
+    while (p.chunk < kMaxChunk && (int64_t)parts_of(p) * p.T * p.H * (kDv + 2) * 4 > kMostPartial) p.chunk = p.chunk * 2 < kMaxChunk ? p.chunk * 2 : kMaxChunk;
+  }
+  return p.chunk;
+}
+
+struct Layout {
+  size_t work, part_ml, part_o, total;
+  int parts;
+  int64_t max_work;
+};
+Layout layout_of(const ExpandedAttnParams& p) {
+  Layout l;
+  l.parts = parts_of(p);
+  l.max_work = (int64_t)blocks_of(p) * l.parts;
+  const int64_t rows = l.parts > 1 ? (int64_t)l.parts * p.T * p.H : 0;
+  l.work = 256;  // the count first
+  l.part_ml = l.work + align_up((size_t)l.max_work * sizeof(int4), 256);
+  l.part_o = l.part_ml + align_up((size_t)rows * sizeof(float2), 256);
+  l.total = l.part_o + (size_t)rows * kDv * sizeof(float);
+  return l;
+}
+
+bool map_of(CUtensorMap* tm, const void* base, int cols, int heads, int rows, int64_t head_stride, int64_t row_stride) {
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)row_stride * 2};
+  const cuuint32_t box[3] = {64, 1, kTile};
+  memset(tm, 0, sizeof(*tm));
+  return encode_tensor_map(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ==
+         CUDA_SUCCESS;
+}
+
+cudaError_t launch(ExpandedAttnParams p, const dsa_expanded_attn_args& a, void* ws, cudaStream_t stream) {
+  const Layout l = layout_of(p);
+  uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+  p.n_work = reinterpret_cast<int*>(base);
+  p.work = reinterpret_cast<int4*>(base + l.work);
+  p.part_ml = reinterpret_cast<float2*>(base + l.part_ml);
+  p.part_o = reinterpret_cast<float*>(base + l.part_o);
+  p.max_work = (int)l.max_work;
+  CUtensorMap tq, tk, tr, tv;
+  // (without positions nothing of k and v is loaded: their maps are q's)
+  const bool any = p.N > 0;
+  const int64_t q_row = (int64_t)p.H * (kNope + kRope);
+  if (!map_of(&tq, a.q, kNope + kRope, p.H, p.T, kNope + kRope, q_row) ||
+      !(any ? map_of(&tk, a.k, kNope, p.H, p.N, a.k_head_stride, a.k_row_stride) : map_of(&tk, a.q, kNope, p.H, p.T, kNope + kRope, q_row)) ||
+      !(any ? map_of(&tv, a.v, kDv, p.H, p.N, a.v_head_stride, a.v_row_stride) : map_of(&tv, a.q, kDv, p.H, p.T, kNope + kRope, q_row)))
+    return cudaErrorInvalidValue;
+  const cuuint64_t dims[2] = {(cuuint64_t)kRope, (cuuint64_t)(any ? p.N : p.T)}, strides[1] = {(cuuint64_t)kRope * 2};
+  const cuuint32_t box[2] = {64, kTile};
+  memset(&tr, 0, sizeof(tr));
+  if (encode_tensor_map(&tr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(any ? a.k_rope : a.q), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) !=
+      CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem_once(&allowed, reinterpret_cast<const void*>(expanded_attn_kernel), kSmem);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_kernel(plan_kernel, dim3(1), dim3(1024), 0, stream, false, p)) != cudaSuccess) return e;
+  const int64_t items = l.max_work * p.H;
+  if ((e = launch_kernel(expanded_attn_kernel, dim3((unsigned)(items < kSms ? items : kSms)), dim3(kThreads), kSmem, stream, true, tq, tk, tr, tv,
+                         p)) != cudaSuccess)
+    return e;
+  if (l.parts > 1) e = launch_kernel(merge_kernel, dim3((unsigned)(((int64_t)p.T * p.H + 7) / 8)), dim3(256), 0, stream, true, p);
+  return e;
+}
+
+dsa_status check_expanded(const dsa_expanded_attn_args* a) {
+  if (!a || a->n_seq < 0 || a->T < 0 || a->N < 0 || a->max_len < 0 || a->H < 1) return DSA_ERR_INVALID_ARG;
+  if (!(a->sm_scale > 0.f) || !(a->sm_scale < INFINITY)) return DSA_ERR_INVALID_ARG;
+  if (a->H > 128 || a->n_seq > kMaxSeq || a->T >= 1 << 24 || a->N >= 1 << 24) return DSA_ERR_UNSUPPORTED;
+  if (a->n_seq == 0 || a->T == 0) return DSA_OK;
+  auto ok16 = [](const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  if (!a->q_start || !a->kv_start || !ok16(a->q) || !ok16(a->out)) return DSA_ERR_INVALID_ARG;
+  if (a->N == 0) return DSA_OK;
+  if (!ok16(a->k) || !ok16(a->k_rope) || !ok16(a->v)) return DSA_ERR_INVALID_ARG;
+  for (const int64_t s : {a->k_row_stride, a->v_row_stride, a->k_head_stride, a->v_head_stride}) {
+    if (s % 8 != 0 || s < kNope) return DSA_ERR_INVALID_ARG;
+    if (s >= 1ll << 39) return DSA_ERR_UNSUPPORTED;
+  }
+  return DSA_OK;
+}
+
+ExpandedAttnParams params_of(const dsa_expanded_attn_args& a) {
+  ExpandedAttnParams p = {};
+  p.q_start = a.q_start;
+  p.kv_start = a.kv_start;
+  p.n_seq = a.n_seq;
+  p.T = a.T;
+  p.N = a.N;
+  p.H = a.H;
+  p.max_len = a.max_len > 0 && a.max_len < a.N ? a.max_len : a.N;
+  p.causal = a.causal != 0;
+  p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  p.v = reinterpret_cast<const __nv_bfloat16*>(a.v);
+  p.v_row_stride = a.v_row_stride;
+  p.v_head_stride = a.v_head_stride;
+  p.out = reinterpret_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  p.chunk = chunk_of(p);
+  return p;
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" {
+
+dsa_status dsa_expanded_attn_workspace_size(const dsa_expanded_attn_args* a, size_t* bytes) {
+  if (!bytes) return DSA_ERR_INVALID_ARG;
+  const dsa_status s = check_expanded(a);
+  if (s != DSA_OK) return s;
+  *bytes = a->n_seq > 0 && a->T > 0 ? layout_of(params_of(*a)).total : 0;
+  return DSA_OK;
+}
+
+dsa_status dsa_expanded_attn(const dsa_expanded_attn_args* a, void* ws, size_t ws_bytes, void* stream) {
+  dsa_status s = check_expanded(a);
+  if (s != DSA_OK || a->n_seq == 0 || a->T == 0) return s;
+  ExpandedAttnParams p = params_of(*a);
+  if (!ws || ws_bytes < layout_of(p).total || (reinterpret_cast<uintptr_t>(ws) & 255) != 0) return DSA_ERR_WORKSPACE;
+  if ((s = check_device_arch()) != DSA_OK) return s;
+  p.err = device_error_word();
+  return launch(p, *a, ws, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+}  // extern "C"

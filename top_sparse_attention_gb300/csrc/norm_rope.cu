@@ -1,0 +1,478 @@
+// Norm of each head's query or key, or of a latent row, with the rotary positions in the same pass (dsa_norm_rope,
+// dsa_norm_rope_append): per vector (a head of a row, or a row)
+//   y_c = (x_c - mu) r w_c + b_c over the normed columns, r = 1 / sqrt(var + eps),
+// with mu = 0 and var = mean x^2 (RMS), or the mean and the variance (layer norm, the variance from the centred values);
+// then the rotary columns turn (rope.cu), and the result is rounded once, to bf16 or to the cache's format.
+//
+// G lanes (8, 16 or 32) take a vector, lane j of them the 8-element chunks j, j + G, ..., so that the sums are G-wide shuffles
+// and everything between the load and the store stays in registers; a warp takes 32 / G heads of a row at a time (rows,
+// where there is one head) and the next ones' loads are in flight meanwhile.  The sines of a row are taken once for
+// all of its heads.  Columns i and i + rot_dim / 2 of a pair lie in different lanes: the rotary columns pass through
+// shared memory.  Norms, sums and angles are fp32.
+// Bound: HBM for many rows, the launch for few.
+#include "rope_common.cuh"
+
+namespace dsa {
+namespace {
+
+struct NormParams {
+  const float* weight;  // [dim] or null (ones)
+  const float* bias;    // [dim] or null
+  int off, dim;
+  float eps, inv_dim;
+  bool layer;
+  int heads_per_item;   // vector form: heads of a row that a warp takes in turn
+};
+
+constexpr int kMaxWidth = 1024;
+constexpr int kSms = 152;
+enum { kFmtBf16 = 0, kFmtRow = 1, kFmtTile = 2, kFmtMx = 3 };
+
+template <int G>
+__device__ __forceinline__ float sum_across(float a) {
+#pragma unroll
+  for (int o = 1; o < G; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  return a;
+}
+template <int G>
+__device__ __forceinline__ float max_across(float a) {
+#pragma unroll
+  for (int o = 1; o < G; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  return a;
+}
+
+template <int FMT, int G, int NCH>
+__global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_vec_kernel(const RopeParams p, const NormParams n) {
+  constexpr int VEC = 32 / G;  // vectors per step of a warp
+  __shared__ RopeSmem sm;
+  __shared__ alignas(16) float stage_s[kWarps][2 * kRopeMaxPairs];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / G, gl = lane % G;
+  const int nch = p.width / 8;
+  const bool one = p.heads == 1;  // then the vectors of a step are rows
+  const int hblocks = one ? 1 : (p.heads + n.heads_per_item - 1) / n.heads_per_item;
+  const int64_t items = one ? ((int64_t)p.rows + VEC - 1) / VEC : (int64_t)p.rows * hblocks;
+  const int64_t step = (int64_t)gridDim.x * kWarps;
+  fill_freq(p, sm);
+  float2* cs = sm.turns[warp];
+  float* stage = stage_s[warp] + g * 2 * p.pairs;
+  const int entries = one ? VEC * p.pairs : p.pairs;  // of the table: pairs of the step's rows, or of the row
+
+  float w[NCH][8];
+#pragma unroll
+  for (int j = 0; j < NCH; ++j) {
+    const int at = 8 * (gl + G * j) - n.off;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[j][k] = 1.f;
+    if (n.weight && at >= 0 && at < n.dim) {
+      const float4 a = *reinterpret_cast<const float4*>(n.weight + at), b = *reinterpret_cast<const float4*>(n.weight + at + 4);
+      w[j][0] = a.x, w[j][1] = a.y, w[j][2] = a.z, w[j][3] = a.w;
+      w[j][4] = b.x, w[j][5] = b.y, w[j][6] = b.z, w[j][7] = b.w;
+    }
+  }
+
+  uint4 raw[NCH];
+  int64_t dst = 0;
+  int pos0 = 0;
+  bool live = false;
+  auto place = [&](int64_t item, int pass, int64_t& row, int& head) {
+    if (one) {
+      row = item * VEC + g;
+      head = 0;
+      return row < p.rows;
+    }
+    row = item / hblocks;
+    const int h0 = (int)(item - row * hblocks) * n.heads_per_item;
+    head = h0 + pass * VEC + g;
+    return head < min(h0 + n.heads_per_item, p.heads);
+  };
+  auto fetch = [&](int64_t item, int pass) {
+    int64_t row;
+    int head;
+    live = place(item, pass, row, head);
+    const __nv_bfloat16* x = p.x + row * p.x_row_stride + head * p.x_head_stride;
+    if (p.dst) dst = !live ? -1 : p.dst_rows ? p.dst_rows[row] : row;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int c = gl + G * j;
+      raw[j] = live && c < nch ? *reinterpret_cast<const uint4*>(x + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (pass == 0 && lane < entries) {  // the position of this lane's first entry of the table
+      const int v = one ? lane / p.pairs : 0;
+      const int64_t r = one ? item * VEC + v : row;
+      if (r < p.rows) pos0 = p.pos[r * p.pos_stride + sm.axis[lane - v * p.pairs]];
+    }
+  };
+  auto passes_of = [&](int64_t item) {
+    if (one) return 1;
+    const int h0 = (int)(item % hblocks) * n.heads_per_item;
+    return (min(n.heads_per_item, p.heads - h0) + VEC - 1) / VEC;
+  };
+
+  int64_t item = (int64_t)blockIdx.x * kWarps + warp;
+  int pass = 0;
+  if (item < items) fetch(item, 0);
+#pragma unroll 1
+  while (item < items) {
+    int64_t row;
+    int head;
+    const bool mine = place(item, pass, row, head);
+    const int64_t to = dst;
+    if (pass == 0) {
+      __syncwarp();  // the table's last row has been used
+      if (lane < entries) cs[lane] = pair_turn(p, sm.freq[one ? lane % p.pairs : lane], pos0);
+      for (int e = lane + 32; e < entries; e += 32) {
+        const int v = one ? e / p.pairs : 0, k = e - v * p.pairs;
+        const int64_t r = one ? item * VEC + v : row;
+        if (r < p.rows) cs[e] = pair_turn(p, sm.freq[k], p.pos[r * p.pos_stride + sm.axis[k]]);
+      }
+      __syncwarp();
+    }
+    float v[NCH][8];
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) unpack8(raw[j], v[j]);
+    // the next step's loads
+    int64_t next = item;
+    int next_pass = pass + 1;
+    if (next_pass == passes_of(item)) next += step, next_pass = 0;
+    if (next < items) fetch(next, next_pass);
+
+    // ---- the norm
+    float mean = 0.f;
+    if (n.layer) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const int at = 8 * (gl + G * j) - n.off;
+        if (at >= 0 && at < n.dim)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) s += v[j][k];
+      }
+      mean = sum_across<G>(s) * n.inv_dim;
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int at = 8 * (gl + G * j) - n.off;
+      if (at >= 0 && at < n.dim)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          v[j][k] -= mean;
+          ss = fmaf(v[j][k], v[j][k], ss);
+        }
+    }
+    const float r = __frsqrt_rn(fmaf(sum_across<G>(ss), n.inv_dim, n.eps));
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int at = 8 * (gl + G * j) - n.off;
+      if (at < 0 || at >= n.dim) continue;
+      float b[8] = {};
+      if (n.bias) {
+        const float4 lo = __ldg(reinterpret_cast<const float4*>(n.bias + at)), hi = __ldg(reinterpret_cast<const float4*>(n.bias + at + 4));
+        b[0] = lo.x, b[1] = lo.y, b[2] = lo.z, b[3] = lo.w, b[4] = hi.x, b[5] = hi.y, b[6] = hi.z, b[7] = hi.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[j][k] = fmaf(v[j][k] * r, w[j][k], b[k]);
+    }
+    // ---- the rotary columns
+    const float2* turns = cs + (one ? g * p.pairs : 0);
+    if (p.half) {
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const int at = 8 * (gl + G * j) - p.rot_off;
+        if (at >= 0 && at < 2 * p.pairs) {
+          *reinterpret_cast<float4*>(stage + at) = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
+          *reinterpret_cast<float4*>(stage + at + 4) = make_float4(v[j][4], v[j][5], v[j][6], v[j][7]);
+        }
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int at = 8 * (gl + G * j) - p.rot_off;
+      if (at < 0 || at >= 2 * p.pairs) continue;
+      if (p.half) {
+        const bool low = at < p.pairs;
+        const float* other = stage + (low ? at + p.pairs : at - p.pairs);
+        const float2* t = turns + (low ? at : at - p.pairs);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float a = low ? v[j][k] : other[k], b = low ? other[k] : v[j][k];
+          turn(a, b, t[k]);
+          v[j][k] = low ? a : b;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) turn(v[j][2 * k], v[j][2 * k + 1], turns[at / 2 + k]);
+      }
+    }
+    // ---- out
+    const bool keep = mine && (!p.dst || (to >= 0 && to < p.dst_count));
+    if (p.dst && mine && to >= p.dst_count && gl == 0) record_error(p.err, DSA_DEVERR_INDEX_RANGE);
+    if constexpr (FMT == kFmtBf16) {
+      __nv_bfloat16* out = p.dst ? reinterpret_cast<__nv_bfloat16*>(p.dst + to * p.dst_row_stride)
+                                 : p.out + row * p.out_row_stride + head * p.out_head_stride;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const int c = gl + G * j;
+        if (keep && c < nch) *reinterpret_cast<uint4*>(out + 8 * c) = pack8(v[j]);
+      }
+    } else if constexpr (FMT == kFmtRow) {
+      float a = 0.f;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) a = fmaxf(a, amax8(v[j]));
+      a = max_across<G>(a);
+      const Quotient div(a > 0.f ? __fdiv_rn(a, 448.f) : 1.f);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const int c = gl + G * j;
+        if (keep && c < nch)
+          *reinterpret_cast<uint2*>(p.dst + to * p.dst_row_stride + 8 * c) = encode8(v[j], div.s, div.r * kBelow, div.r * kAbove, div.fast);
+      }
+      if (keep && gl == 0) reinterpret_cast<float*>(p.scale)[to] = div.s;
+    } else if constexpr (FMT == kFmtTile) {
+      // a tile is a slot of 16 lanes; lane j of them takes slot j's scale and its reciprocal, once instead of NCH times
+      constexpr int T = G < 16 ? G : 16;
+      const int tiles = (nch + 15) / 16;
+      float own = 0.f;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const float a = max_across<T>(amax8(v[j]));
+        if (lane % T == j) own = a;
+      }
+      const Quotient div(own > 0.f ? __fdiv_rn(own, 448.f) : 1.f);
+      const uint32_t fast = __ballot_sync(0xffffffffu, div.fast);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const int c = gl + G * j, from = lane / T * T + j;
+        const float s = __shfl_sync(0xffffffffu, div.s, from), rs = __shfl_sync(0xffffffffu, div.r, from);
+        if (!keep || c >= nch) continue;
+        *reinterpret_cast<uint2*>(p.dst + to * p.dst_row_stride + 8 * c) = encode8(v[j], s, rs * kBelow, rs * kAbove, (fast >> from) & 1);
+        if (c % 16 == 0) reinterpret_cast<float*>(p.scale)[to * tiles + c / 16] = s;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const int c = gl + G * j;
+        const float a = max_across<4>(amax8(v[j]));
+        if (!keep || c >= nch) continue;
+        const int e = mx_exponent(a);
+        const float inv = ldexpf(1.f, -e);  // a power of two: exact
+        *reinterpret_cast<uint2*>(p.dst + to * p.dst_row_stride + 8 * c) =
+            make_uint2(e4m3x4(v[j][0] * inv, v[j][1] * inv, v[j][2] * inv, v[j][3] * inv),
+                       e4m3x4(v[j][4] * inv, v[j][5] * inv, v[j][6] * inv, v[j][7] * inv));
+        if (c % 4 == 0) p.scale[to * (p.width / 32) + c / 4] = (uint8_t)(e + 127);
+      }
+    }
+    item = next;
+    pass = next_pass;
+  }
+}
+
+// Any width up to 1024, offset, pitch and alignment: a warp per vector, which it holds in shared memory.
+constexpr int kPlainWarps = 4;
+template <int FMT>
+__global__ void __launch_bounds__(32 * kPlainWarps) norm_rope_kernel(const RopeParams p, const NormParams n) {
+  __shared__ RopeSmem sm;
+  __shared__ float rows_s[kPlainWarps][kMaxWidth];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  fill_freq(p, sm);
+  float2* cs = sm.turns[warp];
+  float* v = rows_s[warp];
+  const int64_t vectors = (int64_t)p.rows * p.heads, step = (int64_t)gridDim.x * kPlainWarps;
+#pragma unroll 1
+  for (int64_t at = (int64_t)blockIdx.x * kPlainWarps + warp; at < vectors; at += step) {
+    const int64_t row = at / p.heads;
+    const int head = (int)(at - row * p.heads);
+    const __nv_bfloat16* x = p.x + row * p.x_row_stride + head * p.x_head_stride;
+    fill_turns(p, row, sm, cs);
+    for (int c = lane; c < p.width; c += 32) v[c] = __bfloat162float(x[c]);
+    __syncwarp();
+    float mean = 0.f;
+    if (n.layer) {
+      for (int c = lane; c < n.dim; c += 32) mean += v[n.off + c];
+      mean = sum_across<32>(mean) * n.inv_dim;
+    }
+    float ss = 0.f;
+    for (int c = lane; c < n.dim; c += 32) {
+      const float d = v[n.off + c] - mean;
+      ss = fmaf(d, d, ss);
+    }
+    const float r = __frsqrt_rn(fmaf(sum_across<32>(ss), n.inv_dim, n.eps));
+    for (int c = lane; c < n.dim; c += 32)
+      v[n.off + c] = fmaf((v[n.off + c] - mean) * r, n.weight ? n.weight[c] : 1.f, n.bias ? n.bias[c] : 0.f);
+    __syncwarp();
+    for (int k = lane; k < p.pairs; k += 32) {
+      const int c0 = p.rot_off + (p.half ? k : 2 * k), c1 = p.half ? c0 + p.pairs : c0 + 1;
+      turn(v[c0], v[c1], cs[k]);
+    }
+    __syncwarp();
+    if (!p.dst) {
+      __nv_bfloat16* out = p.out + row * p.out_row_stride + head * p.out_head_stride;
+      for (int c = lane; c < p.width; c += 32) out[c] = __float2bfloat16_rn(v[c]);
+      continue;
+    }
+    const int64_t to = p.dst_rows ? p.dst_rows[row] : row;
+    if (to >= p.dst_count && lane == 0) record_error(p.err, DSA_DEVERR_INDEX_RANGE);
+    if (to < 0 || to >= p.dst_count) continue;
+    uint8_t* out = p.dst + to * p.dst_row_stride;
+    if constexpr (FMT == kFmtBf16) {
+      for (int c = lane; c < p.width; c += 32) *reinterpret_cast<__nv_bfloat16*>(out + 2 * c) = __float2bfloat16_rn(v[c]);
+    } else {
+      const int group = FMT == kFmtRow ? p.width : FMT == kFmtTile ? 128 : 32;
+      const int groups = (p.width + group - 1) / group;
+      for (int i = 0; i < groups; ++i) {
+        const int lo = i * group, hi = min(lo + group, p.width);
+        float a = 0.f;
+        for (int c = lo + lane; c < hi; c += 32) a = fmaxf(a, fabsf(v[c]));
+        a = max_across<32>(a);
+        if constexpr (FMT == kFmtMx) {
+          const int e = mx_exponent(a);
+          const float inv = ldexpf(1.f, -e);
+          for (int c = lo + lane; c < hi; c += 32) out[c] = to_e4m3(v[c] * inv);
+          if (lane == 0) p.scale[to * groups + i] = (uint8_t)(e + 127);
+        } else {
+          const Quotient div(a > 0.f ? __fdiv_rn(a, 448.f) : 1.f);
+          for (int c = lo + lane; c < hi; c += 32) out[c] = to_e4m3(div(v[c]));
+          if (lane == 0) reinterpret_cast<float*>(p.scale)[to * groups + i] = div.s;
+        }
+      }
+    }
+  }
+}
+
+using NormKernel = void (*)(const RopeParams, const NormParams);
+
+// The vector form for a width: the fewest lanes that hold it at a chunk each, else a warp.
+template <int FMT>
+NormKernel vec_form(int width, int* lanes) {
+  *lanes = width <= 64 ? 8 : width <= 128 ? 16 : 32;
+  if (width <= 64) return norm_rope_vec_kernel<FMT, 8, 1>;
+  if (width <= 128) return norm_rope_vec_kernel<FMT, 16, 1>;
+  if (width <= 256) return norm_rope_vec_kernel<FMT, 32, 1>;
+  if (width <= 768) return norm_rope_vec_kernel<FMT, 32, 3>;
+  return norm_rope_vec_kernel<FMT, 32, 4>;
+}
+
+dsa_status norm_args(NormParams* n, const dsa_norm* norm, int width) {
+  if (!norm || (norm->kind != DSA_NORM_RMS && norm->kind != DSA_NORM_LAYER)) return DSA_ERR_INVALID_ARG;
+  if (norm->off < 0 || norm->dim < 1 || (int64_t)norm->off + norm->dim > width) return DSA_ERR_INVALID_ARG;
+  if (!(norm->eps >= 0.f) || !(norm->eps < INFINITY)) return DSA_ERR_INVALID_ARG;
+  if (!aligned(norm->weight, 4) || !aligned(norm->bias, 4)) return DSA_ERR_INVALID_ARG;
+  if (width > kMaxWidth) return DSA_ERR_UNSUPPORTED;
+  n->weight = norm->weight;
+  n->bias = norm->bias;
+  n->off = norm->off;
+  n->dim = norm->dim;
+  n->eps = norm->eps;
+  n->inv_dim = 1.f / (float)norm->dim;
+  n->layer = norm->kind == DSA_NORM_LAYER;
+  return DSA_OK;
+}
+
+// The columns that need whole 16-byte chunks, for the vector form.
+bool whole_chunks(const RopeParams& p, const NormParams& n) {
+  return p.width % 8 == 0 && p.rot_off % 8 == 0 && (2 * p.pairs) % 8 == 0 && (!p.half || p.pairs % 8 == 0) && n.off % 8 == 0 &&
+         n.dim % 8 == 0 && aligned(n.weight, 16) && aligned(n.bias, 16) && aligned(p.x, 16) && (p.rows == 1 || p.x_row_stride % 8 == 0) &&
+         p.x_head_stride % 8 == 0;
+}
+
+template <int FMT>
+dsa_status launch_norm(const RopeParams& p, NormParams n, bool vec, cudaStream_t stream) {
+  if (!vec) {
+    const int64_t want = ((int64_t)p.rows * p.heads + kPlainWarps - 1) / kPlainWarps;
+    norm_rope_kernel<FMT><<<(unsigned)(want < 8 * kSms ? want : 8 * kSms), 32 * kPlainWarps, 0, stream>>>(p, n);
+  } else {
+    int lanes;
+    const NormKernel kern = vec_form<FMT>(p.width, &lanes);
+    const int per = 32 / lanes, most = 2 * kSms;
+    // heads of a row for a warp: all of up to 16, or as few as leave no warp idle
+    n.heads_per_item = 16;
+    while (n.heads_per_item > per && (int64_t)p.rows * ((p.heads + n.heads_per_item - 1) / n.heads_per_item) < (int64_t)most * kWarps)
+      n.heads_per_item /= 2;
+    const int64_t items = p.heads == 1 ? ((int64_t)p.rows + per - 1) / per
+                                       : (int64_t)p.rows * ((p.heads + n.heads_per_item - 1) / n.heads_per_item);
+    const int64_t want = (items + kWarps - 1) / kWarps;
+    kern<<<(unsigned)(want < most ? want : most), 32 * kWarps, 0, stream>>>(p, n);
+  }
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" {
+
+dsa_status dsa_norm_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride, int rows, int heads, int width,
+                         const dsa_norm* norm, int rot_off, int rot_dim, const int32_t* pos, int n_axes, const uint8_t* pair_axis,
+                         const float* inv_freq, int style, void* out, int64_t out_row_stride, int64_t out_head_stride, void* stream) {
+  RopeParams p = {};
+  NormParams n = {};
+  if (rows < 0 || heads < 1) return DSA_ERR_INVALID_ARG;
+  dsa_status s = rope_args(&p, width, rot_off, rot_dim, pos, n_axes, pair_axis, inv_freq, style, rows > 0);
+  if (s != DSA_OK || (s = norm_args(&n, norm, width)) != DSA_OK) return s;
+  if (heads > 1 && (x_head_stride < width || out_head_stride < width)) return DSA_ERR_INVALID_ARG;
+  if (rows > 1 && (x_row_stride < width || out_row_stride < width)) return DSA_ERR_INVALID_ARG;
+  if (rows == 0) return DSA_OK;
+  if (!x || !out || !aligned2(x) || !aligned2(out)) return DSA_ERR_INVALID_ARG;
+  // in place means the same elements: another layout over the same memory would race
+  if (x == out && ((rows > 1 && x_row_stride != out_row_stride) || (heads > 1 && x_head_stride != out_head_stride)))
+    return DSA_ERR_INVALID_ARG;
+  if ((s = check_device_arch()) != DSA_OK) return s;
+  p.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.x_row_stride = x_row_stride;
+  p.x_head_stride = heads > 1 ? x_head_stride : 0;
+  p.out_row_stride = out_row_stride;
+  p.out_head_stride = heads > 1 ? out_head_stride : 0;
+  p.rows = rows;
+  p.heads = heads;
+  const bool vec = whole_chunks(p, n) && aligned(out, 16) && (rows == 1 || out_row_stride % 8 == 0) && p.out_head_stride % 8 == 0;
+  return launch_norm<kFmtBf16>(p, n, vec, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dsa_status dsa_norm_rope_append(const void* x, int64_t x_row_stride, int rows, int width, const dsa_norm* norm, int rot_off,
+                                int rot_dim, const int32_t* pos, int n_axes, const uint8_t* pair_axis, const float* inv_freq,
+                                int style, dsa_dtype dtype, void* dst, int64_t dst_row_stride, int64_t dst_count, void* scale,
+                                const int64_t* dst_rows, void* stream) {
+  RopeParams p = {};
+  NormParams n = {};
+  if (rows < 0 || dst_count < 0) return DSA_ERR_INVALID_ARG;
+  dsa_status s = rope_args(&p, width, rot_off, rot_dim, pos, n_axes, pair_axis, inv_freq, style, rows > 0);
+  if (s != DSA_OK || (s = norm_args(&n, norm, width)) != DSA_OK) return s;
+  if (dtype != DSA_BF16 && dtype != DSA_FP8_E4M3 && dtype != DSA_FP8_E4M3_T128 && dtype != DSA_MXFP8_E4M3)
+    return DSA_ERR_UNSUPPORTED;
+  const int64_t elem = dtype == DSA_BF16 ? 2 : 1;
+  if (dst_row_stride < width * elem || dst_row_stride % elem != 0 || (rows > 1 && x_row_stride < width))
+    return DSA_ERR_INVALID_ARG;
+  if (dtype == DSA_MXFP8_E4M3 && width % 32 != 0) return DSA_ERR_INVALID_ARG;
+  if (!dst_rows && rows > dst_count) return DSA_ERR_INVALID_ARG;
+  if (rows == 0) return DSA_OK;
+  if (!x || !dst || !aligned2(x) || (elem == 2 && !aligned2(dst))) return DSA_ERR_INVALID_ARG;
+  if (dtype != DSA_BF16 && !scale) return DSA_ERR_INVALID_ARG;
+  if ((dtype == DSA_FP8_E4M3 || dtype == DSA_FP8_E4M3_T128) && !aligned(scale, 4)) return DSA_ERR_INVALID_ARG;
+  if ((s = check_device_arch()) != DSA_OK) return s;
+  p.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  p.x_row_stride = x_row_stride;
+  p.rows = rows;
+  p.heads = 1;
+  p.dst = reinterpret_cast<uint8_t*>(dst);
+  p.dst_row_stride = dst_row_stride;
+  p.dst_count = dst_count;
+  p.scale = reinterpret_cast<uint8_t*>(scale);
+  p.dst_rows = dst_rows;
+  p.err = device_error_word();
+  const uintptr_t out_align = elem == 2 ? 16 : 8;
+  const bool vec = whole_chunks(p, n) && aligned(dst, out_align) && dst_row_stride % (int64_t)out_align == 0;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  switch (dtype) {
+    case DSA_BF16: return launch_norm<kFmtBf16>(p, n, vec, st);
+    case DSA_FP8_E4M3: return launch_norm<kFmtRow>(p, n, vec, st);
+    case DSA_FP8_E4M3_T128: return launch_norm<kFmtTile>(p, n, vec, st);
+    default: return launch_norm<kFmtMx>(p, n, vec, st);
+  }
+}
+
+}  // extern "C"
