@@ -565,6 +565,26 @@ dsa_status dsa_tree_attn_workspace_size(const dsa_tree_args* a, size_t* bytes);
 dsa_status dsa_tree_attn(const dsa_tree_args* a, void* ws, size_t ws_bytes, void* stream);
 
 /* --------------------------------------------------------------------------------------------
+ * dsa_prefix_attn -- dsa_tree_attn for sequences that share prefixes in groups (questions about one document, requests
+ * behind one system prompt, samples of one prompt): a prefix is attended to once for the whole group instead of once
+ * per sequence.  Same arguments, layouts, results and support as dsa_tree_attn.  Group g is the sequences
+ * group_start[g] ... group_start[g+1] - 1; their first n_shared[g] positions hold the same rows (in a paged cache
+ * usually the same blocks), which are read from the first sequence of the group that has queries.
+ *   group_start  device int32 [n_groups + 1], not decreasing (clamped to [0, n_seq]); sequences outside
+ *                [group_start[0], group_start[n_groups]) share nothing
+ *   n_shared     device int32 [n_groups]: clamped to the least n_ctx of the group's sequences that have queries
+ *                (n_new above 0); a group of one shares nothing
+ * The results differ from dsa_tree_attn's by rounding only (the sums are split elsewhere); they repeat from call to call.
+ * ws: dsa_prefix_attn_workspace_size bytes, 256-byte aligned, contents irrelevant; calls (and captured graphs) that share
+ * it must not run at the same time.  group_start and n_shared of the size query are only tested for being there.
+ * Supported: n_groups <= 4096; n_seq * q_per_seq * H <= 2^26.
+ * ------------------------------------------------------------------------------------------ */
+dsa_status dsa_prefix_attn_workspace_size(const dsa_tree_args* a, const int32_t* group_start, const int32_t* n_shared,
+                                          int n_groups, size_t* bytes);
+dsa_status dsa_prefix_attn(const dsa_tree_args* a, const int32_t* group_start, const int32_t* n_shared, int n_groups,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* --------------------------------------------------------------------------------------------
  * Fused chain: dsa_decode / dsa_prefill run steps 1-3 back to back on `stream` (the indexer's
  * scoring, weighting and Top-K chain followed by the sparse gather kernel, Day 0 Support for New LLM
  * Architectures, Key Optimization 1), keeping the scores in the workspace.  dsa_decode expects

@@ -30,6 +30,7 @@ EXPORTS = (
     "dsa_attn_combine", "dsa_set_attn_kernel", "dsa_block_plan", "dsa_rope", "dsa_rope_append",
     "dsa_tree_attn", "dsa_tree_attn_workspace_size", "dsa_norm_rope", "dsa_norm_rope_append",
     "dsa_latent_expand", "dsa_expanded_attn", "dsa_expanded_attn_workspace_size",
+    "dsa_prefix_attn", "dsa_prefix_attn_workspace_size",
 )
 
 
@@ -149,6 +150,8 @@ def _load():
         "dsa_expanded_attn_workspace_size": (I, [ctypes.POINTER(DsaExpandedAttnArgs), ctypes.POINTER(SZ)]),
         "dsa_tree_attn": (I, [ctypes.POINTER(DsaTreeArgs), P, SZ, P]),
         "dsa_tree_attn_workspace_size": (I, [ctypes.POINTER(DsaTreeArgs), ctypes.POINTER(SZ)]),
+        "dsa_prefix_attn": (I, [ctypes.POINTER(DsaTreeArgs), P, P, I, P, SZ, P]),
+        "dsa_prefix_attn_workspace_size": (I, [ctypes.POINTER(DsaTreeArgs), P, P, I, ctypes.POINTER(SZ)]),
         "dsa_workspace_size": (I, [ctypes.POINTER(DsaArgs), I, ctypes.POINTER(SZ)]),
         "dsa_launch_count": (I, [ctypes.POINTER(DsaArgs), I, ctypes.POINTER(ctypes.c_int)]),
         "dsa_decode": (I, [ctypes.POINTER(DsaArgs), P, SZ, P]),

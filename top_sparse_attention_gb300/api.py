@@ -18,7 +18,7 @@ __all__ = ["dsa_index_score", "dsa_topk", "dsa_topk_noalloc", "dsa_topk_pairs", 
            "dsa_workspace_size", "dsa_launch_count", "dsa_get_device_error", "ld_scores_for",
            "dsa_quantize_mxfp8", "dsa_quantize_fp8_rows", "dsa_quantize_fp8_tiles",
            "dsa_block_plan", "BlockPlan", "dsa_rope", "dsa_rope_append", "dsa_tree_attn",
-           "dsa_norm_rope", "dsa_norm_rope_append", "dsa_latent_expand", "dsa_expanded_attn"]
+           "dsa_norm_rope", "dsa_norm_rope_append", "dsa_latent_expand", "dsa_expanded_attn", "dsa_prefix_attn"]
 
 
 # The current stream's handle and the current device without building torch objects (a serving step makes
@@ -674,21 +674,16 @@ def _latent_cache(what, dev, a, kv, kv_scale, n_seq, block_table, block_size, L,
     a.kv, a.n_seq, a.L = kv.data_ptr(), n_seq, int(L)
 
 
-def dsa_tree_attn(q, kv, n_ctx, *, sm_scale, q_per_seq, n_new=None, tree_mask=None, kv_scale=None, block_table=None,
-                  block_size=0, L=None, out=None, lse=None, ws=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
-    """Attention of drafted tokens over the visible latent cache (see dsa.h): (out [T, H, 512] bf16,
-    lse [T, H] fp32).  q bf16 [n_seq * q_per_seq, H, 576]; kv [n_seq, L, 576] bf16 or uint8 E4M3
-    codes (kv_scale [n_seq, L] or [n_seq, L, 5]), or with `block_table` (int32 [n_seq, max_blocks]) and
-    `block_size` a pool [rows, 576] (kv_scale [rows] or [rows, 5]) with `L` positions per sequence at
-    most.  n_ctx, n_new int32 [n_seq]; tree_mask int32 or uint32 [T, ceil(q_per_seq / 32)] bits, None
-    for a chain.  `ws` (uint8) is scratch that later calls on the same stream may reuse."""
-    what = "dsa_tree_attn"
+def _tree(what, size, fn, groups, q, kv, n_ctx, sm_scale, q_per_seq, n_new, tree_mask, kv_scale, block_table, block_size, L, out, lse,
+          ws, stream):
+    """dsa_tree_attn and dsa_prefix_attn: `groups` makes the arguments behind the struct."""
     dev = _cuda_device(what, q)
     _check(what, dev, "q", q, torch.bfloat16, 3)
     _check(what, dev, "n_ctx", n_ctx, torch.int32, 1)
     _check(what, dev, "n_new", n_new, torch.int32, 1)
     T, H, D = q.shape
     n_seq = n_ctx.shape[0]
+    more = groups(dev)
     if q_per_seq < 1 or T != n_seq * q_per_seq or (n_new is not None and n_new.shape[0] != n_seq):
         raise ValueError(f"{what}: {T} queries are not q_per_seq = {q_per_seq} nodes of {n_seq} sequences")
     if tree_mask is not None:
@@ -714,13 +709,44 @@ def dsa_tree_attn(q, kv, n_ctx, *, sm_scale, q_per_seq, n_new=None, tree_mask=No
     a.n_ctx, a.n_new, a.tree_mask = n_ctx.data_ptr(), _ptr(n_new), _ptr(tree_mask)
     a.q, a.out, a.lse = q.data_ptr(), out.data_ptr(), lse.data_ptr()
     need = ctypes.c_size_t(0)
-    N.check(N.lib.dsa_tree_attn_workspace_size(ctypes.byref(a), ctypes.byref(need)), what)
+    N.check(size(ctypes.byref(a), *more, ctypes.byref(need)), what)
     if ws is None:
         ws = _scratch(side, need.value, torch.uint8, dev) if need.value else None
     else:
         _check(what, dev, "ws", ws, torch.uint8, 1)
-    _run(what, N.lib.dsa_tree_attn, dev, stream, ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel())
+    _run(what, fn, dev, stream, ctypes.byref(a), *more, _ptr(ws), 0 if ws is None else ws.numel())
     return out, lse
+
+
+def dsa_tree_attn(q, kv, n_ctx, *, sm_scale, q_per_seq, n_new=None, tree_mask=None, kv_scale=None, block_table=None,
+                  block_size=0, L=None, out=None, lse=None, ws=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of drafted tokens over the visible latent cache (see dsa.h): (out [T, H, 512] bf16,
+    lse [T, H] fp32).  q bf16 [n_seq * q_per_seq, H, 576]; kv [n_seq, L, 576] bf16 or uint8 E4M3
+    codes (kv_scale [n_seq, L] or [n_seq, L, 5]), or with `block_table` (int32 [n_seq, max_blocks]) and
+    `block_size` a pool [rows, 576] (kv_scale [rows] or [rows, 5]) with `L` positions per sequence at
+    most.  n_ctx, n_new int32 [n_seq]; tree_mask int32 or uint32 [T, ceil(q_per_seq / 32)] bits, None
+    for a chain.  `ws` (uint8) is scratch that later calls on the same stream may reuse."""
+    return _tree("dsa_tree_attn", N.lib.dsa_tree_attn_workspace_size, N.lib.dsa_tree_attn, lambda dev: (), q, kv, n_ctx, sm_scale,
+                 q_per_seq, n_new, tree_mask, kv_scale, block_table, block_size, L, out, lse, ws, stream)
+
+
+def dsa_prefix_attn(q, kv, n_ctx, *, sm_scale, q_per_seq, group_start, n_shared, n_new=None, tree_mask=None, kv_scale=None,
+                    block_table=None, block_size=0, L=None, out=None, lse=None, ws=None,
+                    stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """dsa_tree_attn for sequences that share prefixes in groups, which are attended to once for the group (see dsa.h):
+    sequences group_start[g] ... group_start[g + 1] - 1 (int32 [n_groups + 1]) hold the same rows at their first n_shared[g]
+    positions (int32 [n_groups]).  All other arguments and the results are those of dsa_tree_attn."""
+    what = "dsa_prefix_attn"
+
+    def groups(dev):
+        _check(what, dev, "group_start", group_start, torch.int32, 1)
+        _check(what, dev, "n_shared", n_shared, torch.int32, 1)
+        if group_start.shape[0] != n_shared.shape[0] + 1:
+            raise ValueError(f"{what}: group_start must have one entry more than n_shared")
+        return group_start.data_ptr(), n_shared.data_ptr(), n_shared.shape[0]
+
+    return _tree(what, N.lib.dsa_prefix_attn_workspace_size, N.lib.dsa_prefix_attn, groups, q, kv, n_ctx, sm_scale, q_per_seq, n_new,
+                 tree_mask, kv_scale, block_table, block_size, L, out, lse, ws, stream)
 
 
 def dsa_latent_expand(kv, w, kv_start, *, rows=None, kv_scale=None, block_table=None, block_size=0, L=None, out=None, rope_out=None,

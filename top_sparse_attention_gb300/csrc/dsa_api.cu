@@ -427,6 +427,10 @@ dsa_status check_topk_args(const float* scores, int64_t ld_scores, int T, int q_
   return check_topk(scores, ld_scores, T, q_per_seq, q_pos0, n_valid, L, K, idx);
 }
 
+dsa_status check_tree_args(const dsa_tree_args* a) { return check_tree(a); }
+
+TreeAttnParams tree_attn_params(const dsa_tree_args& a) { return tree_params(a); }
+
 dsa_status check_device_arch() { return check_device(); }
 
 cudaError_t allow_smem_once(std::atomic<uint64_t>* done, const void* kern, int bytes) {

@@ -265,6 +265,8 @@ __device__ __forceinline__ int64_t tree_row(const TreeAttnParams& p, int seq, in
   return (int64_t)b * p.pages.block_size + pos % p.pages.block_size;
 }
 
+dsa_status check_tree_args(const dsa_tree_args* a);
+TreeAttnParams tree_attn_params(const dsa_tree_args& a);  // (without the error word)
 size_t tree_attn_ws_bytes(const TreeAttnParams& p);
 cudaError_t launch_tree_attn(const TreeAttnParams& p, void* ws, cudaStream_t stream);
 
