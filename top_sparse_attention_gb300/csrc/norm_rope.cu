@@ -41,137 +41,131 @@ __device__ __forceinline__ float max_across(float a) {
   return a;
 }
 
-template <int FMT, int G, int NCH>
-__global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_vec_kernel(const RopeParams p, const NormParams n) {
+template <int FMT, int G, int NCH, int CTAS>
+__global__ void __launch_bounds__(32 * kWarps, CTAS) norm_rope_vec_kernel(const RopeParams p, const NormParams n) {
   constexpr int VEC = 32 / G;  // vectors per step of a warp
   __shared__ RopeSmem sm;
-  __shared__ alignas(16) float stage_s[kWarps][2 * kRopeMaxPairs];
+  __shared__ alignas(16) float stage_s[kWarps][VEC * 8 * G * NCH < 256 * VEC ? VEC * 8 * G * NCH : 256 * VEC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / G, gl = lane % G;
   const int nch = p.width / 8;
   const bool one = p.heads == 1;  // then the vectors of a step are rows
   const int hblocks = one ? 1 : (p.heads + n.heads_per_item - 1) / n.heads_per_item;
-  const int64_t items = one ? ((int64_t)p.rows + VEC - 1) / VEC : (int64_t)p.rows * hblocks;
-  const int64_t step = (int64_t)gridDim.x * kWarps;
   fill_freq(p, sm);
   float2* cs = sm.turns[warp];
   float* stage = stage_s[warp] + g * 2 * p.pairs;
   const int entries = one ? VEC * p.pairs : p.pairs;  // of the table: pairs of the step's rows, or of the row
 
-  float w[NCH][8];
-#pragma unroll
-  for (int j = 0; j < NCH; ++j) {
-    const int at = 8 * (gl + G * j) - n.off;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w[j][k] = 1.f;
-    if (n.weight && at >= 0 && at < n.dim) {
-      const float4 a = *reinterpret_cast<const float4*>(n.weight + at), b = *reinterpret_cast<const float4*>(n.weight + at + 4);
-      w[j][0] = a.x, w[j][1] = a.y, w[j][2] = a.z, w[j][3] = a.w;
-      w[j][4] = b.x, w[j][5] = b.y, w[j][6] = b.z, w[j][7] = b.w;
-    }
+  // weights and biases by column, in shared memory (in registers they would spill)
+  __shared__ alignas(16) float w_s[8 * G * NCH], b_s[8 * G * NCH];
+  for (int c = threadIdx.x; c < n.dim; c += 32 * kWarps) {
+    w_s[c] = n.weight ? n.weight[c] : 1.f;
+    b_s[c] = n.bias ? n.bias[c] : 0.f;
   }
+  __syncthreads();
 
   uint4 raw[NCH];
   int64_t dst = 0;
   int pos0 = 0;
-  bool live = false;
-  auto place = [&](int64_t item, int pass, int64_t& row, int& head) {
-    if (one) {
-      row = item * VEC + g;
-      head = 0;
-      return row < p.rows;
-    }
-    row = item / hblocks;
-    const int h0 = (int)(item - row * hblocks) * n.heads_per_item;
-    head = h0 + pass * VEC + g;
-    return head < min(h0 + n.heads_per_item, p.heads);
-  };
-  auto fetch = [&](int64_t item, int pass) {
+  // a step: vectors g of `row` and heads [h0 + VEC pass, ...), or of rows [row, row + VEC)
+  struct Step {
     int64_t row;
-    int head;
-    live = place(item, pass, row, head);
-    const __nv_bfloat16* x = p.x + row * p.x_row_stride + head * p.x_head_stride;
+    int hb, pass;
+  };
+  auto head_of = [&](const Step& s) { return one ? 0 : s.hb * n.heads_per_item + s.pass * VEC + g; };
+  auto row_of = [&](const Step& s) { return one ? s.row + g : s.row; };
+  auto mine_of = [&](const Step& s) {
+    return one ? s.row + g < p.rows : s.pass * VEC + g < n.heads_per_item && head_of(s) < p.heads;
+  };
+  auto fetch = [&](const Step& s) {
+    const bool live = mine_of(s);
+    const int64_t row = row_of(s);
+    const __nv_bfloat16* x = p.x + row * p.x_row_stride + head_of(s) * p.x_head_stride + 8 * gl;
     if (p.dst) dst = !live ? -1 : p.dst_rows ? p.dst_rows[row] : row;
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      const int c = gl + G * j;
-      raw[j] = live && c < nch ? *reinterpret_cast<const uint4*>(x + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (pass == 0 && lane < entries) {  // the position of this lane's first entry of the table
+    for (int j = 0; j < NCH; ++j)
+      raw[j] = live && gl + G * j < nch ? *reinterpret_cast<const uint4*>(x + 8 * G * j) : make_uint4(0u, 0u, 0u, 0u);
+    if (s.pass == 0 && lane < entries) {  // the position of this lane's first entry of the table
       const int v = one ? lane / p.pairs : 0;
-      const int64_t r = one ? item * VEC + v : row;
+      const int64_t r = s.row + v;
       if (r < p.rows) pos0 = p.pos[r * p.pos_stride + sm.axis[lane - v * p.pairs]];
     }
   };
-  auto passes_of = [&](int64_t item) {
-    if (one) return 1;
-    const int h0 = (int)(item % hblocks) * n.heads_per_item;
-    return (min(n.heads_per_item, p.heads - h0) + VEC - 1) / VEC;
-  };
-
-  int64_t item = (int64_t)blockIdx.x * kWarps + warp;
-  int pass = 0;
-  if (item < items) fetch(item, 0);
+  const int64_t item0 = (int64_t)blockIdx.x * kWarps + warp, stride = (int64_t)gridDim.x * kWarps;
+  Step at = {one ? item0 * VEC : item0 / hblocks, one ? 0 : (int)(item0 % hblocks), 0};
+  const int64_t row_step = one ? stride * VEC : stride / hblocks;
+  const int hb_step = one ? 0 : (int)(stride % hblocks);
+  if (at.row < p.rows) fetch(at);
 #pragma unroll 1
-  while (item < items) {
-    int64_t row;
-    int head;
-    const bool mine = place(item, pass, row, head);
-    const int64_t to = dst;
-    if (pass == 0) {
+  while (at.row < p.rows) {
+    const int64_t to = dst, row = row_of(at);
+    const bool mine = mine_of(at);
+    const int head = head_of(at);
+    if (at.pass == 0) {
       __syncwarp();  // the table's last row has been used
       if (lane < entries) cs[lane] = pair_turn(p, sm.freq[one ? lane % p.pairs : lane], pos0);
       for (int e = lane + 32; e < entries; e += 32) {
         const int v = one ? e / p.pairs : 0, k = e - v * p.pairs;
-        const int64_t r = one ? item * VEC + v : row;
-        if (r < p.rows) cs[e] = pair_turn(p, sm.freq[k], p.pos[r * p.pos_stride + sm.axis[k]]);
+        if (at.row + v < p.rows) cs[e] = pair_turn(p, sm.freq[k], p.pos[(at.row + v) * p.pos_stride + sm.axis[k]]);
       }
       __syncwarp();
     }
-    float v[NCH][8];
+    float2 v[NCH][4];
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) unpack8(raw[j], v[j]);
+    for (int j = 0; j < NCH; ++j) {
+      const uint32_t u[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[j][k] = make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xFFFF0000u));
+    }
     // the next step's loads
-    int64_t next = item;
-    int next_pass = pass + 1;
-    if (next_pass == passes_of(item)) next += step, next_pass = 0;
-    if (next < items) fetch(next, next_pass);
+    ++at.pass;
+    if (one || at.pass * VEC >= min(n.heads_per_item, p.heads - at.hb * n.heads_per_item)) {
+      at.pass = 0;
+      at.row += row_step;
+      at.hb += hb_step;
+      if (at.hb >= hblocks) at.hb -= hblocks, ++at.row;
+    }
+    if (at.row < p.rows) fetch(at);
 
     // ---- the norm
     float mean = 0.f;
     if (n.layer) {
-      float s = 0.f;
+      float2 s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
-        const int at = 8 * (gl + G * j) - n.off;
-        if (at >= 0 && at < n.dim)
+        const int c = 8 * (gl + G * j) - n.off;
+        if (c >= 0 && c < n.dim)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) s += v[j][k];
+          for (int k = 0; k < 4; ++k) s.x += v[j][k].x, s.y += v[j][k].y;
       }
-      mean = sum_across<G>(s) * n.inv_dim;
+      mean = sum_across<G>(s.x + s.y) * n.inv_dim;
     }
-    float ss = 0.f;
+    float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const int at = 8 * (gl + G * j) - n.off;
-      if (at >= 0 && at < n.dim)
+      const int c = 8 * (gl + G * j) - n.off;
+      if (c >= 0 && c < n.dim) {
+        if (n.layer)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          v[j][k] -= mean;
-          ss = fmaf(v[j][k], v[j][k], ss);
+          for (int k = 0; k < 4; ++k) v[j][k].x -= mean, v[j][k].y -= mean;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ss = ffma2(v[j][k], v[j][k], ss);
+      }
+    }
+    const float r = __frsqrt_rn(fmaf(sum_across<G>(ss.x + ss.y), n.inv_dim, n.eps));
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int c = 8 * (gl + G * j) - n.off;
+      if (c < 0 || c >= n.dim) continue;
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        const float4 w = *reinterpret_cast<const float4*>(w_s + c + 2 * k);
+        v[j][k] = fmul2(fmul2(v[j][k], make_float2(r, r)), make_float2(w.x, w.y));
+        v[j][k + 1] = fmul2(fmul2(v[j][k + 1], make_float2(r, r)), make_float2(w.z, w.w));
+        if (n.bias) {
+          const float4 b = *reinterpret_cast<const float4*>(b_s + c + 2 * k);
+          v[j][k].x += b.x, v[j][k].y += b.y, v[j][k + 1].x += b.z, v[j][k + 1].y += b.w;
         }
-    }
-    const float r = __frsqrt_rn(fmaf(sum_across<G>(ss), n.inv_dim, n.eps));
-#pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      const int at = 8 * (gl + G * j) - n.off;
-      if (at < 0 || at >= n.dim) continue;
-      float b[8] = {};
-      if (n.bias) {
-        const float4 lo = __ldg(reinterpret_cast<const float4*>(n.bias + at)), hi = __ldg(reinterpret_cast<const float4*>(n.bias + at + 4));
-        b[0] = lo.x, b[1] = lo.y, b[2] = lo.z, b[3] = lo.w, b[4] = hi.x, b[5] = hi.y, b[6] = hi.z, b[7] = hi.w;
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[j][k] = fmaf(v[j][k] * r, w[j][k], b[k]);
     }
     // ---- the rotary columns
     const float2* turns = cs + (one ? g * p.pairs : 0);
@@ -179,65 +173,87 @@ __global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_vec_kernel(const Rop
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
-        const int at = 8 * (gl + G * j) - p.rot_off;
-        if (at >= 0 && at < 2 * p.pairs) {
-          *reinterpret_cast<float4*>(stage + at) = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
-          *reinterpret_cast<float4*>(stage + at + 4) = make_float4(v[j][4], v[j][5], v[j][6], v[j][7]);
+        const int c = 8 * (gl + G * j) - p.rot_off;
+        if (c >= 0 && c < 2 * p.pairs) {
+          *reinterpret_cast<float4*>(stage + c) = make_float4(v[j][0].x, v[j][0].y, v[j][1].x, v[j][1].y);
+          *reinterpret_cast<float4*>(stage + c + 4) = make_float4(v[j][2].x, v[j][2].y, v[j][3].x, v[j][3].y);
         }
       }
       __syncwarp();
     }
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const int at = 8 * (gl + G * j) - p.rot_off;
-      if (at < 0 || at >= 2 * p.pairs) continue;
+      const int c = 8 * (gl + G * j) - p.rot_off;
+      if (c < 0 || c >= 2 * p.pairs) continue;
       if (p.half) {
-        const bool low = at < p.pairs;
-        const float* other = stage + (low ? at + p.pairs : at - p.pairs);
-        const float2* t = turns + (low ? at : at - p.pairs);
+        const bool low = c < p.pairs;
+        const float2* other = reinterpret_cast<const float2*>(stage + (low ? c + p.pairs : c - p.pairs));
+        const float4* t = reinterpret_cast<const float4*>(turns + (low ? c : c - p.pairs));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float a = low ? v[j][k] : other[k], b = low ? other[k] : v[j][k];
-          turn(a, b, t[k]);
-          v[j][k] = low ? a : b;
+        for (int k = 0; k < 4; ++k) {
+          const float4 t2 = t[k];  // (cos, sin) of two pairs
+          const float2 o = other[k];
+          float a0 = low ? v[j][k].x : o.x, b0 = low ? o.x : v[j][k].x, a1 = low ? v[j][k].y : o.y, b1 = low ? o.y : v[j][k].y;
+          turn(a0, b0, make_float2(t2.x, t2.y));
+          turn(a1, b1, make_float2(t2.z, t2.w));
+          v[j][k] = low ? make_float2(a0, a1) : make_float2(b0, b1);
         }
       } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) turn(v[j][2 * k], v[j][2 * k + 1], turns[at / 2 + k]);
+        for (int k = 0; k < 4; ++k) turn(v[j][k].x, v[j][k].y, turns[c / 2 + k]);
       }
     }
     // ---- out
     const bool keep = mine && (!p.dst || (to >= 0 && to < p.dst_count));
     if (p.dst && mine && to >= p.dst_count && gl == 0) record_error(p.err, DSA_DEVERR_INDEX_RANGE);
+    auto amax_of = [&](int j) {
+      float a = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a = fmaxf(a, fmaxf(fabsf(v[j][k].x), fabsf(v[j][k].y)));
+      return a;
+    };
+    auto codes = [&](int j, float s, float lo, float hi, bool fast) {
+      const float y[8] = {v[j][0].x, v[j][0].y, v[j][1].x, v[j][1].y, v[j][2].x, v[j][2].y, v[j][3].x, v[j][3].y};
+      return encode8(y, s, lo, hi, fast);
+    };
     if constexpr (FMT == kFmtBf16) {
       __nv_bfloat16* out = p.dst ? reinterpret_cast<__nv_bfloat16*>(p.dst + to * p.dst_row_stride)
                                  : p.out + row * p.out_row_stride + head * p.out_head_stride;
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
         const int c = gl + G * j;
-        if (keep && c < nch) *reinterpret_cast<uint4*>(out + 8 * c) = pack8(v[j]);
+        uint32_t u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(v[j][k].x, v[j][k].y);
+          u[k] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        if (keep && c < nch) *reinterpret_cast<uint4*>(out + 8 * c) = make_uint4(u[0], u[1], u[2], u[3]);
       }
     } else if constexpr (FMT == kFmtRow) {
       float a = 0.f;
 #pragma unroll
-      for (int j = 0; j < NCH; ++j) a = fmaxf(a, amax8(v[j]));
+      for (int j = 0; j < NCH; ++j) a = fmaxf(a, amax_of(j));
       a = max_across<G>(a);
       const Quotient div(a > 0.f ? __fdiv_rn(a, 448.f) : 1.f);
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
         const int c = gl + G * j;
         if (keep && c < nch)
-          *reinterpret_cast<uint2*>(p.dst + to * p.dst_row_stride + 8 * c) = encode8(v[j], div.s, div.r * kBelow, div.r * kAbove, div.fast);
+          *reinterpret_cast<uint2*>(p.dst + to * p.dst_row_stride + 8 * c) = codes(j, div.s, div.r * kBelow, div.r * kAbove, div.fast);
       }
       if (keep && gl == 0) reinterpret_cast<float*>(p.scale)[to] = div.s;
     } else if constexpr (FMT == kFmtTile) {
-      // a tile is a slot of 16 lanes; lane j of them takes slot j's scale and its reciprocal, once instead of NCH times
+      // A tile is a slot of 16 lanes, or two slots of 8.  Lane j of its lanes takes slot j's scale and its reciprocal, once
+      // instead of NCH times
       constexpr int T = G < 16 ? G : 16;
       const int tiles = (nch + 15) / 16;
       float own = 0.f;
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
-        const float a = max_across<T>(amax8(v[j]));
+        float a = amax_of(j);
+        if (G == 8 && (j ^ 1) < NCH) a = fmaxf(a, amax_of(j ^ 1));
+        a = max_across<T>(a);
         if (lane % T == j) own = a;
       }
       const Quotient div(own > 0.f ? __fdiv_rn(own, 448.f) : 1.f);
@@ -247,25 +263,24 @@ __global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_vec_kernel(const Rop
         const int c = gl + G * j, from = lane / T * T + j;
         const float s = __shfl_sync(0xffffffffu, div.s, from), rs = __shfl_sync(0xffffffffu, div.r, from);
         if (!keep || c >= nch) continue;
-        *reinterpret_cast<uint2*>(p.dst + to * p.dst_row_stride + 8 * c) = encode8(v[j], s, rs * kBelow, rs * kAbove, (fast >> from) & 1);
+        *reinterpret_cast<uint2*>(p.dst + to * p.dst_row_stride + 8 * c) = codes(j, s, rs * kBelow, rs * kAbove, (fast >> from) & 1);
         if (c % 16 == 0) reinterpret_cast<float*>(p.scale)[to * tiles + c / 16] = s;
       }
     } else {
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
         const int c = gl + G * j;
-        const float a = max_across<4>(amax8(v[j]));
+        const float a = max_across<4>(amax_of(j));
         if (!keep || c >= nch) continue;
         const int e = mx_exponent(a);
         const float inv = ldexpf(1.f, -e);  // a power of two: exact
+        const float2* y = v[j];
         *reinterpret_cast<uint2*>(p.dst + to * p.dst_row_stride + 8 * c) =
-            make_uint2(e4m3x4(v[j][0] * inv, v[j][1] * inv, v[j][2] * inv, v[j][3] * inv),
-                       e4m3x4(v[j][4] * inv, v[j][5] * inv, v[j][6] * inv, v[j][7] * inv));
+            make_uint2(e4m3x4(y[0].x * inv, y[0].y * inv, y[1].x * inv, y[1].y * inv),
+                       e4m3x4(y[2].x * inv, y[2].y * inv, y[3].x * inv, y[3].y * inv));
         if (c % 4 == 0) p.scale[to * (p.width / 32) + c / 4] = (uint8_t)(e + 127);
       }
     }
-    item = next;
-    pass = next_pass;
   }
 }
 
@@ -343,15 +358,17 @@ __global__ void __launch_bounds__(32 * kPlainWarps) norm_rope_kernel(const RopeP
 
 using NormKernel = void (*)(const RopeParams, const NormParams);
 
-// The vector form for a width: the fewest lanes that hold it at a chunk each, else a warp.
+// The vector form for a width: the lanes of a vector, and resident CTAs.
 template <int FMT>
-NormKernel vec_form(int width, int* lanes) {
-  *lanes = width <= 64 ? 8 : width <= 128 ? 16 : 32;
-  if (width <= 64) return norm_rope_vec_kernel<FMT, 8, 1>;
-  if (width <= 128) return norm_rope_vec_kernel<FMT, 16, 1>;
-  if (width <= 256) return norm_rope_vec_kernel<FMT, 32, 1>;
-  if (width <= 768) return norm_rope_vec_kernel<FMT, 32, 3>;
-  return norm_rope_vec_kernel<FMT, 32, 4>;
+NormKernel vec_form(int width, int* lanes, int* ctas) {
+  *lanes = width <= 256 ? 8 : width <= 640 ? 16 : 32;
+  *ctas = width <= 256 ? 3 : 2;
+  if (width <= 64) return norm_rope_vec_kernel<FMT, 8, 1, 3>;
+  if (width <= 128) return norm_rope_vec_kernel<FMT, 8, 2, 3>;
+  if (width <= 192) return norm_rope_vec_kernel<FMT, 8, 3, 3>;
+  if (width <= 256) return norm_rope_vec_kernel<FMT, 8, 4, 3>;
+  if (width <= 640) return norm_rope_vec_kernel<FMT, 16, 5, 2>;
+  return norm_rope_vec_kernel<FMT, 32, 4, 2>;
 }
 
 dsa_status norm_args(NormParams* n, const dsa_norm* norm, int width) {
@@ -383,9 +400,9 @@ dsa_status launch_norm(const RopeParams& p, NormParams n, bool vec, cudaStream_t
     const int64_t want = ((int64_t)p.rows * p.heads + kPlainWarps - 1) / kPlainWarps;
     norm_rope_kernel<FMT><<<(unsigned)(want < 8 * kSms ? want : 8 * kSms), 32 * kPlainWarps, 0, stream>>>(p, n);
   } else {
-    int lanes;
-    const NormKernel kern = vec_form<FMT>(p.width, &lanes);
-    const int per = 32 / lanes, most = 2 * kSms;
+    int lanes, ctas;
+    const NormKernel kern = vec_form<FMT>(p.width, &lanes, &ctas);
+    const int per = 32 / lanes, most = ctas * kSms;
     // heads of a row for a warp: all of up to 16, or as few as leave no warp idle
     n.heads_per_item = 16;
     while (n.heads_per_item > per && (int64_t)p.rows * ((p.heads + n.heads_per_item - 1) / n.heads_per_item) < (int64_t)most * kWarps)
