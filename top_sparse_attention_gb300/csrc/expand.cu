@@ -16,7 +16,7 @@
 #include <limits.h>
 #include <string.h>
 
-#include "dsa_internal.h"
+#include "tc_common.cuh"
 
 namespace dsa {
 namespace {
@@ -52,8 +52,8 @@ struct Cfg {
   static constexpr int BOX_B = NT / 2 * 128;       // half of a unit's weight rows, 64 columns
   static constexpr int STAGES = NT == 256 ? 4 : 8;
   static constexpr int OFF_B = kBoxes * kBoxA;
-  static constexpr int OFF_ST = OFF_B + STAGES * BOX_B;  // 4 KB per storing warp
-  static constexpr int OFF_AUX = OFF_ST + 4 * 4096;
+  static constexpr int OFF_ST = OFF_B + STAGES * BOX_B;  // two boxes of 32 rows x 64 columns per storing warp
+  static constexpr int OFF_AUX = OFF_ST + 4 * 2 * 4096;
   static constexpr int SMEM = OFF_AUX + (int)sizeof(Aux) + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -70,7 +70,7 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
       : "memory");
   return ok != 0;
 }
-__device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
+__device__ __noinline__ bool wait_pair_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
   const unsigned long long t0 = globaltimer_ns();
   for (uint32_t i = 0;; ++i) {
     if (try_wait_cluster(bar, parity)) return true;
@@ -83,8 +83,8 @@ __device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, i
     }
   }
 }
-__device__ __forceinline__ bool wait(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
-  return try_wait_cluster(bar, parity) || wait_slow(a, bar, parity, err);
+__device__ __forceinline__ bool wait_pair(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
+  return try_wait_cluster(bar, parity) || wait_pair_slow(a, bar, parity, err);
 }
 
 // The eight loading warps' barrier, and whether all of them are still well (so that all leave together).
@@ -174,7 +174,7 @@ __device__ __forceinline__ uint32_t scaled(uint32_t x, float s) { return bf16x2(
 
 template <int FMT, int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    expand_kernel(const __grid_constant__ CUtensorMap tm, const ExpandParams p) {
+    expand_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_out, const ExpandParams p) {
   using C = Cfg<NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -220,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int64_t u = u0; ok && u < u1; ++u) {
         const int y = (int)(u % per) * NT + rank * (NT / 2);
         for (int k = 0; k < kBoxes; ++k) {
-          ok = wait(a, &a->b_empty[s], ph ^ 1, err);
+          ok = wait_pair(a, &a->b_empty[s], ph ^ 1, err);
           if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(&a->b_full[s], 2 * C::BOX_B);
           tma_load_pair(b_s + s * C::BOX_B, &tm, dsmem_addr(&a->b_full[s], 0), 64 * k, y);
@@ -228,7 +228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       for (int i = 0; ok && i < C::STAGES; ++i) {  // the even CTA's last arrivals here have landed
-        ok = wait(a, &a->b_empty[s], ph ^ 1, err);
+        ok = wait_pair(a, &a->b_empty[s], ph ^ 1, err);
         if (++s == C::STAGES) s = 0, ph ^= 1;
       }
       if (*reinterpret_cast<volatile int*>(&a->abort) && rank == 0)  // wind down: copies in flight land first
@@ -242,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t a_desc = smem_desc_sw128(smem_u32(a_s)), b_desc = smem_desc_sw128(smem_u32(b_s));
       int s = 0, ph = 0, tiles = 0, unit = 0;
       bool ok = true;
-      auto all = [&](uint64_t* bar, uint32_t parity) { ok = __all_sync(0xffffffffu, wait(a, bar, parity, err)) && ok; };
+      auto all = [&](uint64_t* bar, uint32_t parity) { ok = __all_sync(0xffffffffu, wait_pair(a, bar, parity, err)) && ok; };
       for (int64_t u = u0; ok && u < u1; ++u, ++unit) {
         const bool first = u == u0 || u % per == 0, last = u + 1 == u1 || (u + 1) % per == 0;  // of its row tile
         const uint32_t d = tmem + (unit & 1) * NT;
@@ -302,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               v[k][i] = from[i] ? __ldg(reinterpret_cast<const uint4*>(from[i] + 128 * (k0 + k))) : make_uint4(0u, 0u, 0u, 0u);
-          if (k0 == 0) ok = __all_sync(0xffffffffu, wait(a, &a->a_empty, (tiles & 1) ^ 1, err));
+          if (k0 == 0) ok = __all_sync(0xffffffffu, wait_pair(a, &a->a_empty, (tiles & 1) ^ 1, err));
           if (!ok) break;  // (to the barrier below)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -343,7 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int k = 0; k < 5; ++k) f[i][k] = FMT == kFp8Tile && from[i] ? __ldg(sc[i] + k) : 1.f;
-        ok = __all_sync(0xffffffffu, wait(a, &a->a_empty, (tiles & 1) ^ 1, err));
+        ok = __all_sync(0xffffffffu, wait_pair(a, &a->a_empty, (tiles & 1) ^ 1, err));
 #pragma unroll
         for (int k = 0; ok && k < kBoxes; ++k) {
 #pragma unroll
@@ -377,16 +377,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       ok = loaders_ok(ok);  // and the rows' places have been read
     }
-    if (ok && u0 < u1) wait(a, &a->a_empty, (tiles & 1) ^ 1, err);  // the even CTA's last arrival here has landed
+    if (ok && u0 < u1) wait_pair(a, &a->a_empty, (tiles & 1) ^ 1, err);  // the even CTA's last arrival here has landed
   } else if (warp >= 12) {
-    // ---- read out: thread = row = tensor-memory lane
+    // ---- read out: thread = row = tensor-memory lane.  64 columns at a time go through shared memory, from where a TMA
+    // copy takes them, or, where some of the warp's rows are no sequence's, plain stores
     const int quarter = warp & 3;
-    uint8_t* stage = smem + C::OFF_ST + quarter * 4096;
+    uint8_t* stage = smem + C::OFF_ST + quarter * 2 * 4096;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
-    int unit = 0;
+    int unit = 0, piece = 0;
     bool ok = true;
     float s = 1.f;
     uint32_t live = 0;  // rows of this warp that are a sequence's
+    if (lane == 0) prefetch_tmap(&tm_out);
     for (int64_t u = u0; ok && u < u1; ++u, ++unit) {
       const int64_t base = (u / per) * (2 * kRowsCta) + rank * kRowsCta + 32 * quarter;
       if (u == u0 || u % per == 0) {
@@ -395,36 +397,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         live = __ballot_sync(0xffffffffu, src >= 0);
         if (FMT == kFp8Row) s = there ? __ldg(p.kv_scale + src) : 1.f;
       }
-      ok = __all_sync(0xffffffffu, wait(a, &a->acc_full[unit & 1], (unit >> 1) & 1, err));
+      ok = __all_sync(0xffffffffu, wait_pair(a, &a->acc_full[unit & 1], (unit >> 1) & 1, err));
       if (!ok) break;
       tc_fence_after();
-      __nv_bfloat16* out = p.out + base * ((int64_t)p.H * kOut) + (u % per) * NT;
+      const uint32_t acc = lane_base + (unit & 1) * NT;
+      const int col = (int)(u % per) * NT;
+      float v[2][32];
+      tmem_ld_issue(acc, v[0]);
 #pragma unroll 1
-      for (int c0 = 0; c0 < NT; c0 += 64) {
-        float v[2][32];
-        tmem_ld_sync(lane_base + (unit & 1) * NT + c0, v[0]);
-        tmem_ld_sync(lane_base + (unit & 1) * NT + c0 + 32, v[1]);
-        if (c0 + 64 == NT) {
-          tc_fence_before();
+      for (int c0 = 0; c0 < NT; c0 += 64, ++piece) {
+        uint8_t* box = stage + (piece & 1) * 4096;
+        // the copy out of this box two pieces ago has read it
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          tmem_ld_wait(v[h]);
+          if (c0 + 32 * h + 32 < NT) {
+            tmem_ld_issue(acc + c0 + 32 * h + 32, v[h ^ 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_even(&a->acc_empty[unit & 1]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float* x = &v[h][8 * k];
+            const float f = FMT == kFp8Row ? s : 1.f;
+            *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * h + k) ^ (lane & 7)) << 4)) =
+                make_uint4(bf16x2(x[0] * f, x[1] * f), bf16x2(x[2] * f, x[3] * f), bf16x2(x[4] * f, x[5] * f), bf16x2(x[6] * f, x[7] * f));
+          }
+        }
+        if (live == 0xffffffffu) {
+          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) arrive_even(&a->acc_empty[unit & 1]);
-        }
+          if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&tm_out), "r"(col + c0),
+                         "r"((int)base), "r"(smem_u32(box))
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else {
+          __syncwarp();
+          __nv_bfloat16* out = p.out + base * ((int64_t)p.H * kOut) + col + c0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float* x = &v[k >> 2][8 * (k & 3)];
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-              make_uint4(bf16x2(x[0] * s, x[1] * s), bf16x2(x[2] * s, x[3] * s), bf16x2(x[4] * s, x[5] * s), bf16x2(x[6] * s, x[7] * s));
+          for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + (lane >> 3), c = lane & 7;
+            const uint4 x = *reinterpret_cast<const uint4*>(box + r * 128 + ((c ^ (r & 7)) << 4));
+            if ((live >> r) & 1) *reinterpret_cast<uint4*>(out + r * ((int64_t)p.H * kOut) + 8 * c) = x;
+          }
         }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = 4 * k + (lane >> 3), c = lane & 7;
-          const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
-          if ((live >> r) & 1) *reinterpret_cast<uint4*>(out + r * ((int64_t)p.H * kOut) + c0 + 8 * c) = x;
-        }
-        __syncwarp();
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -446,13 +472,21 @@ cudaError_t launch_form(const ExpandParams& p, const void* w, cudaStream_t strea
   if (encode_tensor_map(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(w), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) !=
       CUDA_SUCCESS)
     return cudaErrorInvalidValue;
+  CUtensorMap tm_out;
+  const cuuint64_t out_dims[2] = {(cuuint64_t)p.H * kOut, (cuuint64_t)p.rows};
+  const cuuint64_t out_strides[1] = {(cuuint64_t)p.H * kOut * 2};
+  const cuuint32_t out_box[2] = {64, 32};
+  memset(&tm_out, 0, sizeof(tm_out));
+  if (encode_tensor_map(&tm_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out, out_dims, out_strides, out_box, CU_TENSOR_MAP_SWIZZLE_128B) !=
+      CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   auto kern = expand_kernel<FMT, NT>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem_once(&allowed, reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)((p.rows + 2 * kRowsCta - 1) / (2 * kRowsCta)) * (p.H * kOut / NT);
   const unsigned pairs = (unsigned)(units < kPairs ? units : kPairs);
-  return launch_kernel(kern, dim3(2 * pairs), dim3(kThreads), C::SMEM, stream, false, tm, p);
+  return launch_kernel(kern, dim3(2 * pairs), dim3(kThreads), C::SMEM, stream, false, tm, tm_out, p);
 }
 
 template <int FMT>

@@ -73,7 +73,8 @@ struct ExpandedAttnParams {
 };
 
 struct Aux {
-  uint64_t q_full[2], q_empty[2], full[kRing], empty[kRing], s_full[2], p_full[2], o_done[2], o_free[2], drain;
+  // (k and v: of tiles of positions of even and of odd number)
+  uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_ready[2], v_empty[2], s_full[2], p_full[2], o_done[2], o_free[2], drain[2];
   uint32_t tmem;
   int abort;
   int not_finite;  // an infinity or NaN was cleared from V
@@ -229,9 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&a->q_full[i], 1), mbar_init(&a->q_empty[i], 1);
       mbar_init(&a->s_full[i], 1), mbar_init(&a->p_full[i], 4);
       mbar_init(&a->o_done[i], 1), mbar_init(&a->o_free[i], 4);
+      mbar_init(&a->k_full[i], 1), mbar_init(&a->k_empty[i], 2);  // (both issuers)
+      mbar_init(&a->v_full[i], 1), mbar_init(&a->v_ready[i], 4), mbar_init(&a->v_empty[i], 2);
+      mbar_init(&a->drain[i], 1);
     }
-    for (int i = 0; i < kRing; ++i) mbar_init(&a->full[i], 1), mbar_init(&a->empty[i], 1);
-    mbar_init(&a->drain, 1);
     a->abort = 0;
     a->not_finite = 0;
     fence_mbar_init();
@@ -246,23 +248,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   Work w;
   Facts f;
   int head;
+  // Registers: 384 x 168 at launch; the softmax warps take what the others leave (128 x 88 + 256 x 208 = 64512)
   if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
       // ---- producer
       if (lane == 0) {
         prefetch_tmap(&tm_q), prefetch_tmap(&tm_k), prefetch_tmap(&tm_r), prefetch_tmap(&tm_v);
-        int s = 0, ph = 0, uses[2] = {0, 0};
+        int uses[2] = {0, 0};
+        int g = 0;  // tiles of positions so far; their boxes are 5 g (of K) ... 5 g + 4 (of V), in the ring's order
         bool ok = true;
-        auto box = [&](const CUtensorMap* tm, int x, int y, int z, bool flat) {
-          ok = ok && wait_ahead(a, &a->empty[s], ph ^ 1, err);
-          if (!ok) return;
-          mbar_arrive_expect_tx(&a->full[s], kBox);
-          if (flat) tma_load_2d(ring + s * kBox, tm, &a->full[s], x, z);
-          else tma_load_3d(ring + s * kBox, tm, &a->full[s], x, y, z);
-          if (++s == kRing) s = 0, ph ^= 1;
+        auto load = [&](const CUtensorMap* tm, uint64_t* bar, int box, int x, int z, bool flat) {
+          uint8_t* dst = ring + (uint32_t)box % kRing * kBox;
+          if (flat) tma_load_2d(dst, tm, bar, x, z);
+          else tma_load_3d(dst, tm, bar, x, head, z);
         };
+        auto done = [&](uint64_t* empty, int tile) { ok = ok && (tile < 0 || wait_here<50>(a, &empty[tile & 1], (tile >> 1) & 1, err)); };
         auto query = [&](int t) {
-          ok = ok && wait_ahead(a, &a->q_empty[t], (uses[t] & 1) ^ 1, err);
+          ok = ok && wait_here<50>(a, &a->q_empty[t], (uses[t] & 1) ^ 1, err);
           if (!ok) return;
           ++uses[t];
           mbar_arrive_expect_tx(&a->q_full[t], 3 * kBox);
@@ -271,111 +274,121 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int r = 0; ok && get_work(p, n_items, r, w, head, f); ++r) {
           const int n0 = tiles_for(f, w, 0), n1 = tiles_for(f, w, 1), n = max(n0, n1);
           if (n0) query(0);
-          for (int j = 0; ok && j < n; ++j) {
+          for (int j = 0; ok && j < n; ++j, ++g) {
             const int row = f.k_row + (w.t0 + j) * kTile;
-            box(&tm_k, 0, head, row, false);
-            box(&tm_k, 64, head, row, false);
-            box(&tm_r, 0, 0, row, true);
+            // the boxes of K take the places of the last one of K, and of V, two tiles ago
+            done(a->k_empty, g - 2);
+            if (!ok) break;
+            uint64_t* bar = &a->k_full[g & 1];
+            mbar_arrive_expect_tx(bar, 3 * kBox);
+            load(&tm_k, bar, 5 * g, 0, row, false);
+            done(a->v_empty, g - 2);
+            if (!ok) break;
+            load(&tm_k, bar, 5 * g + 1, 64, row, false);
+            load(&tm_r, bar, 5 * g + 2, 0, row, true);
             if (j == 0 && n1) query(1);
-            box(&tm_v, 0, head, row, false);
-            box(&tm_v, 64, head, row, false);
+            done(a->k_empty, g - 1);  // and V those of the first two of K of the last tile
+            if (!ok) break;
+            bar = &a->v_full[g & 1];
+            mbar_arrive_expect_tx(bar, 2 * kBox);
+            load(&tm_v, bar, 5 * g + 3, 0, row, false);
+            load(&tm_v, bar, 5 * g + 4, 64, row, false);
           }
         }
         if (*reinterpret_cast<volatile int*>(&a->abort)) {  // wind down: the copies in flight land first
-          for (int i = 0; i < kRing; ++i) mbar_wait(&a->full[i], i < s ? ph : ph ^ 1, err);
+          for (int i = max(g - 2, 0); i <= g; ++i) {        // (of a tile that was not armed there is nothing to wait for but time)
+            mbar_wait(&a->k_full[i & 1], (i >> 1) & 1, err);
+            mbar_wait(&a->v_full[i & 1], (i >> 1) & 1, err);
+          }
           for (int t = 0; t < 2; ++t) mbar_wait(&a->q_full[t], (uses[t] & 1) ^ 1, err);
         }
       }
       __syncwarp();
-    } else if (warp == 1) {
-      // ---- MMA issuer
+    } else if (warp <= 2) {
+      // ---- MMA issuers, a warp for each tile of queries.  Issuing an instruction waits for the ones before it, but for a few,
+      // and between two turns lie about 700 cycles of waits and arithmetic, in which the tensor cores would run dry: with two
+      // warps the other one's instructions fill them (8192-token prompt, one issuer and two: 266 and 217 us)
       constexpr uint32_t idesc_qk = make_idesc(1, 1, kTile, kTile);
-      constexpr uint32_t idesc_pv = make_idesc(1, 1, kTile, 64) | (1u << 16);  // B (values) MN-major
-      const uint32_t base = (uint32_t)uniform((int)tmem);
-      const uint32_t q_lo = kmajor_lo(smem_u32(smem)), k_lo = kmajor_lo(smem_u32(ring)), v_lo = mnmajor_lo(smem_u32(ring), kBox);
-      uint32_t at = 0;  // boxes before the tile of positions in hand
-      int used[2] = {0, 0}, soft[2] = {0, 0};  // items and softmax tiles of each tile of queries
+      constexpr uint32_t idesc_pv = idesc_qk | (1u << 16), idesc_pv64 = make_idesc(1, 1, kTile, 64) | (1u << 16);  // B (values) MN-major
+      const uint32_t t = warp - 1;
+      const uint32_t base = (uint32_t)uniform((int)tmem), col_s = base + kColS + kTile * t, col_o = base + kColO + kTile * t;
+      const uint32_t q_lo = kmajor_lo(smem_u32(smem)) + 3 * t * (kBox >> 4), k_lo = kmajor_lo(smem_u32(ring));
+      const uint32_t v_lo = mnmajor_lo(smem_u32(ring), kBox);
+      int g = 0;               // tiles of positions before the item
+      int used = 0, soft = 0;  // items and softmax tiles
       bool ok = true;
-      auto all = [&](uint64_t* bar, uint32_t parity) { ok = __all_sync(0xffffffffu, wait(a, bar, parity, err)) && ok; };
-      auto boxes_full = [&](uint32_t first, int n) {  // one lane per barrier
-        const uint32_t b = first + (lane < n ? lane : 0);
-        all(&a->full[b % kRing], (b / kRing) & 1);
-      };
-      auto release = [&](uint32_t first, int n) {
-        if (elect_one())
-          for (int i = 0; i < n; ++i) tc_commit(&a->empty[(first + i) % kRing]);
-        __syncwarp();
-      };
       for (int r = 0; ok && uniform(get_work(p, n_items, r, w, head, f)); ++r) {
-        const int n0 = uniform(tiles_for(f, w, 0)), n1 = uniform(tiles_for(f, w, 1)), n = max(n0, n1);
-        auto qk = [&](int t, int j) {  // S of tile t and positions j
-          const int nt = t ? n1 : n0;
-          const uint32_t kb = at + 5 * j;
-          boxes_full(kb, 3);
-          if (j == 0) all(&a->q_full[t], used[t] & 1);
-          if (!ok) return;
+        const int n0 = uniform(tiles_for(f, w, 0)), n1 = uniform(tiles_for(f, w, 1)), n = max(n0, n1), nt = t ? n1 : n0;
+        if (n == 0) continue;
+        // A turn: O += P V over positions j, and S of positions j + 1, as far as there are any.  One wait, a lane per barrier (a
+        // wait costs about 120 cycles even when there is nothing to wait for)
+        for (int j = -1; ok && j < n; ++j) {
+          const bool pv = j >= 0 && j < nt, qk = j + 1 < nt;
+          const int gv = g + j, gk = gv + 1;
+          const uint32_t v0 = (uint32_t)uniform((5 * gv + 3) & (kRing - 1)), V = v_lo + v0 * (kBox >> 4);
+          uint32_t B[3];
+#pragma unroll
+          for (int b = 0; b < 3; ++b) B[b] = k_lo + (uint32_t)uniform((5 * gk + b) & (kRing - 1)) * (kBox >> 4);
+          uint64_t* bar = j + 1 < n ? &a->k_full[gk & 1] : &a->v_full[gv & 1];
+          uint32_t parity = j + 1 < n ? (gk >> 1) & 1 : (gv >> 1) & 1;
+          if (j >= 0 && lane == 1) bar = &a->v_full[gv & 1], parity = (gv >> 1) & 1;
+          if (pv && lane == 2) bar = &a->p_full[t], parity = soft & 1;
+          if (pv && lane == 4) bar = &a->v_ready[gv & 1], parity = (gv >> 1) & 1;
+          if (pv && j == 0 && lane == 3) bar = &a->o_free[t], parity = (used & 1) ^ 1;
+          if (qk && j < 0 && lane == 3) bar = &a->q_full[t], parity = used & 1;
+          ok = __all_sync(0xffffffffu, wait_here(a, bar, parity, err)) && ok;
+          if (!ok) break;
+          soft += pv;
           tc_fence_after();
+          const uint32_t acc0 = j > 0 ? 1u : 0u;
           if (elect_one()) {
+            if (pv) {
+              if (v0 != kRing - 1) {
 #pragma unroll
-            for (int b = 0; b < 3; ++b) {
-              const uint32_t B = k_lo + ((kb + b) % kRing) * (kBox >> 4), A = q_lo + (3 * t + b) * (kBox >> 4);
+                for (int i = 0; i < 8; ++i) mma_ts(col_o, col_s + 8 * i, V + i * (2048 >> 4), idesc_pv, i ? 1u : acc0);
+              } else {  // value columns 64 .. 127 are in the ring's first box, not in the one behind
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mma_ss(base + kColS + kTile * t, A + 2 * i, B + 2 * i, idesc_qk, b || i ? 1u : 0u);
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    mma_ts(col_o + 64 * b, col_s + 8 * i, (b ? v_lo : V) + i * (2048 >> 4), idesc_pv64, i ? 1u : acc0);
+              }
+              tc_commit(&a->v_empty[gv & 1]);
+              if (j == nt - 1) tc_commit(&a->o_done[t]);
+            } else if (j >= 0) {
+              mbar_arrive(&a->v_empty[gv & 1]);
             }
-            tc_commit(&a->s_full[t]);
-            if (j == nt - 1) tc_commit(&a->q_empty[t]);
+            if (qk) {
+#pragma unroll
+              for (int b = 0; b < 3; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  mma_ss(col_s, q_lo + b * (kBox >> 4) + 2 * i, B[b] + 2 * i, idesc_qk, b || i ? 1u : 0u);
+              tc_commit(&a->s_full[t]);
+              tc_commit(&a->k_empty[gk & 1]);
+              if (j == nt - 2) tc_commit(&a->q_empty[t]);
+            } else if (j + 1 < n) {
+              mbar_arrive(&a->k_empty[gk & 1]);
+            }
           }
           __syncwarp();
-        };
-        auto pv = [&](int t, int j) {
-          const int nt = t ? n1 : n0;
-          const uint32_t vb = at + 5 * j + 3;
-          boxes_full(vb, 2);
-          all(&a->p_full[t], soft[t] & 1);
-          if (j == 0) all(&a->o_free[t], (used[t] & 1) ^ 1);
-          if (!ok) return;
-          ++soft[t];
-          tc_fence_after();
-          if (elect_one()) {
-            // value columns 0 .. 63 and 64 .. 127 are two boxes, which need not follow each other in the ring
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const uint32_t B = v_lo + ((vb + b) % kRing) * (kBox >> 4);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                mma_ts(base + kColO + kTile * t + 64 * b, base + kColS + kTile * t + 8 * i, B + i * (2048 >> 4), idesc_pv, j || i ? 1u : 0u);
-            }
-            if (j == nt - 1) tc_commit(&a->o_done[t]);
-          }
-          __syncwarp();
-        };
-        if (n0) qk(0, 0);
-        if (ok && n1) qk(1, 0);
-        if (ok && n) release(at, 3);
-        for (int j = 0; ok && j < n; ++j) {
-          if (j < n0) pv(0, j);
-          if (ok && j + 1 < n0) qk(0, j + 1);
-          if (ok && j < n1) pv(1, j);
-          if (ok) release(at + 5 * j + 3, 2);
-          if (ok && j + 1 < n1) qk(1, j + 1);
-          if (ok && j + 1 < n) release(at + 5 * (j + 1), 3);
         }
-        at += 5 * n;
-        used[0] += n0 > 0, used[1] += n1 > 0;
+        g += n;
+        used += nt > 0;
       }
       if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&a->abort))) {  // wind down: what was issued ends first
-        if (elect_one()) tc_commit(&a->drain);
+        if (elect_one()) tc_commit(&a->drain[t]);
         __syncwarp();
-        mbar_wait(&a->drain, 0, err);
+        mbar_wait(&a->drain[t], 0, err);
       }
     }
   } else {
     // ---- softmax: four warps for each tile of queries, a thread a row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = (warp >> 2) - 1, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
     const uint32_t col_s = lane_base + kColS + kTile * t, col_o = lane_base + kColO + kTile * t;
-    uint32_t at = 0;
-    int soft = 0, used = 0;
+    int g = 0, soft = 0, used = 0;
     bool ok = true;
     for (int r = 0; get_work(p, n_items, r, w, head, f); ++r) {
       const int n0 = tiles_for(f, w, 0), n1 = tiles_for(f, w, 1), n = t ? n1 : n0;
@@ -387,55 +400,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < n; ++j, ++soft) {
         const int pos = (w.t0 + j) * kTile;
         const bool edge = pos + kTile > least;
-        if (edge && (t == 0 || j >= n0)) {
-          // a thread a position: its values, where some row does not see it (the tile of later queries finds them so)
-          const uint32_t vb = at + 5 * j + 3;
-          ok = wait(a, &a->full[vb % kRing], (vb / kRing) & 1, err) && ok;
-          ok = wait(a, &a->full[(vb + 1) % kRing], ((vb + 1) / kRing) & 1, err) && ok;
-          const bool behind = pos + row >= f.n;
-          if (ok && pos + row >= least) {
-            bool found = false;
+        ok = wait_here(a, &a->s_full[t], soft & 1, err) && ok;
+        tc_fence_after();
+        if (t == 0 || j >= n0) {  // this tile of queries looks after V (an S that is finished means that the barrier's phase has begun)
+          const int gv = g + j;
+          if (edge) {
+            // a thread a position: its values, where some row does not see it (the tile of later queries finds them so)
+            const uint32_t vb = 5 * gv + 3;
+            ok = wait_here(a, &a->v_full[gv & 1], (gv >> 1) & 1, err) && ok;
+            const bool behind = pos + row >= f.n;
+            if (ok && pos + row >= least) {
+              bool found = false;
 #pragma unroll 1
-            for (int c = 0; c < 16; ++c) {
-              uint4* chunk = reinterpret_cast<uint4*>(ring + ((vb + (c >> 3)) % kRing) * kBox + row * 128 + (((c ^ row) & 7) << 4));
-              uint4 v = make_uint4(0u, 0u, 0u, 0u);
-              bool bad = behind;
-              if (!behind) {
-                v = *chunk;
-                uint32_t u[4] = {v.x, v.y, v.z, v.w};
+              for (int c = 0; c < 16; ++c) {
+                uint4* chunk = reinterpret_cast<uint4*>(ring + ((vb + (c >> 3)) % kRing) * kBox + row * 128 + (((c ^ row) & 7) << 4));
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                bool bad = behind;
+                if (!behind) {
+                  v = *chunk;
+                  uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  if ((u[q] & 0x7F80u) == 0x7F80u) u[q] &= 0xFFFF0000u, bad = true;
-                  if ((u[q] & 0x7F800000u) == 0x7F800000u) u[q] &= 0xFFFFu, bad = true;
+                  for (int q = 0; q < 4; ++q) {
+                    if ((u[q] & 0x7F80u) == 0x7F80u) u[q] &= 0xFFFF0000u, bad = true;
+                    if ((u[q] & 0x7F800000u) == 0x7F800000u) u[q] &= 0xFFFFu, bad = true;
+                  }
+                  v = make_uint4(u[0], u[1], u[2], u[3]);
+                  found |= bad;
                 }
-                v = make_uint4(u[0], u[1], u[2], u[3]);
-                found |= bad;
+                if (bad) *chunk = v;
               }
-              if (bad) *chunk = v;
+              if (found) *reinterpret_cast<volatile int*>(&a->not_finite) = 1;
+              fence_proxy_async_smem();
             }
-            if (found) *reinterpret_cast<volatile int*>(&a->not_finite) = 1;
-            fence_proxy_async_smem();
           }
           __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(&a->v_ready[gv & 1]);
         }
-        ok = wait(a, &a->s_full[t], soft & 1, err) && ok;
-        tc_fence_after();
         const int mine = see - pos;  // positions of the tile that this row sees
-        // S is read twice, for the maximum and for the weights: 128 values at once do not fit the registers
-        auto logits = [&](int c, float (&x)[32]) {
-          tmem_ld_sync(col_s + c, x);
+        auto hide = [&](int c, float (&x)[32]) {
           if (edge) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) x[k] = c + k < mine ? x[k] : -INFINITY;
           }
         };
+        float x[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_issue(col_s + 32 * c, x[c]);
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          float x[32];
-          logits(c, x);
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait(x[c]);
+          hide(32 * c, x[c]);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], x[k]);
+          for (int k = 0; k < 32; k += 2) mx[(k >> 1) & 3] = fmaxf(mx[(k >> 1) & 3], fmaxf(x[c][k], x[c][k + 1]));
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         if (__any_sync(0xffffffffu, top > m + kLazy)) {
@@ -461,18 +478,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 scale = make_float2(p.scale_log2, p.scale_log2), minus = make_float2(mu, mu);
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          float x[32];
-          logits(c, x);
+        for (int c = 0; c < 4; ++c) {
+          float(&y)[32] = x[c];
           uint32_t v[16];
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
-            const float2 y = ffma2(make_float2(x[k], x[k + 1]), scale, minus);
-            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+            const float2 z = ffma2(make_float2(y[k], y[k + 1]), scale, minus);
+            const float2 e = make_float2(ex2(z.x), ex2(z.y));
             sum = add2(sum, e);
             v[k >> 1] = pack_bf16(e.x, e.y);
           }
-          tmem_st16(col_s + c / 2, v);
+          tmem_st16(col_s + 16 * c, v);
         }
         l += sum.x + sum.y;
         tmem_wait_st();
@@ -480,12 +496,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive(&a->p_full[t]);
       }
-      at += 5 * max(n0, n1);
+      g += max(n0, n1);
       // ---- the rows' results
       const int chunks = tiles_of(sees(f, f.nrows - 1)) > p.chunk ? 2 : 1;  // (more than one)
       const bool live = i < f.nrows;
       if (n > 0) {
-        ok = wait(a, &a->o_done[t], used & 1, err) && ok;
+        ok = wait_here(a, &a->o_done[t], used & 1, err) && ok;
         tc_fence_after();
         ++used;
       }

@@ -38,7 +38,7 @@ __device__ __forceinline__ bool wait_ahead(Aux* a, uint64_t* bar, uint32_t parit
   return mbar_test(bar, parity) || wait_slow<50>(a, bar, parity, err);
 }
 template <int SLEEP, class Aux>
-__device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
+__device__ __forceinline__ bool wait_loop(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
   const unsigned long long t0 = globaltimer_ns();
   for (uint32_t i = 0;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -51,6 +51,17 @@ __device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, i
       return false;
     }
   }
+}
+
+template <int SLEEP, class Aux>
+__device__ __noinline__ bool wait_slow(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
+  return wait_loop<SLEEP>(a, bar, parity, err);
+}
+// The same without a call, for kernels that move registers between their warps (a called function would need the
+// registers that a caller may not have).
+template <int SLEEP = 0, class Aux>
+__device__ __forceinline__ bool wait_here(Aux* a, uint64_t* bar, uint32_t parity, int* err) {
+  return mbar_test(bar, parity) || wait_loop<SLEEP>(a, bar, parity, err);
 }
 
 // A value that is the same in all lanes, as one the compiler knows to be so (a warp-wide reduction writes
@@ -154,6 +165,30 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+
+// Tensor memory -> registers in two parts, so that the latency of a load can be spent on the values before it: `issue`
+// starts a load of 32 columns, `wait` ends all loads in flight.  `v` may be used after a wait that names it.
+__device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+        "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
+        "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
+                 "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+                 "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]),
+                 "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
 }
 
 }  // namespace
