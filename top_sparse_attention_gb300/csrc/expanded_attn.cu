@@ -118,6 +118,12 @@ __device__ __forceinline__ int tiles_for(const Facts& f, const Work& w, int t) {
   return max(min(w.t1, tiles_of(sees(f, min(f.nrows, (t + 1) * kTile) - 1))) - w.t0, 0);
 }
 
+// Tiles of positions of an item that are looked through for what some row does not see: of [0, n0) those past what the
+// block's first row sees, of [n0, n) those past what the second tile's first row sees.
+__device__ __forceinline__ int edges_of(const Facts& f, const Work& w, int n0, int n) {
+  return max(n0 - max(sees(f, 0) / kTile - w.t0, 0), 0) + max(n - max(sees(f, kTile) / kTile - w.t0, n0), 0);
+}
+
 // ---------------------------------------------------------------------------------------------
 // the list of work: blocks and their chunks, the longest first (a counting sort by tiles; which of two of equal length
 // comes first does not matter to the results)
@@ -316,10 +322,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t v_lo = mnmajor_lo(smem_u32(ring), kBox);
       int g = 0;               // tiles of positions before the item
       int used = 0, soft = 0;  // items and softmax tiles
+      int edges = 0;           // tiles of positions that were looked through
       bool ok = true;
       for (int r = 0; ok && uniform(get_work(p, n_items, r, w, head, f)); ++r) {
         const int n0 = uniform(tiles_for(f, w, 0)), n1 = uniform(tiles_for(f, w, 1)), n = max(n0, n1), nt = t ? n1 : n0;
         if (n == 0) continue;
+        const int least0 = sees(f, 0), least1 = sees(f, kTile);
         // A turn: O += P V over positions j, and S of positions j + 1, as far as there are any.  One wait, a lane per barrier (a
         // wait costs about 120 cycles even when there is nothing to wait for)
         for (int j = -1; ok && j < n; ++j) {
@@ -333,12 +341,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t parity = j + 1 < n ? (gk >> 1) & 1 : (gv >> 1) & 1;
           if (j >= 0 && lane == 1) bar = &a->v_full[gv & 1], parity = (gv >> 1) & 1;
           if (pv && lane == 2) bar = &a->p_full[t], parity = soft & 1;
-          if (pv && lane == 4) bar = &a->v_ready[gv & 1], parity = (gv >> 1) & 1;
+          // V is looked through where a row of the first tile that takes it does not see all of it
+          const bool edge = j >= 0 && (w.t0 + j + 1) * kTile > (j < n0 ? least0 : least1);
+          if (pv && edge && lane == 4) bar = &a->v_ready[edges & 1], parity = (edges >> 1) & 1;
           if (pv && j == 0 && lane == 3) bar = &a->o_free[t], parity = (used & 1) ^ 1;
           if (qk && j < 0 && lane == 3) bar = &a->q_full[t], parity = used & 1;
           ok = __all_sync(0xffffffffu, wait_here(a, bar, parity, err)) && ok;
           if (!ok) break;
           soft += pv;
+          edges += edge;
           tc_fence_after();
           const uint32_t acc0 = j > 0 ? 1u : 0u;
           if (elect_one()) {
@@ -388,13 +399,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = (warp >> 2) - 1, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
     const uint32_t col_s = lane_base + kColS + kTile * t, col_o = lane_base + kColO + kTile * t;
-    int g = 0, soft = 0, used = 0;
+    int g = 0, soft = 0, used = 0, edges = 0;
     bool ok = true;
     for (int r = 0; get_work(p, n_items, r, w, head, f); ++r) {
       const int n0 = tiles_for(f, w, 0), n1 = tiles_for(f, w, 1), n = t ? n1 : n0;
       const int i = kTile * t + row;                             // row of the block
       const int see = i < f.nrows ? sees(f, i) : 0;              // positions that it sees
       const int least = sees(f, kTile * t);                      // positions that every row of this tile sees
+      const int least0 = sees(f, 0), edges0 = edges;
       const int64_t out_row = (int64_t)(f.q_row + w.q0 + i) * p.H + head;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++soft) {
@@ -402,9 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool edge = pos + kTile > least;
         ok = wait_here(a, &a->s_full[t], soft & 1, err) && ok;
         tc_fence_after();
-        if (t == 0 || j >= n0) {  // this tile of queries looks after V (an S that is finished means that the barrier's phase has begun)
+        if (pos + kTile > (j < n0 ? least0 : least)) {
           const int gv = g + j;
-          if (edge) {
+          if (t == 0 || j >= n0) {
             // a thread a position: its values, where some row does not see it (the tile of later queries finds them so)
             const uint32_t vb = 5 * gv + 3;
             ok = wait_here(a, &a->v_full[gv & 1], (gv >> 1) & 1, err) && ok;
@@ -432,9 +444,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (found) *reinterpret_cast<volatile int*>(&a->not_finite) = 1;
               fence_proxy_async_smem();
             }
+            __syncwarp();
+            // (of two tiles in turn: an S that is finished means that the one before the last has been multiplied)
+            if (lane == 0 && ok) mbar_arrive(&a->v_ready[edges & 1]);
           }
-          __syncwarp();
-          if (lane == 0 && ok) mbar_arrive(&a->v_ready[gv & 1]);
+          ++edges;
         }
         const int mine = see - pos;  // positions of the tile that this row sees
         auto hide = [&](int c, float (&x)[32]) {
@@ -476,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float mu = m == -INFINITY ? 0.f : -m;
         const float2 scale = make_float2(p.scale_log2, p.scale_log2), minus = make_float2(mu, mu);
-        float2 sum = make_float2(0.f, 0.f);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float(&y)[32] = x[c];
@@ -485,18 +499,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 32; k += 2) {
             const float2 z = ffma2(make_float2(y[k], y[k + 1]), scale, minus);
             const float2 e = make_float2(ex2(z.x), ex2(z.y));
-            sum = add2(sum, e);
+            sum[k >> 1 & 1] = add2(sum[k >> 1 & 1], e);
             v[k >> 1] = pack_bf16(e.x, e.y);
           }
           tmem_st16(col_s + 16 * c, v);
         }
-        l += sum.x + sum.y;
+        l += sum[0].x + sum[0].y + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive(&a->p_full[t]);
       }
       g += max(n0, n1);
+      edges = edges0 + edges_of(f, w, n0, max(n0, n1));
       // ---- the rows' results
       const int chunks = tiles_of(sees(f, f.nrows - 1)) > p.chunk ? 2 : 1;  // (more than one)
       const bool live = i < f.nrows;
