@@ -45,7 +45,7 @@ constexpr int kBlock = 2 * kTile;
 constexpr int kBox = kTile * 128;           // 64 columns of 128 rows
 constexpr int kRing = 8;
 constexpr int kOffRing = 6 * kBox;          // two tiles of Q first
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr float kLazy = 8.f;                // log2 growth of a row's maximum that is left unscaled
 constexpr int kSms = 152;
 constexpr int kMaxChunk = 512, kMinChunk = 4;  // tiles
@@ -78,9 +78,10 @@ struct Aux {
   uint32_t tmem;
   int abort;
   int not_finite;  // an infinity or NaN was cleared from V
+  float rows[2][2][kTile];  // per tile of queries and half of the positions: the rows' maxima, at an item's end their sums
 };
 constexpr int kOffAux = kOffRing + kRing * kBox;
-constexpr int kSmem = kOffAux + (int)sizeof(Aux) + 1024;
+constexpr int kSmem = kOffAux + (int)sizeof(Aux);  // (without room to align: the array's own alignment does it)
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 struct Work {
@@ -220,8 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     expanded_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v,
                          const ExpandedAttnParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + kOffRing;
   Aux* a = reinterpret_cast<Aux*>(smem + kOffAux);
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
@@ -234,10 +234,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 32) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&a->q_full[i], 1), mbar_init(&a->q_empty[i], 1);
-      mbar_init(&a->s_full[i], 1), mbar_init(&a->p_full[i], 4);
-      mbar_init(&a->o_done[i], 1), mbar_init(&a->o_free[i], 4);
+      mbar_init(&a->s_full[i], 1), mbar_init(&a->p_full[i], 8);
+      mbar_init(&a->o_done[i], 1), mbar_init(&a->o_free[i], 8);
       mbar_init(&a->k_full[i], 1), mbar_init(&a->k_empty[i], 2);  // (both issuers)
-      mbar_init(&a->v_full[i], 1), mbar_init(&a->v_ready[i], 4), mbar_init(&a->v_empty[i], 2);
+      mbar_init(&a->v_full[i], 1), mbar_init(&a->v_ready[i], 8), mbar_init(&a->v_empty[i], 2);
       mbar_init(&a->drain[i], 1);
     }
     a->abort = 0;
@@ -254,9 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   Work w;
   Facts f;
   int head;
-  // Registers: 384 x 168 at launch; the softmax warps take what the others leave (128 x 88 + 256 x 208 = 64512)
+  // Registers: 640 x 96 at launch; the softmax warps take what the others leave (128 x 64 + 512 x 104 = 61440)
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
       // ---- producer
       if (lane == 0) {
@@ -312,8 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp <= 2) {
       // ---- MMA issuers, a warp for each tile of queries.  Issuing an instruction waits for the ones before it, but for a few,
-      // and between two turns lie about 700 cycles of waits and arithmetic, in which the tensor cores would run dry: with two
-      // warps the other one's instructions fill them (8192-token prompt, one issuer and two: 266 and 217 us)
+      // and between two turns lie about 700 cycles of waits and arithmetic, in which the tensor cores run dry: with two warps
+      // the other one's instructions fill them.  (8192-token prompt: one issuer 266 us, two 237.  Strict turns, which keep one
+      // tile's products against the other's softmax: 244.)
       constexpr uint32_t idesc_qk = make_idesc(1, 1, kTile, kTile);
       constexpr uint32_t idesc_pv = idesc_qk | (1u << 16), idesc_pv64 = make_idesc(1, 1, kTile, 64) | (1u << 16);  // B (values) MN-major
       const uint32_t t = warp - 1;
@@ -394,11 +395,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---- softmax: four warps for each tile of queries, a thread a row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int t = (warp >> 2) - 1, quarter = warp & 3, row = 32 * quarter + lane;
+    // ---- softmax: eight warps for each tile of queries, a thread a row and half of the positions (four, a thread a row and
+    // all of them: 239 us for the 8192-token prompt instead of 237, 17.8 for the short ones instead of 16.7)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int t = (warp - 4) >> 3, h = (warp >> 2 & 1) ^ 1, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
-    const uint32_t col_s = lane_base + kColS + kTile * t, col_o = lane_base + kColO + kTile * t;
+    const uint32_t col_s = lane_base + kColS + kTile * t + 64 * h, col_p = lane_base + kColS + kTile * t + 32 * h;
+    const uint32_t col_o = lane_base + kColO + kTile * t + 64 * h;
+    auto pair_bar = [&]() {  // the two warps that share 32 rows
+      __syncwarp();
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * t + quarter) : "memory");
+    };
     int g = 0, soft = 0, used = 0, edges = 0;
     bool ok = true;
     for (int r = 0; get_work(p, n_items, r, w, head, f); ++r) {
@@ -417,15 +424,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (pos + kTile > (j < n0 ? least0 : least)) {
           const int gv = g + j;
           if (t == 0 || j >= n0) {
-            // a thread a position: its values, where some row does not see it (the tile of later queries finds them so)
+            // a thread a position: half of its values, where some row does not see it (the tile of later queries finds them so)
             const uint32_t vb = 5 * gv + 3;
             ok = wait_here(a, &a->v_full[gv & 1], (gv >> 1) & 1, err) && ok;
             const bool behind = pos + row >= f.n;
             if (ok && pos + row >= least) {
               bool found = false;
 #pragma unroll 1
-              for (int c = 0; c < 16; ++c) {
-                uint4* chunk = reinterpret_cast<uint4*>(ring + ((vb + (c >> 3)) % kRing) * kBox + row * 128 + (((c ^ row) & 7) << 4));
+              for (int c = 0; c < 8; ++c) {
+                uint4* chunk = reinterpret_cast<uint4*>(ring + ((vb + h) % kRing) * kBox + row * 128 + (((c ^ row) & 7) << 4));
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
                 bool bad = behind;
                 if (!behind) {
@@ -454,21 +461,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto hide = [&](int c, float (&x)[32]) {
           if (edge) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = c + k < mine ? x[k] : -INFINITY;
+            for (int k = 0; k < 32; ++k) x[k] = 64 * h + c + k < mine ? x[k] : -INFINITY;
           }
         };
-        float x[4][32];
+        float x[2][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_issue(col_s + 32 * c, x[c]);
+        for (int c = 0; c < 2; ++c) tmem_ld_issue(col_s + 32 * c, x[c]);
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           tmem_ld_wait(x[c]);
           hide(32 * c, x[c]);
 #pragma unroll
           for (int k = 0; k < 32; k += 2) mx[(k >> 1) & 3] = fmaxf(mx[(k >> 1) & 3], fmaxf(x[c][k], x[c][k + 1]));
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        a->rows[t][h][row] = mx[0];
+        pair_bar();  // (and both halves of S have been read: P may take their place)
+        const float top = fmaxf(mx[0], a->rows[t][h ^ 1][row]) * p.scale_log2;
         if (__any_sync(0xffffffffu, top > m + kLazy)) {
           float g = 1.f;
           if (top > m + kLazy) {  // (m = -inf: nothing summed yet, the factor is 0)
@@ -478,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (j > 0) {
 #pragma unroll 1
-            for (int c = 0; c < kDv; c += 16) {
+            for (int c = 0; c < kDv / 2; c += 16) {
               float o[16];
               tmem_ld_sync(col_o + c, o);
               uint32_t v[16];
@@ -492,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 scale = make_float2(p.scale_log2, p.scale_log2), minus = make_float2(mu, mu);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           float(&y)[32] = x[c];
           uint32_t v[16];
 #pragma unroll
@@ -502,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum[k >> 1 & 1] = add2(sum[k >> 1 & 1], e);
             v[k >> 1] = pack_bf16(e.x, e.y);
           }
-          tmem_st16(col_s + 16 * c, v);
+          tmem_st16(col_p + 16 * c, v);
         }
         l += sum[0].x + sum[0].y + (sum[1].x + sum[1].y);
         tmem_wait_st();
@@ -520,9 +530,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         ++used;
       }
+      a->rows[t][h][row] = l;  // (O is finished: the maxima of the last tile have been read)
+      pair_bar();
+      l = a->rows[t][0][row] + a->rows[t][1][row];
       const float inv = l != 0.f ? 1.f / l : 0.f;
       const int part = w.t0 / p.chunk;
-      if (live) {
+      if (live && h == 0) {
         if (chunks > 1) p.part_ml[(int64_t)part * p.T * p.H + out_row] = make_float2(m, l);
         else if (p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
@@ -530,10 +543,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cleared = sees(f, 0) / kTile * kTile;
       const bool odd = n > 0 && *reinterpret_cast<volatile int*>(&a->not_finite);
 #pragma unroll 1
-      for (int c = 0; c < kDv; c += 32) {
+      for (int c0 = 0; c0 < kDv / 2; c0 += 32) {
+        const int c = 64 * h + c0;
         float o[32];
         if (n > 0) {
-          tmem_ld_sync(col_o + c, o);
+          tmem_ld_sync(col_o + c0, o);
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0.f;
@@ -566,6 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
+      pair_bar();  // the sums have been read
       if (n > 0) {
         tc_fence_before();
         __syncwarp();
