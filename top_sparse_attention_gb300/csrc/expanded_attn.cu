@@ -24,11 +24,12 @@
 //
 // Work: blocks of 256 queries x chunks of `chunk` tiles of positions, longest first (plan_kernel: the lengths are on the
 // device), each for every head, dealt to the CTAs back and forth.  Blocks of more than one chunk leave fp32 partial
-// results, merged by merge_kernel.  Chunks of 512 tiles at most: the tensor cores truncate their sums, and O would lose
+// results, merged by the CTA that finishes the last of them (spans) or by merge_chunks_kernel.  Chunks of 512 tiles at most: the tensor cores truncate their sums, and O would lose
 // 2^-24 of itself per step (0.04 % over 65536 positions).
 //
 // Bound: tensor cores, 12 x 64 + 8 x 64 cycles per tile of 128 x 128.
 #include <limits.h>
+#include <stddef.h>
 #include <string.h>
 
 #include <initializer_list>
@@ -49,8 +50,26 @@ constexpr int kThreads = 640;
 constexpr float kLazy = 8.f;                // log2 growth of a row's maximum that is left unscaled
 constexpr int kSms = 152;
 constexpr int kMaxChunk = 512, kMinChunk = 4;  // tiles
+constexpr int kFixed = 3;                      // what starting on a block costs, in tiles
+constexpr int kMinSpan = 4;
 constexpr int kMaxSeq = 4096;
 constexpr uint32_t kColS = 0, kColO = 256;
+
+// What the planning kernel leaves for the others.
+constexpr int kSpanItems = 3 * kSms;         // fewer than this many blocks and heads may be cut into spans
+struct alignas(16) SpanItem {  // (read as two 16-byte words)
+  int seq, q0, t0, t1, head, slot;  // slot: of the partial result, -1: the whole block
+  int parts;                        // of this head of the block (0: nothing to do, no tile of it is in this span)
+  int first;                        // span of the first of them
+};
+struct Plan {
+  int n_work, spans;
+  int done[kSpanItems][2];                   // parts that are finished, of each block and head and each tile of queries
+  int2 place[kSms];                           // of each CTA's items in the list: first, number
+  SpanItem list[kSpanItems + kSms];
+};
+
+static_assert(sizeof(SpanItem) == 32 && offsetof(Plan, list) % 16 == 0 && offsetof(Plan, place) % 8 == 0, "vector reads");
 
 struct ExpandedAttnParams {
   const int32_t* q_start;  // [n_seq + 1]
@@ -64,10 +83,13 @@ struct ExpandedAttnParams {
   __nv_bfloat16* out;      // [T, H, 128]
   float* lse;              // [T, H] or null
   int chunk;               // tiles of 128 positions
+  int grid;                // CTAs of the attention kernel
+  bool may_span;           // blocks may be cut into spans (see plan_kernel)
+  // workspace
+  Plan* plan;
+  int4* work;              // [max_work]
   int max_work;
-  int* n_work;             // workspace: the list of work, partial results [chunks][T][H]
-  int4* work;
-  float2* part_ml;
+  float2* part_ml;         // partial results: reference maximum and sum of weights, output
   float* part_o;
   int* err;                // device error word
 };
@@ -78,6 +100,7 @@ struct Aux {
   uint32_t tmem;
   int abort;
   int not_finite;  // an infinity or NaN was cleared from V
+  int last[2];     // this CTA has finished the last part of a tile's rows
   float rows[2][2][kTile];  // per tile of queries and half of the positions: the rows' maxima, at an item's end their sums
 };
 constexpr int kOffAux = kOffRing + kRing * kBox;
@@ -86,6 +109,10 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 
 struct Work {
   int seq, q0, t0, t1;  // queries q0 ... of the sequence, tiles [t0, t1) of positions
+  int64_t part;         // row of the partial results of the first query, -1: the whole block, written to the output
+  int step;             // between the queries' rows of partial results
+  int parts, first;     // of a block that is cut into spans (0 parts: nothing to do)
+  int item;             // its number
 };
 
 struct Facts {
@@ -169,16 +196,104 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
   if (tid == 0) base[p.n_seq] = run;
   for (int i = tid; i <= kMaxChunk; i += 1024) place[i] = 0;
   __syncthreads();
+  auto find = [&](int b, int& q0) {  // the sequence of block b, and the block's first query
+    int lo = 0, hi = p.n_seq - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (base[mid] <= b) lo = mid;
+      else hi = mid - 1;
+    }
+    q0 = (b - base[lo]) * kBlock;
+    return lo;
+  };
+  if (p.may_span && (int64_t)run * p.H < 3 * p.grid) {
+    // Few blocks: laid end to end, a head of a block after another, each with a fixed cost before its tiles, and cut into one
+    // span for each CTA, if that is shorter than dealing them out whole
+    int q0 = 0, seq = 0, tiles = 0;
+    if (tid < run) {
+      seq = find(tid, q0);
+      tiles = block_tiles(block_facts(p, seq, q0));
+    }
+    const int cost = tid < run ? tiles + kFixed : 0;
+    int incl = cost, most = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    __shared__ int warp_most[32], before[kSpanItems + 1];  // (costs before each block, of one head)
+    if (lane == 31) warp_sum[warp] = incl, warp_most[warp] = most;
+    __syncthreads();
+    int ahead = 0, all = 0, longest = 0;
+    for (int i = 0; i < 32; ++i) {
+      ahead += i < warp ? warp_sum[i] : 0;
+      all += warp_sum[i];
+      longest = max(longest, warp_most[i]);
+    }
+    if (tid < run) before[tid] = ahead + incl - cost;
+    if (tid == run) before[run] = all;
+    __syncthreads();
+    const int items = run * p.H, total = all * p.H, W = max((total + p.grid - 1) / p.grid, 1);  // (below 2^25)
+    const int whole = items <= p.grid ? longest : total / p.grid + longest / 2;
+    if (W >= kMinSpan && W + 2 * kFixed < whole) {
+      if (tid == 0) p.plan->spans = 1;
+      // The order: a sequence after another, of it a head after another, of that the blocks, so that the CTAs that read the
+      // same keys and values are neighbours and do so at about the same time (two chunks of 1125 tokens over 12K positions,
+      // 200 MB of keys and values: 260 us with the heads of a block side by side)
+      auto seq_at = [&](auto&& start, int x) {  // the last sequence that starts at or before x
+        int lo = 0, hi = p.n_seq - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (start(mid) <= x) lo = mid;
+          else hi = mid - 1;
+        }
+        return lo;
+      };
+      auto item_at = [&](int x) {  // that holds cost x
+        const int s = seq_at([&](int i) { return before[base[i]] * p.H; }, x), b0 = base[s], nb = base[s + 1] - b0;
+        const int sum = before[b0 + nb] - before[b0], in = x - before[b0] * p.H, h = in / sum;
+        int b = 0;
+        while (b + 1 < nb && before[b0 + b + 1] - before[b0] <= in - h * sum) ++b;
+        return b0 * p.H + h * nb + b;
+      };
+      if (tid < p.grid) {
+        const int x0 = tid * W, x1 = min(x0 + W, total);
+        int2 mine = make_int2(0, 0);
+        if (x0 < total) {
+          const int i0 = item_at(x0);
+          mine = make_int2(i0 + tid, item_at(x1 - 1) - i0 + 1);
+        }
+        p.plan->place[tid] = mine;
+      }
+      if (tid < items) {  // an item's pieces: entry of item i in span k: i + k
+        const int s = seq_at([&](int i) { return base[i] * p.H; }, tid), b0 = base[s], nb = base[s + 1] - b0;
+        const int head = (tid - b0 * p.H) / nb, b = b0 + (tid - b0 * p.H) % nb;
+        SpanItem it = {};
+        it.seq = s;
+        it.q0 = (b - b0) * kBlock;
+        it.head = head;
+        p.plan->done[tid][0] = p.plan->done[tid][1] = 0;
+        const int c = before[b + 1] - before[b], n = c - kFixed;
+        const int begin = before[b0] * p.H + head * (before[b0 + nb] - before[b0]) + before[b] - before[b0], first = begin + kFixed;
+        it.first = first / W;
+        for (int k = begin / W; k <= (begin + c - 1) / W; ++k) {
+          it.t0 = min(max(k * W - first, 0), n), it.t1 = max(min((k + 1) * W - first, n), it.t0);
+          it.slot = it.t0 == 0 && it.t1 == n ? -1 : it.t0 == 0 ? 2 * k + 1 : 2 * k;
+          it.parts = (n > 0 ? it.t0 == it.t1 : k != begin / W) ? 0 : n > 0 ? (first + n - 1) / W - first / W + 1 : 1;
+          p.plan->list[tid + k] = it;
+        }
+      }
+      return;
+    }
+  }
+  if (tid == 0) p.plan->spans = 0;
+  // Blocks and their chunks, the longest first
   // pass 0 counts, pass 1 places
   for (int pass = 0; pass < 2; ++pass) {
     for (int b = tid; b < run; b += 1024) {
-      int lo = 0, hi = p.n_seq - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (base[mid] <= b) lo = mid;
-        else hi = mid - 1;
-      }
-      const int q0 = (b - base[lo]) * kBlock;
+      int q0;
+      const int lo = find(b, q0);
       const int n = block_tiles(block_facts(p, lo, q0));
       int t0 = 0;
       do {
@@ -190,15 +305,21 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
     }
     __syncthreads();
     if (pass == 0) {
-      if (tid == 0) {
-        int sum = 0;
-        for (int i = kMaxChunk; i >= 0; --i) {
-          const int c = place[i];
-          place[i] = sum;
-          sum += c;
-        }
-        *p.n_work = min(sum, p.max_work);
+      // how many are longer, for each length: the running sum from the longest on
+      static_assert(kMaxChunk < 1024, "a thread a length");
+      const int at = kMaxChunk - tid, c = at >= 0 ? place[at] : 0;
+      int incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
       }
+      if (lane == 31) warp_sum[warp] = incl;
+      __syncthreads();
+      int ahead = 0;
+      for (int i = 0; i < warp; ++i) ahead += warp_sum[i];
+      if (at >= 0) place[at] = ahead + incl - c;
+      if (at == 0) p.plan->n_work = min(ahead + incl, p.max_work);
       __syncthreads();
     }
   }
@@ -206,15 +327,79 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
 
 // ---------------------------------------------------------------------------------------------
 
-__device__ __forceinline__ bool get_work(const ExpandedAttnParams& p, int64_t n_items, int r, Work& w, int& head, Facts& f) {
+// Item r of this CTA: of its span's list, or of the list of work, dealt back and forth, every head of an entry after another.
+struct Mine {
+  bool spans;
+  int first;      // in the span's list
+  int64_t items;  // in it, or all of them
+};
+__device__ __forceinline__ bool get_work(const ExpandedAttnParams& p, const Mine& mine, int r, Work& w, int& head, Facts& f) {
+  if (mine.spans) {
+    if (r >= mine.items) return false;
+    const int4* v = reinterpret_cast<const int4*>(p.plan->list + mine.first + r);
+    const int4 a = v[0], b = v[1];
+    w.seq = a.x, w.q0 = a.y, w.t0 = a.z, w.t1 = a.w, w.parts = b.z, w.first = b.w;
+    w.item = mine.first + r - (int)blockIdx.x;  // (entry of item i in span k: i + k)
+    head = b.x;
+    w.part = b.y < 0 ? -1 : (int64_t)b.y * kBlock, w.step = 1;
+    f = block_facts(p, w.seq, w.q0);
+    return true;
+  }
   const int g = (int)gridDim.x, c = (int)blockIdx.x;
   const int64_t i = (int64_t)r * g + (r & 1 ? g - 1 - c : c);
-  if (i >= n_items) return false;
+  if (i >= mine.items) return false;
   const int4 v = p.work[i / p.H];
   head = (int)(i % p.H);
-  w.seq = v.x, w.q0 = v.y, w.t0 = v.z, w.t1 = v.w;
+  w.seq = v.x, w.q0 = v.y, w.t0 = v.z, w.t1 = v.w, w.parts = 1, w.first = 0, w.item = 0;
   f = block_facts(p, w.seq, w.q0);
+  w.part = block_tiles(f) > p.chunk ? ((int64_t)(w.t0 / p.chunk) * p.T + f.q_row + w.q0) * p.H + head : -1;
+  w.step = p.H;
   return true;
+}
+
+// Merge of partial results: out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.  A warp takes a row, a lane four columns.
+__device__ __forceinline__ void write_merged(const ExpandedAttnParams& p, int64_t row, float M, float l, float4 o) {
+  const int lane = threadIdx.x & 31;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  reinterpret_cast<uint2*>(p.out + row * kDv)[lane] = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+}
+
+// Rows [from, from + 128) of a block that was cut into spans, by eight warps, four rows of each at a time, the parts in order.
+__device__ __forceinline__ void merge_parts(const ExpandedAttnParams& p, const Work& w, const Facts& f, int head, int from, int warp) {
+  constexpr int U = 4;
+  const int lane = threadIdx.x & 31;
+  for (int i0 = from + U * warp; i0 < min(from + kTile, f.nrows); i0 += 8 * U) {
+    float M[U], l[U];
+    float4 o[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) M[u] = -INFINITY, l[u] = 0.f, o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q = 0; q < w.parts; ++q) {
+      // the first part ends a span (its second slot), the others begin the spans behind it
+      const int64_t slot = 2 * (w.first + q) + (q == 0);
+      float2 ml[U];
+      float4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t row = slot * kBlock + min(i0 + u, f.nrows - 1);
+        ml[u] = __ldcg(p.part_ml + row);
+        v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + row * kDv) + lane);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (ml[u].y == 0.f) continue;  // the row saw nothing there
+        const float Mb = fmaxf(M[u], ml[u].x), mu = Mb == -INFINITY ? 0.f : Mb;
+        const float a = exp2f(M[u] - mu), g = exp2f(ml[u].x - mu);
+        M[u] = Mb;
+        l[u] = fmaf(g, ml[u].y, l[u] * a);
+        o[u].x = fmaf(g, v[u].x, o[u].x * a), o[u].y = fmaf(g, v[u].y, o[u].y * a);
+        o[u].z = fmaf(g, v[u].z, o[u].z * a), o[u].w = fmaf(g, v[u].w, o[u].w * a);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u < f.nrows) write_merged(p, (int64_t)(f.q_row + w.q0 + i0 + u) * p.H + head, M[u], l[u], o[u]);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -249,7 +434,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = a->tmem;
   pdl_wait();  // the plan
-  const int64_t n_items = (int64_t)*p.n_work * p.H;
+  Mine mine;
+  mine.spans = p.plan->spans != 0;
+  mine.first = 0;
+  if (mine.spans) {
+    const int2 place = p.plan->place[blockIdx.x];
+    mine.first = place.x, mine.items = place.y;
+  } else {
+    mine.items = (int64_t)p.plan->n_work * p.H;
+  }
 
   Work w;
   Facts f;
@@ -277,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&a->q_full[t], 3 * kBox);
           for (int b = 0; b < 3; ++b) tma_load_3d(smem + (3 * t + b) * kBox, &tm_q, &a->q_full[t], 64 * b, head, f.q_row + w.q0 + kTile * t);
         };
-        for (int r = 0; ok && get_work(p, n_items, r, w, head, f); ++r) {
+        for (int r = 0; ok && get_work(p, mine, r, w, head, f); ++r) {
+          if (w.parts == 0) continue;
           const int n0 = tiles_for(f, w, 0), n1 = tiles_for(f, w, 1), n = max(n0, n1);
           if (n0) query(0);
           for (int j = 0; ok && j < n; ++j, ++g) {
@@ -325,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int used = 0, soft = 0;  // items and softmax tiles
       int edges = 0;           // tiles of positions that were looked through
       bool ok = true;
-      for (int r = 0; ok && uniform(get_work(p, n_items, r, w, head, f)); ++r) {
+      for (int r = 0; ok && uniform(get_work(p, mine, r, w, head, f)); ++r) {
+        if (uniform(w.parts) == 0) continue;
         const int n0 = uniform(tiles_for(f, w, 0)), n1 = uniform(tiles_for(f, w, 1)), n = max(n0, n1), nt = t ? n1 : n0;
         if (n == 0) continue;
         const int least0 = sees(f, 0), least1 = sees(f, kTile);
@@ -408,7 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int g = 0, soft = 0, used = 0, edges = 0;
     bool ok = true;
-    for (int r = 0; get_work(p, n_items, r, w, head, f); ++r) {
+    for (int r = 0; get_work(p, mine, r, w, head, f); ++r) {
+      if (w.parts == 0) continue;
       const int n0 = tiles_for(f, w, 0), n1 = tiles_for(f, w, 1), n = t ? n1 : n0;
       const int i = kTile * t + row;                             // row of the block
       const int see = i < f.nrows ? sees(f, i) : 0;              // positions that it sees
@@ -457,11 +653,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ++edges;
         }
-        const int mine = see - pos;  // positions of the tile that this row sees
+        const int upto = see - pos;  // positions of the tile that this row sees
         auto hide = [&](int c, float (&x)[32]) {
           if (edge) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = 64 * h + c + k < mine ? x[k] : -INFINITY;
+            for (int k = 0; k < 32; ++k) x[k] = 64 * h + c + k < upto ? x[k] : -INFINITY;
           }
         };
         float x[2][32];
@@ -523,7 +719,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       g += max(n0, n1);
       edges = edges0 + edges_of(f, w, n0, max(n0, n1));
       // ---- the rows' results
-      const int chunks = tiles_of(sees(f, f.nrows - 1)) > p.chunk ? 2 : 1;  // (more than one)
       const bool live = i < f.nrows;
       if (n > 0) {
         ok = wait_here(a, &a->o_done[t], used & 1, err) && ok;
@@ -534,9 +729,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       pair_bar();
       l = a->rows[t][0][row] + a->rows[t][1][row];
       const float inv = l != 0.f ? 1.f / l : 0.f;
-      const int part = w.t0 / p.chunk;
+      const int64_t part = w.part + (int64_t)i * w.step;
       if (live && h == 0) {
-        if (chunks > 1) p.part_ml[(int64_t)part * p.T * p.H + out_row] = make_float2(m, l);
+        if (w.part >= 0) p.part_ml[part] = make_float2(m, l);
         else if (p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
       // (from the first tile of positions that was looked through: of the first queries' where they are multiplied with it)
@@ -553,8 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 32; ++k) o[k] = 0.f;
         }
         if (odd && live) {  // what was cleared from V, for the rows that see it (rows before it never read it)
-          const int upto = min(see, (w.t0 + n) * kTile);
-          for (int q = max(cleared, w.t0 * kTile); q < upto; ++q) {
+          const int end = min(see, (w.t0 + n) * kTile);
+          for (int q = max(cleared, w.t0 * kTile); q < end; ++q) {
             const __nv_bfloat16* v = p.v + (int64_t)(f.k_row + q) * p.v_row_stride + head * p.v_head_stride + c;
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
@@ -564,8 +759,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!live) {
-        } else if (chunks > 1) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + ((int64_t)part * p.T * p.H + out_row) * kDv + c);
+        } else if (w.part >= 0) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + part * kDv + c);
 #pragma unroll
           for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         } else {
@@ -586,6 +781,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive(&a->o_free[t]);
       }
+      if (w.parts > 1) {  // whoever finishes the last part of the tile's rows merges them
+        __threadfence();
+        __syncwarp();
+        asm volatile("bar.sync %0, 256;" ::"r"(9 + t) : "memory");
+        if (row == 0 && h == 0) a->last[t] = atomicAdd(&p.plan->done[w.item][t], 1) == w.parts - 1;
+        asm volatile("bar.sync %0, 256;" ::"r"(9 + t) : "memory");
+        if (a->last[t]) {
+          __threadfence();
+          merge_parts(p, w, f, head, kTile * t, (warp - 4) & 7);
+        }
+        asm volatile("bar.sync %0, 256;" ::"r"(11 + t) : "memory");  // (`last` has been read)
+      }
     }
   }
   tc_fence_before();
@@ -596,15 +803,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Merges the chunks of the rows that have more than one: out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.  32
-// threads a row and head, four columns each.
-__global__ void __launch_bounds__(256) merge_kernel(const ExpandedAttnParams p) {
-  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), rows = (int64_t)p.T * p.H;
-  const int lane = threadIdx.x & 31;
+// Of the blocks whose contexts are longer than a chunk.
+__global__ void __launch_bounds__(256) merge_chunks_kernel(const ExpandedAttnParams p) {
+  const int64_t rows = (int64_t)p.T * p.H, at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, t = (int)(at / p.H);
   pdl_wait();
-  if (at >= rows) return;
-  const int t = (int)(at / p.H);
-  if (t < p.q_start[0] || t >= p.q_start[p.n_seq]) return;
+  if (at >= rows || t < p.q_start[0] || t >= p.q_start[p.n_seq]) return;
   int lo = 0, hi = p.n_seq - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -618,22 +822,18 @@ __global__ void __launch_bounds__(256) merge_kernel(const ExpandedAttnParams p) 
   f = block_facts(p, lo, i / kBlock * kBlock);
   const int chunks = (block_tiles(f) + p.chunk - 1) / p.chunk;
   if (chunks <= 1) return;  // written by the attention kernel
-  float M = -INFINITY;
+  float M = -INFINITY, l = 0.f;
   for (int c = 0; c < chunks; ++c) M = fmaxf(M, p.part_ml[c * rows + at].x);
-  const float mu = M == -INFINITY ? 0.f : M;
-  float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int c = 0; c < chunks; ++c) {
     const float2 ml = p.part_ml[c * rows + at];
     if (ml.y == 0.f) continue;  // the row saw nothing there
-    const float g = exp2f(ml.x - mu);
+    const float g = exp2f(ml.x - (M == -INFINITY ? 0.f : M));
     const float4 v = reinterpret_cast<const float4*>(p.part_o + (c * rows + at) * kDv)[lane];
     l = fmaf(g, ml.y, l);
     o.x = fmaf(g, v.x, o.x), o.y = fmaf(g, v.y, o.y), o.z = fmaf(g, v.z, o.z), o.w = fmaf(g, v.w, o.w);
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  reinterpret_cast<uint2*>(p.out + at * kDv)[lane] = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+  write_merged(p, at, M, l, o);
 }
 
 int blocks_of(const ExpandedAttnParams& p) {  // at most
@@ -643,33 +843,36 @@ int blocks_of(const ExpandedAttnParams& p) {  // at most
 int longest(const ExpandedAttnParams& p) { return (int)(((int64_t)(p.max_len < p.N ? p.max_len : p.N) + kTile - 1) / kTile); }
 int parts_of(const ExpandedAttnParams& p) { return longest(p) > p.chunk ? (longest(p) + p.chunk - 1) / p.chunk : 1; }
 
-// Tiles of positions of a chunk: one chunk per block where the blocks of all heads fill the SMs, else as many as
-// make two rounds of them, by the sequences' mean length.
+// Blocks whose contexts may be longer than a chunk are cut at chunks: of 512 tiles where the blocks of all heads fill the
+// SMs, else of as many as make two rounds of them, by the sequences' mean length.  Others may be cut into spans, if there
+// is work enough for that.
 constexpr int64_t kMostPartial = 512ll << 20;
-int chunk_of(ExpandedAttnParams p) {
-  const int64_t items = (int64_t)blocks_of(p) * p.H;
-  const int mean = (int)(((int64_t)p.N + (int64_t)p.n_seq * kTile - 1) / ((int64_t)p.n_seq * kTile));
+void set_cuts(ExpandedAttnParams* p) {
+  const int64_t items = (int64_t)blocks_of(*p) * p->H;
+  p->chunk = kMaxChunk;
+  p->may_span = longest(*p) <= kMaxChunk && items * (longest(*p) + kFixed) >= (int64_t)kMinSpan * kSms;
   const int64_t splits = (2 * kSms) / (items > 0 ? items : 1);
-  p.chunk = kMaxChunk;
-  if (splits > 1) {
-    const int64_t c = ((int64_t)mean + splits - 1) / splits;
-    p.chunk = (int)(c < kMinChunk ? kMinChunk : c > kMaxChunk ? kMaxChunk : c);
-    while (p.chunk < kMaxChunk && (int64_t)parts_of(p) * p.T * p.H * (kDv + 2) * 4 > kMostPartial) p.chunk = p.chunk * 2 < kMaxChunk ? p.chunk * 2 : kMaxChunk;
+  if (longest(*p) > kMaxChunk && splits > 1) {
+    const int64_t mean = ((int64_t)p->N + (int64_t)p->n_seq * kTile - 1) / ((int64_t)p->n_seq * kTile);
+    const int64_t c = (mean + splits - 1) / splits;
+    p->chunk = (int)(c < kMinChunk ? kMinChunk : c > kMaxChunk ? kMaxChunk : c);
+    while (p->chunk < kMaxChunk && (int64_t)parts_of(*p) * p->T * p->H * (kDv + 2) * 4 > kMostPartial)
+      p->chunk = p->chunk * 2 < kMaxChunk ? p->chunk * 2 : kMaxChunk;
   }
-  return p.chunk;
+  const int64_t all = items * parts_of(*p);
+  p->grid = (int)(p->may_span || all > kSms ? kSms : all);
 }
 
 struct Layout {
   size_t work, part_ml, part_o, total;
-  int parts;
   int64_t max_work;
 };
 Layout layout_of(const ExpandedAttnParams& p) {
   Layout l;
-  l.parts = parts_of(p);
-  l.max_work = (int64_t)blocks_of(p) * l.parts;
-  const int64_t rows = l.parts > 1 ? (int64_t)l.parts * p.T * p.H : 0;
-  l.work = 256;  // the count first
+  const int parts = parts_of(p);
+  l.max_work = (int64_t)blocks_of(p) * parts;
+  const int64_t rows = parts > 1 ? (int64_t)parts * p.T * p.H : p.may_span ? 2 * kSms * kBlock : 0;
+  l.work = align_up(sizeof(Plan), 256);
   l.part_ml = l.work + align_up((size_t)l.max_work * sizeof(int4), 256);
   l.part_o = l.part_ml + align_up((size_t)rows * sizeof(float2), 256);
   l.total = l.part_o + (size_t)rows * kDv * sizeof(float);
@@ -688,7 +891,7 @@ bool map_of(CUtensorMap* tm, const void* base, int cols, int heads, int rows, in
 cudaError_t launch(ExpandedAttnParams p, const dsa_expanded_attn_args& a, void* ws, cudaStream_t stream) {
   const Layout l = layout_of(p);
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
-  p.n_work = reinterpret_cast<int*>(base);
+  p.plan = reinterpret_cast<Plan*>(base);
   p.work = reinterpret_cast<int4*>(base + l.work);
   p.part_ml = reinterpret_cast<float2*>(base + l.part_ml);
   p.part_o = reinterpret_cast<float*>(base + l.part_o);
@@ -711,11 +914,12 @@ cudaError_t launch(ExpandedAttnParams p, const dsa_expanded_attn_args& a, void* 
   cudaError_t e = allow_smem_once(&allowed, reinterpret_cast<const void*>(expanded_attn_kernel), kSmem);
   if (e != cudaSuccess) return e;
   if ((e = launch_kernel(plan_kernel, dim3(1), dim3(1024), 0, stream, false, p)) != cudaSuccess) return e;
-  const int64_t items = l.max_work * p.H;
-  if ((e = launch_kernel(expanded_attn_kernel, dim3((unsigned)(items < kSms ? items : kSms)), dim3(kThreads), kSmem, stream, true, tq, tk, tr, tv,
+  if ((e = launch_kernel(expanded_attn_kernel, dim3((unsigned)p.grid), dim3(kThreads), kSmem, stream, true, tq, tk, tr, tv,
                          p)) != cudaSuccess)
     return e;
-  if (l.parts > 1) e = launch_kernel(merge_kernel, dim3((unsigned)(((int64_t)p.T * p.H + 7) / 8)), dim3(256), 0, stream, true, p);
+  if (parts_of(p) > 1) {
+    e = launch_kernel(merge_chunks_kernel, dim3((unsigned)(((int64_t)p.T * p.H + 7) / 8)), dim3(256), 0, stream, true, p);
+  }
   return e;
 }
 
@@ -751,7 +955,7 @@ ExpandedAttnParams params_of(const dsa_expanded_attn_args& a) {
   p.v_head_stride = a.v_head_stride;
   p.out = reinterpret_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
-  p.chunk = chunk_of(p);
+  set_cuts(&p);
   return p;
 }
 
