@@ -162,6 +162,13 @@ __device__ __forceinline__ const uint8_t* row_at(const ExpandParams& p, int64_t 
   return p.kv + seq * p.kv_seq_stride + (row - seq * p.L) * p.kv_row_stride;
 }
 
+// A load that stays where it is written (an ordinary one sinks behind the wait that it is to be in flight during).
+__device__ __forceinline__ uint4 load_now(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -301,7 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              v[k][i] = from[i] ? __ldg(reinterpret_cast<const uint4*>(from[i] + 128 * (k0 + k))) : make_uint4(0u, 0u, 0u, 0u);
+              v[k][i] = from[i] ? load_now(from[i] + 128 * (k0 + k)) : make_uint4(0u, 0u, 0u, 0u);
           if (k0 == 0) ok = __all_sync(0xffffffffu, wait_pair(a, &a->a_empty, (tiles & 1) ^ 1, err));
           if (!ok) break;  // (to the barrier below)
 #pragma unroll
@@ -338,7 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < kBoxes; ++k)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) v[k][i] = from[i] ? __ldg(reinterpret_cast<const uint4*>(from[i] + 64 * k)) : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < 2; ++i) v[k][i] = from[i] ? load_now(from[i] + 64 * k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll

@@ -50,18 +50,16 @@ __global__ void __launch_bounds__(32 * kWarps, CTAS) norm_rope_vec_kernel(const 
   const int nch = p.width / 8;
   const bool one = p.heads == 1;  // then the vectors of a step are rows
   const int hblocks = one ? 1 : (p.heads + n.heads_per_item - 1) / n.heads_per_item;
-  fill_freq(p, sm);
-  float2* cs = sm.turns[warp];
-  float* stage = stage_s[warp] + g * 2 * p.pairs;
-  const int entries = one ? VEC * p.pairs : p.pairs;  // of the table: pairs of the step's rows, or of the row
-
   // weights and biases by column, in shared memory (in registers they would spill)
   __shared__ alignas(16) float w_s[8 * G * NCH], b_s[8 * G * NCH];
   for (int c = threadIdx.x; c < n.dim; c += 32 * kWarps) {
     w_s[c] = n.weight ? n.weight[c] : 1.f;
     b_s[c] = n.bias ? n.bias[c] : 0.f;
   }
-  __syncthreads();
+  fill_freq(p, sm);  // (with the barrier)
+  float2* cs = sm.turns[warp];
+  float* stage = stage_s[warp] + g * 2 * p.pairs;
+  const int entries = one ? VEC * p.pairs : p.pairs;  // of the table: pairs of the step's rows, or of the row
 
   uint4 raw[NCH];
   int64_t dst = 0;
@@ -360,14 +358,15 @@ using NormKernel = void (*)(const RopeParams, const NormParams);
 
 // The vector form for a width: the lanes of a vector, and resident CTAs.
 template <int FMT>
-NormKernel vec_form(int width, int* lanes, int* ctas) {
-  *lanes = width <= 256 ? 8 : width <= 640 ? 16 : 32;
+NormKernel vec_form(int width, bool few, int* lanes, int* ctas) {
+  *lanes = width <= 256 ? 8 : width <= 640 && !few ? 16 : 32;
   *ctas = width <= 256 ? 3 : 2;
   if (width <= 64) return norm_rope_vec_kernel<FMT, 8, 1, 3>;
   if (width <= 128) return norm_rope_vec_kernel<FMT, 8, 2, 3>;
   if (width <= 192) return norm_rope_vec_kernel<FMT, 8, 3, 3>;
   if (width <= 256) return norm_rope_vec_kernel<FMT, 8, 4, 3>;
-  if (width <= 640) return norm_rope_vec_kernel<FMT, 16, 5, 2>;
+  if (width <= 640 && !few) return norm_rope_vec_kernel<FMT, 16, 5, 2>;
+  if (width <= 768) return norm_rope_vec_kernel<FMT, 32, 3, 2>;
   return norm_rope_vec_kernel<FMT, 32, 4, 2>;
 }
 
@@ -401,7 +400,9 @@ dsa_status launch_norm(const RopeParams& p, NormParams n, bool vec, cudaStream_t
     norm_rope_kernel<FMT><<<(unsigned)(want < 8 * kSms ? want : 8 * kSms), 32 * kPlainWarps, 0, stream>>>(p, n);
   } else {
     int lanes, ctas;
-    const NormKernel kern = vec_form<FMT>(p.width, &lanes, &ctas);
+    // a warp per vector where every warp has one at most (latent rows, us: 129 rows 3.6 and 4.2 with half a warp, 4800 5.7 and 5.3)
+    const bool few = (int64_t)p.rows * p.heads <= 2 * kSms * kWarps;
+    const NormKernel kern = vec_form<FMT>(p.width, few, &lanes, &ctas);
     const int per = 32 / lanes, most = ctas * kSms;
     // heads of a row for a warp: all of up to 16, or as few as leave no warp idle
     n.heads_per_item = 16;
