@@ -577,7 +577,8 @@ dsa_status dsa_tree_attn(const dsa_tree_args* a, void* ws, size_t ws_bytes, void
  * The results differ from dsa_tree_attn's by rounding only (the sums are split elsewhere); they repeat from call to call.
  * ws: dsa_prefix_attn_workspace_size bytes, 256-byte aligned, contents irrelevant; calls (and captured graphs) that share
  * it must not run at the same time.  group_start and n_shared of the size query are only tested for being there.
- * Supported: n_groups <= 4096; n_seq * q_per_seq * H <= 2^26.
+ * Supported: n_groups <= 4096; n_seq * q_per_seq * H <= 2^26; (2 n_seq ceil(q_per_seq H / 128) + n_groups) * (L / 64 + 9) below
+ * 2^31 (1024 sequences of 16 heads over 16 million positions).
  * ------------------------------------------------------------------------------------------ */
 dsa_status dsa_prefix_attn_workspace_size(const dsa_tree_args* a, const int32_t* group_start, const int32_t* n_shared,
                                           int n_groups, size_t* bytes);

@@ -51,7 +51,7 @@ constexpr float kLazy = 8.f;                // log2 growth of a row's maximum th
 constexpr int kSms = 152;
 constexpr int kMaxChunk = 512, kMinChunk = 4;  // tiles
 constexpr int kFixed = 3;                      // what starting on a block costs, in tiles
-constexpr int kMinSpan = 4;
+constexpr int kMinSpan = 4;                    // tiles of a span, at least
 constexpr int kMaxSeq = 4096;
 constexpr uint32_t kColS = 0, kColO = 256;
 
@@ -234,9 +234,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
     if (tid < run) before[tid] = ahead + incl - cost;
     if (tid == run) before[run] = all;
     __syncthreads();
-    const int items = run * p.H, total = all * p.H, W = max((total + p.grid - 1) / p.grid, 1);  // (below 2^25)
+    const int items = run * p.H, total = all * p.H, W = max((total + p.grid - 1) / p.grid, kMinSpan);  // (below 2^25)
     const int whole = items <= p.grid ? longest : total / p.grid + longest / 2;
-    if (W >= kMinSpan && W + 2 * kFixed < whole) {
+    if (W + 2 * kFixed < whole) {
       if (tid == 0) p.plan->spans = 1;
       // The order: a sequence after another, of it a head after another, of that the blocks, so that the CTAs that read the
       // same keys and values are neighbours and do so at about the same time (two chunks of 1125 tokens over 12K positions,
@@ -850,7 +850,7 @@ constexpr int64_t kMostPartial = 512ll << 20;
 void set_cuts(ExpandedAttnParams* p) {
   const int64_t items = (int64_t)blocks_of(*p) * p->H;
   p->chunk = kMaxChunk;
-  p->may_span = longest(*p) <= kMaxChunk && items * (longest(*p) + kFixed) >= (int64_t)kMinSpan * kSms;
+  p->may_span = longest(*p) <= kMaxChunk && longest(*p) > kMinSpan + kFixed;
   const int64_t splits = (2 * kSms) / (items > 0 ? items : 1);
   if (longest(*p) > kMaxChunk && splits > 1) {
     const int64_t mean = ((int64_t)p->N + (int64_t)p->n_seq * kTile - 1) / ((int64_t)p->n_seq * kTile);
@@ -859,8 +859,9 @@ void set_cuts(ExpandedAttnParams* p) {
     while (p->chunk < kMaxChunk && (int64_t)parts_of(*p) * p->T * p->H * (kDv + 2) * 4 > kMostPartial)
       p->chunk = p->chunk * 2 < kMaxChunk ? p->chunk * 2 : kMaxChunk;
   }
-  const int64_t all = items * parts_of(*p);
-  p->grid = (int)(p->may_span || all > kSms ? kSms : all);
+  int64_t ctas = items * parts_of(*p);
+  if (p->may_span) ctas = (items * (longest(*p) + kFixed) + kMinSpan - 1) / kMinSpan;
+  p->grid = (int)(ctas < kSms ? ctas : kSms);
 }
 
 struct Layout {
@@ -871,7 +872,7 @@ Layout layout_of(const ExpandedAttnParams& p) {
   Layout l;
   const int parts = parts_of(p);
   l.max_work = (int64_t)blocks_of(p) * parts;
-  const int64_t rows = parts > 1 ? (int64_t)parts * p.T * p.H : p.may_span ? 2 * kSms * kBlock : 0;
+  const int64_t rows = parts > 1 ? (int64_t)parts * p.T * p.H : p.may_span ? 2 * p.grid * kBlock : 0;
   l.work = align_up(sizeof(Plan), 256);
   l.part_ml = l.work + align_up((size_t)l.max_work * sizeof(int4), 256);
   l.part_o = l.part_ml + align_up((size_t)rows * sizeof(float2), 256);

@@ -20,28 +20,30 @@ namespace {
 struct PrefixParams {
   const int32_t* group_start;  // [n_groups + 1]
   const int32_t* n_shared;     // [n_groups]
-  int n_groups;
+  int n_groups, unit_cost;
 };
 
 // The plan, in the workspace.
 struct Group {
   int lo, hi, lead, tiles;     // sequences [lo, hi), the one whose cache is read, tiles of the prefix taken once
-  int first_unit, pad;
-  long long base;              // cost before its units
+  int first_unit, base;        // units, and cost, before its own
 };
 struct PrefixPlan {
-  long long* width;            // [0]: of a span; [1]: the fixed cost of a unit
+  int* width;                  // [0]: of a span; [1]: the fixed cost of a unit
   Group* groups;               // [n_groups]
-  long long* base;             // [n_seq]: cost before a sequence's units
-  int* group_of;               // [n_seq], -1: none
+  int2* seqs;                  // [n_seq]: cost before a sequence's units, its group (-1: none)
   SharedItem* list;
   int2* list_place;            // [pairs]
 };
 
 constexpr int kPairs = 76;
+constexpr int kMaxGroups = 4096, kMaxSeq = 4096;
 constexpr int kPlanThreads = 1024;
+// Fill, query rows and partial results of a unit, in tiles: about 10 us, of tiles of 1.2 us (tile scales: 2.6).  With 4 and 8, us:
+// 64 sequences over 32K shared positions, E4M3 rows 130 and 111; 48 over 3 x 8K, tile scales 141 and 147.
+constexpr int kUnitCost = 8, kUnitCostTiled = 4;
 
-__device__ __forceinline__ int row_tiles(long long rows) { return (int)((rows + kRows - 1) / kRows); }
+__host__ __device__ __forceinline__ int row_tiles(int rows) { return (rows + kRows - 1) / kRows; }
 __device__ __forceinline__ int up8(int x) { return (x + 7) & ~7; }
 
 // A sequence's tail: tiles [from, from + tiles), for `live` row tiles.
@@ -56,7 +58,7 @@ __device__ __forceinline__ Tail tail_of(const TreeAttnParams& p, int seq, int fr
   t.tiles = t.live ? max((t.len + kKeys - 1) / kKeys - from, 0) : 0;
   return t;
 }
-__device__ __forceinline__ long long unit_cost(int tiles, long long fixed) { return tiles ? tiles + fixed : 0; }
+__device__ __forceinline__ int unit_cost(int tiles, int fixed) { return tiles ? tiles + fixed : 0; }  // (all of them: below 2^31)
 
 // First row of partial results of a unit (rounded up to eights, the groups' before the sequences'), without the spans cut
 // before it: 128 rows are kept for the part behind each cut.
@@ -68,36 +70,60 @@ __device__ __forceinline__ int tail_slot(const TreeAttnParams& p, int n_groups, 
   return up8(p.n_seq * rows) + 8 * (n_groups + 1) + seq * up8(rows) + kRows * rt;
 }
 
-// Running sum over the CTA's threads; `total` gets the whole.
-__device__ long long block_scan(long long x, long long* warps, long long& total) {
+// Running sums of two numbers over the CTA's threads; `all` gets the wholes.
+__device__ int2 block_scan(int2 x, int2* warps, int2& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long incl = x;
+  int2 incl = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += u;
+    const int a = __shfl_up_sync(0xffffffffu, incl.x, o), b = __shfl_up_sync(0xffffffffu, incl.y, o);
+    if (lane >= o) incl.x += a, incl.y += b;
   }
-  __syncthreads();
+  __syncthreads();  // (the last sums have been read)
   if (lane == 31) warps[warp] = incl;
   __syncthreads();
-  if (warp == 0) {
-    long long v = warps[lane];
+  int2 mine = warps[lane], run = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    warps[lane] = v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, run.x, o), b = __shfl_up_sync(0xffffffffu, run.y, o);
+    if (lane >= o) run.x += a, run.y += b;
   }
-  __syncthreads();
-  total = warps[31];
-  return incl - x + (warp ? warps[warp - 1] : 0);
+  all = make_int2(__shfl_sync(0xffffffffu, run.x, 31), __shfl_sync(0xffffffffu, run.y, 31));
+  const int bx = __shfl_sync(0xffffffffu, run.x - mine.x, warp), by = __shfl_sync(0xffffffffu, run.y - mine.y, warp);
+  return make_int2(bx + incl.x - x.x, by + incl.y - x.y);
 }
 
+// The last of n entries whose key is at most x (key(0) <= x).
+template <class Key>
+__device__ __forceinline__ int last_at_most(int n, int x, Key&& key) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (key(mid) <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// What is searched lies in shared memory: the groups, and per sequence its cost before, its tail's tiles and its group.
+struct PlanSmem {
+  Group* groups;
+  int* base;
+  int* tiles;
+  int* group_of;
+};
+size_t plan_smem(int n_groups, int n_seq) { return sizeof(Group) * n_groups + 3 * sizeof(int) * n_seq; }
+
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const TreeAttnParams p, const PrefixParams pp, const PrefixPlan pl) {
-  __shared__ long long warps[32];
+  extern __shared__ int plan_s[];
+  __shared__ int2 warps[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long rows = (long long)p.q_per_seq * p.H;
+  const int rows = p.q_per_seq * p.H;
+  PlanSmem sm;
+  sm.groups = reinterpret_cast<Group*>(plan_s);
+  sm.base = reinterpret_cast<int*>(sm.groups + pp.n_groups);
+  sm.tiles = sm.base + p.n_seq;
+  sm.group_of = sm.tiles + p.n_seq;
 
   // ---- the groups: a warp each
   for (int g = warp; g < pp.n_groups; g += kPlanThreads / 32) {
@@ -108,139 +134,119 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const TreeAtt
       seq_facts(p, s, ctx, fresh, len);
       if (fresh) least = min(least, ctx), lead = min(lead, s), ++members;  // (one without queries has no say)
     }
+    const int shared = pp.n_shared[g];
     least = __reduce_min_sync(0xffffffffu, least);
     lead = __reduce_min_sync(0xffffffffu, lead);
     members = __reduce_add_sync(0xffffffffu, members);
     if (lane == 0) {
       Group x = {};
       x.lo = lo, x.hi = hi, x.lead = lead;
-      x.tiles = members > 1 ? min(max(pp.n_shared[g], 0), least) / kKeys : 0;
-      pl.groups[g] = x;
+      x.tiles = members > 1 ? min(max(shared, 0), least) / kKeys : 0;
+      sm.groups[g] = x;
     }
   }
   __syncthreads();
-  // ---- the sequences' groups, and all tiles
-  long long sum = 0;
+  // ---- the sequences' groups and tails, and all tiles
+  int2 sum = make_int2(0, 0), all;
   for (int s = tid; s < p.n_seq; s += kPlanThreads) {
-    int lo = 0, hi = pp.n_groups - 1;  // the last group that starts at or before s
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pl.groups[mid].lo <= s) lo = mid;
-      else hi = mid - 1;
+    int g = -1;
+    if (pp.n_groups > 0) {
+      const int k = last_at_most(pp.n_groups, s, [&](int i) { return sm.groups[i].lo; });
+      if (sm.groups[k].lo <= s && s < sm.groups[k].hi) g = k;
     }
-    const int g = pp.n_groups > 0 && pl.groups[lo].lo <= s && s < pl.groups[lo].hi ? lo : -1;
-    pl.group_of[s] = g;
-    const Tail t = tail_of(p, s, g >= 0 ? pl.groups[g].tiles : 0);
-    sum += (long long)t.tiles * t.live;
+    const Tail t = tail_of(p, s, g >= 0 ? sm.groups[g].tiles : 0);
+    sm.group_of[s] = g;
+    sm.tiles[s] = t.tiles;
+    sm.base[s] = t.live;  // (until the costs are known)
+    sum.x += t.tiles * t.live;
   }
-  for (int g = tid; g < pp.n_groups; g += kPlanThreads) {
-    const Group x = pl.groups[g];
-    sum += (long long)x.tiles * row_tiles((x.hi - x.lo) * rows);
-  }
-  long long total;
-  block_scan(sum, warps, total);
-  // A unit's fixed cost: four tiles' time where spans are long, nothing where there is less than a tile for each pair
+  for (int g = tid; g < pp.n_groups; g += kPlanThreads) sum.x += sm.groups[g].tiles * row_tiles((sm.groups[g].hi - sm.groups[g].lo) * rows);
+  block_scan(sum, warps, all);
+  // A unit's fixed cost: its own where spans are long, nothing where there is less than a tile for each pair
   // (then the time is that of the longest item).
-  const long long fixed = min(max(total / (2 * kPairs), 0ll), 4ll);
+  const int fixed = min(all.x / (2 * kPairs), pp.unit_cost);
   // ---- the units' places: groups, then sequences
-  long long run = 0;
-  int units = 0;
+  int run = 0, units = 0;
   for (int g0 = 0; g0 < pp.n_groups; g0 += kPlanThreads) {
     const int g = g0 + tid;
-    long long c = 0, n = 0, all, all_n;
+    int2 c = make_int2(0, 0);
     if (g < pp.n_groups) {
-      const Group x = pl.groups[g];
-      n = row_tiles((x.hi - x.lo) * rows);
-      c = n * unit_cost(x.tiles, fixed);
+      c.y = row_tiles((sm.groups[g].hi - sm.groups[g].lo) * rows);
+      c.x = c.y * unit_cost(sm.groups[g].tiles, fixed);
     }
-    const long long before = block_scan(c, warps, all), before_n = block_scan(n, warps, all_n);
-    if (g < pp.n_groups) pl.groups[g].base = run + before, pl.groups[g].first_unit = units + (int)before_n;
-    run += all, units += (int)all_n;
+    const int2 before = block_scan(c, warps, all);
+    if (g < pp.n_groups) {
+      sm.groups[g].base = run + before.x, sm.groups[g].first_unit = units + before.y;
+      pl.groups[g] = sm.groups[g];
+    }
+    run += all.x, units += all.y;
   }
   for (int s0 = 0; s0 < p.n_seq; s0 += kPlanThreads) {
     const int s = s0 + tid;
-    long long c = 0, all;
+    int2 c = make_int2(0, 0);
+    if (s < p.n_seq) c.x = sm.base[s] * unit_cost(sm.tiles[s], fixed);
+    const int2 before = block_scan(c, warps, all);
     if (s < p.n_seq) {
-      const int g = pl.group_of[s];
-      const Tail t = tail_of(p, s, g >= 0 ? pl.groups[g].tiles : 0);
-      c = t.live * unit_cost(t.tiles, fixed);
+      sm.base[s] = run + before.x;
+      pl.seqs[s] = make_int2(run + before.x, sm.group_of[s]);
     }
-    const long long before = block_scan(c, warps, all);
-    if (s < p.n_seq) pl.base[s] = run + before;
-    run += all;
+    run += all.x;
   }
-  const long long W = max((run + kPairs - 1) / kPairs, 1ll);
+  const int W = max((int)(((long long)run + kPairs - 1) / kPairs), 1);
   if (tid == 0) pl.width[0] = W, pl.width[1] = fixed;
   __syncthreads();
   // ---- the pairs' lists: a warp each.  Entry of unit u in span k: u + k
   const int per_seq = row_tiles(rows);
-  auto unit_at = [&](long long x) {  // the unit that holds cost x
-    if (pp.n_groups > 0 && (p.n_seq == 0 || x < pl.base[0])) {
-      int lo = 0, hi = pp.n_groups - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pl.groups[mid].base <= x) lo = mid;
-        else hi = mid - 1;
-      }
-      const Group g = pl.groups[lo];
-      return g.first_unit + (int)((x - g.base) / unit_cost(g.tiles, fixed));
+  auto unit_at = [&](int x) {  // the unit that holds cost x
+    if (x < sm.base[0]) {
+      const Group g = sm.groups[last_at_most(pp.n_groups, x, [&](int i) { return sm.groups[i].base; })];
+      return g.first_unit + (x - g.base) / unit_cost(g.tiles, fixed);
     }
-    int lo = 0, hi = p.n_seq - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pl.base[mid] <= x) lo = mid;
-      else hi = mid - 1;
-    }
-    const int g = pl.group_of[lo];
-    const Tail t = tail_of(p, lo, g >= 0 ? pl.groups[g].tiles : 0);
-    return units + lo * per_seq + (int)((x - pl.base[lo]) / unit_cost(t.tiles, fixed));
+    const int s = last_at_most(p.n_seq, x, [&](int i) { return sm.base[i]; });
+    return units + s * per_seq + (x - sm.base[s]) / unit_cost(sm.tiles[s], fixed);
   };
   for (int k = warp; k < kPairs; k += kPlanThreads / 32) {
-    const long long x0 = k * W, x1 = min(x0 + W, run);
-    if (x0 >= run) {
+    const long long from = (long long)k * W;
+    if (from >= run) {
       if (lane == 0) pl.list_place[k] = make_int2(0, 0);
       continue;
     }
+    const int x0 = (int)from, x1 = (int)min(from + W, (long long)run);
     const int u0 = unit_at(x0), u1 = unit_at(x1 - 1);
     if (lane == 0) pl.list_place[k] = make_int2(u0 + k, u1 - u0 + 1);
     for (int u = u0 + lane; u <= u1; u += 32) {
       SharedItem it = {};
-      long long b = 0;  // cost before the unit's tiles, without the fixed one
-      int tiles = 0, from = 0;
+      int b = 0;  // cost before the unit
+      int tiles = 0, from_tile = 0;
       if (u < units) {
-        int lo = 0, hi = pp.n_groups - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (pl.groups[mid].first_unit <= u) lo = mid;
-          else hi = mid - 1;
-        }
-        const Group g = pl.groups[lo];
+        const int gi = last_at_most(pp.n_groups, u, [&](int i) { return sm.groups[i].first_unit; });
+        const Group g = sm.groups[gi];
         const int rt = u - g.first_unit;
         tiles = g.tiles;
         b = g.base + rt * unit_cost(tiles, fixed);
         it.seq = g.lead;
-        it.at = (int)(g.lo * rows) + rt * kRows;
-        it.nrows = (int)min((long long)kRows, (g.hi - g.lo) * rows - (long long)rt * kRows);
+        it.at = g.lo * rows + rt * kRows;
+        it.nrows = min(kRows, (g.hi - g.lo) * rows - rt * kRows);
         it.ctx = it.len = tiles * kKeys;
-        it.slot = group_slot(p, g, lo, rt);
+        it.slot = group_slot(p, g, gi, rt);
       } else {
-        const int s = (u - units) / per_seq, rt = (u - units) % per_seq, g = pl.group_of[s];
-        const Tail t = tail_of(p, s, g >= 0 ? pl.groups[g].tiles : 0);
+        const int s = (u - units) / per_seq, rt = (u - units) % per_seq, g = sm.group_of[s];
+        const Tail t = tail_of(p, s, g >= 0 ? sm.groups[g].tiles : 0);
         tiles = rt < t.live ? t.tiles : 0;
-        from = t.from;
-        b = pl.base[s] + rt * unit_cost(t.tiles, fixed);
+        from_tile = t.from;
+        b = sm.base[s] + rt * unit_cost(t.tiles, fixed);
         it.seq = s;
         it.row_lo = rt * kRows;
-        it.at = (int)(s * rows) + it.row_lo;
-        it.nrows = (int)min((long long)kRows, rows - it.row_lo);
+        it.at = s * rows + it.row_lo;
+        it.nrows = min(kRows, rows - it.row_lo);
         it.ctx = t.ctx, it.fresh = t.fresh, it.len = t.len;
         it.slot = tail_slot(p, pp.n_groups, s, rt);
       }
-      const long long first = b + fixed;
-      const int t0 = (int)min(max(x0 - first, 0ll), (long long)tiles), t1 = (int)min(max(x1 - first, 0ll), (long long)tiles);
-      it.t0 = from + t0, it.t1 = from + max(t1, t0);
+      const int first = b + fixed;
+      const int t0 = min(max(x0 - first, 0), tiles), t1 = min(max(x1 - first, 0), tiles);
+      it.t0 = from_tile + t0, it.t1 = from_tile + max(t1, t0);
       // the parts of a unit behind its first one follow it, as many rows each
-      it.slot += kRows * (int)(b / W) + (int)(k - first / W) * up8(it.nrows);
+      it.slot += kRows * (b / W) + (k - first / W) * up8(it.nrows);
       pl.list[u + k] = it;
     }
   }
@@ -258,29 +264,29 @@ __global__ void __launch_bounds__(G > 1 ? 64 * G : 256) prefix_merge_kernel(cons
   const int row = blockIdx.x * 8 + (at & 7), c4 = blockIdx.z * (T / 8) + (at >> 3);
   pdl_wait();
   int parts_a = 0, parts = 0, r_a = 0, r_b = 0, size_a = 0, size_b = 0;
-  long long slot_a = 0, slot_b = 0;
+  int slot_a = 0, slot_b = 0;
   if (row < p.n_seq * rows) {
     const int s = row / rows, in = row - s * rows;
-    const long long W = pl.width[0], fixed = pl.width[1];
-    const int gi = pl.group_of[s];
+    const int W = pl.width[0], fixed = pl.width[1];
+    const int2 place = pl.seqs[s];
+    const int gi = place.y;
     Group x = {};
     if (gi >= 0) x = pl.groups[gi];
     const Tail t = tail_of(p, s, x.tiles);
     if (in / p.H < t.fresh) {  // (a padding node: zeros)
       if (x.tiles > 0) {
-        const long long ra = (long long)(s - x.lo) * rows + in;
-        const int rt = (int)(ra / kRows);
-        const long long b = x.base + rt * unit_cost(x.tiles, fixed);
-        parts_a = (int)((b + fixed + x.tiles - 1) / W - (b + fixed) / W) + 1;
-        r_a = (int)(ra - (long long)rt * kRows);
-        size_a = up8((int)min((long long)kRows, (long long)(x.hi - x.lo) * rows - (long long)rt * kRows));
+        const int ra = (s - x.lo) * rows + in, rt = ra / kRows;
+        const int b = x.base + rt * unit_cost(x.tiles, fixed);
+        parts_a = (b + fixed + x.tiles - 1) / W - (b + fixed) / W + 1;
+        r_a = ra - rt * kRows;
+        size_a = up8(min(kRows, (x.hi - x.lo) * rows - rt * kRows));
         slot_a = group_slot(p, x, gi, rt) + kRows * (b / W);
       }
       parts = parts_a;
       if (t.tiles > 0) {
         const int rt = in / kRows;
-        const long long b = pl.base[s] + rt * unit_cost(t.tiles, fixed);
-        parts += (int)((b + fixed + t.tiles - 1) / W - (b + fixed) / W) + 1;
+        const int b = place.x + rt * unit_cost(t.tiles, fixed);
+        parts += (b + fixed + t.tiles - 1) / W - (b + fixed) / W + 1;
         r_b = in - rt * kRows;
         size_b = up8(min(kRows, rows - rt * kRows));
         slot_b = tail_slot(p, pp.n_groups, s, rt) + kRows * (b / W);
@@ -314,9 +320,9 @@ __global__ void __launch_bounds__(G > 1 ? 64 * G : 256) prefix_merge_kernel(cons
       if (j < parts) {
         const bool a = j < parts_a;
         const int size = a ? size_a : size_b, r = a ? r_a : r_b;
-        const long long first = a ? slot_a + (long long)j * size : slot_b + (long long)(j - parts_a) * size;
+        const int64_t first = a ? slot_a + j * size : slot_b + (j - parts_a) * size;
         ml[k] = part_ml[first * 2 + (c4 >> 6) * size + r];
-        v[k] = part_o[first * (kDv / 4) + (long long)c4 * size + r];
+        v[k] = part_o[first * (kDv / 4) + c4 * size + r];
       }
     }
     add(ml, v, B);
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(G > 1 ? 64 * G : 256) prefix_merge_kernel(cons
 constexpr size_t kSumBytes = (size_t)kRows * (2 * sizeof(float2) + kDv / 2 * sizeof(float));  // a CTA's sums of long walks
 
 struct Layout {
-  size_t width, groups, base, group_of, place, list, part_ml, part_o, sum, total;
+  size_t width, groups, seqs, place, list, part_ml, part_o, sum, total;
 };
 Layout layout_of(const TreeAttnParams& p, int n_groups) {
   const int64_t rows = (int64_t)p.q_per_seq * p.H, all = rows * p.n_seq;
@@ -347,9 +353,8 @@ Layout layout_of(const TreeAttnParams& p, int n_groups) {
   Layout l;
   l.width = 0;
   l.groups = 256;
-  l.base = align_up(l.groups + sizeof(Group) * n_groups, 256);
-  l.group_of = align_up(l.base + sizeof(long long) * p.n_seq, 256);
-  l.place = align_up(l.group_of + sizeof(int) * p.n_seq, 256);
+  l.seqs = align_up(l.groups + sizeof(Group) * n_groups, 256);
+  l.place = align_up(l.seqs + sizeof(int2) * p.n_seq, 256);
   l.list = align_up(l.place + sizeof(int2) * kPairs, 256);
   l.part_ml = align_up(l.list + sizeof(SharedItem) * units, 256);
   l.part_o = align_up(l.part_ml + sizeof(float2) * 2 * parts, 256);
@@ -367,10 +372,9 @@ cudaError_t launch_form(const TreeAttnParams& p, const PrefixParams& pp, void* w
   const Layout l = layout_of(p, pp.n_groups);
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   PrefixPlan plan;
-  plan.width = reinterpret_cast<long long*>(w + l.width);
+  plan.width = reinterpret_cast<int*>(w + l.width);
   plan.groups = reinterpret_cast<Group*>(w + l.groups);
-  plan.base = reinterpret_cast<long long*>(w + l.base);
-  plan.group_of = reinterpret_cast<int*>(w + l.group_of);
+  plan.seqs = reinterpret_cast<int2*>(w + l.seqs);
   plan.list = reinterpret_cast<SharedItem*>(w + l.list);
   plan.list_place = reinterpret_cast<int2*>(w + l.place);
   TreePlan pl = {};
@@ -384,7 +388,10 @@ cudaError_t launch_form(const TreeAttnParams& p, const PrefixParams& pp, void* w
   auto kern = tree_attn_kernel<FMT, LONG, true>;
   static std::atomic<uint64_t> allowed{0};
   if ((e = allow_smem_once(&allowed, reinterpret_cast<const void*>(kern), C::SMEM)) != cudaSuccess) return e;
-  if ((e = launch_kernel(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, false, p, pp, plan)) != cudaSuccess) return e;
+  static std::atomic<uint64_t> allowed_plan{0};
+  if ((e = allow_smem_once(&allowed_plan, reinterpret_cast<const void*>(prefix_plan_kernel), (int)plan_smem(kMaxGroups, kMaxSeq))) != cudaSuccess)
+    return e;
+  if ((e = launch_kernel(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), plan_smem(pp.n_groups, p.n_seq), stream, false, p, pp, plan)) != cudaSuccess) return e;
   if ((e = launch_kernel(kern, dim3(2 * kPairs), dim3(C::THREADS), C::SMEM, stream, true, tm, p, pl)) != cudaSuccess) return e;
   const int64_t rows = (int64_t)p.n_seq * p.q_per_seq * p.H;
   const unsigned rows8 = (unsigned)((rows + 7) / 8);
@@ -405,7 +412,11 @@ dsa_status check_prefix(const dsa_tree_args* a, const int32_t* group_start, cons
   const dsa_status s = check_tree_args(a);
   if (s != DSA_OK) return s;
   if (n_groups < 0 || (n_groups > 0 && (!group_start || !n_shared))) return DSA_ERR_INVALID_ARG;
-  if (n_groups > 4096 || (int64_t)a->n_seq * a->q_per_seq * a->H > 1 << 26) return DSA_ERR_UNSUPPORTED;
+  const int64_t rows = (int64_t)a->q_per_seq * a->H;
+  if (n_groups > kMaxGroups || a->n_seq > kMaxSeq || a->n_seq * rows > 1 << 26) return DSA_ERR_UNSUPPORTED;
+  // the plan's costs have 31 bits: tiles of positions x row tiles, of the sequences' and of the groups' units
+  const int64_t units = a->n_seq * ((rows + kRows - 1) / kRows) + a->n_seq * rows / kRows + n_groups + 1;
+  if (units * ((int64_t)a->L / kKeys + 1 + kUnitCost) >= 1ll << 31) return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
 }
 
@@ -435,7 +446,7 @@ dsa_status dsa_prefix_attn(const dsa_tree_args* a, const int32_t* group_start, c
   if ((s = check_device_arch()) != DSA_OK) return s;
   TreeAttnParams p = tree_attn_params(*a);
   p.err = device_error_word();
-  const PrefixParams pp = {group_start, n_shared, n_groups};
+  const PrefixParams pp = {group_start, n_shared, n_groups, p.nsc > 1 ? kUnitCostTiled : kUnitCost};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = !p.kv_fp8      ? launch_fmt<kBf16>(p, pp, ws, st)
                         : p.nsc == 1 ? launch_fmt<kFp8Row>(p, pp, ws, st)
