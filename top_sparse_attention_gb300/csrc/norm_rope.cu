@@ -41,6 +41,23 @@ __device__ __forceinline__ float max_across(float a) {
   return a;
 }
 
+// encode8 (rope_common.cuh) of four pairs, two products per instruction: the codes of the IEEE quotients v / s, from the
+// products that enclose them where those agree.
+__device__ __forceinline__ uint32_t e4m3_pairs(float2 a, float2 b) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) | (uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16;
+}
+__device__ __forceinline__ uint2 encode_pairs(const float2 (&v)[4], float s, float r, bool fast) {
+  const float2 lo = make_float2(r * kBelow, r * kBelow), hi = make_float2(r * kAbove, r * kAbove);
+  const uint2 a = make_uint2(e4m3_pairs(fmul2(v[0], lo), fmul2(v[1], lo)), e4m3_pairs(fmul2(v[2], lo), fmul2(v[3], lo)));
+  const uint2 b = make_uint2(e4m3_pairs(fmul2(v[0], hi), fmul2(v[1], hi)), e4m3_pairs(fmul2(v[2], hi), fmul2(v[3], hi)));
+  if (fast && a.x == b.x && a.y == b.y) return a;
+  float2 q[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    q[k] = make_float2(v[k].x == 0.f ? v[k].x : __fdiv_rn(v[k].x, s), v[k].y == 0.f ? v[k].y : __fdiv_rn(v[k].y, s));
+  return make_uint2(e4m3_pairs(q[0], q[1]), e4m3_pairs(q[2], q[3]));
+}
+
 template <int FMT, int G, int NCH, int CTAS>
 __global__ void __launch_bounds__(32 * kWarps, CTAS) norm_rope_vec_kernel(const RopeParams p, const NormParams n) {
   constexpr int VEC = 32 / G;  // vectors per step of a warp
@@ -61,9 +78,18 @@ __global__ void __launch_bounds__(32 * kWarps, CTAS) norm_rope_vec_kernel(const 
   float* stage = stage_s[warp] + g * 2 * p.pairs;
   const int entries = one ? VEC * p.pairs : p.pairs;  // of the table: pairs of the step's rows, or of the row
 
+  // this lane's entries of the table, lane + 32 e: of row `row` of the step, pair `pair` (divisions once, not per step)
+  constexpr int E = 4, EP = 2;  // entries of a lane at most, those whose positions are loaded ahead
+  int entry[E];                 // row | pair << 8 | axis << 16, -1: none
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = lane + 32 * e, v = one ? i / p.pairs : 0, k = i - v * p.pairs;
+    entry[e] = i < entries ? v | k << 8 | sm.axis[k] << 16 : -1;
+  }
+
   uint4 raw[NCH];
   int64_t dst = 0;
-  int pos0 = 0;
+  int pos[EP] = {};
   // a step: vectors g of `row` and heads [h0 + VEC pass, ...), or of rows [row, row + VEC)
   struct Step {
     int64_t row;
@@ -82,10 +108,12 @@ __global__ void __launch_bounds__(32 * kWarps, CTAS) norm_rope_vec_kernel(const 
 #pragma unroll
     for (int j = 0; j < NCH; ++j)
       raw[j] = live && gl + G * j < nch ? *reinterpret_cast<const uint4*>(x + 8 * G * j) : make_uint4(0u, 0u, 0u, 0u);
-    if (s.pass == 0 && lane < entries) {  // the position of this lane's first entry of the table
-      const int v = one ? lane / p.pairs : 0;
-      const int64_t r = s.row + v;
-      if (r < p.rows) pos0 = p.pos[r * p.pos_stride + sm.axis[lane - v * p.pairs]];
+    if (s.pass == 0) {
+#pragma unroll
+      for (int e = 0; e < EP; ++e) {
+        const int64_t r = s.row + (entry[e] & 255);
+        if (entry[e] >= 0 && r < p.rows) pos[e] = p.pos[r * p.pos_stride + (entry[e] >> 16)];
+      }
     }
   };
   const int64_t item0 = (int64_t)blockIdx.x * kWarps + warp, stride = (int64_t)gridDim.x * kWarps;
@@ -100,10 +128,12 @@ __global__ void __launch_bounds__(32 * kWarps, CTAS) norm_rope_vec_kernel(const 
     const int head = head_of(at);
     if (at.pass == 0) {
       __syncwarp();  // the table's last row has been used
-      if (lane < entries) cs[lane] = pair_turn(p, sm.freq[one ? lane % p.pairs : lane], pos0);
-      for (int e = lane + 32; e < entries; e += 32) {
-        const int v = one ? e / p.pairs : 0, k = e - v * p.pairs;
-        if (at.row + v < p.rows) cs[e] = pair_turn(p, sm.freq[k], p.pos[(at.row + v) * p.pos_stride + sm.axis[k]]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (entry[e] < 0) continue;
+        const int64_t r = at.row + (entry[e] & 255);
+        const int where = e < EP ? pos[e < EP ? e : 0] : r < p.rows ? p.pos[r * p.pos_stride + (entry[e] >> 16)] : 0;
+        cs[lane + 32 * e] = pair_turn(p, sm.freq[entry[e] >> 8 & 255], where);
       }
       __syncwarp();
     }
@@ -210,10 +240,6 @@ __global__ void __launch_bounds__(32 * kWarps, CTAS) norm_rope_vec_kernel(const 
       for (int k = 0; k < 4; ++k) a = fmaxf(a, fmaxf(fabsf(v[j][k].x), fabsf(v[j][k].y)));
       return a;
     };
-    auto codes = [&](int j, float s, float lo, float hi, bool fast) {
-      const float y[8] = {v[j][0].x, v[j][0].y, v[j][1].x, v[j][1].y, v[j][2].x, v[j][2].y, v[j][3].x, v[j][3].y};
-      return encode8(y, s, lo, hi, fast);
-    };
     if constexpr (FMT == kFmtBf16) {
       __nv_bfloat16* out = p.dst ? reinterpret_cast<__nv_bfloat16*>(p.dst + to * p.dst_row_stride)
                                  : p.out + row * p.out_row_stride + head * p.out_head_stride;
@@ -238,7 +264,7 @@ __global__ void __launch_bounds__(32 * kWarps, CTAS) norm_rope_vec_kernel(const 
       for (int j = 0; j < NCH; ++j) {
         const int c = gl + G * j;
         if (keep && c < nch)
-          *reinterpret_cast<uint2*>(p.dst + to * p.dst_row_stride + 8 * c) = codes(j, div.s, div.r * kBelow, div.r * kAbove, div.fast);
+          *reinterpret_cast<uint2*>(p.dst + to * p.dst_row_stride + 8 * c) = encode_pairs(v[j], div.s, div.r, div.fast);
       }
       if (keep && gl == 0) reinterpret_cast<float*>(p.scale)[to] = div.s;
     } else if constexpr (FMT == kFmtTile) {
@@ -261,7 +287,7 @@ __global__ void __launch_bounds__(32 * kWarps, CTAS) norm_rope_vec_kernel(const 
         const int c = gl + G * j, from = lane / T * T + j;
         const float s = __shfl_sync(0xffffffffu, div.s, from), rs = __shfl_sync(0xffffffffu, div.r, from);
         if (!keep || c >= nch) continue;
-        *reinterpret_cast<uint2*>(p.dst + to * p.dst_row_stride + 8 * c) = codes(j, s, rs * kBelow, rs * kAbove, (fast >> from) & 1);
+        *reinterpret_cast<uint2*>(p.dst + to * p.dst_row_stride + 8 * c) = encode_pairs(v[j], s, rs, (fast >> from) & 1);
         if (c % 16 == 0) reinterpret_cast<float*>(p.scale)[to * tiles + c / 16] = s;
       }
     } else {
