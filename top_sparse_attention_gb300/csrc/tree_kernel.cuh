@@ -81,12 +81,13 @@ struct Aux {
   uint64_t o_done, o_free, q_full, sc_full[2], sc_empty[2], drain;
   uint32_t tmem;
   int abort;
-  int n_items, list_first;
+  int n_items;
   int tile_bad[8];
   int items[kMaxItems][8];
   alignas(16) float mx[2][2][kRows];  // the rows' maxima over half of a tile
   float sum[2][kRows];                // and, at an item's end, their sums
   uint32_t clear[2][8];               // positions to clear
+  int list_first;                     // of a launch with shared prefixes
 };
 
 template <int FMT>
@@ -128,6 +129,13 @@ struct SharedItem : Item {
   int pad;
 };
 static_assert(sizeof(SharedItem) == 48, "three 16-byte loads");
+// An item's first row: its number within the sequence, that in out and lse; and its rows.
+__device__ __forceinline__ int first_row(const Item& it) { return it.rt * kRows; }
+__device__ __forceinline__ int first_row(const SharedItem& it) { return it.row_lo; }
+__device__ __forceinline__ int64_t first_in_out(const Item& it, int rows, int lo) { return (int64_t)it.seq * rows + lo; }
+__device__ __forceinline__ int64_t first_in_out(const SharedItem& it, int, int) { return it.at; }
+__device__ __forceinline__ int rows_of(const Item&, int rows, int lo) { return min(kRows, rows - lo); }
+__device__ __forceinline__ int rows_of(const SharedItem& it, int, int) { return it.nrows; }
 template <bool SHARED>
 struct ItemOf {
   using type = Item;
@@ -778,12 +786,11 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
     bool ok = true;
 
     for (int i = 0; next_item<LONG>(p, pl, a, i, it, st); ++i) {
-      int row_lo = it.rt * kRows, nrows = min(kRows, rows - row_lo);
-      int64_t at = (int64_t)it.seq * rows + row_lo;  // the item's first row in out and lse
-      if constexpr (SHARED) {
-        if (it.t0 >= it.t1) continue;
-        row_lo = it.row_lo, nrows = it.nrows, at = it.at;
-      } else if (it.t0 >= it.t1) {  // nothing to see: padding nodes, or an empty sequence
+      if (SHARED && it.t0 >= it.t1) continue;
+      const int row_lo = first_row(it);
+      const int64_t at = first_in_out(it, rows, row_lo);  // the item's first row in out and lse
+      const int nrows = rows_of(it, rows, row_lo);
+      if (!SHARED && it.t0 >= it.t1) {  // nothing to see: padding nodes, or an empty sequence
         if (rank == 0) {
           for (int k = tw; k < nrows * (kDv / 8); k += 256)
             reinterpret_cast<uint4*>(p.out + at * kDv)[k] = make_uint4(0u, 0u, 0u, 0u);
@@ -1091,12 +1098,11 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
       pair_bar(quarter);
       l = a->sum[0][row] + a->sum[1][row];
       const bool live = row < nrows && (SHARED || (row_lo + row) / p.H < it.fresh);
-      const int part_rows = SHARED ? (nrows + 7) & ~7 : kRows;                               // rows of this partial result
-      const int64_t part_at = SHARED ? (int64_t)it.slot : (int64_t)it.slot * kRows;  // and those before it
+      const int part_rows = SHARED ? (nrows + 7) & ~7 : kRows;  // rows of this partial result
       const float inv = live && l != 0.f ? 1.f / l : 0.f;
       if (h == 0 && last) {
         // (each CTA's own: the two sum the logits' columns in different orders, so that their maxima may differ)
-        if (SHARED ? row < nrows : it.slot >= 0) pl.part_ml[part_at * 2 + rank * part_rows + row] = make_float2(m, l);
+        if (SHARED ? row < nrows : it.slot >= 0) pl.part_ml[SHARED ? (int64_t)it.slot * 2 + rank * part_rows + row : ((int64_t)it.slot * 2 + rank) * kRows + row] = make_float2(m, l);
         else if (!SHARED && rank == 0 && p.lse && row < nrows) p.lse[at + row] = !live || l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
       ok = wait(a, &a->o_done, items & 1, err) && ok;
@@ -1117,7 +1123,8 @@ __global__ void __launch_bounds__(Cfg<FMT>::THREADS, 1)
         }
         if (!last) {
         } else if (row < nrows && (SHARED || it.slot >= 0)) {
-          float4* dst = pl.part_o + part_at * (kDv / 4) + (256 * rank + c) / 4 * part_rows + row;
+          float4* dst = pl.part_o + (SHARED ? (int64_t)it.slot * (kDv / 4) + (256 * rank + c) / 4 * part_rows
+                                            : ((int64_t)it.slot * (kDv / 4) + (256 * rank + c) / 4) * kRows) + row;
 #pragma unroll
           for (int k = 0; k < 8; ++k) dst[k * part_rows] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         } else if (row < nrows) {
