@@ -12,6 +12,12 @@
 // Formats: E4M3 codes are widened to bf16 exactly; a scale per row multiplies the fp32 sums, a scale per 128 columns the
 // codes, whose product is rounded to bf16 (2^-9 of each product, as much as a bf16 cache has lost).
 //
+// Measured (36864 rows of E4M3 codes x 16 heads: 155 GFLOP, 302 MB written): 121 us, 1270 TFLOP/s and 2.5 TB/s.  Without the
+// output's copies the same kernel takes 95, without reading the sums out 87 (1780 TFLOP/s); writing alone costs as much (torch
+// fills 316 MB in 81 us), and the two do not overlap as they should: the products wait for the read-out, which waits for its
+// boxes to leave.  Tried: stores of 32 bytes straight from registers 129 (140 with eight warps), whole lines by plain stores 128,
+// eight warps with a box each 126, boxes of consecutive lines (another layout) 117.  485 rows of short prompts: 11.6, latency.
+//
 // Warp roles: 0 weights (TMA), 1 MMA issuer (the even CTA's), 4 to 11 gather rows, 12 to 15 read out, scale and store.
 #include <limits.h>
 #include <string.h>
@@ -58,7 +64,7 @@ struct Cfg {
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-// ---- waits.  Bounded; once one has run out the CTA's others return at once and the roles leave (as in tree_attn.cu).
+// ---- waits.  Bounded; once one has run out the CTA's others return at once and the roles leave (as in tc_common.cuh).
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(

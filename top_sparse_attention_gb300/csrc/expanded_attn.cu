@@ -7,7 +7,7 @@
 // of queries and positions:
 //   * S[128 x 128] = Q K^T: 12 steps of K = 16, both operands in shared memory (the rotary columns are a box of K of their
 //     own, that all heads read);
-//   * one pass over the positions keeps a reference maximum m and a sum l per row as in tree_attn.cu: m moves only where
+//   * one pass over the positions keeps a reference maximum m and a sum l per row as in tree_kernel.cuh: m moves only where
 //     a tile's maximum exceeds it by more than 2^8, so that O is rescaled rarely;
 //   * P, bf16, takes the place of S in tensor memory, and O[128 x 128] += P V: 8 steps, A in tensor memory, V MN-major.
 // Tensor memory: S and O of both tiles, 4 x 128 columns.  The two tiles take turns: while four warps take the softmax of one
@@ -22,12 +22,21 @@
 // end is cleared from V, and infinities and NaN at positions that only some rows see too (0 * inf is NaN), which are
 // added afterwards for the rows that see them.
 //
-// Work: blocks of 256 queries x chunks of `chunk` tiles of positions, longest first (plan_kernel: the lengths are on the
-// device), each for every head, dealt to the CTAs back and forth.  Blocks of more than one chunk leave fp32 partial
-// results, merged by the CTA that finishes the last of them (spans) or by merge_chunks_kernel.  Chunks of 512 tiles at most: the tensor cores truncate their sums, and O would lose
-// 2^-24 of itself per step (0.04 % over 65536 positions).
+// Work: blocks of 256 queries, each for every head (plan_kernel: the lengths are on the device).  Three ways to share it out:
+//   * many blocks: dealt to the CTAs back and forth, the longest first;
+//   * few: laid end to end and cut into one span of tiles for each CTA; a block that is cut leaves fp32 partial results, which
+//     the CTA that finishes the last of them merges, in the order of the positions (so results do not depend on which that is);
+//   * contexts that may be longer than 65536 positions: chunks of 512 tiles at most (the tensor cores truncate their sums, and O
+//     would lose 2^-24 of itself per step, 0.04 % over 65536 positions), merged by merge_chunks_kernel.
 //
-// Bound: tensor cores, 12 x 64 + 8 x 64 cycles per tile of 128 x 128.
+// Bound: tensor cores, 12 x 64 + 8 x 64 cycles per tile of 128 x 128, beside shared memory, which the first product's operands
+// fill for as long (4 + 4 KB a step).  Measured: one prompt of 8192 x 16 heads 240 us (1430 TFLOP/s of what causality leaves; tensor cores
+// busy 61 % of the time); two chunks of 1125 over 12288 positions 258 (1140; K and V, 200 MB, do not fit the L2); seven
+// prompts of 150 17.  What is left: two tiles of queries are in flight, and each waits for its softmax (1100 cycles) and the hand-overs
+// (three, of 100 to 300 cycles) before its products (1280) go on, so that a pair of tiles takes 4000 cycles where 2560 would do.
+// Without any softmax, hand-overs and products alone take 205 us, the softmax without products 176.
+// Tried: P handed over in halves 337 us (at 263 of the whole), K's boxes handed over one by one 307 (at 266), strict turns of the two
+// issuers 244, S read twice instead of held in registers 274 (at 266).
 #include <limits.h>
 #include <stddef.h>
 #include <string.h>

@@ -1,4 +1,4 @@
-// What the attention kernels on tcgen05 share (tree_attn.cu, expanded_attn.cu): bounded waits of roles, packed fp32
+// What the attention kernels on tcgen05 share (tree_kernel.cuh, expanded_attn.cu; expand.cu takes parts): bounded waits of roles, packed fp32
 // arithmetic, matrix instructions by 32-bit descriptor words, copies to tensor memory.
 #pragma once
 
