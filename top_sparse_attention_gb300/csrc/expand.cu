@@ -16,7 +16,7 @@
 // output's copies the same kernel takes 95, without reading the sums out 87 (1780 TFLOP/s); writing alone costs as much (torch
 // fills 316 MB in 81 us), and the two do not overlap as they should: the products wait for the read-out, which waits for its
 // boxes to leave.  Tried: stores of 32 bytes straight from registers 129 (140 with eight warps), whole lines by plain stores 128,
-// eight warps with a box each 126, boxes of consecutive lines (another layout) 117.  485 rows of short prompts: 11.6, latency.
+// eight warps with a box each 126, boxes of consecutive lines (another layout) 117.  364 rows of short prompts: 11.6, latency.
 //
 // Warp roles: 0 weights (TMA), 1 MMA issuer (the even CTA's), 4 to 11 gather rows, 12 to 15 read out, scale and store.
 #include <limits.h>

@@ -30,10 +30,12 @@
 //     would lose 2^-24 of itself per step, 0.04 % over 65536 positions), merged by merge_chunks_kernel.
 //
 // Bound: tensor cores, 12 x 64 + 8 x 64 cycles per tile of 128 x 128, beside shared memory, which the first product's operands
-// fill for as long (4 + 4 KB a step).  Measured: one prompt of 8192 x 16 heads 240 us (1430 TFLOP/s of what causality leaves; tensor cores
-// busy 61 % of the time); two chunks of 1125 over 12288 positions 258 (1140; K and V, 200 MB, do not fit the L2); seven
+// fill for as long (4 + 4 KB a step).  Measured: one prompt of 8192 x 16 heads 236 us (1460 TFLOP/s of what causality leaves; tensor cores
+// busy 61 % of the time); two chunks of 1125 over 12288 positions 253 (1160; K and V, 200 MB, do not fit the L2); seven
 // prompts of 150 17.  What is left: two tiles of queries are in flight, and each waits for its softmax (1100 cycles) and the hand-overs
-// (three, of 100 to 300 cycles) before its products (1280) go on, so that a pair of tiles takes 4000 cycles where 2560 would do.
+// (three, of 100 to 300 cycles) before its products (1280) go on, so that a pair of tiles takes 4000 cycles where 2560 would do;
+// and K arrives about 500 cycles late, because its places in the ring are given back that late (the bytes do not matter: a third
+// of them takes as long).
 // Without any softmax, hand-overs and products alone take 205 us, the softmax without products 176.
 // Tried: P handed over in halves 337 us (at 263 of the whole), K's boxes handed over one by one 307 (at 266), strict turns of the two
 // issuers 244, S read twice instead of held in registers 274 (at 266).
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&a->q_full[i], 1), mbar_init(&a->q_empty[i], 1);
       mbar_init(&a->s_full[i], 1), mbar_init(&a->p_full[i], 8);
       mbar_init(&a->o_done[i], 1), mbar_init(&a->o_free[i], 8);
-      mbar_init(&a->k_full[i], 1), mbar_init(&a->k_empty[i], 2);  // (both issuers)
+      mbar_init(&a->k_full[i], 1), mbar_init(&a->k_empty[i], 2);  // (one arrival for each tile of queries)
       mbar_init(&a->v_full[i], 1), mbar_init(&a->v_ready[i], 8), mbar_init(&a->v_empty[i], 2);
       mbar_init(&a->drain[i], 1);
     }
@@ -471,7 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (flat) tma_load_2d(dst, tm, bar, x, z);
           else tma_load_3d(dst, tm, bar, x, head, z);
         };
-        auto done = [&](uint64_t* empty, int tile) { ok = ok && (tile < 0 || wait_here<50>(a, &empty[tile & 1], (tile >> 1) & 1, err)); };
+        // (looked at again at once: the ring holds 1.6 tiles, and what waits for a place arrives just in time; with pauses of 50 ns
+        // 239 us instead of 236)
+        auto done = [&](uint64_t* empty, int tile) { ok = ok && (tile < 0 || wait_here(a, &empty[tile & 1], (tile >> 1) & 1, err)); };
         auto query = [&](int t) {
           ok = ok && wait_here<50>(a, &a->q_empty[t], (uses[t] & 1) ^ 1, err);
           if (!ok) return;
@@ -581,8 +585,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 4; ++i)
                   mma_ss(col_s, q_lo + b * (kBox >> 4) + 2 * i, B[b] + 2 * i, idesc_qk, b || i ? 1u : 0u);
               tc_commit(&a->s_full[t]);
-              tc_commit(&a->k_empty[gk & 1]);
-              if (j == nt - 2) tc_commit(&a->q_empty[t]);
             } else if (j + 1 < n) {
               mbar_arrive(&a->k_empty[gk & 1]);
             }
@@ -610,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * t + quarter) : "memory");
     };
+    const bool teller = (warp & 7) == 4 && lane == 0;  // (the first warp of the tile's eight)
     int g = 0, soft = 0, used = 0, edges = 0;
     bool ok = true;
     for (int r = 0; get_work(p, mine, r, w, head, f); ++r) {
@@ -626,6 +629,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool edge = pos + kTile > least;
         ok = wait_here(a, &a->s_full[t], soft & 1, err) && ok;
         tc_fence_after();
+        if (teller && ok) {
+          // S is finished, and the K (at an item's end also the Q) that it read is free: a thread says so, which saves the issuers a
+          // commit of 100 to 250 cycles.  (V too, which then waits for the next S: 296 us instead of 239.)
+          mbar_arrive(&a->k_empty[(g + j) & 1]);
+          if (j == n - 1) mbar_arrive(&a->q_empty[t]);
+        }
         if (pos + kTile > (j < n0 ? least0 : least)) {
           const int gv = g + j;
           if (t == 0 || j >= n0) {
