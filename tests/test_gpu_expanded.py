@@ -249,7 +249,7 @@ def test_many_short_sequences(dsa, n_seq):
 
 
 def test_chunks_of_positions_are_merged(dsa):
-    # few blocks of queries over long contexts: each is taken in chunks
+    # few blocks of queries over long contexts: each is cut into spans of positions
     c = Packed(4, [3, 260, 1], [9000, 12000, 60], 2)
     c.check(*c.call(dsa))
     c.check(*c.call(dsa, max_len=12000))
@@ -261,6 +261,54 @@ def test_a_context_longer_than_a_chunk_may_be(dsa):
     c = Packed(5, [40], [140000], 1)
     c.kv[..., 128:] = c.kv[..., 128:].abs()
     c.check(*c.call(dsa), more=4096 * 2.0**-23)
+
+
+@pytest.mark.parametrize("new,lens,H", [
+    ([31 * 256 - 9, 100], [9000, 100], 16),  # 512 blocks: 56 behind three rounds of 152, 16 of them too short to be cut in two
+    ([8192], [9300], 24),                    # 768 blocks: 8 behind five rounds, for at most 19 CTAs each
+])
+def test_what_is_left_behind_whole_rounds_is_cut(dsa, new, lens, H):
+    c = Packed(9, new, lens, H)
+    out, lse = c.call(dsa)
+    c.check(out, lse)
+    again = c.call(dsa)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("new,lens", [
+    ([29 * 256], [131072 - 128 + 29 * 256]),              # a block a CTA: 464 of 16 heads
+    ([14 * 256 - 3, 40], [131072 - 128 + 14 * 256 - 3, 70000]),  # spans of more than 512 tiles
+])
+def test_long_contexts_of_many_blocks(dsa, new, lens):
+    # blocks are walked in stretches of 65536 positions, 4096 steps, whose sums are added up in fp32; of the first block's 256
+    # queries the first 128 end where a stretch does
+    c = Packed(8, new, lens, 16, q_first=2, k_first=1, spare=5)
+    c.kv[..., 128:] = c.kv[..., 128:].abs()
+    T, N = c.q.shape[0], c.kv.shape[0]
+    first, last = torch.full((T, 16, 128), 3.0, device="cuda").bfloat16(), torch.full((T, 16), 3.0, device="cuda")
+    out, lse = c.call(dsa, out=first, lse=last)
+    for rows in (slice(0, 2), slice(T - 5, T)):
+        assert bool((out[rows] == 3).all()) and bool((lse[rows] == 3).all())
+    for s, (m, n) in enumerate(zip(new, lens)):
+        qa, ka = int(c.q_start[s]), int(c.kv_start[s])
+        for lo, r, h in ((0, 3, 0), (126, 4, 15), (m // 2, 3, 7), (m - 2, 2, 1), (255, 2, 14)):
+            lo = min(lo, m - r)
+            part = Packed(0, [r], [n - m + lo + r], 1)
+            part.q = c.q[qa + lo:qa + lo + r, h:h + 1]
+            part.kv, part.k_rope = c.kv[ka:ka + n - m + lo + r, h:h + 1], c.k_rope[ka:ka + n - m + lo + r]
+            part.check(out[qa + lo:qa + lo + r, h:h + 1], lse[qa + lo:qa + lo + r, h:h + 1], more=4096 * 2.0**-23)
+    again = c.call(dsa)
+    assert torch.equal(again[0][2:T - 5], out[2:T - 5]) and torch.equal(again[1][2:T - 5], lse[2:T - 5])
+    # a hidden infinity changes nothing, a seen one shows up whichever stretch holds it
+    c.kv[1 + lens[0] - 1, 3, 128 + 9] = float("inf")
+    c.kv[1 + 65536 + 100, 4, 128 + 10] = float("inf")
+    o = c.call(dsa)[0]
+    qa, end = 2, 2 + new[0]
+    same = torch.ones_like(o[qa:end], dtype=torch.bool)
+    same[-1, 3, 9] = False
+    same[:, 4, 10] = False
+    assert bool((o[qa:end] == out[qa:end])[same].all())
+    assert bool(torch.isinf(o[end - 1, 3, 9])) and bool(torch.isinf(o[qa:end, 4, 10]).all())
 
 
 @pytest.mark.parametrize("sm", [0.9, 1e-4])

@@ -160,12 +160,12 @@ def test_expanded_attn_workspaces(native):
     for kw in (dict(n_seq=0), dict(T=0)):
         assert lib.dsa_expanded_attn_workspace_size(attn_args(native, **kw), ctypes.byref(n)) == 0 and n.value == 0
         assert lib.dsa_expanded_attn(attn_args(native, **kw), None, 0, None) == 0
-    # partial results: two for each SM at most, or those of chunks where contexts may be longer than 65536 positions
+    # partial results: two for each SM at most, and one of blocks in stretches where contexts may be longer than 65536 positions
     sizes = []
-    for kw in (dict(T=8192, N=8192, n_seq=1, H=16), dict(T=8192, N=131072, n_seq=1, H=16), dict(T=8192, N=131072, n_seq=4, H=16, max_len=65536)):
+    for kw in (dict(T=8192, N=8192, n_seq=1, H=16), dict(T=1 << 23, N=1 << 23, n_seq=1, H=128), dict(T=8192, N=131072, n_seq=4, H=16, max_len=65536)):
         assert lib.dsa_expanded_attn_workspace_size(attn_args(native, **kw), ctypes.byref(n)) == 0
         sizes.append(n.value)
-    assert sizes[0] < 50 << 20 and sizes[1] > 8192 * 16 * 520 * 2 and sizes[2] < 50 << 20
+    assert sizes[0] < 50 << 20 and sizes[1] < 80 << 20 and sizes[2] < 50 << 20
 
 
 def tree(native, **kw):

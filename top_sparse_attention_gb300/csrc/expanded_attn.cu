@@ -22,16 +22,16 @@
 // end is cleared from V, and infinities and NaN at positions that only some rows see too (0 * inf is NaN), which are
 // added afterwards for the rows that see them.
 //
-// Work: blocks of 256 queries, each for every head (plan_kernel: the lengths are on the device).  Three ways to share it out:
-//   * many blocks: dealt to the CTAs back and forth, the longest first;
+// Work: blocks of 256 queries, each for every head (plan_kernel: the lengths are on the device).  Two ways to share it out:
+//   * many blocks: dealt to the CTAs back and forth, the longest first; what is left behind whole rounds is cut for all CTAs;
 //   * few: laid end to end and cut into one span of tiles for each CTA; a block that is cut leaves fp32 partial results, which
-//     the CTA that finishes the last of them merges, in the order of the positions (so results do not depend on which that is);
-//   * contexts that may be longer than 65536 positions: chunks of 512 tiles at most (the tensor cores truncate their sums, and O
-//     would lose 2^-24 of itself per step, 0.04 % over 65536 positions), merged by merge_chunks_kernel.
+//     the CTA that finishes the last of them merges, in the order of the positions (so results do not depend on which that is).
+// The tensor cores truncate their sums, and O loses 2^-24 of itself per step, 0.04 % over 65536 positions.  Longer contexts
+// are walked in stretches of 512 tiles, whose O and l are added up in fp32, in memory (a form of the kernel of its own).
 //
 // Bound: tensor cores, 12 x 64 + 8 x 64 cycles per tile of 128 x 128, beside shared memory, which the first product's operands
-// fill for as long (4 + 4 KB a step).  Measured: one prompt of 8192 x 16 heads 236 us (1460 TFLOP/s of what causality leaves; tensor cores
-// busy 61 % of the time); two chunks of 1125 over 12288 positions 253 (1160; K and V, 200 MB, do not fit the L2); seven
+// fill for as long (4 + 4 KB a step).  Measured: one prompt of 8192 x 16 heads 234 us (1470 TFLOP/s of what causality leaves; tensor cores
+// busy 61 % of the time); two chunks of 1125 over 12288 positions 252 (1165; K and V, 200 MB, do not fit the L2); seven
 // prompts of 150 17.  What is left: two tiles of queries are in flight, and each waits for its softmax (1100 cycles) and the hand-overs
 // (three, of 100 to 300 cycles) before its products (1280) go on, so that a pair of tiles takes 4000 cycles where 2560 would do;
 // and K arrives about 500 cycles late, because its places in the ring are given back that late (the bytes do not matter: a third
@@ -60,27 +60,28 @@ constexpr int kOffRing = 6 * kBox;          // two tiles of Q first
 constexpr int kThreads = 640;
 constexpr float kLazy = 8.f;                // log2 growth of a row's maximum that is left unscaled
 constexpr int kSms = 152;
-constexpr int kMaxChunk = 512, kMinChunk = 4;  // tiles
+constexpr int kStretch = 512;                  // tiles whose products are summed in tensor memory, at most
+constexpr int kLengths = 512;                  // that the counting sort tells apart
 constexpr int kFixed = 3;                      // what starting on a block costs, in tiles
 constexpr int kMinSpan = 4;                    // tiles of a span, at least
+constexpr int kMinPart = 16;                   // and of a part of an item of the list's last round
 constexpr int kMaxSeq = 4096;
 constexpr uint32_t kColS = 0, kColO = 256;
 
 // What the planning kernel leaves for the others.
 constexpr int kSpanItems = 3 * kSms;         // fewer than this many blocks and heads may be cut into spans
 struct alignas(16) SpanItem {  // (read as two 16-byte words)
-  int seq, q0, t0, t1, head, slot;  // slot: of the partial result, -1: the whole block
-  int parts;                        // of this head of the block (0: nothing to do, no tile of it is in this span)
-  int first;                        // span of the first of them
+  int seq, q0, t0, t1, head, slot;  // head: with the item's number << 8; slot: of the partial result, -1: the whole block
+  int parts;                        // of this head of the block (0: nothing to do here)
+  int first;                        // span, or place in the last round, of the first of them
 };
 struct Plan {
-  int n_work, spans;
   int done[kSpanItems][2];                   // parts that are finished, of each block and head and each tile of queries
-  int2 place[kSms];                           // of each CTA's items in the list: first, number
+  int4 place[kSms];                           // of each CTA: items of the list of work; its own: first, number
   SpanItem list[kSpanItems + kSms];
 };
 
-static_assert(sizeof(SpanItem) == 32 && offsetof(Plan, list) % 16 == 0 && offsetof(Plan, place) % 8 == 0, "vector reads");
+static_assert(sizeof(SpanItem) == 32 && offsetof(Plan, list) % 16 == 0 && offsetof(Plan, place) % 16 == 0, "vector reads");
 
 struct ExpandedAttnParams {
   const int32_t* q_start;  // [n_seq + 1]
@@ -93,7 +94,7 @@ struct ExpandedAttnParams {
   int64_t v_row_stride, v_head_stride;
   __nv_bfloat16* out;      // [T, H, 128]
   float* lse;              // [T, H] or null
-  int chunk;               // tiles of 128 positions
+  int shift;               // of tiles, to lengths of at most kLengths
   int grid;                // CTAs of the attention kernel
   bool may_span;           // blocks may be cut into spans (see plan_kernel)
   // workspace
@@ -102,6 +103,8 @@ struct ExpandedAttnParams {
   int max_work;
   float2* part_ml;         // partial results: reference maximum and sum of weights, output
   float* part_o;
+  float2* sum_ml;          // per CTA, of a block in stretches: the same of the stretches so far, a thread's own
+  float4* sum_o;
   int* err;                // device error word
 };
 
@@ -120,10 +123,8 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 
 struct Work {
   int seq, q0, t0, t1;  // queries q0 ... of the sequence, tiles [t0, t1) of positions
-  int64_t part;         // row of the partial results of the first query, -1: the whole block, written to the output
-  int step;             // between the queries' rows of partial results
-  int parts, first;     // of a block that is cut into spans (0 parts: nothing to do)
-  int item;             // its number
+  int entry;            // of the plan's list, -1: of the list of work (its slot, parts and so on are read when they are needed)
+  bool begins, ends;    // the first, the last stretch of it
 };
 
 struct Facts {
@@ -164,12 +165,12 @@ __device__ __forceinline__ int edges_of(const Facts& f, const Work& w, int n0, i
 }
 
 // ---------------------------------------------------------------------------------------------
-// the list of work: blocks and their chunks, the longest first (a counting sort by tiles; which of two of equal length
+// the list of work: blocks, the longest first (a counting sort by tiles; which of two of equal length
 // comes first does not matter to the results)
 
 __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) {
   __shared__ int base[kMaxSeq + 1];          // blocks before each sequence
-  __shared__ int place[kMaxChunk + 1];       // by tiles: how many, then where the next goes
+  __shared__ int place[kLengths + 1];        // by tiles: how many, then where the next goes
   __shared__ int warp_sum[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int run = 0;
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
     __syncthreads();
   }
   if (tid == 0) base[p.n_seq] = run;
-  for (int i = tid; i <= kMaxChunk; i += 1024) place[i] = 0;
+  for (int i = tid; i <= kLengths; i += 1024) place[i] = 0;
   __syncthreads();
   auto find = [&](int b, int& q0) {  // the sequence of block b, and the block's first query
     int lo = 0, hi = p.n_seq - 1;
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
     q0 = (b - base[lo]) * kBlock;
     return lo;
   };
-  if (p.may_span && (int64_t)run * p.H < 3 * p.grid) {
+  if (p.may_span && (int64_t)run * p.H < kSpanItems) {
     // Few blocks: laid end to end, a head of a block after another, each with a fixed cost before its tiles, and cut into one
     // span for each CTA, if that is shorter than dealing them out whole
     int q0 = 0, seq = 0, tiles = 0;
@@ -248,7 +249,6 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
     const int items = run * p.H, total = all * p.H, W = max((total + p.grid - 1) / p.grid, kMinSpan);  // (below 2^25)
     const int whole = items <= p.grid ? longest : total / p.grid + longest / 2;
     if (W + 2 * kFixed < whole) {
-      if (tid == 0) p.plan->spans = 1;
       // The order: a sequence after another, of it a head after another, of that the blocks, so that the CTAs that read the
       // same keys and values are neighbours and do so at about the same time (two chunks of 1125 tokens over 12K positions,
       // 200 MB of keys and values: 260 us with the heads of a block side by side)
@@ -270,10 +270,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
       };
       if (tid < p.grid) {
         const int x0 = tid * W, x1 = min(x0 + W, total);
-        int2 mine = make_int2(0, 0);
+        int4 mine = make_int4(0, 0, 0, 0);
         if (x0 < total) {
           const int i0 = item_at(x0);
-          mine = make_int2(i0 + tid, item_at(x1 - 1) - i0 + 1);
+          mine = make_int4(0, i0 + tid, item_at(x1 - 1) - i0 + 1, 0);
         }
         p.plan->place[tid] = mine;
       }
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
         SpanItem it = {};
         it.seq = s;
         it.q0 = (b - b0) * kBlock;
-        it.head = head;
+        it.head = head | tid << 8;
         p.plan->done[tid][0] = p.plan->done[tid][1] = 0;
         const int c = before[b + 1] - before[b], n = c - kFixed;
         const int begin = before[b0] * p.H + head * (before[b0 + nb] - before[b0]) + before[b] - before[b0], first = begin + kFixed;
@@ -298,27 +298,21 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
       return;
     }
   }
-  if (tid == 0) p.plan->spans = 0;
-  // Blocks and their chunks, the longest first
+  // Blocks, the longest first
   // pass 0 counts, pass 1 places
   for (int pass = 0; pass < 2; ++pass) {
     for (int b = tid; b < run; b += 1024) {
       int q0;
       const int lo = find(b, q0);
       const int n = block_tiles(block_facts(p, lo, q0));
-      int t0 = 0;
-      do {
-        const int t1 = min(t0 + p.chunk, n);
-        const int at = atomicAdd(&place[t1 - t0], 1);
-        if (pass && at < p.max_work) p.work[at] = make_int4(lo, q0, t0, t1);
-        t0 = t1;
-      } while (t0 < n);
+      const int at = atomicAdd(&place[min(n >> p.shift, kLengths)], 1);
+      if (pass && at < p.max_work) p.work[at] = make_int4(lo, q0, 0, n);
     }
     __syncthreads();
     if (pass == 0) {
       // how many are longer, for each length: the running sum from the longest on
-      static_assert(kMaxChunk < 1024, "a thread a length");
-      const int at = kMaxChunk - tid, c = at >= 0 ? place[at] : 0;
+      static_assert(kLengths < 1024, "a thread a length");
+      const int at = kLengths - tid, c = at >= 0 ? place[at] : 0;
       int incl = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -330,41 +324,83 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
       int ahead = 0;
       for (int i = 0; i < warp; ++i) ahead += warp_sum[i];
       if (at >= 0) place[at] = ahead + incl - c;
-      if (at == 0) p.plan->n_work = min(ahead + incl, p.max_work);
       __syncthreads();
+    }
+  }
+  // What is left behind whole rounds, where that is half a round or less: its items are cut, into parts of kMinPart tiles at
+  // least, for all CTAs (3.4 rounds of 16 heads: 8192 tokens over 20480 positions 1.01 ms, uncut 1.09; over 9216, whose last items
+  // are of 8 to 24 tiles, cut into parts of 8 and more 0.419, uncut 0.407)
+  if (tid < p.grid) {
+    const int items = min(run, p.max_work) * p.H, rounds = items / p.grid, left = items % p.grid;
+    const int ways = left ? max(min(p.grid / left, p.work[rounds * p.grid / p.H].w / kMinPart), 1) : 1;  // (the longest of them)
+    const int at = rounds & 1 ? p.grid - 1 - tid : tid, x = at / ways;
+    p.plan->done[tid][0] = p.plan->done[tid][1] = 0;
+    p.plan->place[tid] = make_int4(rounds + (ways == 1 && at < left), tid, ways > 1 && x < left, 0);
+    if (ways > 1 && x < left) {
+      const int i = rounds * p.grid + x;
+      const int4 v = p.work[i / p.H];
+      const int n = v.w, parts = max(min(ways, n / kMinPart), 1), part = at - x * ways;
+      SpanItem it = {};
+      it.seq = v.x, it.q0 = v.y;
+      it.head = i % p.H | x << 8;
+      it.parts = part < parts ? parts : 0;
+      it.first = x * ways;
+      it.t0 = (int)((int64_t)n * part / parts), it.t1 = (int)((int64_t)n * (part + 1) / parts);
+      it.slot = parts == 1 ? -1 : 2 * at + (part == 0);
+      p.plan->list[tid] = it;
     }
   }
 }
 
 // ---------------------------------------------------------------------------------------------
 
-// Item r of this CTA: of its span's list, or of the list of work, dealt back and forth, every head of an entry after another.
+// Item r of this CTA: of the list of work, dealt back and forth, every head of an entry after another; then of its own
+// list.
 struct Mine {
-  bool spans;
-  int first;      // in the span's list
-  int64_t items;  // in it, or all of them
+  int rounds;
+  int first, items;  // of its own
 };
-__device__ __forceinline__ bool get_work(const ExpandedAttnParams& p, const Mine& mine, int r, Work& w, int& head, Facts& f) {
-  if (mine.spans) {
-    if (r >= mine.items) return false;
-    const int4* v = reinterpret_cast<const int4*>(p.plan->list + mine.first + r);
+__device__ __forceinline__ bool get_work(const ExpandedAttnParams& p, const Mine& mine, int r, Work& w, int& head, Facts& f, bool& skip) {
+  if (r >= mine.rounds) {
+    if (r - mine.rounds >= mine.items) return false;
+    w.entry = mine.first + r - mine.rounds;
+    const int4* v = reinterpret_cast<const int4*>(p.plan->list + w.entry);
     const int4 a = v[0], b = v[1];
-    w.seq = a.x, w.q0 = a.y, w.t0 = a.z, w.t1 = a.w, w.parts = b.z, w.first = b.w;
-    w.item = mine.first + r - (int)blockIdx.x;  // (entry of item i in span k: i + k)
-    head = b.x;
-    w.part = b.y < 0 ? -1 : (int64_t)b.y * kBlock, w.step = 1;
-    f = block_facts(p, w.seq, w.q0);
+    w.seq = a.x, w.q0 = a.y, w.t0 = a.z, w.t1 = a.w;
+    head = b.x & 255;
+    skip = b.z == 0;
+    f = block_facts(p, w.seq, w.q0);  // (once in each branch: behind both it costs the softmax warps 30 spilled registers)
     return true;
+  } else {
+    const int g = (int)gridDim.x, c = (int)blockIdx.x, i = r * g + (r & 1 ? g - 1 - c : c);
+    const int4 v = p.work[i / p.H];
+    head = i % p.H;
+    w.seq = v.x, w.q0 = v.y, w.t0 = v.z, w.t1 = v.w, w.entry = -1;
+    skip = false;
   }
-  const int g = (int)gridDim.x, c = (int)blockIdx.x;
-  const int64_t i = (int64_t)r * g + (r & 1 ? g - 1 - c : c);
-  if (i >= mine.items) return false;
-  const int4 v = p.work[i / p.H];
-  head = (int)(i % p.H);
-  w.seq = v.x, w.q0 = v.y, w.t0 = v.z, w.t1 = v.w, w.parts = 1, w.first = 0, w.item = 0;
   f = block_facts(p, w.seq, w.q0);
-  w.part = block_tiles(f) > p.chunk ? ((int64_t)(w.t0 / p.chunk) * p.T + f.q_row + w.q0) * p.H + head : -1;
-  w.step = p.H;
+  return true;
+}
+
+// The next item with anything to do, or with LONG the next stretch of one.
+struct Walk {
+  int r = 0, stop = 0;  // the next item; where the one in hand ends
+};
+template <bool LONG>
+__device__ __forceinline__ bool next_work(const ExpandedAttnParams& p, const Mine& mine, Walk& k, Work& w, int& head, Facts& f) {
+  if (LONG && w.t1 < k.stop) {
+    w.t0 = w.t1;
+    w.begins = false;
+  } else {
+    bool skip;
+    do {
+      if (!get_work(p, mine, k.r++, w, head, f, skip)) return false;
+    } while (skip);
+    k.stop = w.t1;
+    w.begins = true;
+  }
+  if (LONG) w.t1 = min(k.stop, w.t0 + kStretch);
+  w.ends = w.t1 == k.stop;
   return true;
 }
 
@@ -377,7 +413,7 @@ __device__ __forceinline__ void write_merged(const ExpandedAttnParams& p, int64_
 }
 
 // Rows [from, from + 128) of a block that was cut into spans, by eight warps, four rows of each at a time, the parts in order.
-__device__ __forceinline__ void merge_parts(const ExpandedAttnParams& p, const Work& w, const Facts& f, int head, int from, int warp) {
+__device__ __forceinline__ void merge_parts(const ExpandedAttnParams& p, const Work& w, const Facts& f, int head, int parts, int first, int from, int warp) {
   constexpr int U = 4;
   const int lane = threadIdx.x & 31;
   for (int i0 = from + U * warp; i0 < min(from + kTile, f.nrows); i0 += 8 * U) {
@@ -385,9 +421,9 @@ __device__ __forceinline__ void merge_parts(const ExpandedAttnParams& p, const W
     float4 o[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) M[u] = -INFINITY, l[u] = 0.f, o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int q = 0; q < w.parts; ++q) {
+    for (int q = 0; q < parts; ++q) {
       // the first part ends a span (its second slot), the others begin the spans behind it
-      const int64_t slot = 2 * (w.first + q) + (q == 0);
+      const int64_t slot = 2 * (first + q) + (q == 0);
       float2 ml[U];
       float4 v[U];
 #pragma unroll
@@ -413,6 +449,8 @@ __device__ __forceinline__ void merge_parts(const ExpandedAttnParams& p, const W
   }
 }
 
+// LONG: contexts of more than kStretch tiles, whose blocks are walked in stretches.
+template <bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
     expanded_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v,
@@ -446,16 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = a->tmem;
   pdl_wait();  // the plan
   Mine mine;
-  mine.spans = p.plan->spans != 0;
-  mine.first = 0;
-  if (mine.spans) {
-    const int2 place = p.plan->place[blockIdx.x];
-    mine.first = place.x, mine.items = place.y;
-  } else {
-    mine.items = (int64_t)p.plan->n_work * p.H;
-  }
+  const int4 place = p.plan->place[blockIdx.x];
+  mine.rounds = place.x, mine.first = place.y, mine.items = place.z;
 
   Work w;
+  w.t1 = 0;
   Facts f;
   int head;
   // Registers: 640 x 96 at launch; the softmax warps take what the others leave (128 x 64 + 512 x 104 = 61440)
@@ -483,8 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&a->q_full[t], 3 * kBox);
           for (int b = 0; b < 3; ++b) tma_load_3d(smem + (3 * t + b) * kBox, &tm_q, &a->q_full[t], 64 * b, head, f.q_row + w.q0 + kTile * t);
         };
-        for (int r = 0; ok && get_work(p, mine, r, w, head, f); ++r) {
-          if (w.parts == 0) continue;
+        for (Walk k; ok && next_work<LONG>(p, mine, k, w, head, f);) {
           const int n0 = tiles_for(f, w, 0), n1 = tiles_for(f, w, 1), n = max(n0, n1);
           if (n0) query(0);
           for (int j = 0; ok && j < n; ++j, ++g) {
@@ -532,8 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int used = 0, soft = 0;  // items and softmax tiles
       int edges = 0;           // tiles of positions that were looked through
       bool ok = true;
-      for (int r = 0; ok && uniform(get_work(p, mine, r, w, head, f)); ++r) {
-        if (uniform(w.parts) == 0) continue;
+      for (Walk k; ok && uniform(next_work<LONG>(p, mine, k, w, head, f));) {
         const int n0 = uniform(tiles_for(f, w, 0)), n1 = uniform(tiles_for(f, w, 1)), n = max(n0, n1), nt = t ? n1 : n0;
         if (n == 0) continue;
         const int least0 = sees(f, 0), least1 = sees(f, kTile);
@@ -615,8 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool teller = (warp & 7) == 4 && lane == 0;  // (the first warp of the tile's eight)
     int g = 0, soft = 0, used = 0, edges = 0;
     bool ok = true;
-    for (int r = 0; get_work(p, mine, r, w, head, f); ++r) {
-      if (w.parts == 0) continue;
+    for (Walk walk; next_work<LONG>(p, mine, walk, w, head, f);) {
       const int n0 = tiles_for(f, w, 0), n1 = tiles_for(f, w, 1), n = t ? n1 : n0;
       const int i = kTile * t + row;                             // row of the block
       const int see = i < f.nrows ? sees(f, i) : 0;              // positions that it sees
@@ -743,13 +773,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         ++used;
       }
+      int4 part_of = make_int4(0, -1, 1, 0);  // head and item, slot, parts, first of them
+      if (w.entry >= 0) part_of = reinterpret_cast<const int4*>(p.plan->list + w.entry)[1];
+      const int slot = part_of.y, parts = part_of.z;
+      float now = 1.f, before = 0.f;  // what brings this stretch's sums, and those of the ones before, to their maximum
+      const int64_t own = ((int64_t)blockIdx.x * 2 + t) * 2 + h;  // this thread's: no other one touches them
+      const bool adds = LONG && !(w.begins && w.ends);
+      if (adds) {
+        float2* ml = p.sum_ml + own * kTile + row;
+        const float2 old = w.begins ? make_float2(-INFINITY, 0.f) : *ml;
+        const float M = fmaxf(m, old.x);
+        now = m == -INFINITY ? 0.f : ex2(m - M);
+        before = old.x == -INFINITY ? 0.f : ex2(old.x - M);
+        m = M;
+        l = fmaf(old.y, before, l * now);
+        if (!w.ends) *ml = make_float2(m, l);
+      }
       a->rows[t][h][row] = l;  // (O is finished: the maxima of the last tile have been read)
       pair_bar();
       l = a->rows[t][0][row] + a->rows[t][1][row];
       const float inv = l != 0.f ? 1.f / l : 0.f;
-      const int64_t part = w.part + (int64_t)i * w.step;
-      if (live && h == 0) {
-        if (w.part >= 0) p.part_ml[part] = make_float2(m, l);
+      const int64_t part = (int64_t)slot * kBlock + i;
+      if (live && h == 0 && w.ends) {
+        if (slot >= 0) p.part_ml[part] = make_float2(m, l);
         else if (p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
       // (from the first tile of positions that was looked through: of the first queries' where they are multiplied with it)
@@ -776,8 +822,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (!live) {
-        } else if (w.part >= 0) {
+        if (adds) {
+          float4* sum = p.sum_o + (own * (kDv / 8) + c0 / 4) * kTile + row;
+#pragma unroll
+          for (int k = 0; k < 8; ++k, sum += kTile) {
+            float4 v = w.begins ? make_float4(0.f, 0.f, 0.f, 0.f) : *sum;
+            v.x = fmaf(v.x, before, o[4 * k] * now), v.y = fmaf(v.y, before, o[4 * k + 1] * now);
+            v.z = fmaf(v.z, before, o[4 * k + 2] * now), v.w = fmaf(v.w, before, o[4 * k + 3] * now);
+            if (!w.ends) *sum = v;
+            o[4 * k] = v.x, o[4 * k + 1] = v.y, o[4 * k + 2] = v.z, o[4 * k + 3] = v.w;
+          }
+        }
+        if (!live || !w.ends) {
+        } else if (slot >= 0) {
           float4* dst = reinterpret_cast<float4*>(p.part_o + part * kDv + c);
 #pragma unroll
           for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
@@ -799,15 +856,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive(&a->o_free[t]);
       }
-      if (w.parts > 1) {  // whoever finishes the last part of the tile's rows merges them
+      if (w.ends && parts > 1) {  // whoever finishes the last part of the tile's rows merges them
         __threadfence();
         __syncwarp();
         asm volatile("bar.sync %0, 256;" ::"r"(9 + t) : "memory");
-        if (row == 0 && h == 0) a->last[t] = atomicAdd(&p.plan->done[w.item][t], 1) == w.parts - 1;
+        if (row == 0 && h == 0) a->last[t] = atomicAdd(&p.plan->done[part_of.x >> 8][t], 1) == parts - 1;
         asm volatile("bar.sync %0, 256;" ::"r"(9 + t) : "memory");
         if (a->last[t]) {
           __threadfence();
-          merge_parts(p, w, f, head, kTile * t, (warp - 4) & 7);
+          merge_parts(p, w, f, head, parts, part_of.w, kTile * t, (warp - 4) & 7);
         }
         asm volatile("bar.sync %0, 256;" ::"r"(11 + t) : "memory");  // (`last` has been read)
       }
@@ -821,80 +878,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Of the blocks whose contexts are longer than a chunk.
-__global__ void __launch_bounds__(256) merge_chunks_kernel(const ExpandedAttnParams p) {
-  const int64_t rows = (int64_t)p.T * p.H, at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, t = (int)(at / p.H);
-  pdl_wait();
-  if (at >= rows || t < p.q_start[0] || t >= p.q_start[p.n_seq]) return;
-  int lo = 0, hi = p.n_seq - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.q_start[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  Facts f;
-  seq_facts(p, lo, f);
-  const int i = t - f.q_row;
-  if (i < 0 || i >= f.m) return;
-  f = block_facts(p, lo, i / kBlock * kBlock);
-  const int chunks = (block_tiles(f) + p.chunk - 1) / p.chunk;
-  if (chunks <= 1) return;  // written by the attention kernel
-  float M = -INFINITY, l = 0.f;
-  for (int c = 0; c < chunks; ++c) M = fmaxf(M, p.part_ml[c * rows + at].x);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = 0; c < chunks; ++c) {
-    const float2 ml = p.part_ml[c * rows + at];
-    if (ml.y == 0.f) continue;  // the row saw nothing there
-    const float g = exp2f(ml.x - (M == -INFINITY ? 0.f : M));
-    const float4 v = reinterpret_cast<const float4*>(p.part_o + (c * rows + at) * kDv)[lane];
-    l = fmaf(g, ml.y, l);
-    o.x = fmaf(g, v.x, o.x), o.y = fmaf(g, v.y, o.y), o.z = fmaf(g, v.z, o.z), o.w = fmaf(g, v.w, o.w);
-  }
-  write_merged(p, at, M, l, o);
-}
-
 int blocks_of(const ExpandedAttnParams& p) {  // at most
   const int64_t b = p.n_seq == 1 ? (p.T + kBlock - 1) / kBlock : (int64_t)p.T / kBlock + p.n_seq;
   return (int)(b < p.T ? b : p.T);
 }
 int longest(const ExpandedAttnParams& p) { return (int)(((int64_t)(p.max_len < p.N ? p.max_len : p.N) + kTile - 1) / kTile); }
-int parts_of(const ExpandedAttnParams& p) { return longest(p) > p.chunk ? (longest(p) + p.chunk - 1) / p.chunk : 1; }
-
-// Blocks whose contexts may be longer than a chunk are cut at chunks: of 512 tiles where the blocks of all heads fill the
-// SMs, else of as many as make two rounds of them, by the sequences' mean length.  Others may be cut into spans, if there
-// is work enough for that.
-constexpr int64_t kMostPartial = 512ll << 20;
+// Blocks may be cut into spans where that can pay: where a whole one is longer than a span and two starts.
 void set_cuts(ExpandedAttnParams* p) {
   const int64_t items = (int64_t)blocks_of(*p) * p->H;
-  p->chunk = kMaxChunk;
-  p->may_span = longest(*p) <= kMaxChunk && longest(*p) > kMinSpan + kFixed;
-  const int64_t splits = (2 * kSms) / (items > 0 ? items : 1);
-  if (longest(*p) > kMaxChunk && splits > 1) {
-    const int64_t mean = ((int64_t)p->N + (int64_t)p->n_seq * kTile - 1) / ((int64_t)p->n_seq * kTile);
-    const int64_t c = (mean + splits - 1) / splits;
-    p->chunk = (int)(c < kMinChunk ? kMinChunk : c > kMaxChunk ? kMaxChunk : c);
-    while (p->chunk < kMaxChunk && (int64_t)parts_of(*p) * p->T * p->H * (kDv + 2) * 4 > kMostPartial)
-      p->chunk = p->chunk * 2 < kMaxChunk ? p->chunk * 2 : kMaxChunk;
-  }
-  int64_t ctas = items * parts_of(*p);
+  p->shift = 0;
+  while (longest(*p) >> p->shift > kLengths) ++p->shift;
+  p->may_span = longest(*p) > kMinSpan + kFixed;
+  int64_t ctas = items;
   if (p->may_span) ctas = (items * (longest(*p) + kFixed) + kMinSpan - 1) / kMinSpan;
   p->grid = (int)(ctas < kSms ? ctas : kSms);
 }
 
 struct Layout {
-  size_t work, part_ml, part_o, total;
-  int64_t max_work;
+  size_t work, part_ml, part_o, sum_ml, sum_o, total;
 };
 Layout layout_of(const ExpandedAttnParams& p) {
   Layout l;
-  const int parts = parts_of(p);
-  l.max_work = (int64_t)blocks_of(p) * parts;
-  const int64_t rows = parts > 1 ? (int64_t)parts * p.T * p.H : p.may_span ? 2 * p.grid * kBlock : 0;
+  const size_t rows = p.may_span ? (size_t)2 * p.grid * kBlock : 0, sums = longest(p) > kStretch ? (size_t)p.grid * kBlock : 0;
   l.work = align_up(sizeof(Plan), 256);
-  l.part_ml = l.work + align_up((size_t)l.max_work * sizeof(int4), 256);
-  l.part_o = l.part_ml + align_up((size_t)rows * sizeof(float2), 256);
-  l.total = l.part_o + (size_t)rows * kDv * sizeof(float);
+  l.part_ml = l.work + align_up((size_t)blocks_of(p) * sizeof(int4), 256);
+  l.part_o = l.part_ml + align_up(rows * sizeof(float2), 256);
+  l.sum_ml = l.part_o + rows * kDv * sizeof(float);
+  l.sum_o = l.sum_ml + align_up(2 * sums * sizeof(float2), 256);
+  l.total = l.sum_o + sums * kDv * sizeof(float);
   return l;
 }
 
@@ -914,7 +925,9 @@ cudaError_t launch(ExpandedAttnParams p, const dsa_expanded_attn_args& a, void* 
   p.work = reinterpret_cast<int4*>(base + l.work);
   p.part_ml = reinterpret_cast<float2*>(base + l.part_ml);
   p.part_o = reinterpret_cast<float*>(base + l.part_o);
-  p.max_work = (int)l.max_work;
+  p.sum_ml = reinterpret_cast<float2*>(base + l.sum_ml);
+  p.sum_o = reinterpret_cast<float4*>(base + l.sum_o);
+  p.max_work = blocks_of(p);
   CUtensorMap tq, tk, tr, tv;
   // (without positions nothing of k and v is loaded: their maps are q's)
   const bool any = p.N > 0;
@@ -929,17 +942,13 @@ cudaError_t launch(ExpandedAttnParams p, const dsa_expanded_attn_args& a, void* 
   if (encode_tensor_map(&tr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(any ? a.k_rope : a.q), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) !=
       CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem_once(&allowed, reinterpret_cast<const void*>(expanded_attn_kernel), kSmem);
+  const bool stretches = longest(p) > kStretch;
+  auto kern = stretches ? expanded_attn_kernel<true> : expanded_attn_kernel<false>;
+  static std::atomic<uint64_t> allowed[2];
+  cudaError_t e = allow_smem_once(&allowed[stretches], reinterpret_cast<const void*>(kern), kSmem);
   if (e != cudaSuccess) return e;
   if ((e = launch_kernel(plan_kernel, dim3(1), dim3(1024), 0, stream, false, p)) != cudaSuccess) return e;
-  if ((e = launch_kernel(expanded_attn_kernel, dim3((unsigned)p.grid), dim3(kThreads), kSmem, stream, true, tq, tk, tr, tv,
-                         p)) != cudaSuccess)
-    return e;
-  if (parts_of(p) > 1) {
-    e = launch_kernel(merge_chunks_kernel, dim3((unsigned)(((int64_t)p.T * p.H + 7) / 8)), dim3(256), 0, stream, true, p);
-  }
-  return e;
+  return launch_kernel(kern, dim3((unsigned)p.grid), dim3(kThreads), kSmem, stream, true, tq, tk, tr, tv, p);
 }
 
 dsa_status check_expanded(const dsa_expanded_attn_args* a) {
