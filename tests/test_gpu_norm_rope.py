@@ -94,6 +94,22 @@ def test_heads(dsa, shape, norm, style):
     check_bf16(dsa.dsa_norm_rope(c.x, c.pos, c.freq, **c.kw), *c.want())
 
 
+@pytest.mark.parametrize("rows,width,nd,ro,rd", [
+    (65, 128, 128, 0, 128), (2500, 128, 128, 0, 128), (3, 64, 64, 0, 64), (40, 256, 256, 0, 256), (70, 192, 192, 48, 96), (61, 128, 128, 56, 72),
+    (2600, 576, 512, 320, 256), (2600, 576, 512, 448, 128), (2600, 576, 512, 440, 136), (5, 640, 640, 0, 256),
+])
+@pytest.mark.parametrize("style", ["half", "pairs"])
+def test_one_head_that_turns_many_columns(dsa, rows, width, nd, ro, rd, style):
+    # rows whose pairs are more than a table of turns holds for several rows of a warp
+    c = Case(rows + rd, rows, 1, width, "rms", 0, nd, ro, rd, style)
+    check_bf16(dsa.dsa_norm_rope(c.x, c.pos, c.freq, **c.kw), *c.want())
+    want, err = c.want()
+    for kind in ("fp8", "t128", "mx"):
+        kv, scale = pools(kind, rows, width)
+        dsa.dsa_norm_rope_append(c.x[:, 0], c.pos, c.freq, kv, scale=scale, **c.kw)
+        check_rows(kind, kv, scale, want[:, 0], err[:, 0])
+
+
 @pytest.mark.parametrize("weight,bias", [(False, False), (True, True), (False, True)])
 @pytest.mark.parametrize("axes", [1, 3])
 def test_without_weights_and_with_axes(dsa, weight, bias, axes):

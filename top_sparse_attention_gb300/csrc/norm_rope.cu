@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(32 * kWarps, CTAS) norm_rope_vec_kernel(const 
   const int entries = one ? VEC * p.pairs : p.pairs;  // of the table: pairs of the step's rows, or of the row
 
   // this lane's entries of the table, lane + 32 e: of row `row` of the step, pair `pair` (divisions once, not per step)
-  constexpr int E = 4, EP = 2;  // entries of a lane at most, those whose positions are loaded ahead
+  constexpr int E = kRopeMaxPairs / 32, EP = 2;  // entries of a lane at most, those whose positions are loaded ahead
   int entry[E];                 // row | pair << 8 | axis << 16, -1: none
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -387,16 +387,17 @@ __global__ void __launch_bounds__(32 * kPlainWarps) norm_rope_kernel(const RopeP
 
 using NormKernel = void (*)(const RopeParams, const NormParams);
 
-// The vector form for a width: the lanes of a vector, and resident CTAs.
+// The vector form for a width: the lanes of a vector, and resident CTAs.  `whole`: a warp per vector.
 template <int FMT>
-NormKernel vec_form(int width, bool few, int* lanes, int* ctas) {
-  *lanes = width <= 256 ? 8 : width <= 640 && !few ? 16 : 32;
+NormKernel vec_form(int width, bool few, bool whole, int* lanes, int* ctas) {
+  *lanes = whole ? 32 : width <= 256 ? 8 : width <= 640 && !few ? 16 : 32;
   *ctas = width <= 256 ? 3 : 2;
+  if (whole && width <= 256) return norm_rope_vec_kernel<FMT, 32, 1, 3>;
   if (width <= 64) return norm_rope_vec_kernel<FMT, 8, 1, 3>;
   if (width <= 128) return norm_rope_vec_kernel<FMT, 8, 2, 3>;
   if (width <= 192) return norm_rope_vec_kernel<FMT, 8, 3, 3>;
   if (width <= 256) return norm_rope_vec_kernel<FMT, 8, 4, 3>;
-  if (width <= 640 && !few) return norm_rope_vec_kernel<FMT, 16, 5, 2>;
+  if (width <= 640 && !few && !whole) return norm_rope_vec_kernel<FMT, 16, 5, 2>;
   if (width <= 768) return norm_rope_vec_kernel<FMT, 32, 3, 2>;
   return norm_rope_vec_kernel<FMT, 32, 4, 2>;
 }
@@ -433,7 +434,9 @@ dsa_status launch_norm(const RopeParams& p, NormParams n, bool vec, cudaStream_t
     int lanes, ctas;
     // a warp per vector where every warp has one at most (latent rows, us: 129 rows 3.6 and 4.2 with half a warp, 4800 5.7 and 5.3)
     const bool few = (int64_t)p.rows * p.heads <= 2 * kSms * kWarps;
-    const NormKernel kern = vec_form<FMT>(p.width, few, &lanes, &ctas);
+    // (a step's rows have a table of turns each: of all the pairs that a warp's table holds at most)
+    const bool whole = p.heads == 1 && (p.width <= 256 ? 4 : 2) * p.pairs > kRopeMaxPairs;
+    const NormKernel kern = vec_form<FMT>(p.width, few, whole, &lanes, &ctas);
     const int per = 32 / lanes, most = ctas * kSms;
     // heads of a row for a warp: all of up to 16, or as few as leave no warp idle
     n.heads_per_item = 16;
