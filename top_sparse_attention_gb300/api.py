@@ -5,7 +5,6 @@ workspaces that the caller does not pass are allocated with torch on the inputs'
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import NamedTuple, Optional, Tuple
 
@@ -38,8 +37,11 @@ def _side(stream, device):
 
 
 def _scratch(side, shape, dtype, device, zero=False):
-    with contextlib.nullcontext() if side is None else torch.cuda.stream(side):
-        return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
+    make = torch.zeros if zero else torch.empty
+    if side is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(side):
+        return make(shape, dtype=dtype, device=device)
 
 
 def _hand_back(t, device):
@@ -806,15 +808,21 @@ def dsa_expanded_attn(q, k, k_rope, v, q_start, kv_start, *, sm_scale, causal=Tr
         raise ValueError(f"{what}: q must be [T, H, 192], got {tuple(q.shape)}")
     rows = k.shape[0]
     _check(what, dev, "k_rope", k_rope, torch.bfloat16, 2)
+    strides = []  # of k's and v's rows and heads (an axis of one has any stride)
     for name, t in (("k", k), ("v", v)):
         _check(what, dev, name, t, torch.bfloat16, 3, dense=False)
-        if tuple(t.shape) != (rows, H, 128) or t.stride(2) != 1:
+        row, head, col = t.stride()
+        if t.shape != (rows, H, 128) or col != 1:
             raise ValueError(f"{what}: {name} must be [N, {H}, 128] with dense columns, got {tuple(t.shape)}")
-    if tuple(k_rope.shape) != (rows, 64):
+        if H <= 1:
+            head = 128
+        strides += row if rows > 1 else max(128, head * H), head
+    if k_rope.shape != (rows, 64):
         raise ValueError(f"{what}: k_rope must be [{rows}, 64], got {tuple(k_rope.shape)}")
     _check(what, dev, "q_start", q_start, torch.int32, 1)
     _check(what, dev, "kv_start", kv_start, torch.int32, 1)
-    if q_start.shape[0] < 1 or q_start.shape != kv_start.shape:
+    n_seq = q_start.shape[0] - 1
+    if n_seq < 0 or kv_start.shape[0] != n_seq + 1:
         raise ValueError(f"{what}: q_start and kv_start must have one entry more than there are sequences")
     side = _side(stream, dev)
     if out is None:
@@ -831,23 +839,17 @@ def dsa_expanded_attn(q, k, k_rope, v, q_start, kv_start, *, sm_scale, causal=Tr
             raise ValueError(f"{what}: lse must be [{T}, {H}]")
     if T == 0 or H == 0:
         return out, lse
-    a = N.DsaExpandedAttnArgs()
-    a.n_seq, a.T, a.N, a.H = q_start.shape[0] - 1, T, rows, H
-    a.max_len, a.causal, a.sm_scale = 0 if max_len is None else int(max_len), int(bool(causal)), float(sm_scale)
-    a.q_start, a.kv_start = q_start.data_ptr(), kv_start.data_ptr()
-    a.q, a.k, a.k_rope, a.v = q.data_ptr(), k.data_ptr(), k_rope.data_ptr(), v.data_ptr()
-    for name, t in (("k", k), ("v", v)):  # (an axis of one has any stride)
-        head = t.stride(1) if H > 1 else 128
-        setattr(a, name + "_head_stride", head)
-        setattr(a, name + "_row_stride", t.stride(0) if rows > 1 else max(128, head * H))
-    a.out, a.lse = out.data_ptr(), lse.data_ptr()
+    a = N.DsaExpandedAttnArgs(n_seq, T, rows, H, 0 if max_len is None else int(max_len), int(bool(causal)), float(sm_scale),
+                              q_start.data_ptr(), kv_start.data_ptr(), q.data_ptr(), k.data_ptr(), k_rope.data_ptr(), v.data_ptr(),
+                              *strides, out.data_ptr(), lse.data_ptr())
+    ref = ctypes.byref(a)
     need = ctypes.c_size_t(0)
-    N.check(N.lib.dsa_expanded_attn_workspace_size(ctypes.byref(a), ctypes.byref(need)), what)
+    N.check(N.lib.dsa_expanded_attn_workspace_size(ref, ctypes.byref(need)), what)
     if ws is None:
         ws = _scratch(side, need.value, torch.uint8, dev) if need.value else None
     else:
         _check(what, dev, "ws", ws, torch.uint8, 1)
-    _run(what, N.lib.dsa_expanded_attn, dev, stream, ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel())
+    _run(what, N.lib.dsa_expanded_attn, dev, stream, ref, _ptr(ws), 0 if ws is None else ws.numel())
     return out, lse
 
 
