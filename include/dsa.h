@@ -413,7 +413,8 @@ dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int wi
  *   eps           finite, at least 0 (with 0 a vector of zeros has no norm and gives NaN)
  * All other arguments are those of dsa_rope (without inverse) and dsa_rope_append.  out == x (with equal strides)
  * works in place.
- * Supported: width at most 1024; finite inputs.
+ * Supported: width at most 1024; inputs below 2^59 in size in the normed columns (their squares are summed in fp32, which
+ * also loses those of values below 2^-63: beside eps > 0 they do not count), finite ones elsewhere.
  * ------------------------------------------------------------------------------------------ */
 #define DSA_NORM_RMS 0
 #define DSA_NORM_LAYER 1
