@@ -420,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c0 = 0; c0 < NT; c0 += 64, ++piece) {
         uint8_t* box = stage + (piece & 1) * 4096;
-        // the copy out of this box two pieces ago has read it
+        // the copy out of this box two pieces ago has read it: a piece commits one group (below), so all but the last one's have
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
         __syncwarp();
 #pragma unroll
@@ -444,12 +444,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (live == 0xffffffffu) {
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
+          if (lane == 0)
             asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&tm_out), "r"(col + c0),
                          "r"((int)base), "r"(smem_u32(box))
                          : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          }
         } else {
           __syncwarp();
           __nv_bfloat16* out = p.out + base * ((int64_t)p.H * kOut) + col + c0;
@@ -460,6 +458,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if ((live >> r) & 1) *reinterpret_cast<uint4*>(out + r * ((int64_t)p.H * kOut) + 8 * c) = x;
           }
         }
+        // (of a piece that went by plain stores an empty group: without one the wait of the piece behind would leave the copy
+        // before this one in flight, whose box that piece writes)
+        if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
