@@ -165,12 +165,12 @@ __device__ __forceinline__ int edges_of(const Facts& f, const Work& w, int n0, i
 }
 
 // ---------------------------------------------------------------------------------------------
-// the list of work: blocks, the longest first (a counting sort by tiles; which of two of equal length
-// comes first does not matter to the results)
+// the list of work: blocks, the longest first (a counting sort by tiles)
 
 __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) {
   __shared__ int base[kMaxSeq + 1];          // blocks before each sequence
-  __shared__ int place[kLengths + 1];        // by tiles: how many, then where the next goes
+  __shared__ int place[kLengths + 2];        // by tiles: how many, then where the next goes (the last entry: of threads without a block)
+  __shared__ int longest_block;
   __shared__ int warp_sum[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int run = 0;
@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
     __syncthreads();
   }
   if (tid == 0) base[p.n_seq] = run;
-  for (int i = tid; i <= kLengths; i += 1024) place[i] = 0;
+  for (int i = tid; i < kLengths + 2; i += 1024) place[i] = 0;
+  if (tid == 0) longest_block = 0;
   __syncthreads();
   auto find = [&](int b, int& q0) {  // the sequence of block b, and the block's first query
     int lo = 0, hi = p.n_seq - 1;
@@ -298,40 +299,69 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
       return;
     }
   }
-  // Blocks, the longest first
-  // pass 0 counts, pass 1 places
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int b = tid; b < run; b += 1024) {
-      int q0;
-      const int lo = find(b, q0);
-      const int n = block_tiles(block_facts(p, lo, q0));
-      const int at = atomicAdd(&place[min(n >> p.shift, kLengths)], 1);
-      if (pass && at < p.max_work) p.work[at] = make_int4(lo, q0, 0, n);
-    }
-    __syncthreads();
-    if (pass == 0) {
-      // how many are longer, for each length: the running sum from the longest on
-      static_assert(kLengths < 1024, "a thread a length");
-      const int at = kLengths - tid, c = at >= 0 ? place[at] : 0;
-      int incl = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += u;
-      }
-      if (lane == 31) warp_sum[warp] = incl;
-      __syncthreads();
-      int ahead = 0;
-      for (int i = 0; i < warp; ++i) ahead += warp_sum[i];
-      if (at >= 0) place[at] = ahead + incl - c;
-      __syncthreads();
-    }
+  // Blocks, the longest first: counted, then placed
+  int most = 0;
+  for (int b = tid; b < run; b += 1024) {
+    int q0;
+    const int seq = find(b, q0), n = block_tiles(block_facts(p, seq, q0));
+    atomicAdd(&place[min(n >> p.shift, kLengths)], 1);
+    most = max(most, n);
   }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) atomicMax(&longest_block, most);
+  __syncthreads();
+  {  // how many are longer, for each length: the running sum from the longest on
+    static_assert(kLengths < 1024, "a thread a length");
+    const int at = kLengths - tid, c = at >= 0 ? place[at] : 0;
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int ahead = 0;
+    for (int i = 0; i < warp; ++i) ahead += warp_sum[i];
+    if (at >= 0) place[at] = ahead + incl - c;
+    __syncthreads();
+  }
+  const int items = min(run, p.max_work) * p.H, rounds = items / p.grid, left = items % p.grid;
+  // Where what is left behind whole rounds may be cut (below), blocks of equal length stay in the order of their numbers, a warp
+  // placing its 32 after another: a block that is cut is summed in another order than one that is not, so which ones are may
+  // not go by the warps' speed.  Elsewhere the order does not matter, and they go where an atomic puts them (4096 sequences of
+  // 3 tokens of a head: 138 us, 144 in order).
+  const bool ordered = left > 0 && p.grid / left > 1 && longest_block >= 2 * kMinPart;
+  for (int b0 = 0; b0 < run; b0 += 1024) {
+    const int b = b0 + tid;
+    int4 item = make_int4(0, 0, 0, 0);
+    int key = kLengths + 1, at = p.max_work;
+    if (b < run) {
+      item.x = find(b, item.y);
+      item.w = block_tiles(block_facts(p, item.x, item.y));
+      key = min(item.w >> p.shift, kLengths);
+    }
+    if (!ordered) {
+      if (b < run) at = atomicAdd(&place[key], 1);
+    } else {
+      const uint32_t same = __match_any_sync(0xffffffffu, key), before = same & ((1u << lane) - 1);
+      const int turns = min((run - b0 + 31) / 32, 32);
+      for (int turn = 0; turn < turns; ++turn) {
+        if (warp == turn) {
+          at = place[key] + __popc(before);
+          __syncwarp();
+          if (before == 0) place[key] += __popc(same);
+        }
+        __syncthreads();
+      }
+    }
+    if (b < run && at < p.max_work) p.work[at] = item;
+  }
+  __syncthreads();
   // What is left behind whole rounds, where that is half a round or less: its items are cut, into parts of kMinPart tiles at
   // least, for all CTAs (3.4 rounds of 16 heads: 8192 tokens over 20480 positions 1.01 ms, uncut 1.09; over 9216, whose last items
   // are of 8 to 24 tiles, cut into parts of 8 and more 0.419, uncut 0.407)
   if (tid < p.grid) {
-    const int items = min(run, p.max_work) * p.H, rounds = items / p.grid, left = items % p.grid;
     const int ways = left ? max(min(p.grid / left, p.work[rounds * p.grid / p.H].w / kMinPart), 1) : 1;  // (the longest of them)
     const int at = rounds & 1 ? p.grid - 1 - tid : tid, x = at / ways;
     p.plan->done[tid][0] = p.plan->done[tid][1] = 0;
