@@ -571,8 +571,9 @@ dsa_status dsa_tree_attn(const dsa_tree_args* a, void* ws, size_t ws_bytes, void
  * per sequence.  Same arguments, layouts, results and support as dsa_tree_attn.  Group g is the sequences
  * group_start[g] ... group_start[g+1] - 1; their first n_shared[g] positions hold the same rows (in a paged cache
  * usually the same blocks), which are read from the first sequence of the group that has queries.
- *   group_start  device int32 [n_groups + 1], not decreasing (clamped to [0, n_seq]); sequences outside
- *                [group_start[0], group_start[n_groups]) share nothing
+ *   group_start  device int32 [n_groups + 1], not decreasing (clamped to [0, n_seq]; one that decreases records
+ *                DSA_DEVERR_INDEX_RANGE, and nothing is shared); sequences outside [group_start[0], group_start[n_groups])
+ *                share nothing
  *   n_shared     device int32 [n_groups]: clamped to the least n_ctx of the group's sequences that have queries
  *                (n_new above 0); a group of one shares nothing
  * The results differ from dsa_tree_attn's by rounding only (the sums are split elsewhere); they repeat from call to call.

@@ -131,8 +131,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const TreeAtt
   sm.group_of = sm.tiles + p.n_seq;
 
   // ---- the groups: a warp each
+  bool disorder = false;  // group_start decreases: groups would overlap, and their units be more than there is room for
   for (int g = warp; g < pp.n_groups; g += kPlanThreads / 32) {
-    const int lo = min(max(pp.group_start[g], 0), p.n_seq), hi = min(max(pp.group_start[g + 1], lo), p.n_seq);
+    const int lo = min(max(pp.group_start[g], 0), p.n_seq), end = min(max(pp.group_start[g + 1], 0), p.n_seq), hi = max(end, lo);
+    disorder |= end < lo;
     int least = INT_MAX, lead = INT_MAX, members = 0;
     for (int s = lo + lane; s < hi; s += 32) {
       int ctx, fresh, len;
@@ -150,7 +152,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const TreeAtt
       sm.groups[g] = x;
     }
   }
-  __syncthreads();
+  if (__syncthreads_or(disorder)) {  // nothing is shared
+    if (tid == 0) record_error(p.err, DSA_DEVERR_INDEX_RANGE);
+    for (int g = tid; g < pp.n_groups; g += kPlanThreads) sm.groups[g] = Group{};
+    __syncthreads();
+  }
   // ---- the sequences' groups and tails, and all tiles
   int2 sum = make_int2(0, 0), all;
   for (int s = tid; s < p.n_seq; s += kPlanThreads) {
