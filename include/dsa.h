@@ -452,7 +452,7 @@ dsa_status dsa_norm_rope_append(const void* x, int64_t x_row_stride, int rows, i
  *   w          device bf16 [H, 256, 512]
  *   out        device bf16 [rows, H, 256];  rope_out  device bf16 [rows, 64] or NULL
  * Supported: kv_dtype DSA_BF16, DSA_FP8_E4M3 or DSA_FP8_E4M3_T128 (finite codes); H <= 128; n_seq <= 4096; pointers
- * (but kv_start and block_table) 16-byte aligned, kv_scale 4-byte, row strides multiples of 16 bytes.  No workspace.
+ * 16-byte aligned (kv_start, block_table and kv_scale 4-byte), row strides multiples of 16 bytes.  No workspace.
  * ------------------------------------------------------------------------------------------ */
 typedef struct dsa_expand_args {
   int n_seq, rows, L, H;
@@ -491,8 +491,8 @@ dsa_status dsa_latent_expand(const dsa_expand_args* a, void* stream);
  *   out        device bf16 [T, H, 128];  lse  device fp32 [T, H] or NULL
  * ws: device memory of dsa_expanded_attn_workspace_size bytes, 256-byte aligned, contents irrelevant; calls (and
  * captured graphs) that share it must not run at the same time.
- * Supported: sm_scale > 0; 1 <= H <= 128; n_seq <= 4096; T, N below 2^24 rows; pointers 16-byte aligned, strides
- * multiples of 8 elements, below 2^39.
+ * Supported: sm_scale > 0; 1 <= H <= 128; n_seq <= 4096; T, N below 2^24 rows; pointers 16-byte aligned (q_start, kv_start
+ * and lse 4-byte), strides multiples of 8 elements, below 2^39.
  * ------------------------------------------------------------------------------------------ */
 typedef struct dsa_expanded_attn_args {
   int n_seq, T, N, H, max_len, causal;
@@ -542,8 +542,8 @@ dsa_status dsa_expanded_attn(const dsa_expanded_attn_args* a, void* ws, size_t w
  * not seen.  ws: device memory of dsa_tree_attn_workspace_size bytes (partial results, and with L above 65536
  * the sums of long walks), 16-byte aligned, contents irrelevant; calls (and captured graphs) that share it must not run at the same time.
  * Supported: D_qk = 576, D_v = 512; kv_dtype DSA_BF16, DSA_FP8_E4M3 or DSA_FP8_E4M3_T128 (finite
- * codes); 1 <= H <= 128; 1 <= q_per_seq <= 1024; n_seq <= 4096; L <= 2^31 - 4097; pointers 16-byte aligned, row
- * strides multiples of 16 bytes, below 2^40.
+ * codes); 1 <= H <= 128; 1 <= q_per_seq <= 1024; n_seq <= 4096; L <= 2^31 - 4097; pointers 16-byte aligned (those of int32,
+ * uint32 and float 4-byte), row strides multiples of 16 bytes, below 2^40.
  * ------------------------------------------------------------------------------------------ */
 typedef struct dsa_tree_args {
   int n_seq, q_per_seq, L, H, D_qk, D_v;

@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "dsa_internal.h"
@@ -336,6 +337,9 @@ dsa_status check_tree(const dsa_tree_args* a) {
   }
   if (a->n_seq == 0) return DSA_OK;
   if (!a->n_ctx || !a->q || !a->out || !aligned16(a->q) || !aligned16(a->out)) return DSA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)a->n_ctx, (const void*)a->n_new, (const void*)a->tree_mask, (const void*)a->kv_scale, (const void*)a->lse,
+                        (const void*)a->block_table})
+    if ((reinterpret_cast<uintptr_t>(p) & 3) != 0) return DSA_ERR_INVALID_ARG;
   if (a->L == 0) return DSA_OK;
   if (!a->kv || !aligned16(a->kv)) return DSA_ERR_INVALID_ARG;
   if (a->kv_row_stride % 16 != 0 || a->kv_row_stride < 576 * elem) return DSA_ERR_INVALID_ARG;

@@ -521,6 +521,7 @@ dsa_status check_expand(const dsa_expand_args* a) {
   }
   if (a->n_seq == 0 || a->rows == 0) return DSA_OK;
   auto ok16 = [](const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  if (((reinterpret_cast<uintptr_t>(a->kv_start) | reinterpret_cast<uintptr_t>(a->block_table)) & 3) != 0) return DSA_ERR_INVALID_ARG;
   if (!a->kv_start || !ok16(a->w) || !ok16(a->out) || (a->rope_out && !ok16(a->rope_out))) return DSA_ERR_INVALID_ARG;
   if (!ok16(a->kv) || a->kv_row_stride % 16 != 0 || a->kv_row_stride < kLat + kRope) return DSA_ERR_INVALID_ARG;
   if (a->kv_dtype == DSA_BF16 && a->kv_row_stride < 2 * (kLat + kRope)) return DSA_ERR_INVALID_ARG;

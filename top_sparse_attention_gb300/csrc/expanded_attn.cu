@@ -988,6 +988,8 @@ dsa_status check_expanded(const dsa_expanded_attn_args* a) {
   if (a->n_seq == 0 || a->T == 0) return DSA_OK;
   auto ok16 = [](const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   if (!a->q_start || !a->kv_start || !ok16(a->q) || !ok16(a->out)) return DSA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)a->q_start, (const void*)a->kv_start, (const void*)a->lse})
+    if ((reinterpret_cast<uintptr_t>(p) & 3) != 0) return DSA_ERR_INVALID_ARG;
   if (a->N == 0) return DSA_OK;
   if (!ok16(a->k) || !ok16(a->k_rope) || !ok16(a->v)) return DSA_ERR_INVALID_ARG;
   for (const int64_t s : {a->k_row_stride, a->v_row_stride, a->k_head_stride, a->v_head_stride}) {

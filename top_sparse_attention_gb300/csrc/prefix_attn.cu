@@ -423,6 +423,7 @@ dsa_status check_prefix(const dsa_tree_args* a, const int32_t* group_start, cons
   const dsa_status s = check_tree_args(a);
   if (s != DSA_OK) return s;
   if (n_groups < 0 || (n_groups > 0 && (!group_start || !n_shared))) return DSA_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(group_start) | reinterpret_cast<uintptr_t>(n_shared)) & 3) != 0) return DSA_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)a->q_per_seq * a->H;
   if (n_groups > kMaxGroups || a->n_seq > kMaxSeq || a->n_seq * rows > 1 << 26) return DSA_ERR_UNSUPPORTED;
   // the plan's costs have 31 bits: tiles of positions x row tiles, of the sequences' and of the groups' units

@@ -580,7 +580,7 @@ dsa_status dsa_rope_append(const void* x, int64_t x_row_stride, int rows, int wi
   if (dtype == DSA_MXFP8_E4M3 && width % 32 != 0) return DSA_ERR_INVALID_ARG;
   if (!dst_rows && rows > dst_count) return DSA_ERR_INVALID_ARG;
   if (rows == 0) return DSA_OK;
-  if (!x || !dst || !aligned2(x) || (elem == 2 && !aligned2(dst))) return DSA_ERR_INVALID_ARG;
+  if (!x || !dst || !aligned2(x) || (elem == 2 && !aligned2(dst)) || !aligned(dst_rows, 8)) return DSA_ERR_INVALID_ARG;
   if (dtype != DSA_BF16 && !scale) return DSA_ERR_INVALID_ARG;
   if ((dtype == DSA_FP8_E4M3 || dtype == DSA_FP8_E4M3_T128) && !aligned(scale, 4)) return DSA_ERR_INVALID_ARG;
   if ((s = check_device_arch()) != DSA_OK) return s;

@@ -124,6 +124,7 @@ dsa_status rope_args(RopeParams* p, int width, int rot_off, int rot_dim, const i
   if (rot_dim > 2 * kRopeMaxPairs || n_axes > 4) return DSA_ERR_UNSUPPORTED;
   if (n_axes > 1 && !pair_axis) return DSA_ERR_INVALID_ARG;
   if (any_rows && (!pos || !inv_freq)) return DSA_ERR_INVALID_ARG;
+  if (!aligned(pos, 4) || !aligned(inv_freq, 4)) return DSA_ERR_INVALID_ARG;
   p->pairs = rot_dim / 2;
   for (int i = 0; i < p->pairs; ++i) {
     const int a = pair_axis ? pair_axis[i] : 0;
