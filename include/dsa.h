@@ -477,7 +477,9 @@ dsa_status dsa_latent_expand(const dsa_expand_args* a, void* stream);
  * n - m + i (causal != 0: the queries are the sequence's last positions), or all n:
  *   logit[p] = sm_scale * (q[i, h, :128] . k[p, h, :] + q[i, h, 128:] . k_rope[p, :])
  *   out[i, h, :] = sum_p softmax(logit)[p] * v[p, h, :]  (bf16);   lse[i, h] = ln sum_p exp(logit[p])  (fp32)
- * The weights are rounded to bf16 and summed in fp32.  A query that sees nothing gets out = 0 and lse = -inf.  What
+ * The weights are rounded to bf16 and summed in fp32 by adders that truncate: before its own rounding an output is off by at most
+ * 2^-8 + 2^-13 + 2^-27 min(n, 65536) of sum_p softmax(logit)[p] |v[p, h]| (beside what the logits' fp32 sums are off by).  Calls
+ * repeat to the bit.  A query that sees nothing gets out = 0 and lse = -inf.  What
  * the rows of a position hold does not matter to a query that does not see it (infinities and NaN included); an infinity
  * or NaN in a value that a query sees appears in its output.
  *   q          device bf16 [T, H, 192]
@@ -486,8 +488,9 @@ dsa_status dsa_latent_expand(const dsa_expand_args* a, void* stream);
  *   k_rope     device bf16 [N, 64]
  *   q_start, kv_start  device int32 [n_seq + 1], not decreasing, at most T and N; rows of q behind the last sequence
  *              are not read, their out and lse left as they were
- *   max_len    positions of the longest sequence at most (0: N): sizes the workspace.  A longer sequence records
- *              DSA_DEVERR_INDEX_RANGE and its queries' results are not defined
+ *   max_len    positions of the longest sequence at most (0: N): sizes the workspace, and above 65536 chooses the form for long
+ *              contexts (20 MB more of workspace; a batch of shorter sequences with N above that is up to 4 % slower in it
+ *              than with its max_len).  A longer sequence records DSA_DEVERR_INDEX_RANGE and its queries' results are not defined
  *   out        device bf16 [T, H, 128];  lse  device fp32 [T, H] or NULL
  * ws: device memory of dsa_expanded_attn_workspace_size bytes, 256-byte aligned, contents irrelevant; calls (and
  * captured graphs) that share it must not run at the same time.
@@ -579,7 +582,7 @@ dsa_status dsa_tree_attn(const dsa_tree_args* a, void* ws, size_t ws_bytes, void
  * The results differ from dsa_tree_attn's by rounding only (the sums are split elsewhere); they repeat from call to call.
  * ws: dsa_prefix_attn_workspace_size bytes, 256-byte aligned, contents irrelevant; calls (and captured graphs) that share
  * it must not run at the same time.  group_start and n_shared of the size query are only tested for being there.
- * Supported: n_groups <= 4096; n_seq * q_per_seq * H <= 2^26; (2 n_seq ceil(q_per_seq H / 128) + n_groups) * (L / 64 + 9) below
+ * Supported: n_groups <= 4096; n_seq * q_per_seq * H <= 2^26; (2 n_seq ceil(q_per_seq H / 128) + n_groups + 1) * (L / 64 + 9) below
  * 2^31 (1024 sequences of 16 heads over 16 million positions).
  * ------------------------------------------------------------------------------------------ */
 dsa_status dsa_prefix_attn_workspace_size(const dsa_tree_args* a, const int32_t* group_start, const int32_t* n_shared,

@@ -798,8 +798,8 @@ def dsa_expanded_attn(q, k, k_rope, v, q_start, kv_start, *, sm_scale, causal=Tr
     """Attention of packed ragged prompts, or chunks of them, over expanded keys and values (see dsa.h): (out [T, H, 128]
     bf16, lse [T, H] fp32).  q bf16 [T, H, 192]; k, v bf16 [N, H, 128] with dense columns (views of dsa_latent_expand's
     output); k_rope bf16 [N, 64]; q_start, kv_start int32 [n_seq + 1].  Causal: a sequence's queries are its last
-    positions.  `max_len` (positions of the longest sequence at most; None: N) sizes the workspace; `ws` (uint8) is scratch
-    that later calls on the same stream may reuse."""
+    positions.  `max_len` (positions of the longest sequence at most; None: N) sizes the workspace and above 65536 chooses the
+    form for long contexts: give it with many sequences.  `ws` (uint8) is scratch that later calls on the same stream may reuse."""
     what = "dsa_expanded_attn"
     dev = _cuda_device(what, q)
     _check(what, dev, "q", q, torch.bfloat16, 3)

@@ -9,9 +9,13 @@
 //     own, that all heads read);
 //   * one pass over the positions keeps a reference maximum m and a sum l per row as in tree_kernel.cuh: m moves only where
 //     a tile's maximum exceeds it by more than 2^8, so that O is rescaled rarely;
-//   * P, bf16, takes the place of S in tensor memory, and O[128 x 128] += P V: 8 steps, A in tensor memory, V MN-major.
-// Tensor memory: S and O of both tiles, 4 x 128 columns.  The two tiles take turns: while four warps take the softmax of one
-// (a thread a row), the tensor cores multiply for the other: O += P V of the last positions, then S of the next ones.
+//   * P takes the place of S in tensor memory, and O[128 x 128] += P V: 8 steps, A in tensor memory, V MN-major.  P is rounded to
+//     bf16: an MMA's operands have one 16-bit type, which is V's (the next wider one, tf32, runs at half the rate and would want V
+//     widened too).  A weight is off by at most 2^-8 of itself, as the output is by its own rounding; an output over normal
+//     values is 1.2 to 1.4 times as far from 64 bits as one of fp32 weights.
+// Tensor memory: S and O of both tiles, 4 x 128 columns.  The two tiles take turns: while eight warps take the softmax of one (a
+// thread a row and half of the positions), the tensor cores multiply for the other: O += P V of the last positions, then S
+// of the next ones.
 // The instructions of one thread execute in order, so that S may follow the P V that reads P in the same columns, and a
 // finished S means that the P V before it has finished.
 //
@@ -26,8 +30,10 @@
 //   * many blocks: dealt to the CTAs back and forth, the longest first; what is left behind whole rounds is cut for all CTAs;
 //   * few: laid end to end and cut into one span of tiles for each CTA; a block that is cut leaves fp32 partial results, which
 //     the CTA that finishes the last of them merges, in the order of the positions (so results do not depend on which that is).
-// The tensor cores truncate their sums, and O loses 2^-24 of itself per step, 0.04 % over 65536 positions.  Longer contexts
-// are walked in stretches of 512 tiles, whose O and l are added up in fp32, in memory (a form of the kernel of its own).
+// The tensor cores truncate their sums, and O loses up to 2^-23 of itself per step of 16 positions, 0.05 % over 65536.  Longer
+// contexts are walked in stretches of 512 tiles, whose O and l are added up in fp32, in memory (a form of the kernel of its own,
+// taken where max_len, or without it N, is above 65536; nine prompts of 8192 take 1 to 4 % longer in it, shorter sequences
+// the same).
 //
 // Bound: tensor cores, 12 x 64 + 8 x 64 cycles per tile of 128 x 128, beside shared memory, which the first product's operands
 // fill for as long (4 + 4 KB a step).  Measured: one prompt of 8192 x 16 heads 234 us (1470 TFLOP/s of what causality leaves; tensor cores
@@ -66,6 +72,7 @@ constexpr int kFixed = 3;                      // what starting on a block costs
 constexpr int kMinSpan = 4;                    // tiles of a span, at least
 constexpr int kMinPart = 16;                   // and of a part of an item of the list's last round
 constexpr int kMaxSeq = 4096;
+constexpr int kMaxRows = 1 << 24;              // of q, and of k and v: fewer
 constexpr uint32_t kColS = 0, kColO = 256;
 
 // What the planning kernel leaves for the others.
@@ -247,7 +254,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
     if (tid < run) before[tid] = ahead + incl - cost;
     if (tid == run) before[run] = all;
     __syncthreads();
-    const int items = run * p.H, total = all * p.H, W = max((total + p.grid - 1) / p.grid, kMinSpan);  // (below 2^25)
+    const int items = run * p.H, total = all * p.H, W = max((total + p.grid - 1) / p.grid, kMinSpan);
+    static_assert((int64_t)kSpanItems * (kMaxRows / kTile + kFixed) < 1 << 26, "costs are ints");
     const int whole = items <= p.grid ? longest : total / p.grid + longest / 2;
     if (W + 2 * kFixed < whole) {
       // The order: a sequence after another, of it a head after another, of that the blocks, so that the CTAs that read the
@@ -984,7 +992,7 @@ cudaError_t launch(ExpandedAttnParams p, const dsa_expanded_attn_args& a, void* 
 dsa_status check_expanded(const dsa_expanded_attn_args* a) {
   if (!a || a->n_seq < 0 || a->T < 0 || a->N < 0 || a->max_len < 0 || a->H < 1) return DSA_ERR_INVALID_ARG;
   if (!(a->sm_scale > 0.f) || !(a->sm_scale < INFINITY)) return DSA_ERR_INVALID_ARG;
-  if (a->H > 128 || a->n_seq > kMaxSeq || a->T >= 1 << 24 || a->N >= 1 << 24) return DSA_ERR_UNSUPPORTED;
+  if (a->H > 128 || a->n_seq > kMaxSeq || a->T >= kMaxRows || a->N >= kMaxRows) return DSA_ERR_UNSUPPORTED;
   if (a->n_seq == 0 || a->T == 0) return DSA_OK;
   auto ok16 = [](const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   if (!a->q_start || !a->kv_start || !ok16(a->q) || !ok16(a->out)) return DSA_ERR_INVALID_ARG;

@@ -44,8 +44,15 @@ struct PrefixPlan {
 constexpr int kPairs = 76;
 constexpr int kMaxGroups = 4096, kMaxSeq = 4096;
 constexpr int kPlanThreads = 1024;
-// Fill, query rows and partial results of a unit, in tiles: about 10 us, of tiles of 1.2 us (tile scales: 2.6).  With 4 and 8, us:
-// 64 sequences over 32K shared positions, E4M3 rows 130 and 111; 48 over 3 x 8K, tile scales 141 and 147.
+// Fill, query rows and partial results of a unit, in tiles: about 10 us, of tiles of 1.2 us (tile scales: 2.6).  Device us with 2, 4,
+// 8 and 16, tails of up to 256 to 1500 positions:
+//                                               bf16                  row scales            tile scales
+//   64 x 16 rows behind 32768 positions         125, 111, 115, 125    160, 129, 112, 121    215, 205, 214, 236
+//   32 x 128 rows behind two of up to 16384     180, 154, 137, 145    201, 170, 136, 141    286, 248, 255, 273
+//   48 x 64 rows behind three of up to 8192      87,  82,  85,  95    100,  89,  84,  93    142, 138, 149, 169
+//   256 x 16 rows behind 32 of up to 1024        74,  77,  81,  82     94,  84,  87,  87    106, 115, 126, 126
+// and the same for 16 x 16 rows behind 4096 (37, 44, 47) and 8 x 128 behind 2048 (36, 41, 46), where a CTA has one tile or two and
+// the cost is taken as one tile at most (prefix_plan_kernel).
 constexpr int kUnitCost = 8, kUnitCostTiled = 4;
 
 __host__ __device__ __forceinline__ int row_tiles(int rows) { return (rows + kRows - 1) / kRows; }
