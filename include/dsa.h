@@ -486,8 +486,9 @@ dsa_status dsa_latent_expand(const dsa_expand_args* a, void* stream);
  *   k, v       device bf16: head h of row r at r * row_stride + h * head_stride ELEMENTS, 128 columns (with
  *              dsa_latent_expand's output, k = out and v = out + 128, strides 256 H and 256)
  *   k_rope     device bf16 [N, 64]
- *   q_start, kv_start  device int32 [n_seq + 1], not decreasing, at most T and N; rows of q behind the last sequence
- *              are not read, their out and lse left as they were
+ *   q_start, kv_start  device int32 [n_seq + 1], not decreasing, from 0 to T and N (else they are clamped,
+ *              DSA_DEVERR_INDEX_RANGE is recorded and the results of the sequences concerned are not defined); rows of q behind
+ *              the last sequence are not read, their out and lse left as they were
  *   max_len    positions of the longest sequence at most (0: N): sizes the workspace, and above 65536 chooses the form for long
  *              contexts (20 MB more of workspace; a batch of shorter sequences with N above that is up to 4 % slower in it
  *              than with its max_len).  A longer sequence records DSA_DEVERR_INDEX_RANGE and its queries' results are not defined

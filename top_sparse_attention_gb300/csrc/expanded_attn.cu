@@ -188,7 +188,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const ExpandedAttnParams p) 
     if (s < p.n_seq) {
       seq_facts(p, s, f);
       c = (f.m + kBlock - 1) / kBlock;
-      if (p.kv_start[s + 1] - p.kv_start[s] > f.n) record_error(p.err, DSA_DEVERR_INDEX_RANGE);
+      // a start that decreases or lies outside of the rows, a sequence longer than max_len
+      if ((int64_t)p.kv_start[s + 1] - p.kv_start[s] != f.n || (int64_t)p.q_start[s + 1] - p.q_start[s] != f.m)
+        record_error(p.err, DSA_DEVERR_INDEX_RANGE);
     }
     int incl = c;
 #pragma unroll
